@@ -253,6 +253,100 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
                        int num_blocks, int num_kv_heads, int head_dim, int page_size, void *k_shuf,
                        void *v_shuf, void *stream);
 
+/* How sk_rope_frequencies fits the frequencies w_i = base^(-2 i / rot_dim) to contexts `factor` times
+ * longer than the trained ones. */
+typedef enum {
+    SK_ROPE_PLAIN = 0,        /* w_i */
+    SK_ROPE_LINEAR = 1,       /* w_i / factor (positions interpolated) */
+    SK_ROPE_BASE = 2,         /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+    SK_ROPE_BANDS = 3         /* by the turns r = original_len * w_i / (2 pi) that a frequency makes in the trained
+                                 context: w_i / factor up to `low` turns, w_i from `high` on, a linear blend between */
+} sk_rope_scaling;
+
+/* Frequencies of the rotary positions, on the host, in 64 bits: freqs[rot_dim / 2] (host, caller-owned),
+ * and in *attn_factor (may be NULL) the factor that goes with them (0.1 ln(factor) + 1 for
+ * SK_ROPE_BANDS, else 1).  original_len, low and high are read for SK_ROPE_BANDS only.
+ * Returns SK_OK, or SK_ERR_INVALID (odd rot_dim, base <= 1, factor < 1, high <= low). */
+int sk_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double low,
+                        double high, double *freqs, double *attn_factor);
+
+/* Rotary positions with the KV write: turns this step's q and k, and stores k and v like
+ * sk_reshape_and_cache.
+ *
+ * For token t at position p = positions[t], pair i < rot_dim / 2 of a head is elements (2 i, 2 i + 1)
+ * (interleaved != 0) or (i, i + rot_dim / 2), and
+ *   a' = attn_factor (a cos(p w_i) - b sin(p w_i)),  b' = attn_factor (b cos(p w_i) + a sin(p w_i))
+ * with w_i = freqs[i] radians per position; elements from rot_dim on pass through unchanged.
+ *   q_out[t]           every query head of q, turned
+ *   kv_pages (slot t)  K: every KV head of key, turned; V: value; bf16 pages round once from the fp32
+ *                      result, e4m3fn pages take the fp32 result divided by k_scale (v_scale)
+ *                      and rounded like sk_reshape_and_cache
+ *   acc_pages (slot t), pos_pages (slot t)  0 and p for every KV head, where the arrays are given
+ * A negative slot writes q_out only.  A slot at or past num_blocks * page_size writes q_out only and sets
+ * SK_DEV_BAD_BLOCK.  Two tokens with the same slot leave that row undefined.  Angles are taken
+ * in 64 bits modulo a revolution, so far positions lose no more than the rounding of freqs; positions may be
+ * negative.
+ *
+ * Layouts (device, caller-owned): q bf16 [num_tokens, num_q_heads, 128] with q_stride elements between
+ * tokens (heads contiguous; a view of a fused projection will do), key and value likewise with
+ * num_kv_heads; strides are multiples of 8.  q_out is contiguous and may be q itself (when that is
+ * contiguous).  positions, slot_mapping int64 [num_tokens]; freqs float64 [rot_dim / 2] (device);
+ * rot_dim a multiple of 16 up to 128.  kv_pages as for sk_reshape_and_cache.  acc_pages fp32 and pos_pages
+ * int32 [num_blocks, num_kv_heads, page_size], or NULL.  q, key, value, q_out and kv_pages are 16-byte
+ * aligned.  Asynchronous on `stream`, no allocation, capture safe.
+ * Returns SK_OK or a negative sk_status. */
+int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t q_stride, int64_t key_stride,
+                      int64_t value_stride, const int64_t *positions, const double *freqs, int rot_dim,
+                      int interleaved, float attn_factor, const int64_t *slot_mapping, int num_tokens,
+                      int num_q_heads, int num_kv_heads, int head_dim, void *q_out, void *kv_pages, int kv_dtype,
+                      float k_scale, float v_scale, int num_blocks, int page_size, float *acc_pages,
+                      int32_t *pos_pages, void *stream);
+
+/* Eviction of cached rows by gathered attention weight, first step: which rows stay.
+ *
+ * A sequence with L = seq_lens[s] > budget keeps `budget` rows of every KV head.  Row r of (s, h) has the
+ * weight acc_pages and the position pos_pages at its place in the pages.  Rows with a position of at least
+ * next_pos[s] - recent rank first (next_pos: the position that the sequence's next token will have), then
+ * rows rank by weight, larger first; equal ranks go to the lower row; NaN ranks like -inf.  The first
+ * `budget` rows stay.
+ *   counts[s][h]                n = how many rows at or past `budget` stay
+ *   src_rows[s][h][m], m < n    the m-th of them, ascending
+ *   dst_rows[s][h][m], m < n    the m-th row below `budget` that does not stay, ascending
+ *   new_lens[s]                 min(L, budget)
+ * Entries from n on are left as they were.  sk_evict_move then moves src_rows[m] to dst_rows[m].  Rows
+ * below `budget` that stay do not move, so the rows of a head are not in order of position after it; the
+ * attention of this library does not depend on the order of rows that every query token sees.  A sequence
+ * with L <= budget has n = 0.  L above max_seq_len (or below 0) sets SK_DEV_BAD_SEQ: n = 0, new_lens = L.
+ * A row in a block outside [0, num_blocks) ranks like -inf and sets SK_DEV_BAD_BLOCK.
+ *
+ * acc_pages fp32, pos_pages int32 [num_blocks, num_kv_heads, page_size]; src_rows, dst_rows int32 [bs,
+ * num_kv_heads, capacity], capacity >= sk_evict_capacity(budget, max_seq_len); counts int32 [bs,
+ * num_kv_heads]; new_lens int32 [bs], not seq_lens itself.  max_seq_len: an upper bound on the lengths, at
+ * most 786432; it sizes the launch.  0 <= recent <= budget.  Asynchronous on `stream`, no allocation,
+ * capture safe, the same result whatever the timing.
+ * Returns SK_OK or a negative sk_status. */
+int sk_evict_select(const float *acc_pages, const int32_t *pos_pages, const int32_t *block_table,
+                    int block_table_stride, int num_blocks, int page_size, const int32_t *seq_lens,
+                    const int32_t *next_pos, int bs, int num_kv_heads, int budget, int recent, int max_seq_len,
+                    int capacity, int32_t *src_rows, int32_t *dst_rows, int32_t *counts, int32_t *new_lens,
+                    void *stream);
+
+/* Smallest capacity of the move lists: max(1, min(budget, max_seq_len - budget)).  Host-only arithmetic;
+ * SK_ERR_INVALID for budget < 1 or a negative length. */
+int sk_evict_capacity(int budget, int max_seq_len);
+
+/* Eviction, second step: for every (s, h) and m < counts[s][h], copies row src_rows[s][h][m] of the pages
+ * (K and V of that head), of acc_pages and of pos_pages to row dst_rows[s][h][m].  All moves run at once,
+ * so no row may be both a source and a destination and no destination may be listed twice;
+ * sk_evict_select's lists are so.  Sources keep their contents.  A row outside [0, block_table_stride *
+ * page_size), or a count outside [0, capacity], sets SK_DEV_BAD_SEQ, a block outside [0, num_blocks)
+ * SK_DEV_BAD_BLOCK; such a move is skipped (of a count above the capacity, the listed moves run).
+ * kv_pages [num_blocks, num_kv_heads, 16, 256] bf16 or e4m3fn, 16-byte aligned.  Asynchronous on `stream`,
+ * no allocation, capture safe.  Returns SK_OK or a negative sk_status. */
+int sk_evict_move(const int32_t *src_rows, const int32_t *dst_rows, const int32_t *counts, int capacity, int bs,
+                  int num_kv_heads, int head_dim, const int32_t *block_table, int block_table_stride, int num_blocks,
+                  int page_size, void *kv_pages, int kv_dtype, float *acc_pages, int32_t *pos_pages, void *stream);
+
 /* The whole attention call -- plan (use_plan != 0) or fixed split, split-KV
  * attention, merge -- without any device allocation, for callers that cannot
  * allocate: a host engine that owns all device memory through its own

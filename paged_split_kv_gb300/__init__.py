@@ -23,7 +23,8 @@ __all__ = [
     "paged_decode_attention", "plan_capacity", "sk_plan_capacity", "sk_paged_decode_attention_static",
     "sk_static_scratch_bytes", "sk_reshape_and_cache", "sk_std_to_shuffled", "sk_set_wait_limit",
     "SK_OK", "SK_CACHED", "SK_ERR_TIMEOUT", "SK_KV_BF16", "SK_KV_FP8_E4M3", "SK_DEV_BAD_BLOCK",
-    "SK_DEV_BAD_SEQ", "SK_DEV_TIMEOUT",
+    "SK_DEV_BAD_SEQ", "SK_DEV_TIMEOUT", "sk_rope_frequencies", "sk_rope_and_cache", "sk_evict_capacity",
+    "sk_evict_select", "sk_evict_move", "evict_rows",
 ]
 
 SK_OK = 0
@@ -81,6 +82,18 @@ def lib():
         L.sk_reshape_and_cache.argtypes = [P, P, P, i32, i32, i32, P, i32, f32, f32, i32, i32, P]
         L.sk_std_to_shuffled.restype = i32
         L.sk_std_to_shuffled.argtypes = [P, i32, P, i32, i32, i32, i32, i32, P, P, P]
+        i64, f64, PD = ctypes.c_int64, ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+        L.sk_rope_frequencies.restype = i32
+        L.sk_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, PD, PD]
+        L.sk_rope_and_cache.restype = i32
+        L.sk_rope_and_cache.argtypes = [P, P, P, i64, i64, i64, P, P, i32, i32, f32, P, i32, i32, i32, i32, P, P, i32,
+                                        f32, f32, i32, i32, P, P, P]
+        L.sk_evict_capacity.restype = i32
+        L.sk_evict_capacity.argtypes = [i32, i32]
+        L.sk_evict_select.restype = i32
+        L.sk_evict_select.argtypes = [P, P, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32, P, P, P, P, P]
+        L.sk_evict_move.restype = i32
+        L.sk_evict_move.argtypes = [P, P, P, i32, i32, i32, i32, P, i32, i32, i32, P, i32, P, P, P]
         L.sk_get_device_status.restype = i32
         L.sk_get_device_status.argtypes = [P, i32]
         L.sk_paged_decode_attention_static.restype = i32
@@ -349,6 +362,203 @@ def sk_paged_decode_attention_static(q, kv_pages, block_table, seq_lens, cu_seql
         1 if use_plan else 0, seq_lens.numel(), nt, int(max_q_len), hq, hkv, d, float(sm_scale),
         1 if causal else 0, int(num_sms), int(seg_max), _ptr(out), _ptr(lse), _stream(stream))
     return _check(rc, "sk_paged_decode_attention_static")
+
+
+_ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
+
+
+def _launch(dev, stream, name, call) -> int:
+    """Runs ``call(stream pointer)`` with tensor device ``dev`` current (its streams and status word are
+    per device) and checks the status it returns."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        return _check(call(_stream(stream)), name)
+    with torch.cuda.device(dev):
+        return _check(call(_stream(stream)), name)
+
+
+def _same_device(first, **tensors):
+    """Every tensor lives on ``first``'s CUDA device."""
+    if not first.is_cuda:
+        raise ValueError("the arguments must be CUDA tensors")
+    for name, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be a CUDA tensor on {first.device}, is on {t.device}")
+
+
+def _heads_view(t, name):
+    """[tokens, heads, 128] bf16 whose heads are contiguous; returns the stride between tokens."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bfloat16 [num_tokens, heads, head_dim], is {t.dtype} {tuple(t.shape)}")
+    nt, h, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d != 1) or (sh != d and h != 1):
+        raise ValueError(f"{name} must have contiguous heads, has strides {t.stride()}")
+    return st if nt > 1 else max(st, h * d)
+
+
+def _state_pages(kv_pages, acc_pages, pos_pages):
+    """fp32 weights and int32 positions [NB, H_kv, page] that go with kv_pages."""
+    import torch
+    for t, dt, name in ((acc_pages, torch.float32, "acc_pages"), (pos_pages, torch.int32, "pos_pages")):
+        if t is not None:
+            _need(t, dt, name, 3)
+            _shape(t, kv_pages.shape[:3], name)
+
+
+def sk_rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "plain", factor: float = 1.0,
+                        original_len: float = 0.0, low: float = 1.0, high: float = 32.0, device=None):
+    """Rotary frequencies (float64 [rot_dim / 2] on ``device``) and their attention factor.
+    ``scaling``: "plain", "linear" (w / factor), "base" (a larger base) or "bands" (by the turns a
+    frequency makes in ``original_len`` positions: w / factor up to ``low``, w from ``high`` on)."""
+    import torch
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling {scaling!r}: expected one of {sorted(_ROPE_SCALING)}")
+    out = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    af = ctypes.c_double(1.0)
+    _check(lib().sk_rope_frequencies(int(rot_dim), float(base), _ROPE_SCALING[scaling], float(factor),
+                                     float(original_len), float(low), float(high), out, ctypes.byref(af)),
+           "sk_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64, device=device), af.value
+
+
+def sk_rope_and_cache(q, key, value, positions, freqs, slot_mapping, kv_pages, q_out, *, interleaved: bool = False,
+                      attn_factor: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, acc_pages=None,
+                      pos_pages=None, stream=None) -> int:
+    """Turns q ([num_tokens, num_q_heads, 128] bf16) into ``q_out`` and key by the tokens' ``positions``
+    (int64) and stores key and ``value`` ([num_tokens, num_kv_heads, 128] bf16) into ``kv_pages`` at
+    ``slot_mapping`` (int64, negative = no slot).  q, key and value may be views with a stride between
+    tokens.  ``freqs``: float64 [rot_dim / 2], radians per position (sk_rope_frequencies), rot_dim a
+    multiple of 16; ``interleaved`` pairs (2i, 2i + 1) instead of halves.  ``acc_pages`` (fp32) and
+    ``pos_pages`` (int32), both [num_blocks, num_kv_heads, page], receive 0 and the position of each
+    stored token: the state that eviction works on."""
+    import torch
+    qs, ks, vs = _heads_view(q, "q"), _heads_view(key, "key"), _heads_view(value, "value")
+    nt, hq, d = q.shape
+    hkv = key.shape[1]
+    _shape(key, (nt, hkv, d), "key")
+    _shape(value, (nt, hkv, d), "value")
+    _need(positions, torch.int64, "positions", 1)
+    _need(slot_mapping, torch.int64, "slot_mapping", 1)
+    _shape(positions, (nt,), "positions")
+    _shape(slot_mapping, (nt,), "slot_mapping")
+    _need(freqs, torch.float64, "freqs", 1)
+    _need(q_out, torch.bfloat16, "q_out", 3)
+    _shape(q_out, (nt, hq, d), "q_out")
+    _need(kv_pages, None, "kv_pages", 4)
+    nb, hkv2, page, d2 = kv_pages.shape
+    if hkv2 != hkv or d2 != 2 * d:
+        raise ValueError("kv_pages must be [num_blocks, num_kv_heads, page, 2 * head_dim]")
+    _state_pages(kv_pages, acc_pages, pos_pages)
+    _same_device(q, key=key, value=value, positions=positions, freqs=freqs, slot_mapping=slot_mapping,
+                 kv_pages=kv_pages, q_out=q_out, acc_pages=acc_pages, pos_pages=pos_pages)
+    f = lib().sk_rope_and_cache
+    return _launch(q.device, stream, "sk_rope_and_cache", lambda st: f(
+        q.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs, positions.data_ptr(), freqs.data_ptr(),
+        2 * freqs.numel(), 1 if interleaved else 0, attn_factor, slot_mapping.data_ptr(), nt, hq, hkv, d,
+        q_out.data_ptr(), kv_pages.data_ptr(), _kv_dtype(kv_pages), k_scale, v_scale, nb, page, _ptr(acc_pages),
+        _ptr(pos_pages), st))
+
+
+def sk_evict_capacity(budget: int, max_seq_len: int) -> int:
+    """Smallest length of the move lists (computed by the library)."""
+    return _check(lib().sk_evict_capacity(int(budget), int(max_seq_len)), "sk_evict_capacity")
+
+
+def sk_evict_select(acc_pages, pos_pages, block_table, seq_lens, next_pos, src_rows, dst_rows, counts, new_lens, *,
+                    budget: int, recent: int = 0, max_seq_len: Optional[int] = None, stream=None) -> int:
+    """Which ``budget`` rows of each (sequence, KV head) stay: the rows of the last ``recent`` positions, then
+    those with the largest weight.  Writes the moves that bring the staying rows below row ``budget``
+    (src_rows, dst_rows int32 [bs, num_kv_heads, capacity], counts int32 [bs, num_kv_heads]) and the
+    new lengths; see sk_evict_move.  ``max_seq_len`` bounds the lengths (default: what the block table
+    holds)."""
+    import torch
+    _need(acc_pages, torch.float32, "acc_pages", 3)
+    _need(pos_pages, torch.int32, "pos_pages", 3)
+    _shape(pos_pages, acc_pages.shape, "pos_pages")
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    nb, hkv, page = acc_pages.shape
+    bs = seq_lens.numel()
+    if block_table.shape[0] < bs:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows for {bs} sequences")
+    _need(next_pos, torch.int32, "next_pos", 1)
+    _shape(next_pos, (bs,), "next_pos")
+    _need(src_rows, torch.int32, "src_rows", 3)
+    _need(dst_rows, torch.int32, "dst_rows", 3)
+    _need(counts, torch.int32, "counts", 2)
+    _need(new_lens, torch.int32, "new_lens", 1)
+    cap = src_rows.shape[2]
+    _shape(src_rows, (bs, hkv, cap), "src_rows")
+    _shape(dst_rows, (bs, hkv, cap), "dst_rows")
+    _shape(counts, (bs, hkv), "counts")
+    _shape(new_lens, (bs,), "new_lens")
+    if bs and new_lens.data_ptr() == seq_lens.data_ptr():
+        raise ValueError("new_lens must not be seq_lens itself")
+    _same_device(acc_pages, pos_pages=pos_pages, block_table=block_table, seq_lens=seq_lens, next_pos=next_pos,
+                 src_rows=src_rows, dst_rows=dst_rows, counts=counts, new_lens=new_lens)
+    if max_seq_len is None:
+        max_seq_len = block_table.shape[1] * page
+    f = lib().sk_evict_select
+    return _launch(acc_pages.device, stream, "sk_evict_select", lambda st: f(
+        acc_pages.data_ptr(), pos_pages.data_ptr(), block_table.data_ptr(), block_table.shape[1], nb, page,
+        seq_lens.data_ptr(), next_pos.data_ptr(), bs, hkv, budget, recent, max_seq_len, cap, src_rows.data_ptr(),
+        dst_rows.data_ptr(), counts.data_ptr(), new_lens.data_ptr(), st))
+
+
+def sk_evict_move(src_rows, dst_rows, counts, block_table, kv_pages, acc_pages, pos_pages, *, stream=None) -> int:
+    """Moves rows src_rows to dst_rows (sk_evict_select's lists) of ``kv_pages``, ``acc_pages`` and
+    ``pos_pages``, in place."""
+    import torch
+    _need(src_rows, torch.int32, "src_rows", 3)
+    _need(dst_rows, torch.int32, "dst_rows", 3)
+    _shape(dst_rows, src_rows.shape, "dst_rows")
+    _need(counts, torch.int32, "counts", 2)
+    bs, hkv, cap = src_rows.shape
+    _shape(counts, (bs, hkv), "counts")
+    _need(block_table, torch.int32, "block_table", 2)
+    if block_table.shape[0] < bs:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows for {bs} sequences")
+    _need(kv_pages, None, "kv_pages", 4)
+    nb, hkv2, page, d2 = kv_pages.shape
+    if hkv2 != hkv:
+        raise ValueError(f"kv_pages has {hkv2} KV heads, the move lists {hkv}")
+    if acc_pages is None or pos_pages is None:
+        raise ValueError("acc_pages and pos_pages are required")
+    _state_pages(kv_pages, acc_pages, pos_pages)
+    _same_device(src_rows, dst_rows=dst_rows, counts=counts, block_table=block_table, kv_pages=kv_pages,
+                 acc_pages=acc_pages, pos_pages=pos_pages)
+    f = lib().sk_evict_move
+    return _launch(src_rows.device, stream, "sk_evict_move", lambda st: f(
+        src_rows.data_ptr(), dst_rows.data_ptr(), counts.data_ptr(), cap, bs, hkv, d2 // 2, block_table.data_ptr(),
+        block_table.shape[1], nb, page, kv_pages.data_ptr(), _kv_dtype(kv_pages), acc_pages.data_ptr(),
+        pos_pages.data_ptr(), st))
+
+
+def evict_rows(kv_pages, acc_pages, pos_pages, block_table, seq_lens, next_pos, *, budget: int, recent: int = 0,
+               max_seq_len: Optional[int] = None, workspace=None, stream=None):
+    """One eviction: sk_evict_select and sk_evict_move.  Every sequence longer than ``budget`` is cut down to
+    ``budget`` rows per KV head, in place.  ``workspace`` is an optional dict of preallocated buffers
+    (src_rows, dst_rows, counts) reused across calls of the same shapes.  Returns the new lengths (int32
+    [bs], a new tensor); the pages past them can be handed out again."""
+    import torch
+    bs, hkv, page = seq_lens.numel(), kv_pages.shape[1], kv_pages.shape[2]
+    dev = kv_pages.device
+    if max_seq_len is None:
+        max_seq_len = block_table.shape[1] * page
+    ws = workspace if workspace is not None else {}
+    if "src_rows" not in ws:
+        cap = sk_evict_capacity(budget, max_seq_len)
+        ws["src_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
+        ws["dst_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
+        ws["counts"] = torch.empty((bs, hkv), dtype=torch.int32, device=dev)
+    new_lens = torch.empty_like(seq_lens)
+    sk_evict_select(acc_pages, pos_pages, block_table, seq_lens, next_pos, ws["src_rows"], ws["dst_rows"],
+                    ws["counts"], new_lens, budget=budget, recent=recent, max_seq_len=max_seq_len, stream=stream)
+    sk_evict_move(ws["src_rows"], ws["dst_rows"], ws["counts"], block_table, kv_pages, acc_pages, pos_pages,
+                  stream=stream)
+    return new_lens
 
 
 def sk_get_device_status(stream=None, clear: bool = True) -> int:

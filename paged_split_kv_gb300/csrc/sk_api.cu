@@ -495,6 +495,175 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
     return SK_OK;
 }
 
+int sk_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double low,
+                        double high, double *freqs, double *attn_factor)
+{
+    if (rot_dim < 2 || (rot_dim & 1) || freqs == nullptr)
+        return fail(SK_ERR_INVALID, "sk_rope_frequencies: rot_dim=%d, freqs=%p", rot_dim, (void *)freqs);
+    if (!(base > 1.0 && base < INFINITY) || !(factor >= 1.0 && factor < INFINITY))
+        return fail(SK_ERR_INVALID, "sk_rope_frequencies: base=%g must exceed 1 and factor=%g be at least 1", base,
+                    factor);
+    if (scaling < SK_ROPE_PLAIN || scaling > SK_ROPE_BANDS)
+        return fail(SK_ERR_INVALID, "sk_rope_frequencies: scaling=%d", scaling);
+    if (scaling == SK_ROPE_BASE && rot_dim < 4)
+        return fail(SK_ERR_INVALID, "sk_rope_frequencies: a rescaled base needs rot_dim of 4 or more");
+    if (scaling == SK_ROPE_BANDS && !(original_len > 0.0 && original_len < INFINITY && low >= 0.0 && high > low &&
+                                      high < INFINITY))
+        return fail(SK_ERR_INVALID, "sk_rope_frequencies: original_len=%g low=%g high=%g", original_len, low, high);
+    const double pi2 = 6.283185307179586476925;
+    if (scaling == SK_ROPE_BASE)
+        base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double w = pow(base, -2.0 * i / rot_dim);
+        if (scaling == SK_ROPE_LINEAR) {
+            w /= factor;
+        } else if (scaling == SK_ROPE_BANDS) {
+            double keep = (original_len * w / pi2 - low) / (high - low);
+            keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+            w = (1.0 - keep) * (w / factor) + keep * w;
+        }
+        freqs[i] = w;
+    }
+    if (attn_factor != nullptr)
+        *attn_factor = scaling == SK_ROPE_BANDS ? 0.1 * log(factor) + 1.0 : 1.0;
+    return SK_OK;
+}
+
+int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t q_stride, int64_t key_stride,
+                      int64_t value_stride, const int64_t *positions, const double *freqs, int rot_dim,
+                      int interleaved, float attn_factor, const int64_t *slot_mapping, int num_tokens,
+                      int num_q_heads, int num_kv_heads, int head_dim, void *q_out, void *kv_pages, int kv_dtype,
+                      float k_scale, float v_scale, int num_blocks, int page_size, float *acc_pages,
+                      int32_t *pos_pages, void *stream)
+{
+    if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1)
+        return fail(SK_ERR_INVALID, "sk_rope_and_cache: num_tokens=%d num_q_heads=%d num_kv_heads=%d num_blocks=%d",
+                    num_tokens, num_q_heads, num_kv_heads, num_blocks);
+    if (num_q_heads > (1 << 20) || num_kv_heads > (1 << 20))
+        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: %d query heads, %d kv heads", num_q_heads, num_kv_heads);
+    if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
+        return fail(SK_ERR_INVALID, "sk_rope_and_cache: kv_dtype=%d", kv_dtype);
+    if (head_dim != kHeadDim)
+        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: head_dim=%d (only 128)", head_dim);
+    if (page_size != kPage)
+        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: page_size=%d (only 16)", page_size);
+    if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0)
+        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: rot_dim=%d (multiples of 16 up to 128)", rot_dim);
+    if (!(attn_factor > 0.f && attn_factor < INFINITY))
+        return fail(SK_ERR_INVALID, "sk_rope_and_cache: attn_factor must be positive and finite");
+    if (kv_dtype == SK_KV_FP8_E4M3 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY))
+        return fail(SK_ERR_INVALID, "sk_rope_and_cache: scales must be positive and finite");
+    if (num_tokens == 0)
+        return SK_OK;
+    if (q == nullptr || key == nullptr || value == nullptr || positions == nullptr || freqs == nullptr ||
+        slot_mapping == nullptr || q_out == nullptr || kv_pages == nullptr)
+        return fail(SK_ERR_INVALID, "sk_rope_and_cache: null pointer argument");
+    if (q_stride < (int64_t)num_q_heads * kHeadDim || key_stride < (int64_t)num_kv_heads * kHeadDim ||
+        value_stride < (int64_t)num_kv_heads * kHeadDim || ((q_stride | key_stride | value_stride) & 7))
+        return fail(SK_ERR_INVALID,
+                    "sk_rope_and_cache: token strides %lld, %lld, %lld must cover the heads and be multiples of 8",
+                    (long long)q_stride, (long long)key_stride, (long long)value_stride);
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value) |
+         reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(kv_pages)) & 15)
+        return fail(SK_ERR_INVALID, "sk_rope_and_cache: q, key, value, q_out and kv_pages must be 16-byte aligned");
+    int *status = nullptr;
+    int sms = 0;
+    int rc = status_ptr(&status);
+    if (rc == SK_OK)
+        rc = sm_count(&sms);
+    if (rc != SK_OK)
+        return rc;
+    cudaError_t e = launch_rope_cache(static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(key),
+                                      static_cast<const uint16_t *>(value), q_stride, key_stride, value_stride,
+                                      positions, freqs, slot_mapping, num_tokens, num_q_heads, num_kv_heads, rot_dim,
+                                      interleaved ? 1 : 0, attn_factor, static_cast<uint16_t *>(q_out), kv_pages,
+                                      kv_dtype, k_scale, v_scale, num_blocks, acc_pages, pos_pages, status, sms,
+                                      static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "rope kernel launch");
+    return SK_OK;
+}
+
+int sk_evict_capacity(int budget, int max_seq_len)
+{
+    if (budget < 1 || max_seq_len < 0)
+        return fail(SK_ERR_INVALID, "sk_evict_capacity: budget=%d max_seq_len=%d", budget, max_seq_len);
+    const int over = max_seq_len > budget ? max_seq_len - budget : 0;
+    return over < budget ? (over > 0 ? over : 1) : budget;
+}
+
+int sk_evict_select(const float *acc_pages, const int32_t *pos_pages, const int32_t *block_table,
+                    int block_table_stride, int num_blocks, int page_size, const int32_t *seq_lens,
+                    const int32_t *next_pos, int bs, int num_kv_heads, int budget, int recent, int max_seq_len,
+                    int capacity, int32_t *src_rows, int32_t *dst_rows, int32_t *counts, int32_t *new_lens,
+                    void *stream)
+{
+    if (bs < 1 || bs > 32767 || num_kv_heads < 1 || num_blocks < 1 || block_table_stride < 1)
+        return fail(SK_ERR_INVALID, "sk_evict_select: bs=%d num_kv_heads=%d num_blocks=%d stride=%d", bs, num_kv_heads,
+                    num_blocks, block_table_stride);
+    if (page_size != kPage)
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_select: page_size=%d (only 16)", page_size);
+    if (budget < 1 || recent < 0 || recent > budget || max_seq_len < 0)
+        return fail(SK_ERR_INVALID, "sk_evict_select: budget=%d, recent=%d (at most the budget), max_seq_len=%d",
+                    budget, recent, max_seq_len);
+    if (max_seq_len > kEvictMaxCluster * kEvictMaxChunk)
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_select: max_seq_len=%d above %d", max_seq_len,
+                    kEvictMaxCluster * kEvictMaxChunk);
+    if ((long long)bs * num_kv_heads * kEvictMaxCluster > 0x7FFFFFFFLL)
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_select: %d sequences of %d heads", bs, num_kv_heads);
+    if (capacity < sk_evict_capacity(budget, max_seq_len))
+        return fail(SK_ERR_CAPACITY, "sk_evict_select: capacity=%d below min(budget, max_seq_len - budget) = %d",
+                    capacity, sk_evict_capacity(budget, max_seq_len));
+    if (acc_pages == nullptr || pos_pages == nullptr || block_table == nullptr || seq_lens == nullptr ||
+        next_pos == nullptr || src_rows == nullptr || dst_rows == nullptr || counts == nullptr || new_lens == nullptr)
+        return fail(SK_ERR_INVALID, "sk_evict_select: null pointer argument");
+    int *status = nullptr;
+    const int rc = status_ptr(&status);
+    if (rc != SK_OK)
+        return rc;
+    cudaError_t e = launch_evict_select(acc_pages, pos_pages, block_table, block_table_stride, num_blocks, seq_lens,
+                                        next_pos, bs, num_kv_heads, budget, recent, max_seq_len, capacity, src_rows,
+                                        dst_rows, counts, new_lens, status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "eviction select kernel launch");
+    return SK_OK;
+}
+
+int sk_evict_move(const int32_t *src_rows, const int32_t *dst_rows, const int32_t *counts, int capacity, int bs,
+                  int num_kv_heads, int head_dim, const int32_t *block_table, int block_table_stride, int num_blocks,
+                  int page_size, void *kv_pages, int kv_dtype, float *acc_pages, int32_t *pos_pages, void *stream)
+{
+    if (bs < 1 || bs > 32767 || num_kv_heads < 1 || num_blocks < 1 || block_table_stride < 1 || capacity < 1)
+        return fail(SK_ERR_INVALID, "sk_evict_move: bs=%d num_kv_heads=%d num_blocks=%d stride=%d capacity=%d", bs,
+                    num_kv_heads, num_blocks, block_table_stride, capacity);
+    if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
+        return fail(SK_ERR_INVALID, "sk_evict_move: kv_dtype=%d", kv_dtype);
+    if (head_dim != kHeadDim)
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_move: head_dim=%d (only 128)", head_dim);
+    if (page_size != kPage)
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_move: page_size=%d (only 16)", page_size);
+    if ((long long)bs * num_kv_heads > (1 << 24))
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_move: %d sequences of %d heads", bs, num_kv_heads);
+    if (src_rows == nullptr || dst_rows == nullptr || counts == nullptr || block_table == nullptr ||
+        kv_pages == nullptr || acc_pages == nullptr || pos_pages == nullptr)
+        return fail(SK_ERR_INVALID, "sk_evict_move: null pointer argument");
+    if (reinterpret_cast<uintptr_t>(kv_pages) & 15)
+        return fail(SK_ERR_INVALID, "sk_evict_move: kv_pages must be 16-byte aligned");
+    int *status = nullptr;
+    int sms = 0;
+    int rc = status_ptr(&status);
+    if (rc == SK_OK)
+        rc = sm_count(&sms);
+    if (rc != SK_OK)
+        return rc;
+    cudaError_t e = launch_evict_move(src_rows, dst_rows, counts, capacity, bs, num_kv_heads, block_table,
+                                      block_table_stride, num_blocks, kv_pages, kv_dtype, acc_pages, pos_pages,
+                                      status, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "eviction move kernel launch");
+    return SK_OK;
+}
+
 int sk_get_device_status(void *stream, int clear)
 {
     int *status = nullptr;

@@ -165,6 +165,23 @@ cudaError_t launch_kv_write(const uint16_t *key, const uint16_t *value, const in
 cudaError_t launch_std_to_shuffled(const void *pages, int kv_dtype, const int32_t *ids, int num_ids,
                                    long long num_blocks, int num_kv_heads, void *k_out, void *v_out,
                                    int *status, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16_t *v, long long q_stride,
+                              long long k_stride, long long v_stride, const int64_t *pos, const double *freqs,
+                              const int64_t *slots, int num_tokens, int hq, int hkv, int rot, int interleaved,
+                              float factor, uint16_t *q_out, void *pages, int kv_dtype, float k_scale, float v_scale,
+                              long long num_blocks, float *acc, int32_t *pos_pages, int *status, int num_sms,
+                              cudaStream_t stream);
+// Eviction: one cluster of up to kEvictMaxCluster CTAs selects for a (sequence, head), each CTA keeping the
+// keys of up to kEvictMaxChunk rows in shared memory.
+constexpr int kEvictMaxCluster = 16;
+constexpr int kEvictMaxChunk = 49152;
+cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int32_t *block_table, int bt_stride,
+                                int num_blocks, const int32_t *seq_lens, const int32_t *next_pos, int bs, int hkv,
+                                int budget, int recent, int max_len, int cap, int32_t *src, int32_t *dst,
+                                int32_t *counts, int32_t *new_lens, int *status, cudaStream_t stream);
+cudaError_t launch_evict_move(const int32_t *src, const int32_t *dst, const int32_t *counts, int cap, int bs, int hkv,
+                              const int32_t *block_table, int bt_stride, int num_blocks, void *pages, int kv_dtype,
+                              float *acc, int32_t *pos, int *status, int num_sms, cudaStream_t stream);
 cudaError_t launch_merge(const float *part_o, const float *part_m, const float *part_l,
                          const int32_t *tok_nseg, int fixed_nseg, int num_tokens, int H_q,
                          int seg_max, uint16_t *out, float *lse, cudaStream_t stream);
