@@ -253,6 +253,35 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
                        int num_blocks, int num_kv_heads, int head_dim, int page_size, void *k_shuf,
                        void *v_shuf, void *stream);
 
+/* Attention of a chunk of new tokens over the paged cache: prefill, chunked prefill, a follow-up turn on a
+ * long conversation, cross attention (causal == 0).  The result of sk_paged_decode_attn + sk_merge_segments, by
+ * a kernel for many query rows: the softmax runs over all of a sequence's keys in one pass, without a plan.
+ *
+ *   out[t][hq] = sum_p softmax(score)_p V_p,  lse[t][hq] = log sum_p exp(score_p)
+ * with scores sm_scale * k_scale * <q, k> over the keys that token t sees (the masking, layouts and scales of
+ * sk_paged_decode_attn; the chunk's own keys are already in the pages and counted in seq_lens).  A token that
+ * sees no key gets out = 0 and lse = -inf.  Query lengths may differ and may be 0; max_q_len bounds them (more
+ * sets SK_DEV_BAD_SEQ and skips the sequence, whose rows are then undefined).  num_tokens rows past cu_seqlens_q[bs] are left as they were.
+ *
+ * nsplit CTAs share the keys of each block of 256 query rows (G * q_len rows per sequence and KV head).  With
+ * nsplit > 1 the partial states go through part_o, part_m and part_l (fp32 [num_tokens, nsplit, num_q_heads
+ * (, 128)], as in sk_paged_decode_attn) and the call ends with the merge; then rows past cu_seqlens_q[bs] are
+ * undefined.  With nsplit == 1 the three may be NULL.  sk_prefill_nsplit gives a good number.
+ * q, kv_pages, out and part_o are 16-byte aligned; lse may be NULL.  bf16 pages round the probabilities to
+ * bf16, e4m3fn pages to two e4m3 terms (within 2^-8); sums are fp32.
+ * Returns SK_OK or a negative sk_status. */
+int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                          const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                          const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int nsplit,
+                          float *part_o, float *part_m, float *part_l, void *out, float *lse, void *stream);
+
+/* Number of CTAs that should share the keys of a row block of sk_paged_prefill_attn, 1 to 64, for sequences of
+ * up to max_seq_len keys (an estimate from the number of row blocks and key tiles).  num_sms == 0 takes the
+ * current device's.  Host-only arithmetic.  SK_ERR_INVALID for sizes out of range. */
+int sk_prefill_nsplit(int bs, int num_tokens, int max_q_len, int num_q_heads, int num_kv_heads, int max_seq_len,
+                      int num_sms);
+
 /* How sk_rope_frequencies fits the frequencies w_i = base^(-2 i / rot_dim) to contexts `factor` times
  * longer than the trained ones. */
 typedef enum {

@@ -24,7 +24,8 @@ __all__ = [
     "sk_static_scratch_bytes", "sk_reshape_and_cache", "sk_std_to_shuffled", "sk_set_wait_limit",
     "SK_OK", "SK_CACHED", "SK_ERR_TIMEOUT", "SK_KV_BF16", "SK_KV_FP8_E4M3", "SK_DEV_BAD_BLOCK",
     "SK_DEV_BAD_SEQ", "SK_DEV_TIMEOUT", "sk_rope_frequencies", "sk_rope_and_cache", "sk_evict_capacity",
-    "sk_evict_select", "sk_evict_move", "evict_rows",
+    "sk_evict_select", "sk_evict_move", "evict_rows", "sk_prefill_nsplit",
+    "sk_paged_prefill_attn", "paged_prefill_attention",
 ]
 
 SK_OK = 0
@@ -88,6 +89,11 @@ def lib():
         L.sk_rope_and_cache.restype = i32
         L.sk_rope_and_cache.argtypes = [P, P, P, i64, i64, i64, P, P, i32, i32, f32, P, i32, i32, i32, i32, P, P, i32,
                                         f32, f32, i32, i32, P, P, P]
+        L.sk_prefill_nsplit.restype = i32
+        L.sk_prefill_nsplit.argtypes = [i32] * 7
+        L.sk_paged_prefill_attn.restype = i32
+        L.sk_paged_prefill_attn.argtypes = [P, P, i32, f32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32,
+                                            f32, i32, i32, P, P, P, P, P, P]
         L.sk_evict_capacity.restype = i32
         L.sk_evict_capacity.argtypes = [i32, i32]
         L.sk_evict_select.restype = i32
@@ -459,6 +465,82 @@ def sk_rope_and_cache(q, key, value, positions, freqs, slot_mapping, kv_pages, q
         2 * freqs.numel(), 1 if interleaved else 0, attn_factor, slot_mapping.data_ptr(), nt, hq, hkv, d,
         q_out.data_ptr(), kv_pages.data_ptr(), _kv_dtype(kv_pages), k_scale, v_scale, nb, page, _ptr(acc_pages),
         _ptr(pos_pages), st))
+
+
+def sk_prefill_nsplit(bs: int, num_tokens: int, max_q_len: int, num_q_heads: int, num_kv_heads: int,
+                      max_seq_len: int, num_sms: int = 0) -> int:
+    """CTAs that should share the keys of a block of 256 query rows (computed by the library; ``num_sms`` 0:
+    the current device's)."""
+    return _check(lib().sk_prefill_nsplit(bs, num_tokens, max_q_len, num_q_heads, num_kv_heads, max_seq_len, num_sms),
+                  "sk_prefill_nsplit")
+
+
+def sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse=None, *, max_q_len: int,
+                          sm_scale: float, k_scale: float = 1.0, v_scale: float = 1.0, causal: bool = True,
+                          part_o=None, part_m=None, part_l=None, stream=None) -> int:
+    """Attention of a chunk of new tokens over the paged cache into ``out`` (bf16 [num_tokens, num_q_heads, 128])
+    and ``lse`` (fp32 [num_tokens, num_q_heads], or None).  ``part_o`` (fp32 [num_tokens, nsplit, num_q_heads,
+    128]), ``part_m`` and ``part_l`` split the keys over nsplit CTAs; without them one CTA takes all keys of its
+    rows."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(kv_pages, None, "kv_pages", 4)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
+    _need(out, torch.bfloat16, "out", 3)
+    nt, hq, d, nb, hkv, page, bs = _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
+    _shape(out, (nt, hq, d), "out")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", 2)
+        _shape(lse, (nt, hq), "lse")
+    nsplit = 1
+    if part_o is not None:
+        _need(part_o, torch.float32, "part_o", 4)
+        _need(part_m, torch.float32, "part_m", 3)
+        _need(part_l, torch.float32, "part_l", 3)
+        nsplit = part_o.shape[1]
+        _shape(part_o, (nt, nsplit, hq, d), "part_o")
+        _shape(part_m, (nt, nsplit, hq), "part_m")
+        _shape(part_l, (nt, nsplit, hq), "part_l")
+    _same_device(q, kv_pages=kv_pages, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q, out=out,
+                 lse=lse, part_o=part_o, part_m=part_m, part_l=part_l)
+    f = lib().sk_paged_prefill_attn
+    return _launch(q.device, stream, "sk_paged_prefill_attn", lambda st: f(
+        q.data_ptr(), kv_pages.data_ptr(), _kv_dtype(kv_pages), k_scale, v_scale, block_table.data_ptr(),
+        block_table.shape[1], nb, page, seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), bs, nt, max_q_len, hq, hkv, d,
+        sm_scale, 1 if causal else 0, nsplit, _ptr(part_o), _ptr(part_m), _ptr(part_l), out.data_ptr(), _ptr(lse), st))
+
+
+def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *, max_q_len: int, sm_scale: float,
+                            max_seq_len: Optional[int] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                            causal: bool = True, workspace=None, out=None, lse=None, stream=None):
+    """One attention call of a chunk of new tokens (prompts, chunks of prompts, follow-up turns) over the paged
+    cache.  ``max_seq_len`` bounds seq_lens (default: what the block table holds); it only decides over how many
+    CTAs the keys are split.  ``workspace`` is an optional dict that keeps the split's buffers across calls of
+    the same shapes.  Returns (out bf16 [NT, H_q, 128], lse fp32 [NT, H_q])."""
+    import torch
+    nt, hq, d = q.shape
+    dev = q.device
+    if max_seq_len is None:
+        max_seq_len = block_table.shape[1] * kv_pages.shape[2]
+    if out is None:
+        out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((nt, hq), dtype=torch.float32, device=dev)
+    ws = workspace if workspace is not None else {}
+    key = ("prefill", nt, hq, seq_lens.numel(), max_q_len, max_seq_len)
+    if key not in ws:
+        n = sk_prefill_nsplit(seq_lens.numel(), nt, max_q_len, hq, kv_pages.shape[1], max_seq_len)
+        ws[key] = None if n == 1 else (
+            torch.empty((nt, n, hq, d), dtype=torch.float32, device=dev),
+            torch.empty((nt, n, hq), dtype=torch.float32, device=dev),
+            torch.empty((nt, n, hq), dtype=torch.float32, device=dev))
+    po, pm, pl = ws[key] or (None, None, None)
+    sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, max_q_len=max_q_len,
+                          sm_scale=sm_scale, k_scale=k_scale, v_scale=v_scale, causal=causal, part_o=po, part_m=pm,
+                          part_l=pl, stream=stream)
+    return out, lse
 
 
 def sk_evict_capacity(budget: int, max_seq_len: int) -> int:

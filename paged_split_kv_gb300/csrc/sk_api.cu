@@ -664,6 +664,106 @@ int sk_evict_move(const int32_t *src_rows, const int32_t *dst_rows, const int32_
     return SK_OK;
 }
 
+int sk_prefill_nsplit(int bs, int num_tokens, int max_q_len, int num_q_heads, int num_kv_heads, int max_seq_len,
+                      int num_sms)
+{
+    if (bs < 1 || bs > 32767 || num_tokens < 0 || max_q_len < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
+        num_q_heads % num_kv_heads != 0 || max_seq_len < 0 || num_sms < 0)
+        return fail(SK_ERR_INVALID,
+                    "sk_prefill_nsplit: bs=%d num_tokens=%d max_q_len=%d heads %d/%d max_seq_len=%d num_sms=%d", bs,
+                    num_tokens, max_q_len, num_q_heads, num_kv_heads, max_seq_len, num_sms);
+    if (num_sms == 0) {
+        const int rc = sm_count(&num_sms);
+        if (rc != SK_OK)
+            return rc;
+    }
+    return prefill_nsplit(bs, num_tokens, max_q_len, num_q_heads, num_kv_heads, max_seq_len, num_sms);
+}
+
+int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                          const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                          const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int nsplit,
+                          float *part_o, float *part_m, float *part_l, void *out, float *lse, void *stream)
+{
+    if (q == nullptr || kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr ||
+        cu_seqlens_q == nullptr || out == nullptr)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: null pointer argument");
+    if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: kv_dtype=%d", kv_dtype);
+    if (head_dim != kHeadDim)
+        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: head_dim=%d (only 128)", head_dim);
+    if (page_size != kPage)
+        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: page_size=%d (only 16)", page_size);
+    if (bs < 1 || bs > 32767)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: bs=%d outside [1, 32767]", bs);
+    if (num_tokens < 0 || max_q_len < 0 || (num_tokens > 0 && max_q_len < 1) || block_table_stride < 1 ||
+        num_blocks < 1)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: num_tokens=%d max_q_len=%d stride=%d num_blocks=%d",
+                    num_tokens, max_q_len, block_table_stride, num_blocks);
+    if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: %d query heads, %d kv heads", num_q_heads, num_kv_heads);
+    if (nsplit < 1 || nsplit > 0xFFFF)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: nsplit=%d outside [1, 65535]", nsplit);
+    if (nsplit > 1 && (part_o == nullptr || part_m == nullptr || part_l == nullptr))
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: nsplit=%d needs part_o, part_m and part_l", nsplit);
+    if (!(sm_scale > 0.f && sm_scale < INFINITY) ||
+        (kv_dtype == SK_KV_FP8_E4M3 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY)))
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: scales must be positive and finite");
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(kv_pages) | reinterpret_cast<uintptr_t>(out) |
+         reinterpret_cast<uintptr_t>(part_o)) & 15)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: q, kv_pages, out and part_o must be 16-byte aligned");
+    const int G = num_q_heads / num_kv_heads;
+    const long long rows = (long long)G * max_q_len;
+    const long long blocks = (rows + kPrefillRows - 1) / kPrefillRows;
+    if (rows > 0x3FFFFFFFLL || blocks * nsplit * num_kv_heads > 0x7FFFFFFFLL / bs ||
+        (long long)num_blocks * num_kv_heads * 2 > 0x7FFFFFFFLL)
+        return fail(SK_ERR_UNSUPPORTED,
+                    "sk_paged_prefill_attn: %lld rows, %d splits, %d sequences and %d blocks of %d heads exceed the "
+                    "kernel's limits (2^31 CTAs, 2^30 block-heads)",
+                    rows, nsplit, bs, num_blocks, num_kv_heads);
+    if (num_tokens == 0)
+        return SK_OK;
+    int *status = nullptr;
+    int rc = status_ptr(&status);
+    if (rc != SK_OK)
+        return rc;
+    PrefillParams p;
+    p.q = static_cast<const uint16_t *>(q);
+    p.kv = kv_pages;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.cu_q = cu_seqlens_q;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.part_o = part_o;
+    p.part_m = part_m;
+    p.part_l = part_l;
+    p.status = status;
+    p.num_blocks = num_blocks;
+    p.bt_stride = block_table_stride;
+    p.bs = bs;
+    p.num_tokens = num_tokens;
+    p.max_q_len = max_q_len;
+    p.H_q = num_q_heads;
+    p.H_kv = num_kv_heads;
+    p.G = G;
+    p.row_blocks = (int)blocks;
+    p.nsplit = nsplit;
+    p.causal = causal ? 1 : 0;
+    const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
+    p.score_scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
+    p.v_scale = fp8 ? v_scale : 1.f;
+    p.wait_limit = wait_limit();
+    cudaError_t e = launch_prefill(p, kv_dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "chunk attention kernel launch");
+    if (nsplit > 1)
+        return sk_merge_segments(part_o, part_m, part_l, nullptr, nsplit, num_tokens, num_q_heads, head_dim, nsplit,
+                                 out, lse, stream);
+    return SK_OK;
+}
+
 int sk_get_device_status(void *stream, int clear)
 {
     int *status = nullptr;

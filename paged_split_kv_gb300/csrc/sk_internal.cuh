@@ -165,6 +165,28 @@ cudaError_t launch_kv_write(const uint16_t *key, const uint16_t *value, const in
 cudaError_t launch_std_to_shuffled(const void *pages, int kv_dtype, const int32_t *ids, int num_ids,
                                    long long num_blocks, int num_kv_heads, void *k_out, void *v_out,
                                    int *status, int num_sms, cudaStream_t stream);
+// Attention of a chunk of new tokens, resolved on the host.
+struct PrefillParams {
+    const uint16_t *q;           // bf16 bits [NT, H_q, D]
+    const void *kv;              // pages
+    const int32_t *block_table, *seq_lens, *cu_q;
+    uint16_t *out;               // nsplit == 1: bf16 bits [NT, H_q, D]
+    float *lse;                  // nsplit == 1: [NT, H_q] or NULL
+    float *part_o, *part_m, *part_l;   // nsplit > 1: [NT, nsplit, H_q(, D)]
+    int *status;
+    int64_t num_blocks;
+    int bt_stride, bs, num_tokens, max_q_len;
+    int H_q, H_kv, G;
+    int row_blocks;              // blocks of 256 rows that a sequence of max_q_len tokens has
+    int nsplit;                  // CTAs that share the keys of a row block
+    int causal;
+    float score_scale_log2;      // sm_scale * k_scale * log2(e)
+    float v_scale;
+    long long wait_limit;
+};
+constexpr int kPrefillRows = 256;
+int prefill_nsplit(int bs, int num_tokens, int max_q_len, int H_q, int H_kv, int max_seq_len, int num_sms);
+cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, cudaStream_t stream);
 cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16_t *v, long long q_stride,
                               long long k_stride, long long v_stride, const int64_t *pos, const double *freqs,
                               const int64_t *slots, int num_tokens, int hq, int hkv, int rot, int interleaved,

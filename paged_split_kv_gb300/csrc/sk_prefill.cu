@@ -1,0 +1,664 @@
+// Attention of a chunk of new tokens over the paged cache (bf16 or e4m3 pages) on the tcgen05 tensor cores.
+//
+// For the rows r = j * G + i (query token j, head i of the group) of one (sequence, KV head):
+//     S = scale Q K^T over the keys p <= L - q + j,   O = softmax(S) V,   lse = log sum exp S
+// with one pass over the keys: a running reference maximum and sum per row, O rescaled when the reference moves.
+//
+// Bound by the tensor cores: 4 * 128 flops per (row, key) against 512 bytes of K and V per key that 256 rows
+// share.  One CTA takes 256 rows as two tiles A and B of 128 (the MMA's M) and streams the keys in tiles of
+// 128 (its N): while the softmax of one row tile runs, the products of the other fill the tensor pipe.  In
+// issue order, for key tile j:
+//     O_A += P_A(j) V(j);  S_A = Q_A K(j+1)^T;  O_B += P_B(j) V(j);  S_B = Q_B K(j+1)^T
+// S_A, S_B, O_A and O_B fill the 512 TMEM columns; P overwrites the first half of its S as bf16 (or as two e4m3
+// terms) and is the A operand of PV straight from TMEM, so probabilities never pass through shared memory.
+// A row is one TMEM lane and so one thread: the row's maximum and sum need no exchange between threads.
+//
+// Roles (384 threads):
+//   warp 0      copies: K and V of a key tile apart, 32 KB (16 KB e4m3) slots, one TMA copy per page and part, so
+//               the ring holds two and a half (five) key tiles beside Q
+//   warp 1      allocates TMEM, issues every product through one elected lane
+//   warps 4-7   Q tile A into shared memory; softmax of A, its rescaling, its output
+//   warps 8-11  the same for B
+// S(j) complete implies PV(j - 1) complete (products of a CTA complete in issue order), so the softmax may rescale O
+// at once; it does so only when a score beats the reference by 2^8 (2^4 for e4m3).
+//
+// e4m3 pages: both products run as kind::f8f6f4 on the codes.  Q is two e4m3 terms with a power-of-two scale per row
+// (exact for bf16 elements within 2^-9 of the row's largest), as two products into one S; P is p * 2^4 = hi + lo
+// (within 2^-8), as two products into one O.
+//
+// Few row tiles on a long axis: the keys of every row tile are split over `nsplit` CTAs that write partial
+// softmax states, joined by the library's merge.
+//
+// Every wait is bounded as in the decode kernel: on expiry SK_DEV_TIMEOUT is set and every role gives up; the
+// producer waits for its copies and the issuer for its last commit before the CTA exits.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "sk_attn_util.cuh"
+#include "sk_internal.cuh"
+#include "sk_sm100.cuh"
+
+namespace sk {
+namespace {
+
+using namespace sm100;
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kRows = 128;                           // rows of one tile (MMA M)
+constexpr int kKeys = 128;                           // keys of one tile (MMA N)
+constexpr int kThreads = 384;
+constexpr long long kDrainLimit = 4000000000LL;      // cycles (~2 s): waits for work already issued
+constexpr int kMaxSmem = 232448;
+// registers per thread after the reallocation: copies and products, softmax (3 x 168 at launch)
+constexpr int kRegsIssue = 72, kRegsSoftmax = 208;
+
+template <bool FP8>
+struct PCfg {
+    static constexpr int kQTile = kRows * 256;                     // bf16: two 64-dimension chunks; e4m3: hi and lo
+    static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K (or V) of 8 tokens
+    static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
+    static constexpr int kMisc = 3072;
+    static constexpr int kSlots = (kMaxSmem - 2 * kQTile - kMisc) / kSlotBytes;
+    static constexpr int kOffQ = kSlots * kSlotBytes;
+    static constexpr int kOffMisc = kOffQ + 2 * kQTile;
+    static constexpr int kSmemBytes = kOffMisc + kMisc;
+    static constexpr int kPagesPerTile = kKeys / kPage;
+    static constexpr float kThrLog2 = FP8 ? 4.0f : 8.0f;
+    static constexpr int kPShift = FP8 ? 4 : 0;
+    // misc area
+    static constexpr int kBarFull = 0;
+    static constexpr int kBarEmpty = 8 * kSlots;
+    static constexpr int kBarQ = 16 * kSlots;                      // [2]
+    static constexpr int kBarS = kBarQ + 16;                       // [2] S complete
+    static constexpr int kBarP = kBarS + 16;                       // [2] P written
+    static constexpr int kBarO = kBarP + 16;                       // [2] last PV complete
+    static constexpr int kBarDrain = kBarO + 16;
+    static constexpr int kTmemSlot = kBarDrain + 8;
+    static constexpr int kAbort = kTmemSlot + 4;
+    static constexpr int kCrow = 512;                              // float[256]: score scale of each row (e4m3)
+    static_assert(kAbort + 4 <= kCrow && kCrow + 1024 <= kMisc, "misc area");
+    static_assert(kSlots >= 3 && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0, "shared memory");
+};
+
+// TMEM map (columns)
+constexpr int kColS = 0, kColO = 256;                // S_A, S_B, then O_A, O_B, 128 each
+
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p)
+{
+    using C = PCfg<FP8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+
+    wait_prior_grid();
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_q + p.bs) != p.num_tokens))
+        atomicOr(p.status, SK_DEV_BAD_SEQ);
+    // row blocks of one (sequence, head) are neighbours, the longest first, so that they share K and V in L2
+    int b = blockIdx.x;
+    const int g = b % p.nsplit;
+    b /= p.nsplit;
+    const int rb = p.row_blocks - 1 - b % p.row_blocks;
+    b /= p.row_blocks;
+    const int h = b % p.H_kv;
+    const int s = b / p.H_kv;
+    const int L = __ldg(p.seq_lens + s);
+    const int tok0 = __ldg(p.cu_q + s);
+    const int q_len = __ldg(p.cu_q + s + 1) - tok0;
+    const uint32_t sbase = smem_u32(smem);
+    if (q_len < 0 || q_len > p.max_q_len || tok0 < 0 || tok0 + q_len > p.num_tokens || L < 0 ||
+        (long long)L > (long long)p.bt_stride * kPage || (sbase & 1023u) != 0) {
+        if (threadIdx.x == 0)
+            atomicOr(p.status, (sbase & 1023u) != 0 ? SK_DEV_INTERNAL : SK_DEV_BAD_SEQ);
+        return;
+    }
+    const int R_all = p.G * q_len;
+    const int row0 = rb * 2 * kRows;
+    if (row0 >= R_all)
+        return;
+    const int rowsA = min(kRows, R_all - row0), rowsB = max(0, min(kRows, R_all - row0 - kRows));
+
+    // key tiles: the row block's tiles are cut into nsplit ranges; a row tile stops where its last row does
+    auto tiles_of = [&](int first, int rows) {
+        if (rows <= 0)
+            return 0;
+        return (visible_keys(L, q_len, (first + rows - 1) / p.G, p.causal) + kKeys - 1) / kKeys;
+    };
+    const int tA = tiles_of(row0, rowsA), tB = tiles_of(row0 + kRows, rowsB);
+    const int t_all = max(tA, tB);
+    const int t0 = (int)((long long)t_all * g / p.nsplit), t1 = (int)((long long)t_all * (g + 1) / p.nsplit);
+    const int nA = max(0, min(t1, tA) - t0), nB = max(0, min(t1, tB) - t0);
+    const int n = max(nA, nB);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *misc = smem + C::kOffMisc;
+    const uint32_t mbase = sbase + C::kOffMisc;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + C::kAbort);
+    auto bar_full = [&](int i) { return mbase + C::kBarFull + 8 * i; };
+    auto bar_empty = [&](int i) { return mbase + C::kBarEmpty + 8 * i; };
+    auto bar_q = [&](int x) { return mbase + C::kBarQ + 8 * x; };
+    auto bar_s = [&](int x) { return mbase + C::kBarS + 8 * x; };
+    auto bar_p = [&](int x) { return mbase + C::kBarP + 8 * x; };
+    auto bar_o = [&](int x) { return mbase + C::kBarO + 8 * x; };
+    const uint32_t bar_drain = mbase + C::kBarDrain;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(bar_full(i), 1);
+            mbar_init(bar_empty(i), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar_q(x), 4);
+            mbar_init(bar_s(x), 1);
+            mbar_init(bar_p(x), 4);
+            mbar_init(bar_o(x), 1);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(mbase + C::kTmemSlot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc + C::kTmemSlot);
+
+    if (warp < 4) {
+        reg_dec<kRegsIssue>();
+        if (warp == 0) {
+            // ============================================================ copies
+            // slot i holds, in turn, K(0), V(0), K(1), V(1), ...
+            if (lane == 0)
+                prefetch_tensormap(&kv_map);
+            const int page0 = t0 * C::kPagesPerTile, page_end = (L + kPage - 1) / kPage;
+            const int32_t *bt = p.block_table + (long long)s * p.bt_stride;
+            auto block_at = [&](int j) {
+                const int pg = page0 + j * C::kPagesPerTile + lane;
+                return (lane < C::kPagesPerTile && j < n && pg < page_end) ? __ldg(bt + pg) : -1;
+            };
+            int blk = block_at(0), blk1 = block_at(1);
+            int issued = 0;
+            bool ok = true;
+            for (int u = 0; u < 2 * n && ok; ++u) {
+                const int j = u >> 1, part = u & 1, i = u % C::kSlots;
+                if (u >= C::kSlots)
+                    ok = mbar_wait_bounded(bar_empty(i), (u / C::kSlots - 1) & 1, abort_flag, p.wait_limit);
+                ok = __all_sync(kFull, ok);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar_full(i), C::kSlotBytes);
+                __syncwarp();
+                if (lane < C::kPagesPerTile) {
+                    int grp = -2;                    // whole box out of bounds: zero fill
+                    if (page0 + j * C::kPagesPerTile + lane < page_end) {
+                        if (blk >= 0 && blk < p.num_blocks)
+                            grp = (blk * p.H_kv + h) * 2;
+                        else
+                            atomicOr(p.status, SK_DEV_BAD_BLOCK);
+                    }
+                    tma_load_4d(sbase + i * C::kSlotBytes + lane * 2 * C::kGroupBytes, &kv_map, 0, 0,
+                                part * (FP8 ? 1 : 2), grp, bar_full(i));
+                }
+                issued = u + 1;
+                if (part) {
+                    blk = blk1;
+                    blk1 = block_at(j + 2);
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                if (lane == 0)
+                    atomicOr(p.status, SK_DEV_TIMEOUT);
+            }
+            // every copy issued lands before the CTA exits
+            for (int u = issued > C::kSlots ? issued - C::kSlots : 0; u < issued; ++u)
+                mbar_wait_bounded(bar_full(u % C::kSlots), (u / C::kSlots) & 1, nullptr, kDrainLimit);
+        } else if (warp == 1) {
+            // ============================================================ products
+            constexpr uint32_t idesc_qk = FP8 ? idesc_e4m3_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
+            constexpr uint32_t idesc_pv = FP8 ? idesc_e4m3_f32(kRows, kHeadDim, 0, 1)
+                                              : idesc_bf16_f32(kRows, kHeadDim, 0, 1);
+            const uint64_t d_k0 = smem_desc_sw128(sbase, 16, C::kGroupBytes);       // K-major K
+            const uint64_t d_v0 = smem_desc_sw128(sbase, 1024, C::kGroupBytes);     // dimension-major V
+            const uint64_t d_q0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);      // K-major Q
+            auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
+            bool ok = true;
+            int issued = 0;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (ok)
+                    ok = mbar_wait_bounded(bar, parity, abort_flag, p.wait_limit);
+                ok = __all_sync(kFull, ok);
+                if (ok)
+                    tc_fence_after();
+                return ok;
+            };
+            auto wait_slot = [&](int u) { return wait(bar_full(u % C::kSlots), (u / C::kSlots) & 1); };
+            auto qk = [&](int x, int j) {
+                const uint32_t so = (uint32_t)(2 * j % C::kSlots) * C::kSlotBytes, qo = x * C::kQTile;
+                const uint32_t sd = tmem + kColS + x * 128;
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f8_ss_warp(sd, adv(d_q0, qo + t * (kRows * 128) + k * 32), adv(d_k0, so + k * 32),
+                                           idesc_qk, (t > 0 || k > 0) ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_ss_warp(sd, adv(d_q0, qo + (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                                        adv(d_k0, so + (k >> 2) * 1024 + (k & 3) * 32), idesc_qk, k > 0 ? 1u : 0u);
+                }
+                mma_commit_warp(bar_s(x));
+                issued = 1;
+            };
+            auto pv = [&](int x, int j) {
+                const uint32_t so = (uint32_t)((2 * j + 1) % C::kSlots) * C::kSlotBytes;
+                const uint32_t od = tmem + kColO + x * 128, pa = tmem + kColS + x * 128;
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f8_ts_warp(od, pa + t * 32 + k * 8, adv(d_v0, so + k * 4 * C::kGroupBytes), idesc_pv,
+                                           (j > 0 || t > 0 || k > 0) ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_ts_warp(od, pa + k * 8, adv(d_v0, so + k * 2 * C::kGroupBytes), idesc_pv,
+                                        (j > 0 || k > 0) ? 1u : 0u);
+                }
+            };
+            if (n > 0) {
+                if (nA > 0)
+                    wait(bar_q(0), 0);
+                if (nB > 0)
+                    wait(bar_q(1), 0);
+                if (wait_slot(0)) {
+                    if (nA > 0)
+                        qk(0, 0);
+                    if (nB > 0)
+                        qk(1, 0);
+                    mma_commit_warp(bar_empty(0));
+                }
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                if (!wait_slot(2 * j + 1))
+                    break;
+                // a slot is free once the last product that reads it is: B's where B has the tile
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int nx = x ? nB : nA;
+                    if (!ok || j >= nx)
+                        continue;
+                    if (!wait(bar_p(x), j & 1))
+                        continue;
+                    pv(x, j);
+                    if (j + 1 == nx)
+                        mma_commit_warp(bar_o(x));
+                    if (x == 1 || j >= nB)
+                        mma_commit_warp(bar_empty((2 * j + 1) % C::kSlots));
+                    if (j + 1 < nx) {
+                        if (!wait_slot(2 * j + 2))
+                            continue;
+                        qk(x, j + 1);
+                        if (x == 1 || j + 1 >= nB)
+                            mma_commit_warp(bar_empty((2 * j + 2) % C::kSlots));
+                    }
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                if (lane == 0)
+                    atomicOr(p.status, SK_DEV_TIMEOUT);
+            }
+            // every product completes before TMEM is freed and shared memory is left
+            if (issued) {
+                mma_commit_warp(bar_drain);
+                mbar_wait_bounded(bar_drain, 0, nullptr, kDrainLimit);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================================================================ softmax of row tile x
+        reg_inc<kRegsSoftmax>();
+        const int x = (warp >> 2) - 1;
+        const int quarter = warp & 3;
+        const int tau = quarter * 32 + lane;                       // row of the tile, TMEM lane
+        const int nx = x ? nB : nA;
+        const int rows = x ? rowsB : rowsA;
+        const int rx0 = row0 + x * kRows;                          // first row of the tile
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tmem + kColS + x * 128 + lane_off, to = tmem + kColO + x * 128 + lane_off;
+        float *crow = reinterpret_cast<float *>(misc + C::kCrow) + x * kRows;
+
+        // ---- Q rows of this warp into shared memory (K-major, 128-byte swizzle); zeros past the rows
+        uint8_t *qs = smem + C::kOffQ + x * C::kQTile;
+        if (nx > 0) {
+            if constexpr (!FP8) {
+#pragma unroll
+                for (int k0 = 0; k0 < 16; k0 += 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = quarter * 32 + (k0 + k) * 2 + (lane >> 4), unit = lane & 15;
+                        v[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < rows) {
+                            const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
+                            v[k] = __ldg(reinterpret_cast<const uint4 *>(
+                                p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + unit * 8));
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = quarter * 32 + (k0 + k) * 2 + (lane >> 4), unit = lane & 15;
+                        *reinterpret_cast<uint4 *>(qs + (unit >> 3) * (kRows * 128) + r * 128 +
+                                                   (((unit & 7) ^ (r & 7)) << 4)) = v[k];
+                    }
+                }
+            } else {
+                for (int k0 = 0; k0 < 32; k0 += 8) {
+                    uint2 raw[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = quarter * 32 + k0 + k;
+                        raw[k] = make_uint2(0u, 0u);
+                        if (r < rows) {
+                            const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
+                            raw[k] = __ldg(reinterpret_cast<const uint2 *>(
+                                p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + lane * 4));
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = quarter * 32 + k0 + k;
+                        uint32_t hi, lo;
+                        int e;
+                        split_q_row(raw[k], hi, lo, e);
+                        const uint32_t off = (uint32_t)(r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
+                        *reinterpret_cast<uint32_t *>(qs + off) = hi;
+                        *reinterpret_cast<uint32_t *>(qs + kRows * 128 + off) = lo;
+                        if (lane == 0)
+                            crow[r] = p.score_scale_log2 * ldexpf(1.f, -e);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_q(x));
+        }
+        const float c = FP8 ? (nx > 0 ? crow[tau] : 0.f) : p.score_scale_log2;
+
+        const int r = rx0 + tau;                                   // this thread's row
+        const int jq = r / p.G, iq = r - jq * p.G;
+        const bool live = tau < rows;
+        const int limit = live ? visible_keys(L, q_len, jq, p.causal) : 0;
+        float m_ref = -CUDART_INF_F, m_thr = -CUDART_INF_F;
+        float2 l2 = make_float2(0.f, 0.f);
+        bool failed = false;
+        for (int j = 0; j < nx; ++j) {
+            const int key0 = (t0 + j) * kKeys;
+            bool ok = mbar_wait_bounded(bar_s(x), j & 1, abort_flag, p.wait_limit);
+            ok = __all_sync(kFull, ok);
+            if (!ok) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            float v[128];
+#pragma unroll
+            for (int cc = 0; cc < 128; cc += 32)
+                tmem_ld32<32>(ts + cc, v + cc);
+            tmem_wait_ld();
+            const int lim = limit - key0;                          // columns [0, lim) are visible
+            if (!__all_sync(kFull, lim >= kKeys)) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    v[i] = i < lim ? v[i] : -CUDART_INF_F;
+            }
+            float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int i = 4; i < 124; i += 8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mx[k] = fmax3(mx[k], v[i + k], v[i + 4 + k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mx[k] = fmaxf(mx[k], v[124 + k]);
+            const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c;
+            if (__any_sync(kFull, top > m_thr)) {
+                const float mn = fmaxf(m_ref, top);
+                const float alpha = m_ref == -CUDART_INF_F ? 0.f : exp2f(m_ref - mn);
+                m_ref = mn;
+                m_thr = mn + C::kThrLog2;
+                l2.x *= alpha;
+                l2.y *= alpha;
+                if (j > 0) {
+#pragma unroll
+                    for (int cc = 0; cc < 128; cc += 32) {
+                        float o[32];
+                        tmem_ld32<32>(to + cc, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] *= alpha;
+                        tmem_st32<32>(to + cc, o);
+                    }
+                }
+            }
+            const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref - (float)C::kPShift;
+            const float2 c2 = make_float2(c, c), s2 = make_float2(-msub, -msub);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int k = hf * 64 + 2 * i;
+                    const float2 d = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
+                    const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
+                    l2 = fadd2(l2, e);
+                    pk[i] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                }
+                if constexpr (FP8) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t a = pk[2 * i], bb = pk[2 * i + 1];
+                        const uint32_t ah = a & 0xFF80FF80u, bh = bb & 0xFF80FF80u;     // 3 fraction bits
+                        hi[i] = e4m3x4_from_f16x2(ah, bh);
+                        lo[i] = e4m3x4_from_f16x2(hsub2(a, ah), hsub2(bb, bh));
+                    }
+                    tmem_st32_u<16>(ts + hf * 16, hi);
+                    tmem_st32_u<16>(ts + 32 + hf * 16, lo);
+                } else {
+                    tmem_st32_u<32>(ts + hf * 32, pk);
+                }
+            }
+            tmem_wait_st();
+            // rows past the sequence's end in its last page hold anything, and 0 * NaN would reach O: their V
+            // becomes zeros, by the first row tile that multiplies it
+            if ((x == 0 || j >= nA) && L < key0 + kKeys && (L & (kPage - 1)) != 0) {
+                ok = mbar_wait_bounded(bar_full((2 * j + 1) % C::kSlots), ((2 * j + 1) / C::kSlots) & 1, abort_flag,
+                                       p.wait_limit);
+                ok = __all_sync(kFull, ok);
+                const int tok = key0 + tau;
+                if (ok && tok >= L && tok < (L + kPage - 1) / kPage * kPage) {
+                    uint8_t *row = smem + (2 * j + 1) % C::kSlots * C::kSlotBytes + (tau >> 3) * C::kGroupBytes +
+                                   (tau & 7) * 128;
+#pragma unroll
+                    for (int cc = 0; cc < C::kGroupBytes / 1024; ++cc)
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            *reinterpret_cast<uint4 *>(row + cc * 1024 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                if (!ok) {
+                    failed = true;
+                    break;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_p(x));
+        }
+        if (!failed && nx > 0) {
+            bool ok = mbar_wait_bounded(bar_o(x), 0, abort_flag, p.wait_limit);
+            failed = !__all_sync(kFull, ok);
+        }
+        if (failed) {
+            *abort_flag = 1;
+        } else if (rows > 0) {
+            tc_fence_after();
+            const float l = l2.x + l2.y;
+            const long long qrow = (long long)(tok0 + jq) * p.H_q + h * p.G + iq;
+            const long long slot = ((long long)(tok0 + jq) * p.nsplit + g) * p.H_q + h * p.G + iq;
+            const float mul = p.nsplit > 1 ? p.v_scale * (FP8 ? 0x1p-4f : 1.f) : (l == 0.f ? 0.f : p.v_scale / l);
+#pragma unroll
+            for (int cc = 0; cc < 128; cc += 32) {
+                float o[32];
+                if (nx > 0) {
+                    tmem_ld32<32>(to + cc, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    o[i] = (nx > 0 && !(l == 0.f)) ? o[i] * mul : 0.f;
+                if (!live)
+                    continue;
+                if (p.nsplit > 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4 *>(p.part_o + slot * kHeadDim + cc + i) =
+                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4 *>(p.out + qrow * kHeadDim + cc + i) =
+                            make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
+                                       pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
+                }
+            }
+            if (live) {
+                const float ln2 = 0.69314718055994531f;
+                const float lt = FP8 ? l * 0x1p-4f : l;            // the sum without P's shift
+                if (p.nsplit > 1) {
+                    p.part_m[slot] = lt > 0.f ? m_ref * ln2 : -CUDART_INF_F;
+                    p.part_l[slot] = lt;
+                } else if (p.lse != nullptr) {
+                    p.lse[qrow] = l == 0.f ? -CUDART_INF_F : m_ref * ln2 + logf(lt);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool FP8>
+cudaError_t launch_t(const CUtensorMap &map, const PrefillParams &p, cudaStream_t stream)
+{
+    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               PCfg<FP8>::kSmemBytes);
+    if (e != cudaSuccess)
+        return e;
+    // the warpgroups' shares after the reallocation may not exceed what the CTA was launched with
+    static const int regs = [] {
+        cudaFuncAttributes a{};
+        return cudaFuncGetAttributes(&a, prefill_kernel<FP8>) == cudaSuccess ? a.numRegs : 0;
+    }();
+    if (3 * regs < kRegsIssue + 2 * kRegsSoftmax)
+        return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)p.nsplit * p.row_blocks * p.H_kv * p.bs);
+    return launch_pdl(prefill_kernel<FP8>, grid, dim3(kThreads), PCfg<FP8>::kSmemBytes, stream, map, p);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+}  // namespace
+
+cudaError_t encode_page_map(CUtensorMap *map, const void *pages, long long num_blocks, int H_kv, bool fp8, int chunks)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr)
+        return cudaErrorNotSupported;
+    const cuuint64_t row_bytes = (cuuint64_t)(2 * kHeadDim * (fp8 ? 1 : 2));
+    const cuuint64_t dims[4] = {(cuuint64_t)(fp8 ? 128 : 64), 8, row_bytes / 128, (cuuint64_t)num_blocks * H_kv * 2};
+    const cuuint64_t strides[3] = {row_bytes, 128, 8 * row_bytes};
+    const cuuint32_t box[4] = {fp8 ? 128u : 64u, 8, (cuuint32_t)chunks, 2};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<void *>(pages), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// CTAs that share the keys of a row block: the number with the least estimated time.  A CTA takes `kFixed` to start
+// and finish and `kTile` per key tile; `units` row blocks run num_sms at a time; a split adds the merge, which reads
+// what the partial states' writes left (520 bytes per row, head and split, both ways).  More CTAs even out the last
+// round of row blocks, or, when there are fewer than SMs, fill the GPU.
+int prefill_nsplit(int bs, int num_tokens, int max_q_len, int H_q, int H_kv, int max_seq_len, int num_sms)
+{
+    constexpr double kFixed = 4.0, kTile = 1.4, kMerge = 3.0, kBytesPerUs = 4e6;
+    const long long rows = (long long)(H_q / H_kv) * max_q_len;
+    const long long units = (rows + kPrefillRows - 1) / kPrefillRows * H_kv * bs;
+    const int tiles = (max_seq_len + kKeys - 1) / kKeys;
+    int best = 1;
+    double best_t = 1e300;
+    for (int n = 1; n <= 64 && (n == 1 || n <= tiles); ++n) {
+        const long long waves = (units * n + num_sms - 1) / num_sms;
+        double t = waves * (kFixed + kTile * ((tiles + n - 1) / n));
+        if (n > 1)
+            t += kMerge + 2.0 * n * num_tokens * H_q * 520.0 / kBytesPerUs;
+        if (t < best_t * (n > 1 ? 0.97 : 1.0)) {
+            best_t = t;
+            best = n;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, cudaStream_t stream)
+{
+    const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
+    CUtensorMap map;
+    // one box: K (or V) of one page and head
+    const cudaError_t e = encode_page_map(&map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 1 : 2);
+    if (e != cudaSuccess)
+        return e;
+    return fp8 ? launch_t<true>(map, p, stream) : launch_t<false>(map, p, stream);
+}
+
+}  // namespace sk
