@@ -282,6 +282,30 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
 int sk_prefill_nsplit(int bs, int num_tokens, int max_q_len, int num_q_heads, int num_kv_heads, int max_seq_len,
                       int num_sms);
 
+/* Attention weight gathered by each cached key: for every sequence s, KV head h and key p < seq_lens[s],
+ *   acc_pages (place of p) += sum over query tokens t of s that see p, and heads hq of the group of h, of
+ *                             exp(score(t, hq, p) - lse[t][hq])
+ * with the scores and the masking of sk_paged_decode_attn (max_q_len as there) and `lse` as written by the
+ * attention calls (fp32 [num_tokens, num_q_heads], natural logarithm): each (t, hq) adds weights that sum to 1
+ * over its keys.  A row whose lse is -inf adds nothing.  Places of no key, and those of blocks outside
+ * [0, num_blocks) (which set SK_DEV_BAD_BLOCK), are left as they were.  Where sequences share a block, all add to
+ * it (in no fixed order; otherwise the same bits every time).
+ *
+ * acc_pages fp32 [num_blocks, num_kv_heads, page_size], updated in place.  workspace (device, 16-byte aligned):
+ * sk_accum_workspace_bytes(num_tokens, num_q_heads, kv_dtype) bytes, 0 for bf16 pages (then it may be NULL); its
+ * contents do not matter, and calls that may overlap need one each.  q and kv_pages are 16-byte aligned.
+ * Scores and sums are fp32; with e4m3fn pages q is two e4m3 terms per element, exact for elements of at least
+ * 2^-9 of the row's largest.  Asynchronous on `stream`, no allocation, capture safe.
+ * Returns SK_OK or a negative sk_status. */
+int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, float k_scale,
+                          const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                          const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal,
+                          const float *lse, float *acc_pages, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of sk_accum_attn_weights.  Host-only arithmetic; a negative sk_status for bad sizes. */
+int64_t sk_accum_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype);
+
 /* How sk_rope_frequencies fits the frequencies w_i = base^(-2 i / rot_dim) to contexts `factor` times
  * longer than the trained ones. */
 typedef enum {

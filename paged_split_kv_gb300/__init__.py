@@ -25,7 +25,7 @@ __all__ = [
     "SK_OK", "SK_CACHED", "SK_ERR_TIMEOUT", "SK_KV_BF16", "SK_KV_FP8_E4M3", "SK_DEV_BAD_BLOCK",
     "SK_DEV_BAD_SEQ", "SK_DEV_TIMEOUT", "sk_rope_frequencies", "sk_rope_and_cache", "sk_evict_capacity",
     "sk_evict_select", "sk_evict_move", "evict_rows", "sk_prefill_nsplit",
-    "sk_paged_prefill_attn", "paged_prefill_attention",
+    "sk_paged_prefill_attn", "paged_prefill_attention", "sk_accum_attn_weights", "sk_accum_workspace_bytes",
 ]
 
 SK_OK = 0
@@ -94,6 +94,11 @@ def lib():
         L.sk_paged_prefill_attn.restype = i32
         L.sk_paged_prefill_attn.argtypes = [P, P, i32, f32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32,
                                             f32, i32, i32, P, P, P, P, P, P]
+        L.sk_accum_workspace_bytes.restype = i64
+        L.sk_accum_workspace_bytes.argtypes = [i32, i32, i32]
+        L.sk_accum_attn_weights.restype = i32
+        L.sk_accum_attn_weights.argtypes = [P, P, i32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32, f32,
+                                            i32, P, P, P, i64, P]
         L.sk_evict_capacity.restype = i32
         L.sk_evict_capacity.argtypes = [i32, i32]
         L.sk_evict_select.restype = i32
@@ -541,6 +546,47 @@ def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *,
                           sm_scale=sm_scale, k_scale=k_scale, v_scale=v_scale, causal=causal, part_o=po, part_m=pm,
                           part_l=pl, stream=stream)
     return out, lse
+
+
+def sk_accum_workspace_bytes(num_tokens: int, num_q_heads: int, kv_dtype: int) -> int:
+    """Bytes of device workspace that sk_accum_attn_weights needs (computed by the library)."""
+    return _check(lib().sk_accum_workspace_bytes(num_tokens, num_q_heads, kv_dtype), "sk_accum_workspace_bytes")
+
+
+def sk_accum_attn_weights(q, kv_pages, block_table, seq_lens, cu_seqlens_q, lse, acc_pages, *, max_q_len: int,
+                          sm_scale: float, k_scale: float = 1.0, causal: bool = True, workspace=None,
+                          stream=None) -> int:
+    """Adds to ``acc_pages`` (fp32 [num_blocks, num_kv_heads, page]) the attention weight that each cached key
+    receives from this step's query tokens: exp(score - lse) summed over the tokens that see it and the
+    heads of its group, ``lse`` (fp32 [num_tokens, num_q_heads]) being what the attention call returned.
+    ``workspace`` is an optional dict that keeps the buffer of e4m3 pages across calls."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(kv_pages, None, "kv_pages", 4)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
+    _need(lse, torch.float32, "lse", 2)
+    nt, hq, d, nb, hkv, page, bs = _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
+    _shape(lse, (nt, hq), "lse")
+    if acc_pages is None:
+        raise ValueError("acc_pages is required")
+    _state_pages(kv_pages, acc_pages, None)
+    _same_device(q, kv_pages=kv_pages, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q, lse=lse,
+                 acc_pages=acc_pages)
+    dt = _kv_dtype(kv_pages)
+    buf, need = None, 0
+    if dt == SK_KV_FP8_E4M3:
+        need = sk_accum_workspace_bytes(nt, hq, dt)
+        ws = workspace if workspace is not None else {}
+        buf = ws.get("accum")
+        if buf is None or buf.numel() < need or buf.device != q.device:
+            buf = ws["accum"] = torch.empty(need, dtype=torch.uint8, device=q.device)
+    f = lib().sk_accum_attn_weights
+    return _launch(q.device, stream, "sk_accum_attn_weights", lambda st: f(
+        q.data_ptr(), kv_pages.data_ptr(), dt, k_scale, block_table.data_ptr(), block_table.shape[1], nb, page,
+        seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0,
+        lse.data_ptr(), acc_pages.data_ptr(), _ptr(buf), need, st))
 
 
 def sk_evict_capacity(budget: int, max_seq_len: int) -> int:

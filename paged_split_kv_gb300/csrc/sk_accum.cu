@@ -1,0 +1,647 @@
+// Attention weight that each cached key has gathered:
+//     acc[key p of (s, h)] += sum over the rows r = j * G + i of the group that see p of exp(score(r, p) - lse(r))
+// with the scores of the attention and its log-sum-exp.  Only the K half of the pages is read.
+//
+// The product is taken as S^T [128 keys x rows] = K Q^T, so that a TMEM lane, and with it a thread, is one key: the sum
+// over the rows is that thread's own running sum in fp32, in a fixed order, added to the key's weight once: the same
+// bits every time, unless sequences share a block.
+//
+// Bound by HBM for a few rows (decode, verify: 256 or 128 bytes of K per key against up to 64 rows), by the
+// exponentials and the tensor cores for a chunk (256 flops and one exponential per (row, key)).
+//
+// The cache is cut into tiles of 128 keys; each CTA (one per SM) takes a contiguous run of all the batch's tiles, as
+// many rows' worth as the others, found from the lengths on the device.  Inside a run it works on groups of up to four
+// tiles of one (sequence, head): tile i of a group belongs to softmax warpgroup i and its 128 TMEM columns.
+//   few rows (kMany false): the rows are one Q block of 16, 32 or 64 rows that stays for the whole item while K tiles
+//     stream through a ring;
+//   many rows (kMany true): the group's K tiles stay (128 KB of bf16) while Q streams through in blocks of 128 rows, so
+//     that a block's 32 KB meet 512 keys: with fewer the L2 could not deliver Q as fast as the tensor cores take it.
+//
+// Roles (640 threads): warp 0 copies K pages, warp 1 issues the products, warp 2 copies Q blocks (TMA: a box is
+// whole tokens of the group's heads), warp 3 lays the rows' lse and scale beside them, warps 4-19 are the four
+// softmax warpgroups.
+//
+// e4m3 pages: the products run as kind::f8f6f4 on the codes, with Q as two e4m3 terms and a power-of-two scale per row
+// (prepared by a small kernel into a workspace; exact for bf16 elements within 2^-9 of the row's largest).
+//
+// Waits are bounded as in the attention kernels.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "sk_attn_util.cuh"
+#include "sk_internal.cuh"
+#include "sk_sm100.cuh"
+
+namespace sk {
+namespace {
+
+using namespace sm100;
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kKeys = 128;
+constexpr int kGroup = 4;                            // tiles of a group, softmax warpgroups
+constexpr int kThreads = 128 + kGroup * 128;
+constexpr long long kDrainLimit = 4000000000LL;
+constexpr int kMaxSmem = 232448;
+
+template <int RB, bool MANY, bool FP8>
+struct ACfg {
+    static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K of 8 tokens
+    static constexpr int kKSlot = kKeys / 8 * kGroupBytes;
+    static constexpr int kQSlot = RB * 256;
+    static constexpr int kQSlots = MANY ? 3 : 2;
+    static constexpr int kAuxEach = FP8 ? 2 * RB : RB;             // floats per Q block: -lse, and e4m3's scales
+    static constexpr int kMisc = FP8 ? 4096 : 3072;
+    static constexpr int kFit = (kMaxSmem - kQSlots * kQSlot - kMisc) / kKSlot;
+    static constexpr int kKSlots = kFit < 12 ? kFit : 12;
+    static constexpr int kOffQ = kKSlots * kKSlot;
+    static constexpr int kOffMisc = kOffQ + kQSlots * kQSlot;
+    static constexpr int kSmemBytes = kOffMisc + kMisc;
+    static constexpr int kPagesPerTile = kKeys / kPage;
+    // misc area
+    static constexpr int kBarKFull = 0;
+    static constexpr int kBarKEmpty = 8 * kKSlots;
+    static constexpr int kBarQFull = 16 * kKSlots;                 // [kQSlots]
+    static constexpr int kBarQEmpty = kBarQFull + 8 * kQSlots;
+    static constexpr int kBarAFull = kBarQEmpty + 8 * kQSlots;     // rows' lse and scale
+    static constexpr int kBarAEmpty = kBarAFull + 8 * kQSlots;
+    static constexpr int kBarS = kBarAEmpty + 8 * kQSlots;         // [kGroup] S complete
+    static constexpr int kBarSFree = kBarS + 8 * kGroup;
+    static constexpr int kBarDrain = kBarSFree + 8 * kGroup;
+    static constexpr int kTmemSlot = kBarDrain + 8;
+    static constexpr int kAbort = kTmemSlot + 4;
+    static constexpr int kStart = kAbort + 4;                      // int: first sequence; long long: its offset
+    static constexpr int kAux = 512;                               // float[kQSlots][kAuxEach], log2 units
+    static_assert(kStart + 24 <= kAux && kAux + kQSlots * kAuxEach * 4 <= kMisc, "misc area");
+    static_assert(kKSlots >= (MANY ? kGroup : 3) && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0 && kQSlot % 1024 == 0,
+                  "shared memory");
+};
+
+// One (sequence, head) share of a CTA's run, and the blocks that its rows make.
+struct Item {
+    int s, h, L, q_len, tok0, a, b;                  // tiles [a, b)
+    int nblk;                                        // Q blocks
+};
+
+// The tiles of a CTA's run, item after item; every role walks it alike.
+struct Walk {
+    const AccumParams &p;
+    long long lo, hi, off;                           // the run, and the current sequence's start, in block-tiles
+    int s, h;
+    __device__ Walk(const AccumParams &pp, long long lo_, long long hi_, int s0, long long off0)
+        : p(pp), lo(lo_), hi(hi_), off(off0), s(s0), h(0)
+    {
+    }
+    __device__ __forceinline__ bool next(Item &it)
+    {
+        while (s < p.bs && off < hi) {
+            int L, q, tok0;
+            const int w = accum_weight(p, s, L, q, tok0);
+            const int tiles = (L + kKeys - 1) / kKeys;
+            if (w > 0 && h < p.H_kv) {
+                const long long start = off + (long long)h * tiles * w;
+                const int hh = h++;
+                if (start >= hi)
+                    return false;
+                // a tile belongs to the run that its start lies in
+                const long long a = lo > start ? (lo - start + w - 1) / w : 0;
+                const long long b = (hi - start + w - 1) / w;
+                if (a < tiles && a < b) {
+                    it.s = s;
+                    it.h = hh;
+                    it.L = L;
+                    it.q_len = q;
+                    it.tok0 = tok0;
+                    it.a = (int)a;
+                    it.b = (int)(b < tiles ? b : tiles);
+                    it.nblk = w;
+                    return true;
+                }
+                continue;
+            }
+            off += (long long)tiles * w * p.H_kv;
+            ++s;
+            h = 0;
+        }
+        return false;
+    }
+    // Q blocks of a sequence with q query tokens; 0 when it has nothing to do (and a bad one is reported once)
+    static __device__ __forceinline__ int accum_weight(const AccumParams &p, int s, int &L, int &q, int &tok0)
+    {
+        L = __ldg(p.seq_lens + s);
+        tok0 = __ldg(p.cu_q + s);
+        q = __ldg(p.cu_q + s + 1) - tok0;
+        if (q < 0 || q > p.max_q_len || tok0 < 0 || tok0 + q > p.num_tokens || L < 0 ||
+            (long long)L > (long long)p.bt_stride * kPage) {
+            atomicOr(p.status, SK_DEV_BAD_SEQ);
+            L = q = 0;
+        }
+        return L > 0 ? (q + p.tpb - 1) / p.tpb * p.nsub : 0;
+    }
+};
+
+template <int RB, bool MANY, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+             const AccumParams p)
+{
+    using C = ACfg<RB, MANY, FP8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(smem);
+    uint8_t *misc = smem + C::kOffMisc;
+    const uint32_t mbase = sbase + C::kOffMisc;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + C::kAbort);
+    auto bar_kfull = [&](int i) { return mbase + C::kBarKFull + 8 * i; };
+    auto bar_kempty = [&](int i) { return mbase + C::kBarKEmpty + 8 * i; };
+    auto bar_qfull = [&](int i) { return mbase + C::kBarQFull + 8 * i; };
+    auto bar_qempty = [&](int i) { return mbase + C::kBarQEmpty + 8 * i; };
+    auto bar_afull = [&](int i) { return mbase + C::kBarAFull + 8 * i; };
+    auto bar_aempty = [&](int i) { return mbase + C::kBarAEmpty + 8 * i; };
+    auto bar_s = [&](int i) { return mbase + C::kBarS + 8 * i; };
+    auto bar_sfree = [&](int i) { return mbase + C::kBarSFree + 8 * i; };
+    const uint32_t bar_drain = mbase + C::kBarDrain;
+    long long *run = reinterpret_cast<long long *>(misc + C::kStart);     // offset of the first sequence, its index
+
+    wait_prior_grid();
+    // ---- this CTA's run: block-tiles [lo, hi) of the batch's total, and the sequence that lo lies in
+    long long *part = reinterpret_cast<long long *>(smem);       // in the K slots, before the first copy
+    const int per = (p.bs + kThreads - 1) / kThreads;
+    const int s_lo = min(p.bs, (int)threadIdx.x * per), s_hi = min(p.bs, s_lo + per);
+    long long mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) {
+        int L, q, tok0;
+        const int w = Walk::accum_weight(p, s, L, q, tok0);
+        mine += (long long)((L + kKeys - 1) / kKeys) * w * p.H_kv;
+    }
+    part[threadIdx.x] = mine;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kKSlots; ++i) {
+            mbar_init(bar_kfull(i), 1);
+            mbar_init(bar_kempty(i), 1);
+        }
+        for (int i = 0; i < C::kQSlots; ++i) {
+            mbar_init(bar_qfull(i), 1);
+            mbar_init(bar_qempty(i), 1);
+            mbar_init(bar_afull(i), 1);
+            mbar_init(bar_aempty(i), 4 * kGroup);
+        }
+        for (int i = 0; i < kGroup; ++i) {
+            mbar_init(bar_s(i), 1);
+            mbar_init(bar_sfree(i), 4);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        if (blockIdx.x == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_q + p.bs) != p.num_tokens))
+            atomicOr(p.status, SK_DEV_BAD_SEQ);
+    }
+    if (warp == 1) {
+        tmem_alloc(mbase + C::kTmemSlot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        // inclusive prefix of the 640 partial sums, 20 a lane
+        constexpr int kEach = kThreads / 32;
+        long long sum = 0;
+        for (int i = 0; i < kEach; ++i)
+            sum += part[lane * kEach + i];
+        long long incl = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(kFull, incl, o);
+            incl += lane >= o ? u : 0;
+        }
+        long long at = incl - sum;
+        for (int i = 0; i < kEach; ++i) {
+            at += part[lane * kEach + i];
+            part[lane * kEach + i] = at;
+        }
+    }
+    __syncthreads();
+    const long long total = part[kThreads - 1];
+    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    {
+        const long long before = part[threadIdx.x] - mine;
+        if (mine > 0 && lo >= before && lo < before + mine) {
+            long long off = before;
+            int s = s_lo;
+            for (; s < s_hi - 1; ++s) {
+                int L, q, tok0;
+                const int w = Walk::accum_weight(p, s, L, q, tok0);
+                const long long size = (long long)((L + kKeys - 1) / kKeys) * w * p.H_kv;
+                if (lo < off + size)
+                    break;
+                off += size;
+            }
+            run[0] = off;
+            run[1] = s;
+        }
+    }
+    fence_proxy_async_smem();                        // the copies come after these uses of the slots
+    __syncthreads();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc + C::kTmemSlot);
+    const bool any = (sbase & 1023u) == 0 && lo < hi;
+    if ((sbase & 1023u) != 0 && threadIdx.x == 0)
+        atomicOr(p.status, SK_DEV_INTERNAL);
+    Walk walk(p, lo, hi, any ? (int)run[1] : p.bs, any ? run[0] : 0);
+    Item it;
+
+    // groups of an item: its tiles in equal shares of up to four
+    auto groups_of = [&](const Item &w) { return (w.b - w.a + kGroup - 1) / kGroup; };
+    auto group_at = [&](const Item &w, int ng, int g) { return w.a + (int)((long long)(w.b - w.a) * g / ng); };
+    // first Q block with a row that sees key p0: causal rows start at token p0 - (L - q)
+    auto first_block = [&](const Item &w, int tile) {
+        const int j = p.causal ? tile * kKeys - (w.L - w.q_len) : 0;
+        return j > 0 ? j / p.tpb * p.nsub : 0;
+    };
+
+    if (warp == 0) {
+        // ============================================================ K pages
+        if (lane == 0)
+            prefetch_tensormap(&kv_map);
+        int u = 0;                                   // tiles issued
+        bool ok = true;
+        while (ok && walk.next(it)) {
+            const int page_end = (it.L + kPage - 1) / kPage;
+            const int32_t *bt = p.block_table + (long long)it.s * p.bt_stride;
+            auto block_at = [&](int t) {
+                const int pg = t * C::kPagesPerTile + lane;
+                return (lane < C::kPagesPerTile && t < it.b && pg < page_end) ? __ldg(bt + pg) : -1;
+            };
+            int blk[3] = {block_at(it.a), block_at(it.a + 1), block_at(it.a + 2)};
+            for (int t = it.a; t < it.b && ok; ++t, ++u) {
+                const int i = u % C::kKSlots;
+                if (u >= C::kKSlots)
+                    ok = mbar_wait_bounded(bar_kempty(i), (u / C::kKSlots - 1) & 1, abort_flag, p.wait_limit);
+                ok = __all_sync(kFull, ok);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar_kfull(i), C::kKSlot);
+                __syncwarp();
+                if (lane < C::kPagesPerTile) {
+                    int grp = -2;                    // whole box out of bounds: zero fill
+                    if (t * C::kPagesPerTile + lane < page_end) {
+                        if (blk[0] >= 0 && blk[0] < p.num_blocks)
+                            grp = (blk[0] * p.H_kv + it.h) * 2;
+                        else
+                            atomicOr(p.status, SK_DEV_BAD_BLOCK);
+                    }
+                    tma_load_4d(sbase + i * C::kKSlot + lane * 2 * C::kGroupBytes, &kv_map, 0, 0, 0, grp, bar_kfull(i));
+                }
+                blk[0] = blk[1];
+                blk[1] = blk[2];
+                blk[2] = block_at(t + 3);
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                atomicOr(p.status, SK_DEV_TIMEOUT);
+        }
+        for (int t = u > C::kKSlots ? u - C::kKSlots : 0; t < u; ++t)
+            mbar_wait_bounded(bar_kfull(t % C::kKSlots), (t / C::kKSlots) & 1, nullptr, kDrainLimit);
+    } else if (warp == 1) {
+        // ============================================================ products
+        constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(kKeys, RB, 0, 0) : idesc_bf16_f32(kKeys, RB, 0, 0);
+        const uint64_t d_k0 = smem_desc_sw128(sbase, 16, C::kGroupBytes);
+        const uint64_t d_q0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+        auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
+        bool ok = true;
+        int u = 0, v = 0;                            // K tiles and Q blocks used up
+        uint32_t uses[kGroup] = {0, 0, 0, 0};        // products of each TMEM buffer
+        bool issued = false;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (ok)
+                ok = mbar_wait_bounded(bar, parity, abort_flag, p.wait_limit);
+            ok = __all_sync(kFull, ok);
+            if (ok)
+                tc_fence_after();
+            return ok;
+        };
+        while (ok && walk.next(it)) {
+            const int ng = groups_of(it);
+            for (int g = 0; g < ng && ok; ++g) {
+                const int ta = group_at(it, ng, g), nt = group_at(it, ng, g + 1) - ta;
+                for (int qb = MANY ? first_block(it, ta) : 0; qb < it.nblk && ok; ++qb) {
+                    const int qi = v % C::kQSlots;
+                    if ((MANY || g == 0) && !wait(bar_qfull(qi), (v / C::kQSlots) & 1))
+                        break;
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i) {
+                        if (i >= nt || !ok)
+                            continue;
+                        const int f = MANY ? first_block(it, ta + i) : 0;
+                        const int ki = (u + i) % C::kKSlots;
+                        if (qb >= f) {
+                            if (qb == f && !wait(bar_kfull(ki), ((u + i) / C::kKSlots) & 1))
+                                continue;
+                            if (uses[i] > 0 && !wait(bar_sfree(i), (uses[i] - 1) & 1))
+                                continue;
+                            const uint32_t so = (uint32_t)ki * C::kKSlot, qo = (uint32_t)qi * C::kQSlot;
+                            const uint32_t sd = tmem + i * 128;
+                            if constexpr (FP8) {
+#pragma unroll
+                                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        mma_f8_ss_warp(sd, adv(d_k0, so + k * 32), adv(d_q0, qo + t * (RB * 128) + k * 32),
+                                                       idesc, (t > 0 || k > 0) ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_f16_ss_warp(sd, adv(d_k0, so + (k >> 2) * 1024 + (k & 3) * 32),
+                                                    adv(d_q0, qo + (k >> 2) * (RB * 128) + (k & 3) * 32), idesc,
+                                                    k > 0 ? 1u : 0u);
+                            }
+                            mma_commit_warp(bar_s(i));
+                            ++uses[i];
+                            issued = true;
+                        }
+                        if (qb + 1 == it.nblk) {
+                            // a tile that no row sees is not waited for before: its copy has to have landed
+                            if (qb < f && !wait(bar_kfull(ki), ((u + i) / C::kKSlots) & 1))
+                                continue;
+                            mma_commit_warp(bar_kempty(ki));
+                        }
+                    }
+                    if (MANY || g + 1 == ng) {
+                        mma_commit_warp(bar_qempty(qi));
+                        ++v;
+                    }
+                }
+                u += nt;
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                atomicOr(p.status, SK_DEV_TIMEOUT);
+        }
+        if (issued) {
+            mma_commit_warp(bar_drain);
+            mbar_wait_bounded(bar_drain, 0, nullptr, kDrainLimit);
+        }
+    } else if (warp == 2 || warp == 3) {
+        // ============================================================ Q blocks (warp 2), their rows' lse and scale (3)
+        bool ok = true;
+        int v = 0;
+        while (ok && walk.next(it)) {
+            const int ng = MANY ? groups_of(it) : 1;
+            for (int g = 0; g < ng && ok; ++g)
+                for (int qb = MANY ? first_block(it, group_at(it, ng, g)) : 0; qb < it.nblk && ok; ++qb, ++v) {
+                    const int qi = v % C::kQSlots;
+                    const int j0 = qb / p.nsub * p.tpb, i0 = (qb % p.nsub) * p.gb;
+                    const int hq0 = it.h * p.G + i0;
+                    if (v >= C::kQSlots)
+                        ok = mbar_wait_bounded(warp == 2 ? bar_qempty(qi) : bar_aempty(qi), (v / C::kQSlots - 1) & 1,
+                                               abort_flag, p.wait_limit);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok)
+                        break;
+                    if (warp == 2) {
+                        if (lane == 0) {
+                            const uint32_t dst = sbase + C::kOffQ + qi * C::kQSlot;
+                            mbar_arrive_expect_tx(bar_qfull(qi), (uint32_t)(p.gb * p.tpb * 256));
+                            tma_load_3d(dst, &q_map, 0, hq0, it.tok0 + j0, bar_qfull(qi));
+                            tma_load_3d(dst + RB * 128, &q_map, FP8 ? 128 : 64, hq0, it.tok0 + j0, bar_qfull(qi));
+                        }
+                        __syncwarp();
+                    } else {
+                        float *aux = reinterpret_cast<float *>(misc + C::kAux) + qi * C::kAuxEach;
+                        for (int r = lane; r < RB; r += 32) {
+                            const int jj = r / p.gb, ii = r - jj * p.gb;
+                            float nl = -CUDART_INF_F;
+                            [[maybe_unused]] float sc = 1.f;   // a masked -inf stays -inf
+                            if (jj < p.tpb && j0 + jj < it.q_len && i0 + ii < p.G) {
+                                const long long at = (long long)(it.tok0 + j0 + jj) * p.H_q + hq0 + ii;
+                                nl = __ldg(p.lse + at) * -1.4426950408889634f;
+                                nl = nl == CUDART_INF_F ? -CUDART_INF_F : nl;     // a row that sees nothing
+                                if constexpr (FP8)
+                                    sc = __ldg(p.q_scale + at) * p.score_scale_log2;
+                            }
+                            aux[r] = nl;
+                            if constexpr (FP8)
+                                aux[RB + r] = sc;
+                        }
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar_afull(qi));
+                    }
+                }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                atomicOr(p.status, SK_DEV_TIMEOUT);
+        }
+        if (warp == 2)
+            for (int t = v > C::kQSlots ? v - C::kQSlots : 0; t < v; ++t)
+                mbar_wait_bounded(bar_qfull(t % C::kQSlots), (t / C::kQSlots) & 1, nullptr, kDrainLimit);
+    } else {
+        // ============================================================ sums of the exponentials
+        const int wg = (warp >> 2) - 1;
+        const int quarter = warp & 3;
+        const int tau = quarter * 32 + lane;
+        const uint32_t ts = tmem + wg * 128 + ((uint32_t)(quarter * 32) << 16);
+        uint32_t uses = 0;
+        int v = 0;
+        bool ok = true;
+        while (ok && walk.next(it)) {
+            const int ng = groups_of(it);
+            const int32_t *bt = p.block_table + (long long)it.s * p.bt_stride;
+            for (int g = 0; g < ng && ok; ++g) {
+                const int ta = group_at(it, ng, g), nt = group_at(it, ng, g + 1) - ta;
+                const int key = (ta + wg) * kKeys + tau;
+                const bool live = wg < nt && key < it.L;
+                float *place = nullptr;
+                if (live) {
+                    const int blk = __ldg(bt + key / kPage);
+                    if (blk >= 0 && blk < p.num_blocks)
+                        place = p.acc + ((long long)blk * p.H_kv + it.h) * kPage + key % kPage;
+                }
+                const int f = MANY ? first_block(it, ta + wg) : 0;
+                const int jmin = p.causal ? key - (it.L - it.q_len) : 0;       // first token that sees the key
+                float2 sum = make_float2(0.f, 0.f);
+                for (int qb = MANY ? first_block(it, ta) : 0; qb < it.nblk && ok; ++qb) {
+                    const int qi = v % C::kQSlots;
+                    if (MANY || g == 0)
+                        ok = __all_sync(kFull, mbar_wait_bounded(bar_afull(qi), (v / C::kQSlots) & 1, abort_flag,
+                                                                 p.wait_limit));
+                    if (ok && wg < nt && qb >= f) {
+                        ok = mbar_wait_bounded(bar_s(wg), uses & 1, abort_flag, p.wait_limit);
+                        ++uses;
+                        ok = __all_sync(kFull, ok);
+                        if (ok) {
+                            tc_fence_after();
+                            const float *aux = reinterpret_cast<const float *>(misc + C::kAux) + qi * C::kAuxEach;
+                            const int j0 = qb / p.nsub * p.tpb;
+                            // rows [rmin, rows) of the block see this key
+                            const int rmin = jmin > j0 ? (jmin - j0) * p.gb : 0;
+                            const int rows = p.nsub > 1 ? min(p.gb, p.G - qb % p.nsub * p.gb)
+                                                        : min(p.tpb, it.q_len - j0) * p.gb;
+                            constexpr int kLd = RB < 32 ? RB : 32;
+#pragma unroll
+                            for (int c0 = 0; c0 < RB; c0 += kLd) {
+                                if (c0 >= rows)
+                                    break;
+                                float x[kLd];
+                                tmem_ld32<kLd>(ts + c0, x);
+                                tmem_wait_ld();
+                                if (c0 + kLd >= rows) {              // the buffer's last read
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0)
+                                        mbar_arrive(bar_sfree(wg));
+                                }
+                                const bool whole = __all_sync(kFull, rmin <= c0) && c0 + kLd <= rows;
+                                if (!whole) {
+#pragma unroll
+                                    for (int r = 0; r < kLd; ++r)
+                                        x[r] = (c0 + r >= rmin && c0 + r < rows) ? x[r] : -CUDART_INF_F;
+                                }
+#pragma unroll
+                                for (int r = 0; r < kLd; r += 4) {
+                                    const float4 nl = *reinterpret_cast<const float4 *>(aux + c0 + r);
+                                    float4 sc = make_float4(p.score_scale_log2, p.score_scale_log2, p.score_scale_log2,
+                                                            p.score_scale_log2);
+                                    if constexpr (FP8)
+                                        sc = *reinterpret_cast<const float4 *>(aux + RB + c0 + r);
+                                    const float2 d0 = ffma2(make_float2(x[r], x[r + 1]), make_float2(sc.x, sc.y),
+                                                            make_float2(nl.x, nl.y));
+                                    const float2 d1 = ffma2(make_float2(x[r + 2], x[r + 3]), make_float2(sc.z, sc.w),
+                                                            make_float2(nl.z, nl.w));
+                                    sum = fadd2(sum, make_float2(ex2_ftz(d0.x), ex2_ftz(d0.y)));
+                                    sum = fadd2(sum, make_float2(ex2_ftz(d1.x), ex2_ftz(d1.y)));
+                                }
+                            }
+                        }
+                    }
+                    if (ok && (MANY || g + 1 == ng)) {
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar_aempty(qi));
+                        ++v;
+                    }
+                }
+                // one addition per key (more only where sequences share a block)
+                if (ok && place != nullptr)
+                    atomicAdd(place, sum.x + sum.y);
+            }
+        }
+        if (!ok)
+            *abort_flag = 1;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Q as two e4m3 terms for e4m3 pages: row (t, hq) becomes 128 hi codes, then 128 lo codes, and 2^-e.
+__global__ void __launch_bounds__(256) split_q_kernel(const uint16_t *__restrict__ q, long long rows,
+                                                      uint8_t *__restrict__ codes, float *__restrict__ scale)
+{
+    wait_prior_grid();
+    const int lane = threadIdx.x & 31;
+    constexpr int kAtOnce = 4;
+    const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kAtOnce;
+    uint2 raw[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+        raw[i] = r0 + i < rows ? __ldg(reinterpret_cast<const uint2 *>(q + (r0 + i) * kHeadDim) + lane)
+                               : make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+        if (r0 + i >= rows)
+            break;
+        uint32_t hi, lo;
+        int e;
+        split_q_row(raw[i], hi, lo, e);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(codes + (r0 + i) * 256);
+        dst[lane] = hi;
+        dst[32 + lane] = lo;
+        if (lane == 0)
+            scale[r0 + i] = ldexpf(1.f, -e);
+    }
+}
+
+template <int RB, bool MANY, bool FP8>
+cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const AccumParams &p, int num_sms,
+                     cudaStream_t stream)
+{
+    using C = ACfg<RB, MANY, FP8>;
+    const cudaError_t e = cudaFuncSetAttribute(accum_kernel<RB, MANY, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               C::kSmemBytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(accum_kernel<RB, MANY, FP8>, dim3((unsigned)num_sms), dim3(kThreads), C::kSmemBytes, stream,
+                      kv_map, q_map, p);
+}
+
+}  // namespace
+
+// Rows of a Q block: 16, 32 or 64 when that holds all of a sequence's rows (they then stay while K streams), else 128.
+int accum_block_rows(int G, long long max_q_len)
+{
+    for (int rb = 16; rb <= 64; rb *= 2)
+        if ((long long)G * max_q_len <= rb)
+            return rb;
+    return 128;
+}
+
+cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *q_codes, int num_sms, cudaStream_t stream)
+{
+    const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
+    AccumParams p = params;
+    const int rb = accum_block_rows(p.G, p.max_q_len);
+    p.gb = p.G < rb ? p.G : rb;
+    p.nsub = (p.G + p.gb - 1) / p.gb;
+    p.tpb = rb / p.gb;
+    const void *q = p.q;
+    if (fp8) {
+        const long long rows = (long long)p.num_tokens * p.H_q;
+        uint8_t *codes = static_cast<uint8_t *>(q_codes);
+        float *scale = reinterpret_cast<float *>(codes + rows * 256);
+        const cudaError_t e = launch_pdl(split_q_kernel, dim3((unsigned)((rows + 31) / 32)), dim3(256), 0, stream, p.q,
+                                         rows, codes, scale);
+        if (e != cudaSuccess)
+            return e;
+        q = codes;
+        p.q_scale = scale;
+    }
+    CUtensorMap kv_map, q_map;
+    cudaError_t e = encode_page_map(&kv_map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 1 : 2);
+    if (e == cudaSuccess)
+        e = encode_q_map(&q_map, q, p.num_tokens, p.H_q, fp8, p.gb, p.tpb);
+    if (e != cudaSuccess)
+        return e;
+    switch (rb * 2 + (fp8 ? 1 : 0)) {
+    case 32:
+        return launch_t<16, false, false>(kv_map, q_map, p, num_sms, stream);
+    case 33:
+        return launch_t<16, false, true>(kv_map, q_map, p, num_sms, stream);
+    case 64:
+        return launch_t<32, false, false>(kv_map, q_map, p, num_sms, stream);
+    case 65:
+        return launch_t<32, false, true>(kv_map, q_map, p, num_sms, stream);
+    case 128:
+        return launch_t<64, false, false>(kv_map, q_map, p, num_sms, stream);
+    case 129:
+        return launch_t<64, false, true>(kv_map, q_map, p, num_sms, stream);
+    case 256:
+        return launch_t<128, true, false>(kv_map, q_map, p, num_sms, stream);
+    default:
+        return launch_t<128, true, true>(kv_map, q_map, p, num_sms, stream);
+    }
+}
+
+}  // namespace sk

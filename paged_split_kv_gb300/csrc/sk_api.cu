@@ -764,6 +764,87 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
     return SK_OK;
 }
 
+int64_t sk_accum_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype)
+{
+    if (num_tokens < 0 || num_q_heads < 1 || (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3))
+        return fail(SK_ERR_INVALID, "sk_accum_workspace_bytes: num_tokens=%d num_q_heads=%d kv_dtype=%d", num_tokens,
+                    num_q_heads, kv_dtype);
+    // e4m3 pages: Q's two terms and a scale per row
+    return kv_dtype == SK_KV_FP8_E4M3 ? (int64_t)num_tokens * num_q_heads * (2 * kHeadDim + 4) : 0;
+}
+
+int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, float k_scale,
+                          const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                          const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal,
+                          const float *lse, float *acc_pages, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (q == nullptr || kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr ||
+        cu_seqlens_q == nullptr || lse == nullptr || acc_pages == nullptr)
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: null pointer argument");
+    if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: kv_dtype=%d", kv_dtype);
+    if (head_dim != kHeadDim)
+        return fail(SK_ERR_UNSUPPORTED, "sk_accum_attn_weights: head_dim=%d (only 128)", head_dim);
+    if (page_size != kPage)
+        return fail(SK_ERR_UNSUPPORTED, "sk_accum_attn_weights: page_size=%d (only 16)", page_size);
+    if (bs < 1 || bs > 32767)
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: bs=%d outside [1, 32767]", bs);
+    if (num_tokens < 0 || max_q_len < 0 || (num_tokens > 0 && max_q_len < 1) || block_table_stride < 1 ||
+        num_blocks < 1)
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: num_tokens=%d max_q_len=%d stride=%d num_blocks=%d",
+                    num_tokens, max_q_len, block_table_stride, num_blocks);
+    if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: %d query heads, %d kv heads", num_q_heads, num_kv_heads);
+    if (!(sm_scale > 0.f && sm_scale < INFINITY) ||
+        (kv_dtype == SK_KV_FP8_E4M3 && !(k_scale > 0.f && k_scale < INFINITY)))
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: scales must be positive and finite");
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(kv_pages)) & 15)
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: q and kv_pages must be 16-byte aligned");
+    if ((long long)num_blocks * num_kv_heads * 2 > 0x7FFFFFFFLL || (long long)num_q_heads * max_q_len > 0x3FFFFFFFLL)
+        return fail(SK_ERR_UNSUPPORTED, "sk_accum_attn_weights: %d blocks of %d heads or %d query tokens of %d heads "
+                    "exceed the kernel's limits (2^30)", num_blocks, num_kv_heads, max_q_len, num_q_heads);
+    const int64_t need = sk_accum_workspace_bytes(num_tokens, num_q_heads, kv_dtype);
+    if (workspace_bytes < need || (need > 0 && workspace == nullptr))
+        return fail(SK_ERR_CAPACITY, "sk_accum_attn_weights: workspace of %lld bytes, %lld needed",
+                    (long long)workspace_bytes, (long long)need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 15)
+        return fail(SK_ERR_INVALID, "sk_accum_attn_weights: workspace must be 16-byte aligned");
+    if (num_tokens == 0)
+        return SK_OK;
+    int *status = nullptr;
+    int sms = 0;
+    int rc = status_ptr(&status);
+    if (rc == SK_OK)
+        rc = sm_count(&sms);
+    if (rc != SK_OK)
+        return rc;
+    AccumParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.kv = kv_pages;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.cu_q = cu_seqlens_q;
+    p.lse = lse;
+    p.acc = acc_pages;
+    p.status = status;
+    p.num_blocks = num_blocks;
+    p.bt_stride = block_table_stride;
+    p.bs = bs;
+    p.num_tokens = num_tokens;
+    p.max_q_len = max_q_len;
+    p.H_q = num_q_heads;
+    p.H_kv = num_kv_heads;
+    p.G = num_q_heads / num_kv_heads;
+    p.causal = causal ? 1 : 0;
+    p.score_scale_log2 = sm_scale * (kv_dtype == SK_KV_FP8_E4M3 ? k_scale : 1.f) * 1.4426950408889634f;
+    p.wait_limit = wait_limit();
+    cudaError_t e = launch_accum(p, kv_dtype, workspace, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "attention weight kernel launch");
+    return SK_OK;
+}
+
 int sk_get_device_status(void *stream, int clear)
 {
     int *status = nullptr;

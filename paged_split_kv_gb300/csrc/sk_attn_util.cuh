@@ -166,6 +166,18 @@ __device__ __forceinline__ void mma_f8_ts_warp(uint32_t d_tmem, uint32_t a_tmem,
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Tensor map of Q rows [tokens][heads][256 bytes] (bf16, or e4m3 hi and lo codes): a box is 128 bytes of `heads` heads
+// of `toks` tokens and lands as consecutive 128-byte-swizzled rows.
+cudaError_t encode_q_map(CUtensorMap *map, const void *q, long long num_tokens, int H_q, bool fp8, int heads, int toks);
+
 // Tensor map of the pages [blocks][heads][16 tokens][K | V] as 4-D: (128 bytes of a row, token within an 8-token
 // group, 128-byte chunk of the row, 8-token group across all pages).  A box is `chunks` chunks of one page of one
 // head and lands group by group, chunk by chunk, as 8 x 128 B swizzle atoms.

@@ -187,6 +187,24 @@ struct PrefillParams {
 constexpr int kPrefillRows = 256;
 int prefill_nsplit(int bs, int num_tokens, int max_q_len, int H_q, int H_kv, int max_seq_len, int num_sms);
 cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, cudaStream_t stream);
+// Gathered attention weights, resolved on the host.
+struct AccumParams {
+    const uint16_t *q;           // bf16 bits [NT, H_q, D]
+    const float *q_scale;        // e4m3 pages: 2^-e of each row of the split Q (set by the launcher)
+    const void *kv;              // pages
+    const int32_t *block_table, *seq_lens, *cu_q;
+    const float *lse;            // [NT, H_q]
+    float *acc;                  // [NB, H_kv, 16]
+    int *status;
+    int64_t num_blocks;
+    int bt_stride, bs, num_tokens, max_q_len;
+    int H_q, H_kv, G;
+    int gb, tpb, nsub;           // heads and tokens of a Q block, blocks per token (set by the launcher)
+    int causal;
+    float score_scale_log2;
+    long long wait_limit;
+};
+cudaError_t launch_accum(const AccumParams &p, int kv_dtype, void *q_codes, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16_t *v, long long q_stride,
                               long long k_stride, long long v_stride, const int64_t *pos, const double *freqs,
                               const int64_t *slots, int num_tokens, int hq, int hkv, int rot, int interleaved,

@@ -625,6 +625,22 @@ cudaError_t encode_page_map(CUtensorMap *map, const void *pages, long long num_b
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_q_map(CUtensorMap *map, const void *q, long long num_tokens, int H_q, bool fp8, int heads, int toks)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)(fp8 ? 256 : 128), (cuuint64_t)H_q, (cuuint64_t)num_tokens};
+    const cuuint64_t strides[2] = {256, (cuuint64_t)H_q * 256};
+    const cuuint32_t box[3] = {fp8 ? 128u : 64u, (cuuint32_t)heads, (cuuint32_t)toks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                           const_cast<void *>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // CTAs that share the keys of a row block: the number with the least estimated time.  A CTA takes `kFixed` to start
 // and finish and `kTile` per key tile; `units` row blocks run num_sms at a time; a split adds the merge, which reads
 // what the partial states' writes left (520 bytes per row, head and split, both ways).  More CTAs even out the last

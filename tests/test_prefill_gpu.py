@@ -76,7 +76,7 @@ def check(b, out, lse, ref=None):
     ro, rl, to, tl = ref or reference(b)
     assert not torch.isnan(out.float()).any()
     err = (out.double() - ro).abs()
-    bad = err > to + 1e-30
+    bad = ~(err <= to + 1e-30)
     assert not bool(bad.any()), (int(bad.sum()), float((err / (to + 1e-30)).max()), bad.nonzero()[:4].tolist())
     dead = torch.isinf(rl)
     assert torch.equal(torch.isinf(lse) & (lse < 0), dead)
