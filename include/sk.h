@@ -372,7 +372,7 @@ int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t
  * with L <= budget has n = 0.  L above max_seq_len (or below 0) sets SK_DEV_BAD_SEQ: n = 0, new_lens = L.
  * A row in a block outside [0, num_blocks) ranks like -inf and sets SK_DEV_BAD_BLOCK.
  *
- * acc_pages fp32, pos_pages int32 [num_blocks, num_kv_heads, page_size]; src_rows, dst_rows int32 [bs,
+ * acc_pages fp32, pos_pages int32 [num_blocks, num_kv_heads, page_size], 16-byte aligned; src_rows, dst_rows int32 [bs,
  * num_kv_heads, capacity], capacity >= sk_evict_capacity(budget, max_seq_len); counts int32 [bs,
  * num_kv_heads]; new_lens int32 [bs], not seq_lens itself.  max_seq_len: an upper bound on the lengths, at
  * most 786432; it sizes the launch.  0 <= recent <= budget.  Asynchronous on `stream`, no allocation,

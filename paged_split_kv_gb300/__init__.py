@@ -378,44 +378,53 @@ def sk_paged_decode_attention_static(q, kv_pages, block_table, seq_lens, cu_seql
 _ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
 
-def _launch(dev, stream, name, call) -> int:
-    """Runs ``call(stream pointer)`` with tensor device ``dev`` current (its streams and status word are
-    per device) and checks the status it returns."""
+def _fits(t, dtype, shape, name, dev) -> int:
+    """Checks one argument in one expression (calls of a decode step are short): its type, shape, layout and
+    device ``dev`` (an ordinal, -1 for the CPU).  Returns its address."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _need(t, dtype, name, len(shape))
+    _shape(t, shape, name)
+    raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments, is on {t.device}")
+
+
+def _pages(kv_pages, dev):
+    """Address, type and shape of the pages."""
+    _need(kv_pages, None, "kv_pages", 4)
+    if kv_pages.get_device() != dev:
+        raise ValueError(f"kv_pages must be a CUDA tensor on the device of the other arguments, is on {kv_pages.device}")
+    return kv_pages.data_ptr(), _kv_dtype(kv_pages), kv_pages.shape
+
+
+def _launch(dev: int, stream, name, f, *args) -> int:
+    """Calls ``f(*args, stream)`` with device ``dev`` current (streams and the status word are per device); the
+    stream is that device's current one by default."""
     import torch
-    if torch.cuda.current_device() == dev.index:
-        return _check(call(_stream(stream)), name)
-    with torch.cuda.device(dev):
-        return _check(call(_stream(stream)), name)
+    if dev < 0:
+        raise ValueError(f"{name}: the arguments must be CUDA tensors")
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, name, f, *args)
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    rc = f(*args, st)
+    return rc if rc >= 0 else _check(rc, name)
 
 
-def _same_device(first, **tensors):
-    """Every tensor lives on ``first``'s CUDA device."""
-    if not first.is_cuda:
-        raise ValueError("the arguments must be CUDA tensors")
-    for name, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be a CUDA tensor on {first.device}, is on {t.device}")
-
-
-def _heads_view(t, name):
-    """[tokens, heads, 128] bf16 whose heads are contiguous; returns the stride between tokens."""
+def _heads_view(t, name, dev):
+    """[tokens, heads, 128] bf16 whose heads are contiguous; returns the address and the stride between tokens."""
     import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name} must be bfloat16 [num_tokens, heads, head_dim], is {t.dtype} {tuple(t.shape)}")
     nt, h, d = t.shape
     st, sh, sd = t.stride()
     if (sd != 1 and d != 1) or (sh != d and h != 1):
         raise ValueError(f"{name} must have contiguous heads, has strides {t.stride()}")
-    return st if nt > 1 else max(st, h * d)
-
-
-def _state_pages(kv_pages, acc_pages, pos_pages):
-    """fp32 weights and int32 positions [NB, H_kv, page] that go with kv_pages."""
-    import torch
-    for t, dt, name in ((acc_pages, torch.float32, "acc_pages"), (pos_pages, torch.int32, "pos_pages")):
-        if t is not None:
-            _need(t, dt, name, 3)
-            _shape(t, kv_pages.shape[:3], name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments, is on {t.device}")
+    return t.data_ptr(), st if nt > 1 else max(st, h * d)
 
 
 def sk_rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "plain", factor: float = 1.0,
@@ -445,31 +454,39 @@ def sk_rope_and_cache(q, key, value, positions, freqs, slot_mapping, kv_pages, q
     ``pos_pages`` (int32), both [num_blocks, num_kv_heads, page], receive 0 and the position of each
     stored token: the state that eviction works on."""
     import torch
-    qs, ks, vs = _heads_view(q, "q"), _heads_view(key, "key"), _heads_view(value, "value")
+    dev = q.get_device()
+    (pq, qs), (pk, ks), (pv, vs) = _heads_view(q, "q", dev), _heads_view(key, "key", dev), _heads_view(value, "value", dev)
     nt, hq, d = q.shape
     hkv = key.shape[1]
     _shape(key, (nt, hkv, d), "key")
     _shape(value, (nt, hkv, d), "value")
-    _need(positions, torch.int64, "positions", 1)
-    _need(slot_mapping, torch.int64, "slot_mapping", 1)
-    _shape(positions, (nt,), "positions")
-    _shape(slot_mapping, (nt,), "slot_mapping")
-    _need(freqs, torch.float64, "freqs", 1)
-    _need(q_out, torch.bfloat16, "q_out", 3)
-    _shape(q_out, (nt, hq, d), "q_out")
-    _need(kv_pages, None, "kv_pages", 4)
-    nb, hkv2, page, d2 = kv_pages.shape
+    pp, dt, (nb, hkv2, page, d2) = _pages(kv_pages, dev)
     if hkv2 != hkv or d2 != 2 * d:
         raise ValueError("kv_pages must be [num_blocks, num_kv_heads, page, 2 * head_dim]")
-    _state_pages(kv_pages, acc_pages, pos_pages)
-    _same_device(q, key=key, value=value, positions=positions, freqs=freqs, slot_mapping=slot_mapping,
-                 kv_pages=kv_pages, q_out=q_out, acc_pages=acc_pages, pos_pages=pos_pages)
-    f = lib().sk_rope_and_cache
-    return _launch(q.device, stream, "sk_rope_and_cache", lambda st: f(
-        q.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs, positions.data_ptr(), freqs.data_ptr(),
-        2 * freqs.numel(), 1 if interleaved else 0, attn_factor, slot_mapping.data_ptr(), nt, hq, hkv, d,
-        q_out.data_ptr(), kv_pages.data_ptr(), _kv_dtype(kv_pages), k_scale, v_scale, nb, page, _ptr(acc_pages),
-        _ptr(pos_pages), st))
+    acc = None if acc_pages is None else _fits(acc_pages, torch.float32, (nb, hkv, page), "acc_pages", dev)
+    pos = None if pos_pages is None else _fits(pos_pages, torch.int32, (nb, hkv, page), "pos_pages", dev)
+    rot2 = freqs.numel()
+    return _launch(dev, stream, "sk_rope_and_cache", lib().sk_rope_and_cache, pq, pk, pv, qs, ks, vs,
+                   _fits(positions, torch.int64, (nt,), "positions", dev),
+                   _fits(freqs, torch.float64, (rot2,), "freqs", dev), 2 * rot2, 1 if interleaved else 0, attn_factor,
+                   _fits(slot_mapping, torch.int64, (nt,), "slot_mapping", dev), nt, hq, hkv, d,
+                   _fits(q_out, torch.bfloat16, (nt, hq, d), "q_out", dev), pp, dt, k_scale, v_scale, nb, page, acc,
+                   pos)
+
+
+def _batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q):
+    """Addresses and sizes of a batch over the paged cache, its shapes and devices checked."""
+    import torch
+    dev = q.get_device()
+    _need(q, torch.bfloat16, "q", 3)
+    pp, dt, _ = _pages(kv_pages, dev)
+    if block_table.dim() != 2 or seq_lens.dim() != 1 or cu_seqlens_q.dim() != 1:
+        raise ValueError("block_table must have 2 dimensions, seq_lens and cu_seqlens_q 1")
+    nt, hq, d, nb, hkv, page, bs = _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
+    return (dev, q.data_ptr(), pp, dt, _fits(block_table, torch.int32, block_table.shape, "block_table", dev),
+            _fits(seq_lens, torch.int32, (bs,), "seq_lens", dev),
+            _fits(cu_seqlens_q, torch.int32, (bs + 1,), "cu_seqlens_q", dev), nt, hq, d, nb, hkv, page, bs,
+            block_table.shape[1])
 
 
 def sk_prefill_nsplit(bs: int, num_tokens: int, max_q_len: int, num_q_heads: int, num_kv_heads: int,
@@ -488,33 +505,18 @@ def sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out,
     128]), ``part_m`` and ``part_l`` split the keys over nsplit CTAs; without them one CTA takes all keys of its
     rows."""
     import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(kv_pages, None, "kv_pages", 4)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
-    _need(out, torch.bfloat16, "out", 3)
-    nt, hq, d, nb, hkv, page, bs = _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
-    _shape(out, (nt, hq, d), "out")
-    if lse is not None:
-        _need(lse, torch.float32, "lse", 2)
-        _shape(lse, (nt, hq), "lse")
-    nsplit = 1
+    dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,
+                                                                               cu_seqlens_q)
+    nsplit, po, pm, pl = 1, None, None, None
     if part_o is not None:
-        _need(part_o, torch.float32, "part_o", 4)
-        _need(part_m, torch.float32, "part_m", 3)
-        _need(part_l, torch.float32, "part_l", 3)
         nsplit = part_o.shape[1]
-        _shape(part_o, (nt, nsplit, hq, d), "part_o")
-        _shape(part_m, (nt, nsplit, hq), "part_m")
-        _shape(part_l, (nt, nsplit, hq), "part_l")
-    _same_device(q, kv_pages=kv_pages, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q, out=out,
-                 lse=lse, part_o=part_o, part_m=part_m, part_l=part_l)
-    f = lib().sk_paged_prefill_attn
-    return _launch(q.device, stream, "sk_paged_prefill_attn", lambda st: f(
-        q.data_ptr(), kv_pages.data_ptr(), _kv_dtype(kv_pages), k_scale, v_scale, block_table.data_ptr(),
-        block_table.shape[1], nb, page, seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), bs, nt, max_q_len, hq, hkv, d,
-        sm_scale, 1 if causal else 0, nsplit, _ptr(part_o), _ptr(part_m), _ptr(part_l), out.data_ptr(), _ptr(lse), st))
+        po = _fits(part_o, torch.float32, (nt, nsplit, hq, d), "part_o", dev)
+        pm = _fits(part_m, torch.float32, (nt, nsplit, hq), "part_m", dev)
+        pl = _fits(part_l, torch.float32, (nt, nsplit, hq), "part_l", dev)
+    return _launch(dev, stream, "sk_paged_prefill_attn", lib().sk_paged_prefill_attn, pq, pp, dt, k_scale, v_scale, pb,
+                   stride, nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0, nsplit, po,
+                   pm, pl, _fits(out, torch.bfloat16, (nt, hq, d), "out", dev),
+                   None if lse is None else _fits(lse, torch.float32, (nt, hq), "lse", dev))
 
 
 def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *, max_q_len: int, sm_scale: float,
@@ -561,32 +563,20 @@ def sk_accum_attn_weights(q, kv_pages, block_table, seq_lens, cu_seqlens_q, lse,
     heads of its group, ``lse`` (fp32 [num_tokens, num_q_heads]) being what the attention call returned.
     ``workspace`` is an optional dict that keeps the buffer of e4m3 pages across calls."""
     import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(kv_pages, None, "kv_pages", 4)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
-    _need(lse, torch.float32, "lse", 2)
-    nt, hq, d, nb, hkv, page, bs = _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
-    _shape(lse, (nt, hq), "lse")
-    if acc_pages is None:
-        raise ValueError("acc_pages is required")
-    _state_pages(kv_pages, acc_pages, None)
-    _same_device(q, kv_pages=kv_pages, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q, lse=lse,
-                 acc_pages=acc_pages)
-    dt = _kv_dtype(kv_pages)
+    dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,
+                                                                               cu_seqlens_q)
+    pl = _fits(lse, torch.float32, (nt, hq), "lse", dev)
+    pa = _fits(acc_pages, torch.float32, (nb, hkv, page), "acc_pages", dev)
     buf, need = None, 0
-    if dt == SK_KV_FP8_E4M3:
+    if dt == SK_KV_FP8_E4M3 and dev >= 0:
         need = sk_accum_workspace_bytes(nt, hq, dt)
         ws = workspace if workspace is not None else {}
-        buf = ws.get("accum")
-        if buf is None or buf.numel() < need or buf.device != q.device:
-            buf = ws["accum"] = torch.empty(need, dtype=torch.uint8, device=q.device)
-    f = lib().sk_accum_attn_weights
-    return _launch(q.device, stream, "sk_accum_attn_weights", lambda st: f(
-        q.data_ptr(), kv_pages.data_ptr(), dt, k_scale, block_table.data_ptr(), block_table.shape[1], nb, page,
-        seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0,
-        lse.data_ptr(), acc_pages.data_ptr(), _ptr(buf), need, st))
+        t = ws.get("accum")
+        if t is None or t.numel() < need or t.get_device() != dev:
+            t = ws["accum"] = torch.empty(need, dtype=torch.uint8, device=q.device)
+        buf = t.data_ptr()
+    return _launch(dev, stream, "sk_accum_attn_weights", lib().sk_accum_attn_weights, pq, pp, dt, k_scale, pb, stride,
+                   nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0, pl, pa, buf, need)
 
 
 def sk_evict_capacity(budget: int, max_seq_len: int) -> int:
@@ -602,66 +592,45 @@ def sk_evict_select(acc_pages, pos_pages, block_table, seq_lens, next_pos, src_r
     new lengths; see sk_evict_move.  ``max_seq_len`` bounds the lengths (default: what the block table
     holds)."""
     import torch
+    dev = acc_pages.get_device()
     _need(acc_pages, torch.float32, "acc_pages", 3)
-    _need(pos_pages, torch.int32, "pos_pages", 3)
-    _shape(pos_pages, acc_pages.shape, "pos_pages")
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
     nb, hkv, page = acc_pages.shape
-    bs = seq_lens.numel()
-    if block_table.shape[0] < bs:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows for {bs} sequences")
-    _need(next_pos, torch.int32, "next_pos", 1)
-    _shape(next_pos, (bs,), "next_pos")
-    _need(src_rows, torch.int32, "src_rows", 3)
-    _need(dst_rows, torch.int32, "dst_rows", 3)
-    _need(counts, torch.int32, "counts", 2)
-    _need(new_lens, torch.int32, "new_lens", 1)
-    cap = src_rows.shape[2]
-    _shape(src_rows, (bs, hkv, cap), "src_rows")
-    _shape(dst_rows, (bs, hkv, cap), "dst_rows")
-    _shape(counts, (bs, hkv), "counts")
-    _shape(new_lens, (bs,), "new_lens")
-    if bs and new_lens.data_ptr() == seq_lens.data_ptr():
-        raise ValueError("new_lens must not be seq_lens itself")
-    _same_device(acc_pages, pos_pages=pos_pages, block_table=block_table, seq_lens=seq_lens, next_pos=next_pos,
-                 src_rows=src_rows, dst_rows=dst_rows, counts=counts, new_lens=new_lens)
+    bs, cap = seq_lens.numel(), src_rows.shape[-1]
+    if block_table.dim() != 2 or block_table.shape[0] < bs:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)} for {bs} sequences")
+    stride = block_table.shape[1]
     if max_seq_len is None:
-        max_seq_len = block_table.shape[1] * page
-    f = lib().sk_evict_select
-    return _launch(acc_pages.device, stream, "sk_evict_select", lambda st: f(
-        acc_pages.data_ptr(), pos_pages.data_ptr(), block_table.data_ptr(), block_table.shape[1], nb, page,
-        seq_lens.data_ptr(), next_pos.data_ptr(), bs, hkv, budget, recent, max_seq_len, cap, src_rows.data_ptr(),
-        dst_rows.data_ptr(), counts.data_ptr(), new_lens.data_ptr(), st))
+        max_seq_len = stride * page
+    pl, pn = _fits(seq_lens, torch.int32, (bs,), "seq_lens", dev), _fits(new_lens, torch.int32, (bs,), "new_lens", dev)
+    if pl == pn and bs:
+        raise ValueError("new_lens must not be seq_lens itself")
+    return _launch(dev, stream, "sk_evict_select", lib().sk_evict_select, acc_pages.data_ptr(),
+                   _fits(pos_pages, torch.int32, (nb, hkv, page), "pos_pages", dev),
+                   _fits(block_table, torch.int32, block_table.shape, "block_table", dev), stride, nb, page, pl,
+                   _fits(next_pos, torch.int32, (bs,), "next_pos", dev), bs, hkv, budget, recent, max_seq_len, cap,
+                   _fits(src_rows, torch.int32, (bs, hkv, cap), "src_rows", dev),
+                   _fits(dst_rows, torch.int32, (bs, hkv, cap), "dst_rows", dev),
+                   _fits(counts, torch.int32, (bs, hkv), "counts", dev), pn)
 
 
 def sk_evict_move(src_rows, dst_rows, counts, block_table, kv_pages, acc_pages, pos_pages, *, stream=None) -> int:
     """Moves rows src_rows to dst_rows (sk_evict_select's lists) of ``kv_pages``, ``acc_pages`` and
     ``pos_pages``, in place."""
     import torch
+    dev = src_rows.get_device()
     _need(src_rows, torch.int32, "src_rows", 3)
-    _need(dst_rows, torch.int32, "dst_rows", 3)
-    _shape(dst_rows, src_rows.shape, "dst_rows")
-    _need(counts, torch.int32, "counts", 2)
     bs, hkv, cap = src_rows.shape
-    _shape(counts, (bs, hkv), "counts")
-    _need(block_table, torch.int32, "block_table", 2)
-    if block_table.shape[0] < bs:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows for {bs} sequences")
-    _need(kv_pages, None, "kv_pages", 4)
-    nb, hkv2, page, d2 = kv_pages.shape
+    if block_table.dim() != 2 or block_table.shape[0] < bs:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)} for {bs} sequences")
+    pp, dt, (nb, hkv2, page, d2) = _pages(kv_pages, dev)
     if hkv2 != hkv:
         raise ValueError(f"kv_pages has {hkv2} KV heads, the move lists {hkv}")
-    if acc_pages is None or pos_pages is None:
-        raise ValueError("acc_pages and pos_pages are required")
-    _state_pages(kv_pages, acc_pages, pos_pages)
-    _same_device(src_rows, dst_rows=dst_rows, counts=counts, block_table=block_table, kv_pages=kv_pages,
-                 acc_pages=acc_pages, pos_pages=pos_pages)
-    f = lib().sk_evict_move
-    return _launch(src_rows.device, stream, "sk_evict_move", lambda st: f(
-        src_rows.data_ptr(), dst_rows.data_ptr(), counts.data_ptr(), cap, bs, hkv, d2 // 2, block_table.data_ptr(),
-        block_table.shape[1], nb, page, kv_pages.data_ptr(), _kv_dtype(kv_pages), acc_pages.data_ptr(),
-        pos_pages.data_ptr(), st))
+    return _launch(dev, stream, "sk_evict_move", lib().sk_evict_move, src_rows.data_ptr(),
+                   _fits(dst_rows, torch.int32, (bs, hkv, cap), "dst_rows", dev),
+                   _fits(counts, torch.int32, (bs, hkv), "counts", dev), cap, bs, hkv, d2 // 2,
+                   _fits(block_table, torch.int32, block_table.shape, "block_table", dev), block_table.shape[1], nb,
+                   page, pp, dt, _fits(acc_pages, torch.float32, (nb, hkv, page), "acc_pages", dev),
+                   _fits(pos_pages, torch.int32, (nb, hkv, page), "pos_pages", dev))
 
 
 def evict_rows(kv_pages, acc_pages, pos_pages, block_table, seq_lens, next_pos, *, budget: int, recent: int = 0,

@@ -617,13 +617,18 @@ int sk_evict_select(const float *acc_pages, const int32_t *pos_pages, const int3
     if (acc_pages == nullptr || pos_pages == nullptr || block_table == nullptr || seq_lens == nullptr ||
         next_pos == nullptr || src_rows == nullptr || dst_rows == nullptr || counts == nullptr || new_lens == nullptr)
         return fail(SK_ERR_INVALID, "sk_evict_select: null pointer argument");
+    if ((reinterpret_cast<uintptr_t>(acc_pages) | reinterpret_cast<uintptr_t>(pos_pages)) & 15)
+        return fail(SK_ERR_INVALID, "sk_evict_select: acc_pages and pos_pages must be 16-byte aligned");
     int *status = nullptr;
-    const int rc = status_ptr(&status);
+    int sms = 0;
+    int rc = status_ptr(&status);
+    if (rc == SK_OK)
+        rc = sm_count(&sms);
     if (rc != SK_OK)
         return rc;
     cudaError_t e = launch_evict_select(acc_pages, pos_pages, block_table, block_table_stride, num_blocks, seq_lens,
                                         next_pos, bs, num_kv_heads, budget, recent, max_seq_len, capacity, src_rows,
-                                        dst_rows, counts, new_lens, status, static_cast<cudaStream_t>(stream));
+                                        dst_rows, counts, new_lens, status, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "eviction select kernel launch");
     return SK_OK;

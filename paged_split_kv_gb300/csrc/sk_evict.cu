@@ -7,17 +7,19 @@
 // below `budget` that stay are not touched, so a step that is n rows over its budget moves at most n rows
 // a head instead of closing every gap, and no place is both read and written.
 //
-// The threshold is found by radix selection on a 32-bit key that orders like the weight (11, 11 and 10
-// bits): histogram in shared memory, then the digit that holds the budget-th largest key.  One cluster of
-// up to 16 CTAs serves a (sequence, head); each CTA keeps the keys of its contiguous share of the rows in
-// shared memory, so weights and positions are read once, and the cluster's histograms and counts are
-// summed through distributed shared memory.  Everything is counted, nothing depends on timing: ranks come
-// from ballots and prefix sums.
+// The threshold is found by radix selection on a 32-bit key that orders like the weight (11, 11 and 10 bits, fewer
+// when a digit settles it): histogram in shared memory, then the digit that holds the budget-th largest key.  One
+// cluster of up to 16 CTAs serves a (sequence, head); each CTA keeps the keys of its contiguous share of the rows in
+// shared memory, so weights and positions are read once, four rows a load, and the cluster's histograms and counts
+// are summed through distributed shared memory.  Two walks over the keys follow: one counts, per warp, the rows above
+// the threshold and at it, below and past row `budget` (from these counts of all warps and CTAs follows how many ties
+// each may take and where its lists start), one writes the lists.  Nothing depends on timing.
 //
 // Move.  One warp (half a warp for e4m3 rows) copies a row of 2 * head_dim elements, 16 bytes a lane, its
 // weight and its position; several rows are in flight per warp.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -41,15 +43,20 @@ struct SelectArgs {
     const int32_t *next_pos;
     int32_t *src, *dst, *counts, *new_lens;
     int *status;
-    int bt_stride, num_blocks, hkv, budget, recent, cap, max_len, chunk;   // chunk: rows per CTA, a multiple of 32
+    int bt_stride, num_blocks, hkv, budget, recent, cap, max_len;
+};
+
+// Rows above the threshold and at it, below row `budget` (low) and from it on.
+struct Counts {
+    uint32_t above_low, ties_low, above_high, ties_high;
 };
 
 struct SelectShared {
     uint32_t hist[3][kBins];
     uint32_t warp_sum[kSelWarps];
-    uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
-    uint32_t found_digit, found_above;
-    uint32_t ties, holes, tails;                 // this CTA's counts, read by the cluster
+    Counts warp[kSelWarps];
+    Counts cta;                                  // read by the cluster
+    uint32_t found_digit, found_above, found_count;
 };
 
 // Order-preserving key of a weight: larger weight, larger key; NaN like -inf; both zeros alike.
@@ -62,30 +69,44 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 
 __device__ __forceinline__ uint32_t warp_sum_u32(uint32_t v) { return __reduce_add_sync(kFull, v); }
 
-// Exclusive prefix over the CTA's warps of a per-warp count (the same in every lane); also the total.
-__device__ __forceinline__ uint32_t warps_prefix(uint32_t v, uint32_t *buf, int warp, int lane, uint32_t *total)
+// Counts one digit of the warp's live keys.  Equal digits in the whole warp (rows never looked at, all zero) would
+// serialise: one addition for all.
+__device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t digit, bool live)
 {
-    if (lane == 0)
-        buf[warp] = v;
-    __syncthreads();
-    const uint32_t mine = buf[lane];             // kSelWarps == 32
-    const uint32_t before = warp_sum_u32(lane < warp ? mine : 0u);
-    *total = warp_sum_u32(mine);
-    __syncthreads();
-    return before;
+    const uint32_t active = __ballot_sync(kFull, live);
+    if (active == 0)
+        return;
+    const int first_lane = __ffs(active) - 1;
+    const uint32_t first = __shfl_sync(kFull, digit, first_lane);
+    if (__all_sync(kFull, !live || digit == first)) {
+        if ((int)(threadIdx.x & 31) == first_lane)
+            atomicAdd(hist + first, (uint32_t)__popc(active));
+    } else if (live) {
+        atomicAdd(hist + digit, 1u);
+    }
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a)
 {
-    extern __shared__ uint32_t keys[];           // [chunk]
+    extern __shared__ uint4 keys4[];             // four rows each
     __shared__ SelectShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int csize = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pair = blockIdx.x / csize;
     const int s = pair / a.hkv, h = pair - s * a.hkv;
+    auto meet = [&]() {
+        if (csize > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+#pragma unroll
+    for (int d = 0; d < 3; ++d)
+        reinterpret_cast<uint2 *>(sh.hist[d])[tid] = make_uint2(0u, 0u);
     wait_prior_grid();
     const int L = __ldg(a.seq_lens + s);
+    const int edge = __ldg(a.next_pos + s) - a.recent;
     const bool bad = L < 0 || L > a.max_len || (long long)L > (long long)a.bt_stride * kPage;
     const bool over = !bad && L > a.budget;
     if (crank == 0 && tid == 0) {
@@ -99,72 +120,96 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     if (!over)
         return;                                  // the whole cluster takes this branch
 
-    const int lo = crank * a.chunk;
-    const int n = max(0, min(a.chunk, L - lo));  // this CTA's rows [lo, lo + n)
-    const int edge = __ldg(a.next_pos + s) - a.recent;
-    for (int i = tid; i < 3 * kBins; i += kSelThreads)
-        (&sh.hist[0][0])[i] = 0;
+    const int chunk = ((L + csize - 1) / csize + 127) / 128 * 128;
+    const int lo = min(L, crank * chunk);
+    const int n = min(chunk, L - lo);            // this CTA's rows [lo, lo + n)
+    const int quads = (n + 3) / 4;
     __syncthreads();
 
     // ---- keys, and the first digit's histogram
     const int32_t *bt = a.block_table + (long long)s * a.bt_stride;
-    auto count_digit = [&](uint32_t *hist, uint32_t digit, bool live) {
-        // equal digits in the whole warp (rows never looked at, all zero) would serialise: one add
-        const uint32_t active = __ballot_sync(kFull, live);
-        if (active == 0)
-            return;
-        const uint32_t first = __shfl_sync(kFull, digit, __ffs(active) - 1);
-        if (__all_sync(kFull, !live || digit == first)) {
-            if (lane == 0)
-                atomicAdd(hist + first, (uint32_t)__popc(active));
-        } else if (live) {
-            atomicAdd(hist + digit, 1u);
+    constexpr int kAtOnce = 4;
+    for (int i0 = 0; i0 < quads; i0 += kSelThreads * kAtOnce) {
+        int blk[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = i0 + u * kSelThreads + tid;
+            blk[u] = i < quads ? __ldg(bt + (lo + 4 * i) / kPage) : 0;
         }
-    };
-    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        const bool live = i < n;
-        uint32_t key = 0;
-        if (live) {
-            const int r = lo + i;
-            const int blk = __ldg(bt + r / kPage);
-            float w = -CUDART_INF_F;
-            int pos = edge - 1;
-            if (blk >= 0 && blk < a.num_blocks) {
-                const long long at = ((long long)blk * a.hkv + h) * kPage + r % kPage;
-                w = a.acc[at];
-                pos = a.pos[at];
-            } else {
-                atomicOr(a.status, SK_DEV_BAD_BLOCK);
+        float4 w[kAtOnce];
+        int4 p[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = i0 + u * kSelThreads + tid;
+            w[u] = make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+            p[u] = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
+            if (i < quads) {
+                if (blk[u] >= 0 && blk[u] < a.num_blocks) {
+                    const long long at = ((long long)blk[u] * a.hkv + h) * kPage + (lo + 4 * i) % kPage;
+                    w[u] = *reinterpret_cast<const float4 *>(a.acc + at);
+                    if (a.recent > 0)
+                        p[u] = *reinterpret_cast<const int4 *>(a.pos + at);
+                } else {
+                    atomicOr(a.status, SK_DEV_BAD_BLOCK);
+                }
             }
-            key = (a.recent > 0 && pos >= edge) ? 0xFFFFFFFFu : weight_key(w);
-            keys[i] = key;
         }
-        count_digit(sh.hist[0], key >> 21, live);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = i0 + u * kSelThreads + tid;
+            if (i0 + u * kSelThreads + warp * 32 >= quads)
+                break;                           // uniform in the warp
+            const bool rec = a.recent > 0;
+            uint4 k;
+            k.x = rec && p[u].x >= edge ? 0xFFFFFFFFu : weight_key(w[u].x);
+            k.y = rec && p[u].y >= edge ? 0xFFFFFFFFu : weight_key(w[u].y);
+            k.z = rec && p[u].z >= edge ? 0xFFFFFFFFu : weight_key(w[u].z);
+            k.w = rec && p[u].w >= edge ? 0xFFFFFFFFu : weight_key(w[u].w);
+            if (i < quads)
+                keys4[i] = k;
+            count_digit(sh.hist[0], k.x >> 21, 4 * i < n);
+            count_digit(sh.hist[0], k.y >> 21, 4 * i + 1 < n);
+            count_digit(sh.hist[0], k.z >> 21, 4 * i + 2 < n);
+            count_digit(sh.hist[0], k.w >> 21, 4 * i + 3 < n);
+        }
     }
 
-    // ---- the budget-th largest key, digit by digit
-    uint32_t prefix = 0, want = (uint32_t)a.budget;      // keys still to take among those with this prefix
-    const int shift[3] = {21, 10, 0}, width[3] = {11, 11, 10};
-#pragma unroll 1
+    // ---- the budget-th largest key, digit by digit, until a digit's keys are all taken
+    uint32_t prefix = 0, mask = 0, want = (uint32_t)a.budget;    // keys still to take among those with this prefix
+    bool settled = false;
+#pragma unroll
     for (int d = 0; d < 3; ++d) {
+        constexpr int shift[3] = {21, 10, 0};
+        if (settled)
+            continue;
         if (d > 0) {
-            const uint32_t mask = d == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-            for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+            for (int i0 = 0; i0 < quads; i0 += kSelThreads) {
                 const int i = i0 + tid;
-                const uint32_t key = i < n ? keys[i] : 0u;
-                count_digit(sh.hist[d], (key >> shift[d]) & ((1u << width[d]) - 1u), i < n && (key & mask) == prefix);
+                const uint4 k = i < quads ? keys4[i] : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    count_digit(sh.hist[d], (kk[e] >> shift[d]) & (d == 1 ? 0x7FFu : 0x3FFu),
+                                4 * i + e < n && (kk[e] & mask) == prefix);
             }
         }
-        cluster.sync();                          // every CTA's histogram is complete
+        meet();                                  // every CTA's histogram is complete
         // thread t holds bins 2 t and 2 t + 1, summed over the cluster; suffix sums from the top bin down
         uint32_t b0 = 0, b1 = 0;
-        for (int c = 0; c < csize; ++c) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(&sh.hist[d][2 * tid], c));
-            b0 += v.x;
-            b1 += v.y;
+        if (csize > 1) {
+#pragma unroll 4
+            for (int c = 0; c < csize; ++c) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(&sh.hist[d][2 * tid], c));
+                b0 += v.x;
+                b1 += v.y;
+            }
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(&sh.hist[d][2 * tid]);
+            b0 = v.x;
+            b1 = v.y;
         }
         uint32_t above = b0 + b1;                // inclusive suffix over the warp's higher lanes
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t u = __shfl_down_sync(kFull, above, o);
             above += lane + o < 32 ? u : 0u;
@@ -177,83 +222,141 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         if (above < want && above + b1 >= want) {
             sh.found_digit = 2 * tid + 1;
             sh.found_above = above;
+            sh.found_count = b1;
         } else if (above + b1 < want && above + b1 + b0 >= want) {
             sh.found_digit = 2 * tid;
             sh.found_above = above + b1;
+            sh.found_count = b0;
         }
         __syncthreads();
         prefix |= sh.found_digit << shift[d];
+        mask = d == 0 ? 0xFFE00000u : (d == 1 ? 0xFFFFFC00u : 0xFFFFFFFFu);
         want -= sh.found_above;
-        __syncthreads();
+        settled = sh.found_count == want;
     }
-    // keys above `prefix` stay, and the first `want` rows whose key equals it
+    // rows with (key & mask) above `prefix` stay, and the first `want` rows that equal it
 
-    // ---- a warp's rows are contiguous: [w0, w1) of this CTA's
-    const int per_warp = (n + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+    // ---- first walk: a warp's rows are contiguous, [w0, w1) of this CTA's, 128 at a time
+    const int per_warp = (n + kSelWarps * 128 - 1) / (kSelWarps * 128) * 128;
     const int w0 = min(n, warp * per_warp), w1 = min(n, w0 + per_warp);
-    uint32_t ties = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        ties += __popc(__ballot_sync(kFull, i < w1 && keys[i] == prefix));
-    }
-    uint32_t cta_ties;
-    uint32_t tie0 = warps_prefix(ties, sh.warp_sum, warp, lane, &cta_ties);
-    if (tid == 0)
-        sh.ties = cta_ties;
-    cluster.sync();
-    for (int c = 0; c < crank; ++c)
-        tie0 += *cluster.map_shared_rank(&sh.ties, c);
-
-    // the rows that go below the budget, and those that stay at or past it
-    auto walk = [&](auto &&visit) {
-        uint32_t tie = tie0;
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-            const int i = i0 + lane;
-            const uint32_t key = i < w1 ? keys[i] : 0u;
-            const bool eq = i < w1 && key == prefix;
-            const uint32_t eqs = __ballot_sync(kFull, eq);
-            const uint32_t rank = tie + __popc(eqs & ((1u << lane) - 1u));
-            tie += __popc(eqs);
-            const bool stays = i < w1 && (key > prefix || (eq && rank < want));
-            const int r = lo + i;
-            visit(r, i < w1 && !stays && r < a.budget, stays && r >= a.budget);
+    Counts mine = {0, 0, 0, 0};
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        const uint4 k = i < w1 ? keys4[i / 4] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t kk[4] = {k.x & mask, k.y & mask, k.z & mask, k.w & mask};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool live = i + e < w1, low = lo + i + e < a.budget;
+            const uint32_t gt = live && kk[e] > prefix, eq = live && kk[e] == prefix;
+            mine.above_low += low ? gt : 0u;
+            mine.above_high += low ? 0u : gt;
+            mine.ties_low += low ? eq : 0u;
+            mine.ties_high += low ? 0u : eq;
         }
+    }
+    mine.above_low = warp_sum_u32(mine.above_low);
+    mine.above_high = warp_sum_u32(mine.above_high);
+    mine.ties_low = warp_sum_u32(mine.ties_low);
+    mine.ties_high = warp_sum_u32(mine.ties_high);
+    if (lane == 0)
+        sh.warp[warp] = mine;
+    __syncthreads();
+    const Counts other = sh.warp[lane];          // kSelWarps == 32
+    if (warp == 0) {
+        const Counts all = {warp_sum_u32(other.above_low), warp_sum_u32(other.ties_low),
+                            warp_sum_u32(other.above_high), warp_sum_u32(other.ties_high)};
+        if (lane == 0)
+            sh.cta = all;
+    }
+    meet();
+    // ---- where this CTA's lists start: the CTAs before it, in row order
+    uint32_t tie0 = 0, hole0 = 0, tail0 = 0;
+    auto pass = [&](const Counts &c, int first_row, int rows) {
+        // of `rows` rows from first_row on, ties are taken in order while the threshold has room
+        const uint32_t low_rows = (uint32_t)max(0, min(rows, a.budget - first_row));
+        const uint32_t room = want > tie0 ? want - tie0 : 0u;
+        const uint32_t taken_low = min(room, c.ties_low), taken_high = min(room - taken_low, c.ties_high);
+        hole0 += low_rows - c.above_low - taken_low;
+        tail0 += c.above_high + taken_high;
+        tie0 += c.ties_low + c.ties_high;
     };
-    uint32_t holes = 0, tails = 0;
-    walk([&](int, bool hole, bool tail) {
-        holes += __popc(__ballot_sync(kFull, hole));
-        tails += __popc(__ballot_sync(kFull, tail));
-    });
-    uint32_t cta_holes, cta_tails;
-    uint32_t hole0 = warps_prefix(holes, sh.warp_a, warp, lane, &cta_holes);
-    uint32_t tail0 = warps_prefix(tails, sh.warp_b, warp, lane, &cta_tails);
-    if (tid == 0) {
-        sh.holes = cta_holes;
-        sh.tails = cta_tails;
-    }
-    cluster.sync();
-    for (int c = 0; c < crank; ++c) {
-        hole0 += *cluster.map_shared_rank(&sh.holes, c);
-        tail0 += *cluster.map_shared_rank(&sh.tails, c);
-    }
+    for (int c = 0; c < crank; ++c)
+        pass(*cluster.map_shared_rank(&sh.cta, c), c * chunk, min(chunk, L - c * chunk));
     if (crank == csize - 1 && tid == 0) {
-        const uint32_t all = tail0 + cta_tails;  // warp 0's prefix is 0
-        a.counts[pair] = (int32_t)all;
-        if (all > (uint32_t)a.cap)
+        const uint32_t before_tie = tie0, before_hole = hole0, before_tail = tail0;
+        pass(sh.cta, lo, n);
+        a.counts[pair] = (int32_t)tail0;
+        if (tail0 > (uint32_t)a.cap)
             atomicOr(a.status, SK_DEV_INTERNAL);
+        tie0 = before_tie;
+        hole0 = before_hole;
+        tail0 = before_tail;
     }
+    if (csize > 1)
+        cluster.barrier_arrive();                // this CTA has read the others' shared memory
+    // and where this warp's do
+    for (int w = 0; w < warp; ++w)
+        pass(sh.warp[w], lo + min(n, w * per_warp), max(0, min(n, (w + 1) * per_warp) - min(n, w * per_warp)));
+
+    // ---- second walk: the lists
     int32_t *src = a.src + (long long)pair * a.cap, *dst = a.dst + (long long)pair * a.cap;
-    walk([&](int r, bool hole, bool tail) {
-        const uint32_t hm = __ballot_sync(kFull, hole), tm = __ballot_sync(kFull, tail);
-        const uint32_t below = (1u << lane) - 1u;
-        if (hole && hole0 + __popc(hm & below) < (uint32_t)a.cap)
-            dst[hole0 + __popc(hm & below)] = r;
-        if (tail && tail0 + __popc(tm & below) < (uint32_t)a.cap)
-            src[tail0 + __popc(tm & below)] = r;
-        hole0 += __popc(hm);
-        tail0 += __popc(tm);
-    });
-    cluster.sync();                              // no CTA leaves while another reads its counts
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        const uint4 k = i < w1 ? keys4[i / 4] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t kk[4] = {k.x & mask, k.y & mask, k.z & mask, k.w & mask};
+        uint32_t eqs = 0, stays = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            eqs |= (i + e < w1 && kk[e] == prefix) ? 1u << e : 0u;
+            stays |= (i + e < w1 && kk[e] > prefix) ? 1u << e : 0u;
+        }
+        if (__any_sync(kFull, eqs != 0)) {
+            uint32_t rank = __popc(eqs);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(kFull, rank, o);
+                rank += lane >= o ? u : 0u;
+            }
+            const uint32_t total = __shfl_sync(kFull, rank, 31);
+            rank += tie0 - __popc(eqs);
+            tie0 += total;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (eqs >> e & 1u) {
+                    stays |= rank < want ? 1u << e : 0u;
+                    ++rank;
+                }
+            }
+        }
+        uint32_t holes = 0, tails = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool low = lo + i + e < a.budget, live = i + e < w1, st = stays >> e & 1u;
+            holes |= live && low && !st ? 1u << e : 0u;
+            tails |= live && !low && st ? 1u << e : 0u;
+        }
+        uint32_t both = __popc(holes) | __popc(tails) << 16;
+        const uint32_t own = both;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(kFull, both, o);
+            both += lane >= o ? u : 0u;
+        }
+        const uint32_t total = __shfl_sync(kFull, both, 31);
+        both -= own;
+        uint32_t hp = hole0 + (both & 0xFFFFu), tp = tail0 + (both >> 16);
+        hole0 += total & 0xFFFFu;
+        tail0 += total >> 16;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if ((holes >> e & 1u) && hp++ < (uint32_t)a.cap)
+                dst[hp - 1] = lo + i + e;
+            if ((tails >> e & 1u) && tp++ < (uint32_t)a.cap)
+                src[tp - 1] = lo + i + e;
+        }
+    }
+    if (csize > 1)
+        cluster.barrier_wait();                  // no CTA leaves while another reads its counts
 }
 
 constexpr int kMoveThreads = 256;
@@ -334,17 +437,20 @@ evict_move_kernel(const int32_t *__restrict__ src, const int32_t *__restrict__ d
 cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int32_t *block_table, int bt_stride,
                                 int num_blocks, const int32_t *seq_lens, const int32_t *next_pos, int bs, int hkv,
                                 int budget, int recent, int max_len, int cap, int32_t *src, int32_t *dst,
-                                int32_t *counts, int32_t *new_lens, int *status, cudaStream_t stream)
+                                int32_t *counts, int32_t *new_lens, int *status, int num_sms, cudaStream_t stream)
 {
-    // the smallest cluster whose CTAs hold their share of the keys in half an SM's shared memory, so that
-    // two CTAs fit; 16 CTAs (a size that has to be allowed explicitly) with up to 192 KB each past that
-    int c = 1;
-    while (c < kEvictMaxCluster && (long long)c * (kEvictMaxChunk / 2) < max_len)
-        c *= 2;
+    // The CTAs of a cluster hold all keys of the longest sequence in shared memory; with SMs to spare the cluster
+    // grows to 8 CTAs (above that a cluster needs a whole GPC), as long as each has 4096 rows.
+    const int pairs = bs * hkv;
+    int c = (max_len + kEvictMaxChunk - 1) / kEvictMaxChunk;
+    c = c < 1 ? 1 : c;
+    int more = num_sms / pairs < (max_len + 4095) / 4096 ? num_sms / pairs : (max_len + 4095) / 4096;
+    more = more < 8 ? more : 8;
+    c = c > more ? c : more;
     SelectArgs a{acc, pos, block_table, seq_lens, next_pos, src, dst, counts, new_lens, status,
-                 bt_stride, num_blocks, hkv, budget, recent, cap, max_len, 0};
-    a.chunk = ((max_len + c - 1) / c + 31) / 32 * 32;
-    const size_t smem = (size_t)a.chunk * 4;
+                 bt_stride, num_blocks, hkv, budget, recent, cap, max_len};
+    const int chunk = ((max_len + c - 1) / c + 127) / 128 * 128;
+    const size_t smem = (size_t)chunk * 4;
     cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kEvictMaxChunk * 4);
     if (e == cudaSuccess)
@@ -364,7 +470,7 @@ cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int3
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = c > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
 }
 

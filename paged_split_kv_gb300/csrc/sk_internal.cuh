@@ -218,7 +218,7 @@ constexpr int kEvictMaxChunk = 49152;
 cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int32_t *block_table, int bt_stride,
                                 int num_blocks, const int32_t *seq_lens, const int32_t *next_pos, int bs, int hkv,
                                 int budget, int recent, int max_len, int cap, int32_t *src, int32_t *dst,
-                                int32_t *counts, int32_t *new_lens, int *status, cudaStream_t stream);
+                                int32_t *counts, int32_t *new_lens, int *status, int num_sms, cudaStream_t stream);
 cudaError_t launch_evict_move(const int32_t *src, const int32_t *dst, const int32_t *counts, int cap, int bs, int hkv,
                               const int32_t *block_table, int bt_stride, int num_blocks, void *pages, int kv_dtype,
                               float *acc, int32_t *pos, int *status, int num_sms, cudaStream_t stream);

@@ -43,7 +43,7 @@ def test_evict_refusals(sk):
     call = caller(sk.lib().sk_evict_select, dict(
         acc=FAKE, pos=FAKE, bt=FAKE, stride=10, nb=8, page=16, lens=FAKE, nxt=FAKE, bs=2, hkv=2, budget=32, recent=4,
         mx=160, cap=32, src=FAKE, dst=FAKE, cnt=FAKE, new=FAKE, st=None))
-    for kw in (dict(bs=0), dict(bs=32768), dict(hkv=0), dict(nb=0), dict(stride=0), dict(budget=0), dict(recent=-1),
+    for kw in (dict(bs=0), dict(bs=32768), dict(hkv=0), dict(nb=0), dict(stride=0), dict(budget=0), dict(recent=-1), dict(acc=ODD),
                dict(recent=33), dict(mx=-1), dict(acc=None), dict(nxt=None), dict(new=None)):
         assert call(**kw) == -1, kw
     assert call(page=8) == -3 and call(mx=786433) == -3
