@@ -374,8 +374,8 @@ int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t
  *
  * acc_pages fp32, pos_pages int32 [num_blocks, num_kv_heads, page_size], 16-byte aligned; src_rows, dst_rows int32 [bs,
  * num_kv_heads, capacity], capacity >= sk_evict_capacity(budget, max_seq_len); counts int32 [bs,
- * num_kv_heads]; new_lens int32 [bs], not seq_lens itself.  max_seq_len: an upper bound on the lengths, at
- * most 786432; it sizes the launch.  0 <= recent <= budget.  Asynchronous on `stream`, no allocation,
+ * num_kv_heads]; new_lens int32 [bs], not seq_lens itself.  max_seq_len: an upper bound on the lengths; it
+ * sizes the launch.  0 <= recent <= budget.  Asynchronous on `stream`, no allocation,
  * capture safe, the same result whatever the timing.
  * Returns SK_OK or a negative sk_status. */
 int sk_evict_select(const float *acc_pages, const int32_t *pos_pages, const int32_t *block_table,

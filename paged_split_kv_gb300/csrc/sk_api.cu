@@ -606,10 +606,7 @@ int sk_evict_select(const float *acc_pages, const int32_t *pos_pages, const int3
     if (budget < 1 || recent < 0 || recent > budget || max_seq_len < 0)
         return fail(SK_ERR_INVALID, "sk_evict_select: budget=%d, recent=%d (at most the budget), max_seq_len=%d",
                     budget, recent, max_seq_len);
-    if (max_seq_len > kEvictMaxCluster * kEvictMaxChunk)
-        return fail(SK_ERR_UNSUPPORTED, "sk_evict_select: max_seq_len=%d above %d", max_seq_len,
-                    kEvictMaxCluster * kEvictMaxChunk);
-    if ((long long)bs * num_kv_heads * kEvictMaxCluster > 0x7FFFFFFFLL)
+    if ((long long)bs * num_kv_heads * 16 > 0x7FFFFFFFLL)
         return fail(SK_ERR_UNSUPPORTED, "sk_evict_select: %d sequences of %d heads", bs, num_kv_heads);
     if (capacity < sk_evict_capacity(budget, max_seq_len))
         return fail(SK_ERR_CAPACITY, "sk_evict_select: capacity=%d below min(budget, max_seq_len - budget) = %d",

@@ -10,7 +10,7 @@
 // The threshold is found by radix selection on a 32-bit key that orders like the weight (11, 11 and 10 bits, fewer
 // when a digit settles it): histogram in shared memory, then the digit that holds the budget-th largest key.  One
 // cluster of up to 16 CTAs serves a (sequence, head); each CTA keeps the keys of its contiguous share of the rows in
-// shared memory, so weights and positions are read once, four rows a load, and the cluster's histograms and counts
+// shared memory (the first 51200 of them), so weights and positions are read once, four rows a load, and the cluster's histograms and counts
 // are summed through distributed shared memory.  Two walks over the keys follow: one counts, per warp, the rows above
 // the threshold and at it, below and past row `budget` (from these counts of all warps and CTAs follows how many ties
 // each may take and where its lists start), one writes the lists.  Nothing depends on timing.
@@ -34,6 +34,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kEvictKept = 51200;                // keys (200 KB) that a CTA keeps in shared memory beside its histograms
 
 struct SelectArgs {
     const float *acc;
@@ -44,6 +45,7 @@ struct SelectArgs {
     int32_t *src, *dst, *counts, *new_lens;
     int *status;
     int bt_stride, num_blocks, hkv, budget, recent, cap, max_len;
+    int kept;                                    // rows per CTA whose keys fit in shared memory
 };
 
 // Rows above the threshold and at it, below row `budget` (low) and from it on.
@@ -86,10 +88,36 @@ __device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t digit, bool
     }
 }
 
+// Lane l holds the counts of the l-th of up to 32 consecutive parts of a row range.  Ties are taken in row order while
+// the threshold has room for them: gives the number of ties before lane l's part, and the part's rows for either list.
+struct Part {
+    uint32_t ties_before, holes, tails;
+};
+
+__device__ __forceinline__ Part part_of(const Counts &c, int first_row, int rows, int budget, uint32_t want,
+                                        uint32_t ties_before, int lane)
+{
+    const uint32_t ties = c.ties_low + c.ties_high;
+    uint32_t incl = ties;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(kFull, incl, o);
+        incl += lane >= o ? u : 0u;
+    }
+    Part p;
+    p.ties_before = ties_before + incl - ties;
+    const uint32_t room = want > p.ties_before ? want - p.ties_before : 0u;
+    const uint32_t low = min(room, c.ties_low), high = min(room - low, c.ties_high);
+    p.holes = (uint32_t)max(0, min(rows, budget - first_row)) - c.above_low - low;
+    p.tails = c.above_high + high;
+    return p;
+}
+
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a)
 {
-    extern __shared__ uint4 keys4[];             // four rows each
+    extern __shared__ uint4 keys4[];             // four rows each, the first a.kept rows of this CTA's
     __shared__ SelectShared sh;
+    const uint32_t *keys = reinterpret_cast<const uint32_t *>(keys4);
     cg::cluster_group cluster = cg::this_cluster();
     const int csize = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -101,9 +129,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         else
             __syncthreads();
     };
-#pragma unroll
-    for (int d = 0; d < 3; ++d)
-        reinterpret_cast<uint2 *>(sh.hist[d])[tid] = make_uint2(0u, 0u);
+    for (int i = tid; i < 3 * kBins / 2; i += kSelThreads)
+        reinterpret_cast<uint2 *>(sh.hist)[i] = make_uint2(0u, 0u);
     wait_prior_grid();
     const int L = __ldg(a.seq_lens + s);
     const int edge = __ldg(a.next_pos + s) - a.recent;
@@ -124,48 +151,61 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     const int lo = min(L, crank * chunk);
     const int n = min(chunk, L - lo);            // this CTA's rows [lo, lo + n)
     const int quads = (n + 3) / 4;
+    const int32_t *bt = a.block_table + (long long)s * a.bt_stride;
     __syncthreads();
 
-    // ---- keys, and the first digit's histogram
-    const int32_t *bt = a.block_table + (long long)s * a.bt_stride;
-    constexpr int kAtOnce = 4;
-    for (int i0 = 0; i0 < quads; i0 += kSelThreads * kAtOnce) {
-        int blk[kAtOnce];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int i = i0 + u * kSelThreads + tid;
-            blk[u] = i < quads ? __ldg(bt + (lo + 4 * i) / kPage) : 0;
+    // the keys of row quad i, from its weights and positions
+    auto block_of = [&](int i) { return i < quads ? __ldg(bt + (lo + 4 * i) / kPage) : 0; };
+    auto load_quad = [&](int i, int blk, float4 &w, int4 &p) {
+        w = make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+        p = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
+        if (i >= quads)
+            return;
+        if (blk >= 0 && blk < a.num_blocks) {
+            const long long at = ((long long)blk * a.hkv + h) * kPage + (lo + 4 * i) % kPage;
+            w = *reinterpret_cast<const float4 *>(a.acc + at);
+            if (a.recent > 0)
+                p = *reinterpret_cast<const int4 *>(a.pos + at);
+        } else {
+            atomicOr(a.status, SK_DEV_BAD_BLOCK);
         }
+    };
+    auto key_of = [&](float w, int pos) { return a.recent > 0 && pos >= edge ? 0xFFFFFFFFu : weight_key(w); };
+    auto quad_key = [&](const float4 &w, const int4 &p) {
+        return make_uint4(key_of(w.x, p.x), key_of(w.y, p.y), key_of(w.z, p.z), key_of(w.w, p.w));
+    };
+    auto quad_at = [&](int i) {                  // as kept, or computed again past what is kept
+        if (4 * i < a.kept)
+            return i < quads ? keys4[i] : make_uint4(0u, 0u, 0u, 0u);
+        float4 w;
+        int4 p;
+        load_quad(i, block_of(i), w, p);
+        return quad_key(w, p);
+    };
+
+    // ---- keys, and the first digit's histogram
+    constexpr int kAtOnce = 4;
+    int blk[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+        blk[u] = block_of(u * kSelThreads + tid);
+#pragma unroll 1
+    for (int i0 = tid; i0 - lane < quads; i0 += kSelThreads * kAtOnce) {
         float4 w[kAtOnce];
         int4 p[kAtOnce];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int i = i0 + u * kSelThreads + tid;
-            w[u] = make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
-            p[u] = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
-            if (i < quads) {
-                if (blk[u] >= 0 && blk[u] < a.num_blocks) {
-                    const long long at = ((long long)blk[u] * a.hkv + h) * kPage + (lo + 4 * i) % kPage;
-                    w[u] = *reinterpret_cast<const float4 *>(a.acc + at);
-                    if (a.recent > 0)
-                        p[u] = *reinterpret_cast<const int4 *>(a.pos + at);
-                } else {
-                    atomicOr(a.status, SK_DEV_BAD_BLOCK);
-                }
-            }
-        }
+        for (int u = 0; u < kAtOnce; ++u)
+            load_quad(i0 + u * kSelThreads, blk[u], w[u], p[u]);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+            blk[u] = block_of(i0 + (u + kAtOnce) * kSelThreads);
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-            const int i = i0 + u * kSelThreads + tid;
-            if (i0 + u * kSelThreads + warp * 32 >= quads)
+            const int i = i0 + u * kSelThreads;
+            if (i - lane >= quads)
                 break;                           // uniform in the warp
-            const bool rec = a.recent > 0;
-            uint4 k;
-            k.x = rec && p[u].x >= edge ? 0xFFFFFFFFu : weight_key(w[u].x);
-            k.y = rec && p[u].y >= edge ? 0xFFFFFFFFu : weight_key(w[u].y);
-            k.z = rec && p[u].z >= edge ? 0xFFFFFFFFu : weight_key(w[u].z);
-            k.w = rec && p[u].w >= edge ? 0xFFFFFFFFu : weight_key(w[u].w);
-            if (i < quads)
+            const uint4 k = quad_key(w[u], p[u]);
+            if (i < quads && 4 * i < a.kept)
                 keys4[i] = k;
             count_digit(sh.hist[0], k.x >> 21, 4 * i < n);
             count_digit(sh.hist[0], k.y >> 21, 4 * i + 1 < n);
@@ -176,37 +216,34 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 
     // ---- the budget-th largest key, digit by digit, until a digit's keys are all taken
     uint32_t prefix = 0, mask = 0, want = (uint32_t)a.budget;    // keys still to take among those with this prefix
-    bool settled = false;
-#pragma unroll
+#pragma unroll 1
     for (int d = 0; d < 3; ++d) {
-        constexpr int shift[3] = {21, 10, 0};
-        if (settled)
-            continue;
+        const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
         if (d > 0) {
-            for (int i0 = 0; i0 < quads; i0 += kSelThreads) {
-                const int i = i0 + tid;
-                const uint4 k = i < quads ? keys4[i] : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    count_digit(sh.hist[d], (kk[e] >> shift[d]) & (d == 1 ? 0x7FFu : 0x3FFu),
-                                4 * i + e < n && (kk[e] & mask) == prefix);
+            const uint32_t digit = d == 1 ? 0x7FFu : 0x3FFu;
+#pragma unroll 1
+            for (int i = tid; i - lane < quads; i += kSelThreads) {
+                const uint4 k = quad_at(i);
+                const int left = n - 4 * i;
+                const bool m0 = left > 0 && (k.x & mask) == prefix, m1 = left > 1 && (k.y & mask) == prefix;
+                const bool m2 = left > 2 && (k.z & mask) == prefix, m3 = left > 3 && (k.w & mask) == prefix;
+                if (!__any_sync(kFull, m0 || m1 || m2 || m3))
+                    continue;
+                count_digit(sh.hist[d], k.x >> shift & digit, m0);
+                count_digit(sh.hist[d], k.y >> shift & digit, m1);
+                count_digit(sh.hist[d], k.z >> shift & digit, m2);
+                count_digit(sh.hist[d], k.w >> shift & digit, m3);
             }
         }
         meet();                                  // every CTA's histogram is complete
         // thread t holds bins 2 t and 2 t + 1, summed over the cluster; suffix sums from the top bin down
         uint32_t b0 = 0, b1 = 0;
-        if (csize > 1) {
 #pragma unroll 4
-            for (int c = 0; c < csize; ++c) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(&sh.hist[d][2 * tid], c));
-                b0 += v.x;
-                b1 += v.y;
-            }
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(&sh.hist[d][2 * tid]);
-            b0 = v.x;
-            b1 = v.y;
+        for (int c = 0; c < csize; ++c) {
+            const uint2 *at = reinterpret_cast<const uint2 *>(&sh.hist[d][2 * tid]);
+            const uint2 v = csize > 1 ? *cluster.map_shared_rank(at, c) : *at;
+            b0 += v.x;
+            b1 += v.y;
         }
         uint32_t above = b0 + b1;                // inclusive suffix over the warp's higher lanes
 #pragma unroll
@@ -229,130 +266,103 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
             sh.found_count = b0;
         }
         __syncthreads();
-        prefix |= sh.found_digit << shift[d];
-        mask = d == 0 ? 0xFFE00000u : (d == 1 ? 0xFFFFFC00u : 0xFFFFFFFFu);
+        prefix |= sh.found_digit << shift;
+        mask = 0xFFFFFFFFu << shift;
         want -= sh.found_above;
-        settled = sh.found_count == want;
+        if (sh.found_count == want)
+            break;                               // the same in every thread of the cluster
     }
     // rows with (key & mask) above `prefix` stay, and the first `want` rows that equal it
 
-    // ---- first walk: a warp's rows are contiguous, [w0, w1) of this CTA's, 128 at a time
-    const int per_warp = (n + kSelWarps * 128 - 1) / (kSelWarps * 128) * 128;
-    const int w0 = min(n, warp * per_warp), w1 = min(n, w0 + per_warp);
+    // ---- first walk: a warp's rows are contiguous, [w0, w1) of this CTA's; those before wm lie below the budget
+    const int per_warp = (n + kSelThreads - 1) / kSelThreads * 32;
+    const int w0 = min(n, warp * per_warp), w1 = min(n, w0 + per_warp), wm = min(w1, max(w0, a.budget - lo));
+    auto key_at = [&](int i) {
+        if (i < a.kept)
+            return keys[i] & mask;
+        const int blk1 = __ldg(bt + (lo + i) / kPage);
+        if (blk1 < 0 || blk1 >= a.num_blocks)
+            return weight_key(-CUDART_INF_F) & mask;
+        const long long at = ((long long)blk1 * a.hkv + h) * kPage + (lo + i) % kPage;
+        return key_of(a.acc[at], a.recent > 0 ? a.pos[at] : 0) & mask;
+    };
     Counts mine = {0, 0, 0, 0};
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-        const int i = i0 + 4 * lane;
-        const uint4 k = i < w1 ? keys4[i / 4] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t kk[4] = {k.x & mask, k.y & mask, k.z & mask, k.w & mask};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool live = i + e < w1, low = lo + i + e < a.budget;
-            const uint32_t gt = live && kk[e] > prefix, eq = live && kk[e] == prefix;
-            mine.above_low += low ? gt : 0u;
-            mine.above_high += low ? 0u : gt;
-            mine.ties_low += low ? eq : 0u;
-            mine.ties_high += low ? 0u : eq;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+        uint32_t gt = 0, eq = 0;
+#pragma unroll 4
+        for (int i = (part ? wm : w0) + lane; i < (part ? w1 : wm); i += 32) {
+            const uint32_t k = key_at(i);
+            gt += k > prefix;
+            eq += k == prefix;
         }
+        gt = warp_sum_u32(gt);
+        eq = warp_sum_u32(eq);
+        (part ? mine.above_high : mine.above_low) = gt;
+        (part ? mine.ties_high : mine.ties_low) = eq;
     }
-    mine.above_low = warp_sum_u32(mine.above_low);
-    mine.above_high = warp_sum_u32(mine.above_high);
-    mine.ties_low = warp_sum_u32(mine.ties_low);
-    mine.ties_high = warp_sum_u32(mine.ties_high);
     if (lane == 0)
         sh.warp[warp] = mine;
     __syncthreads();
     const Counts other = sh.warp[lane];          // kSelWarps == 32
-    if (warp == 0) {
-        const Counts all = {warp_sum_u32(other.above_low), warp_sum_u32(other.ties_low),
-                            warp_sum_u32(other.above_high), warp_sum_u32(other.ties_high)};
-        if (lane == 0)
-            sh.cta = all;
-    }
-    meet();
-    // ---- where this CTA's lists start: the CTAs before it, in row order
+    const Counts all = {warp_sum_u32(other.above_low), warp_sum_u32(other.ties_low), warp_sum_u32(other.above_high),
+                        warp_sum_u32(other.ties_high)};
     uint32_t tie0 = 0, hole0 = 0, tail0 = 0;
-    auto pass = [&](const Counts &c, int first_row, int rows) {
-        // of `rows` rows from first_row on, ties are taken in order while the threshold has room
-        const uint32_t low_rows = (uint32_t)max(0, min(rows, a.budget - first_row));
-        const uint32_t room = want > tie0 ? want - tie0 : 0u;
-        const uint32_t taken_low = min(room, c.ties_low), taken_high = min(room - taken_low, c.ties_high);
-        hole0 += low_rows - c.above_low - taken_low;
-        tail0 += c.above_high + taken_high;
-        tie0 += c.ties_low + c.ties_high;
-    };
-    for (int c = 0; c < crank; ++c)
-        pass(*cluster.map_shared_rank(&sh.cta, c), c * chunk, min(chunk, L - c * chunk));
-    if (crank == csize - 1 && tid == 0) {
-        const uint32_t before_tie = tie0, before_hole = hole0, before_tail = tail0;
-        pass(sh.cta, lo, n);
-        a.counts[pair] = (int32_t)tail0;
-        if (tail0 > (uint32_t)a.cap)
-            atomicOr(a.status, SK_DEV_INTERNAL);
-        tie0 = before_tie;
-        hole0 = before_hole;
-        tail0 = before_tail;
-    }
-    if (csize > 1)
+    if (csize > 1) {
+        // where this CTA's lists start: the CTAs before it, in row order
+        if (tid == 0)
+            sh.cta = all;
+        cluster.sync();
+        Counts c = {0, 0, 0, 0};
+        if (lane < csize)
+            c = *cluster.map_shared_rank(&sh.cta, lane);
         cluster.barrier_arrive();                // this CTA has read the others' shared memory
-    // and where this warp's do
-    for (int w = 0; w < warp; ++w)
-        pass(sh.warp[w], lo + min(n, w * per_warp), max(0, min(n, (w + 1) * per_warp) - min(n, w * per_warp)));
+        const int first = min(L, lane * chunk);
+        const Part part = part_of(c, first, lane < csize ? min(chunk, L - first) : 0, a.budget, want, 0, lane);
+        tie0 = __shfl_sync(kFull, part.ties_before, crank);
+        hole0 = warp_sum_u32(lane < crank ? part.holes : 0u);
+        tail0 = warp_sum_u32(lane < crank ? part.tails : 0u);
+    }
+    {
+        // and where this warp's do
+        const int first = min(n, lane * per_warp);
+        const Part part = part_of(other, lo + first, min(per_warp, n - first), a.budget, want, tie0, lane);
+        if (crank == csize - 1 && warp == 0) {
+            const uint32_t moves = tail0 + warp_sum_u32(part.tails);
+            if (lane == 0) {
+                a.counts[pair] = (int32_t)moves;
+                if (moves > (uint32_t)a.cap)
+                    atomicOr(a.status, SK_DEV_INTERNAL);
+            }
+        }
+        tie0 = __shfl_sync(kFull, part.ties_before, warp);
+        hole0 += warp_sum_u32(lane < warp ? part.holes : 0u);
+        tail0 += warp_sum_u32(lane < warp ? part.tails : 0u);
+    }
 
-    // ---- second walk: the lists
-    int32_t *src = a.src + (long long)pair * a.cap, *dst = a.dst + (long long)pair * a.cap;
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-        const int i = i0 + 4 * lane;
-        const uint4 k = i < w1 ? keys4[i / 4] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t kk[4] = {k.x & mask, k.y & mask, k.z & mask, k.w & mask};
-        uint32_t eqs = 0, stays = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            eqs |= (i + e < w1 && kk[e] == prefix) ? 1u << e : 0u;
-            stays |= (i + e < w1 && kk[e] > prefix) ? 1u << e : 0u;
-        }
-        if (__any_sync(kFull, eqs != 0)) {
-            uint32_t rank = __popc(eqs);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t u = __shfl_up_sync(kFull, rank, o);
-                rank += lane >= o ? u : 0u;
+    // ---- second walk: the lists, 32 rows at a time
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+        int32_t *list = (part ? a.src : a.dst) + (long long)pair * a.cap;
+        const int end = part ? w1 : wm;
+        uint32_t at = part ? tail0 : hole0;
+#pragma unroll 4
+        for (int i0 = part ? wm : w0; i0 < end; i0 += 32) {
+            const int i = i0 + lane;
+            const bool live = i < end;
+            const uint32_t k = live ? key_at(i) : 0u;
+            bool stays = k > prefix;
+            const uint32_t eq = __ballot_sync(kFull, live && k == prefix);
+            if (eq != 0) {
+                stays = stays || ((eq >> lane & 1u) && tie0 + __popc(eq & below) < want);
+                tie0 += __popc(eq);
             }
-            const uint32_t total = __shfl_sync(kFull, rank, 31);
-            rank += tie0 - __popc(eqs);
-            tie0 += total;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (eqs >> e & 1u) {
-                    stays |= rank < want ? 1u << e : 0u;
-                    ++rank;
-                }
-            }
-        }
-        uint32_t holes = 0, tails = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool low = lo + i + e < a.budget, live = i + e < w1, st = stays >> e & 1u;
-            holes |= live && low && !st ? 1u << e : 0u;
-            tails |= live && !low && st ? 1u << e : 0u;
-        }
-        uint32_t both = __popc(holes) | __popc(tails) << 16;
-        const uint32_t own = both;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(kFull, both, o);
-            both += lane >= o ? u : 0u;
-        }
-        const uint32_t total = __shfl_sync(kFull, both, 31);
-        both -= own;
-        uint32_t hp = hole0 + (both & 0xFFFFu), tp = tail0 + (both >> 16);
-        hole0 += total & 0xFFFFu;
-        tail0 += total >> 16;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if ((holes >> e & 1u) && hp++ < (uint32_t)a.cap)
-                dst[hp - 1] = lo + i + e;
-            if ((tails >> e & 1u) && tp++ < (uint32_t)a.cap)
-                src[tp - 1] = lo + i + e;
+            const uint32_t listed = __ballot_sync(kFull, live && stays == (part != 0));
+            const uint32_t to = at + __popc(listed & below);
+            if ((listed >> lane & 1u) && to < (uint32_t)a.cap)
+                list[to] = lo + i;
+            at += __popc(listed);
         }
     }
     if (csize > 1)
@@ -439,20 +449,24 @@ cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int3
                                 int budget, int recent, int max_len, int cap, int32_t *src, int32_t *dst,
                                 int32_t *counts, int32_t *new_lens, int *status, int num_sms, cudaStream_t stream)
 {
-    // The CTAs of a cluster hold all keys of the longest sequence in shared memory; with SMs to spare the cluster
-    // grows to 8 CTAs (above that a cluster needs a whole GPC), as long as each has 4096 rows.
+    // As many CTAs per cluster as there are SMs for, up to 8 (more need a whole GPC, which few clusters can have at a
+    // time), or as many as keep all rows in shared memory, up to 16; each has 4096 rows or more.  (32 clusters for up
+    // to 248k rows: 5 CTAs, which keep all rows but do not all run at once, 67 us; 4, which all run but read a sixth of
+    // their rows again in each pass, 91 us; 6 72 us, 8 86 us.)
     const int pairs = bs * hkv;
-    int c = (max_len + kEvictMaxChunk - 1) / kEvictMaxChunk;
-    c = c < 1 ? 1 : c;
-    int more = num_sms / pairs < (max_len + 4095) / 4096 ? num_sms / pairs : (max_len + 4095) / 4096;
-    more = more < 8 ? more : 8;
-    c = c > more ? c : more;
-    SelectArgs a{acc, pos, block_table, seq_lens, next_pos, src, dst, counts, new_lens, status,
-                 bt_stride, num_blocks, hkv, budget, recent, cap, max_len};
+    int c = num_sms / pairs;
+    c = c < 8 ? c : 8;
+    const int fit = (max_len + kEvictKept - 1) / kEvictKept;
+    c = c > fit ? c : fit;
+    c = c < 16 ? c : 16;
+    c = c < (max_len + 4095) / 4096 ? c : (max_len + 4095) / 4096;
+    c = c > 1 ? c : 1;
     const int chunk = ((max_len + c - 1) / c + 127) / 128 * 128;
-    const size_t smem = (size_t)chunk * 4;
+    SelectArgs a{acc, pos, block_table, seq_lens, next_pos, src, dst, counts, new_lens, status,
+                 bt_stride, num_blocks, hkv, budget, recent, cap, max_len, chunk < kEvictKept ? chunk : kEvictKept};
+    const size_t smem = (size_t)a.kept * 4;
     cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kEvictMaxChunk * 4);
+                                         kEvictKept * 4);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess)

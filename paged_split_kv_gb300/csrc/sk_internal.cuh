@@ -211,10 +211,6 @@ cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16
                               float factor, uint16_t *q_out, void *pages, int kv_dtype, float k_scale, float v_scale,
                               long long num_blocks, float *acc, int32_t *pos_pages, int *status, int num_sms,
                               cudaStream_t stream);
-// Eviction: one cluster of up to kEvictMaxCluster CTAs selects for a (sequence, head), each CTA keeping the
-// keys of up to kEvictMaxChunk rows in shared memory.
-constexpr int kEvictMaxCluster = 16;
-constexpr int kEvictMaxChunk = 49152;
 cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int32_t *block_table, int bt_stride,
                                 int num_blocks, const int32_t *seq_lens, const int32_t *next_pos, int bs, int hkv,
                                 int budget, int recent, int max_len, int cap, int32_t *src, int32_t *dst,

@@ -46,7 +46,7 @@ def test_evict_refusals(sk):
     for kw in (dict(bs=0), dict(bs=32768), dict(hkv=0), dict(nb=0), dict(stride=0), dict(budget=0), dict(recent=-1), dict(acc=ODD),
                dict(recent=33), dict(mx=-1), dict(acc=None), dict(nxt=None), dict(new=None)):
         assert call(**kw) == -1, kw
-    assert call(page=8) == -3 and call(mx=786433) == -3
+    assert call(page=8) == -3 and call(bs=32767, hkv=1 << 20) == -3
     assert call(cap=31) == -2 and call(mx=60, cap=27) == -2
     call = caller(sk.lib().sk_evict_move, dict(src=FAKE, dst=FAKE, cnt=FAKE, cap=4, bs=2, hkv=2, d=128, bt=FAKE,
                                                stride=10, nb=8, page=16, pg=FAKE, dt=0, acc=FAKE, pos=FAKE, st=None))

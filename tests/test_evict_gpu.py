@@ -111,14 +111,24 @@ def test_select_against_a_sort(lens, hkv, budget, recent, weights):
 
 
 @pytest.mark.parametrize("length,budget,recent", [(24577, 24576, 64), (60000, 8192, 512), (100001, 60000, 3),
-                                                  (248000, 1, 0), (400000, 1000, 999), (786432, 700000, 5000)])
+                                                  (248000, 1, 0), (400000, 1000, 999), (786432, 700000, 5000),
+                                                  (1000001, 300000, 7)])
 def test_select_over_clusters(length, budget, recent):
-    """Lengths around and past what one CTA holds, up to the longest that is taken."""
+    """Lengths around and past what one CTA, and a cluster, keeps in shared memory."""
     lens = [length, length // 3]
     bt, acc, pos, _ = cache(lens, 1, length, weights=coarse if length == 60000 else None)
     got = run_select(bt, acc, pos, lens, np.asarray(lens), 1, budget, recent)
     assert sk.sk_get_device_status() == 0
     check_select(got, reference(bt, acc, pos, lens, np.asarray(lens), 1, budget, recent), lens, 1, budget)
+
+
+def test_many_long_rows():
+    """More pairs than SMs for clusters: a CTA each, most of whose rows are past what it keeps."""
+    lens = [60001] * 19 + [150000]
+    bt, acc, pos, _ = cache(lens, 8, 5, weights=coarse)
+    got = run_select(bt, acc, pos, lens, np.asarray(lens), 8, 40000, 300)
+    assert sk.sk_get_device_status() == 0
+    check_select(got, reference(bt, acc, pos, lens, np.asarray(lens), 8, 40000, 300), lens, 8, 40000)
 
 
 def test_more_recent_rows_than_the_budget():
