@@ -117,6 +117,12 @@ __device__ __forceinline__ void split_q_row(uint2 raw, uint32_t &hi, uint32_t &l
     }
 }
 
+// mbar_wait_bounded with a test before the first suspending wait: a wait for what is complete costs less.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int *abort, long long limit)
+{
+    return sm100::mbar_test_wait(bar, parity) || sm100::mbar_wait_bounded(bar, parity, abort, limit);
+}
+
 // Gives registers of this warpgroup back / takes them, all its warps together.
 template <int N>
 __device__ __forceinline__ void reg_dec()

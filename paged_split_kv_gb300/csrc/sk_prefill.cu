@@ -6,21 +6,22 @@
 //
 // Bound by the tensor cores: 4 * 128 flops per (row, key) against 512 bytes of K and V per key that 256 rows
 // share.  One CTA takes 256 rows as two tiles A and B of 128 (the MMA's M) and streams the keys in tiles of
-// 128 (its N): while the softmax of one row tile runs, the products of the other fill the tensor pipe.  In
-// issue order, for key tile j:
-//     O_A += P_A(j) V(j);  S_A = Q_A K(j+1)^T;  O_B += P_B(j) V(j);  S_B = Q_B K(j+1)^T
-// S_A, S_B, O_A and O_B fill the 512 TMEM columns; P overwrites the first half of its S as bf16 (or as two e4m3
-// terms) and is the A operand of PV straight from TMEM, so probabilities never pass through shared memory.
+// 128 (its N): while the softmax of one row tile runs, the products of the other fill the tensor pipe.  For each row
+// tile x, in issue order over the key tiles j:
+//     O_x += P_x(j) V(j);  S_x = Q_x K(j+1)^T
+// S_A, S_B, O_A and O_B fill the 512 TMEM columns; P overwrites S, as bf16 (or as two e4m3 terms) in half the columns, and is the A operand of PV straight from TMEM, so probabilities never pass through shared memory.
 // A row is one TMEM lane and so one thread: the row's maximum and sum need no exchange between threads.
 //
 // Roles (384 threads):
 //   warp 0      copies: K and V of a key tile apart, 32 KB (16 KB e4m3) slots, one TMA copy per page and part, so
 //               the ring holds two and a half (five) key tiles beside Q
-//   warp 1      allocates TMEM, issues every product through one elected lane
+//   warps 1, 2  issue the products of A and of B, each through one elected lane (warp 1 also allocates TMEM); one issuer
+//               for both was the bottleneck: its waits, 200 cycles each even for what is complete, came one after the
+//               other (3300 cycles per key tile against 2048 of products)
 //   warps 4-7   Q tile A into shared memory; softmax of A, its rescaling, its output
 //   warps 8-11  the same for B
-// S(j) complete implies PV(j - 1) complete (products of a CTA complete in issue order), so the softmax may rescale O
-// at once; it does so only when a score beats the reference by 2^8 (2^4 for e4m3).
+// S(j) complete implies PV(j - 1) complete (products of one issuer complete in issue order), so the softmax may rescale O
+// at once; it does so only when a score beats the reference by far (2^40; 2^4 for e4m3).
 //
 // e4m3 pages: both products run as kind::f8f6f4 on the codes.  Q is two e4m3 terms with a power-of-two scale per row
 // (exact for bf16 elements within 2^-9 of the row's largest), as two products into one S; P is p * 2^4 = hi + lo
@@ -53,22 +54,22 @@ constexpr int kKeys = 128;                           // keys of one tile (MMA N)
 constexpr int kThreads = 384;
 constexpr long long kDrainLimit = 4000000000LL;      // cycles (~2 s): waits for work already issued
 constexpr int kMaxSmem = 232448;
+constexpr int kPShift = 4;                           // e4m3: P is formed as p * 2^kPShift ...
+constexpr float kThrLog2 = 4.0f;                     // ... which stays below 2^8
 // registers per thread after the reallocation: copies and products, softmax (3 x 168 at launch)
-constexpr int kRegsIssue = 72, kRegsSoftmax = 208;
+constexpr int kRegsIssue = 104, kRegsSoftmax = 200;
 
 template <bool FP8>
 struct PCfg {
     static constexpr int kQTile = kRows * 256;                     // bf16: two 64-dimension chunks; e4m3: hi and lo
     static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K (or V) of 8 tokens
     static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
-    static constexpr int kMisc = 3072;
+    static constexpr int kMisc = 3072;                             // barriers, then kCrow
     static constexpr int kSlots = (kMaxSmem - 2 * kQTile - kMisc) / kSlotBytes;
     static constexpr int kOffQ = kSlots * kSlotBytes;
     static constexpr int kOffMisc = kOffQ + 2 * kQTile;
     static constexpr int kSmemBytes = kOffMisc + kMisc;
     static constexpr int kPagesPerTile = kKeys / kPage;
-    static constexpr float kThrLog2 = FP8 ? 4.0f : 8.0f;
-    static constexpr int kPShift = FP8 ? 4 : 0;
     // misc area
     static constexpr int kBarFull = 0;
     static constexpr int kBarEmpty = 8 * kSlots;
@@ -76,8 +77,9 @@ struct PCfg {
     static constexpr int kBarS = kBarQ + 16;                       // [2] S complete
     static constexpr int kBarP = kBarS + 16;                       // [2] P written
     static constexpr int kBarO = kBarP + 16;                       // [2] last PV complete
-    static constexpr int kBarDrain = kBarO + 16;
-    static constexpr int kTmemSlot = kBarDrain + 8;
+    static constexpr int kBarTurn = kBarO + 16;                    // [2] the other issuer has issued its products
+    static constexpr int kBarDrain = kBarTurn + 16;                // [2]
+    static constexpr int kTmemSlot = kBarDrain + 16;
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kCrow = 512;                              // float[256]: score scale of each row (e4m3)
     static_assert(kAbort + 4 <= kCrow && kCrow + 1024 <= kMisc, "misc area");
@@ -143,20 +145,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
     auto bar_s = [&](int x) { return mbase + C::kBarS + 8 * x; };
     auto bar_p = [&](int x) { return mbase + C::kBarP + 8 * x; };
     auto bar_o = [&](int x) { return mbase + C::kBarO + 8 * x; };
-    const uint32_t bar_drain = mbase + C::kBarDrain;
+    auto bar_turn = [&](int x) { return mbase + C::kBarTurn + 8 * x; };
+    auto bar_drain = [&](int x) { return mbase + C::kBarDrain + 8 * x; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(bar_full(i), 1);
-            mbar_init(bar_empty(i), 1);
+            mbar_init(bar_empty(i), 2);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar_q(x), 4);
             mbar_init(bar_s(x), 1);
             mbar_init(bar_p(x), 4);
             mbar_init(bar_o(x), 1);
+            mbar_init(bar_turn(x), 1);
+            mbar_init(bar_drain(x), 1);
         }
-        mbar_init(bar_drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -188,7 +192,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             for (int u = 0; u < 2 * n && ok; ++u) {
                 const int j = u >> 1, part = u & 1, i = u % C::kSlots;
                 if (u >= C::kSlots)
-                    ok = mbar_wait_bounded(bar_empty(i), (u / C::kSlots - 1) & 1, abort_flag, p.wait_limit);
+                    ok = wait_bar(bar_empty(i), (u / C::kSlots - 1) & 1, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 if (!ok)
                     break;
@@ -220,99 +224,91 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             // every copy issued lands before the CTA exits
             for (int u = issued > C::kSlots ? issued - C::kSlots : 0; u < issued; ++u)
                 mbar_wait_bounded(bar_full(u % C::kSlots), (u / C::kSlots) & 1, nullptr, kDrainLimit);
-        } else if (warp == 1) {
-            // ============================================================ products
+        } else if (warp <= 2) {
+            // ============================================================ products of row tile x
             constexpr uint32_t idesc_qk = FP8 ? idesc_e4m3_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
             constexpr uint32_t idesc_pv = FP8 ? idesc_e4m3_f32(kRows, kHeadDim, 0, 1)
                                               : idesc_bf16_f32(kRows, kHeadDim, 0, 1);
+            const int x = warp - 1;
+            const int nx = x ? nB : nA;
             const uint64_t d_k0 = smem_desc_sw128(sbase, 16, C::kGroupBytes);       // K-major K
             const uint64_t d_v0 = smem_desc_sw128(sbase, 1024, C::kGroupBytes);     // dimension-major V
-            const uint64_t d_q0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);      // K-major Q
+            const uint64_t d_q = smem_desc_sw128(sbase + C::kOffQ + x * C::kQTile, 16, 1024);   // K-major Q
+            const uint32_t sd = tmem + kColS + x * 128, od = tmem + kColO + x * 128;
             auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
             bool ok = true;
-            int issued = 0;
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 if (ok)
-                    ok = mbar_wait_bounded(bar, parity, abort_flag, p.wait_limit);
+                    ok = wait_bar(bar, parity, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
-                if (ok)
-                    tc_fence_after();
                 return ok;
             };
             auto wait_slot = [&](int u) { return wait(bar_full(u % C::kSlots), (u / C::kSlots) & 1); };
-            auto qk = [&](int x, int j) {
-                const uint32_t so = (uint32_t)(2 * j % C::kSlots) * C::kSlotBytes, qo = x * C::kQTile;
-                const uint32_t sd = tmem + kColS + x * 128;
-                if constexpr (FP8) {
+            // passes the turn with half of the products still to issue: the other issuer wakes up meanwhile
+            auto pass_turn = [&]() {
+                if (lane == 0)
+                    mbar_arrive(bar_turn(1 - x));
+                __syncwarp();
+            };
+            auto qk = [&](int j) {
+                const uint32_t so = (uint32_t)(2 * j % C::kSlots) * C::kSlotBytes;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f8_ss_warp(sd, adv(d_q0, qo + t * (kRows * 128) + k * 32), adv(d_k0, so + k * 32),
-                                           idesc_qk, (t > 0 || k > 0) ? 1u : 0u);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_f16_ss_warp(sd, adv(d_q0, qo + (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (FP8)
+                        mma_f8_ss_warp(sd, adv(d_q, (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                                       adv(d_k0, so + (k & 3) * 32), idesc_qk, k > 0 ? 1u : 0u);
+                    else
+                        mma_f16_ss_warp(sd, adv(d_q, (k >> 2) * (kRows * 128) + (k & 3) * 32),
                                         adv(d_k0, so + (k >> 2) * 1024 + (k & 3) * 32), idesc_qk, k > 0 ? 1u : 0u);
+                    if (k == 3 && j > 0)
+                        pass_turn();
                 }
                 mma_commit_warp(bar_s(x));
-                issued = 1;
             };
-            auto pv = [&](int x, int j) {
+            auto pv = [&](int j) {
                 const uint32_t so = (uint32_t)((2 * j + 1) % C::kSlots) * C::kSlotBytes;
-                const uint32_t od = tmem + kColO + x * 128, pa = tmem + kColS + x * 128;
-                if constexpr (FP8) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f8_ts_warp(od, pa + t * 32 + k * 8, adv(d_v0, so + k * 4 * C::kGroupBytes), idesc_pv,
-                                           (j > 0 || t > 0 || k > 0) ? 1u : 0u);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_f16_ts_warp(od, pa + k * 8, adv(d_v0, so + k * 2 * C::kGroupBytes), idesc_pv,
-                                        (j > 0 || k > 0) ? 1u : 0u);
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (FP8)                             // hi and lo terms of four groups of 32 keys
+                        mma_f8_ts_warp(od, sd + (k >> 2) * 64 + (k & 1) * 16 + (k >> 1 & 1) * 8,
+                                       adv(d_v0, so + (k >> 1) * 4 * C::kGroupBytes), idesc_pv,
+                                       (j > 0 || k > 0) ? 1u : 0u);
+                    else
+                        mma_f16_ts_warp(od, sd + (k >> 2) * 64 + (k & 3) * 8, adv(d_v0, so + k * 2 * C::kGroupBytes),
+                                        idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
                 }
             };
-            if (n > 0) {
-                if (nA > 0)
-                    wait(bar_q(0), 0);
-                if (nB > 0)
-                    wait(bar_q(1), 0);
-                if (wait_slot(0)) {
-                    if (nA > 0)
-                        qk(0, 0);
-                    if (nB > 0)
-                        qk(1, 0);
-                    mma_commit_warp(bar_empty(0));
-                }
+            // Both issuers pass every slot on, also those of tiles that only the other multiplies (they wait for them
+            // all the same, so that neither is a turn of the ring ahead).
+            if (n > 0 && (nx == 0 || wait(bar_q(x), 0)) && wait_slot(0)) {
+                tc_fence_after();
+                if (nx > 0)
+                    qk(0);
+                mma_commit_warp(bar_empty(0));
             }
             for (int j = 0; j < n && ok; ++j) {
-                if (!wait_slot(2 * j + 1))
+                // what has to have landed is checked while the softmax still works on the tile
+                if (!wait_slot(2 * j + 1) || (j + 1 < n && !wait_slot(2 * j + 2)))
                     break;
-                // a slot is free once the last product that reads it is: B's where B has the tile
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int nx = x ? nB : nA;
-                    if (!ok || j >= nx)
-                        continue;
+                if (j < nx) {
+                    // the row tiles take turns, so that one's softmax runs beside the other's products
+                    if (x == 0 ? (j > 0 && j - 1 < nB && !wait(bar_turn(0), (j - 1) & 1))
+                               : (j < nA && !wait(bar_turn(1), j & 1)))
+                        break;
                     if (!wait(bar_p(x), j & 1))
-                        continue;
-                    pv(x, j);
-                    if (j + 1 == nx)
-                        mma_commit_warp(bar_o(x));
-                    if (x == 1 || j >= nB)
-                        mma_commit_warp(bar_empty((2 * j + 1) % C::kSlots));
+                        break;
+                    tc_fence_after();
+                    pv(j);
                     if (j + 1 < nx) {
-                        if (!wait_slot(2 * j + 2))
-                            continue;
-                        qk(x, j + 1);
-                        if (x == 1 || j + 1 >= nB)
-                            mma_commit_warp(bar_empty((2 * j + 2) % C::kSlots));
+                        qk(j + 1);
+                    } else {
+                        mma_commit_warp(bar_o(x));
+                        pass_turn();
                     }
                 }
+                mma_commit_warp(bar_empty((2 * j + 1) % C::kSlots));
+                if (j + 1 < n)
+                    mma_commit_warp(bar_empty((2 * j + 2) % C::kSlots));
             }
             if (!ok) {
                 *abort_flag = 1;
@@ -320,10 +316,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                     atomicOr(p.status, SK_DEV_TIMEOUT);
             }
             // every product completes before TMEM is freed and shared memory is left
-            if (issued) {
-                mma_commit_warp(bar_drain);
-                mbar_wait_bounded(bar_drain, 0, nullptr, kDrainLimit);
-            }
+            mma_commit_warp(bar_drain(x));
+            mbar_wait_bounded(bar_drain(x), 0, nullptr, kDrainLimit);
         }
         __syncwarp();
     } else {
@@ -343,51 +337,46 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
         uint8_t *qs = smem + C::kOffQ + x * C::kQTile;
         if (nx > 0) {
             if constexpr (!FP8) {
+                uint4 v[16];
 #pragma unroll
-                for (int k0 = 0; k0 < 16; k0 += 8) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = quarter * 32 + (k0 + k) * 2 + (lane >> 4), unit = lane & 15;
-                        v[k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < rows) {
-                            const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
-                            v[k] = __ldg(reinterpret_cast<const uint4 *>(
-                                p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + unit * 8));
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = quarter * 32 + (k0 + k) * 2 + (lane >> 4), unit = lane & 15;
-                        *reinterpret_cast<uint4 *>(qs + (unit >> 3) * (kRows * 128) + r * 128 +
-                                                   (((unit & 7) ^ (r & 7)) << 4)) = v[k];
+                for (int k = 0; k < 16; ++k) {
+                    const int r = quarter * 32 + k * 2 + (lane >> 4), unit = lane & 15;
+                    v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows) {
+                        const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
+                        v[k] = __ldg(reinterpret_cast<const uint4 *>(
+                            p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + unit * 8));
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int r = quarter * 32 + k * 2 + (lane >> 4), unit = lane & 15;
+                    *reinterpret_cast<uint4 *>(qs + (unit >> 3) * (kRows * 128) + r * 128 +
+                                               (((unit & 7) ^ (r & 7)) << 4)) = v[k];
+                }
             } else {
-                for (int k0 = 0; k0 < 32; k0 += 8) {
-                    uint2 raw[8];
+                uint2 raw[32];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = quarter * 32 + k0 + k;
-                        raw[k] = make_uint2(0u, 0u);
-                        if (r < rows) {
-                            const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
-                            raw[k] = __ldg(reinterpret_cast<const uint2 *>(
-                                p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + lane * 4));
-                        }
+                for (int k = 0; k < 32; ++k) {
+                    const int r = quarter * 32 + k;
+                    raw[k] = make_uint2(0u, 0u);
+                    if (r < rows) {
+                        const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
+                        raw[k] = __ldg(reinterpret_cast<const uint2 *>(
+                            p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + lane * 4));
                     }
+                }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = quarter * 32 + k0 + k;
-                        uint32_t hi, lo;
-                        int e;
-                        split_q_row(raw[k], hi, lo, e);
-                        const uint32_t off = (uint32_t)(r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
-                        *reinterpret_cast<uint32_t *>(qs + off) = hi;
-                        *reinterpret_cast<uint32_t *>(qs + kRows * 128 + off) = lo;
-                        if (lane == 0)
-                            crow[r] = p.score_scale_log2 * ldexpf(1.f, -e);
-                    }
+                for (int k = 0; k < 32; ++k) {
+                    const int r = quarter * 32 + k;
+                    uint32_t hi, lo;
+                    int e;
+                    split_q_row(raw[k], hi, lo, e);
+                    const uint32_t off = (uint32_t)(r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
+                    *reinterpret_cast<uint32_t *>(qs + off) = hi;
+                    *reinterpret_cast<uint32_t *>(qs + kRows * 128 + off) = lo;
+                    if (lane == 0)
+                        crow[r] = p.score_scale_log2 * ldexpf(1.f, -e);
                 }
             }
             fence_proxy_async_smem();
@@ -401,12 +390,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
         const int jq = r / p.G, iq = r - jq * p.G;
         const bool live = tau < rows;
         const int limit = live ? visible_keys(L, q_len, jq, p.causal) : 0;
-        float m_ref = -CUDART_INF_F, m_thr = -CUDART_INF_F;
+        const int least = __reduce_min_sync(kFull, limit);         // keys that every row of the warp sees
+        float m_ref = -CUDART_INF_F;
+        bool anchored = false;                                     // every row that sees a key has a reference
         float2 l2 = make_float2(0.f, 0.f);
         bool failed = false;
         for (int j = 0; j < nx; ++j) {
             const int key0 = (t0 + j) * kKeys;
-            bool ok = mbar_wait_bounded(bar_s(x), j & 1, abort_flag, p.wait_limit);
+            bool ok = wait_bar(bar_s(x), j & 1, abort_flag, p.wait_limit);
             ok = __all_sync(kFull, ok);
             if (!ok) {
                 failed = true;
@@ -419,31 +410,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                 tmem_ld32<32>(ts + cc, v + cc);
             tmem_wait_ld();
             const int lim = limit - key0;                          // columns [0, lim) are visible
-            if (!__all_sync(kFull, lim >= kKeys)) {
+            if (key0 + kKeys > least) {                            // uniform in the warp
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     v[i] = i < lim ? v[i] : -CUDART_INF_F;
             }
-            float mx[4] = {v[0], v[1], v[2], v[3]};
+            // the tile's largest score, in log2 units
+            auto tile_top = [&]() {
+                float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-            for (int i = 4; i < 124; i += 8) {
+                for (int i = 4; i < 124; i += 8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx[k] = fmax3(mx[k], v[i + k], v[i + 4 + k]);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mx[k] = fmax3(mx[k], v[i + k], v[i + 4 + k]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mx[k] = fmaxf(mx[k], v[124 + k]);
-            const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c;
-            if (__any_sync(kFull, top > m_thr)) {
+                    mx[k] = fmaxf(mx[k], v[124 + k]);
+                return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c;
+            };
+            // moves the rows' reference up to `top` and rescales what they have summed; `in_o`: O holds something
+            auto raise = [&](float top, bool in_o) {
                 const float mn = fmaxf(m_ref, top);
                 const float alpha = m_ref == -CUDART_INF_F ? 0.f : exp2f(m_ref - mn);
                 m_ref = mn;
-                m_thr = mn + C::kThrLog2;
                 l2.x *= alpha;
                 l2.y *= alpha;
-                if (j > 0) {
-#pragma unroll
+                if (in_o) {
+#pragma unroll 1
                     for (int cc = 0; cc < 128; cc += 32) {
                         float o[32];
                         tmem_ld32<32>(to + cc, o);
@@ -454,39 +448,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                         tmem_st32<32>(to + cc, o);
                     }
                 }
-            }
-            const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref - (float)C::kPShift;
-            const float2 c2 = make_float2(c, c), s2 = make_float2(-msub, -msub);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int k = hf * 64 + 2 * i;
-                    const float2 d = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
-                    const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
-                    l2 = fadd2(l2, e);
-                    pk[i] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
-                }
-                if constexpr (FP8) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t a = pk[2 * i], bb = pk[2 * i + 1];
-                        const uint32_t ah = a & 0xFF80FF80u, bh = bb & 0xFF80FF80u;     // 3 fraction bits
-                        hi[i] = e4m3x4_from_f16x2(ah, bh);
-                        lo[i] = e4m3x4_from_f16x2(hsub2(a, ah), hsub2(bb, bh));
-                    }
-                    tmem_st32_u<16>(ts + hf * 16, hi);
-                    tmem_st32_u<16>(ts + 32 + hf * 16, lo);
-                } else {
-                    tmem_st32_u<32>(ts + hf * 32, pk);
+            };
+            if constexpr (FP8) {
+                const float top = tile_top();
+                if (__any_sync(kFull, top > m_ref + kThrLog2 || (m_ref == -CUDART_INF_F && top > m_ref)))
+                    raise(top, j > 0);
+            } else {
+                // only a row's first scores need their maximum before they are exponentiated (see below)
+                if (!anchored) {
+                    if (__any_sync(kFull, m_ref == -CUDART_INF_F && lim > 0))
+                        raise(tile_top(), j > 0);
+                    anchored = !__any_sync(kFull, m_ref == -CUDART_INF_F && limit > 0);
                 }
             }
-            tmem_wait_st();
             // rows past the sequence's end in its last page hold anything, and 0 * NaN would reach O: their V
-            // becomes zeros, by the first row tile that multiplies it
-            if ((x == 0 || j >= nA) && L < key0 + kKeys && (L & (kPage - 1)) != 0) {
+            // becomes zeros, before either row tile multiplies it
+            if (L < key0 + kKeys && (L & (kPage - 1)) != 0) {
                 ok = mbar_wait_bounded(bar_full((2 * j + 1) % C::kSlots), ((2 * j + 1) / C::kSlots) & 1, abort_flag,
                                        p.wait_limit);
                 ok = __all_sync(kFull, ok);
@@ -501,11 +478,67 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                             *reinterpret_cast<uint4 *>(row + cc * 1024 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
-                if (!ok) {
-                    failed = true;
-                    break;
-                }
+                if (!ok)
+                    *abort_flag = 1;                               // the other roles' waits end with it
             }
+            // P overwrites the first columns of each half of S
+            const float2 c2 = make_float2(c, c);
+            if constexpr (FP8) {
+                const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref - (float)kPShift;
+                const float2 s2 = make_float2(-msub, -msub);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int k = q * 32 + 4 * i;
+                        const float2 d0 = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
+                        const float2 d1 = ffma2(make_float2(v[k + 2], v[k + 3]), c2, s2);
+                        const float2 e0 = make_float2(ex2_ftz(d0.x), ex2_ftz(d0.y));
+                        const float2 e1 = make_float2(ex2_ftz(d1.x), ex2_ftz(d1.y));
+                        l2 = fadd2(fadd2(l2, e0), e1);
+                        const uint32_t a = pack_f16x2(e0.x, e0.y), bb = pack_f16x2(e1.x, e1.y);
+                        const uint32_t ah = a & 0xFF80FF80u, bh = bb & 0xFF80FF80u;     // 3 fraction bits
+                        hi[i] = e4m3x4_from_f16x2(ah, bh);
+                        lo[i] = e4m3x4_from_f16x2(hsub2(a, ah), hsub2(bb, bh));
+                    }
+                    tmem_st32_u<8>(ts + (q >> 1) * 64 + (q & 1) * 8, hi);
+                    tmem_st32_u<8>(ts + (q >> 1) * 64 + 16 + (q & 1) * 8, lo);
+                }
+            } else {
+                // Probabilities keep bf16's relative precision at any size, so a row's reference need not follow its
+                // maximum: 2^40 times what the reference stands for is as good, and the tile's sum shows whether some
+                // probability passed that.  Only then is the maximum taken, the reference raised, O rescaled and
+                // the tile done again.
+                float2 h2;
+#pragma unroll 1
+                for (int again = 0; again < 2; ++again) {
+                    const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+                    const float2 s2 = make_float2(-msub, -msub);
+                    h2 = make_float2(0.f, 0.f);
+                    float2 g2 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int k = q * 32 + 2 * i;
+                            const float2 d = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
+                            const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
+                            (i & 1 ? g2 : h2) = fadd2(i & 1 ? g2 : h2, e);
+                            pk[i] = pack_bf16x2(e.x, e.y);
+                        }
+                        tmem_st32_u<16>(ts + (q >> 1) * 64 + (q & 1) * 16, pk);
+                    }
+                    h2 = fadd2(h2, g2);
+                    if (again || !__any_sync(kFull, !(h2.x + h2.y <= 0x1p40f)))
+                        break;
+                    tmem_wait_st();
+                    raise(tile_top(), j > 0);
+                }
+                l2 = fadd2(l2, h2);
+            }
+            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
