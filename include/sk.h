@@ -267,8 +267,8 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
  * nsplit > 1 the partial states go through part_o, part_m and part_l (fp32 [num_tokens, nsplit, num_q_heads
  * (, 128)], as in sk_paged_decode_attn) and the call ends with the merge; then rows past cu_seqlens_q[bs] are
  * undefined.  With nsplit == 1 the three may be NULL.  sk_prefill_nsplit gives a good number.
- * q, kv_pages, out and part_o are 16-byte aligned; lse may be NULL.  bf16 pages round the probabilities to
- * bf16, e4m3fn pages to two e4m3 terms (within 2^-8); sums are fp32.
+ * q, kv_pages, out and part_o are 16-byte aligned; lse may be NULL.  Probabilities round to bf16 (f16
+ * for e4m3fn pages); sums are fp32.
  * Returns SK_OK or a negative sk_status. */
 int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
                           const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,

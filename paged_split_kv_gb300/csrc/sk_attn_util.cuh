@@ -63,23 +63,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b)
+// The e4m3 pair in the low 16 bits as a packed f16 pair (exact).
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t v)
 {
     uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// Two packed f16 pairs to four e4m3 codes, nearest even, saturated to +-448.
-__device__ __forceinline__ uint32_t e4m3x4_from_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 lo, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 hi, %2;\n\t"
-        "mov.b32 %0, {lo, hi};\n\t}"
-        : "=r"(r)
-        : "r"(a), "r"(b));
+    const uint16_t h = (uint16_t)(v & 0xFFFFu);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
     return r;
 }
 
@@ -105,8 +94,7 @@ __device__ __forceinline__ void split_q_row(uint2 raw, uint32_t &hi, uint32_t &l
         const float x0 = ldexpf(q[k], e), x1 = ldexpf(q[k + 1], e);
         uint16_t hc, lc;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hc) : "f"(x1), "f"(x0));
-        uint32_t hf;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hf) : "h"(hc));
+        const uint32_t hf = f16x2_of_e4m3(hc);
         float h0, h1;
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
             : "=f"(h0), "=f"(h1)
@@ -156,18 +144,6 @@ __device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem
         "setp.ne.b32 p, %4, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_f8_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }

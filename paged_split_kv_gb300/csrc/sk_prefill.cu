@@ -9,7 +9,9 @@
 // 128 (its N): while the softmax of one row tile runs, the products of the other fill the tensor pipe.  For each row
 // tile x, in issue order over the key tiles j:
 //     O_x += P_x(j) V(j);  S_x = Q_x K(j+1)^T
-// S_A, S_B, O_A and O_B fill the 512 TMEM columns; P overwrites S, as bf16 (or as two e4m3 terms) in half the columns, and is the A operand of PV straight from TMEM, so probabilities never pass through shared memory.
+// S_A, S_B, O_A and O_B fill the 512 TMEM columns; P overwrites
+// S in half its columns, as bf16 (f16 for e4m3 pages), and is the A operand of PV straight from TMEM, so that
+// probabilities never pass through shared memory.
 // A row is one TMEM lane and so one thread: the row's maximum and sum need no exchange between threads.
 //
 // Roles (384 threads):
@@ -21,11 +23,13 @@
 //   warps 4-7   Q tile A into shared memory; softmax of A, its rescaling, its output
 //   warps 8-11  the same for B
 // S(j) complete implies PV(j - 1) complete (products of one issuer complete in issue order), so the softmax may rescale O
-// at once; it does so only when a score beats the reference by far (2^40; 2^4 for e4m3).
+// at once; it does so only when scores beat the reference by far.
 //
-// e4m3 pages: both products run as kind::f8f6f4 on the codes.  Q is two e4m3 terms with a power-of-two scale per row
-// (exact for bf16 elements within 2^-9 of the row's largest), as two products into one S; P is p * 2^4 = hi + lo
-// (within 2^-8), as two products into one O.
+// e4m3 pages: QK runs as kind::f8f6f4 on the codes, with Q as two e4m3 terms and a power-of-two scale per row (exact for
+// bf16 elements within 2^-9 of the row's largest), as two products into one S.  V's codes become f16 (exactly) in
+// shared memory, by four more warps (12-15), and PV runs on f16.  (P as two e4m3 terms with V's codes as they are
+// needs no conversion, but costs the softmax two more instructions per score: 263 against TODO us on 4 chunks of up to
+// 1024 tokens over 16k keys.)
 //
 // Few row tiles on a long axis: the keys of every row tile are split over `nsplit` CTAs that write partial
 // softmax states, joined by the library's merge.
@@ -51,25 +55,30 @@ using namespace sm100;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRows = 128;                           // rows of one tile (MMA M)
 constexpr int kKeys = 128;                           // keys of one tile (MMA N)
-constexpr int kThreads = 384;
 constexpr long long kDrainLimit = 4000000000LL;      // cycles (~2 s): waits for work already issued
 constexpr int kMaxSmem = 232448;
-constexpr int kPShift = 4;                           // e4m3: P is formed as p * 2^kPShift ...
-constexpr float kThrLog2 = 4.0f;                     // ... which stays below 2^8
-// registers per thread after the reallocation: copies and products, softmax (3 x 168 at launch)
-constexpr int kRegsIssue = 104, kRegsSoftmax = 200;
-
 template <bool FP8>
 struct PCfg {
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    // registers per thread after the reallocation: copies and products, softmax, e4m3's conversion of V; no more in all
+    // than at launch (4 x 128, or 3 x 168)
+    static constexpr int kRegsLaunch = FP8 ? 128 : 168;
+    static constexpr int kRegsIssue = FP8 ? 80 : 104, kRegsSoftmax = FP8 ? 192 : 200, kRegsConvert = 48;
+    static_assert(kRegsIssue + 2 * kRegsSoftmax + (FP8 ? kRegsConvert : 0) <= kThreads / 128 * kRegsLaunch, "registers");
     static constexpr int kQTile = kRows * 256;                     // bf16: two 64-dimension chunks; e4m3: hi and lo
-    static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K (or V) of 8 tokens
+    static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K (or V) of 8 tokens, as copied
     static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
+    static constexpr int kVBytes = FP8 ? kKeys * 256 : 0;          // e4m3: V of a tile as f16, two of them
     static constexpr int kMisc = 3072;                             // barriers, then kCrow
-    static constexpr int kSlots = (kMaxSmem - 2 * kQTile - kMisc) / kSlotBytes;
-    static constexpr int kOffQ = kSlots * kSlotBytes;
+    static constexpr int kSlots = (kMaxSmem - 2 * kQTile - 2 * kVBytes - kMisc) / kSlotBytes;
+    static constexpr int kOffV = kSlots * kSlotBytes;
+    static constexpr int kOffQ = kOffV + 2 * kVBytes;
     static constexpr int kOffMisc = kOffQ + 2 * kQTile;
     static constexpr int kSmemBytes = kOffMisc + kMisc;
     static constexpr int kPagesPerTile = kKeys / kPage;
+    // The sum of a tile's probabilities (relative to the reference) up to which they are as good as with the maximum
+    // for reference: bf16 keeps its precision at any size, f16 ends at 2^16.
+    static constexpr float kSumMost = FP8 ? 0x1p15f : 0x1p40f;
     // misc area
     static constexpr int kBarFull = 0;
     static constexpr int kBarEmpty = 8 * kSlots;
@@ -78,19 +87,21 @@ struct PCfg {
     static constexpr int kBarP = kBarS + 16;                       // [2] P written
     static constexpr int kBarO = kBarP + 16;                       // [2] last PV complete
     static constexpr int kBarTurn = kBarO + 16;                    // [2] the other issuer has issued its products
-    static constexpr int kBarDrain = kBarTurn + 16;                // [2]
+    static constexpr int kBarVFull = kBarTurn + 16;                // [2] e4m3: V of a tile as f16
+    static constexpr int kBarVEmpty = kBarVFull + 16;              // [2]
+    static constexpr int kBarDrain = kBarVEmpty + 16;              // [2]
     static constexpr int kTmemSlot = kBarDrain + 16;
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kCrow = 512;                              // float[256]: score scale of each row (e4m3)
     static_assert(kAbort + 4 <= kCrow && kCrow + 1024 <= kMisc, "misc area");
-    static_assert(kSlots >= 3 && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0, "shared memory");
+    static_assert(kSlots >= 3 && (!FP8 || kSlots % 2 == 0) && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0, "shared memory");
 };
 
 // TMEM map (columns)
 constexpr int kColS = 0, kColO = 256;                // S_A, S_B, then O_A, O_B, 128 each
 
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PCfg<FP8>::kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p)
 {
     using C = PCfg<FP8>;
@@ -145,13 +156,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
     auto bar_s = [&](int x) { return mbase + C::kBarS + 8 * x; };
     auto bar_p = [&](int x) { return mbase + C::kBarP + 8 * x; };
     auto bar_o = [&](int x) { return mbase + C::kBarO + 8 * x; };
+    auto bar_vfull = [&](int i) { return mbase + C::kBarVFull + 8 * i; };
+    auto bar_vempty = [&](int i) { return mbase + C::kBarVEmpty + 8 * i; };
     auto bar_turn = [&](int x) { return mbase + C::kBarTurn + 8 * x; };
     auto bar_drain = [&](int x) { return mbase + C::kBarDrain + 8 * x; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(bar_full(i), 1);
-            mbar_init(bar_empty(i), 2);
+            mbar_init(bar_empty(i), FP8 && (i & 1) ? 4 : 2);       // both issuers; e4m3's V: the converting warps
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar_q(x), 4);
@@ -159,6 +172,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             mbar_init(bar_p(x), 4);
             mbar_init(bar_o(x), 1);
             mbar_init(bar_turn(x), 1);
+            mbar_init(bar_vfull(x), 4);
+            mbar_init(bar_vempty(x), 2);
             mbar_init(bar_drain(x), 1);
         }
         *abort_flag = 0;
@@ -174,7 +189,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc + C::kTmemSlot);
 
     if (warp < 4) {
-        reg_dec<kRegsIssue>();
+        reg_dec<C::kRegsIssue>();
         if (warp == 0) {
             // ============================================================ copies
             // slot i holds, in turn, K(0), V(0), K(1), V(1), ...
@@ -227,12 +242,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
         } else if (warp <= 2) {
             // ============================================================ products of row tile x
             constexpr uint32_t idesc_qk = FP8 ? idesc_e4m3_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
-            constexpr uint32_t idesc_pv = FP8 ? idesc_e4m3_f32(kRows, kHeadDim, 0, 1)
+            constexpr uint32_t idesc_pv = FP8 ? idesc_f16_f32(kRows, kHeadDim, 0, 1)
                                               : idesc_bf16_f32(kRows, kHeadDim, 0, 1);
             const int x = warp - 1;
             const int nx = x ? nB : nA;
             const uint64_t d_k0 = smem_desc_sw128(sbase, 16, C::kGroupBytes);       // K-major K
-            const uint64_t d_v0 = smem_desc_sw128(sbase, 1024, C::kGroupBytes);     // dimension-major V
+            const uint64_t d_v0 = smem_desc_sw128(sbase + (FP8 ? C::kOffV : 0), 1024, 2048);    // dimension-major V
             const uint64_t d_q = smem_desc_sw128(sbase + C::kOffQ + x * C::kQTile, 16, 1024);   // K-major Q
             const uint32_t sd = tmem + kColS + x * 128, od = tmem + kColO + x * 128;
             auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
@@ -266,18 +281,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                 mma_commit_warp(bar_s(x));
             };
             auto pv = [&](int j) {
-                const uint32_t so = (uint32_t)((2 * j + 1) % C::kSlots) * C::kSlotBytes;
+                const uint32_t so = FP8 ? (uint32_t)(j & 1) * C::kVBytes : (uint32_t)((2 * j + 1) % C::kSlots) * C::kSlotBytes;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if constexpr (FP8)                             // hi and lo terms of four groups of 32 keys
-                        mma_f8_ts_warp(od, sd + (k >> 2) * 64 + (k & 1) * 16 + (k >> 1 & 1) * 8,
-                                       adv(d_v0, so + (k >> 1) * 4 * C::kGroupBytes), idesc_pv,
-                                       (j > 0 || k > 0) ? 1u : 0u);
-                    else
-                        mma_f16_ts_warp(od, sd + (k >> 2) * 64 + (k & 3) * 8, adv(d_v0, so + k * 2 * C::kGroupBytes),
-                                        idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
-                }
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ts_warp(od, sd + (k >> 2) * 64 + (k & 3) * 8, adv(d_v0, so + k * 4096), idesc_pv,
+                                    (j > 0 || k > 0) ? 1u : 0u);
             };
+            auto wait_v = [&](int j) { return FP8 ? wait(bar_vfull(j & 1), (j >> 1) & 1) : wait_slot(2 * j + 1); };
             // Both issuers pass every slot on, also those of tiles that only the other multiplies (they wait for them
             // all the same, so that neither is a turn of the ring ahead).
             if (n > 0 && (nx == 0 || wait(bar_q(x), 0)) && wait_slot(0)) {
@@ -288,7 +298,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             }
             for (int j = 0; j < n && ok; ++j) {
                 // what has to have landed is checked while the softmax still works on the tile
-                if (!wait_slot(2 * j + 1) || (j + 1 < n && !wait_slot(2 * j + 2)))
+                if (!wait_v(j) || (j + 1 < n && !wait_slot(2 * j + 2)))
                     break;
                 if (j < nx) {
                     // the row tiles take turns, so that one's softmax runs beside the other's products
@@ -306,7 +316,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                         pass_turn();
                     }
                 }
-                mma_commit_warp(bar_empty((2 * j + 1) % C::kSlots));
+                mma_commit_warp(FP8 ? bar_vempty(j & 1) : bar_empty((2 * j + 1) % C::kSlots));
                 if (j + 1 < n)
                     mma_commit_warp(bar_empty((2 * j + 2) % C::kSlots));
             }
@@ -320,9 +330,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             mbar_wait_bounded(bar_drain(x), 0, nullptr, kDrainLimit);
         }
         __syncwarp();
-    } else {
+    } else if (!FP8 || warp < 12) {
         // ================================================================ softmax of row tile x
-        reg_inc<kRegsSoftmax>();
+        reg_inc<C::kRegsSoftmax>();
         const int x = (warp >> 2) - 1;
         const int quarter = warp & 3;
         const int tau = quarter * 32 + lane;                       // row of the tile, TMEM lane
@@ -449,21 +459,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                     }
                 }
             };
-            if constexpr (FP8) {
-                const float top = tile_top();
-                if (__any_sync(kFull, top > m_ref + kThrLog2 || (m_ref == -CUDART_INF_F && top > m_ref)))
-                    raise(top, j > 0);
-            } else {
-                // only a row's first scores need their maximum before they are exponentiated (see below)
-                if (!anchored) {
-                    if (__any_sync(kFull, m_ref == -CUDART_INF_F && lim > 0))
-                        raise(tile_top(), j > 0);
-                    anchored = !__any_sync(kFull, m_ref == -CUDART_INF_F && limit > 0);
-                }
+            // only a row's first scores need their maximum before they are exponentiated (see below)
+            if (!anchored) {
+                if (__any_sync(kFull, m_ref == -CUDART_INF_F && lim > 0))
+                    raise(tile_top(), j > 0);
+                anchored = !__any_sync(kFull, m_ref == -CUDART_INF_F && limit > 0);
             }
             // rows past the sequence's end in its last page hold anything, and 0 * NaN would reach O: their V
             // becomes zeros, before either row tile multiplies it
-            if (L < key0 + kKeys && (L & (kPage - 1)) != 0) {
+            if (!FP8 && L < key0 + kKeys && (L & (kPage - 1)) != 0) {
                 ok = mbar_wait_bounded(bar_full((2 * j + 1) % C::kSlots), ((2 * j + 1) / C::kSlots) & 1, abort_flag,
                                        p.wait_limit);
                 ok = __all_sync(kFull, ok);
@@ -481,63 +485,37 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                 if (!ok)
                     *abort_flag = 1;                               // the other roles' waits end with it
             }
-            // P overwrites the first columns of each half of S
+            // P overwrites the first columns of each half of S.  A row's reference need not follow its maximum while
+            // the probabilities stay well inside their type's range, and the tile's sum shows whether some did not.
+            // Only then is the maximum taken, the reference raised, O rescaled and the tile done again.
             const float2 c2 = make_float2(c, c);
-            if constexpr (FP8) {
-                const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref - (float)kPShift;
+            float2 h2;
+#pragma unroll 1
+            for (int again = 0; again < 2; ++again) {
+                const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref;
                 const float2 s2 = make_float2(-msub, -msub);
+                h2 = make_float2(0.f, 0.f);
+                float2 g2 = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t hi[8], lo[8];
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int k = q * 32 + 4 * i;
-                        const float2 d0 = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
-                        const float2 d1 = ffma2(make_float2(v[k + 2], v[k + 3]), c2, s2);
-                        const float2 e0 = make_float2(ex2_ftz(d0.x), ex2_ftz(d0.y));
-                        const float2 e1 = make_float2(ex2_ftz(d1.x), ex2_ftz(d1.y));
-                        l2 = fadd2(fadd2(l2, e0), e1);
-                        const uint32_t a = pack_f16x2(e0.x, e0.y), bb = pack_f16x2(e1.x, e1.y);
-                        const uint32_t ah = a & 0xFF80FF80u, bh = bb & 0xFF80FF80u;     // 3 fraction bits
-                        hi[i] = e4m3x4_from_f16x2(ah, bh);
-                        lo[i] = e4m3x4_from_f16x2(hsub2(a, ah), hsub2(bb, bh));
+                    for (int i = 0; i < 16; ++i) {
+                        const int k = q * 32 + 2 * i;
+                        const float2 d = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
+                        const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
+                        (i & 1 ? g2 : h2) = fadd2(i & 1 ? g2 : h2, e);
+                        pk[i] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                     }
-                    tmem_st32_u<8>(ts + (q >> 1) * 64 + (q & 1) * 8, hi);
-                    tmem_st32_u<8>(ts + (q >> 1) * 64 + 16 + (q & 1) * 8, lo);
+                    tmem_st32_u<16>(ts + (q >> 1) * 64 + (q & 1) * 16, pk);
                 }
-            } else {
-                // Probabilities keep bf16's relative precision at any size, so a row's reference need not follow its
-                // maximum: 2^40 times what the reference stands for is as good, and the tile's sum shows whether some
-                // probability passed that.  Only then is the maximum taken, the reference raised, O rescaled and
-                // the tile done again.
-                float2 h2;
-#pragma unroll 1
-                for (int again = 0; again < 2; ++again) {
-                    const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-                    const float2 s2 = make_float2(-msub, -msub);
-                    h2 = make_float2(0.f, 0.f);
-                    float2 g2 = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int k = q * 32 + 2 * i;
-                            const float2 d = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
-                            const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
-                            (i & 1 ? g2 : h2) = fadd2(i & 1 ? g2 : h2, e);
-                            pk[i] = pack_bf16x2(e.x, e.y);
-                        }
-                        tmem_st32_u<16>(ts + (q >> 1) * 64 + (q & 1) * 16, pk);
-                    }
-                    h2 = fadd2(h2, g2);
-                    if (again || !__any_sync(kFull, !(h2.x + h2.y <= 0x1p40f)))
-                        break;
-                    tmem_wait_st();
-                    raise(tile_top(), j > 0);
-                }
-                l2 = fadd2(l2, h2);
+                h2 = fadd2(h2, g2);
+                if (again || !__any_sync(kFull, !(h2.x + h2.y <= C::kSumMost)))
+                    break;
+                tmem_wait_st();
+                raise(tile_top(), j > 0);
             }
+            l2 = fadd2(l2, h2);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -555,7 +533,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             const float l = l2.x + l2.y;
             const long long qrow = (long long)(tok0 + jq) * p.H_q + h * p.G + iq;
             const long long slot = ((long long)(tok0 + jq) * p.nsplit + g) * p.H_q + h * p.G + iq;
-            const float mul = p.nsplit > 1 ? p.v_scale * (FP8 ? 0x1p-4f : 1.f) : (l == 0.f ? 0.f : p.v_scale / l);
+            const float mul = p.nsplit > 1 ? p.v_scale : (l == 0.f ? 0.f : p.v_scale / l);
 #pragma unroll
             for (int cc = 0; cc < 128; cc += 32) {
                 float o[32];
@@ -583,13 +561,54 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             }
             if (live) {
                 const float ln2 = 0.69314718055994531f;
-                const float lt = FP8 ? l * 0x1p-4f : l;            // the sum without P's shift
                 if (p.nsplit > 1) {
-                    p.part_m[slot] = lt > 0.f ? m_ref * ln2 : -CUDART_INF_F;
-                    p.part_l[slot] = lt;
+                    p.part_m[slot] = l > 0.f ? m_ref * ln2 : -CUDART_INF_F;
+                    p.part_l[slot] = l;
                 } else if (p.lse != nullptr) {
-                    p.lse[qrow] = l == 0.f ? -CUDART_INF_F : m_ref * ln2 + logf(lt);
+                    p.lse[qrow] = l == 0.f ? -CUDART_INF_F : m_ref * ln2 + logf(l);
                 }
+            }
+        }
+    } else {
+        // ================================================================ e4m3: V codes to f16 (exact)
+        reg_dec<C::kRegsConvert>();
+        const int w = warp - 12;
+        // a warp's load is four tokens' 128 codes, 16 a lane; token t's unit u lies at u ^ (t % 8) in its row.  The 16
+        // dimensions become units 2 u and 2 u + 1 of f16, the upper half of the lanes storing the odd one first, so
+        // that a store's lanes meet no bank twice
+        const int u = lane & 7, sub = lane >> 3;
+        for (int j = 0; j < n; ++j) {
+            const int slot = (2 * j + 1) % C::kSlots, vb = j & 1;
+            bool ok = wait_bar(bar_full(slot), ((2 * j + 1) / C::kSlots) & 1, abort_flag, p.wait_limit);
+            if (ok && j >= 2)
+                ok = wait_bar(bar_vempty(vb), ((j >> 1) - 1) & 1, abort_flag, p.wait_limit);
+            if (!__all_sync(kFull, ok)) {
+                *abort_flag = 1;
+                break;
+            }
+            const uint8_t *src = smem + slot * C::kSlotBytes;
+            uint8_t *dst = smem + C::kOffV + vb * C::kVBytes;
+            const int key0 = (t0 + j) * kKeys;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int t = w * 32 + k * 4 + sub, x8 = t & 7;
+                uint4 a = *reinterpret_cast<const uint4 *>(src + (t >> 3) * 1024 + x8 * 128 + ((u ^ x8) << 4));
+                if (key0 + t >= L)                                 // past the end the page holds anything
+                    a = make_uint4(0u, 0u, 0u, 0u);
+                const uint4 lo = make_uint4(f16x2_of_e4m3(a.x), f16x2_of_e4m3(a.x >> 16), f16x2_of_e4m3(a.y),
+                                            f16x2_of_e4m3(a.y >> 16));
+                const uint4 hi = make_uint4(f16x2_of_e4m3(a.z), f16x2_of_e4m3(a.z >> 16), f16x2_of_e4m3(a.w),
+                                            f16x2_of_e4m3(a.w >> 16));
+                uint8_t *row = dst + (t >> 3) * 2048 + (u >> 2) * 1024 + x8 * 128;
+                const int first = (2 * u & 7) + (u >> 2), second = first ^ 1;
+                *reinterpret_cast<uint4 *>(row + ((first ^ x8) << 4)) = u >> 2 ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + ((second ^ x8) << 4)) = u >> 2 ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar_vfull(vb));
+                mbar_arrive(bar_empty(slot));
             }
         }
     }
@@ -614,10 +633,10 @@ cudaError_t launch_t(const CUtensorMap &map, const PrefillParams &p, cudaStream_
         cudaFuncAttributes a{};
         return cudaFuncGetAttributes(&a, prefill_kernel<FP8>) == cudaSuccess ? a.numRegs : 0;
     }();
-    if (3 * regs < kRegsIssue + 2 * kRegsSoftmax)
+    if (regs < PCfg<FP8>::kRegsLaunch)
         return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)p.nsplit * p.row_blocks * p.H_kv * p.bs);
-    return launch_pdl(prefill_kernel<FP8>, grid, dim3(kThreads), PCfg<FP8>::kSmemBytes, stream, map, p);
+    return launch_pdl(prefill_kernel<FP8>, grid, dim3(PCfg<FP8>::kThreads), PCfg<FP8>::kSmemBytes, stream, map, p);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -674,21 +693,23 @@ cudaError_t encode_q_map(CUtensorMap *map, const void *q, long long num_tokens, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// CTAs that share the keys of a row block: the number with the least estimated time.  A CTA takes `kFixed` to start
-// and finish and `kTile` per key tile; `units` row blocks run num_sms at a time; a split adds the merge, which reads
-// what the partial states' writes left (520 bytes per row, head and split, both ways).  More CTAs even out the last
-// round of row blocks, or, when there are fewer than SMs, fill the GPU.
+// CTAs that share the keys of a row block: the number with the least estimated time.  A CTA takes kFixed to start and
+// finish and kTile per key tile (us); the GPU works off `units` row blocks (at most; with ragged query lengths the
+// tokens' own count bounds them) num_sms at a time, the last round half full on average; a split adds the merge, whose
+// partial states (520 bytes per row, head and split) are written and read.
 int prefill_nsplit(int bs, int num_tokens, int max_q_len, int H_q, int H_kv, int max_seq_len, int num_sms)
 {
-    constexpr double kFixed = 4.0, kTile = 1.4, kMerge = 3.0, kBytesPerUs = 4e6;
-    const long long rows = (long long)(H_q / H_kv) * max_q_len;
-    const long long units = (rows + kPrefillRows - 1) / kPrefillRows * H_kv * bs;
+    constexpr double kFixed = 4.0, kTile = 1.25, kMerge = 3.0, kBytesPerUs = 5e6;
+    const long long G = H_q / H_kv;
+    const long long most = (G * max_q_len + kPrefillRows - 1) / kPrefillRows * bs;
+    const long long have = (G * num_tokens + kPrefillRows - 1) / kPrefillRows + bs;
+    const double units = (double)(most < have ? most : have) * H_kv;
     const int tiles = (max_seq_len + kKeys - 1) / kKeys;
     int best = 1;
     double best_t = 1e300;
     for (int n = 1; n <= 64 && (n == 1 || n <= tiles); ++n) {
-        const long long waves = (units * n + num_sms - 1) / num_sms;
-        double t = waves * (kFixed + kTile * ((tiles + n - 1) / n));
+        const double cta = kFixed + kTile * ((tiles + n - 1) / n), rounds = units * n / num_sms;
+        double t = cta * (rounds <= 1.0 ? 1.0 : rounds + 0.5);
         if (n > 1)
             t += kMerge + 2.0 * n * num_tokens * H_q * 520.0 / kBytesPerUs;
         if (t < best_t * (n > 1 ? 0.97 : 1.0)) {

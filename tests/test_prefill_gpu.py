@@ -1,9 +1,9 @@
 """Attention of a chunk of new tokens against the definition in 64 bits.
 
 Tolerances.  Scores accumulate 128 products in fp32: at most 130 * 2^-24 * scale * sum |q k| off (e: that over the
-largest row, plus 2^-20 for the exponential and the sums).  bf16 pages round each probability by 2^-8, e4m3 pages
-by 2^-8 plus 2^-13 of the weight of the row's reference key; the output rounds by another 2^-8:
-    |out - ref| <= 2^-8 |ref| + (2^-8 + 2 e) sum p |v| [+ 2^-13 sum |v| / sum exp(s - max)].  lse is off by e."""
+largest row, plus 2^-20 for the exponential and the sums).  Each probability rounds by at most 2^-8 (bf16; f16 for e4m3
+pages) and the output by another 2^-8:
+    |out - ref| <= 2^-8 |ref| + (2^-8 + 2 e) sum p |v|.  lse is off by e."""
 import math
 
 import numpy as np
@@ -65,10 +65,7 @@ def reference(b):
                 ref = p @ v
                 out[a:a + q, i], lse[a:a + q, i] = ref, torch.logsumexp(sc, 1)
                 tol_l[a:a + q, i] = e + 2.0 ** -22 * lse[a:a + q, i].abs().nan_to_num(posinf=0)
-                t = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * e)[:, None] * (p @ v.abs())
-                if w.kv_dtype == si.KV_FP8:
-                    t += 2.0 ** -13 * ((~hide).double() @ v.abs()) * p.amax(1, keepdim=True) if n else 0
-                tol_o[a:a + q, i] = t
+                tol_o[a:a + q, i] = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * e)[:, None] * (p @ v.abs())
     return out, lse, tol_o, tol_l
 
 
