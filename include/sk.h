@@ -263,24 +263,21 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
  * sees no key gets out = 0 and lse = -inf.  Query lengths may differ and may be 0; max_q_len bounds them (more
  * sets SK_DEV_BAD_SEQ and skips the sequence, whose rows are then undefined).  num_tokens rows past cu_seqlens_q[bs] are left as they were.
  *
- * nsplit CTAs share the keys of each block of 256 query rows (G * q_len rows per sequence and KV head).  With
- * nsplit > 1 the partial states go through part_o, part_m and part_l (fp32 [num_tokens, nsplit, num_q_heads
- * (, 128)], as in sk_paged_decode_attn) and the call ends with the merge; then rows past cu_seqlens_q[bs] are
- * undefined.  With nsplit == 1 the three may be NULL.  sk_prefill_nsplit gives a good number.
- * q, kv_pages, out and part_o are 16-byte aligned; lse may be NULL.  Probabilities round to bf16 (f16
- * for e4m3fn pages); sums are fp32.
+ * The work is divided evenly over the SMs, in the key axis too, so few query rows on a long cache use the
+ * whole GPU.  max_seq_len, an upper bound on the lengths, sizes the launch of small calls only.  workspace (device, 16-byte
+ * aligned): sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype) bytes; its contents do not matter, and
+ * calls that may overlap need one each.  q, kv_pages and out are 16-byte aligned; lse may be NULL.  Probabilities
+ * round to bf16 (f16 for e4m3fn pages); sums are fp32; the same bits every time on the same device.
  * Returns SK_OK or a negative sk_status. */
 int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
                           const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
                           const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
-                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int nsplit,
-                          float *part_o, float *part_m, float *part_l, void *out, float *lse, void *stream);
+                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int max_seq_len,
+                          void *workspace, int64_t workspace_bytes, void *out, float *lse, void *stream);
 
-/* Number of CTAs that should share the keys of a row block of sk_paged_prefill_attn, 1 to 64, for sequences of
- * up to max_seq_len keys (an estimate from the number of row blocks and key tiles).  num_sms == 0 takes the
- * current device's.  Host-only arithmetic.  SK_ERR_INVALID for sizes out of range. */
-int sk_prefill_nsplit(int bs, int num_tokens, int max_q_len, int num_q_heads, int num_kv_heads, int max_seq_len,
-                      int num_sms);
+/* Bytes of workspace of sk_paged_prefill_attn on the current device (two partial states of 256 rows per SM, and for
+ * e4m3fn pages q in two terms).  A negative sk_status for bad sizes or if a CUDA call fails. */
+int64_t sk_prefill_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype);
 
 /* Attention weight gathered by each cached key: for every sequence s, KV head h and key p < seq_lens[s],
  *   acc_pages (place of p) += sum over query tokens t of s that see p, and heads hq of the group of h, of

@@ -24,7 +24,7 @@ __all__ = [
     "sk_static_scratch_bytes", "sk_reshape_and_cache", "sk_std_to_shuffled", "sk_set_wait_limit",
     "SK_OK", "SK_CACHED", "SK_ERR_TIMEOUT", "SK_KV_BF16", "SK_KV_FP8_E4M3", "SK_DEV_BAD_BLOCK",
     "SK_DEV_BAD_SEQ", "SK_DEV_TIMEOUT", "sk_rope_frequencies", "sk_rope_and_cache", "sk_evict_capacity",
-    "sk_evict_select", "sk_evict_move", "evict_rows", "sk_prefill_nsplit",
+    "sk_evict_select", "sk_evict_move", "evict_rows", "sk_prefill_workspace_bytes",
     "sk_paged_prefill_attn", "paged_prefill_attention", "sk_accum_attn_weights", "sk_accum_workspace_bytes",
 ]
 
@@ -89,11 +89,11 @@ def lib():
         L.sk_rope_and_cache.restype = i32
         L.sk_rope_and_cache.argtypes = [P, P, P, i64, i64, i64, P, P, i32, i32, f32, P, i32, i32, i32, i32, P, P, i32,
                                         f32, f32, i32, i32, P, P, P]
-        L.sk_prefill_nsplit.restype = i32
-        L.sk_prefill_nsplit.argtypes = [i32] * 7
+        L.sk_prefill_workspace_bytes.restype = i64
+        L.sk_prefill_workspace_bytes.argtypes = [i32, i32, i32]
         L.sk_paged_prefill_attn.restype = i32
         L.sk_paged_prefill_attn.argtypes = [P, P, i32, f32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32,
-                                            f32, i32, i32, P, P, P, P, P, P]
+                                            f32, i32, i32, P, i64, P, P, P]
         L.sk_accum_workspace_bytes.restype = i64
         L.sk_accum_workspace_bytes.argtypes = [i32, i32, i32]
         L.sk_accum_attn_weights.restype = i32
@@ -489,64 +489,60 @@ def _batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q):
             block_table.shape[1])
 
 
-def sk_prefill_nsplit(bs: int, num_tokens: int, max_q_len: int, num_q_heads: int, num_kv_heads: int,
-                      max_seq_len: int, num_sms: int = 0) -> int:
-    """CTAs that should share the keys of a block of 256 query rows (computed by the library; ``num_sms`` 0:
-    the current device's)."""
-    return _check(lib().sk_prefill_nsplit(bs, num_tokens, max_q_len, num_q_heads, num_kv_heads, max_seq_len, num_sms),
-                  "sk_prefill_nsplit")
+def sk_prefill_workspace_bytes(num_tokens: int, num_q_heads: int, kv_dtype: int) -> int:
+    """Bytes of device workspace that sk_paged_prefill_attn needs on the current device (computed by the library)."""
+    return _check(lib().sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype), "sk_prefill_workspace_bytes")
+
+
+def _buffer(ws, key, need, device):
+    """A byte buffer of at least ``need`` bytes, kept in the workspace dict."""
+    import torch
+    t = ws.get(key)
+    if t is None or t.numel() < need or t.device != device:
+        t = ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
+    return t.data_ptr()
 
 
 def sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse=None, *, max_q_len: int,
-                          sm_scale: float, k_scale: float = 1.0, v_scale: float = 1.0, causal: bool = True,
-                          part_o=None, part_m=None, part_l=None, stream=None) -> int:
+                          sm_scale: float, max_seq_len: Optional[int] = None, k_scale: float = 1.0,
+                          v_scale: float = 1.0, causal: bool = True, workspace=None, stream=None) -> int:
     """Attention of a chunk of new tokens over the paged cache into ``out`` (bf16 [num_tokens, num_q_heads, 128])
-    and ``lse`` (fp32 [num_tokens, num_q_heads], or None).  ``part_o`` (fp32 [num_tokens, nsplit, num_q_heads,
-    128]), ``part_m`` and ``part_l`` split the keys over nsplit CTAs; without them one CTA takes all keys of its
-    rows."""
+    and ``lse`` (fp32 [num_tokens, num_q_heads], or None).  ``max_seq_len`` bounds seq_lens (default: what the block
+    table holds) and only sizes the launch of small calls.  ``workspace`` is an optional dict that keeps the call's
+    buffer; calls that may overlap need one each."""
     import torch
     dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,
                                                                                cu_seqlens_q)
-    nsplit, po, pm, pl = 1, None, None, None
-    if part_o is not None:
-        nsplit = part_o.shape[1]
-        po = _fits(part_o, torch.float32, (nt, nsplit, hq, d), "part_o", dev)
-        pm = _fits(part_m, torch.float32, (nt, nsplit, hq), "part_m", dev)
-        pl = _fits(part_l, torch.float32, (nt, nsplit, hq), "part_l", dev)
+    po = _fits(out, torch.bfloat16, (nt, hq, d), "out", dev)
+    pl = None if lse is None else _fits(lse, torch.float32, (nt, hq), "lse", dev)
+    buf, need = None, 0
+    if dev >= 0:
+        ws = workspace if workspace is not None else {}
+        need = ws.get(("prefill bytes", nt, hq, dt, dev))
+        if need is None:
+            with torch.cuda.device(dev):
+                need = ws[("prefill bytes", nt, hq, dt, dev)] = sk_prefill_workspace_bytes(nt, hq, dt)
+        buf = _buffer(ws, "prefill", need, q.device)
     return _launch(dev, stream, "sk_paged_prefill_attn", lib().sk_paged_prefill_attn, pq, pp, dt, k_scale, v_scale, pb,
-                   stride, nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0, nsplit, po,
-                   pm, pl, _fits(out, torch.bfloat16, (nt, hq, d), "out", dev),
-                   None if lse is None else _fits(lse, torch.float32, (nt, hq), "lse", dev))
+                   stride, nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0,
+                   stride * page if max_seq_len is None else max_seq_len, buf, need, po, pl)
 
 
 def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *, max_q_len: int, sm_scale: float,
                             max_seq_len: Optional[int] = None, k_scale: float = 1.0, v_scale: float = 1.0,
                             causal: bool = True, workspace=None, out=None, lse=None, stream=None):
-    """One attention call of a chunk of new tokens (prompts, chunks of prompts, follow-up turns) over the paged
-    cache.  ``max_seq_len`` bounds seq_lens (default: what the block table holds); it only decides over how many
-    CTAs the keys are split.  ``workspace`` is an optional dict that keeps the split's buffers across calls of
-    the same shapes.  Returns (out bf16 [NT, H_q, 128], lse fp32 [NT, H_q])."""
+    """One attention call of a chunk of new tokens (prompts, chunks of prompts, follow-up turns; cross attention when
+    not ``causal``) over the paged cache; arguments as sk_paged_prefill_attn.  Returns (out bf16 [NT, H_q, 128], lse
+    fp32 [NT, H_q])."""
     import torch
     nt, hq, d = q.shape
-    dev = q.device
-    if max_seq_len is None:
-        max_seq_len = block_table.shape[1] * kv_pages.shape[2]
     if out is None:
-        out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((nt, hq), dtype=torch.float32, device=dev)
-    ws = workspace if workspace is not None else {}
-    key = ("prefill", nt, hq, seq_lens.numel(), max_q_len, max_seq_len)
-    if key not in ws:
-        n = sk_prefill_nsplit(seq_lens.numel(), nt, max_q_len, hq, kv_pages.shape[1], max_seq_len)
-        ws[key] = None if n == 1 else (
-            torch.empty((nt, n, hq, d), dtype=torch.float32, device=dev),
-            torch.empty((nt, n, hq), dtype=torch.float32, device=dev),
-            torch.empty((nt, n, hq), dtype=torch.float32, device=dev))
-    po, pm, pl = ws[key] or (None, None, None)
+        lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
     sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, max_q_len=max_q_len,
-                          sm_scale=sm_scale, k_scale=k_scale, v_scale=v_scale, causal=causal, part_o=po, part_m=pm,
-                          part_l=pl, stream=stream)
+                          sm_scale=sm_scale, max_seq_len=max_seq_len, k_scale=k_scale, v_scale=v_scale, causal=causal,
+                          workspace=workspace, stream=stream)
     return out, lse
 
 
@@ -570,11 +566,7 @@ def sk_accum_attn_weights(q, kv_pages, block_table, seq_lens, cu_seqlens_q, lse,
     buf, need = None, 0
     if dt == SK_KV_FP8_E4M3 and dev >= 0:
         need = sk_accum_workspace_bytes(nt, hq, dt)
-        ws = workspace if workspace is not None else {}
-        t = ws.get("accum")
-        if t is None or t.numel() < need or t.get_device() != dev:
-            t = ws["accum"] = torch.empty(need, dtype=torch.uint8, device=q.device)
-        buf = t.data_ptr()
+        buf = _buffer(workspace if workspace is not None else {}, "accum", need, q.device)
     return _launch(dev, stream, "sk_accum_attn_weights", lib().sk_accum_attn_weights, pq, pp, dt, k_scale, pb, stride,
                    nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0, pl, pa, buf, need)
 

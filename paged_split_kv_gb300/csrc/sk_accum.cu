@@ -72,7 +72,7 @@ struct ACfg {
     static constexpr int kBarDrain = kBarSFree + 8 * kGroup;
     static constexpr int kTmemSlot = kBarDrain + 8;
     static constexpr int kAbort = kTmemSlot + 4;
-    static constexpr int kStart = kAbort + 4;                      // int: first sequence; long long: its offset
+    static constexpr int kStart = (kAbort + 4 + 7) / 8 * 8;        // where the run starts
     static constexpr int kAux = 512;                               // float[kQSlots][kAuxEach], log2 units
     static_assert(kStart + 24 <= kAux && kAux + kQSlots * kAuxEach * 4 <= kMisc, "misc area");
     static_assert(kKSlots >= (MANY ? kGroup : 3) && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0 && kQSlot % 1024 == 0,
@@ -163,20 +163,8 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     auto bar_s = [&](int i) { return mbase + C::kBarS + 8 * i; };
     auto bar_sfree = [&](int i) { return mbase + C::kBarSFree + 8 * i; };
     const uint32_t bar_drain = mbase + C::kBarDrain;
-    long long *run = reinterpret_cast<long long *>(misc + C::kStart);     // offset of the first sequence, its index
 
     wait_prior_grid();
-    // ---- this CTA's run: block-tiles [lo, hi) of the batch's total, and the sequence that lo lies in
-    long long *part = reinterpret_cast<long long *>(smem);       // in the K slots, before the first copy
-    const int per = (p.bs + kThreads - 1) / kThreads;
-    const int s_lo = min(p.bs, (int)threadIdx.x * per), s_hi = min(p.bs, s_lo + per);
-    long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) {
-        int L, q, tok0;
-        const int w = Walk::accum_weight(p, s, L, q, tok0);
-        mine += (long long)((L + kKeys - 1) / kKeys) * w * p.H_kv;
-    }
-    part[threadIdx.x] = mine;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kKSlots; ++i) {
             mbar_init(bar_kfull(i), 1);
@@ -205,50 +193,20 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) {
-        // inclusive prefix of the 640 partial sums, 20 a lane
-        constexpr int kEach = kThreads / 32;
-        long long sum = 0;
-        for (int i = 0; i < kEach; ++i)
-            sum += part[lane * kEach + i];
-        long long incl = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(kFull, incl, o);
-            incl += lane >= o ? u : 0;
-        }
-        long long at = incl - sum;
-        for (int i = 0; i < kEach; ++i) {
-            at += part[lane * kEach + i];
-            part[lane * kEach + i] = at;
-        }
-    }
-    __syncthreads();
-    const long long total = part[kThreads - 1];
-    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-    {
-        const long long before = part[threadIdx.x] - mine;
-        if (mine > 0 && lo >= before && lo < before + mine) {
-            long long off = before;
-            int s = s_lo;
-            for (; s < s_hi - 1; ++s) {
-                int L, q, tok0;
-                const int w = Walk::accum_weight(p, s, L, q, tok0);
-                const long long size = (long long)((L + kKeys - 1) / kKeys) * w * p.H_kv;
-                if (lo < off + size)
-                    break;
-                off += size;
-            }
-            run[0] = off;
-            run[1] = s;
-        }
-    }
+    // this CTA's run of the batch's block-tiles (found in the K slots' memory, before the first copy)
+    const Run run = find_run<kThreads>(p.bs, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(smem),
+                                       reinterpret_cast<long long *>(misc + C::kStart), [&](int s) {
+                                           int L, q, tok0;
+                                           const int w = Walk::accum_weight(p, s, L, q, tok0);
+                                           return (long long)((L + kKeys - 1) / kKeys) * w * p.H_kv;
+                                       });
     fence_proxy_async_smem();                        // the copies come after these uses of the slots
     __syncthreads();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc + C::kTmemSlot);
-    const bool any = (sbase & 1023u) == 0 && lo < hi;
-    if ((sbase & 1023u) != 0 && threadIdx.x == 0)
+    const bool any = (sbase & 1023u) == 0;
+    if (!any && threadIdx.x == 0)
         atomicOr(p.status, SK_DEV_INTERNAL);
-    Walk walk(p, lo, hi, any ? (int)run[1] : p.bs, any ? run[0] : 0);
+    Walk walk(p, run.lo, run.hi, any ? run.s : p.bs, run.before);
     Item it;
 
     // groups of an item: its tiles in equal shares of up to four
@@ -546,7 +504,6 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     }
 }
 
-// Q as two e4m3 terms for e4m3 pages: row (t, hq) becomes 128 hi codes, then 128 lo codes, and 2^-e.
 __global__ void __launch_bounds__(256) split_q_kernel(const uint16_t *__restrict__ q, long long rows,
                                                       uint8_t *__restrict__ codes, float *__restrict__ scale)
 {
@@ -589,6 +546,13 @@ cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const 
 
 }  // namespace
 
+cudaError_t launch_split_q(const uint16_t *q, long long rows, void *codes, cudaStream_t stream)
+{
+    uint8_t *c = static_cast<uint8_t *>(codes);
+    return launch_pdl(split_q_kernel, dim3((unsigned)((rows + 31) / 32)), dim3(256), 0, stream, q, rows, c,
+                      reinterpret_cast<float *>(c + rows * 256));
+}
+
 // Rows of a Q block: 16, 32 or 64 when that holds all of a sequence's rows (they then stay while K streams), else 128.
 int accum_block_rows(int G, long long max_q_len)
 {
@@ -609,14 +573,11 @@ cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *q_codes,
     const void *q = p.q;
     if (fp8) {
         const long long rows = (long long)p.num_tokens * p.H_q;
-        uint8_t *codes = static_cast<uint8_t *>(q_codes);
-        float *scale = reinterpret_cast<float *>(codes + rows * 256);
-        const cudaError_t e = launch_pdl(split_q_kernel, dim3((unsigned)((rows + 31) / 32)), dim3(256), 0, stream, p.q,
-                                         rows, codes, scale);
+        const cudaError_t e = launch_split_q(p.q, rows, q_codes, stream);
         if (e != cudaSuccess)
             return e;
-        q = codes;
-        p.q_scale = scale;
+        q = q_codes;
+        p.q_scale = reinterpret_cast<const float *>(static_cast<uint8_t *>(q_codes) + rows * 256);
     }
     CUtensorMap kv_map, q_map;
     cudaError_t e = encode_page_map(&kv_map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 1 : 2);

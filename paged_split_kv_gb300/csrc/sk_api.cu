@@ -666,27 +666,21 @@ int sk_evict_move(const int32_t *src_rows, const int32_t *dst_rows, const int32_
     return SK_OK;
 }
 
-int sk_prefill_nsplit(int bs, int num_tokens, int max_q_len, int num_q_heads, int num_kv_heads, int max_seq_len,
-                      int num_sms)
+int64_t sk_prefill_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype)
 {
-    if (bs < 1 || bs > 32767 || num_tokens < 0 || max_q_len < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
-        num_q_heads % num_kv_heads != 0 || max_seq_len < 0 || num_sms < 0)
-        return fail(SK_ERR_INVALID,
-                    "sk_prefill_nsplit: bs=%d num_tokens=%d max_q_len=%d heads %d/%d max_seq_len=%d num_sms=%d", bs,
-                    num_tokens, max_q_len, num_q_heads, num_kv_heads, max_seq_len, num_sms);
-    if (num_sms == 0) {
-        const int rc = sm_count(&num_sms);
-        if (rc != SK_OK)
-            return rc;
-    }
-    return prefill_nsplit(bs, num_tokens, max_q_len, num_q_heads, num_kv_heads, max_seq_len, num_sms);
+    if (num_tokens < 0 || num_q_heads < 1 || (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3))
+        return fail(SK_ERR_INVALID, "sk_prefill_workspace_bytes: num_tokens=%d num_q_heads=%d kv_dtype=%d", num_tokens,
+                    num_q_heads, kv_dtype);
+    int sms = 0;
+    const int rc = sm_count(&sms);
+    return rc != SK_OK ? rc : prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
 }
 
 int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
                           const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
                           const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
-                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int nsplit,
-                          float *part_o, float *part_m, float *part_l, void *out, float *lse, void *stream)
+                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int max_seq_len,
+                          void *workspace, int64_t workspace_bytes, void *out, float *lse, void *stream)
 {
     if (q == nullptr || kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr ||
         cu_seqlens_q == nullptr || out == nullptr)
@@ -705,32 +699,33 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
                     num_tokens, max_q_len, block_table_stride, num_blocks);
     if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
         return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: %d query heads, %d kv heads", num_q_heads, num_kv_heads);
-    if (nsplit < 1 || nsplit > 0xFFFF)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: nsplit=%d outside [1, 65535]", nsplit);
-    if (nsplit > 1 && (part_o == nullptr || part_m == nullptr || part_l == nullptr))
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: nsplit=%d needs part_o, part_m and part_l", nsplit);
+    if (max_seq_len < 0)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: max_seq_len=%d", max_seq_len);
     if (!(sm_scale > 0.f && sm_scale < INFINITY) ||
         (kv_dtype == SK_KV_FP8_E4M3 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY)))
         return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: scales must be positive and finite");
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(kv_pages) | reinterpret_cast<uintptr_t>(out) |
-         reinterpret_cast<uintptr_t>(part_o)) & 15)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: q, kv_pages, out and part_o must be 16-byte aligned");
+         reinterpret_cast<uintptr_t>(workspace)) & 15)
+        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: q, kv_pages, out and workspace must be 16-byte aligned");
     const int G = num_q_heads / num_kv_heads;
-    const long long rows = (long long)G * max_q_len;
-    const long long blocks = (rows + kPrefillRows - 1) / kPrefillRows;
-    if (rows > 0x3FFFFFFFLL || blocks * nsplit * num_kv_heads > 0x7FFFFFFFLL / bs ||
+    if ((long long)num_q_heads * max_q_len > 0x3FFFFFFFLL || (long long)num_q_heads * num_tokens > 0x7FFFFFFFLL ||
         (long long)num_blocks * num_kv_heads * 2 > 0x7FFFFFFFLL)
-        return fail(SK_ERR_UNSUPPORTED,
-                    "sk_paged_prefill_attn: %lld rows, %d splits, %d sequences and %d blocks of %d heads exceed the "
-                    "kernel's limits (2^31 CTAs, 2^30 block-heads)",
-                    rows, nsplit, bs, num_blocks, num_kv_heads);
+        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: %d blocks of %d heads or %d query tokens of %d heads "
+                    "exceed the kernel's limits (2^30)", num_blocks, num_kv_heads, max_q_len, num_q_heads);
     if (num_tokens == 0)
         return SK_OK;
     int *status = nullptr;
+    int sms = 0;
     int rc = status_ptr(&status);
+    if (rc == SK_OK)
+        rc = sm_count(&sms);
     if (rc != SK_OK)
         return rc;
-    PrefillParams p;
+    const int64_t need = prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
+    if (workspace == nullptr || workspace_bytes < need)
+        return fail(SK_ERR_CAPACITY, "sk_paged_prefill_attn: workspace of %lld bytes, %lld needed",
+                    (long long)workspace_bytes, (long long)need);
+    PrefillParams p{};
     p.q = static_cast<const uint16_t *>(q);
     p.kv = kv_pages;
     p.block_table = block_table;
@@ -738,9 +733,6 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
     p.cu_q = cu_seqlens_q;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
-    p.part_o = part_o;
-    p.part_m = part_m;
-    p.part_l = part_l;
     p.status = status;
     p.num_blocks = num_blocks;
     p.bt_stride = block_table_stride;
@@ -750,19 +742,14 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
     p.H_q = num_q_heads;
     p.H_kv = num_kv_heads;
     p.G = G;
-    p.row_blocks = (int)blocks;
-    p.nsplit = nsplit;
     p.causal = causal ? 1 : 0;
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
     p.score_scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
     p.v_scale = fp8 ? v_scale : 1.f;
     p.wait_limit = wait_limit();
-    cudaError_t e = launch_prefill(p, kv_dtype, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_prefill(p, kv_dtype, max_seq_len, workspace, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "chunk attention kernel launch");
-    if (nsplit > 1)
-        return sk_merge_segments(part_o, part_m, part_l, nullptr, nsplit, num_tokens, num_q_heads, head_dim, nsplit,
-                                 out, lse, stream);
     return SK_OK;
 }
 

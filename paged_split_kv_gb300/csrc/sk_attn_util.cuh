@@ -105,10 +105,52 @@ __device__ __forceinline__ void split_q_row(uint2 raw, uint32_t &hi, uint32_t &l
     }
 }
 
-// mbar_wait_bounded with a test before the first suspending wait: a wait for what is complete costs less.
+// Waits for the phase with the given parity like mbar_wait_bounded, in few instructions (every role waits in many places,
+// and their code shares the instruction cache): a test, then suspended waits that a limit below kPollBelowCycles asks not
+// to suspend.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int *abort, long long limit)
 {
-    return sm100::mbar_test_wait(bar, parity) || sm100::mbar_wait_bounded(bar, parity, abort, limit);
+    if (sm100::mbar_test_wait(bar, parity))
+        return true;
+    const uint32_t hint = limit < sm100::kPollBelowCycles ? 0u : 0x989680u;      // ns
+    const long long t0 = clock64();
+    do {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(hint)
+            : "memory");
+        if (ok)
+            return true;
+    } while (!(abort != nullptr && *abort) && clock64() - t0 <= limit);
+    return false;
+}
+
+// Transposes a 4 x 4 matrix of 16-byte units held by a quad of lanes: lane b ends with unit b of every lane.
+__device__ __forceinline__ void quad_transpose(uint4 (&w)[4], int lane)
+{
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1) {
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & m)
+                continue;
+            uint4 &a = w[k], &b = w[k | m];
+            uint4 send = up ? a : b;
+            send.x = __shfl_xor_sync(0xffffffffu, send.x, m);
+            send.y = __shfl_xor_sync(0xffffffffu, send.y, m);
+            send.z = __shfl_xor_sync(0xffffffffu, send.z, m);
+            send.w = __shfl_xor_sync(0xffffffffu, send.w, m);
+            if (up)
+                a = send;
+            else
+                b = send;
+        }
+    }
 }
 
 // Gives registers of this warpgroup back / takes them, all its warps together.
@@ -134,18 +176,53 @@ __device__ __forceinline__ void tmem_st32_u(uint32_t taddr, const uint32_t *v)
     sm100::tmem_st32<N>(taddr, f);
 }
 
-// D (TMEM) (+)= A (TMEM, one row per lane, packed along the columns) x B (shared memory); called by a converged
-// warp, issued by its elected lane.
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate)
+// Four products D (TMEM) (+)= A x B in one block: one lane is elected for all, and the descriptors (or A's tensor
+// memory address) advance by constants.  Called by a converged warp.
+#define SK_MMA4(A_OP, A_TYPE)                                                                                    \
+    "{\n\t.reg .pred p, t, e;\n\t.reg ." A_TYPE " a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"                              \
+    "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"                                                               \
+    "add.s" A_OP " a1, %1, %5;\n\tadd.s" A_OP " a2, %1, %5 + %5;\n\tadd.s" A_OP " a3, %1, %5 + %5 + %5;\n\t"         \
+    "add.s64 b1, %2, %6;\n\tadd.s64 b2, %2, %6 + %6;\n\tadd.s64 b3, %2, %6 + %6 + %6;\n\t"                           \
+    "elect.sync _|e, 0xffffffff;\n\t"
+
+template <int kStepA, int kStepB>
+__device__ __forceinline__ void mma4_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    asm volatile(SK_MMA4("64", "b64")
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepA), "n"(kStepB)
+                 : "memory");
+}
+
+template <int kStepA, int kStepB>
+__device__ __forceinline__ void mma4_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(SK_MMA4("64", "b64")
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepA), "n"(kStepB)
+                 : "memory");
+}
+
+// A in tensor memory, one row per lane, packed along the columns.
+template <int kStepA, int kStepB>
+__device__ __forceinline__ void mma4_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(SK_MMA4("32", "b32")
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepA), "n"(kStepB)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
@@ -155,6 +232,68 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+
+// The run of a CTA: the batch's total cost, sequence s costing cost(s), is cut into `count` equal runs, and [lo, hi) is
+// that of `index`.  Finds the sequence that lo lies in and the cost before it.  `part` and `found` are shared memory
+// (kThreads / 32 and 2 words of 64 bits); every thread of the block calls it, and all get the same answer.
+struct Run {
+    long long lo, hi, before;
+    int s;
+};
+
+template <int kThreads, typename Cost>
+__device__ __forceinline__ Run find_run(int bs, int index, int count, long long *part, long long *found, Cost cost)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (bs + kThreads - 1) / kThreads;
+    const int s0 = min(bs, tid * per), s1 = min(bs, s0 + per);
+    long long mine = 0;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s)
+        mine += cost(s);
+    long long incl = mine;                           // inclusive prefix within the warp
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+        incl += lane >= o ? u : 0;
+    }
+    if (lane == 31)
+        part[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const long long u = part[w];
+        before += w < warp ? u : 0;
+        total += u;
+    }
+    __syncthreads();                                 // the caller may use the memory for something else
+    Run r;
+    // a little more than total / count (a 64-bit division takes thousands of cycles in all threads)
+    const long long each = (long long)((float)total / (float)count * (1.f + 0x1p-20f)) + 1;
+    r.lo = min(total, each * index);
+    r.hi = min(total, each * (index + 1));
+    if (mine > 0 && r.lo >= before && r.lo < before + mine) {
+        int s = s0;
+#pragma unroll 1
+        for (; s < s1 - 1; ++s) {
+            const long long size = cost(s);
+            if (r.lo < before + size)
+                break;
+            before += size;
+        }
+        found[0] = before;
+        found[1] = s;
+    }
+    __syncthreads();
+    r.before = r.lo < r.hi ? found[0] : 0;
+    r.s = r.lo < r.hi ? (int)found[1] : bs;
+    return r;
+}
+
+// Q as two e4m3 terms for e4m3 pages: row (t, hq) becomes 128 hi codes, then 128 lo codes at codes + 256 * row, and
+// 2^-e in the float array behind them.
+cudaError_t launch_split_q(const uint16_t *q, long long rows, void *codes, cudaStream_t stream);
 
 // Tensor map of Q rows [tokens][heads][256 bytes] (bf16, or e4m3 hi and lo codes): a box is 128 bytes of `heads` heads
 // of `toks` tokens and lands as consecutive 128-byte-swizzled rows.

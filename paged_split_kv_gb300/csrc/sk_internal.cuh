@@ -165,28 +165,38 @@ cudaError_t launch_kv_write(const uint16_t *key, const uint16_t *value, const in
 cudaError_t launch_std_to_shuffled(const void *pages, int kv_dtype, const int32_t *ids, int num_ids,
                                    long long num_blocks, int num_kv_heads, void *k_out, void *v_out,
                                    int *status, int num_sms, cudaStream_t stream);
+// Chunk attention: a piece of a unit of work (two row tiles of one sequence and KV head), key tiles [a, b) of its t.
+struct PrefillPiece {
+    int s, h, unit, L, q_len, tok0;
+    int t, a, b;
+    int nA, nB;                  // tiles of [a, b) that row tiles A and B need
+    int pad;
+};
+
 // Attention of a chunk of new tokens, resolved on the host.
 struct PrefillParams {
     const uint16_t *q;           // bf16 bits [NT, H_q, D]
+    const float *q_scale;        // e4m3 pages: 2^-e of each row of the split Q (set by the launcher)
     const void *kv;              // pages
     const int32_t *block_table, *seq_lens, *cu_q;
-    uint16_t *out;               // nsplit == 1: bf16 bits [NT, H_q, D]
-    float *lse;                  // nsplit == 1: [NT, H_q] or NULL
-    float *part_o, *part_m, *part_l;   // nsplit > 1: [NT, nsplit, H_q(, D)]
+    uint16_t *out;               // bf16 bits [NT, H_q, D]
+    float *lse;                  // [NT, H_q] or NULL
+    float *part_o, *part_m, *part_l;   // partial states of the pieces (set by the launcher) ...
+    PrefillPiece *shared;        // ... and what they are pieces of, two per run
     int *status;
     int64_t num_blocks;
     int bt_stride, bs, num_tokens, max_q_len;
     int H_q, H_kv, G;
-    int row_blocks;              // blocks of 256 rows that a sequence of max_q_len tokens has
-    int nsplit;                  // CTAs that share the keys of a row block
+    int gb, tpb, nsub;           // heads and tokens of a row tile, row tiles per token (set by the launcher)
+    int deal;                    // whole units are dealt to the CTAs first (set by the launcher)
     int causal;
     float score_scale_log2;      // sm_scale * k_scale * log2(e)
     float v_scale;
     long long wait_limit;
 };
-constexpr int kPrefillRows = 256;
-int prefill_nsplit(int bs, int num_tokens, int max_q_len, int H_q, int H_kv, int max_seq_len, int num_sms);
-cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, cudaStream_t stream);
+long long prefill_workspace_bytes(int num_tokens, int H_q, int kv_dtype, int num_sms);
+cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,
+                           cudaStream_t stream);
 // Gathered attention weights, resolved on the host.
 struct AccumParams {
     const uint16_t *q;           // bf16 bits [NT, H_q, D]

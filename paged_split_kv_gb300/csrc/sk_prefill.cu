@@ -14,13 +14,15 @@
 // probabilities never pass through shared memory.
 // A row is one TMEM lane and so one thread: the row's maximum and sum need no exchange between threads.
 //
-// Roles (384 threads):
+// Roles (384 threads; 512 for e4m3 pages):
 //   warp 0      copies: K and V of a key tile apart, 32 KB (16 KB e4m3) slots, one TMA copy per page and part, so
 //               the ring holds two and a half (five) key tiles beside Q
-//   warps 1, 2  issue the products of A and of B, each through one elected lane (warp 1 also allocates TMEM); one issuer
-//               for both was the bottleneck: its waits, 200 cycles each even for what is complete, came one after the
-//               other (3300 cycles per key tile against 2048 of products)
-//   warps 4-7   Q tile A into shared memory; softmax of A, its rescaling, its output
+//   warps 1, 2  issue the products of A and of B, each through one elected lane (warp 1 also allocates TMEM), and take
+//               turns: one issuer for both was the bottleneck, its waits, 200 cycles each even for what is complete,
+//               coming one after the other (3300 cycles per key tile against 2048 of products), and two that did not
+//               take turns fell into step, both softmaxes at once (4000)
+//   warp 3      finds the pieces of the CTA's share, publishes them to the others, copies their Q tiles
+//   warps 4-7   softmax of A, its rescaling, its output
 //   warps 8-11  the same for B
 // S(j) complete implies PV(j - 1) complete (products of one issuer complete in issue order), so the softmax may rescale O
 // at once; it does so only when scores beat the reference by far.
@@ -28,16 +30,19 @@
 // e4m3 pages: QK runs as kind::f8f6f4 on the codes, with Q as two e4m3 terms and a power-of-two scale per row (exact for
 // bf16 elements within 2^-9 of the row's largest), as two products into one S.  V's codes become f16 (exactly) in
 // shared memory, by four more warps (12-15), and PV runs on f16.  (P as two e4m3 terms with V's codes as they are
-// needs no conversion, but costs the softmax two more instructions per score: 263 against TODO us on 4 chunks of up to
-// 1024 tokens over 16k keys.)
+// needs no conversion, but costs the softmax two more instructions per score: 325 against 266 us on 2432 tokens over
+// 10.6k keys, 32/8 heads.)
 //
-// Few row tiles on a long axis: the keys of every row tile are split over `nsplit` CTAs that write partial
-// softmax states, joined by the library's merge.
+// Division of the work: one CTA per SM with an equal share of the batch's cost, cut in the key axis where a share ends
+// (below); what several CTAs have of a unit is joined by a second kernel.  Inside its share a CTA goes from unit to unit
+// without a pause: the copies run ahead, Q comes by TMA when its last product is done, and a unit's output is written
+// while the other row tile's products run.
 //
 // Every wait is bounded as in the decode kernel: on expiry SK_DEV_TIMEOUT is set and every role gives up; the
 // producer waits for its copies and the issuer for its last commit before the CTA exits.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -57,19 +62,20 @@ constexpr int kRows = 128;                           // rows of one tile (MMA M)
 constexpr int kKeys = 128;                           // keys of one tile (MMA N)
 constexpr long long kDrainLimit = 4000000000LL;      // cycles (~2 s): waits for work already issued
 constexpr int kMaxSmem = 232448;
+constexpr int kRing = 4;                             // pieces published ahead
 template <bool FP8>
 struct PCfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
     // registers per thread after the reallocation: copies and products, softmax, e4m3's conversion of V; no more in all
     // than at launch (4 x 128, or 3 x 168)
     static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-    static constexpr int kRegsIssue = FP8 ? 80 : 104, kRegsSoftmax = FP8 ? 192 : 200, kRegsConvert = 48;
+    static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoftmax = FP8 ? 208 : 216, kRegsConvert = 32;
     static_assert(kRegsIssue + 2 * kRegsSoftmax + (FP8 ? kRegsConvert : 0) <= kThreads / 128 * kRegsLaunch, "registers");
     static constexpr int kQTile = kRows * 256;                     // bf16: two 64-dimension chunks; e4m3: hi and lo
     static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K (or V) of 8 tokens, as copied
     static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
     static constexpr int kVBytes = FP8 ? kKeys * 256 : 0;          // e4m3: V of a tile as f16, two of them
-    static constexpr int kMisc = 3072;                             // barriers, then kCrow
+    static constexpr int kMisc = 1024;                             // barriers
     static constexpr int kSlots = (kMaxSmem - 2 * kQTile - 2 * kVBytes - kMisc) / kSlotBytes;
     static constexpr int kOffV = kSlots * kSlotBytes;
     static constexpr int kOffQ = kOffV + 2 * kVBytes;
@@ -82,8 +88,9 @@ struct PCfg {
     // misc area
     static constexpr int kBarFull = 0;
     static constexpr int kBarEmpty = 8 * kSlots;
-    static constexpr int kBarQ = 16 * kSlots;                      // [2]
-    static constexpr int kBarS = kBarQ + 16;                       // [2] S complete
+    static constexpr int kBarQ = 16 * kSlots;                      // [2] Q tile landed
+    static constexpr int kBarQFree = kBarQ + 16;                   // [2] the last product that reads it complete
+    static constexpr int kBarS = kBarQFree + 16;                       // [2] S complete
     static constexpr int kBarP = kBarS + 16;                       // [2] P written
     static constexpr int kBarO = kBarP + 16;                       // [2] last PV complete
     static constexpr int kBarTurn = kBarO + 16;                    // [2] the other issuer has issued its products
@@ -92,74 +99,329 @@ struct PCfg {
     static constexpr int kBarDrain = kBarVEmpty + 16;              // [2]
     static constexpr int kTmemSlot = kBarDrain + 16;
     static constexpr int kAbort = kTmemSlot + 4;
-    static constexpr int kCrow = 512;                              // float[256]: score scale of each row (e4m3)
-    static_assert(kAbort + 4 <= kCrow && kCrow + 1024 <= kMisc, "misc area");
+    static constexpr int kStart = (kAbort + 4 + 7) / 8 * 8;        // where the run starts
+    static constexpr int kBarPieceFull = kStart + 24;              // [kRing]
+    static constexpr int kBarPieceEmpty = kBarPieceFull + 8 * kRing;
+    static constexpr int kPieces = (kBarPieceEmpty + 8 * kRing + 15) / 16 * 16;   // Piece[kRing]
+    static constexpr int kReaders = FP8 ? 15 : 11;                 // warps that read the pieces
+    static_assert(kPieces + kRing * 48 <= kMisc, "misc area");
     static_assert(kSlots >= 3 && (!FP8 || kSlots % 2 == 0) && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0, "shared memory");
 };
 
 // TMEM map (columns)
 constexpr int kColS = 0, kColO = 256;                // S_A, S_B, then O_A, O_B, 128 each
 
+// ------------------------------------------------------------------ the work and its division
+// A row tile is `tpb` query tokens times `gb` heads of the group (nsub tiles per token when the group has more than 128);
+// a unit is two neighbouring row tiles of one (sequence, KV head), A and B, over all keys that its last token sees.
+// Units cost their keys plus a fixed part; each CTA takes an equal share of the batch's cost, a contiguous run of units
+// cut where the share ends, in the key axis too.  A unit inside one run goes straight to the output; the pieces of
+// a unit that several runs share go to a slot each, as partial softmax states, and prefill_join_kernel joins them.
+// A batch whose K and V are too large to stay in the L2 begins with whole units, dealt to the CTAs in turn, and only
+// what is left over is shared out like that: CTAs that work at the same time then read the same heads (4096 tokens over
+// 32k keys, 8 KV heads, 151 MB: 1433 us with 0.2 GB read from HBM, against 1543 us and 3.6 GB).
+struct Seq {
+    int L, q_len, tok0, units;                       // units of one head
+    long long base, step;                            // unit i costs base + step * (i + 1)
+    __device__ __forceinline__ long long before(int i) const { return i * base + step * i * (i + 1) / 2; }
+    __device__ __forceinline__ long long cost(int i) const { return base + step * (i + 1); }
+};
+
+constexpr double kL2Share = 60e6;                    // bytes of K and V that stay in the L2 (126 MB in two halves)
+constexpr int kUnitFixed = 384;                      // cost of starting and finishing a unit, in keys
+
+__device__ __forceinline__ Seq sequence(const PrefillParams &p, int s)
+{
+    Seq q;
+    q.L = __ldg(p.seq_lens + s);
+    q.tok0 = __ldg(p.cu_q + s);
+    q.q_len = __ldg(p.cu_q + s + 1) - q.tok0;
+    if (q.q_len < 0 || q.q_len > p.max_q_len || q.tok0 < 0 || q.tok0 + q.q_len > p.num_tokens || q.L < 0 ||
+        (long long)q.L > (long long)p.bt_stride * kPage) {
+        atomicOr(p.status, SK_DEV_BAD_SEQ);
+        q.q_len = 0;
+    }
+    q.units = ((q.q_len + p.tpb - 1) / p.tpb * p.nsub + 1) / 2;
+    const bool rising = p.causal && p.nsub == 1;     // later units see more keys
+    q.base = kUnitFixed + (rising ? max(0, q.L - q.q_len) : q.L);
+    q.step = rising ? 2 * p.tpb : 0;
+    return q;
+}
+
+using Piece = PrefillPiece;
+static_assert(sizeof(Piece) == 48, "the ring holds pieces of three 16-byte words");
+
+// First token and head (within the group) of row tile T.
+__device__ __forceinline__ void tile_origin(const PrefillParams &p, int T, int &j0, int &i0)
+{
+    j0 = T * p.tpb;
+    i0 = 0;
+    if (p.nsub > 1) {
+        j0 = T / p.nsub;                             // then a row tile is part of one token
+        i0 = (T - j0 * p.nsub) * p.gb;
+    }
+}
+
+// Key tiles that row tile T of a sequence needs (0 when it has no tokens).
+__device__ __forceinline__ int tiles_of(const PrefillParams &p, int L, int q_len, int T)
+{
+    int j0, i0;
+    tile_origin(p, T, j0, i0);
+    if (j0 >= q_len)
+        return 0;
+    return (visible_keys(L, q_len, min(q_len, j0 + p.tpb) - 1, p.causal) + kKeys - 1) / kKeys;
+}
+
+// What a CTA has to do: whole units first, first + stride, ... below `dealt` (in the order of sequence, head, unit), then the
+// pieces of the run [lo, hi) of the cost, which starts in sequence s, `before` in.
+struct Share {
+    long long lo, hi, before;
+    int s, first, stride, dealt;
+};
+
+// Walks a share's pieces; called by a converged warp.
+struct Walk {
+    const PrefillParams &p;
+    long long lo, hi, off;                           // the run, and where the current sequence starts
+    int s, h, unit;
+    int deal, stride, dealt, seek, passed;           // next unit dealt; the sequence that the search is at, units before it
+    bool loaded;
+    Seq q;
+    __device__ Walk(const PrefillParams &pp, const Share &sh)
+        : p(pp), lo(sh.lo), hi(sh.hi), off(sh.before), s(sh.s), h(0), unit(-1), deal(sh.first), stride(sh.stride),
+          dealt(sh.dealt), seek(0), passed(0), loaded(false)
+    {
+    }
+    __device__ __forceinline__ void fill(Piece &pc, int s_, int h_, int unit_, const Seq &sq, int &tA, int &tB) const
+    {
+        pc.s = s_;
+        pc.h = h_;
+        pc.unit = unit_;
+        pc.L = sq.L;
+        pc.q_len = sq.q_len;
+        pc.tok0 = sq.tok0;
+        tA = tiles_of(p, sq.L, sq.q_len, 2 * unit_);
+        tB = tiles_of(p, sq.L, sq.q_len, 2 * unit_ + 1);
+        pc.t = max(tA, tB);
+    }
+    // Unit number `deal`: 32 sequences at a time until the one that has it.
+    __device__ __forceinline__ void dealt_unit(Piece &pc)
+    {
+        const int lane = threadIdx.x & 31;
+        Seq sq;
+        int own, incl;
+        while (true) {
+            sq = sequence(p, min(seek + lane, p.bs - 1));
+            own = seek + lane < p.bs ? sq.units * p.H_kv : 0;
+            incl = own;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFull, incl, o);
+                incl += lane >= o ? u : 0;
+            }
+            const int all = __shfl_sync(kFull, incl, 31);
+            if (deal < passed + all)
+                break;
+            passed += all;
+            seek += 32;
+        }
+        const int src = __ffs(__ballot_sync(kFull, deal < passed + incl)) - 1;
+        const int index = deal - passed - __shfl_sync(kFull, incl - own, src);
+        const int at = seek + src;
+        Seq found = sequence(p, at);
+        int tA, tB;
+        fill(pc, at, index / found.units, index % found.units, found, tA, tB);
+        pc.a = 0;
+        pc.b = pc.t;
+        pc.nA = tA;
+        pc.nB = tB;
+        deal += stride;
+    }
+    // This run's key tiles of a unit.  A cut near either end of the unit moves there (a piece costs its start, its end and
+    // its share of the join), and where else it falls is rounded in fp32: alike in both runs that it divides, and that
+    // is all that matters.
+    __device__ __forceinline__ void cut(Piece &pc, long long start, long long cost) const
+    {
+        auto tile = [&](long long at) {
+            return at <= kUnitFixed             ? 0
+                   : at >= cost - kUnitFixed ? pc.t
+                                             : max(0, min(pc.t, (int)((float)pc.t * __fdividef((float)at, (float)cost))));
+        };
+        pc.a = tile(max(0LL, lo - start));
+        pc.b = tile(hi - start);
+    }
+    __device__ __forceinline__ bool next(Piece &pc)
+    {
+        if (deal < dealt) {
+            dealt_unit(pc);
+            return true;
+        }
+        while (s < p.bs && off < hi) {
+            if (!loaded) {
+                q = sequence(p, s);
+                loaded = true;
+            }
+            const long long head = q.before(q.units);
+            if (h >= p.H_kv || q.units == 0) {
+                off += head * p.H_kv;
+                ++s;
+                h = 0;
+                unit = -1;
+                loaded = false;
+                continue;
+            }
+            const long long h0 = off + h * head;
+            if (h0 + head <= lo) {
+                ++h;
+                continue;
+            }
+            if (unit < 0) {
+                unit = 0;
+                if (lo > h0) {                       // the last unit that starts at lo or before
+                    int left = 0, right = q.units - 1;
+                    while (left < right) {
+                        const int mid = (left + right + 1) >> 1;
+                        if (q.before(mid) <= lo - h0)
+                            left = mid;
+                        else
+                            right = mid - 1;
+                    }
+                    unit = left;
+                }
+            }
+            const long long start = h0 + q.before(unit);
+            if (start >= hi)
+                return false;
+            int tA, tB;
+            fill(pc, s, h, unit, q, tA, tB);
+            cut(pc, start, q.cost(unit));
+            if (++unit == q.units) {
+                ++h;
+                unit = -1;
+            }
+            pc.nA = max(0, min(pc.b, tA) - pc.a);
+            pc.nB = max(0, min(pc.b, tB) - pc.a);
+            // a unit without keys belongs to the run that it starts in
+            if (pc.a < pc.b || (pc.t == 0 && start >= lo))
+                return true;
+        }
+        return false;
+    }
+};
+
+// The share of CTA `index` of `count`; every thread of the block calls it.  `part` (2 words of 64 bits per warp) and
+// `found` (3) are shared memory; the share is there for all threads on return.
+template <int kThreads>
+__device__ __forceinline__ Share find_share(const PrefillParams &p, int index, int count, long long *part, long long *found)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.bs + kThreads - 1) / kThreads;
+    const int s0 = min(p.bs, tid * per), s1 = min(p.bs, s0 + per);
+    long long cost = 0;
+    int units = 0;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) {
+        const Seq q = sequence(p, s);
+        cost += q.before(q.units) * p.H_kv;
+        units += q.units * p.H_kv;
+    }
+    long long cost_to = cost;                        // inclusive prefixes within the warp
+    int units_to = units;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(kFull, cost_to, o);
+        const int w = __shfl_up_sync(kFull, units_to, o);
+        cost_to += lane >= o ? u : 0;
+        units_to += lane >= o ? w : 0;
+    }
+    if (lane == 31) {
+        part[2 * warp] = cost_to;
+        part[2 * warp + 1] = units_to;
+    }
+    __syncthreads();
+    long long total = 0, cost_before = cost_to - cost;
+    int all = 0, units_before = units_to - units;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+        cost_before += w < warp ? part[2 * w] : 0;
+        units_before += w < warp ? (int)part[2 * w + 1] : 0;
+        total += part[2 * w];
+        all += (int)part[2 * w + 1];
+    }
+    Share sh;
+    sh.first = index;
+    sh.stride = count;
+    sh.dealt = p.deal ? all / count * count : 0;
+    // the cost of what is dealt, then the run's bounds, in one search each among this thread's sequences
+    if (tid == 0)
+        found[2] = sh.dealt == all ? total : 0;
+    __syncthreads();
+    if (sh.dealt > 0 && units > 0 && sh.dealt >= units_before && sh.dealt < units_before + units) {
+        long long before = cost_before;
+        int left = sh.dealt - units_before;
+#pragma unroll 1
+        for (int s = s0; s < s1; ++s) {
+            const Seq q = sequence(p, s);
+            const int here = q.units * p.H_kv;
+            if (left < here) {
+                found[2] = before + (long long)(left / q.units) * q.before(q.units) + q.before(left % q.units);
+                break;
+            }
+            left -= here;
+            before += q.before(q.units) * p.H_kv;
+        }
+    }
+    __syncthreads();
+    const long long base = found[2], rest = total - base;
+    // a little more than rest / count (a 64-bit division takes thousands of cycles in all threads)
+    const long long each = (long long)((float)rest / (float)count * (1.f + 0x1p-20f)) + 1;
+    sh.lo = min(total, base + each * index);
+    sh.hi = min(total, base + each * (index + 1));
+    if (cost > 0 && sh.lo >= cost_before && sh.lo < cost_before + cost) {
+        long long before = cost_before;
+        int s = s0;
+#pragma unroll 1
+        for (; s < s1 - 1; ++s) {
+            const Seq q = sequence(p, s);
+            const long long here = q.before(q.units) * p.H_kv;
+            if (sh.lo < before + here)
+                break;
+            before += here;
+        }
+        found[0] = before;
+        found[1] = s;
+    }
+    __syncthreads();
+    sh.before = sh.lo < sh.hi ? found[0] : 0;
+    sh.s = sh.lo < sh.hi ? (int)found[1] : p.bs;
+    return sh;
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(PCfg<FP8>::kThreads, 1)
-prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p)
+prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+               const PrefillParams p)
 {
     using C = PCfg<FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];
-
-    wait_prior_grid();
-    if (blockIdx.x == 0 && threadIdx.x == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_q + p.bs) != p.num_tokens))
-        atomicOr(p.status, SK_DEV_BAD_SEQ);
-    // row blocks of one (sequence, head) are neighbours, the longest first, so that they share K and V in L2
-    int b = blockIdx.x;
-    const int g = b % p.nsplit;
-    b /= p.nsplit;
-    const int rb = p.row_blocks - 1 - b % p.row_blocks;
-    b /= p.row_blocks;
-    const int h = b % p.H_kv;
-    const int s = b / p.H_kv;
-    const int L = __ldg(p.seq_lens + s);
-    const int tok0 = __ldg(p.cu_q + s);
-    const int q_len = __ldg(p.cu_q + s + 1) - tok0;
-    const uint32_t sbase = smem_u32(smem);
-    if (q_len < 0 || q_len > p.max_q_len || tok0 < 0 || tok0 + q_len > p.num_tokens || L < 0 ||
-        (long long)L > (long long)p.bt_stride * kPage || (sbase & 1023u) != 0) {
-        if (threadIdx.x == 0)
-            atomicOr(p.status, (sbase & 1023u) != 0 ? SK_DEV_INTERNAL : SK_DEV_BAD_SEQ);
-        return;
-    }
-    const int R_all = p.G * q_len;
-    const int row0 = rb * 2 * kRows;
-    if (row0 >= R_all)
-        return;
-    const int rowsA = min(kRows, R_all - row0), rowsB = max(0, min(kRows, R_all - row0 - kRows));
-
-    // key tiles: the row block's tiles are cut into nsplit ranges; a row tile stops where its last row does
-    auto tiles_of = [&](int first, int rows) {
-        if (rows <= 0)
-            return 0;
-        return (visible_keys(L, q_len, (first + rows - 1) / p.G, p.causal) + kKeys - 1) / kKeys;
-    };
-    const int tA = tiles_of(row0, rowsA), tB = tiles_of(row0 + kRows, rowsB);
-    const int t_all = max(tA, tB);
-    const int t0 = (int)((long long)t_all * g / p.nsplit), t1 = (int)((long long)t_all * (g + 1) / p.nsplit);
-    const int nA = max(0, min(t1, tA) - t0), nB = max(0, min(t1, tB) - t0);
-    const int n = max(nA, nB);
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(smem);
     uint8_t *misc = smem + C::kOffMisc;
     const uint32_t mbase = sbase + C::kOffMisc;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + C::kAbort);
     auto bar_full = [&](int i) { return mbase + C::kBarFull + 8 * i; };
     auto bar_empty = [&](int i) { return mbase + C::kBarEmpty + 8 * i; };
     auto bar_q = [&](int x) { return mbase + C::kBarQ + 8 * x; };
+    auto bar_qfree = [&](int x) { return mbase + C::kBarQFree + 8 * x; };
     auto bar_s = [&](int x) { return mbase + C::kBarS + 8 * x; };
     auto bar_p = [&](int x) { return mbase + C::kBarP + 8 * x; };
     auto bar_o = [&](int x) { return mbase + C::kBarO + 8 * x; };
+    auto bar_turn = [&](int x) { return mbase + C::kBarTurn + 8 * x; };
     auto bar_vfull = [&](int i) { return mbase + C::kBarVFull + 8 * i; };
     auto bar_vempty = [&](int i) { return mbase + C::kBarVEmpty + 8 * i; };
-    auto bar_turn = [&](int x) { return mbase + C::kBarTurn + 8 * x; };
     auto bar_drain = [&](int x) { return mbase + C::kBarDrain + 8 * x; };
+    auto bar_piece = [&](int i) { return mbase + C::kBarPieceFull + 8 * i; };
+    auto bar_piece_free = [&](int i) { return mbase + C::kBarPieceEmpty + 8 * i; };
+    Piece *ring = reinterpret_cast<Piece *>(misc + C::kPieces);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
@@ -167,7 +429,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             mbar_init(bar_empty(i), FP8 && (i & 1) ? 4 : 2);       // both issuers; e4m3's V: the converting warps
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(bar_q(x), 4);
+            mbar_init(bar_q(x), 1);
+            mbar_init(bar_qfree(x), 1);
             mbar_init(bar_s(x), 1);
             mbar_init(bar_p(x), 4);
             mbar_init(bar_o(x), 1);
@@ -176,6 +439,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             mbar_init(bar_vempty(x), 2);
             mbar_init(bar_drain(x), 1);
         }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar_piece(i), 1);
+            mbar_init(bar_piece_free(i), C::kReaders);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -183,52 +450,80 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
         tmem_alloc(mbase + C::kTmemSlot, 512);
         tmem_relinquish();
     }
+    wait_prior_grid();
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_q + p.bs) != p.num_tokens))
+        atomicOr(p.status, SK_DEV_BAD_SEQ);
+    // found in the K and V slots' memory, before the first copy
+    Share share = find_share<C::kThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(smem),
+                                          reinterpret_cast<long long *>(misc + C::kStart));
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc + C::kTmemSlot);
+    const bool aligned = (sbase & 1023u) == 0;
+    if (!aligned && threadIdx.x == 0)
+        atomicOr(p.status, SK_DEV_INTERNAL);
+    // The next published piece; false at the end of the run, or (ok becomes false) when the wait gave up.
+    int read = 0;
+    auto next_piece = [&](Piece &pc, bool &ok) {
+        const int i = read % kRing;
+        ok = __all_sync(kFull, wait_bar(bar_piece(i), (read / kRing) & 1, abort_flag, p.wait_limit));
+        if (!ok)
+            return false;
+        pc = ring[i];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar_piece_free(i));
+        ++read;
+        return pc.s >= 0;
+    };
+    Piece pc;
 
     if (warp < 4) {
         reg_dec<C::kRegsIssue>();
         if (warp == 0) {
-            // ============================================================ copies
-            // slot i holds, in turn, K(0), V(0), K(1), V(1), ...
+            // ============================================================ K and V pages
+            // slots hold, in turn, K(0), V(0), K(1), V(1), ... of piece after piece
             if (lane == 0)
                 prefetch_tensormap(&kv_map);
-            const int page0 = t0 * C::kPagesPerTile, page_end = (L + kPage - 1) / kPage;
-            const int32_t *bt = p.block_table + (long long)s * p.bt_stride;
-            auto block_at = [&](int j) {
-                const int pg = page0 + j * C::kPagesPerTile + lane;
-                return (lane < C::kPagesPerTile && j < n && pg < page_end) ? __ldg(bt + pg) : -1;
-            };
-            int blk = block_at(0), blk1 = block_at(1);
-            int issued = 0;
+            int u = 0;
             bool ok = true;
-            for (int u = 0; u < 2 * n && ok; ++u) {
-                const int j = u >> 1, part = u & 1, i = u % C::kSlots;
-                if (u >= C::kSlots)
-                    ok = wait_bar(bar_empty(i), (u / C::kSlots - 1) & 1, abort_flag, p.wait_limit);
-                ok = __all_sync(kFull, ok);
-                if (!ok)
-                    break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar_full(i), C::kSlotBytes);
-                __syncwarp();
-                if (lane < C::kPagesPerTile) {
-                    int grp = -2;                    // whole box out of bounds: zero fill
-                    if (page0 + j * C::kPagesPerTile + lane < page_end) {
-                        if (blk >= 0 && blk < p.num_blocks)
-                            grp = (blk * p.H_kv + h) * 2;
-                        else
-                            atomicOr(p.status, SK_DEV_BAD_BLOCK);
+            while (ok && next_piece(pc, ok)) {
+                const int page_end = (pc.L + kPage - 1) / kPage;
+                const int32_t *bt = p.block_table + (long long)pc.s * p.bt_stride;
+                auto block_at = [&](int t) {
+                    const int pg = t * C::kPagesPerTile + lane;
+                    return (lane < C::kPagesPerTile && t < pc.b && pg < page_end) ? __ldg(bt + pg) : -1;
+                };
+                int blk = block_at(pc.a), blk1 = block_at(pc.a + 1);
+                for (int t = pc.a; t < pc.b && ok; ++t) {
+                    const int blk2 = block_at(t + 2);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part, ++u) {
+                        const int i = u % C::kSlots;
+                        if (u >= C::kSlots)
+                            ok = wait_bar(bar_empty(i), (u / C::kSlots - 1) & 1, abort_flag, p.wait_limit);
+                        ok = __all_sync(kFull, ok);
+                        if (!ok)
+                            break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(bar_full(i), C::kSlotBytes);
+                        __syncwarp();
+                        if (lane < C::kPagesPerTile) {
+                            int grp = -2;            // whole box out of bounds: zero fill
+                            if (t * C::kPagesPerTile + lane < page_end) {
+                                if (blk >= 0 && blk < p.num_blocks)
+                                    grp = (blk * p.H_kv + pc.h) * 2;
+                                else
+                                    atomicOr(p.status, SK_DEV_BAD_BLOCK);
+                            }
+                            tma_load_4d(sbase + i * C::kSlotBytes + lane * 2 * C::kGroupBytes, &kv_map, 0, 0,
+                                        part * (FP8 ? 1 : 2), grp, bar_full(i));
+                        }
                     }
-                    tma_load_4d(sbase + i * C::kSlotBytes + lane * 2 * C::kGroupBytes, &kv_map, 0, 0,
-                                part * (FP8 ? 1 : 2), grp, bar_full(i));
-                }
-                issued = u + 1;
-                if (part) {
                     blk = blk1;
-                    blk1 = block_at(j + 2);
+                    blk1 = blk2;
                 }
             }
             if (!ok) {
@@ -237,88 +532,159 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                     atomicOr(p.status, SK_DEV_TIMEOUT);
             }
             // every copy issued lands before the CTA exits
-            for (int u = issued > C::kSlots ? issued - C::kSlots : 0; u < issued; ++u)
-                mbar_wait_bounded(bar_full(u % C::kSlots), (u / C::kSlots) & 1, nullptr, kDrainLimit);
+            for (int t = u > C::kSlots ? u - C::kSlots : 0; t < u; ++t)
+                wait_bar(bar_full(t % C::kSlots), (t / C::kSlots) & 1, nullptr, kDrainLimit);
+        } else if (warp == 3) {
+            // ============================================================ the pieces, and their Q tiles
+            if (!aligned) {
+                share.s = p.bs;
+                share.dealt = 0;
+            }
+            Walk walk(p, share);
+            Piece *shared = p.shared + 2 * blockIdx.x;   // this run's pieces of units that others have a part of
+            if (lane < 2)
+                shared[lane].s = -1;
+            __syncwarp();
+            int used[2] = {0, 0};                        // Q tiles copied
+            bool ok = true, more = true;
+            for (int k = 0; ok && more; ++k) {
+                more = walk.next(pc);
+                if (!more)
+                    pc.s = -1;
+                if (k >= kRing)
+                    ok = wait_bar(bar_piece_free(k % kRing), (k / kRing - 1) & 1, abort_flag, p.wait_limit);
+                ok = __all_sync(kFull, ok);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    ring[k % kRing] = pc;
+                    if (more && (pc.a > 0 || pc.b < pc.t))
+                        shared[pc.a > 0 ? 0 : 1] = pc;
+                    mbar_arrive(bar_piece(k % kRing));
+                }
+                __syncwarp();
+                if (!more)
+                    break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || (x ? pc.nB : pc.nA) == 0)
+                        continue;
+                    if (used[x] > 0)
+                        ok = wait_bar(bar_qfree(x), (used[x] - 1) & 1, abort_flag, p.wait_limit);
+                    ok = __all_sync(kFull, ok);
+                    if (ok && lane == 0) {
+                        int j0, i0;
+                        tile_origin(p, 2 * pc.unit + x, j0, i0);
+                        const uint32_t dst = sbase + C::kOffQ + x * C::kQTile;
+                        mbar_arrive_expect_tx(bar_q(x), (uint32_t)(p.gb * p.tpb * 256));
+                        tma_load_3d(dst, &q_map, 0, pc.h * p.G + i0, pc.tok0 + j0, bar_q(x));
+                        tma_load_3d(dst + kRows * 128, &q_map, FP8 ? 128 : 64, pc.h * p.G + i0, pc.tok0 + j0, bar_q(x));
+                    }
+                    __syncwarp();
+                    used[x] += ok ? 1 : 0;
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                if (lane == 0)
+                    atomicOr(p.status, SK_DEV_TIMEOUT);
+            }
+            for (int x = 0; x < 2; ++x)
+                if (used[x] > 0)
+                    wait_bar(bar_q(x), (used[x] - 1) & 1, nullptr, kDrainLimit);
         } else if (warp <= 2) {
             // ============================================================ products of row tile x
             constexpr uint32_t idesc_qk = FP8 ? idesc_e4m3_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
             constexpr uint32_t idesc_pv = FP8 ? idesc_f16_f32(kRows, kHeadDim, 0, 1)
                                               : idesc_bf16_f32(kRows, kHeadDim, 0, 1);
             const int x = warp - 1;
-            const int nx = x ? nB : nA;
             const uint64_t d_k0 = smem_desc_sw128(sbase, 16, C::kGroupBytes);       // K-major K
             const uint64_t d_v0 = smem_desc_sw128(sbase + (FP8 ? C::kOffV : 0), 1024, 2048);    // dimension-major V
             const uint64_t d_q = smem_desc_sw128(sbase + C::kOffQ + x * C::kQTile, 16, 1024);   // K-major Q
             const uint32_t sd = tmem + kColS + x * 128, od = tmem + kColO + x * 128;
             auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
             bool ok = true;
+            int u = 0, tiles = 0;                    // slots and key tiles before this piece
+            int mine = 0, pieces = 0;                // this row tile's key tiles and pieces so far
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 if (ok)
                     ok = wait_bar(bar, parity, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 return ok;
             };
-            auto wait_slot = [&](int u) { return wait(bar_full(u % C::kSlots), (u / C::kSlots) & 1); };
+            auto wait_slot = [&](int i) { return wait(bar_full(i % C::kSlots), (i / C::kSlots) & 1); };
             // passes the turn with half of the products still to issue: the other issuer wakes up meanwhile
             auto pass_turn = [&]() {
                 if (lane == 0)
                     mbar_arrive(bar_turn(1 - x));
                 __syncwarp();
             };
-            auto qk = [&](int j) {
-                const uint32_t so = (uint32_t)(2 * j % C::kSlots) * C::kSlotBytes;
+            auto qk = [&](int slot, bool pass) {
+                const uint64_t k0 = adv(d_k0, (uint32_t)(slot % C::kSlots) * C::kSlotBytes);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int h = 0; h < 2; ++h) {
                     if constexpr (FP8)
-                        mma_f8_ss_warp(sd, adv(d_q, (k >> 2) * (kRows * 128) + (k & 3) * 32),
-                                       adv(d_k0, so + (k & 3) * 32), idesc_qk, k > 0 ? 1u : 0u);
+                        mma4_f8_ss<2, 2>(sd, adv(d_q, h * (kRows * 128)), k0, idesc_qk, h);
                     else
-                        mma_f16_ss_warp(sd, adv(d_q, (k >> 2) * (kRows * 128) + (k & 3) * 32),
-                                        adv(d_k0, so + (k >> 2) * 1024 + (k & 3) * 32), idesc_qk, k > 0 ? 1u : 0u);
-                    if (k == 3 && j > 0)
+                        mma4_f16_ss<2, 2>(sd, adv(d_q, h * (kRows * 128)), adv(k0, h * 1024), idesc_qk, h);
+                    if (h == 0 && pass)
                         pass_turn();
                 }
                 mma_commit_warp(bar_s(x));
             };
             auto pv = [&](int j) {
-                const uint32_t so = FP8 ? (uint32_t)(j & 1) * C::kVBytes : (uint32_t)((2 * j + 1) % C::kSlots) * C::kSlotBytes;
+                const uint64_t v0 = adv(d_v0, FP8 ? (uint32_t)((tiles + j) & 1) * C::kVBytes
+                                                  : (uint32_t)((u + 2 * j + 1) % C::kSlots) * C::kSlotBytes);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16_ts_warp(od, sd + (k >> 2) * 64 + (k & 3) * 8, adv(d_v0, so + k * 4096), idesc_pv,
-                                    (j > 0 || k > 0) ? 1u : 0u);
+                for (int h = 0; h < 2; ++h)
+                    mma4_f16_ts<8, 256>(od, sd + h * 64, adv(v0, h * 16384), idesc_pv, j > 0 || h > 0);
             };
-            auto wait_v = [&](int j) { return FP8 ? wait(bar_vfull(j & 1), (j >> 1) & 1) : wait_slot(2 * j + 1); };
+            auto wait_v = [&](int j) {
+                return FP8 ? wait(bar_vfull((tiles + j) & 1), ((tiles + j) >> 1) & 1) : wait_slot(u + 2 * j + 1);
+            };
             // Both issuers pass every slot on, also those of tiles that only the other multiplies (they wait for them
             // all the same, so that neither is a turn of the ring ahead).
-            if (n > 0 && (nx == 0 || wait(bar_q(x), 0)) && wait_slot(0)) {
-                tc_fence_after();
-                if (nx > 0)
-                    qk(0);
-                mma_commit_warp(bar_empty(0));
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                // what has to have landed is checked while the softmax still works on the tile
-                if (!wait_v(j) || (j + 1 < n && !wait_slot(2 * j + 2)))
+            while (ok && next_piece(pc, ok)) {
+                const int n = pc.b - pc.a, nx = x ? pc.nB : pc.nA;
+                if (n == 0)
+                    continue;
+                if (nx > 0 && !wait(bar_q(x), pieces & 1))
                     break;
-                if (j < nx) {
-                    // the row tiles take turns, so that one's softmax runs beside the other's products
-                    if (x == 0 ? (j > 0 && j - 1 < nB && !wait(bar_turn(0), (j - 1) & 1))
-                               : (j < nA && !wait(bar_turn(1), j & 1)))
+                for (int j = -1; j < n && ok; ++j) {
+                    // what has to have landed is checked while the softmax still works on the tile
+                    if ((j >= 0 && !wait_v(j)) || (j + 1 < n && !wait_slot(u + 2 * j + 2)))
                         break;
-                    if (!wait(bar_p(x), j & 1))
-                        break;
+                    if (j >= 0) {
+                        // The row tiles take turns, so that one's softmax runs beside the other's products: A's products
+                        // of a tile come after B's of the tile before, B's after A's of the same.  A row tile that has
+                        // none there passes its turn on, so that neither is ever two turns ahead (a barrier shows only
+                        // whether the last turn of a parity is over).
+                        if ((x || tiles + j > 0) && !wait(bar_turn(x), (tiles + j - 1 + x) & 1))
+                            break;
+                        if (j < nx && !wait(bar_p(x), (mine + j) & 1))
+                            break;
+                    }
                     tc_fence_after();
-                    pv(j);
+                    if (j >= 0 && j < nx)
+                        pv(j);
                     if (j + 1 < nx) {
-                        qk(j + 1);
-                    } else {
-                        mma_commit_warp(bar_o(x));
+                        qk(u + 2 * j + 2, j >= 0);
+                        if (j + 2 == nx)
+                            mma_commit_warp(bar_qfree(x));
+                    } else if (j >= 0) {
+                        if (j + 1 == nx)
+                            mma_commit_warp(bar_o(x));
                         pass_turn();
                     }
+                    if (j >= 0)
+                        mma_commit_warp(FP8 ? bar_vempty((tiles + j) & 1) : bar_empty((u + 2 * j + 1) % C::kSlots));
+                    if (j + 1 < n)
+                        mma_commit_warp(bar_empty((u + 2 * j + 2) % C::kSlots));
                 }
-                mma_commit_warp(FP8 ? bar_vempty(j & 1) : bar_empty((2 * j + 1) % C::kSlots));
-                if (j + 1 < n)
-                    mma_commit_warp(bar_empty((2 * j + 2) % C::kSlots));
+                u += 2 * n;
+                tiles += n;
+                mine += nx;
+                pieces += nx > 0 ? 1 : 0;
             }
             if (!ok) {
                 *abort_flag = 1;
@@ -327,7 +693,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             }
             // every product completes before TMEM is freed and shared memory is left
             mma_commit_warp(bar_drain(x));
-            mbar_wait_bounded(bar_drain(x), 0, nullptr, kDrainLimit);
+            wait_bar(bar_drain(x), 0, nullptr, kDrainLimit);
         }
         __syncwarp();
     } else if (!FP8 || warp < 12) {
@@ -336,78 +702,48 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
         const int x = (warp >> 2) - 1;
         const int quarter = warp & 3;
         const int tau = quarter * 32 + lane;                       // row of the tile, TMEM lane
-        const int nx = x ? nB : nA;
-        const int rows = x ? rowsB : rowsA;
-        const int rx0 = row0 + x * kRows;                          // first row of the tile
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + kColS + x * 128 + lane_off, to = tmem + kColO + x * 128 + lane_off;
-        float *crow = reinterpret_cast<float *>(misc + C::kCrow) + x * kRows;
-
-        // ---- Q rows of this warp into shared memory (K-major, 128-byte swizzle); zeros past the rows
-        uint8_t *qs = smem + C::kOffQ + x * C::kQTile;
-        if (nx > 0) {
-            if constexpr (!FP8) {
-                uint4 v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int r = quarter * 32 + k * 2 + (lane >> 4), unit = lane & 15;
-                    v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows) {
-                        const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
-                        v[k] = __ldg(reinterpret_cast<const uint4 *>(
-                            p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + unit * 8));
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int r = quarter * 32 + k * 2 + (lane >> 4), unit = lane & 15;
-                    *reinterpret_cast<uint4 *>(qs + (unit >> 3) * (kRows * 128) + r * 128 +
-                                               (((unit & 7) ^ (r & 7)) << 4)) = v[k];
-                }
-            } else {
-                uint2 raw[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const int r = quarter * 32 + k;
-                    raw[k] = make_uint2(0u, 0u);
-                    if (r < rows) {
-                        const int j = (rx0 + r) / p.G, i = rx0 + r - j * p.G;
-                        raw[k] = __ldg(reinterpret_cast<const uint2 *>(
-                            p.q + ((long long)(tok0 + j) * p.H_q + h * p.G + i) * kHeadDim + lane * 4));
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const int r = quarter * 32 + k;
-                    uint32_t hi, lo;
-                    int e;
-                    split_q_row(raw[k], hi, lo, e);
-                    const uint32_t off = (uint32_t)(r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
-                    *reinterpret_cast<uint32_t *>(qs + off) = hi;
-                    *reinterpret_cast<uint32_t *>(qs + kRows * 128 + off) = lo;
-                    if (lane == 0)
-                        crow[r] = p.score_scale_log2 * ldexpf(1.f, -e);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_q(x));
+        int mine = 0, pieces = 0, u = 0;                           // this row tile's key tiles and pieces, slots so far
+        bool failed = false;
+        while (!failed) {
+        // The piece stays in the ring, to be read again for the output, until that is written: in registers it would
+        // spill the scores.
+        const int place = read % kRing;
+        volatile Piece *pc = ring + place;
+        if (!__all_sync(kFull, wait_bar(bar_piece(place), (read / kRing) & 1, abort_flag, p.wait_limit))) {
+            failed = true;
+            break;
         }
-        const float c = FP8 ? (nx > 0 ? crow[tau] : 0.f) : p.score_scale_log2;
-
-        const int r = rx0 + tau;                                   // this thread's row
-        const int jq = r / p.G, iq = r - jq * p.G;
-        const bool live = tau < rows;
-        const int limit = live ? visible_keys(L, q_len, jq, p.causal) : 0;
-        const int least = __reduce_min_sync(kFull, limit);         // keys that every row of the warp sees
+        if (pc->s < 0)
+            break;
+        ++read;
+        // this row: its token, and its head in the group
+        auto row_at = [&](int &j, int &i) {
+            tile_origin(p, 2 * pc->unit + x, j, i);
+            const int jj = tau / p.gb;
+            j += jj;
+            i += tau - jj * p.gb;
+            return jj < p.tpb && j < pc->q_len && i < p.G;
+        };
+        const int nx = x ? pc->nB : pc->nA;
+        const int first_key = pc->a * kKeys, L = pc->L;
+        int limit, least;                                          // keys that the row sees; that all of the warp's see
+        float c = p.score_scale_log2;
+        {
+            int j, i;
+            const bool live = row_at(j, i);
+            limit = live ? visible_keys(L, pc->q_len, j, p.causal) : 0;
+            least = __reduce_min_sync(kFull, live ? limit : INT_MAX);        // what padding rows hold is never used
+            if (FP8 && live)
+                c *= __ldg(p.q_scale + (long long)(pc->tok0 + j) * p.H_q + pc->h * p.G + i);
+        }
         float m_ref = -CUDART_INF_F;
         bool anchored = false;                                     // every row that sees a key has a reference
         float2 l2 = make_float2(0.f, 0.f);
-        bool failed = false;
         for (int j = 0; j < nx; ++j) {
-            const int key0 = (t0 + j) * kKeys;
-            bool ok = wait_bar(bar_s(x), j & 1, abort_flag, p.wait_limit);
+            const int key0 = first_key + j * kKeys;
+            bool ok = wait_bar(bar_s(x), (mine + j) & 1, abort_flag, p.wait_limit);
             ok = __all_sync(kFull, ok);
             if (!ok) {
                 failed = true;
@@ -459,21 +795,26 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                     }
                 }
             };
-            // only a row's first scores need their maximum before they are exponentiated (see below)
+            // A row's first scores give it a reference: the largest of the first 16 will do (see below).
             if (!anchored) {
-                if (__any_sync(kFull, m_ref == -CUDART_INF_F && lim > 0))
-                    raise(tile_top(), j > 0);
+                if (__any_sync(kFull, m_ref == -CUDART_INF_F && lim > 0)) {
+                    float top = v[0];
+#pragma unroll
+                    for (int i = 1; i < 15; i += 2)
+                        top = fmax3(top, v[i], v[i + 1]);
+                    raise(fmaxf(top, v[15]) * c, j > 0);
+                }
                 anchored = !__any_sync(kFull, m_ref == -CUDART_INF_F && limit > 0);
             }
             // rows past the sequence's end in its last page hold anything, and 0 * NaN would reach O: their V
             // becomes zeros, before either row tile multiplies it
             if (!FP8 && L < key0 + kKeys && (L & (kPage - 1)) != 0) {
-                ok = mbar_wait_bounded(bar_full((2 * j + 1) % C::kSlots), ((2 * j + 1) / C::kSlots) & 1, abort_flag,
-                                       p.wait_limit);
+                const int i = u + 2 * j + 1;
+                ok = wait_bar(bar_full(i % C::kSlots), (i / C::kSlots) & 1, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 const int tok = key0 + tau;
                 if (ok && tok >= L && tok < (L + kPage - 1) / kPage * kPage) {
-                    uint8_t *row = smem + (2 * j + 1) % C::kSlots * C::kSlotBytes + (tau >> 3) * C::kGroupBytes +
+                    uint8_t *row = smem + i % C::kSlots * C::kSlotBytes + (tau >> 3) * C::kGroupBytes +
                                    (tau & 7) * 128;
 #pragma unroll
                     for (int cc = 0; cc < C::kGroupBytes / 1024; ++cc)
@@ -510,7 +851,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
                     tmem_st32_u<16>(ts + (q >> 1) * 64 + (q & 1) * 16, pk);
                 }
                 h2 = fadd2(h2, g2);
-                if (again || !__any_sync(kFull, !(h2.x + h2.y <= C::kSumMost)))
+                if (again || !__any_sync(kFull, limit > 0 && !(h2.x + h2.y <= C::kSumMost)))
                     break;
                 tmem_wait_st();
                 raise(tile_top(), j > 0);
@@ -522,53 +863,79 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
             if (lane == 0)
                 mbar_arrive(bar_p(x));
         }
-        if (!failed && nx > 0) {
-            bool ok = mbar_wait_bounded(bar_o(x), 0, abort_flag, p.wait_limit);
-            failed = !__all_sync(kFull, ok);
-        }
-        if (failed) {
-            *abort_flag = 1;
-        } else if (rows > 0) {
+        if (failed)
+            break;
+        if (nx > 0) {
+            const bool ok = wait_bar(bar_o(x), pieces & 1, abort_flag, p.wait_limit);
+            if (!__all_sync(kFull, ok)) {
+                failed = true;
+                break;
+            }
             tc_fence_after();
-            const float l = l2.x + l2.y;
-            const long long qrow = (long long)(tok0 + jq) * p.H_q + h * p.G + iq;
-            const long long slot = ((long long)(tok0 + jq) * p.nsplit + g) * p.H_q + h * p.G + iq;
-            const float mul = p.nsplit > 1 ? p.v_scale : (l == 0.f ? 0.f : p.v_scale / l);
+        }
+        // ---- the row's output, or its partial state.  A lane's row is transposed within quads of lanes, so that a
+        // warp's store writes 64 contiguous bytes of eight rows (with 16 bytes of 32 rows it took 5000 cycles)
+        int jr, ir;
+        const bool live = row_at(jr, ir);
+        const bool whole = pc->a == 0 && pc->b == pc->t;
+        const int qrow = live ? (pc->tok0 + jr) * p.H_q + pc->h * p.G + ir : -1;
+        // a run has at most one piece that does not start its unit, and one more that does not end it
+        const int part = (2 * blockIdx.x + (pc->a > 0 ? 0 : 1)) * (2 * kRows) + x * kRows + tau;
+        const float l = l2.x + l2.y;
+        const float mul = !whole ? p.v_scale : (l == 0.f ? 0.f : p.v_scale / l);
+        int to_row[4];                                             // the quad's rows
 #pragma unroll
-            for (int cc = 0; cc < 128; cc += 32) {
-                float o[32];
-                if (nx > 0) {
-                    tmem_ld32<32>(to + cc, o);
-                    tmem_wait_ld();
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = (nx > 0 && !(l == 0.f)) ? o[i] * mul : 0.f;
-                if (!live)
-                    continue;
-                if (p.nsplit > 1) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4 *>(p.part_o + slot * kHeadDim + cc + i) =
-                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4 *>(p.out + qrow * kHeadDim + cc + i) =
-                            make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
-                                       pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
-                }
+        for (int i = 0; i < 4; ++i)
+            to_row[i] = __shfl_sync(kFull, whole || !live ? qrow : part, (lane & ~3) + i);
+        // a row that saw nothing is zero, whatever V holds
+        const bool empty = __any_sync(kFull, nx == 0 || l == 0.f);
+        uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out) : reinterpret_cast<uint8_t *>(p.part_o);
+        const int row_bytes = whole ? kHeadDim * 2 : kHeadDim * 4;
+#pragma unroll 1
+        for (int cc = 0, at = (lane & 3) * 16; at < row_bytes; cc += whole ? 32 : 16, at += 64) {
+            // 64 bytes of every row: 32 dimensions rounded, or 16 as they are
+            float o[32];
+            if (nx > 0) {
+                tmem_ld32<16>(to + cc, o);
+                if (whole)
+                    tmem_ld32<16>(to + cc + 16, o + 16);
+                tmem_wait_ld();
             }
-            if (live) {
-                const float ln2 = 0.69314718055994531f;
-                if (p.nsplit > 1) {
-                    p.part_m[slot] = l > 0.f ? m_ref * ln2 : -CUDART_INF_F;
-                    p.part_l[slot] = l;
-                } else if (p.lse != nullptr) {
-                    p.lse[qrow] = l == 0.f ? -CUDART_INF_F : m_ref * ln2 + logf(l);
-                }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                o[i] = empty && (nx == 0 || l == 0.f) ? 0.f : o[i] * mul;
+            uint4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = whole ? make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                          pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]))
+                             : make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                                          __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+            quad_transpose(w, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (to_row[i] >= 0)
+                    *reinterpret_cast<uint4 *>(dst + (long long)to_row[i] * row_bytes + at) = w[i];
+        }
+        if (live) {
+            if (!whole) {
+                p.part_m[part] = m_ref;
+                p.part_l[part] = l;
+            } else if (p.lse != nullptr) {
+                p.lse[qrow] = l == 0.f ? -CUDART_INF_F : m_ref * 0.69314718055994531f + logf(l);
             }
         }
+        // the next piece's first product into O waits for its P, which this thread writes after these reads
+        tc_fence_before();
+        mine += nx;
+        pieces += nx > 0 ? 1 : 0;
+        u += 2 * (pc->b - pc->a);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar_piece_free(place));
+        }
+        if (failed)
+            *abort_flag = 1;
     } else {
         // ================================================================ e4m3: V codes to f16 (exact)
         reg_dec<C::kRegsConvert>();
@@ -577,23 +944,27 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
         // dimensions become units 2 u and 2 u + 1 of f16, the upper half of the lanes storing the odd one first, so
         // that a store's lanes meet no bank twice
         const int u = lane & 7, sub = lane >> 3;
-        for (int j = 0; j < n; ++j) {
-            const int slot = (2 * j + 1) % C::kSlots, vb = j & 1;
-            bool ok = wait_bar(bar_full(slot), ((2 * j + 1) / C::kSlots) & 1, abort_flag, p.wait_limit);
-            if (ok && j >= 2)
-                ok = wait_bar(bar_vempty(vb), ((j >> 1) - 1) & 1, abort_flag, p.wait_limit);
-            if (!__all_sync(kFull, ok)) {
+        int v = 0;                                                 // key tiles so far
+        bool ok = true;
+        while (ok && next_piece(pc, ok))
+        for (int tile = pc.a; tile < pc.b; ++tile, ++v) {
+            const int slot = (2 * v + 1) % C::kSlots, vb = v & 1;
+            ok = wait_bar(bar_full(slot), ((2 * v + 1) / C::kSlots) & 1, abort_flag, p.wait_limit);
+            if (ok && v >= 2)
+                ok = wait_bar(bar_vempty(vb), ((v >> 1) - 1) & 1, abort_flag, p.wait_limit);
+            ok = __all_sync(kFull, ok);
+            if (!ok) {
                 *abort_flag = 1;
                 break;
             }
             const uint8_t *src = smem + slot * C::kSlotBytes;
             uint8_t *dst = smem + C::kOffV + vb * C::kVBytes;
-            const int key0 = (t0 + j) * kKeys;
+            const int key0 = tile * kKeys;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int t = w * 32 + k * 4 + sub, x8 = t & 7;
                 uint4 a = *reinterpret_cast<const uint4 *>(src + (t >> 3) * 1024 + x8 * 128 + ((u ^ x8) << 4));
-                if (key0 + t >= L)                                 // past the end the page holds anything
+                if (key0 + t >= pc.L)                               // past the end the page holds anything
                     a = make_uint4(0u, 0u, 0u, 0u);
                 const uint4 lo = make_uint4(f16x2_of_e4m3(a.x), f16x2_of_e4m3(a.x >> 16), f16x2_of_e4m3(a.y),
                                             f16x2_of_e4m3(a.y >> 16));
@@ -621,8 +992,91 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefillParams p
     }
 }
 
+// Joins the pieces of the units that several runs share: block (run, part) those of the unit whose last piece is run's
+// first.  Its other pieces are the first ones of the runs before, back to the run that the unit starts in, whose last piece
+// it is.  They are taken in key order, whatever the timing of the runs.  With M = max m_i over the pieces with l_i > 0:
+//     out = sum o_i 2^(m_i - M) / sum l_i 2^(m_i - M)
+constexpr int kJoinThreads = 256, kJoinParts = 16;
+constexpr int kMaxRuns = 1024;                       // runs (SMs) at most
+constexpr int kJoinRows = 2 * kRows / kJoinParts / (kJoinThreads / 32);      // rows of one warp
+
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillParams p)
+{
+    __shared__ int slots[kMaxRuns], count;
+    wait_prior_grid();
+    const int index = blockIdx.x / kJoinParts, part = blockIdx.x % kJoinParts;
+    const Piece pc = p.shared[2 * index];
+    if (pc.s < 0 || pc.b != pc.t)
+        return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        // from this run back, 32 at a time, until a piece that starts the unit; then in key order
+        int n = 0;
+        for (int r0 = index; r0 >= 0; r0 -= 32) {
+            const int r = r0 - lane;
+            const bool last = r >= 0 && r < index && p.shared[2 * r + 1].s >= 0;
+            const uint32_t ends = __ballot_sync(kFull, last);
+            const int stop = ends ? __ffs(ends) - 1 : 31;
+            const bool has = r >= 0 && lane <= stop && (last || p.shared[2 * r].s >= 0);
+            const uint32_t all = __ballot_sync(kFull, has);
+            if (has)
+                slots[n + __popc(all & ((1u << lane) - 1u))] = 2 * r + (last ? 1 : 0);
+            n += __popc(all);
+            if (ends)
+                break;
+        }
+        if (lane == 0)
+            count = n;
+    }
+    __syncthreads();
+    const int pieces = count;
+    const int tok0 = __ldg(p.cu_q + pc.s);
+    for (int k = 0; k < kJoinRows; ++k) {
+        const int row = (part * (kJoinThreads / 32) + warp) * kJoinRows + k;     // of the unit's 256
+        const int x = row / kRows, tau = row % kRows;
+        int j0, i0;
+        tile_origin(p, 2 * pc.unit + x, j0, i0);
+        const int jj = tau / p.gb, ii = tau - jj * p.gb;
+        if (!(jj < p.tpb && j0 + jj < pc.q_len && i0 + ii < p.G))
+            continue;                                // uniform in the warp
+        float M = -CUDART_INF_F, lam = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kAtOnce = 8;
+        for (int g0 = 0; g0 < pieces; g0 += kAtOnce) {
+            float m[kAtOnce], l[kAtOnce];
+            float4 o[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const long long slot = (long long)slots[max(pieces - 1 - g0 - i, 0)] * (2 * kRows) + row;
+                m[i] = __ldg(p.part_m + slot);
+                l[i] = g0 + i < pieces ? __ldg(p.part_l + slot) : 0.f;
+                o[i] = __ldg(reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim) + lane);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (l[i] == 0.f)
+                    continue;
+                const float mn = fmaxf(M, m[i]), wa = M == -CUDART_INF_F ? 0.f : exp2f(M - mn), wb = exp2f(m[i] - mn);
+                M = mn;
+                lam = lam * wa + l[i] * wb;
+                acc.x = acc.x * wa + o[i].x * wb;
+                acc.y = acc.y * wa + o[i].y * wb;
+                acc.z = acc.z * wa + o[i].z * wb;
+                acc.w = acc.w * wa + o[i].w * wb;
+            }
+        }
+        const float inv = lam == 0.f ? 0.f : 1.f / lam;
+        const long long qrow = (long long)(tok0 + j0 + jj) * p.H_q + pc.h * p.G + i0 + ii;
+        *reinterpret_cast<uint2 *>(p.out + qrow * kHeadDim + lane * 4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (lane == 0 && p.lse != nullptr)
+            p.lse[qrow] = lam == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(lam);
+    }
+}
+
 template <bool FP8>
-cudaError_t launch_t(const CUtensorMap &map, const PrefillParams &p, cudaStream_t stream)
+cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const PrefillParams &p, int runs,
+                     cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                PCfg<FP8>::kSmemBytes);
@@ -635,8 +1089,8 @@ cudaError_t launch_t(const CUtensorMap &map, const PrefillParams &p, cudaStream_
     }();
     if (regs < PCfg<FP8>::kRegsLaunch)
         return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)p.nsplit * p.row_blocks * p.H_kv * p.bs);
-    return launch_pdl(prefill_kernel<FP8>, grid, dim3(PCfg<FP8>::kThreads), PCfg<FP8>::kSmemBytes, stream, map, p);
+    return launch_pdl(prefill_kernel<FP8>, dim3((unsigned)runs), dim3(PCfg<FP8>::kThreads), PCfg<FP8>::kSmemBytes,
+                      stream, kv_map, q_map, p);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -693,42 +1147,58 @@ cudaError_t encode_q_map(CUtensorMap *map, const void *q, long long num_tokens, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// CTAs that share the keys of a row block: the number with the least estimated time.  A CTA takes kFixed to start and
-// finish and kTile per key tile (us); the GPU works off `units` row blocks (at most; with ragged query lengths the
-// tokens' own count bounds them) num_sms at a time, the last round half full on average; a split adds the merge, whose
-// partial states (520 bytes per row, head and split) are written and read.
-int prefill_nsplit(int bs, int num_tokens, int max_q_len, int H_q, int H_kv, int max_seq_len, int num_sms)
+// Bytes of the workspace: two pieces of 256 rows (o, m, l) per run with what they are pieces of, and for e4m3 pages Q in
+// two terms.
+long long prefill_workspace_bytes(int num_tokens, int H_q, int kv_dtype, int num_sms)
 {
-    constexpr double kFixed = 4.0, kTile = 1.25, kMerge = 3.0, kBytesPerUs = 5e6;
-    const long long G = H_q / H_kv;
-    const long long most = (G * max_q_len + kPrefillRows - 1) / kPrefillRows * bs;
-    const long long have = (G * num_tokens + kPrefillRows - 1) / kPrefillRows + bs;
-    const double units = (double)(most < have ? most : have) * H_kv;
-    const int tiles = (max_seq_len + kKeys - 1) / kKeys;
-    int best = 1;
-    double best_t = 1e300;
-    for (int n = 1; n <= 64 && (n == 1 || n <= tiles); ++n) {
-        const double cta = kFixed + kTile * ((tiles + n - 1) / n), rounds = units * n / num_sms;
-        double t = cta * (rounds <= 1.0 ? 1.0 : rounds + 0.5);
-        if (n > 1)
-            t += kMerge + 2.0 * n * num_tokens * H_q * 520.0 / kBytesPerUs;
-        if (t < best_t * (n > 1 ? 0.97 : 1.0)) {
-            best_t = t;
-            best = n;
-        }
-    }
-    return best;
+    const long long parts = 2LL * num_sms * (2 * kRows * (kHeadDim + 2) * 4 + (long long)sizeof(PrefillPiece));
+    return parts + (kv_dtype == SK_KV_FP8_E4M3 ? (long long)num_tokens * H_q * (2 * kHeadDim + 4) : 0);
 }
 
-cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, cudaStream_t stream)
+cudaError_t launch_prefill(const PrefillParams &params, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,
+                           cudaStream_t stream)
 {
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
-    CUtensorMap map;
-    // one box: K (or V) of one page and head
-    const cudaError_t e = encode_page_map(&map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 1 : 2);
+    PrefillParams p = params;
+    p.gb = p.G < kRows ? p.G : kRows;
+    p.nsub = (p.G + p.gb - 1) / p.gb;
+    p.tpb = kRows / p.gb;
+    const long long slots = 2LL * num_sms * 2 * kRows;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_m = p.part_o + slots * kHeadDim;
+    p.part_l = p.part_m + slots;
+    p.shared = reinterpret_cast<PrefillPiece *>(p.part_l + slots);
+    const void *q = p.q;
+    if (fp8) {
+        uint8_t *codes = reinterpret_cast<uint8_t *>(p.shared + 2 * num_sms);
+        const long long rows = (long long)p.num_tokens * p.H_q;
+        const cudaError_t e = launch_split_q(p.q, rows, codes, stream);
+        if (e != cudaSuccess)
+            return e;
+        q = codes;
+        p.q_scale = reinterpret_cast<const float *>(codes + rows * 256);
+    }
+    CUtensorMap kv_map, q_map;
+    // one box of the pages: K (or V) of one page and head
+    cudaError_t e = encode_page_map(&kv_map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 1 : 2);
+    if (e == cudaSuccess)
+        e = encode_q_map(&q_map, q, p.num_tokens, p.H_q, fp8, p.gb, p.tpb);
     if (e != cudaSuccess)
         return e;
-    return fp8 ? launch_t<true>(map, p, stream) : launch_t<false>(map, p, stream);
+    // A run per SM, but none of less than two key tiles on average: the number of units and of key tiles is bounded by
+    // the tokens and by max_seq_len.
+    const long long per_seq = ((long long)(p.max_q_len + p.tpb - 1) / p.tpb * p.nsub + 1) / 2 * p.bs;
+    const long long by_tokens = ((long long)(p.num_tokens + p.tpb - 1) / p.tpb * p.nsub + 1) / 2 + p.bs;
+    const long long units = (per_seq < by_tokens ? per_seq : by_tokens) * p.H_kv;
+    const long long tiles = (max_seq_len + kKeys - 1) / kKeys;
+    long long runs = units * (tiles < 2 ? 1 : tiles / 2);
+    runs = runs < 1 ? 1 : (runs < num_sms ? runs : num_sms);
+    runs = runs < kMaxRuns ? runs : kMaxRuns;
+    p.deal = (double)p.bs * max_seq_len * p.H_kv * (fp8 ? 256 : 512) > kL2Share ? 1 : 0;
+    e = fp8 ? launch_t<true>(kv_map, q_map, p, (int)runs, stream) : launch_t<false>(kv_map, q_map, p, (int)runs, stream);
+    if (e != cudaSuccess || runs == 1)
+        return e;
+    return launch_pdl(prefill_join_kernel, dim3((unsigned)runs * kJoinParts), dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace sk

@@ -152,11 +152,11 @@ def test_binding_checks_shapes_before_raw_pointers(sk):
 def test_prefill_refusals(sk):
     call = caller(sk.lib().sk_paged_prefill_attn, dict(
         q=FAKE, kv=FAKE, dt=0, ks=1.0, vs=1.0, bt=FAKE, stride=10, nb=100, page=16, lens=FAKE, cu=FAKE, bs=4, nt=16,
-        mq=4, hq=32, hkv=2, d=128, scale=0.088, causal=1, n=1, po=None, pm=None, pl=None, out=FAKE, lse=None, st=None))
+        mq=4, hq=32, hkv=2, d=128, scale=0.088, causal=1, mx=160, ws=FAKE, wb=1 << 30, out=FAKE, lse=None, st=None))
     for kw in (dict(q=None), dict(out=None), dict(cu=None), dict(dt=3), dict(bs=0), dict(bs=32768), dict(nt=-1),
-               dict(mq=0), dict(stride=0), dict(nb=0), dict(hq=31), dict(hkv=0), dict(n=0), dict(n=65536), dict(n=2),
+               dict(mq=0), dict(stride=0), dict(nb=0), dict(hq=31), dict(hkv=0), dict(mx=-1), dict(ws=ODD),
                dict(scale=0.0), dict(scale=float("inf")), dict(dt=1, ks=0.0), dict(dt=1, vs=float("nan")), dict(q=ODD),
-               dict(kv=ODD), dict(out=ODD), dict(n=2, po=ODD, pm=FAKE, pl=FAKE)):
+               dict(kv=ODD), dict(out=ODD)):
         assert call(**kw) == -1, kw
     assert call(d=64) == -3 and call(page=32) == -3
     assert call(nb=1 << 30) == -3 and call(mq=1 << 30) == -3
@@ -179,27 +179,13 @@ def test_accum_refusals(sk):
         sk.sk_accum_workspace_bytes(16, 0, 1)
 
 
-def test_prefill_splits(sk):
-    """One CTA per row block when those fill the GPU many times over; more when there are few; never more than
-    key tiles; sizes out of range are refused."""
-    assert sk.sk_prefill_nsplit(64, 64 * 4096, 4096, 32, 8, 4096, 152) == 1
-    assert sk.sk_prefill_nsplit(1, 8, 8, 32, 2, 100000, 152) >= 32
-    assert sk.sk_prefill_nsplit(1, 8, 8, 32, 2, 100, 152) == 1
-    for n in (0, 1, 128, 129, 1000):
-        assert 1 <= sk.sk_prefill_nsplit(1, 8, 8, 32, 2, n, 152) <= max(1, (n + 127) // 128)
-    for bad in ((0, 8, 8, 32, 2, 100, 152), (1, 8, 8, 31, 2, 100, 152), (1, -1, 8, 32, 2, 100, 152),
-                (1, 8, 8, 32, 2, -1, 152), (1, 8, 8, 32, 2, 100, -1)):
-        with pytest.raises(sk.SkError):
-            sk.sk_prefill_nsplit(*bad)
-
-
 def test_binding_checks_attention_shapes(sk):
     bf, i32 = torch.bfloat16, torch.int32
 
     def base(**kw):
         a = dict(q=torch.zeros(8, 8, 128, dtype=bf), kv=torch.zeros(4, 2, 16, 256, dtype=bf),
                  bt=torch.zeros(2, 3, dtype=i32), lens=torch.zeros(2, dtype=i32), cu=torch.zeros(3, dtype=i32),
-                 out=torch.zeros(8, 8, 128, dtype=bf), lse=torch.zeros(8, 8), po=None, pm=None, pl=None,
+                 out=torch.zeros(8, 8, 128, dtype=bf), lse=torch.zeros(8, 8),
                  acc=torch.zeros(4, 2, 16))
         a.update(kw)
         return a
@@ -207,7 +193,7 @@ def test_binding_checks_attention_shapes(sk):
     def prefill(**kw):
         a = base(**kw)
         return sk.sk_paged_prefill_attn(a["q"], a["kv"], a["bt"], a["lens"], a["cu"], a["out"], a["lse"], max_q_len=4,
-                                        sm_scale=0.1, part_o=a["po"], part_m=a["pm"], part_l=a["pl"])
+                                        sm_scale=0.1)
 
     def accum(**kw):
         a = base(**kw)
@@ -221,8 +207,7 @@ def test_binding_checks_attention_shapes(sk):
         for f in (prefill, accum):
             with pytest.raises(ValueError):
                 f(**kw)
-    for kw in (dict(out=torch.zeros(7, 8, 128, dtype=bf)), dict(po=torch.zeros(8, 2, 8, 128)),
-               dict(po=torch.zeros(8, 2, 8, 128), pm=torch.zeros(8, 3, 8), pl=torch.zeros(8, 2, 8))):
+    for kw in (dict(out=torch.zeros(7, 8, 128, dtype=bf)), dict(out=torch.zeros(8, 8, 128)), dict(out=None)):
         with pytest.raises(ValueError):
             prefill(**kw)
     for kw in (dict(acc=torch.zeros(4, 2, 8)), dict(acc=None), dict(lse=None)):

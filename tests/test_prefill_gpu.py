@@ -81,7 +81,7 @@ def check(b, out, lse, ref=None):
     assert bool((le <= tl[~dead]).all()), float((le / tl[~dead]).max())
 
 
-def run(b, nsplit=None, **kw):
+def run(b, **kw):
     w = b["w"]
     args = dict(max_q_len=max(1, w.max_q_len), sm_scale=w.sm_scale, k_scale=w.k_scale, v_scale=w.v_scale,
                 causal=bool(w.causal))
@@ -89,13 +89,7 @@ def run(b, nsplit=None, **kw):
     nt, hq = w.num_tokens, w.num_q_heads
     out = torch.full((nt, hq, D), float("nan"), dtype=torch.bfloat16, device=DEV)
     lse = torch.full((nt, hq), float("nan"), device=DEV)
-    if nsplit is None:
-        sk.paged_prefill_attention(b["q"], b["kv"], b["bt"], b["lens"], b["cu"], out=out, lse=lse, **args)
-    else:
-        part = [torch.full((nt, nsplit, hq) + x, float("nan"), device=DEV) for x in ((D,), (), ())] if nsplit > 1 \
-            else [None] * 3
-        sk.sk_paged_prefill_attn(b["q"], b["kv"], b["bt"], b["lens"], b["cu"], out, lse, part_o=part[0],
-                                 part_m=part[1], part_l=part[2], **args)
+    sk.paged_prefill_attention(b["q"], b["kv"], b["bt"], b["lens"], b["cu"], out=out, lse=lse, **args)
     torch.cuda.synchronize()
     return out, lse
 
@@ -115,8 +109,8 @@ SHAPES = [
 def test_against_64_bits(lens, qs, hq, hkv, causal, fp8):
     b = batch(lens, qs, hq, hkv, fp8, 31 + len(lens), causal)
     ref = reference(b)
-    for nsplit in (1, 3):
-        out, lse = run(b, nsplit)
+    for most in (0, None):                        # one run for all, and as many as there is work for
+        out, lse = run(b, max_seq_len=most)
         assert sk.sk_get_device_status() == 0
         check(b, out, lse, ref)
 
@@ -134,22 +128,35 @@ def test_flat_and_peaked_scores(gain, fp8):
         if not fp8:
             for i, blk in enumerate(order.tolist()):
                 b["kv"][blk, :, :, :D] = b["kv"][blk, :, :, :D] * (0.2 + 2 * lift[i * PAGE])
-    out, lse = run(b, 1)
+    out, lse = run(b)
     assert sk.sk_get_device_status() == 0
     check(b, out, lse)
-    out, lse = run(b, 5)
-    check(b, out, lse)
 
 
-def test_the_automatic_split_long_cache():
-    """A short follow-up on two long caches: the keys of few rows go over many CTAs."""
-    b = batch([30000, 21001], [33, 9], 32, 2, False, 5)
-    assert sk.sk_prefill_nsplit(2, 42, 33, 32, 2, 30000) > 4
+@pytest.mark.parametrize("lens,qs,hq,hkv,fp8", [
+    ([30000, 21001], [33, 9], 32, 2, False), ([50001], [1], 5, 1, True), ([3000] * 30, [1] * 30, 8, 2, False),
+    ([1500, 1, 700, 2999, 40], [900, 1, 700, 100, 40], 8, 4, False), ([4000, 2500], [600, 900], 16, 2, True)])
+def test_units_cut_between_runs(lens, qs, hq, hkv, fp8):
+    """A short follow-up on two long caches, single tokens, ragged chunks: runs start and end inside units, several
+    runs share one, and all bits are the same the second time."""
+    b = batch(lens, qs, hq, hkv, fp8, 5)
     out, lse = run(b)
     assert sk.sk_get_device_status() == 0
     check(b, out, lse)
     again, lse2 = run(b)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lens,qs,hq,hkv,fp8", [
+    ([20000, 9000, 17], [1400, 300, 17], 32, 8, False), ([2500 + i for i in range(45)], [30 + i % 7 for i in range(45)], 8, 8, True),
+    ([6000] * 3 + [0] * 40 + [9001] * 2, [130] * 3 + [0] * 40 + [64] * 2, 160, 8, False)])
+def test_units_dealt_out_whole(lens, qs, hq, hkv, fp8):
+    """Batches whose K and V do not stay in the L2: whole units first, over more than 32 sequences and past empty ones, then
+    the rest in shares."""
+    b = batch(lens, qs, hq, hkv, fp8, 15)
+    out, lse = run(b)
+    assert sk.sk_get_device_status() == 0
+    check(b, out, lse)
 
 
 def test_rows_past_the_last_sequence_stay():
@@ -159,7 +166,8 @@ def test_rows_past_the_last_sequence_stay():
     out = torch.full((57, 4, D), 3.0, dtype=torch.bfloat16, device=DEV)
     lse = torch.full((57, 4), 3.0, device=DEV)
     sk.sk_get_device_status(clear=True)
-    sk.sk_paged_prefill_attn(q, b["kv"], b["bt"], b["lens"], b["cu"], out, lse, max_q_len=64, sm_scale=w.sm_scale)
+    sk.sk_paged_prefill_attn(q, b["kv"], b["bt"], b["lens"], b["cu"], out, lse, max_q_len=64,
+                             sm_scale=w.sm_scale)
     assert sk.sk_get_device_status() == sk.SK_DEV_BAD_SEQ          # the offsets do not cover the tokens
     check(b, out[:50], lse[:50])
     assert bool((out[50:] == 3).all()) and bool((lse[50:] == 3).all())
@@ -187,7 +195,7 @@ def test_like_decode_attention_and_without_lse():
     """The same batch through the decode path: both within their bounds of the other."""
     b = batch([1000, 17, 0, 333], [4, 4, 4, 4], 16, 2, False, 8)
     w = b["w"]
-    out, lse = run(b, 1)
+    out, lse = run(b)
     o2, l2 = sk.paged_decode_attention(b["q"], b["kv"], b["bt"], b["lens"], b["cu"], max_q_len=4, sm_scale=w.sm_scale,
                                        num_sms=148)
     _, _, to, tl = reference(b)
