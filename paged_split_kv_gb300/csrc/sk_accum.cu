@@ -17,9 +17,11 @@
 //   many rows (kMany true): the group's K tiles stay (128 KB of bf16) while Q streams through in blocks of 128 rows, so
 //     that a block's 32 KB meet 512 keys: with fewer the L2 could not deliver Q as fast as the tensor cores take it.
 //
-// Roles (640 threads): warp 0 copies K pages, warp 1 issues the products, warp 2 copies Q blocks (TMA: a box is
-// whole tokens of the group's heads), warp 3 lays the rows' lse and scale beside them, warps 4-19 are the four
-// softmax warpgroups.
+// Roles (640 threads): warp 0 copies K pages; warps 1 and 2 issue the products of every other tile of a group (an
+// issuer's waits cost it more than the products do: one alone for all four tiles took 196 us where two take XX, a chunk
+// of 2000 rows a head over 16k keys of e4m3); warp 3 finds the items (the parts of the run in one sequence and head) and
+// publishes them, copies Q blocks (TMA: a box is whole tokens of the group's heads) and lays the rows' lse and scale
+// beside them; warps 4-19 are the four softmax warpgroups.
 //
 // e4m3 pages: the products run as kind::f8f6f4 on the codes, with Q as two e4m3 terms and a power-of-two scale per row
 // (prepared by a small kernel into a workspace; exact for bf16 elements within 2^-9 of the row's largest).
@@ -45,7 +47,7 @@ constexpr int kGroup = 4;                            // tiles of a group, softma
 constexpr int kThreads = 128 + kGroup * 128;
 constexpr long long kDrainLimit = 4000000000LL;
 constexpr int kMaxSmem = 232448;
-
+constexpr int kRing = 4;                             // items published ahead
 template <int RB, bool MANY, bool FP8>
 struct ACfg {
     static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K of 8 tokens
@@ -70,11 +72,14 @@ struct ACfg {
     static constexpr int kBarS = kBarAEmpty + 8 * kQSlots;         // [kGroup] S complete
     static constexpr int kBarSFree = kBarS + 8 * kGroup;
     static constexpr int kBarDrain = kBarSFree + 8 * kGroup;
-    static constexpr int kTmemSlot = kBarDrain + 8;
+    static constexpr int kTmemSlot = kBarDrain + 16;
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kStart = (kAbort + 4 + 7) / 8 * 8;        // where the run starts
-    static constexpr int kAux = 512;                               // float[kQSlots][kAuxEach], log2 units
-    static_assert(kStart + 24 <= kAux && kAux + kQSlots * kAuxEach * 4 <= kMisc, "misc area");
+    static constexpr int kBarItem = kStart + 16;                   // [kRing] items published, and read
+    static constexpr int kBarItemFree = kBarItem + 8 * kRing;
+    static constexpr int kItems = (kBarItemFree + 8 * kRing + 15) / 16 * 16;
+    static constexpr int kAux = 640;                               // float[kQSlots][kAuxEach], log2 units
+    static_assert(kItems + kRing * 32 <= kAux && kAux + kQSlots * kAuxEach * 4 <= kMisc, "misc area");
     static_assert(kKSlots >= (MANY ? kGroup : 3) && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0 && kQSlot % 1024 == 0,
                   "shared memory");
 };
@@ -84,8 +89,9 @@ struct Item {
     int s, h, L, q_len, tok0, a, b;                  // tiles [a, b)
     int nblk;                                        // Q blocks
 };
+static_assert(sizeof(Item) == 32, "the ring holds items of two 16-byte words");
 
-// The tiles of a CTA's run, item after item; every role walks it alike.
+// The tiles of a CTA's run, item after item.
 struct Walk {
     const AccumParams &p;
     long long lo, hi, off;                           // the run, and the current sequence's start, in block-tiles
@@ -162,7 +168,10 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     auto bar_aempty = [&](int i) { return mbase + C::kBarAEmpty + 8 * i; };
     auto bar_s = [&](int i) { return mbase + C::kBarS + 8 * i; };
     auto bar_sfree = [&](int i) { return mbase + C::kBarSFree + 8 * i; };
-    const uint32_t bar_drain = mbase + C::kBarDrain;
+    auto bar_item = [&](int i) { return mbase + C::kBarItem + 8 * i; };
+    auto bar_item_free = [&](int i) { return mbase + C::kBarItemFree + 8 * i; };
+    Item *ring = reinterpret_cast<Item *>(misc + C::kItems);
+    auto bar_drain = [&](int i) { return mbase + C::kBarDrain + 8 * i; };
 
     wait_prior_grid();
     if (threadIdx.x == 0) {
@@ -172,7 +181,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
         }
         for (int i = 0; i < C::kQSlots; ++i) {
             mbar_init(bar_qfull(i), 1);
-            mbar_init(bar_qempty(i), 1);
+            mbar_init(bar_qempty(i), 2);
             mbar_init(bar_afull(i), 1);
             mbar_init(bar_aempty(i), 4 * kGroup);
         }
@@ -180,7 +189,12 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             mbar_init(bar_s(i), 1);
             mbar_init(bar_sfree(i), 4);
         }
-        mbar_init(bar_drain, 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar_item(i), 1);
+            mbar_init(bar_item_free(i), 3 + 4 * kGroup);
+        }
+        mbar_init(bar_drain(0), 1);
+        mbar_init(bar_drain(1), 1);
         *abort_flag = 0;
         fence_mbar_init();
         if (blockIdx.x == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_q + p.bs) != p.num_tokens))
@@ -206,7 +220,20 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     const bool any = (sbase & 1023u) == 0;
     if (!any && threadIdx.x == 0)
         atomicOr(p.status, SK_DEV_INTERNAL);
-    Walk walk(p, run.lo, run.hi, any ? run.s : p.bs, run.before);
+    // The next published item; false at the end of the run, or (ok becomes false) when the wait gave up.
+    int read = 0;
+    auto next_item = [&](Item &item, bool &ok) {
+        const int i = read % kRing;
+        ok = __all_sync(kFull, wait_bar(bar_item(i), (read / kRing) & 1, abort_flag, p.wait_limit));
+        if (!ok)
+            return false;
+        item = ring[i];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar_item_free(i));
+        ++read;
+        return item.s >= 0;
+    };
     Item it;
 
     // groups of an item: its tiles in equal shares of up to four
@@ -224,7 +251,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             prefetch_tensormap(&kv_map);
         int u = 0;                                   // tiles issued
         bool ok = true;
-        while (ok && walk.next(it)) {
+        while (ok && next_item(it, ok)) {
             const int page_end = (it.L + kPage - 1) / kPage;
             const int32_t *bt = p.block_table + (long long)it.s * p.bt_stride;
             auto block_at = [&](int t) {
@@ -235,7 +262,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             for (int t = it.a; t < it.b && ok; ++t, ++u) {
                 const int i = u % C::kKSlots;
                 if (u >= C::kKSlots)
-                    ok = mbar_wait_bounded(bar_kempty(i), (u / C::kKSlots - 1) & 1, abort_flag, p.wait_limit);
+                    ok = wait_bar(bar_kempty(i), (u / C::kKSlots - 1) & 1, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 if (!ok)
                     break;
@@ -263,26 +290,26 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 atomicOr(p.status, SK_DEV_TIMEOUT);
         }
         for (int t = u > C::kKSlots ? u - C::kKSlots : 0; t < u; ++t)
-            mbar_wait_bounded(bar_kfull(t % C::kKSlots), (t / C::kKSlots) & 1, nullptr, kDrainLimit);
-    } else if (warp == 1) {
-        // ============================================================ products
+            wait_bar(bar_kfull(t % C::kKSlots), (t / C::kKSlots) & 1, nullptr, kDrainLimit);
+    } else if (warp <= 2) {
+        // ============================================================ products: tiles 0 and 2 of a group, or 1 and 3
+        const int e = warp - 1;
         constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(kKeys, RB, 0, 0) : idesc_bf16_f32(kKeys, RB, 0, 0);
         const uint64_t d_k0 = smem_desc_sw128(sbase, 16, C::kGroupBytes);
         const uint64_t d_q0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
         auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
         bool ok = true;
         int u = 0, v = 0;                            // K tiles and Q blocks used up
-        uint32_t uses[kGroup] = {0, 0, 0, 0};        // products of each TMEM buffer
-        bool issued = false;
+        uint32_t uses[kGroup / 2] = {0, 0};          // products of each TMEM buffer of this issuer
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if (ok)
-                ok = mbar_wait_bounded(bar, parity, abort_flag, p.wait_limit);
+                ok = wait_bar(bar, parity, abort_flag, p.wait_limit);
             ok = __all_sync(kFull, ok);
             if (ok)
                 tc_fence_after();
             return ok;
         };
-        while (ok && walk.next(it)) {
+        while (ok && next_item(it, ok)) {
             const int ng = groups_of(it);
             for (int g = 0; g < ng && ok; ++g) {
                 const int ta = group_at(it, ng, g), nt = group_at(it, ng, g + 1) - ta;
@@ -291,7 +318,8 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                     if ((MANY || g == 0) && !wait(bar_qfull(qi), (v / C::kQSlots) & 1))
                         break;
 #pragma unroll
-                    for (int i = 0; i < kGroup; ++i) {
+                    for (int ii = 0; ii < kGroup / 2; ++ii) {
+                        const int i = 2 * ii + e;
                         if (i >= nt || !ok)
                             continue;
                         const int f = MANY ? first_block(it, ta + i) : 0;
@@ -299,34 +327,23 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                         if (qb >= f) {
                             if (qb == f && !wait(bar_kfull(ki), ((u + i) / C::kKSlots) & 1))
                                 continue;
-                            if (uses[i] > 0 && !wait(bar_sfree(i), (uses[i] - 1) & 1))
+                            if (uses[ii] > 0 && !wait(bar_sfree(i), (uses[ii] - 1) & 1))
                                 continue;
-                            const uint32_t so = (uint32_t)ki * C::kKSlot, qo = (uint32_t)qi * C::kQSlot;
+                            const uint64_t k0 = adv(d_k0, (uint32_t)ki * C::kKSlot);
+                            const uint64_t q0 = adv(d_q0, (uint32_t)qi * C::kQSlot);
                             const uint32_t sd = tmem + i * 128;
-                            if constexpr (FP8) {
 #pragma unroll
-                                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        mma_f8_ss_warp(sd, adv(d_k0, so + k * 32), adv(d_q0, qo + t * (RB * 128) + k * 32),
-                                                       idesc, (t > 0 || k > 0) ? 1u : 0u);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_f16_ss_warp(sd, adv(d_k0, so + (k >> 2) * 1024 + (k & 3) * 32),
-                                                    adv(d_q0, qo + (k >> 2) * (RB * 128) + (k & 3) * 32), idesc,
-                                                    k > 0 ? 1u : 0u);
+                            for (int hf = 0; hf < 2; ++hf) {
+                                if constexpr (FP8)
+                                    mma4_f8_ss<2, 2>(sd, k0, adv(q0, hf * (RB * 128)), idesc, hf);
+                                else
+                                    mma4_f16_ss<2, 2>(sd, adv(k0, hf * 1024), adv(q0, hf * (RB * 128)), idesc, hf);
                             }
                             mma_commit_warp(bar_s(i));
-                            ++uses[i];
-                            issued = true;
+                            ++uses[ii];
                         }
-                        if (qb + 1 == it.nblk) {
-                            // a tile that no row sees is not waited for before: its copy has to have landed
-                            if (qb < f && !wait(bar_kfull(ki), ((u + i) / C::kKSlots) & 1))
-                                continue;
+                        if (qb + 1 == it.nblk)               // the last row sees every tile
                             mma_commit_warp(bar_kempty(ki));
-                        }
                     }
                     if (MANY || g + 1 == ng) {
                         mma_commit_warp(bar_qempty(qi));
@@ -341,36 +358,51 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             if (lane == 0)
                 atomicOr(p.status, SK_DEV_TIMEOUT);
         }
-        if (issued) {
-            mma_commit_warp(bar_drain);
-            mbar_wait_bounded(bar_drain, 0, nullptr, kDrainLimit);
-        }
-    } else if (warp == 2 || warp == 3) {
-        // ============================================================ Q blocks (warp 2), their rows' lse and scale (3)
+        mma_commit_warp(bar_drain(e));
+        wait_bar(bar_drain(e), 0, nullptr, kDrainLimit);
+    } else if (warp == 3) {
+        // ============================================================ the items; Q blocks, and their rows' lse and scale
+        Walk walk(p, run.lo, run.hi, any ? run.s : p.bs, run.before);
         bool ok = true;
         int v = 0;
-        while (ok && walk.next(it)) {
+        for (int k = 0; ok; ++k) {
+            const bool more = walk.next(it);
+            if (!more)
+                it.s = -1;
+            if (k >= kRing)
+                ok = wait_bar(bar_item_free(k % kRing), (k / kRing - 1) & 1, abort_flag, p.wait_limit);
+            ok = __all_sync(kFull, ok);
+            if (!ok)
+                break;
+            if (lane == 0) {
+                ring[k % kRing] = it;
+                mbar_arrive(bar_item(k % kRing));
+            }
+            __syncwarp();
+            if (!more)
+                break;
             const int ng = MANY ? groups_of(it) : 1;
             for (int g = 0; g < ng && ok; ++g)
                 for (int qb = MANY ? first_block(it, group_at(it, ng, g)) : 0; qb < it.nblk && ok; ++qb, ++v) {
                     const int qi = v % C::kQSlots;
                     const int j0 = qb / p.nsub * p.tpb, i0 = (qb % p.nsub) * p.gb;
                     const int hq0 = it.h * p.G + i0;
-                    if (v >= C::kQSlots)
-                        ok = mbar_wait_bounded(warp == 2 ? bar_qempty(qi) : bar_aempty(qi), (v / C::kQSlots - 1) & 1,
-                                               abort_flag, p.wait_limit);
+                    if (v >= C::kQSlots) {
+                        ok = wait_bar(bar_qempty(qi), (v / C::kQSlots - 1) & 1, abort_flag, p.wait_limit);
+                        if (ok)
+                            ok = wait_bar(bar_aempty(qi), (v / C::kQSlots - 1) & 1, abort_flag, p.wait_limit);
+                    }
                     ok = __all_sync(kFull, ok);
                     if (!ok)
                         break;
-                    if (warp == 2) {
-                        if (lane == 0) {
-                            const uint32_t dst = sbase + C::kOffQ + qi * C::kQSlot;
-                            mbar_arrive_expect_tx(bar_qfull(qi), (uint32_t)(p.gb * p.tpb * 256));
-                            tma_load_3d(dst, &q_map, 0, hq0, it.tok0 + j0, bar_qfull(qi));
-                            tma_load_3d(dst + RB * 128, &q_map, FP8 ? 128 : 64, hq0, it.tok0 + j0, bar_qfull(qi));
-                        }
-                        __syncwarp();
-                    } else {
+                    if (lane == 0) {
+                        const uint32_t dst = sbase + C::kOffQ + qi * C::kQSlot;
+                        mbar_arrive_expect_tx(bar_qfull(qi), (uint32_t)(p.gb * p.tpb * 256));
+                        tma_load_3d(dst, &q_map, 0, hq0, it.tok0 + j0, bar_qfull(qi));
+                        tma_load_3d(dst + RB * 128, &q_map, FP8 ? 128 : 64, hq0, it.tok0 + j0, bar_qfull(qi));
+                    }
+                    __syncwarp();
+                    {
                         float *aux = reinterpret_cast<float *>(misc + C::kAux) + qi * C::kAuxEach;
                         for (int r = lane; r < RB; r += 32) {
                             const int jj = r / p.gb, ii = r - jj * p.gb;
@@ -398,9 +430,8 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             if (lane == 0)
                 atomicOr(p.status, SK_DEV_TIMEOUT);
         }
-        if (warp == 2)
-            for (int t = v > C::kQSlots ? v - C::kQSlots : 0; t < v; ++t)
-                mbar_wait_bounded(bar_qfull(t % C::kQSlots), (t / C::kQSlots) & 1, nullptr, kDrainLimit);
+        for (int t = v > C::kQSlots ? v - C::kQSlots : 0; t < v; ++t)
+            wait_bar(bar_qfull(t % C::kQSlots), (t / C::kQSlots) & 1, nullptr, kDrainLimit);
     } else {
         // ============================================================ sums of the exponentials
         const int wg = (warp >> 2) - 1;
@@ -410,7 +441,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
         uint32_t uses = 0;
         int v = 0;
         bool ok = true;
-        while (ok && walk.next(it)) {
+        while (ok && next_item(it, ok)) {
             const int ng = groups_of(it);
             const int32_t *bt = p.block_table + (long long)it.s * p.bt_stride;
             for (int g = 0; g < ng && ok; ++g) {
@@ -429,10 +460,10 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 for (int qb = MANY ? first_block(it, ta) : 0; qb < it.nblk && ok; ++qb) {
                     const int qi = v % C::kQSlots;
                     if (MANY || g == 0)
-                        ok = __all_sync(kFull, mbar_wait_bounded(bar_afull(qi), (v / C::kQSlots) & 1, abort_flag,
+                        ok = __all_sync(kFull, wait_bar(bar_afull(qi), (v / C::kQSlots) & 1, abort_flag,
                                                                  p.wait_limit));
                     if (ok && wg < nt && qb >= f) {
-                        ok = mbar_wait_bounded(bar_s(wg), uses & 1, abort_flag, p.wait_limit);
+                        ok = wait_bar(bar_s(wg), uses & 1, abort_flag, p.wait_limit);
                         ++uses;
                         ok = __all_sync(kFull, ok);
                         if (ok) {
@@ -443,13 +474,15 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                             const int rmin = jmin > j0 ? (jmin - j0) * p.gb : 0;
                             const int rows = p.nsub > 1 ? min(p.gb, p.G - qb % p.nsub * p.gb)
                                                         : min(p.tpb, it.q_len - j0) * p.gb;
-                            constexpr int kLd = RB < 32 ? RB : 32;
+                            constexpr int kLd = RB < 64 ? RB : 64;
 #pragma unroll
                             for (int c0 = 0; c0 < RB; c0 += kLd) {
                                 if (c0 >= rows)
                                     break;
                                 float x[kLd];
-                                tmem_ld32<kLd>(ts + c0, x);
+#pragma unroll
+                                for (int c = 0; c < kLd; c += kLd < 32 ? kLd : 32)
+                                    tmem_ld32<(kLd < 32 ? kLd : 32)>(ts + c0 + c, x + c);
                                 tmem_wait_ld();
                                 if (c0 + kLd >= rows) {              // the buffer's last read
                                     tc_fence_before();
