@@ -289,8 +289,9 @@ int64_t sk_prefill_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype
  * it (in no fixed order; otherwise the same bits every time).
  *
  * acc_pages fp32 [num_blocks, num_kv_heads, page_size], updated in place.  workspace (device, 16-byte aligned):
- * sk_accum_workspace_bytes(num_tokens, num_q_heads, kv_dtype) bytes, 0 for bf16 pages (then it may be NULL); its
- * contents do not matter, and calls that may overlap need one each.  q and kv_pages are 16-byte aligned.
+ * sk_accum_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype) bytes, 0 for bf16 pages and at
+ * most 64 rows (max_q_len times the heads of a group; then it may be NULL); its contents do not matter, and calls that
+ * may overlap need one each.  q and kv_pages are 16-byte aligned.
  * Scores and sums are fp32; with e4m3fn pages q is two e4m3 terms per element, exact for elements of at least
  * 2^-9 of the row's largest.  Asynchronous on `stream`, no allocation, capture safe.
  * Returns SK_OK or a negative sk_status. */
@@ -301,7 +302,7 @@ int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, flo
                           const float *lse, float *acc_pages, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of sk_accum_attn_weights.  Host-only arithmetic; a negative sk_status for bad sizes. */
-int64_t sk_accum_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype);
+int64_t sk_accum_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int max_q_len, int kv_dtype);
 
 /* How sk_rope_frequencies fits the frequencies w_i = base^(-2 i / rot_dim) to contexts `factor` times
  * longer than the trained ones. */

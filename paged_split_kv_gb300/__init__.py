@@ -95,7 +95,7 @@ def lib():
         L.sk_paged_prefill_attn.argtypes = [P, P, i32, f32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32,
                                             f32, i32, i32, P, i64, P, P, P]
         L.sk_accum_workspace_bytes.restype = i64
-        L.sk_accum_workspace_bytes.argtypes = [i32, i32, i32]
+        L.sk_accum_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
         L.sk_accum_attn_weights.restype = i32
         L.sk_accum_attn_weights.argtypes = [P, P, i32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32, f32,
                                             i32, P, P, P, i64, P]
@@ -546,9 +546,10 @@ def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *,
     return out, lse
 
 
-def sk_accum_workspace_bytes(num_tokens: int, num_q_heads: int, kv_dtype: int) -> int:
+def sk_accum_workspace_bytes(num_tokens: int, num_q_heads: int, num_kv_heads: int, max_q_len: int, kv_dtype: int) -> int:
     """Bytes of device workspace that sk_accum_attn_weights needs (computed by the library)."""
-    return _check(lib().sk_accum_workspace_bytes(num_tokens, num_q_heads, kv_dtype), "sk_accum_workspace_bytes")
+    return _check(lib().sk_accum_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype),
+                  "sk_accum_workspace_bytes")
 
 
 def sk_accum_attn_weights(q, kv_pages, block_table, seq_lens, cu_seqlens_q, lse, acc_pages, *, max_q_len: int,
@@ -557,15 +558,15 @@ def sk_accum_attn_weights(q, kv_pages, block_table, seq_lens, cu_seqlens_q, lse,
     """Adds to ``acc_pages`` (fp32 [num_blocks, num_kv_heads, page]) the attention weight that each cached key
     receives from this step's query tokens: exp(score - lse) summed over the tokens that see it and the
     heads of its group, ``lse`` (fp32 [num_tokens, num_q_heads]) being what the attention call returned.
-    ``workspace`` is an optional dict that keeps the buffer of e4m3 pages across calls."""
+    ``workspace`` is an optional dict that keeps the call's buffer; calls that may overlap need one each."""
     import torch
     dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,
                                                                                cu_seqlens_q)
     pl = _fits(lse, torch.float32, (nt, hq), "lse", dev)
     pa = _fits(acc_pages, torch.float32, (nb, hkv, page), "acc_pages", dev)
     buf, need = None, 0
-    if dt == SK_KV_FP8_E4M3 and dev >= 0:
-        need = sk_accum_workspace_bytes(nt, hq, dt)
+    if dev >= 0 and (dt == SK_KV_FP8_E4M3 or max_q_len * (hq // hkv) > 64):
+        need = sk_accum_workspace_bytes(nt, hq, hkv, max_q_len, dt)
         buf = _buffer(workspace if workspace is not None else {}, "accum", need, q.device)
     return _launch(dev, stream, "sk_accum_attn_weights", lib().sk_accum_attn_weights, pq, pp, dt, k_scale, pb, stride,
                    nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0, pl, pa, buf, need)

@@ -9,19 +9,21 @@
 // Bound by HBM for a few rows (decode, verify: 256 or 128 bytes of K per key against up to 64 rows), by the
 // exponentials and the tensor cores for a chunk (256 flops and one exponential per (row, key)).
 //
-// The cache is cut into tiles of 128 keys; each CTA (one per SM) takes a contiguous run of all the batch's tiles, as
-// many rows' worth as the others, found from the lengths on the device.  Inside a run it works on groups of up to four
-// tiles of one (sequence, head): tile i of a group belongs to softmax warpgroup i and its 128 TMEM columns.
-//   few rows (kMany false): the rows are one Q block of 16, 32 or 64 rows that stays for the whole item while K tiles
-//     stream through a ring;
-//   many rows (kMany true): the group's K tiles stay (128 KB of bf16) while Q streams through in blocks of 128 rows, so
-//     that a block's 32 KB meet 512 keys: with fewer the L2 could not deliver Q as fast as the tensor cores take it.
+// One CTA per SM works on groups of up to four tiles of 128 keys of one (sequence, head): tile i of a group belongs to
+// softmax warpgroup i and its 128 TMEM columns.  Each CTA takes an equal share of the batch's cost, a contiguous run found
+// from the lengths on the device.
+//   few rows (MANY false): the rows are one Q block of 16, 32 or 64 rows that stays for the whole item while K tiles
+//     stream through a ring; runs are cut between tiles.
+//   many rows (MANY true): a group's K tiles stay (128 KB of bf16) while Q streams through in blocks of 128 rows, so
+//     that a block's 32 KB meet 512 keys: with fewer the L2 could not deliver Q as fast as the tensor cores take it.  Runs
+//     are cut inside a group, between Q blocks: cut between tiles they came out at one to three tiles each, which
+//     left CTAs idle and a group's pipeline half empty (1190 and 1500 tokens over 18k and 8k keys of e4m3, 8 heads
+//     a KV head: 184 us, now 126).  The sums of a group that several runs share meet in accum_join_kernel.
 //
-// Roles (640 threads): warp 0 copies K pages; warps 1 and 2 issue the products of every other tile of a group (an
-// issuer's waits cost it more than the products do: one alone for all four tiles took 196 us where two take XX, a chunk
-// of 2000 rows a head over 16k keys of e4m3); warp 3 finds the items (the parts of the run in one sequence and head) and
-// publishes them, copies Q blocks (TMA: a box is whole tokens of the group's heads) and lays the rows' lse and scale
-// beside them; warps 4-19 are the four softmax warpgroups.
+// Roles (640 threads): warp 0 copies K pages; warps 1 and 2 issue the products of every other tile of a group; warp 3
+// finds the items (the parts of the run in one sequence and head) and publishes them, copies Q blocks (TMA: a box is
+// whole tokens of the group's heads) and lays the rows' lse and scale beside them; warps 4-19 are the four softmax
+// warpgroups.
 //
 // e4m3 pages: the products run as kind::f8f6f4 on the codes, with Q as two e4m3 terms and a power-of-two scale per row
 // (prepared by a small kernel into a workspace; exact for bf16 elements within 2^-9 of the row's largest).
@@ -31,6 +33,8 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "sk_attn_util.cuh"
 #include "sk_internal.cuh"
@@ -47,6 +51,8 @@ constexpr int kGroup = 4;                            // tiles of a group, softma
 constexpr int kThreads = 128 + kGroup * 128;
 constexpr long long kDrainLimit = 4000000000LL;
 constexpr int kMaxSmem = 232448;
+constexpr int kAccumRuns = 256;                      // runs (SMs) at most
+constexpr long long kAccumParts = 2LL * kAccumRuns * (kGroup * kKeys * 4 + (long long)sizeof(AccumPiece));
 constexpr int kRing = 4;                             // items published ahead
 template <int RB, bool MANY, bool FP8>
 struct ACfg {
@@ -79,72 +85,188 @@ struct ACfg {
     static constexpr int kBarItemFree = kBarItem + 8 * kRing;
     static constexpr int kItems = (kBarItemFree + 8 * kRing + 15) / 16 * 16;
     static constexpr int kAux = 640;                               // float[kQSlots][kAuxEach], log2 units
-    static_assert(kItems + kRing * 32 <= kAux && kAux + kQSlots * kAuxEach * 4 <= kMisc, "misc area");
+    static_assert(kItems + kRing * 48 <= kAux && kAux + kQSlots * kAuxEach * 4 <= kMisc, "misc area");
     static_assert(kKSlots >= (MANY ? kGroup : 3) && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0 && kQSlot % 1024 == 0,
                   "shared memory");
 };
 
-// One (sequence, head) share of a CTA's run, and the blocks that its rows make.
-struct Item {
-    int s, h, L, q_len, tok0, a, b;                  // tiles [a, b)
-    int nblk;                                        // Q blocks
+// What a CTA works on at a time: Q blocks [q0, q1) against tiles [a, b) of one (sequence, head).
+struct __align__(16) Item {
+    int s, h, L, q_len, tok0, a, b, q0, q1;
+    int slot;                                        // of the run's shared units, or -1: the sums are complete
+    int ends;                                        // the unit's last rows are among them
+    int pad;
 };
-static_assert(sizeof(Item) == 32, "the ring holds items of two 16-byte words");
+static_assert(sizeof(Item) == 48, "the ring holds items of three 16-byte words");
 
-// The tiles of a CTA's run, item after item.
-struct Walk {
+// First Q block of a sequence with a row that sees tile `tile`: causal rows start at token p0 - (L - q).
+__device__ __forceinline__ int first_block(const AccumParams &p, int L, int q_len, int tile)
+{
+    const int j = p.causal ? tile * kKeys - (L - q_len) : 0;
+    return j > 0 ? j / p.tpb * p.nsub : 0;
+}
+
+// Q blocks of sequence s; 0 when it has nothing to do (and a bad one is reported).
+__device__ __forceinline__ int blocks_of(const AccumParams &p, int s, int &L, int &q, int &tok0)
+{
+    L = __ldg(p.seq_lens + s);
+    tok0 = __ldg(p.cu_q + s);
+    q = __ldg(p.cu_q + s + 1) - tok0;
+    if (q < 0 || q > p.max_q_len || tok0 < 0 || tok0 + q > p.num_tokens || L < 0 ||
+        (long long)L > (long long)p.bt_stride * kPage) {
+        atomicOr(p.status, SK_DEV_BAD_SEQ);
+        L = q = 0;
+    }
+    return L > 0 ? (q + p.tpb - 1) / p.tpb * p.nsub : 0;
+}
+
+// Many rows: a unit is a group of four tiles against the Q blocks that see it.  It costs its tokens plus a fixed part (K
+// tiles of the next unit are not there yet when one ends), times the tiles of a group and one.
+struct Units {
+    int L, q, tok0, nblk, units, w;
+    long long fixed, ctx;
+    __device__ __forceinline__ long long before(long long i) const
+    {
+        const int keys = kGroup * kKeys;
+        const long long g1 = ctx < 0 ? 0 : ctx / keys + 1;           // first group that some rows do not see
+        const long long unseen = i > g1 ? keys * ((i * (i - 1) - g1 * (g1 - 1)) / 2) - ctx * (i - g1) : 0;
+        return (i * (fixed + q) - unseen) * w;
+    }
+};
+constexpr int kUnitFixed = 3;                        // Q blocks
+
+__device__ __forceinline__ Units units_of(const AccumParams &p, int s)
+{
+    Units u;
+    u.nblk = blocks_of(p, s, u.L, u.q, u.tok0);
+    const int tiles = (u.L + kKeys - 1) / kKeys;
+    u.units = u.nblk > 0 ? (tiles + kGroup - 1) / kGroup : 0;
+    u.w = min(tiles, kGroup) + 1;
+    u.fixed = kUnitFixed * p.tpb;
+    u.ctx = p.causal ? u.L - u.q : u.L;
+    return u;
+}
+
+// Walks the units of a CTA's run [lo, hi) of the cost, cut in the rows where the run ends.
+struct UnitWalk {
     const AccumParams &p;
-    long long lo, hi, off;                           // the run, and the current sequence's start, in block-tiles
+    long long lo, hi, off;                           // the run, and where the current sequence starts
+    int s, h, unit;
+    bool loaded;
+    Units q;
+    __device__ UnitWalk(const AccumParams &pp, const Run &run, int s0)
+        : p(pp), lo(run.lo), hi(run.hi), off(run.before), s(s0), h(0), unit(-1), loaded(false)
+    {
+    }
+    __device__ __forceinline__ bool next(Item &it)
+    {
+        while (s < p.bs && off < hi) {
+            if (!loaded) {
+                q = units_of(p, s);
+                loaded = true;
+            }
+            const long long head = q.before(q.units);
+            if (h >= p.H_kv || q.units == 0) {
+                off += head * p.H_kv;
+                ++s;
+                h = 0;
+                unit = -1;
+                loaded = false;
+                continue;
+            }
+            const long long h0 = off + h * head;
+            if (h0 + head <= lo) {
+                ++h;
+                continue;
+            }
+            if (unit < 0) {
+                int left = 0, right = q.units - 1;   // the last unit that starts at lo or before
+                while (left < right) {
+                    const int mid = (left + right + 1) >> 1;
+                    if (q.before(mid) <= lo - h0)
+                        left = mid;
+                    else
+                        right = mid - 1;
+                }
+                unit = left;
+            }
+            const long long start = h0 + q.before(unit), cost = h0 + q.before(unit + 1) - start;
+            if (start >= hi)
+                return false;
+            it.s = s;
+            it.h = h;
+            it.L = q.L;
+            it.q_len = q.q;
+            it.tok0 = q.tok0;
+            it.a = unit * kGroup;
+            it.b = min(it.a + kGroup, (q.L + kKeys - 1) / kKeys);
+            // A cut near either end of the unit moves there, and where else it falls is rounded in fp32: alike in both
+            // runs that it divides, and that is all that matters.
+            const int f = first_block(p, q.L, q.q, it.a);
+            const long long edge = q.fixed * q.w;
+            auto block = [&](long long at) {
+                const int n = q.nblk - f;
+                return f + (at <= edge          ? 0
+                            : at >= cost - edge ? n
+                                                : max(0, min(n, (int)((float)n * __fdividef((float)at, (float)cost)))));
+            };
+            it.q0 = block(max(0LL, lo - start));
+            it.q1 = block(hi - start);
+            it.slot = it.q0 > f ? 0 : (it.q1 < q.nblk ? 1 : -1);
+            it.ends = it.q1 == q.nblk;
+            if (++unit == q.units) {
+                ++h;
+                unit = -1;
+            }
+            if (it.q0 < it.q1)
+                return true;
+        }
+        return false;
+    }
+};
+
+// Few rows: one Q block a sequence.  The tiles of a CTA's run, (sequence, head) after (sequence, head).
+struct TileWalk {
+    const AccumParams &p;
+    long long lo, hi, off;                           // the run, and the current sequence's start, in tiles
     int s, h;
-    __device__ Walk(const AccumParams &pp, long long lo_, long long hi_, int s0, long long off0)
-        : p(pp), lo(lo_), hi(hi_), off(off0), s(s0), h(0)
+    __device__ TileWalk(const AccumParams &pp, const Run &run, int s0)
+        : p(pp), lo(run.lo), hi(run.hi), off(run.before), s(s0), h(0)
     {
     }
     __device__ __forceinline__ bool next(Item &it)
     {
         while (s < p.bs && off < hi) {
             int L, q, tok0;
-            const int w = accum_weight(p, s, L, q, tok0);
+            const bool some = blocks_of(p, s, L, q, tok0) > 0;
             const int tiles = (L + kKeys - 1) / kKeys;
-            if (w > 0 && h < p.H_kv) {
-                const long long start = off + (long long)h * tiles * w;
+            if (some && h < p.H_kv) {
+                const long long start = off + (long long)h * tiles;
                 const int hh = h++;
                 if (start >= hi)
                     return false;
-                // a tile belongs to the run that its start lies in
-                const long long a = lo > start ? (lo - start + w - 1) / w : 0;
-                const long long b = (hi - start + w - 1) / w;
-                if (a < tiles && a < b) {
+                const long long a = max(0LL, lo - start), b = min((long long)tiles, hi - start);
+                if (a < b) {
                     it.s = s;
                     it.h = hh;
                     it.L = L;
                     it.q_len = q;
                     it.tok0 = tok0;
                     it.a = (int)a;
-                    it.b = (int)(b < tiles ? b : tiles);
-                    it.nblk = w;
+                    it.b = (int)b;
+                    it.q0 = 0;
+                    it.q1 = 1;
+                    it.slot = -1;
+                    it.ends = 1;
                     return true;
                 }
                 continue;
             }
-            off += (long long)tiles * w * p.H_kv;
+            off += some ? (long long)tiles * p.H_kv : 0;
             ++s;
             h = 0;
         }
         return false;
-    }
-    // Q blocks of a sequence with q query tokens; 0 when it has nothing to do (and a bad one is reported once)
-    static __device__ __forceinline__ int accum_weight(const AccumParams &p, int s, int &L, int &q, int &tok0)
-    {
-        L = __ldg(p.seq_lens + s);
-        tok0 = __ldg(p.cu_q + s);
-        q = __ldg(p.cu_q + s + 1) - tok0;
-        if (q < 0 || q > p.max_q_len || tok0 < 0 || tok0 + q > p.num_tokens || L < 0 ||
-            (long long)L > (long long)p.bt_stride * kPage) {
-            atomicOr(p.status, SK_DEV_BAD_SEQ);
-            L = q = 0;
-        }
-        return L > 0 ? (q + p.tpb - 1) / p.tpb * p.nsub : 0;
     }
 };
 
@@ -207,12 +329,17 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // this CTA's run of the batch's block-tiles (found in the K slots' memory, before the first copy)
+    // this CTA's run of the batch's cost (found in the K slots' memory, before the first copy)
     const Run run = find_run<kThreads>(p.bs, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(smem),
                                        reinterpret_cast<long long *>(misc + C::kStart), [&](int s) {
-                                           int L, q, tok0;
-                                           const int w = Walk::accum_weight(p, s, L, q, tok0);
-                                           return (long long)((L + kKeys - 1) / kKeys) * w * p.H_kv;
+                                           if constexpr (MANY) {
+                                               const Units u = units_of(p, s);
+                                               return u.before(u.units) * p.H_kv;
+                                           } else {
+                                               int L, q, tok0;
+                                               const bool some = blocks_of(p, s, L, q, tok0) > 0;
+                                               return some ? (long long)((L + kKeys - 1) / kKeys) * p.H_kv : 0LL;
+                                           }
                                        });
     fence_proxy_async_smem();                        // the copies come after these uses of the slots
     __syncthreads();
@@ -236,13 +363,10 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     };
     Item it;
 
-    // groups of an item: its tiles in equal shares of up to four
-    auto groups_of = [&](const Item &w) { return (w.b - w.a + kGroup - 1) / kGroup; };
-    auto group_at = [&](const Item &w, int ng, int g) { return w.a + (int)((long long)(w.b - w.a) * g / ng); };
-    // first Q block with a row that sees key p0: causal rows start at token p0 - (L - q)
-    auto first_block = [&](const Item &w, int tile) {
-        const int j = p.causal ? tile * kKeys - (w.L - w.q_len) : 0;
-        return j > 0 ? j / p.tpb * p.nsub : 0;
+    // groups of an item: its tiles in equal shares of up to four (many rows: one group)
+    auto groups_of = [&](const Item &w) { return MANY ? 1 : (w.b - w.a + kGroup - 1) / kGroup; };
+    auto group_at = [&](const Item &w, int ng, int g) {
+        return MANY ? (g ? w.b : w.a) : w.a + (int)((long long)(w.b - w.a) * g / ng);
     };
 
     if (warp == 0) {
@@ -313,7 +437,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             const int ng = groups_of(it);
             for (int g = 0; g < ng && ok; ++g) {
                 const int ta = group_at(it, ng, g), nt = group_at(it, ng, g + 1) - ta;
-                for (int qb = MANY ? first_block(it, ta) : 0; qb < it.nblk && ok; ++qb) {
+                for (int qb = it.q0; qb < it.q1 && ok; ++qb) {
                     const int qi = v % C::kQSlots;
                     if ((MANY || g == 0) && !wait(bar_qfull(qi), (v / C::kQSlots) & 1))
                         break;
@@ -322,11 +446,10 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                         const int i = 2 * ii + e;
                         if (i >= nt || !ok)
                             continue;
-                        const int f = MANY ? first_block(it, ta + i) : 0;
                         const int ki = (u + i) % C::kKSlots;
-                        if (qb >= f) {
-                            if (qb == f && !wait(bar_kfull(ki), ((u + i) / C::kKSlots) & 1))
-                                continue;
+                        if (qb == it.q0 && !wait(bar_kfull(ki), ((u + i) / C::kKSlots) & 1))
+                            continue;
+                        if (!MANY || qb >= first_block(p, it.L, it.q_len, ta + i)) {
                             if (uses[ii] > 0 && !wait(bar_sfree(i), (uses[ii] - 1) & 1))
                                 continue;
                             const uint64_t k0 = adv(d_k0, (uint32_t)ki * C::kKSlot);
@@ -342,7 +465,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                             mma_commit_warp(bar_s(i));
                             ++uses[ii];
                         }
-                        if (qb + 1 == it.nblk)               // the last row sees every tile
+                        if (qb + 1 == it.q1)
                             mma_commit_warp(bar_kempty(ki));
                     }
                     if (MANY || g + 1 == ng) {
@@ -362,7 +485,12 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
         wait_bar(bar_drain(e), 0, nullptr, kDrainLimit);
     } else if (warp == 3) {
         // ============================================================ the items; Q blocks, and their rows' lse and scale
-        Walk walk(p, run.lo, run.hi, any ? run.s : p.bs, run.before);
+        using Walk = std::conditional_t<MANY, UnitWalk, TileWalk>;
+        Walk walk(p, run, any ? run.s : p.bs);
+        AccumPiece *shared = p.shared + 2 * blockIdx.x;      // this run's parts of units that others have a part of
+        if (MANY && lane < 2)
+            shared[lane].s = -1;
+        __syncwarp();
         bool ok = true;
         int v = 0;
         for (int k = 0; ok; ++k) {
@@ -376,14 +504,15 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 break;
             if (lane == 0) {
                 ring[k % kRing] = it;
+                if (MANY && more && it.slot >= 0)
+                    shared[it.slot] = AccumPiece{it.s, it.h, it.a, it.ends};
                 mbar_arrive(bar_item(k % kRing));
             }
             __syncwarp();
             if (!more)
                 break;
-            const int ng = MANY ? groups_of(it) : 1;
-            for (int g = 0; g < ng && ok; ++g)
-                for (int qb = MANY ? first_block(it, group_at(it, ng, g)) : 0; qb < it.nblk && ok; ++qb, ++v) {
+            {
+                for (int qb = it.q0; qb < it.q1 && ok; ++qb, ++v) {
                     const int qi = v % C::kQSlots;
                     const int j0 = qb / p.nsub * p.tpb, i0 = (qb % p.nsub) * p.gb;
                     const int hq0 = it.h * p.G + i0;
@@ -424,6 +553,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                             mbar_arrive(bar_afull(qi));
                     }
                 }
+            }
         }
         if (!ok) {
             *abort_flag = 1;
@@ -448,16 +578,18 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 const int ta = group_at(it, ng, g), nt = group_at(it, ng, g + 1) - ta;
                 const int key = (ta + wg) * kKeys + tau;
                 const bool live = wg < nt && key < it.L;
-                float *place = nullptr;
-                if (live) {
+                float *place = nullptr;              // where the key's sum goes
+                if (live && it.slot >= 0)
+                    place = p.part + (2LL * blockIdx.x + it.slot) * (kGroup * kKeys) + wg * kKeys + tau;
+                else if (live) {
                     const int blk = __ldg(bt + key / kPage);
                     if (blk >= 0 && blk < p.num_blocks)
                         place = p.acc + ((long long)blk * p.H_kv + it.h) * kPage + key % kPage;
                 }
-                const int f = MANY ? first_block(it, ta + wg) : 0;
+                const int f = MANY ? first_block(p, it.L, it.q_len, ta + wg) : 0;
                 const int jmin = p.causal ? key - (it.L - it.q_len) : 0;       // first token that sees the key
                 float2 sum = make_float2(0.f, 0.f);
-                for (int qb = MANY ? first_block(it, ta) : 0; qb < it.nblk && ok; ++qb) {
+                for (int qb = it.q0; qb < it.q1 && ok; ++qb) {
                     const int qi = v % C::kQSlots;
                     if (MANY || g == 0)
                         ok = __all_sync(kFull, wait_bar(bar_afull(qi), (v / C::kQSlots) & 1, abort_flag,
@@ -521,8 +653,13 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                     }
                 }
                 // one addition per key (more only where sequences share a block)
-                if (ok && place != nullptr)
-                    atomicAdd(place, sum.x + sum.y);
+                if (ok && place != nullptr) {
+                    if (it.slot >= 0)
+                        *place = sum.x + sum.y;
+                    else
+                        atomicAdd(place, sum.x + sum.y);
+                }
+                __syncwarp();
             }
         }
         if (!ok)
@@ -535,6 +672,34 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Adds up the parts of the units that several runs share: block r those of the unit whose last part is run r's first.
+// Its other parts are the first ones of the runs before, back to the run that the unit starts in, whose last part it is;
+// they are added in the rows' order, whatever the timing of the runs.
+__global__ void __launch_bounds__(kGroup * kKeys) accum_join_kernel(const AccumParams p)
+{
+    __shared__ int slots[kAccumRuns], count;
+    wait_prior_grid();
+    const int index = blockIdx.x;
+    const AccumPiece pc = p.shared[2 * index];
+    if (pc.s < 0 || !pc.ends)
+        return;
+    if (threadIdx.x < 32) {
+        const int n = shared_slots(index, [&](int slot) { return p.shared[slot].s >= 0; }, slots);
+        if (threadIdx.x == 0)
+            count = n;
+    }
+    const int key = pc.a * kKeys + threadIdx.x;
+    const bool live = key < __ldg(p.seq_lens + pc.s);
+    const int blk = live ? __ldg(p.block_table + (long long)pc.s * p.bt_stride + key / kPage) : -1;
+    __syncthreads();
+    if (blk < 0 || blk >= p.num_blocks)
+        return;
+    float sum = 0.f;
+    for (int i = count - 1; i >= 0; --i)
+        sum += p.part[(long long)slots[i] * (kGroup * kKeys) + threadIdx.x];
+    atomicAdd(p.acc + ((long long)blk * p.H_kv + pc.h) * kPage + key % kPage, sum);
 }
 
 __global__ void __launch_bounds__(256) split_q_kernel(const uint16_t *__restrict__ q, long long rows,
@@ -573,8 +738,12 @@ cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const 
                                                C::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(accum_kernel<RB, MANY, FP8>, dim3((unsigned)num_sms), dim3(kThreads), C::kSmemBytes, stream,
-                      kv_map, q_map, p);
+    const int runs = num_sms < kAccumRuns ? num_sms : kAccumRuns;
+    const cudaError_t l = launch_pdl(accum_kernel<RB, MANY, FP8>, dim3((unsigned)runs), dim3(kThreads), C::kSmemBytes,
+                                     stream, kv_map, q_map, p);
+    if (!MANY || runs == 1 || l != cudaSuccess)
+        return l;
+    return launch_pdl(accum_join_kernel, dim3((unsigned)runs), dim3(kGroup * kKeys), 0, stream, p);
 }
 
 }  // namespace
@@ -595,7 +764,14 @@ int accum_block_rows(int G, long long max_q_len)
     return 128;
 }
 
-cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *q_codes, int num_sms, cudaStream_t stream)
+// Bytes of the workspace: for many rows the parts of shared units, and for e4m3 pages Q in two terms.
+long long accum_workspace_bytes(int num_tokens, int H_q, int H_kv, int max_q_len, int kv_dtype)
+{
+    const bool many = accum_block_rows(H_q / H_kv, max_q_len) == 128;
+    return (many ? kAccumParts : 0) + (kv_dtype == SK_KV_FP8_E4M3 ? (long long)num_tokens * H_q * (2 * kHeadDim + 4) : 0);
+}
+
+cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *workspace, int num_sms, cudaStream_t stream)
 {
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
     AccumParams p = params;
@@ -603,6 +779,12 @@ cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *q_codes,
     p.gb = p.G < rb ? p.G : rb;
     p.nsub = (p.G + p.gb - 1) / p.gb;
     p.tpb = rb / p.gb;
+    uint8_t *q_codes = static_cast<uint8_t *>(workspace);
+    if (rb == 128) {
+        p.part = static_cast<float *>(workspace);
+        p.shared = reinterpret_cast<AccumPiece *>(p.part + 2LL * kAccumRuns * kGroup * kKeys);
+        q_codes += kAccumParts;
+    }
     const void *q = p.q;
     if (fp8) {
         const long long rows = (long long)p.num_tokens * p.H_q;
@@ -610,7 +792,7 @@ cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *q_codes,
         if (e != cudaSuccess)
             return e;
         q = q_codes;
-        p.q_scale = reinterpret_cast<const float *>(static_cast<uint8_t *>(q_codes) + rows * 256);
+        p.q_scale = reinterpret_cast<const float *>(q_codes + rows * 256);
     }
     CUtensorMap kv_map, q_map;
     cudaError_t e = encode_page_map(&kv_map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 1 : 2);

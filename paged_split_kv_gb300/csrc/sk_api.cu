@@ -753,13 +753,13 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
     return SK_OK;
 }
 
-int64_t sk_accum_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype)
+int64_t sk_accum_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int max_q_len, int kv_dtype)
 {
-    if (num_tokens < 0 || num_q_heads < 1 || (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3))
-        return fail(SK_ERR_INVALID, "sk_accum_workspace_bytes: num_tokens=%d num_q_heads=%d kv_dtype=%d", num_tokens,
-                    num_q_heads, kv_dtype);
-    // e4m3 pages: Q's two terms and a scale per row
-    return kv_dtype == SK_KV_FP8_E4M3 ? (int64_t)num_tokens * num_q_heads * (2 * kHeadDim + 4) : 0;
+    if (num_tokens < 0 || max_q_len < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 ||
+        (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3))
+        return fail(SK_ERR_INVALID, "sk_accum_workspace_bytes: num_tokens=%d num_q_heads=%d num_kv_heads=%d max_q_len=%d "
+                    "kv_dtype=%d", num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype);
+    return accum_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype);
 }
 
 int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, float k_scale,
@@ -793,7 +793,7 @@ int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, flo
     if ((long long)num_blocks * num_kv_heads * 2 > 0x7FFFFFFFLL || (long long)num_q_heads * max_q_len > 0x3FFFFFFFLL)
         return fail(SK_ERR_UNSUPPORTED, "sk_accum_attn_weights: %d blocks of %d heads or %d query tokens of %d heads "
                     "exceed the kernel's limits (2^30)", num_blocks, num_kv_heads, max_q_len, num_q_heads);
-    const int64_t need = sk_accum_workspace_bytes(num_tokens, num_q_heads, kv_dtype);
+    const int64_t need = sk_accum_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype);
     if (workspace_bytes < need || (need > 0 && workspace == nullptr))
         return fail(SK_ERR_CAPACITY, "sk_accum_attn_weights: workspace of %lld bytes, %lld needed",
                     (long long)workspace_bytes, (long long)need);

@@ -291,6 +291,30 @@ __device__ __forceinline__ Run find_run(int bs, int index, int count, long long 
     return r;
 }
 
+// A run has two slots for its parts of what several runs share: 0 for one that does not start it, 1 for one that does.
+// The slots of the parts of what ends in `index`'s slot 0, the last one first: the first slots of the runs before, back to
+// the run with a part that starts it.  Called by a warp; returns how many.
+template <typename Used>
+__device__ __forceinline__ int shared_slots(int index, Used used, int *slots)
+{
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int r0 = index; r0 >= 0; r0 -= 32) {
+        const int r = r0 - lane;
+        const bool first = r >= 0 && r < index && used(2 * r + 1);
+        const uint32_t starts = __ballot_sync(0xffffffffu, first);
+        const int stop = starts ? __ffs(starts) - 1 : 31;
+        const bool has = r >= 0 && lane <= stop && (first || used(2 * r));
+        const uint32_t all = __ballot_sync(0xffffffffu, has);
+        if (has)
+            slots[n + __popc(all & ((1u << lane) - 1u))] = 2 * r + (first ? 1 : 0);
+        n += __popc(all);
+        if (starts)
+            break;
+    }
+    return n;
+}
+
 // Q as two e4m3 terms for e4m3 pages: row (t, hq) becomes 128 hi codes, then 128 lo codes at codes + 256 * row, and
 // 2^-e in the float array behind them.
 cudaError_t launch_split_q(const uint16_t *q, long long rows, void *codes, cudaStream_t stream);

@@ -197,6 +197,12 @@ struct PrefillParams {
 long long prefill_workspace_bytes(int num_tokens, int H_q, int kv_dtype, int num_sms);
 cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,
                            cudaStream_t stream);
+// A run's part of a unit that others share: the keys from tile a on of a sequence and head, and whether it has the unit's
+// last rows.
+struct AccumPiece {
+    int s, h, a, ends;
+};
+
 // Gathered attention weights, resolved on the host.
 struct AccumParams {
     const uint16_t *q;           // bf16 bits [NT, H_q, D]
@@ -213,8 +219,11 @@ struct AccumParams {
     int causal;
     float score_scale_log2;
     long long wait_limit;
+    float *part;                 // workspace, set by the launcher: sums of shared units, and what they are parts of
+    AccumPiece *shared;
 };
-cudaError_t launch_accum(const AccumParams &p, int kv_dtype, void *q_codes, int num_sms, cudaStream_t stream);
+long long accum_workspace_bytes(int num_tokens, int H_q, int H_kv, int max_q_len, int kv_dtype);
+cudaError_t launch_accum(const AccumParams &p, int kv_dtype, void *workspace, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16_t *v, long long q_stride,
                               long long k_stride, long long v_stride, const int64_t *pos, const double *freqs,
                               const int64_t *slots, int num_tokens, int hq, int hkv, int rot, int interleaved,

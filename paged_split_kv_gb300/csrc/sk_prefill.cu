@@ -825,6 +825,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                 fence_proxy_async_smem();
                 if (!ok)
                     *abort_flag = 1;                               // the other roles' waits end with it
+                __syncwarp();
             }
             // P overwrites the first columns of each half of S.  A row's reference need not follow its maximum while
             // the probabilities stay well inside their type's range, and the tile's sum shows whether some did not.
@@ -916,6 +917,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
             for (int i = 0; i < 4; ++i)
                 if (to_row[i] >= 0)
                     *reinterpret_cast<uint4 *>(dst + (long long)to_row[i] * row_bytes + at) = w[i];
+            __syncwarp();
         }
         if (live) {
             if (!whole) {
@@ -1010,21 +1012,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        // from this run back, 32 at a time, until a piece that starts the unit; then in key order
-        int n = 0;
-        for (int r0 = index; r0 >= 0; r0 -= 32) {
-            const int r = r0 - lane;
-            const bool last = r >= 0 && r < index && p.shared[2 * r + 1].s >= 0;
-            const uint32_t ends = __ballot_sync(kFull, last);
-            const int stop = ends ? __ffs(ends) - 1 : 31;
-            const bool has = r >= 0 && lane <= stop && (last || p.shared[2 * r].s >= 0);
-            const uint32_t all = __ballot_sync(kFull, has);
-            if (has)
-                slots[n + __popc(all & ((1u << lane) - 1u))] = 2 * r + (last ? 1 : 0);
-            n += __popc(all);
-            if (ends)
-                break;
-        }
+        const int n = shared_slots(index, [&](int slot) { return p.shared[slot].s >= 0; }, slots);
         if (lane == 0)
             count = n;
     }

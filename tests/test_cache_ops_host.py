@@ -171,12 +171,15 @@ def test_accum_refusals(sk):
                dict(scale=-1.0), dict(dt=1, ks=0.0), dict(kv=ODD), dict(ws=ODD)):
         assert call(**kw) == -1, kw
     assert call(d=64) == -3 and call(page=32) == -3 and call(nb=1 << 30) == -3
-    need = sk.sk_accum_workspace_bytes(16, 32, 1)
-    assert need == 16 * 32 * 260 and sk.sk_accum_workspace_bytes(16, 32, 0) == 0
+    need = sk.sk_accum_workspace_bytes(16, 32, 2, 4, 1)
+    assert need == 16 * 32 * 260 and sk.sk_accum_workspace_bytes(16, 32, 2, 4, 0) == 0
+    parts = sk.sk_accum_workspace_bytes(16, 32, 2, 5, 0)
+    assert parts > 0 and sk.sk_accum_workspace_bytes(16, 32, 2, 5, 1) == need + parts
+    assert call(mq=5, ws=FAKE, wb=parts - 1) == -2 and call(mq=5) == -2
     assert call(dt=1, ws=FAKE, wb=need - 1) == -2 and call(dt=1, ws=None, wb=need) == -2
     assert call(nt=0, mq=0) == 0
     with pytest.raises(sk.SkError):
-        sk.sk_accum_workspace_bytes(16, 0, 1)
+        sk.sk_accum_workspace_bytes(16, 0, 2, 4, 1)
 
 
 def test_binding_checks_attention_shapes(sk):
