@@ -63,7 +63,8 @@ struct ACfg {
     static constexpr int kAuxEach = FP8 ? 2 * RB : RB;             // floats per Q block: -lse, and e4m3's scales
     static constexpr int kMisc = FP8 ? 4096 : 3072;
     static constexpr int kFit = (kMaxSmem - kQSlots * kQSlot - kMisc) / kKSlot;
-    static constexpr int kKSlots = kFit < 12 ? kFit : 12;
+    static constexpr int kKSlots = (kFit < 12 ? kFit : 12) / 2 * 2;        // every other one for either issuer
+    static constexpr int kHalf = kKSlots / 2;
     static constexpr int kOffQ = kKSlots * kKSlot;
     static constexpr int kOffMisc = kOffQ + kQSlots * kQSlot;
     static constexpr int kSmemBytes = kOffMisc + kMisc;
@@ -373,7 +374,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
         // ============================================================ K pages
         if (lane == 0)
             prefetch_tensormap(&kv_map);
-        int u = 0;                                   // tiles issued
+        int used[2] = {0, 0};                        // tiles issued for either issuer
         bool ok = true;
         while (ok && next_item(it, ok)) {
             const int page_end = (it.L + kPage - 1) / kPage;
@@ -383,10 +384,18 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 return (lane < C::kPagesPerTile && t < it.b && pg < page_end) ? __ldg(bt + pg) : -1;
             };
             int blk[3] = {block_at(it.a), block_at(it.a + 1), block_at(it.a + 2)};
-            for (int t = it.a; t < it.b && ok; ++t, ++u) {
-                const int i = u % C::kKSlots;
-                if (u >= C::kKSlots)
-                    ok = wait_bar(bar_kempty(i), (u / C::kKSlots - 1) & 1, abort_flag, p.wait_limit);
+            const int ng = groups_of(it);
+            int g = 0, e = 0, end = group_at(it, ng, 1);
+            for (int t = it.a; t < it.b && ok; ++t, e ^= 1) {
+                if (t == end) {
+                    ++g;
+                    end = group_at(it, ng, g + 1);
+                    e = 0;
+                }
+                const int n = e ? used[1] : used[0];
+                const int i = 2 * (n % C::kHalf) + e;
+                if (n >= C::kHalf)
+                    ok = wait_bar(bar_kempty(i), (n / C::kHalf - 1) & 1, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 if (!ok)
                     break;
@@ -406,6 +415,8 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 blk[0] = blk[1];
                 blk[1] = blk[2];
                 blk[2] = block_at(t + 3);
+                used[0] += 1 - e;
+                used[1] += e;
             }
         }
         if (!ok) {
@@ -413,17 +424,20 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             if (lane == 0)
                 atomicOr(p.status, SK_DEV_TIMEOUT);
         }
-        for (int t = u > C::kKSlots ? u - C::kKSlots : 0; t < u; ++t)
-            wait_bar(bar_kfull(t % C::kKSlots), (t / C::kKSlots) & 1, nullptr, kDrainLimit);
+        for (int e = 0; e < 2; ++e)
+            for (int t = max(0, used[e] - C::kHalf); t < used[e]; ++t)
+                wait_bar(bar_kfull(2 * (t % C::kHalf) + e), (t / C::kHalf) & 1, nullptr, kDrainLimit);
     } else if (warp <= 2) {
         // ============================================================ products: tiles 0 and 2 of a group, or 1 and 3
+        // Either issuer has every other K slot for itself: a barrier shows only whether the last phase of a parity is
+        // over, so each of a slot's phases has to be waited for by the same warp.
         const int e = warp - 1;
         constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(kKeys, RB, 0, 0) : idesc_bf16_f32(kKeys, RB, 0, 0);
         const uint64_t d_k0 = smem_desc_sw128(sbase, 16, C::kGroupBytes);
         const uint64_t d_q0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
         auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
         bool ok = true;
-        int u = 0, v = 0;                            // K tiles and Q blocks used up
+        int u = 0, v = 0;                            // own K tiles and Q blocks used up
         uint32_t uses[kGroup / 2] = {0, 0};          // products of each TMEM buffer of this issuer
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if (ok)
@@ -446,8 +460,8 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                         const int i = 2 * ii + e;
                         if (i >= nt || !ok)
                             continue;
-                        const int ki = (u + i) % C::kKSlots;
-                        if (qb == it.q0 && !wait(bar_kfull(ki), ((u + i) / C::kKSlots) & 1))
+                        const int ki = 2 * ((u + ii) % C::kHalf) + e;
+                        if (qb == it.q0 && !wait(bar_kfull(ki), ((u + ii) / C::kHalf) & 1))
                             continue;
                         if (!MANY || qb >= first_block(p, it.L, it.q_len, ta + i)) {
                             if (uses[ii] > 0 && !wait(bar_sfree(i), (uses[ii] - 1) & 1))
@@ -473,7 +487,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                         ++v;
                     }
                 }
-                u += nt;
+                u += (nt + 1 - e) / 2;
             }
         }
         if (!ok) {

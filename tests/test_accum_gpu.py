@@ -114,6 +114,25 @@ def test_many_tiles_and_the_same_bits_twice(lens, qs, hq, hkv, fp8):
     assert math.isclose(acc.double().sum().item(), w.num_tokens * hq, rel_tol=1e-5)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,qs,hq,hkv", [([700, 1, 400, 1025, 130, 0, 513] * 20, [1, 1, 2, 4, 3, 1, 0] * 20, 16, 8),
+                                            ([1500, 260, 129, 2600] * 20, [1, 2, 1, 4] * 20, 32, 8),
+                                            ([700, 200, 1800] * 20, [70, 150, 40] * 20, 8, 2)])
+def test_many_short_sequences_a_run(lens, qs, hq, hkv, fp8):
+    """Every ring of a CTA turns over several times between short items: the same bits in each of many calls."""
+    b = batch(lens, qs, hq, hkv, fp8, 52)
+    lse = attention(b)[1].float()
+    acc0 = start(b, 3)
+    acc = acc0.clone()
+    run(b, lse, acc)
+    for _ in range(20):
+        again = acc0.clone()
+        run(b, lse, again)
+        assert torch.equal(acc, again)
+    assert sk.sk_get_device_status() == 0
+    check(b, lse, acc0, acc)
+
+
 def test_rows_that_saw_nothing_add_nothing():
     b = batch([500, 200], [3, 2], 4, 1, False, 61)
     lse = attention(b)[1].float()
