@@ -370,6 +370,8 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
         return MANY ? (g ? w.b : w.a) : w.a + (int)((long long)(w.b - w.a) * g / ng);
     };
 
+    auto first_token = [&](int qb) { return p.nsub > 1 ? qb / p.nsub : qb * p.tpb; };      // (nsub > 1: tpb is 1)
+
     if (warp == 0) {
         // ============================================================ K pages
         if (lane == 0)
@@ -528,7 +530,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
             {
                 for (int qb = it.q0; qb < it.q1 && ok; ++qb, ++v) {
                     const int qi = v % C::kQSlots;
-                    const int j0 = qb / p.nsub * p.tpb, i0 = (qb % p.nsub) * p.gb;
+                    const int j0 = first_token(qb), i0 = p.nsub > 1 ? (qb % p.nsub) * p.gb : 0;
                     const int hq0 = it.h * p.G + i0;
                     if (v >= C::kQSlots) {
                         ok = wait_bar(bar_qempty(qi), (v / C::kQSlots - 1) & 1, abort_flag, p.wait_limit);
@@ -605,17 +607,20 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 float2 sum = make_float2(0.f, 0.f);
                 for (int qb = it.q0; qb < it.q1 && ok; ++qb) {
                     const int qi = v % C::kQSlots;
+                    // S is there long after the rows' lse: both barriers are tested at once (each test takes 200 cycles)
+                    const bool work = wg < nt && qb >= f;
+                    const bool early = work && sm100::mbar_test_wait(bar_s(wg), uses & 1);
                     if (MANY || g == 0)
                         ok = __all_sync(kFull, wait_bar(bar_afull(qi), (v / C::kQSlots) & 1, abort_flag,
                                                                  p.wait_limit));
-                    if (ok && wg < nt && qb >= f) {
-                        ok = wait_bar(bar_s(wg), uses & 1, abort_flag, p.wait_limit);
+                    if (ok && work) {
+                        ok = early || wait_bar(bar_s(wg), uses & 1, abort_flag, p.wait_limit);
                         ++uses;
                         ok = __all_sync(kFull, ok);
                         if (ok) {
                             tc_fence_after();
                             const float *aux = reinterpret_cast<const float *>(misc + C::kAux) + qi * C::kAuxEach;
-                            const int j0 = qb / p.nsub * p.tpb;
+                            const int j0 = first_token(qb);
                             // rows [rmin, rows) of the block see this key
                             const int rmin = jmin > j0 ? (jmin - j0) * p.gb : 0;
                             const int rows = p.nsub > 1 ? min(p.gb, p.G - qb % p.nsub * p.gb)
