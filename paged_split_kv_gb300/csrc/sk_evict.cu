@@ -9,11 +9,14 @@
 //
 // The threshold is found by radix selection on a 32-bit key that orders like the weight (11, 11 and 10 bits, fewer
 // when a digit settles it): histogram in shared memory, then the digit that holds the budget-th largest key.  One
-// cluster of up to 16 CTAs serves a (sequence, head); each CTA keeps the keys of its contiguous share of the rows in
-// shared memory (the first 51200 of them), so weights and positions are read once, four rows a load, and the cluster's histograms and counts
-// are summed through distributed shared memory.  Two walks over the keys follow: one counts, per warp, the rows above
-// the threshold and at it, below and past row `budget` (from these counts of all warps and CTAs follows how many ties
-// each may take and where its lists start), one writes the lists.  Nothing depends on timing.
+// cluster of up to 16 CTAs serves a (sequence, head); each CTA keeps the keys of its contiguous share of the rows, the
+// first 49152 in shared memory and 16384 more in registers, so weights and positions are read once, four rows a load, and the
+// cluster's histograms and counts are summed through distributed shared memory.  Two walks over the keys follow: one
+// counts, per warp, the rows above the threshold and at it, below and past row `budget` (from these counts of all warps
+// and CTAs follows how many ties each may take and where its lists start), one writes the lists.  Nothing depends on
+// timing.  Bound by instructions, a few per row and pass: four rows a lane throughout, with a path without masks for
+// whole blocks of 128 rows (32 heads of up to 248k rows, 62k rows a CTA: load and first digit 18.5 us, second digit
+// 8.5, walks 4 and 9, three exchanges 8).
 //
 // Move.  One warp (half a warp for e4m3 rows) copies a row of 2 * head_dim elements, 16 bytes a lane, its
 // weight and its position; several rows are in flight per warp.
@@ -34,7 +37,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kEvictKept = 51200;                // keys (200 KB) that a CTA keeps in shared memory beside its histograms
+constexpr int kAtOnce = 4;                       // row quads a thread loads at once
+// Row quads of a CTA that are kept: the first in shared memory (192 KB, beside the histograms), the next in registers.
+constexpr int kSharedQuads = 12 * kSelThreads, kKeptQuads = kSharedQuads + kAtOnce * kSelThreads;
 
 struct SelectArgs {
     const float *acc;
@@ -45,7 +50,6 @@ struct SelectArgs {
     int32_t *src, *dst, *counts, *new_lens;
     int *status;
     int bt_stride, num_blocks, hkv, budget, recent, cap, max_len;
-    int kept;                                    // rows per CTA whose keys fit in shared memory
 };
 
 // Rows above the threshold and at it, below row `budget` (low) and from it on.
@@ -71,21 +75,25 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 
 __device__ __forceinline__ uint32_t warp_sum_u32(uint32_t v) { return __reduce_add_sync(kFull, v); }
 
-// Counts one digit of the warp's live keys.  Equal digits in the whole warp (rows never looked at, all zero) would
-// serialise: one addition for all.
-__device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t digit, bool live)
+// Counts one digit of the live ones among four keys a lane.  Equal digits in the whole warp (rows never looked at, all
+// zero) would serialise: one addition for all.
+__device__ __forceinline__ void count_digits(uint32_t *hist, const uint4 &digit, bool m0, bool m1, bool m2, bool m3)
 {
-    const uint32_t active = __ballot_sync(kFull, live);
-    if (active == 0)
+    const uint32_t first = __shfl_sync(kFull, digit.x, 0);
+    const bool same = digit.x == first && digit.y == first && digit.z == first && digit.w == first;
+    if (__all_sync(kFull, same && m0 && m1 && m2 && m3)) {
+        if ((threadIdx.x & 31) == 0)
+            atomicAdd(hist + first, 128u);
         return;
-    const int first_lane = __ffs(active) - 1;
-    const uint32_t first = __shfl_sync(kFull, digit, first_lane);
-    if (__all_sync(kFull, !live || digit == first)) {
-        if ((int)(threadIdx.x & 31) == first_lane)
-            atomicAdd(hist + first, (uint32_t)__popc(active));
-    } else if (live) {
-        atomicAdd(hist + digit, 1u);
     }
+    if (m0)
+        atomicAdd(hist + digit.x, 1u);
+    if (m1)
+        atomicAdd(hist + digit.y, 1u);
+    if (m2)
+        atomicAdd(hist + digit.z, 1u);
+    if (m3)
+        atomicAdd(hist + digit.w, 1u);
 }
 
 // Lane l holds the counts of the l-th of up to 32 consecutive parts of a row range.  Ties are taken in row order while
@@ -115,9 +123,8 @@ __device__ __forceinline__ Part part_of(const Counts &c, int first_row, int rows
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a)
 {
-    extern __shared__ uint4 keys4[];             // four rows each, the first a.kept rows of this CTA's
+    extern __shared__ uint4 keys4[];             // four rows each, the first kSharedQuads of this CTA's
     __shared__ SelectShared sh;
-    const uint32_t *keys = reinterpret_cast<const uint32_t *>(keys4);
     cg::cluster_group cluster = cg::this_cluster();
     const int csize = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -174,9 +181,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     auto quad_key = [&](const float4 &w, const int4 &p) {
         return make_uint4(key_of(w.x, p.x), key_of(w.y, p.y), key_of(w.z, p.z), key_of(w.w, p.w));
     };
-    auto quad_at = [&](int i) {                  // as kept, or computed again past what is kept
-        if (4 * i < a.kept)
-            return i < quads ? keys4[i] : make_uint4(0u, 0u, 0u, 0u);
+    auto quad_again = [&](int i) {               // computed again, past what is kept
         float4 w;
         int4 p;
         load_quad(i, block_of(i), w, p);
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     };
 
     // ---- keys, and the first digit's histogram
-    constexpr int kAtOnce = 4;
+    uint4 held[kAtOnce] = {};                    // this thread's quads kSharedQuads + u * kSelThreads + tid
     int blk[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
@@ -205,35 +210,45 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
             if (i - lane >= quads)
                 break;                           // uniform in the warp
             const uint4 k = quad_key(w[u], p[u]);
-            if (i < quads && 4 * i < a.kept)
-                keys4[i] = k;
-            count_digit(sh.hist[0], k.x >> 21, 4 * i < n);
-            count_digit(sh.hist[0], k.y >> 21, 4 * i + 1 < n);
-            count_digit(sh.hist[0], k.z >> 21, 4 * i + 2 < n);
-            count_digit(sh.hist[0], k.w >> 21, 4 * i + 3 < n);
+            if (i < kSharedQuads) {
+                if (i < quads)
+                    keys4[i] = k;
+            } else if (i < kKeptQuads) {
+                held[u] = k;
+            }
+            count_digits(sh.hist[0], make_uint4(k.x >> 21, k.y >> 21, k.z >> 21, k.w >> 21), 4 * i < n, 4 * i + 1 < n,
+                         4 * i + 2 < n, 4 * i + 3 < n);
         }
     }
 
     // ---- the budget-th largest key, digit by digit, until a digit's keys are all taken
     uint32_t prefix = 0, mask = 0, want = (uint32_t)a.budget;    // keys still to take among those with this prefix
+    int used = 0;                                // digits
 #pragma unroll 1
     for (int d = 0; d < 3; ++d) {
         const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
         if (d > 0) {
             const uint32_t digit = d == 1 ? 0x7FFu : 0x3FFu;
-#pragma unroll 1
-            for (int i = tid; i - lane < quads; i += kSelThreads) {
-                const uint4 k = quad_at(i);
+            auto count_quad = [&](int i, const uint4 &k) {
                 const int left = n - 4 * i;
                 const bool m0 = left > 0 && (k.x & mask) == prefix, m1 = left > 1 && (k.y & mask) == prefix;
                 const bool m2 = left > 2 && (k.z & mask) == prefix, m3 = left > 3 && (k.w & mask) == prefix;
                 if (!__any_sync(kFull, m0 || m1 || m2 || m3))
-                    continue;
-                count_digit(sh.hist[d], k.x >> shift & digit, m0);
-                count_digit(sh.hist[d], k.y >> shift & digit, m1);
-                count_digit(sh.hist[d], k.z >> shift & digit, m2);
-                count_digit(sh.hist[d], k.w >> shift & digit, m3);
-            }
+                    return;
+                count_digits(sh.hist[d], make_uint4(k.x >> shift & digit, k.y >> shift & digit, k.z >> shift & digit,
+                                                    k.w >> shift & digit), m0, m1, m2, m3);
+            };
+            const int in_shared = min(quads, kSharedQuads);
+#pragma unroll 1
+            for (int i = tid; i - lane < in_shared; i += kSelThreads)
+                count_quad(i, i < in_shared ? keys4[i] : make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+                if (kSharedQuads + u * kSelThreads + tid - lane < quads)
+                    count_quad(kSharedQuads + u * kSelThreads + tid, held[u]);
+#pragma unroll 1
+            for (int i = kKeptQuads + tid; i - lane < quads; i += kSelThreads)
+                count_quad(i, quad_again(i));
         }
         meet();                                  // every CTA's histogram is complete
         // thread t holds bins 2 t and 2 t + 1, summed over the cluster; suffix sums from the top bin down
@@ -269,38 +284,77 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         prefix |= sh.found_digit << shift;
         mask = 0xFFFFFFFFu << shift;
         want -= sh.found_above;
+        ++used;
         if (sh.found_count == want)
             break;                               // the same in every thread of the cluster
     }
     // rows with (key & mask) above `prefix` stay, and the first `want` rows that equal it
 
-    // ---- first walk: a warp's rows are contiguous, [w0, w1) of this CTA's; those before wm lie below the budget
-    const int per_warp = (n + kSelThreads - 1) / kSelThreads * 32;
-    const int w0 = min(n, warp * per_warp), w1 = min(n, w0 + per_warp), wm = min(w1, max(w0, a.budget - lo));
-    auto key_at = [&](int i) {
-        if (i < a.kept)
-            return keys[i] & mask;
-        const int blk1 = __ldg(bt + (lo + i) / kPage);
-        if (blk1 < 0 || blk1 >= a.num_blocks)
-            return weight_key(-CUDART_INF_F) & mask;
-        const long long at = ((long long)blk1 * a.hkv + h) * kPage + (lo + i) % kPage;
-        return key_of(a.acc[at], a.recent > 0 ? a.pos[at] : 0) & mask;
+    const uint32_t top = prefix | ~mask;         // the largest key of that prefix
+    // Of four rows, bits 0-3: above the threshold; bits 4-7: at it.
+    auto classes = [&](const uint4 &k) {
+        const uint32_t gt = (uint32_t)(k.x > top) | (uint32_t)(k.y > top) << 1 | (uint32_t)(k.z > top) << 2 |
+                            (uint32_t)(k.w > top) << 3;
+        const uint32_t ge = (uint32_t)(k.x >= prefix) | (uint32_t)(k.y >= prefix) << 1 |
+                            (uint32_t)(k.z >= prefix) << 2 | (uint32_t)(k.w >= prefix) << 3;
+        return gt | (ge ^ gt) << 4;
     };
-    Counts mine = {0, 0, 0, 0};
-#pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-        uint32_t gt = 0, eq = 0;
-#pragma unroll 4
-        for (int i = (part ? wm : w0) + lane; i < (part ? w1 : wm); i += 32) {
-            const uint32_t k = key_at(i);
-            gt += k > prefix;
-            eq += k == prefix;
-        }
-        gt = warp_sum_u32(gt);
-        eq = warp_sum_u32(eq);
-        (part ? mine.above_high : mine.above_low) = gt;
-        (part ? mine.ties_high : mine.ties_low) = eq;
+    // the quads in registers lie at other warps than those that walk over them: their classes go to a histogram that
+    // no CTA reads any more
+    uint8_t *flags = reinterpret_cast<uint8_t *>(sh.hist[used % 3]);
+    if (quads > kSharedQuads) {
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+            flags[u * kSelThreads + tid] = (uint8_t)classes(held[u]);
+        __syncthreads();
     }
+
+    // ---- first walk: a warp's rows are contiguous, [w0, w1) of this CTA's, four a lane; those before wm lie below the
+    // budget
+    const int per_warp = (n + 4 * kSelThreads - 1) / (4 * kSelThreads) * 128;
+    const int w0 = min(n, warp * per_warp), w1 = min(n, w0 + per_warp), wm = min(w1, max(w0, a.budget - lo));
+    // classes of rows [r, r + 4), of those before w1, and which of them lie below the budget
+    auto quad_classes = [&](int r, uint32_t &low) {
+        const int i = r / 4;
+        low = 0;
+        if (r >= w1)
+            return 0u;
+        const uint32_t c = i < kSharedQuads  ? classes(keys4[i])
+                           : i < kKeptQuads ? flags[i - kSharedQuads]
+                                            : classes(quad_again(i));
+        low = wm - r >= 4 ? 15u : (1u << max(0, wm - r)) - 1u;
+        const uint32_t real = w1 - r >= 4 ? 15u : (1u << (w1 - r)) - 1u;
+        return c & (real | real << 4);
+    };
+    // 128 rows from r0 on that are real, kept in shared memory and on one side of the budget need no masks
+    auto plain = [&](int r0) { return r0 + 128 <= min(w1, 4 * kSharedQuads) && (r0 + 128 <= wm || r0 >= wm); };
+    Counts mine = {0, 0, 0, 0};
+#pragma unroll 2
+    for (int r = w0 + 4 * lane; r - 4 * lane < w1; r += 128) {
+        if (plain(r - 4 * lane)) {
+            const uint4 k = keys4[r / 4];
+            const uint32_t gt = (k.x > top) + (k.y > top) + (k.z > top) + (k.w > top);
+            const uint32_t eq = (k.x >= prefix) + (k.y >= prefix) + (k.z >= prefix) + (k.w >= prefix) - gt;
+            if (r - 4 * lane < wm) {
+                mine.above_low += gt;
+                mine.ties_low += eq;
+            } else {
+                mine.above_high += gt;
+                mine.ties_high += eq;
+            }
+            continue;
+        }
+        uint32_t low;
+        const uint32_t c = quad_classes(r, low), gt = c & 15u, eq = c >> 4;
+        mine.above_low += __popc(gt & low);
+        mine.ties_low += __popc(eq & low);
+        mine.above_high += __popc(gt & ~low);
+        mine.ties_high += __popc(eq & ~low);
+    }
+    mine.above_low = warp_sum_u32(mine.above_low);
+    mine.ties_low = warp_sum_u32(mine.ties_low);
+    mine.above_high = warp_sum_u32(mine.above_high);
+    mine.ties_high = warp_sum_u32(mine.ties_high);
     if (lane == 0)
         sh.warp[warp] = mine;
     __syncthreads();
@@ -340,30 +394,78 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         tail0 += warp_sum_u32(lane < warp ? part.tails : 0u);
     }
 
-    // ---- second walk: the lists, 32 rows at a time
+    // ---- second walk: the lists, 128 rows at a time
     const uint32_t below = (1u << lane) - 1u;
+    int32_t *dst = a.dst + (long long)pair * a.cap, *src = a.src + (long long)pair * a.cap;
 #pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-        int32_t *list = (part ? a.src : a.dst) + (long long)pair * a.cap;
-        const int end = part ? w1 : wm;
-        uint32_t at = part ? tail0 : hole0;
-#pragma unroll 4
-        for (int i0 = part ? wm : w0; i0 < end; i0 += 32) {
-            const int i = i0 + lane;
-            const bool live = i < end;
-            const uint32_t k = live ? key_at(i) : 0u;
-            bool stays = k > prefix;
-            const uint32_t eq = __ballot_sync(kFull, live && k == prefix);
-            if (eq != 0) {
-                stays = stays || ((eq >> lane & 1u) && tie0 + __popc(eq & below) < want);
-                tie0 += __popc(eq);
+    for (int r = w0 + 4 * lane; r - 4 * lane < w1; r += 128) {
+        const int r0 = r - 4 * lane;
+        if (plain(r0)) {                         // row r0 + 32 j + lane is this lane's: fewer instructions a row
+            int32_t *list = r0 < wm ? dst : src;
+            const uint32_t flip = r0 < wm ? kFull : 0u;
+            uint32_t at = r0 < wm ? hole0 : tail0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t k = reinterpret_cast<const uint32_t *>(keys4)[r0 + 32 * j + lane];
+                uint32_t stays = __ballot_sync(kFull, k > top);
+                const uint32_t ties = __ballot_sync(kFull, k >= prefix) ^ stays;
+                if (ties != 0) {                 // they stay in row order while there is room
+                    stays |= __ballot_sync(kFull, (ties >> lane & 1u) && tie0 + __popc(ties & below) < want);
+                    tie0 += __popc(ties);
+                }
+                const uint32_t listed = stays ^ flip, to = at + __popc(listed & below);
+                if ((listed >> lane & 1u) && to < (uint32_t)a.cap)
+                    list[to] = lo + r0 + 32 * j + lane;
+                at += __popc(listed);
             }
-            const uint32_t listed = __ballot_sync(kFull, live && stays == (part != 0));
-            const uint32_t to = at + __popc(listed & below);
-            if ((listed >> lane & 1u) && to < (uint32_t)a.cap)
-                list[to] = lo + i;
-            at += __popc(listed);
+            (r0 < wm ? hole0 : tail0) = at;
+            continue;
         }
+        uint32_t low;
+        const uint32_t c = quad_classes(r, low);
+        const uint32_t real = r >= w1 ? 0u : w1 - r >= 4 ? 15u : (1u << (w1 - r)) - 1u;
+        uint32_t stays = c & 15u;
+        if (__any_sync(kFull, c >> 4 != 0)) {    // ties stay in row order while there is room
+            const uint32_t ties = __popc(c >> 4);
+            uint32_t incl = ties;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(kFull, incl, o);
+                incl += lane >= o ? u : 0u;
+            }
+            uint32_t room = want > tie0 + incl - ties ? want - (tie0 + incl - ties) : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool take = (c >> (4 + j) & 1u) && room > 0;
+                stays |= take ? 1u << j : 0u;
+                room -= take ? 1u : 0u;
+            }
+            tie0 += __shfl_sync(kFull, incl, 31);
+        }
+        const uint32_t holes = ~stays & low & real, tails = stays & ~low & real;
+        // rows of either list in the lanes before, and in all
+        const uint32_t num = __popc(holes) | __popc(tails) << 16;
+        uint32_t incl = num;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(kFull, incl, o);
+            incl += lane >= o ? u : 0u;
+        }
+        const uint32_t all_here = __shfl_sync(kFull, incl, 31);
+        auto write = [&](int32_t *list, uint32_t rows, uint32_t to) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if ((rows >> j & 1u) && to < (uint32_t)a.cap)
+                    list[to] = lo + r + j;
+                to += rows >> j & 1u;
+            }
+        };
+        if (r0 < wm)
+            write(dst, holes, hole0 + (incl - num & 0xFFFFu));
+        if (r0 + 128 > wm)
+            write(src, tails, tail0 + (incl - num >> 16));
+        hole0 += all_here & 0xFFFFu;
+        tail0 += all_here >> 16;
     }
     if (csize > 1)
         cluster.barrier_wait();                  // no CTA leaves while another reads its counts
@@ -450,23 +552,22 @@ cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int3
                                 int32_t *counts, int32_t *new_lens, int *status, int num_sms, cudaStream_t stream)
 {
     // As many CTAs per cluster as there are SMs for, up to 8 (more need a whole GPC, which few clusters can have at a
-    // time), or as many as keep all rows in shared memory, up to 16; each has 4096 rows or more.  (32 clusters for up
-    // to 248k rows: 5 CTAs, which keep all rows but do not all run at once, 67 us; 4, which all run but read a sixth of
-    // their rows again in each pass, 91 us; 6 72 us, 8 86 us.)
+    // time), or as many as keep all rows, up to 16; each has 4096 rows or more.  (32 clusters for up to 248k rows: 4
+    // CTAs, which all run at once, 50 us; 5, 59 us; 6, 64; 8, 78.)
     const int pairs = bs * hkv;
     int c = num_sms / pairs;
     c = c < 8 ? c : 8;
-    const int fit = (max_len + kEvictKept - 1) / kEvictKept;
+    const int fit = (max_len + 4 * kKeptQuads - 1) / (4 * kKeptQuads);
     c = c > fit ? c : fit;
     c = c < 16 ? c : 16;
     c = c < (max_len + 4095) / 4096 ? c : (max_len + 4095) / 4096;
     c = c > 1 ? c : 1;
     const int chunk = ((max_len + c - 1) / c + 127) / 128 * 128;
     SelectArgs a{acc, pos, block_table, seq_lens, next_pos, src, dst, counts, new_lens, status,
-                 bt_stride, num_blocks, hkv, budget, recent, cap, max_len, chunk < kEvictKept ? chunk : kEvictKept};
-    const size_t smem = (size_t)a.kept * 4;
+                 bt_stride, num_blocks, hkv, budget, recent, cap, max_len};
+    const size_t smem = (size_t)(chunk < 4 * kSharedQuads ? chunk : 4 * kSharedQuads) * 4;
     cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kEvictKept * 4);
+                                         kSharedQuads * 16);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess)
