@@ -681,8 +681,11 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
                 __syncwarp();
             }
         }
-        if (!ok)
+        if (!ok) {
             *abort_flag = 1;
+            if (lane == 0)
+                atomicOr(p.status, SK_DEV_TIMEOUT);
+        }
     }
 
     tc_fence_before();

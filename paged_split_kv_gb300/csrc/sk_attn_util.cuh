@@ -106,27 +106,26 @@ __device__ __forceinline__ void split_q_row(uint2 raw, uint32_t &hi, uint32_t &l
 }
 
 // Waits for the phase with the given parity like mbar_wait_bounded, in few instructions (every role waits in many places,
-// and their code shares the instruction cache): a test, then suspended waits that a limit below kPollBelowCycles asks not
-// to suspend.
+// and their code shares the instruction cache): a test, then suspended waits.  One that ends later than the limit allows
+// has failed, whether the phase is over by then or not, so that a short limit expires although try_wait suspends.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int *abort, long long limit)
 {
     if (sm100::mbar_test_wait(bar, parity))
         return true;
-    const uint32_t hint = limit < sm100::kPollBelowCycles ? 0u : 0x989680u;      // ns
     const long long t0 = clock64();
+    uint32_t ok;
+    bool late;
     do {
-        uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 0x989680;\n\t"               // ns
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(hint)
+            : "r"(bar), "r"(parity)
             : "memory");
-        if (ok)
-            return true;
-    } while (!(abort != nullptr && *abort) && clock64() - t0 <= limit);
-    return false;
+        late = clock64() - t0 > limit;
+    } while (!ok && !late && !(abort != nullptr && *abort));
+    return ok && !late;
 }
 
 // Transposes a 4 x 4 matrix of 16-byte units held by a quad of lanes: lane b ends with unit b of every lane.

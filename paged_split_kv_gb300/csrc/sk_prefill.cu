@@ -823,8 +823,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                             *reinterpret_cast<uint4 *>(row + cc * 1024 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
-                if (!ok)
+                if (!ok) {
                     *abort_flag = 1;                               // the other roles' waits end with it
+                    atomicOr(p.status, SK_DEV_TIMEOUT);
+                }
                 __syncwarp();
             }
             // P overwrites the first columns of each half of S.  A row's reference need not follow its maximum while
@@ -936,8 +938,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
         if (lane == 0)
             mbar_arrive(bar_piece_free(place));
         }
-        if (failed)
+        if (failed) {
             *abort_flag = 1;
+            if (lane == 0)
+                atomicOr(p.status, SK_DEV_TIMEOUT);
+        }
     } else {
         // ================================================================ e4m3: V codes to f16 (exact)
         reg_dec<C::kRegsConvert>();
@@ -955,10 +960,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
             if (ok && v >= 2)
                 ok = wait_bar(bar_vempty(vb), ((v >> 1) - 1) & 1, abort_flag, p.wait_limit);
             ok = __all_sync(kFull, ok);
-            if (!ok) {
-                *abort_flag = 1;
+            if (!ok)
                 break;
-            }
             const uint8_t *src = smem + slot * C::kSlotBytes;
             uint8_t *dst = smem + C::kOffV + vb * C::kVBytes;
             const int key0 = tile * kKeys;
@@ -983,6 +986,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                 mbar_arrive(bar_vfull(vb));
                 mbar_arrive(bar_empty(slot));
             }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                atomicOr(p.status, SK_DEV_TIMEOUT);
         }
     }
 
