@@ -37,7 +37,7 @@
 #include <type_traits>
 
 #include "sk_attn_util.cuh"
-#include "sk_internal.cuh"
+#include "sk_cache_ops.cuh"
 #include "sk_sm100.cuh"
 
 namespace sk {

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "sk.h"
+#include "sk_cache_ops.cuh"
 #include "sk_internal.cuh"
 
 namespace sk {

@@ -7,7 +7,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
-#include "sk_internal.cuh"
+#include "sk_cache_ops.cuh"
 #include "sk_sm100.cuh"
 
 namespace sk {

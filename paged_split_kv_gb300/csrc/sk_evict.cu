@@ -26,7 +26,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
-#include "sk_internal.cuh"
+#include "sk_cache_ops.cuh"
 
 namespace sk {
 namespace {

@@ -20,7 +20,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "sk_internal.cuh"
+#include "sk_cache_ops.cuh"
 #include "sk_quant.cuh"
 
 namespace sk {
