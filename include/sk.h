@@ -19,6 +19,10 @@
  * A NULL plan selects the fixed split of the Motivation section (used for
  * bs == 1, where it already gives 64 segments).
  *
+ * Around them, on the same pages: the writes of new tokens (sk_reshape_and_cache, or with rotary positions
+ * sk_rope_and_cache), attention of many new tokens at once (sk_paged_prefill_attn), and a cache bounded by eviction
+ * (sk_accum_attn_weights, sk_evict_select, sk_evict_move).
+ *
  * Conventions for every call:
  *  - Pointers marked "device" are device memory owned by the caller; the
  *    library keeps no reference after the call returns.  It allocates no
@@ -264,7 +268,8 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
  * sets SK_DEV_BAD_SEQ and skips the sequence, whose rows are then undefined).  num_tokens rows past cu_seqlens_q[bs] are left as they were.
  *
  * The work is divided evenly over the SMs, in the key axis too, so few query rows on a long cache use the
- * whole GPU.  max_seq_len, an upper bound on the lengths, sizes the launch of small calls only.  workspace (device, 16-byte
+ * whole GPU.  max_seq_len, an upper bound on the lengths, decides how many CTAs a small call launches and how the work is
+ * divided; a wrong one costs time only.  workspace (device, 16-byte
  * aligned): sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype) bytes; its contents do not matter, and
  * calls that may overlap need one each.  q, kv_pages and out are 16-byte aligned; lse may be NULL.  Probabilities
  * round to bf16 (f16 for e4m3fn pages); sums are fp32; the same bits every time on the same device.

@@ -7,8 +7,13 @@ and the KV write and page conversion around it run in the CUDA kernels of
 the C names (``sk_build_plan``, ``sk_paged_decode_attn``,
 ``sk_merge_segments``, ``sk_plan_cache_reset``, ``sk_reshape_and_cache``,
 ``sk_std_to_shuffled``) and take torch tensors; ``paged_decode_attention``
-chains the three attention calls the way a serving step does.  If
-``libsk.so`` has not been built, every call raises: there is no fallback.
+chains the three attention calls the way a serving step does.  Around them:
+``sk_rope_and_cache`` (rotary positions with the KV write),
+``paged_prefill_attention`` (attention of a chunk of new tokens over the
+pages), ``sk_accum_attn_weights`` (the attention weight each cached key
+receives) and ``evict_rows`` (a cache cut down to its heaviest and latest
+rows).  If ``libsk.so`` has not been built, every call raises: there is no
+fallback.
 """
 from __future__ import annotations
 
@@ -508,7 +513,7 @@ def sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out,
                           v_scale: float = 1.0, causal: bool = True, workspace=None, stream=None) -> int:
     """Attention of a chunk of new tokens over the paged cache into ``out`` (bf16 [num_tokens, num_q_heads, 128])
     and ``lse`` (fp32 [num_tokens, num_q_heads], or None).  ``max_seq_len`` bounds seq_lens (default: what the block
-    table holds) and only sizes the launch of small calls.  ``workspace`` is an optional dict that keeps the call's
+    table holds) and decides how the work is divided.  ``workspace`` is an optional dict that keeps the call's
     buffer; calls that may overlap need one each."""
     import torch
     dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,

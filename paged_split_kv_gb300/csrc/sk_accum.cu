@@ -18,7 +18,7 @@
 //     that a block's 32 KB meet 512 keys: with fewer the L2 could not deliver Q as fast as the tensor cores take it.  Runs
 //     are cut inside a group, between Q blocks: cut between tiles they came out at one to three tiles each, which
 //     left CTAs idle and a group's pipeline half empty (1190 and 1500 tokens over 18k and 8k keys of e4m3, 8 heads
-//     a KV head: 184 us, now 126).  The sums of a group that several runs share meet in accum_join_kernel.
+//     a KV head: 184 us, now 125).  The sums of a group that several runs share meet in accum_join_kernel.
 //
 // Roles (640 threads): warp 0 copies K pages; warps 1 and 2 issue the products of every other tile of a group; warp 3
 // finds the items (the parts of the run in one sequence and head) and publishes them, copies Q blocks (TMA: a box is
@@ -61,7 +61,7 @@ struct ACfg {
     static constexpr int kQSlot = RB * 256;
     static constexpr int kQSlots = MANY ? 3 : 2;
     static constexpr int kAuxEach = FP8 ? 2 * RB : RB;             // floats per Q block: -lse, and e4m3's scales
-    static constexpr int kMisc = FP8 ? 4096 : 3072;
+    static constexpr int kMisc = (FP8 ? 4 : 3) * 1024;
     static constexpr int kFit = (kMaxSmem - kQSlots * kQSlot - kMisc) / kKSlot;
     static constexpr int kKSlots = (kFit < 12 ? kFit : 12) / 2 * 2;        // every other one for either issuer
     static constexpr int kHalf = kKSlots / 2;
