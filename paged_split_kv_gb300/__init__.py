@@ -17,6 +17,7 @@ fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -499,12 +500,24 @@ def sk_prefill_workspace_bytes(num_tokens: int, num_q_heads: int, kv_dtype: int)
     return _check(lib().sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype), "sk_prefill_workspace_bytes")
 
 
-def _buffer(ws, key, need, device):
+def _owned_by(stream, device):
+    """Context in which memory for a call on ``stream`` is taken: it belongs to that stream, so that it is not handed
+    out again to another one while the call's kernels still use it."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _buffer(ws, key, need, device, stream):
     """A byte buffer of at least ``need`` bytes, kept in the workspace dict."""
     import torch
     t = ws.get(key)
     if t is None or t.numel() < need or t.device != device:
-        t = ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        with _owned_by(stream, device):
+            t = ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
     return t.data_ptr()
 
 
@@ -522,12 +535,9 @@ def sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out,
     pl = None if lse is None else _fits(lse, torch.float32, (nt, hq), "lse", dev)
     buf, need = None, 0
     if dev >= 0:
-        ws = workspace if workspace is not None else {}
-        need = ws.get(("prefill bytes", nt, hq, dt, dev))
-        if need is None:
-            with torch.cuda.device(dev):
-                need = ws[("prefill bytes", nt, hq, dt, dev)] = sk_prefill_workspace_bytes(nt, hq, dt)
-        buf = _buffer(ws, "prefill", need, q.device)
+        with contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev):
+            need = sk_prefill_workspace_bytes(nt, hq, dt)
+        buf = _buffer(workspace if workspace is not None else {}, "prefill", need, q.device, stream)
     return _launch(dev, stream, "sk_paged_prefill_attn", lib().sk_paged_prefill_attn, pq, pp, dt, k_scale, v_scale, pb,
                    stride, nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0,
                    stride * page if max_seq_len is None else max_seq_len, buf, need, po, pl)
@@ -541,10 +551,11 @@ def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *,
     fp32 [NT, H_q])."""
     import torch
     nt, hq, d = q.shape
-    if out is None:
-        out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
+    with _owned_by(stream, q.device):
+        if out is None:
+            out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
     sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, max_q_len=max_q_len,
                           sm_scale=sm_scale, max_seq_len=max_seq_len, k_scale=k_scale, v_scale=v_scale, causal=causal,
                           workspace=workspace, stream=stream)
@@ -570,9 +581,10 @@ def sk_accum_attn_weights(q, kv_pages, block_table, seq_lens, cu_seqlens_q, lse,
     pl = _fits(lse, torch.float32, (nt, hq), "lse", dev)
     pa = _fits(acc_pages, torch.float32, (nb, hkv, page), "acc_pages", dev)
     buf, need = None, 0
-    if dev >= 0 and (dt == SK_KV_FP8_E4M3 or max_q_len * (hq // hkv) > 64):
+    if dev >= 0:
         need = sk_accum_workspace_bytes(nt, hq, hkv, max_q_len, dt)
-        buf = _buffer(workspace if workspace is not None else {}, "accum", need, q.device)
+        if need:
+            buf = _buffer(workspace if workspace is not None else {}, "accum", need, q.device, stream)
     return _launch(dev, stream, "sk_accum_attn_weights", lib().sk_accum_attn_weights, pq, pp, dt, k_scale, pb, stride,
                    nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0, pl, pa, buf, need)
 
@@ -643,12 +655,13 @@ def evict_rows(kv_pages, acc_pages, pos_pages, block_table, seq_lens, next_pos, 
     if max_seq_len is None:
         max_seq_len = block_table.shape[1] * page
     ws = workspace if workspace is not None else {}
-    if "src_rows" not in ws:
-        cap = sk_evict_capacity(budget, max_seq_len)
-        ws["src_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
-        ws["dst_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
-        ws["counts"] = torch.empty((bs, hkv), dtype=torch.int32, device=dev)
-    new_lens = torch.empty_like(seq_lens)
+    with _owned_by(stream, dev):
+        if "src_rows" not in ws:
+            cap = sk_evict_capacity(budget, max_seq_len)
+            ws["src_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
+            ws["dst_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
+            ws["counts"] = torch.empty((bs, hkv), dtype=torch.int32, device=dev)
+        new_lens = torch.empty_like(seq_lens)
     sk_evict_select(acc_pages, pos_pages, block_table, seq_lens, next_pos, ws["src_rows"], ws["dst_rows"],
                     ws["counts"], new_lens, budget=budget, recent=recent, max_seq_len=max_seq_len, stream=stream)
     sk_evict_move(ws["src_rows"], ws["dst_rows"], ws["counts"], block_table, kv_pages, acc_pages, pos_pages,

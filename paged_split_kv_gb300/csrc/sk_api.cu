@@ -496,6 +496,9 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
     return SK_OK;
 }
 
+static constexpr int kMaxStride = 1 << 26;       // blocks a sequence: row numbers stay below 2^30
+static constexpr int kMaxPairs = 1 << 24;        // (sequence, KV head) pairs
+
 int sk_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double low,
                         double high, double *freqs, double *attn_factor)
 {
@@ -607,8 +610,9 @@ int sk_evict_select(const float *acc_pages, const int32_t *pos_pages, const int3
     if (budget < 1 || recent < 0 || recent > budget || max_seq_len < 0)
         return fail(SK_ERR_INVALID, "sk_evict_select: budget=%d, recent=%d (at most the budget), max_seq_len=%d",
                     budget, recent, max_seq_len);
-    if ((long long)bs * num_kv_heads * 16 > 0x7FFFFFFFLL)
-        return fail(SK_ERR_UNSUPPORTED, "sk_evict_select: %d sequences of %d heads", bs, num_kv_heads);
+    if ((long long)bs * num_kv_heads > kMaxPairs || block_table_stride > kMaxStride || max_seq_len > kMaxStride * kPage)
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_select: %d sequences of %d heads (at most 2^24), %d blocks a sequence "
+                    "(2^26), max_seq_len=%d (2^30)", bs, num_kv_heads, block_table_stride, max_seq_len);
     if (capacity < sk_evict_capacity(budget, max_seq_len))
         return fail(SK_ERR_CAPACITY, "sk_evict_select: capacity=%d below min(budget, max_seq_len - budget) = %d",
                     capacity, sk_evict_capacity(budget, max_seq_len));
@@ -645,8 +649,9 @@ int sk_evict_move(const int32_t *src_rows, const int32_t *dst_rows, const int32_
         return fail(SK_ERR_UNSUPPORTED, "sk_evict_move: head_dim=%d (only 128)", head_dim);
     if (page_size != kPage)
         return fail(SK_ERR_UNSUPPORTED, "sk_evict_move: page_size=%d (only 16)", page_size);
-    if ((long long)bs * num_kv_heads > (1 << 24))
-        return fail(SK_ERR_UNSUPPORTED, "sk_evict_move: %d sequences of %d heads", bs, num_kv_heads);
+    if ((long long)bs * num_kv_heads > kMaxPairs || block_table_stride > kMaxStride)
+        return fail(SK_ERR_UNSUPPORTED, "sk_evict_move: %d sequences of %d heads (at most 2^24), %d blocks a sequence "
+                    "(2^26)", bs, num_kv_heads, block_table_stride);
     if (src_rows == nullptr || dst_rows == nullptr || counts == nullptr || block_table == nullptr ||
         kv_pages == nullptr || acc_pages == nullptr || pos_pages == nullptr)
         return fail(SK_ERR_INVALID, "sk_evict_move: null pointer argument");
@@ -713,6 +718,9 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
         (long long)num_blocks * num_kv_heads * 2 > 0x7FFFFFFFLL)
         return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: %d blocks of %d heads or %d query tokens of %d heads "
                     "exceed the kernel's limits (2^30)", num_blocks, num_kv_heads, max_q_len, num_q_heads);
+    if (block_table_stride > kMaxStride || (long long)bs * num_kv_heads > kMaxPairs)
+        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: %d blocks a sequence (at most 2^26), %d sequences of %d "
+                    "heads (2^24)", block_table_stride, bs, num_kv_heads);
     if (num_tokens == 0)
         return SK_OK;
     int *status = nullptr;
@@ -794,6 +802,9 @@ int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, flo
     if ((long long)num_blocks * num_kv_heads * 2 > 0x7FFFFFFFLL || (long long)num_q_heads * max_q_len > 0x3FFFFFFFLL)
         return fail(SK_ERR_UNSUPPORTED, "sk_accum_attn_weights: %d blocks of %d heads or %d query tokens of %d heads "
                     "exceed the kernel's limits (2^30)", num_blocks, num_kv_heads, max_q_len, num_q_heads);
+    if (block_table_stride > kMaxStride || (long long)bs * num_kv_heads > kMaxPairs)
+        return fail(SK_ERR_UNSUPPORTED, "sk_accum_attn_weights: %d blocks a sequence (at most 2^26), %d sequences of %d "
+                    "heads (2^24)", block_table_stride, bs, num_kv_heads);
     const int64_t need = sk_accum_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype);
     if (workspace_bytes < need || (need > 0 && workspace == nullptr))
         return fail(SK_ERR_CAPACITY, "sk_accum_attn_weights: workspace of %lld bytes, %lld needed",

@@ -174,3 +174,36 @@ def test_a_captured_step_replayed_goes_on_as_the_calls_do(fp8):
     assert sk.sk_get_device_status() == 0
     assert torch.equal(eager.pages.view(torch.uint8), replayed.pages.view(torch.uint8))
     assert torch.equal(eager.acc, replayed.acc) and torch.equal(eager.pos, replayed.pos)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_memory_of_calls_on_another_stream(fp8):
+    """Calls on a stream of their own, without workspaces: what the caller's stream allocates next must not be memory that
+    those calls, still waiting on their stream, will use."""
+    qs = [64, 64, 100, 70]
+    servers = [Server(4, 8, 2, 64, 8, fp8, 128, 6, 100) for _ in range(2)]
+    want = servers[0].calls(servers[0].inputs(qs))
+    server, x = servers[1], servers[1].inputs(qs)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    args = dict(max_q_len=100, sm_scale=D ** -0.5, k_scale=server.ks)
+    qr = torch.empty(x.nt, 8, D, dtype=torch.bfloat16, device=DEV)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    sk.sk_rope_and_cache(x.q, x.k, x.v, x.pos, server.freqs, x.slots, server.pages, qr, attn_factor=server.factor,
+                         k_scale=server.ks, v_scale=server.vs, acc_pages=server.acc, pos_pages=server.pos, stream=side)
+    out, lse = sk.paged_prefill_attention(qr, server.pages, server.bt, x.lens, x.cu, v_scale=server.vs, stream=side, **args)
+    sk.sk_accum_attn_weights(qr, server.pages, server.bt, x.lens, x.cu, lse, server.acc, stream=side.cuda_stream, **args)
+    new = sk.evict_rows(server.pages, server.acc, server.pos, server.bt, x.lens, x.next_pos, budget=64, recent=8,
+                        stream=side)
+    held = []
+    for need in (sk.sk_prefill_workspace_bytes(x.nt, 8, int(fp8)), sk.sk_accum_workspace_bytes(x.nt, 8, 2, 100, int(fp8)),
+                 4 * 2 * sk.sk_evict_capacity(64, server.bt.shape[1] * PAGE) * 4, 4 * 2 * 4):
+        held += [torch.full((need,), 0xA5, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert sk.sk_get_device_status() == 0
+    for got, right in zip((qr, out, lse, new), want):
+        assert torch.equal(got, right)
+    assert all(bool((t == 0xA5).all()) for t in held)
+    assert torch.equal(server.pages.view(torch.uint8), servers[0].pages.view(torch.uint8))
+    assert torch.equal(server.acc, servers[0].acc) and torch.equal(server.pos, servers[0].pos)

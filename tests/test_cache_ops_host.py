@@ -219,3 +219,26 @@ def test_binding_checks_attention_shapes(sk):
     for f in (prefill, accum):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+def test_limits_of_row_numbers_and_pairs(sk):
+    """Row numbers stay below 2^30 and (sequence, head) pairs at 2^24 or below, whatever the arrays hold."""
+    lib = sk.lib()
+    attn = dict(q=FAKE, kv=FAKE, dt=0, ks=1.0, vs=1.0, bt=FAKE, stride=10, nb=100, page=16, lens=FAKE, cu=FAKE, bs=4,
+                nt=0, mq=0, hq=1024, hkv=1024, d=128, scale=0.088, causal=1, mx=160, ws=FAKE, wb=1 << 30, out=FAKE,
+                lse=None, st=None)
+    prefill = caller(lib.sk_paged_prefill_attn, attn)
+    weights = {k: attn[k] for k in attn if k not in ("vs", "mx", "ws", "wb", "out", "lse", "st")}
+    accum = caller(lib.sk_accum_attn_weights, dict(weights, lse=FAKE, acc=FAKE, ws=FAKE, wb=1 << 30, st=None))
+    for call in (prefill, accum):
+        assert call() == 0 and call(stride=1 << 26) == 0
+        assert call(stride=(1 << 26) + 1) == -3 and call(bs=20000) == -3
+    select = caller(lib.sk_evict_select, dict(
+        acc=FAKE, pos=FAKE, bt=FAKE, stride=10, nb=100, page=16, lens=FAKE, nxt=FAKE, bs=4, hkv=2, budget=8, recent=0,
+        mx=160, cap=8, src=FAKE, dst=FAKE, cnt=FAKE, new=FAKE, st=None))
+    move = caller(lib.sk_evict_move, dict(
+        src=FAKE, dst=FAKE, cnt=FAKE, cap=8, bs=4, hkv=2, d=128, bt=FAKE, stride=10, nb=100, page=16, kv=FAKE, dt=0,
+        acc=FAKE, pos=FAKE, st=None))
+    for call in (select, move):
+        assert call(stride=(1 << 26) + 1) == -3 and call(bs=20000, hkv=1024) == -3
+    assert select(mx=(1 << 30) + 1) == -3
