@@ -868,16 +868,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
         }
         if (failed)
             break;
-        if (nx > 0) {
-            const bool ok = wait_bar(bar_o(x), pieces & 1, abort_flag, p.wait_limit);
-            if (!__all_sync(kFull, ok)) {
-                failed = true;
-                break;
-            }
-            tc_fence_after();
-        }
-        // ---- the row's output, or its partial state.  A lane's row is transposed within quads of lanes, so that a
-        // warp's store writes 64 contiguous bytes of eight rows (with 16 bytes of 32 rows it took 5000 cycles)
+        // ---- the row's output, or its partial state (its place is found while the last products run).  A lane's row is
+        // transposed within quads of lanes, so that a warp's store writes 64 contiguous bytes of eight rows (with 16 bytes
+        // of 32 rows it took 5000 cycles)
         int jr, ir;
         const bool live = row_at(jr, ir);
         const bool whole = pc->a == 0 && pc->b == pc->t;
@@ -894,6 +887,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
         const bool empty = __any_sync(kFull, nx == 0 || l == 0.f);
         uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out) : reinterpret_cast<uint8_t *>(p.part_o);
         const int row_bytes = whole ? kHeadDim * 2 : kHeadDim * 4;
+        if (nx > 0) {
+            const bool ok = wait_bar(bar_o(x), pieces & 1, abort_flag, p.wait_limit);
+            if (!__all_sync(kFull, ok)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+        }
 #pragma unroll 1
         for (int cc = 0, at = (lane & 3) * 16; at < row_bytes; cc += whole ? 32 : 16, at += 64) {
             // 64 bytes of every row: 32 dimensions rounded, or 16 as they are
