@@ -53,6 +53,12 @@ constexpr long long kDrainLimit = 4000000000LL;
 constexpr int kMaxSmem = 232448;
 constexpr int kAccumRuns = 256;                      // runs (SMs) at most
 constexpr long long kAccumParts = 2LL * kAccumRuns * (kGroup * kKeys * 4 + (long long)sizeof(AccumPiece));
+// Few rows, long runs: equal runs end up to a fifth apart (SMs see different shares of the bandwidth), so a last 16th
+// of the batch goes out in short runs to the SMs that are free first (16 x 119k keys, 4 tokens: 182 us without, 173 with a
+// 16th, 182 with an 8th).  Only where the tables' pages would make runs of so many tiles: the short runs are a start of a
+// CTA each, 1 to 3 us in a batch that turns out too short for them (16 x 2052 keys under tables of 8192 blocks: 11.8 us
+// against 8.9).
+constexpr int kTailLeast = 96;
 constexpr int kRing = 4;                             // items published ahead
 template <int RB, bool MANY, bool FP8>
 struct ACfg {
@@ -331,7 +337,7 @@ accum_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     // this CTA's run of the batch's cost (found in the K slots' memory, before the first copy)
-    const Run run = find_run<kThreads>(p.bs, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(smem),
+    const Run run = find_run<kThreads>(p.bs, blockIdx.x, p.runs, p.tail, kTailLeast, reinterpret_cast<long long *>(smem),
                                        reinterpret_cast<long long *>(misc + C::kStart), [&](int s) {
                                            if constexpr (MANY) {
                                                const Units u = units_of(p, s);
@@ -752,20 +758,18 @@ __global__ void __launch_bounds__(256) split_q_kernel(const uint16_t *__restrict
 }
 
 template <int RB, bool MANY, bool FP8>
-cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const AccumParams &p, int num_sms,
-                     cudaStream_t stream)
+cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const AccumParams &p, cudaStream_t stream)
 {
     using C = ACfg<RB, MANY, FP8>;
     const cudaError_t e = cudaFuncSetAttribute(accum_kernel<RB, MANY, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    const int runs = num_sms < kAccumRuns ? num_sms : kAccumRuns;
-    const cudaError_t l = launch_pdl(accum_kernel<RB, MANY, FP8>, dim3((unsigned)runs), dim3(kThreads), C::kSmemBytes,
-                                     stream, kv_map, q_map, p);
-    if (!MANY || runs == 1 || l != cudaSuccess)
+    const cudaError_t l = launch_pdl(accum_kernel<RB, MANY, FP8>, dim3((unsigned)(p.runs + p.tail)), dim3(kThreads),
+                                     C::kSmemBytes, stream, kv_map, q_map, p);
+    if (!MANY || p.runs == 1 || l != cudaSuccess)
         return l;
-    return launch_pdl(accum_join_kernel, dim3((unsigned)runs), dim3(kGroup * kKeys), 0, stream, p);
+    return launch_pdl(accum_join_kernel, dim3((unsigned)p.runs), dim3(kGroup * kKeys), 0, stream, p);
 }
 
 }  // namespace
@@ -816,6 +820,9 @@ cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *workspac
         q = q_codes;
         p.q_scale = reinterpret_cast<const float *>(q_codes + rows * 256);
     }
+    p.runs = num_sms < kAccumRuns ? num_sms : kAccumRuns;
+    const long long most = (long long)p.bs * p.H_kv * p.bt_stride / (kKeys / kPage);         // tiles of the tables' pages
+    p.tail = rb < 128 && most >= (long long)kTailLeast * p.runs ? p.runs : 0;
     CUtensorMap kv_map, q_map;
     cudaError_t e = encode_page_map(&kv_map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 1 : 2);
     if (e == cudaSuccess)
@@ -824,21 +831,21 @@ cudaError_t launch_accum(const AccumParams &params, int kv_dtype, void *workspac
         return e;
     switch (rb * 2 + (fp8 ? 1 : 0)) {
     case 32:
-        return launch_t<16, false, false>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<16, false, false>(kv_map, q_map, p, stream);
     case 33:
-        return launch_t<16, false, true>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<16, false, true>(kv_map, q_map, p, stream);
     case 64:
-        return launch_t<32, false, false>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<32, false, false>(kv_map, q_map, p, stream);
     case 65:
-        return launch_t<32, false, true>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<32, false, true>(kv_map, q_map, p, stream);
     case 128:
-        return launch_t<64, false, false>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<64, false, false>(kv_map, q_map, p, stream);
     case 129:
-        return launch_t<64, false, true>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<64, false, true>(kv_map, q_map, p, stream);
     case 256:
-        return launch_t<128, true, false>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<128, true, false>(kv_map, q_map, p, stream);
     default:
-        return launch_t<128, true, true>(kv_map, q_map, p, num_sms, stream);
+        return launch_t<128, true, true>(kv_map, q_map, p, stream);
     }
 }
 

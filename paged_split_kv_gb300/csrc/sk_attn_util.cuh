@@ -234,7 +234,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 }
 
 // The run of a CTA: the batch's total cost, sequence s costing cost(s), is cut into `count` equal runs, and [lo, hi) is
-// that of `index`.  Finds the sequence that lo lies in and the cost before it.  `part` and `found` are shared memory
+// that of `index`.  With `tail` > 0 as many short runs follow, which share the last 16th of the cost between them (nothing
+// when the runs are shorter than `least`).  Finds the sequence that lo lies in and the cost before it.  `part` and `found` are shared memory
 // (kThreads / 32 and 2 words of 64 bits); every thread of the block calls it, and all get the same answer.
 struct Run {
     long long lo, hi, before;
@@ -242,7 +243,8 @@ struct Run {
 };
 
 template <int kThreads, typename Cost>
-__device__ __forceinline__ Run find_run(int bs, int index, int count, long long *part, long long *found, Cost cost)
+__device__ __forceinline__ Run find_run(int bs, int index, int count, int tail, long long least, long long *part,
+                                        long long *found, Cost cost)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (bs + kThreads - 1) / kThreads;
@@ -270,9 +272,16 @@ __device__ __forceinline__ Run find_run(int bs, int index, int count, long long 
     __syncthreads();                                 // the caller may use the memory for something else
     Run r;
     // a little more than total / count (a 64-bit division takes thousands of cycles in all threads)
-    const long long each = (long long)((float)total / (float)count * (1.f + 0x1p-20f)) + 1;
-    r.lo = min(total, each * index);
-    r.hi = min(total, each * (index + 1));
+    auto share = [](long long cost, int runs) {
+        return (long long)((float)cost / (float)runs * (1.f + 0x1p-20f)) + 1;
+    };
+    const long long first = tail > 0 && total >= least * count ? total - total / 16 : total;
+    const long long each = share(first, count), after = share(total - first, max(tail, 1));
+    auto bound = [&](int i) {
+        return i <= count ? min(first, each * i) : min(total, first + after * (i - count));
+    };
+    r.lo = bound(index);
+    r.hi = bound(index + 1);
     if (mine > 0 && r.lo >= before && r.lo < before + mine) {
         int s = s0;
 #pragma unroll 1

@@ -61,6 +61,7 @@ struct AccumParams {
     int causal;
     float score_scale_log2;
     long long wait_limit;
+    int runs, tail;              // equal shares of the cost, and short ones after them (set by the launcher)
     float *part;                 // workspace, set by the launcher: sums of shared units, and what they are parts of
     AccumPiece *shared;
 };
