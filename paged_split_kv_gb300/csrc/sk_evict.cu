@@ -121,6 +121,13 @@ __device__ __forceinline__ Part part_of(const Counts &c, int first_row, int rows
     return p;
 }
 
+// Waits until all but the last N groups of this thread's asynchronous copies are done.
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a)
 {
     extern __shared__ uint4 keys4[];             // four rows each, the first kSharedQuads of this CTA's
@@ -161,64 +168,120 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     const int32_t *bt = a.block_table + (long long)s * a.bt_stride;
     __syncthreads();
 
-    // the keys of row quad i, from its weights and positions
-    auto block_of = [&](int i) { return i < quads ? __ldg(bt + (lo + 4 * i) / kPage) : 0; };
-    auto load_quad = [&](int i, int blk, float4 &w, int4 &p) {
-        w = make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
-        p = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
-        if (i >= quads)
-            return;
-        if (blk >= 0 && blk < a.num_blocks) {
-            const long long at = ((long long)blk * a.hkv + h) * kPage + (lo + 4 * i) % kPage;
-            w = *reinterpret_cast<const float4 *>(a.acc + at);
-            if (a.recent > 0)
-                p = *reinterpret_cast<const int4 *>(a.pos + at);
-        } else {
+    // the keys of row quad i, from its weights and positions; block_of is -1 past the rows, and for a bad block (reported)
+    auto block_of = [&](int i) {
+        const int blk = i < quads ? __ldg(bt + (lo + 4 * i) / kPage) : 0;
+        if (blk < 0 || blk >= a.num_blocks)
             atomicOr(a.status, SK_DEV_BAD_BLOCK);
-        }
+        return i < quads && blk < a.num_blocks ? blk : -1;
+    };
+    auto place_of = [&](int i, int blk) { return ((long long)blk * a.hkv + h) * kPage + (lo + 4 * i) % kPage; };
+    const float4 no_weight = make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+    const int4 no_pos = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
+    auto weights = [&](int i, int blk) {
+        return blk >= 0 ? *reinterpret_cast<const float4 *>(a.acc + place_of(i, blk)) : no_weight;
+    };
+    auto positions = [&](int i, int blk) {
+        return blk >= 0 && a.recent > 0 ? *reinterpret_cast<const int4 *>(a.pos + place_of(i, blk)) : no_pos;
     };
     auto key_of = [&](float w, int pos) { return a.recent > 0 && pos >= edge ? 0xFFFFFFFFu : weight_key(w); };
     auto quad_key = [&](const float4 &w, const int4 &p) {
         return make_uint4(key_of(w.x, p.x), key_of(w.y, p.y), key_of(w.z, p.z), key_of(w.w, p.w));
     };
     auto quad_again = [&](int i) {               // computed again, past what is kept
-        float4 w;
-        int4 p;
-        load_quad(i, block_of(i), w, p);
-        return quad_key(w, p);
+        const int blk = block_of(i);
+        return quad_key(weights(i, blk), positions(i, blk));
+    };
+    auto count_first = [&](int i, const uint4 &k) {
+        count_digits(sh.hist[0], make_uint4(k.x >> 21, k.y >> 21, k.z >> 21, k.w >> 21), 4 * i < n, 4 * i + 1 < n,
+                     4 * i + 2 < n, 4 * i + 3 < n);
     };
 
-    // ---- keys, and the first digit's histogram
+    // ---- keys, and the first digit's histogram.  The weights of all quads kept in shared memory are copied there at
+    // once, asynchronously, and become keys in place; positions are loaded a round ahead (against loads four at a time: 68
+    // us for 72 with a cold L2, 49 for 50 with a warm one).
+    constexpr int kRounds = kSharedQuads / (kAtOnce * kSelThreads);
+    static_assert(kRounds == 3, "the waits below");
+    int blk[kRounds * kAtOnce];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        if (r * kAtOnce * kSelThreads >= quads)
+            break;                               // uniform in the CTA
+#pragma unroll
+        for (int u = r * kAtOnce; u < (r + 1) * kAtOnce; ++u)
+            blk[u] = block_of(u * kSelThreads + tid);
+    }
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        if (r * kAtOnce * kSelThreads >= quads)
+            break;
+#pragma unroll
+        for (int u = r * kAtOnce; u < (r + 1) * kAtOnce; ++u) {
+            const int i = u * kSelThreads + tid;
+            if (blk[u] >= 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(keys4 + i)),
+                             "l"(a.acc + place_of(i, blk[u]))
+                             : "memory");
+            else if (i < quads)
+                reinterpret_cast<float4 *>(keys4)[i] = no_weight;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
     uint4 held[kAtOnce] = {};                    // this thread's quads kSharedQuads + u * kSelThreads + tid
-    int blk[kAtOnce];
+    int4 p[2][kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
-        blk[u] = block_of(u * kSelThreads + tid);
-#pragma unroll 1
-    for (int i0 = tid; i0 - lane < quads; i0 += kSelThreads * kAtOnce) {
-        float4 w[kAtOnce];
-        int4 p[kAtOnce];
+        p[0][u] = positions(u * kSelThreads + tid, blk[u]);
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-            load_quad(i0 + u * kSelThreads, blk[u], w[u], p[u]);
+    for (int r = 0; r < kRounds; ++r) {
+        if (r * kAtOnce * kSelThreads >= quads)
+            break;
+        if (r + 1 < kRounds && (r + 1) * kAtOnce * kSelThreads < quads) {
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-            blk[u] = block_of(i0 + (u + kAtOnce) * kSelThreads);
+            for (int u = 0; u < kAtOnce; ++u)
+                p[(r + 1) & 1][u] = positions(((r + 1) * kAtOnce + u) * kSelThreads + tid, blk[(r + 1) * kAtOnce + u]);
+        }
+        // with fewer rounds there are fewer groups behind this one
+        if (r == 0 && 2 * kAtOnce * kSelThreads < quads)
+            copies_wait<2>();
+        else if (r <= 1 && (r + 1) * kAtOnce * kSelThreads < quads)
+            copies_wait<1>();
+        else
+            copies_wait<0>();
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-            const int i = i0 + u * kSelThreads;
+            const int i = (r * kAtOnce + u) * kSelThreads + tid;
             if (i - lane >= quads)
                 break;                           // uniform in the warp
-            const uint4 k = quad_key(w[u], p[u]);
-            if (i < kSharedQuads) {
-                if (i < quads)
-                    keys4[i] = k;
-            } else if (i < kKeptQuads) {
-                held[u] = k;
+            uint4 k = make_uint4(0u, 0u, 0u, 0u);
+            if (i < quads) {
+                k = quad_key(reinterpret_cast<const float4 *>(keys4)[i], p[r & 1][u]);
+                keys4[i] = k;
             }
-            count_digits(sh.hist[0], make_uint4(k.x >> 21, k.y >> 21, k.z >> 21, k.w >> 21), 4 * i < n, 4 * i + 1 < n,
-                         4 * i + 2 < n, 4 * i + 3 < n);
+            count_first(i, k);
         }
+    }
+    if (kSharedQuads + tid - lane < quads) {
+        float4 w[kAtOnce];
+        int4 q[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = kSharedQuads + u * kSelThreads + tid, b = block_of(i);
+            w[u] = weights(i, b);
+            q[u] = positions(i, b);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = kSharedQuads + u * kSelThreads + tid;
+            if (i - lane >= quads)
+                break;
+            held[u] = quad_key(w[u], q[u]);
+            count_first(i, held[u]);
+        }
+#pragma unroll 1
+        for (int i = kKeptQuads + tid; i - lane < quads; i += kSelThreads)
+            count_first(i, quad_again(i));
     }
 
     // ---- the budget-th largest key, digit by digit, until a digit's keys are all taken
@@ -553,7 +616,7 @@ cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int3
 {
     // As many CTAs per cluster as there are SMs for, up to 8 (more need a whole GPC, which few clusters can have at a
     // time), or as many as keep all rows, up to 16; each has 4096 rows or more.  (32 clusters for up to 248k rows: 4
-    // CTAs, which all run at once, 50 us; 5, 59 us; 6, 64; 8, 78.)
+    // CTAs, which all run at once, 49 us; 5, 59 us; 6, 64; 8, 78.)
     const int pairs = bs * hkv;
     int c = num_sms / pairs;
     c = c < 8 ? c : 8;
