@@ -202,14 +202,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     // us for 72 with a cold L2, 49 for 50 with a warm one).
     constexpr int kRounds = kSharedQuads / (kAtOnce * kSelThreads);
     static_assert(kRounds == 3, "the waits below");
-    int blk[kRounds * kAtOnce];
+    int blk[kRounds * kAtOnce];                  // -1 where this CTA has no rows (in short sequences, some have none at all)
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
-        if (r * kAtOnce * kSelThreads >= quads)
-            break;                               // uniform in the CTA
 #pragma unroll
         for (int u = r * kAtOnce; u < (r + 1) * kAtOnce; ++u)
-            blk[u] = block_of(u * kSelThreads + tid);
+            blk[u] = -1;
+        if (r * kAtOnce * kSelThreads < quads) {     // uniform in the CTA
+#pragma unroll
+            for (int u = r * kAtOnce; u < (r + 1) * kAtOnce; ++u)
+                blk[u] = block_of(u * kSelThreads + tid);
+        }
     }
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
