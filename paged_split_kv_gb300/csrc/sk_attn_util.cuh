@@ -235,8 +235,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 
 // The run of a CTA: the batch's total cost, sequence s costing cost(s), is cut into `count` equal runs, and [lo, hi) is
 // that of `index`.  With `tail` > 0 as many short runs follow, which share the last 16th of the cost between them (nothing
-// when the runs are shorter than `least`).  Finds the sequence that lo lies in and the cost before it.  `part` and `found` are shared memory
-// (kThreads / 32 and 2 words of 64 bits); every thread of the block calls it, and all get the same answer.
+// when the runs are shorter than `least`).  Finds the sequence that lo lies in and the cost before it.  `part` and `found`
+// are shared memory (kThreads / 32 and 2 words of 64 bits); every thread of the block calls it, and all get the same
+// answer.
 struct Run {
     long long lo, hi, before;
     int s;

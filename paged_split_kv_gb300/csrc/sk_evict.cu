@@ -544,7 +544,8 @@ template <bool FP8>
 __global__ void __launch_bounds__(kMoveThreads)
 evict_move_kernel(const int32_t *__restrict__ src, const int32_t *__restrict__ dst,
                   const int32_t *__restrict__ counts, int cap, int ctas_per_pair,
-                  const int32_t *__restrict__ block_table, int bt_stride, int num_blocks, int hkv, uint8_t *pages, float *acc, int32_t *pos, int *status)
+                  const int32_t *__restrict__ block_table, int bt_stride, int num_blocks, int hkv, uint8_t *pages,
+                  float *acc, int32_t *pos, int *status)
 {
     constexpr int kLanes = FP8 ? 16 : 32;        // lanes per row, 16 bytes each
     constexpr int kRowBytes = kLanes * 16;
