@@ -133,6 +133,29 @@ def test_many_short_sequences_a_run(lens, qs, hq, hkv, fp8):
     check(b, lse, acc0, acc)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,qs,hq,hkv", [([25000, 24999, 129, 30001] * 3, [1, 2, 0, 1] * 3, 16, 8),
+                                            ([33000, 1, 20000, 18000, 40001], [4, 1, 3, 4, 2], 256, 16)])
+def test_long_batches_of_few_rows(lens, qs, hq, hkv, fp8):
+    """The last part of a long batch goes out in short runs; under wide tables a short batch leaves those empty."""
+    b = batch(lens, qs, hq, hkv, fp8, 53)
+    lse = (torch.randn(b["w"].num_tokens, hq, device=DEV) + 12).contiguous()
+    acc0 = start(b, 4)
+    acc, again = acc0.clone(), acc0.clone()
+    run(b, lse, acc)
+    run(b, lse, again)
+    assert sk.sk_get_device_status() == 0 and torch.equal(acc, again)
+    check(b, lse, acc0, acc)
+    few = batch([300, 1, 0, 77], [1, 1, 0, 1], hq, hkv, fp8, 54)
+    few["bt"] = torch.nn.functional.pad(few["bt"], (0, 20000), value=-1)
+    lse = attention(few)[1].float()
+    acc0 = start(few, 5)
+    acc = acc0.clone()
+    run(few, lse, acc)
+    assert sk.sk_get_device_status() == 0
+    check(few, lse, acc0, acc)
+
+
 def test_rows_that_saw_nothing_add_nothing():
     b = batch([500, 200], [3, 2], 4, 1, False, 61)
     lse = attention(b)[1].float()
