@@ -56,6 +56,8 @@ class SkError(RuntimeError):
 def lib():
     """Load libsk.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -396,7 +398,8 @@ def _fits(t, dtype, shape, name, dev) -> int:
 
 def _pages(kv_pages, dev):
     """Address, type and shape of the pages."""
-    _need(kv_pages, None, "kv_pages", 4)
+    if kv_pages is None or kv_pages.dim() != 4 or not kv_pages.is_contiguous():
+        _need(kv_pages, None, "kv_pages", 4)
     if kv_pages.get_device() != dev:
         raise ValueError(f"kv_pages must be a CUDA tensor on the device of the other arguments, is on {kv_pages.device}")
     return kv_pages.data_ptr(), _kv_dtype(kv_pages), kv_pages.shape
@@ -484,15 +487,19 @@ def _batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q):
     """Addresses and sizes of a batch over the paged cache, its shapes and devices checked."""
     import torch
     dev = q.get_device()
-    _need(q, torch.bfloat16, "q", 3)
-    pp, dt, _ = _pages(kv_pages, dev)
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+        _need(q, torch.bfloat16, "q", 3)
+    pp, dt, (nb, hkv, page, d2) = _pages(kv_pages, dev)
     if block_table.dim() != 2 or seq_lens.dim() != 1 or cu_seqlens_q.dim() != 1:
         raise ValueError("block_table must have 2 dimensions, seq_lens and cu_seqlens_q 1")
-    nt, hq, d, nb, hkv, page, bs = _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
-    return (dev, q.data_ptr(), pp, dt, _fits(block_table, torch.int32, block_table.shape, "block_table", dev),
-            _fits(seq_lens, torch.int32, (bs,), "seq_lens", dev),
-            _fits(cu_seqlens_q, torch.int32, (bs + 1,), "cu_seqlens_q", dev), nt, hq, d, nb, hkv, page, bs,
-            block_table.shape[1])
+    nt, hq, d = q.shape
+    shape, bs = block_table.shape, seq_lens.shape[0]
+    if d2 != 2 * d or hkv < 1 or hq % hkv or shape[0] < bs or cu_seqlens_q.shape[0] != bs + 1:
+        _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
+    i32 = torch.int32
+    return (dev, q.data_ptr(), pp, dt, _fits(block_table, i32, shape, "block_table", dev),
+            _fits(seq_lens, i32, (bs,), "seq_lens", dev), _fits(cu_seqlens_q, i32, (bs + 1,), "cu_seqlens_q", dev), nt,
+            hq, d, nb, hkv, page, bs, shape[1])
 
 
 def sk_prefill_workspace_bytes(num_tokens: int, num_q_heads: int, kv_dtype: int) -> int:
@@ -535,8 +542,11 @@ def sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out,
     pl = None if lse is None else _fits(lse, torch.float32, (nt, hq), "lse", dev)
     buf, need = None, 0
     if dev >= 0:
-        with contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev):
+        if torch.cuda.current_device() == dev:
             need = sk_prefill_workspace_bytes(nt, hq, dt)
+        else:
+            with torch.cuda.device(dev):
+                need = sk_prefill_workspace_bytes(nt, hq, dt)
         buf = _buffer(workspace if workspace is not None else {}, "prefill", need, q.device, stream)
     return _launch(dev, stream, "sk_paged_prefill_attn", lib().sk_paged_prefill_attn, pq, pp, dt, k_scale, v_scale, pb,
                    stride, nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, 1 if causal else 0,
@@ -551,11 +561,12 @@ def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *,
     fp32 [NT, H_q])."""
     import torch
     nt, hq, d = q.shape
-    with _owned_by(stream, q.device):
-        if out is None:
-            out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
+    if out is None or lse is None:
+        with _owned_by(stream, q.device):
+            if out is None:
+                out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=q.device)
+            if lse is None:
+                lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
     sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, max_q_len=max_q_len,
                           sm_scale=sm_scale, max_seq_len=max_seq_len, k_scale=k_scale, v_scale=v_scale, causal=causal,
                           workspace=workspace, stream=stream)
