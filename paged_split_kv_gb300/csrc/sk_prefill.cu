@@ -831,7 +831,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
             }
             // P overwrites the first columns of each half of S.  A row's reference need not follow its maximum while
             // the probabilities stay well inside their type's range, and the tile's sum shows whether some did not.
-            // Only then is the maximum taken, the reference raised, O rescaled and the tile done again.
+            // Only then is the maximum taken, the reference raised, O rescaled and the tile done again.  The same for a
+            // row whose first 16 scores were all minus infinity: what it sums relative to no reference is not kept.
             const float2 c2 = make_float2(c, c);
             float2 h2;
 #pragma unroll 1
@@ -854,7 +855,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                     tmem_st32_u<16>(ts + (q >> 1) * 64 + (q & 1) * 16, pk);
                 }
                 h2 = fadd2(h2, g2);
-                if (again || !__any_sync(kFull, limit > 0 && !(h2.x + h2.y <= C::kSumMost)))
+                const bool redo = limit > 0 && !(h2.x + h2.y <= C::kSumMost);
+                if (again || !__any_sync(kFull, redo || (lim > 0 && m_ref == -CUDART_INF_F)))
                     break;
                 tmem_wait_st();
                 raise(tile_top(), j > 0);
