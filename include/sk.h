@@ -274,7 +274,8 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
  * divided; a wrong one costs time only.  workspace (device, 16-byte
  * aligned): sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype) bytes; its contents do not matter, and
  * calls that may overlap need one each.  q, kv_pages and out are 16-byte aligned; lse may be NULL.  Probabilities
- * round to bf16 (f16 for e4m3fn pages); sums are fp32; the same bits every time on the same device.
+ * round to bf16 (for e4m3fn pages to f16, by 2^-11 of themselves or 2^-33 of the row's sum, whichever is more); sums
+ * are fp32; the same bits every time on the same device.
  * Returns SK_OK or a negative sk_status. */
 int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
                           const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,

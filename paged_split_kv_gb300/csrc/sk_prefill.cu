@@ -82,9 +82,13 @@ struct PCfg {
     static constexpr int kOffMisc = kOffQ + 2 * kQTile;
     static constexpr int kSmemBytes = kOffMisc + kMisc;
     static constexpr int kPagesPerTile = kKeys / kPage;
+    // The reference stands this far (in log2 units) below the score that sets it: 0 for bf16, whose precision is the same
+    // at any size.  f16 rounds by a fixed 2^-25 below 2^-14: with probabilities of 2^8 for the row's largest scores
+    // that is 2^-33 of its sum or less, instead of 2^-25, which a key far above many others made their whole weight.
+    static constexpr float kAbove = FP8 ? 8.f : 0.f;
     // The sum of a tile's probabilities (relative to the reference) up to which they are as good as with the maximum
-    // for reference: bf16 keeps its precision at any size, f16 ends at 2^16.
-    static constexpr float kSumMost = FP8 ? 0x1p15f : 0x1p40f;
+    // for reference: f16 ends at 65504 (128 equal scores sum to 2^15).
+    static constexpr float kSumMost = FP8 ? 65504.f : 0x1p40f;
     // misc area
     static constexpr int kBarFull = 0;
     static constexpr int kBarEmpty = 8 * kSlots;
@@ -775,9 +779,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                     mx[k] = fmaxf(mx[k], v[124 + k]);
                 return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c;
             };
-            // moves the rows' reference up to `top` and rescales what they have summed; `in_o`: O holds something
+            // moves the rows' reference up to kAbove below `top` and rescales what they have summed; `in_o`: O holds
+            // something
             auto raise = [&](float top, bool in_o) {
-                const float mn = fmaxf(m_ref, top);
+                const float mn = fmaxf(m_ref, top - C::kAbove);
                 const float alpha = m_ref == -CUDART_INF_F ? 0.f : exp2f(m_ref - mn);
                 m_ref = mn;
                 l2.x *= alpha;

@@ -1,8 +1,11 @@
-"""Chunk attention where values are at the edge: keys whose scores are minus infinity.
+"""Chunk attention where values are at the edge: keys whose scores are minus infinity, and a key far above the rest on
+e4m3 pages.
 
 Tolerances, as for the other batches: a score is off by e = 130 * 2^-24 * scale * sum |q k| (128 products in fp32) and
-2^-20 (the exponential and the sums), the output rounds by 2^-8, a probability by 2^-8 of itself.
-    |out - ref| <= 2^-8 |ref| + sum (2^-8 + 2 e) p |v|"""
+2^-20 (the exponential and the sums), the output rounds by 2^-8, a probability by 2^-8 of itself in bf16.  In f16 (e4m3
+pages) it rounds by 2^-11 of itself or by a fixed 2^-25, whichever is more; a key that the row sees has at least 2^8 there,
+so that is at most 2^-33 of the row's sum.
+    |out - ref| <= 2^-8 |ref| + sum (2^-8 p + 2 e p + 2^-33) |v|,  without the last term for bf16"""
 import math
 
 import pytest
@@ -19,6 +22,7 @@ D, PAGE = 128, 16
 def check(b, out, lse, gone=()):
     """Compares with the definition in 64 bits; keys `gone` of every sequence have the weight 0."""
     w = b["w"]
+    fp8 = b["kv"].element_size() == 1
     assert not torch.isnan(out.float()).any() and not torch.isnan(lse).any()
     for s in range(w.bs):
         n, q, a = int(w.seq_lens[s]), int(w.q_lens[s]), int(w.cu_q[s])
@@ -36,7 +40,8 @@ def check(b, out, lse, gone=()):
                 e = 130 * 2.0 ** -24 * w.sm_scale * (x.abs() @ k.abs().t()).amax(1) + 2.0 ** -20
                 p = torch.softmax(sc, 1)
                 ref, want = p @ v, torch.logsumexp(sc, 1)
-                tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * e)[:, None] * (p @ v.abs())
+                floor = 2.0 ** -33 if fp8 else 0.0
+                tol = 2.0 ** -8 * ref.abs() + ((2.0 ** -8 + 2 * e)[:, None] * p + floor * ~hide) @ v.abs()
                 err = (out[a:a + q, i].double() - ref).abs()
                 assert bool((err <= tol).all()), (s, i, float((err / tol).max()))
                 off = (lse[a:a + q, i].double() - want).abs()
@@ -65,3 +70,23 @@ def test_scores_of_minus_infinity(lens, qs, hq, hkv, gone, most):
     out, lse = run(b, max_seq_len=most)
     assert sk.sk_get_device_status() == 0
     check(b, out, lse, list(gone))
+
+
+@pytest.mark.parametrize("most", [0, None])
+@pytest.mark.parametrize("code,nats", [(36.0, 12.7), (44.0, 15.6), (52.0, 18.4), (56.0, 19.8)])
+@pytest.mark.parametrize("lens,qs,hq,hkv", [([20000], [16], 8, 1), ([6000, 3000], [200, 64], 8, 2)])
+def test_a_key_far_above_the_rest_on_e4m3_pages(lens, qs, hq, hkv, code, nats, most):
+    """The first key of each sequence lies `nats` above scores that are nearly equal, and its V is 0: the output is what the
+    others give."""
+    b = batch(lens, qs, hq, hkv, True, 92)
+    b["q"] *= 0.125
+    b["q"][..., 0] = 8.0
+    kv = b["kv"].view(torch.float8_e4m3fn)
+    for s in range(len(lens)):
+        kv[b["bt"][s, :(lens[s] + PAGE - 1) // PAGE].long(), :, :, 0] = 0.0
+        kv[b["bt"][s, 0].long(), :, 0, 0] = code
+        kv[b["bt"][s, 0].long(), :, 0, D:] = 0.0
+    assert abs(8 * code * b["w"].k_scale * b["w"].sm_scale - nats) < 0.1
+    out, lse = run(b, max_seq_len=most)
+    assert sk.sk_get_device_status() == 0
+    check(b, out, lse)
