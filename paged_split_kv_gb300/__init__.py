@@ -507,24 +507,47 @@ def sk_prefill_workspace_bytes(num_tokens: int, num_q_heads: int, kv_dtype: int)
     return _check(lib().sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype), "sk_prefill_workspace_bytes")
 
 
+def _raw_stream(device, stream):
+    """The handle of ``stream``, by default of the current one of ``device``."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index) if device.type == "cuda" else 0
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_object(stream, device):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
 def _owned_by(stream, device):
     """Context in which memory for a call on ``stream`` is taken: it belongs to that stream, so that it is not handed
     out again to another one while the call's kernels still use it."""
     import torch
     if stream is None:
         return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)
+    return torch.cuda.stream(_stream_object(stream, device))
 
 
 def _buffer(ws, key, need, device, stream):
-    """A byte buffer of at least ``need`` bytes, kept in the workspace dict."""
+    """A byte buffer of at least ``need`` bytes, kept in the workspace dict.  One that has become too small stays in
+    the dict as well, for a captured graph may hold its address; sizes at least double, so that all of them together
+    take no more than twice the last.  A call on another stream than the one that the buffer was taken on is recorded,
+    so that its memory is not handed out again while that stream uses it."""
     import torch
     t = ws.get(key)
+    raw = _raw_stream(device, stream)
     if t is None or t.numel() < need or t.device != device:
+        if t is not None:
+            ws.setdefault("outgrown", []).append(t)
+            need = max(need, 2 * t.numel())
         with _owned_by(stream, device):
             t = ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        ws[key + "_stream"] = raw
+    elif raw != ws.get(key + "_stream"):
+        t.record_stream(_stream_object(stream, device))
     return t.data_ptr()
 
 
@@ -534,7 +557,7 @@ def sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out,
     """Attention of a chunk of new tokens over the paged cache into ``out`` (bf16 [num_tokens, num_q_heads, 128])
     and ``lse`` (fp32 [num_tokens, num_q_heads], or None).  ``max_seq_len`` bounds seq_lens (default: what the block
     table holds) and decides how the work is divided.  ``workspace`` is an optional dict that keeps the call's
-    buffer; calls that may overlap need one each."""
+    buffer (and those that it outgrew, which captured graphs may use); calls that may overlap need one each."""
     import torch
     dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,
                                                                                cu_seqlens_q)
