@@ -677,29 +677,50 @@ def sk_evict_move(src_rows, dst_rows, counts, block_table, kv_pages, acc_pages, 
                    _fits(pos_pages, torch.int32, (nb, hkv, page), "pos_pages", dev))
 
 
+def _move_lists(ws, bs, hkv, cap, device, stream):
+    """src_rows, dst_rows and counts of an eviction in the workspace dict: those that are there where they fit, else cut from
+    a kept buffer."""
+    import torch
+    names, i32 = ("src_rows", "dst_rows", "counts"), torch.int32
+    src, dst, counts = found = [ws.get(name) for name in names]
+    shape = (bs, hkv, cap if src is None or src.dim() != 3 else max(cap, src.shape[2]))
+    fit = all(t is not None and t.dtype is i32 and t.device == device and t.is_contiguous() for t in found) and \
+        src.shape == shape and dst.shape == shape and counts.shape == shape[:2]
+    own = ws.get("evict")
+    if fit and (own is None or src.data_ptr() != own.data_ptr()):
+        return src, dst, counts
+    if not fit:
+        if own is None:                              # lists of the caller's that are too small stay, as outgrown buffers do
+            ws.setdefault("outgrown", []).extend(t for t in found if t is not None)
+        shape = (bs, hkv, cap)
+    n, m = shape[0] * shape[1] * shape[2], bs * hkv
+    _buffer(ws, "evict", 4 * (2 * n + m), device, stream)
+    if not fit:
+        flat = ws["evict"][:4 * (2 * n + m)].view(i32)
+        src, dst, counts = flat[:n].view(shape), flat[n:2 * n].view(shape), flat[2 * n:].view(bs, hkv)
+        ws.update(zip(names, (src, dst, counts)))
+    return src, dst, counts
+
+
 def evict_rows(kv_pages, acc_pages, pos_pages, block_table, seq_lens, next_pos, *, budget: int, recent: int = 0,
                max_seq_len: Optional[int] = None, workspace=None, stream=None):
     """One eviction: sk_evict_select and sk_evict_move.  Every sequence longer than ``budget`` is cut down to
-    ``budget`` rows per KV head, in place.  ``workspace`` is an optional dict of preallocated buffers
-    (src_rows, dst_rows, counts) reused across calls of the same shapes.  Returns the new lengths (int32
-    [bs], a new tensor); the pages past them can be handed out again."""
+    ``budget`` rows per KV head, in place.  ``workspace`` is an optional dict that keeps the lists
+    (src_rows, dst_rows, counts, of this call's shapes; ones put there beforehand are used where they fit); calls
+    that may overlap need one each.  Returns the new lengths (int32 [bs], a new tensor); the pages past them can be
+    handed out again."""
     import torch
     bs, hkv, page = seq_lens.numel(), kv_pages.shape[1], kv_pages.shape[2]
     dev = kv_pages.device
     if max_seq_len is None:
         max_seq_len = block_table.shape[1] * page
-    ws = workspace if workspace is not None else {}
+    src, dst, counts = _move_lists(workspace if workspace is not None else {}, bs, hkv,
+                                   sk_evict_capacity(budget, max_seq_len), dev, stream)
     with _owned_by(stream, dev):
-        if "src_rows" not in ws:
-            cap = sk_evict_capacity(budget, max_seq_len)
-            ws["src_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
-            ws["dst_rows"] = torch.empty((bs, hkv, cap), dtype=torch.int32, device=dev)
-            ws["counts"] = torch.empty((bs, hkv), dtype=torch.int32, device=dev)
         new_lens = torch.empty_like(seq_lens)
-    sk_evict_select(acc_pages, pos_pages, block_table, seq_lens, next_pos, ws["src_rows"], ws["dst_rows"],
-                    ws["counts"], new_lens, budget=budget, recent=recent, max_seq_len=max_seq_len, stream=stream)
-    sk_evict_move(ws["src_rows"], ws["dst_rows"], ws["counts"], block_table, kv_pages, acc_pages, pos_pages,
-                  stream=stream)
+    sk_evict_select(acc_pages, pos_pages, block_table, seq_lens, next_pos, src, dst, counts, new_lens, budget=budget,
+                    recent=recent, max_seq_len=max_seq_len, stream=stream)
+    sk_evict_move(src, dst, counts, block_table, kv_pages, acc_pages, pos_pages, stream=stream)
     return new_lens
 
 

@@ -1,8 +1,10 @@
 """Workspaces that captured calls and other streams still use when a later call needs more of them."""
+import numpy as np
 import pytest
 import torch
 
 import paged_split_kv_gb300 as sk
+from test_evict_gpu import PAGE, cache, dev, reference as evicted
 from test_prefill_gpu import batch
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +64,25 @@ def test_a_workspace_used_on_another_stream_and_dropped():
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(acc, want[2])
     assert all(bool((t == 0xA5).all()) for t in held)
     assert sk.sk_get_device_status() == 0
+
+
+def test_evictions_of_growing_lengths_and_other_batches_with_one_workspace():
+    """What a server does that passes its longest length of the moment: the lists follow."""
+    ws = {}
+    for lens, hkv, longest in (([30, 20, 32], 2, 32), ([33, 30, 36], 2, 36), ([33, 64, 100], 2, 100), ([300] * 5, 2, 300),
+                               ([64], 2, 64), ([70, 40], 4, 70)):
+        bt, acc, pos, pages = cache(lens, hkv, 31 + longest)
+        want = evicted(bt, acc, pos, lens, lens, hkv, 32, 4)
+        pg, a, p = dev(pages).view(torch.bfloat16), dev(acc), dev(pos)
+        n = dev(lens, torch.int32)
+        new = sk.evict_rows(pg, a, p, dev(bt), n, n, budget=32, recent=4, max_seq_len=longest, workspace=ws)
+        assert sk.sk_get_device_status() == 0
+        assert new.tolist() == [min(x, 32) for x in lens]
+        for (s, h), (x, y) in want.items():
+            assert ws["counts"][s, h] == len(x)
+            assert ws["src_rows"][s, h, :len(x)].tolist() == x.tolist() and ws["dst_rows"][s, h, :len(x)].tolist() == y.tolist()
+            for t in (pages, acc, pos):
+                t[bt[s, y // PAGE], h, y % PAGE] = t[bt[s, x // PAGE], h, x % PAGE]
+        np.testing.assert_array_equal(pg.view(torch.uint8).cpu().numpy(), pages)
+        np.testing.assert_array_equal(a.cpu().numpy(), acc)
+        np.testing.assert_array_equal(p.cpu().numpy(), pos)
