@@ -375,7 +375,8 @@ int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t
  * Entries from n on are left as they were.  sk_evict_move then moves src_rows[m] to dst_rows[m].  Rows
  * below `budget` that stay do not move, so the rows of a head are not in order of position after it; the
  * attention of this library does not depend on the order of rows that every query token sees.  A sequence
- * with L <= budget has n = 0.  L above max_seq_len (or below 0) sets SK_DEV_BAD_SEQ: n = 0, new_lens = L.
+ * with L <= budget has n = 0.  Each sequence is ranked by itself: one whose blocks another sequence shares (a common
+ * prefix) needs blocks of its own before it is evicted, see sk_evict_move.  L above max_seq_len (or below 0) sets SK_DEV_BAD_SEQ: n = 0, new_lens = L.
  * A row in a block outside [0, num_blocks) ranks like -inf and sets SK_DEV_BAD_BLOCK.
  *
  * acc_pages fp32, pos_pages int32 [num_blocks, num_kv_heads, page_size], 16-byte aligned; src_rows, dst_rows int32 [bs,
@@ -396,8 +397,10 @@ int sk_evict_capacity(int budget, int max_seq_len);
 
 /* Eviction, second step: for every (s, h) and m < counts[s][h], copies row src_rows[s][h][m] of the pages
  * (K and V of that head), of acc_pages and of pos_pages to row dst_rows[s][h][m].  All moves run at once,
- * so no row may be both a source and a destination and no destination may be listed twice;
- * sk_evict_select's lists are so.  Sources keep their contents.  A row outside [0, block_table_stride *
+ * so no row of the pages may be both a source and a destination and no destination may be listed twice, over all
+ * sequences.  sk_evict_select's lists are so where the sequences share no blocks.  Where they do (a common prefix), the
+ * moves of a sequence that is evicted overwrite rows that the others read, and moves of two sequences race; nothing
+ * reports it.  So give a sequence over its budget its own copy of shared blocks first.  Sources keep their contents.  A row outside [0, block_table_stride *
  * page_size), or a count outside [0, capacity], sets SK_DEV_BAD_SEQ, a block outside [0, num_blocks)
  * SK_DEV_BAD_BLOCK; such a move is skipped (of a count above the capacity, the listed moves run).
  * kv_pages [num_blocks, num_kv_heads, 16, 256] bf16 or e4m3fn, 16-byte aligned.  Asynchronous on `stream`,

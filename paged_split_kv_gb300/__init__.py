@@ -659,7 +659,8 @@ def sk_evict_select(acc_pages, pos_pages, block_table, seq_lens, next_pos, src_r
 
 def sk_evict_move(src_rows, dst_rows, counts, block_table, kv_pages, acc_pages, pos_pages, *, stream=None) -> int:
     """Moves rows src_rows to dst_rows (sk_evict_select's lists) of ``kv_pages``, ``acc_pages`` and
-    ``pos_pages``, in place."""
+    ``pos_pages``, in place.  Sequences with moves must not share blocks with others (a common prefix): copy those
+    first."""
     import torch
     dev = src_rows.get_device()
     _need(src_rows, torch.int32, "src_rows", 3)
@@ -705,7 +706,8 @@ def _move_lists(ws, bs, hkv, cap, device, stream):
 def evict_rows(kv_pages, acc_pages, pos_pages, block_table, seq_lens, next_pos, *, budget: int, recent: int = 0,
                max_seq_len: Optional[int] = None, workspace=None, stream=None):
     """One eviction: sk_evict_select and sk_evict_move.  Every sequence longer than ``budget`` is cut down to
-    ``budget`` rows per KV head, in place.  ``workspace`` is an optional dict that keeps the lists
+    ``budget`` rows per KV head, in place; such a sequence must not share blocks with others (a common prefix: copy
+    those blocks first).  ``workspace`` is an optional dict that keeps the lists
     (src_rows, dst_rows, counts, of this call's shapes; ones put there beforehand are used where they fit); calls
     that may overlap need one each.  Returns the new lengths (int32 [bs], a new tensor); the pages past them can be
     handed out again."""
