@@ -269,9 +269,10 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
  * num_tokens (which sets SK_DEV_BAD_SEQ), are left as they were.  At most 2^26 blocks a sequence and 2^24 (sequence,
  * KV head) pairs, here and in the three calls of eviction.
  *
- * The work is divided evenly over the SMs, in the key axis too, so few query rows on a long cache use the
- * whole GPU.  max_seq_len, an upper bound on the lengths, decides how many CTAs a small call launches and how the work is
- * divided; a wrong one costs time only.  workspace (device, 16-byte
+ * The work is divided evenly over the SMs, in the key axis too, so few query rows on a long cache use the whole
+ * GPU, beside many short sequences as well; in a batch larger than the L2 whose units of 256 rows cost alike, or are
+ * many, whole units go out first, which is nearly as even.  max_seq_len, an upper bound on the lengths, decides how many
+ * CTAs a small call launches and how the work is divided; a wrong one costs time only.  workspace (device, 16-byte
  * aligned): sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype) bytes; its contents do not matter, and
  * calls that may overlap need one each.  q, kv_pages and out are 16-byte aligned; lse may be NULL.  Probabilities
  * round to bf16 (for e4m3fn pages to f16, by 2^-11 of themselves or 2^-33 of the row's sum, whichever is more); sums

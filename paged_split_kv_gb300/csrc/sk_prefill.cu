@@ -123,7 +123,9 @@ constexpr int kColS = 0, kColO = 256;                // S_A, S_B, then O_A, O_B,
 // a unit that several runs share go to a slot each, as partial softmax states, and prefill_join_kernel joins them.
 // A batch whose K and V are too large to stay in the L2 begins with whole units, dealt to the CTAs in turn, and only
 // what is left over is shared out like that: CTAs that work at the same time then read the same heads (4096 tokens over
-// 32k keys, 8 KV heads, 151 MB: 1433 us with 0.2 GB read from HBM, against 1543 us and 3.6 GB).
+// 32k keys, 8 KV heads, 151 MB: 1433 us with 0.2 GB read from HBM, against 1543 us and 3.6 GB).  Dealing takes no account of
+// what units cost, so it is done only where the largest costs at most 1.4 times the mean (no CTA then gets more
+// than that times its share) or an eighth of a CTA's share.
 struct Seq {
     int L, q_len, tok0, units;                       // units of one head
     long long base, step;                            // unit i costs base + step * (i + 1)
@@ -322,11 +324,14 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
     const int s0 = min(p.bs, tid * per), s1 = min(p.bs, s0 + per);
     long long cost = 0;
     int units = 0;
+    uint32_t largest = 0;                            // one unit's cost (its keys and the fixed part: below 2^32)
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
         const Seq q = sequence(p, s);
         cost += q.before(q.units) * p.H_kv;
         units += q.units * p.H_kv;
+        if (q.units > 0)
+            largest = max(largest, (uint32_t)q.cost(q.units - 1));
     }
     long long cost_to = cost;                        // inclusive prefixes within the warp
     int units_to = units;
@@ -337,24 +342,29 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
         cost_to += lane >= o ? u : 0;
         units_to += lane >= o ? w : 0;
     }
+    largest = __reduce_max_sync(kFull, largest);
     if (lane == 31) {
         part[2 * warp] = cost_to;
-        part[2 * warp + 1] = units_to;
+        part[2 * warp + 1] = (long long)largest << 32 | (uint32_t)units_to;
     }
     __syncthreads();
     long long total = 0, cost_before = cost_to - cost;
     int all = 0, units_before = units_to - units;
 #pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
+        const long long both = part[2 * w + 1];
         cost_before += w < warp ? part[2 * w] : 0;
-        units_before += w < warp ? (int)part[2 * w + 1] : 0;
+        units_before += w < warp ? (int)both : 0;
         total += part[2 * w];
-        all += (int)part[2 * w + 1];
+        all += (int)both;
+        largest = max(largest, (uint32_t)(both >> 32));
     }
     Share sh;
     sh.first = index;
     sh.stride = count;
-    sh.dealt = p.deal ? all / count * count : 0;
+    const bool alike = (float)largest * (float)all <= 1.4f * (float)total ||
+                       (float)largest * (float)count * 8.f <= (float)total;
+    sh.dealt = p.deal && alike ? all / count * count : 0;
     // the cost of what is dealt, then the run's bounds, in one search each among this thread's sequences
     if (tid == 0)
         found[2] = sh.dealt == all ? total : 0;
