@@ -118,12 +118,14 @@ __device__ __forceinline__ int blocks_of(const AccumParams &p, int s, int &L, in
 {
     L = __ldg(p.seq_lens + s);
     tok0 = __ldg(p.cu_q + s);
-    q = __ldg(p.cu_q + s + 1) - tok0;
-    if (q < 0 || q > p.max_q_len || tok0 < 0 || tok0 + q > p.num_tokens || L < 0 ||
-        (long long)L > (long long)p.bt_stride * kPage) {
+    const int end = __ldg(p.cu_q + s + 1);
+    const bool bad = tok0 < 0 || end < tok0 || end > p.num_tokens || end - tok0 > p.max_q_len || L < 0 ||
+                     (long long)L > (long long)p.bt_stride * kPage;
+    if (bad) {
         atomicOr(p.status, SK_DEV_BAD_SEQ);
-        L = q = 0;
+        L = 0;
     }
+    q = bad ? 0 : end - tok0;
     return L > 0 ? (q + p.tpb - 1) / p.tpb * p.nsub : 0;
 }
 

@@ -141,12 +141,12 @@ __device__ __forceinline__ Seq sequence(const PrefillParams &p, int s)
     Seq q;
     q.L = __ldg(p.seq_lens + s);
     q.tok0 = __ldg(p.cu_q + s);
-    q.q_len = __ldg(p.cu_q + s + 1) - q.tok0;
-    if (q.q_len < 0 || q.q_len > p.max_q_len || q.tok0 < 0 || q.tok0 + q.q_len > p.num_tokens || q.L < 0 ||
-        (long long)q.L > (long long)p.bt_stride * kPage) {
+    const int end = __ldg(p.cu_q + s + 1);
+    const bool bad = q.tok0 < 0 || end < q.tok0 || end > p.num_tokens || end - q.tok0 > p.max_q_len || q.L < 0 ||
+                     (long long)q.L > (long long)p.bt_stride * kPage;
+    if (bad)
         atomicOr(p.status, SK_DEV_BAD_SEQ);
-        q.q_len = 0;
-    }
+    q.q_len = bad ? 0 : end - q.tok0;
     q.units = ((q.q_len + p.tpb - 1) / p.tpb * p.nsub + 1) / 2;
     const bool rising = p.causal && p.nsub == 1;     // later units see more keys
     q.base = kUnitFixed + (rising ? max(0, q.L - q.q_len) : q.L);
@@ -333,45 +333,46 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
         if (q.units > 0)
             largest = max(largest, (uint32_t)q.cost(q.units - 1));
     }
-    long long cost_to = cost;                        // inclusive prefixes within the warp
-    int units_to = units;
+    long long cost_to = cost, units_to = units;      // inclusive prefixes within the warp
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(kFull, cost_to, o);
-        const int w = __shfl_up_sync(kFull, units_to, o);
+        const long long w = __shfl_up_sync(kFull, units_to, o);
         cost_to += lane >= o ? u : 0;
         units_to += lane >= o ? w : 0;
     }
     largest = __reduce_max_sync(kFull, largest);
     if (lane == 31) {
         part[2 * warp] = cost_to;
-        part[2 * warp + 1] = (long long)largest << 32 | (uint32_t)units_to;
+        part[2 * warp + 1] = (long long)((unsigned long long)(largest >> 4) << 36 | units_to);
     }
     __syncthreads();
     long long total = 0, cost_before = cost_to - cost;
-    int all = 0, units_before = units_to - units;
+    // (offsets that overlap may give more units than an int holds; such a batch, which is reported, is not dealt out)
+    long long all = 0, units_before = units_to - units;
 #pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
-        const long long both = part[2 * w + 1];
+        const unsigned long long both = part[2 * w + 1];     // units, and a 16th of their largest cost
+        const long long here = both & ((1ull << 36) - 1);
         cost_before += w < warp ? part[2 * w] : 0;
-        units_before += w < warp ? (int)both : 0;
+        units_before += w < warp ? here : 0;
         total += part[2 * w];
-        all += (int)both;
-        largest = max(largest, (uint32_t)(both >> 32));
+        all += here;
+        largest = max(largest, (uint32_t)(both >> 36) << 4);
     }
     Share sh;
     sh.first = index;
     sh.stride = count;
     const bool alike = (float)largest * (float)all <= 1.4f * (float)total ||
                        (float)largest * (float)count * 8.f <= (float)total;
-    sh.dealt = p.deal && alike ? all / count * count : 0;
+    sh.dealt = p.deal && alike && all <= INT_MAX ? (int)all / count * count : 0;
     // the cost of what is dealt, then the run's bounds, in one search each among this thread's sequences
     if (tid == 0)
         found[2] = sh.dealt == all ? total : 0;
     __syncthreads();
     if (sh.dealt > 0 && units > 0 && sh.dealt >= units_before && sh.dealt < units_before + units) {
         long long before = cost_before;
-        int left = sh.dealt - units_before;
+        int left = sh.dealt - (int)units_before;
 #pragma unroll 1
         for (int s = s0; s < s1; ++s) {
             const Seq q = sequence(p, s);
