@@ -264,10 +264,11 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
  *   out[t][hq] = sum_p softmax(score)_p V_p,  lse[t][hq] = log sum_p exp(score_p)
  * with scores sm_scale * k_scale * <q, k> over the keys that token t sees (the masking, layouts and scales of
  * sk_paged_decode_attn; the chunk's own keys are already in the pages and counted in seq_lens).  A token that
- * sees no key gets out = 0 and lse = -inf.  Query lengths may differ and may be 0; max_q_len bounds them (more
- * sets SK_DEV_BAD_SEQ and skips the sequence, whose rows are then undefined).  Rows past cu_seqlens_q[bs], if that is below
- * num_tokens (which sets SK_DEV_BAD_SEQ), are left as they were.  At most 2^26 blocks a sequence and 2^24 (sequence,
- * KV head) pairs, here and in the three calls of eviction.
+ * sees no key gets out = 0 and lse = -inf.  Query lengths may differ and may be 0; with no tokens at all nothing is launched,
+ * and q, out and lse may be NULL.  max_q_len bounds the query lengths (more sets SK_DEV_BAD_SEQ and skips the sequence,
+ * whose rows are then undefined).  Rows past cu_seqlens_q[bs], if that is below num_tokens (which sets SK_DEV_BAD_SEQ), are
+ * left as they were.  At most 2^26 blocks a sequence and 2^24 (sequence, KV head) pairs, here and in the three calls
+ * of eviction.
  *
  * The work is divided evenly over the SMs, in the key axis too, so few query rows on a long cache use the whole
  * GPU, beside many short sequences as well; in a batch larger than the L2 whose units of 256 rows cost alike, or are

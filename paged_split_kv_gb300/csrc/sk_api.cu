@@ -688,8 +688,8 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
                           int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int max_seq_len,
                           void *workspace, int64_t workspace_bytes, void *out, float *lse, void *stream)
 {
-    if (q == nullptr || kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr ||
-        cu_seqlens_q == nullptr || out == nullptr)
+    if (kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr || cu_seqlens_q == nullptr ||
+        (num_tokens != 0 && (q == nullptr || out == nullptr)))       // arrays of no tokens may have no address
         return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: null pointer argument");
     if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
         return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: kv_dtype=%d", kv_dtype);
@@ -777,8 +777,8 @@ int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, flo
                           int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal,
                           const float *lse, float *acc_pages, void *workspace, int64_t workspace_bytes, void *stream)
 {
-    if (q == nullptr || kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr ||
-        cu_seqlens_q == nullptr || lse == nullptr || acc_pages == nullptr)
+    if (kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr || cu_seqlens_q == nullptr ||
+        acc_pages == nullptr || (num_tokens != 0 && (q == nullptr || lse == nullptr)))
         return fail(SK_ERR_INVALID, "sk_accum_attn_weights: null pointer argument");
     if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
         return fail(SK_ERR_INVALID, "sk_accum_attn_weights: kv_dtype=%d", kv_dtype);
