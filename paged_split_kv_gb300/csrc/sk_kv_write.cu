@@ -16,12 +16,10 @@
 // 16 l (bf16) or 8 l (e4m3) of the row either way.  Each warp takes four rows
 // at a time, loads first, so about 2 KB per warp is in flight.
 #include <cuda_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
-#include <cmath>
-
 #include "sk_internal.cuh"
+#include "sk_quant.cuh"
 
 namespace sk {
 namespace {
@@ -38,19 +36,11 @@ __device__ __forceinline__ uint4 ld_stream(const void *p)
     return v;
 }
 
-// Two bf16 values (one packed word) divided by `scale` -> two e4m3fn codes
-// (low byte from the low half), nearest even, saturated.  With RECIP the
-// caller guarantees scale = 2^k and inv = 2^-k exactly, so x * inv is the
-// correctly rounded x / scale (both round the same real number).
+// Two bf16 values (one packed word) divided by `scale`, as two e4m3fn codes.
 template <bool RECIP>
 __device__ __forceinline__ uint32_t quant2(uint32_t w, float scale, float inv)
 {
-    const float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xFFFF0000u);
-    const float lo = RECIP ? a * inv : __fdiv_rn(a, scale);
-    const float hi = RECIP ? b * inv : __fdiv_rn(b, scale);
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
+    return quant_e4m3x2<RECIP>(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u), scale, inv);
 }
 
 template <bool FP8, bool RECIP>
@@ -119,17 +109,10 @@ cudaError_t launch_kv_write(const uint16_t *key, const uint16_t *value, const in
     const long long cap = (long long)(num_sms > 0 ? num_sms : 1) * 8;   // 8 CTAs of 256 per SM
     blocks = blocks < cap ? blocks : cap;
     const long long num_slots = num_blocks * kPage;
-    // a power-of-two scale with a normal reciprocal: multiply instead of divide
-    auto exact_recip = [](float sc) {
-        int e = 0;
-        const float m = frexpf(sc, &e);
-        const float r = 1.f / sc;
-        return m == 0.5f && r * sc == 1.f && std::isnormal(r) && std::isnormal(sc);
-    };
     const dim3 grid((unsigned)blocks);
-    auto kernel = kv_dtype != SK_KV_FP8_E4M3                     ? kv_write_kernel<false, false>
-                  : (exact_recip(k_scale) && exact_recip(v_scale)) ? kv_write_kernel<true, true>
-                                                                   : kv_write_kernel<true, false>;
+    auto kernel = kv_dtype != SK_KV_FP8_E4M3                                 ? kv_write_kernel<false, false>
+                  : (exact_reciprocal(k_scale) && exact_reciprocal(v_scale)) ? kv_write_kernel<true, true>
+                                                                             : kv_write_kernel<true, false>;
     return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, key, value, slot_mapping, rows, num_kv_heads, num_slots,
                       pages, k_scale, v_scale, status);
 }
