@@ -277,7 +277,9 @@ int sk_std_to_shuffled(const void *kv_pages, int kv_dtype, const int32_t *block_
  * aligned): sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype) bytes; its contents do not matter, and
  * calls that may overlap need one each.  q, kv_pages and out are 16-byte aligned; lse may be NULL.  Probabilities
  * round to bf16 (for e4m3fn pages to f16, by 2^-11 of themselves or 2^-33 of the row's sum, whichever is more); sums
- * are fp32; the same bits every time on the same device.
+ * are fp32; the same bits every time on the same device.  With e4m3fn pages q is two e4m3 terms per element, as for
+ * sk_accum_attn_weights.  A key that a row does not see weighs exactly 0 there: a NaN or an infinity in its K does not
+ * matter, one in its V may reach the row as 0 times it.  (The page rows past a sequence's end may hold anything.)
  * Returns SK_OK or a negative sk_status. */
 int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
                           const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
@@ -303,7 +305,7 @@ int64_t sk_prefill_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype
  * most 64 rows (max_q_len times the heads of a group; then it may be NULL); its contents do not matter, and calls that
  * may overlap need one each.  q and kv_pages are 16-byte aligned.
  * Scores and sums are fp32; with e4m3fn pages q is two e4m3 terms per element, exact for elements of at least
- * 2^-9 of the row's largest.  Asynchronous on `stream`, no allocation, capture safe.
+ * 2^-9 of the row's largest (an infinite element saturates: it counts as 896, beside the others as they are).  Asynchronous on `stream`, no allocation, capture safe.
  * Returns SK_OK or a negative sk_status. */
 int sk_accum_attn_weights(const void *q, const void *kv_pages, int kv_dtype, float k_scale,
                           const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
@@ -342,7 +344,7 @@ int sk_rope_frequencies(int rot_dim, double base, int scaling, double factor, do
  *   kv_pages (slot t)  K: every KV head of key, turned; V: value; bf16 pages round once from the fp32
  *                      result, e4m3fn pages take the fp32 result divided by k_scale (v_scale)
  *                      and rounded like sk_reshape_and_cache
- *   acc_pages (slot t), pos_pages (slot t)  0 and p for every KV head, where the arrays are given
+ *   acc_pages (slot t), pos_pages (slot t)  0 and p (its low 32 bits) for every KV head, where the arrays are given
  * A negative slot writes q_out only.  A slot at or past num_blocks * page_size writes q_out only and sets
  * SK_DEV_BAD_BLOCK.  Two tokens with the same slot leave that row undefined.  Angles are taken
  * in 64 bits modulo a revolution, so far positions lose no more than the rounding of freqs; positions may be
@@ -460,9 +462,10 @@ int sk_get_device_status(void *stream, int clear);
  * thread read (0 before the first call). */
 int sk_last_device_status(void);
 
-/* Limit, in SM clock cycles, of each wait of the attention kernel that can
- * give up (for a copy to land, a product to complete, another role to finish
- * its part of a tile).  It applies to the launches made after the call;
+/* Limit, in SM clock cycles, of each wait of the attention kernels (decode and
+ * verify, chunk attention, attention weights) that can give up (for a copy to
+ * land, a product to complete, another role to finish its part of a tile).
+ * It applies to the launches made after the call;
  * cycles < 0 restores the default of 4e9 (about two seconds).  Returns the
  * previous limit.  Waits for work a CTA has already issued -- its copies and
  * products in flight, before the CTA exits -- keep the default whatever this

@@ -203,7 +203,7 @@ plan_capacity = sk_plan_capacity
 
 
 def sk_set_wait_limit(cycles: int) -> int:
-    """Sets the attention kernel's abortable-wait limit in SM cycles (negative:
+    """Sets the attention kernels' abortable-wait limit in SM cycles (negative:
     the default, about two seconds) for later launches; returns the previous one.
     A test hook for the timeout path."""
     return int(lib().sk_set_wait_limit(int(cycles)))
