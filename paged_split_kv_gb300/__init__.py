@@ -545,9 +545,10 @@ def _buffer(ws, key, need, device, stream):
             need = max(need, 2 * t.numel())
         with _owned_by(stream, device):
             t = ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
-        ws[key + "_stream"] = raw
-    elif raw != ws.get(key + "_stream"):
+        ws[key + "_streams"] = {raw}
+    elif raw not in ws.setdefault(key + "_streams", set()):
         t.record_stream(_stream_object(stream, device))
+        ws[key + "_streams"].add(raw)                # once is enough: it lasts until the memory is free
     return t.data_ptr()
 
 

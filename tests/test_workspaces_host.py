@@ -115,3 +115,10 @@ def test_eviction_lists_follow_the_call(monkeypatch):
     ws = dict(mine)
     assert evict(ws, 3, 150) is mine["src_rows"] and ws["src_rows"] is mine["src_rows"]
     assert evict(ws, 3, 151) is not mine["src_rows"] and any(t is mine["src_rows"] for t in ws["outgrown"])
+
+
+def test_a_stream_is_recorded_once(streams):
+    dev, ws = torch.device("cuda", 0), {}
+    for handle in (7, 8, 7, 8, 9, 8, 9):
+        sk._buffer(ws, "prefill", 10, dev, Stream(handle))
+    assert [s.cuda_stream for s in ws["prefill"].used_on] == [8, 9]
