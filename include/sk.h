@@ -20,8 +20,9 @@
  * bs == 1, where it already gives 64 segments).
  *
  * Around them, on the same pages: the writes of new tokens (sk_reshape_and_cache, or with rotary positions
- * sk_rope_and_cache), attention of many new tokens at once (sk_paged_prefill_attn), and a cache bounded by eviction
- * (sk_accum_attn_weights, sk_evict_select, sk_evict_move).
+ * sk_rope_and_cache, of several axes sk_rope_axes_and_cache), attention of many new tokens at once
+ * (sk_paged_prefill_attn), attention with a sliding window and sinks (sk_paged_window_attn), and a cache bounded by
+ * eviction (sk_accum_attn_weights, sk_evict_select, sk_evict_move).
  *
  * Conventions for every call:
  *  - Pointers marked "device" are device memory owned by the caller; the
@@ -287,6 +288,35 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
                           int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int max_seq_len,
                           void *workspace, int64_t workspace_bytes, void *out, float *lse, void *stream);
 
+/* Attention with a sliding window and sinks, of one token a sequence up to whole prompts: the query token in row
+ * P = seq_lens[s] - q_s + j of its sequence (j < q_s, its query length) sees the rows r <= P with
+ *   r < sinks  or  r > P - window,
+ * so its last `window` rows, its own among them, and the first `sinks` ones (window >= 1, sinks >= 0; with a window of
+ * at least seq_lens[s] it is causal attention over the whole cache).  Everything else as for sk_paged_prefill_attn with
+ * causal set: arguments, layouts, outputs, roundings, workspace rules and status bits.  A row with P < 0 sees nothing:
+ * its output is 0, its lse -inf.  Rows are counted along the block table, so a cache that sk_evict_move has reordered
+ * has no window.
+ *
+ * Pages that no query token of the sequence sees are not read, and their block table entries are not looked at: a
+ * server may hand them back and leave anything there.  They are the whole pages between row sinks and row
+ * seq_lens[s] - q_s + 1 - window.  Rows in pages that are read, but that no token of the call sees, may hold anything as
+ * well.  The rule on a NaN or an infinity in V that sk_paged_prefill_attn gives holds for rows that only some
+ * tokens of the call see.
+ *
+ * workspace (device, 16-byte aligned): sk_window_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len,
+ * kv_dtype) bytes.  max_seq_len as for sk_paged_prefill_attn.  Asynchronous on `stream`, no allocation, capture safe.
+ * Returns SK_OK or a negative sk_status. */
+int sk_paged_window_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                         const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                         const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                         int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int window, int sinks,
+                         int max_seq_len, void *workspace, int64_t workspace_bytes, void *out, float *lse,
+                         void *stream);
+
+/* Bytes of workspace of sk_paged_window_attn on the current device.  A negative sk_status for bad sizes or if a CUDA call
+ * fails. */
+int64_t sk_window_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int max_q_len, int kv_dtype);
+
 /* Bytes of workspace of sk_paged_prefill_attn on the current device (two partial states of 256 rows per SM, and for
  * e4m3fn pages q in two terms).  A negative sk_status for bad sizes or if a CUDA call fails. */
 int64_t sk_prefill_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype);
@@ -364,6 +394,31 @@ int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t
                       int num_q_heads, int num_kv_heads, int head_dim, void *q_out, void *kv_pages, int kv_dtype,
                       float k_scale, float v_scale, int num_blocks, int page_size, float *acc_pages,
                       int32_t *pos_pages, void *stream);
+
+/* Axes of sk_rope_axes_and_cache at most. */
+#define SK_MAX_AXES 4
+
+/* Which axis turns each pair of a rotary embedding with several axes (such as time, height and width), on the host:
+ * axes[rot_dim / 2] (host, caller-owned).  sections[a], a < num_axes, is how many pairs axis a has; they add up to
+ * rot_dim / 2.  cycled == 0: the axes' pairs follow one another (axis 0 has the first sections[0]).  cycled != 0: pair i
+ * belongs to axis i mod num_axes while that axis has pairs left, and what is left at the end to axis 0.
+ * Returns SK_OK, or SK_ERR_INVALID (odd rot_dim, sections that do not add up or, cycled, do not go round). */
+int sk_rope_axes(int rot_dim, int num_axes, const int *sections, int cycled, uint8_t *axes);
+
+/* The rotary write with several axes: sk_rope_and_cache where pair i of token t turns by the angle
+ * p w_i with p = positions[axes[i]][t], its position on the pair's axis.  Text tokens have the same position on
+ * every axis; an image or video patch has its place in the grid.
+ *
+ * positions int64 [num_axes][num_tokens] with positions_stride elements between axes (a view of a wider buffer will do);
+ * axes uint8 [rot_dim / 2] (device), from sk_rope_axes or the caller's own; 1 <= num_axes <= SK_MAX_AXES.  pos_pages, where
+ * given, receives the position on axis 0.  An axis of num_axes or more sets SK_DEV_BAD_SEQ, and its pair does not
+ * turn (it is multiplied by attn_factor).  Everything else as for sk_rope_and_cache. */
+int sk_rope_axes_and_cache(const void *q, const void *key, const void *value, int64_t q_stride, int64_t key_stride,
+                           int64_t value_stride, const int64_t *positions, int64_t positions_stride, int num_axes,
+                           const double *freqs, const uint8_t *axes, int rot_dim, int interleaved, float attn_factor,
+                           const int64_t *slot_mapping, int num_tokens, int num_q_heads, int num_kv_heads,
+                           int head_dim, void *q_out, void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                           int num_blocks, int page_size, float *acc_pages, int32_t *pos_pages, void *stream);
 
 /* Eviction of cached rows by gathered attention weight, first step: which rows stay.
  *

@@ -9,8 +9,10 @@ the C names (``sk_build_plan``, ``sk_paged_decode_attn``,
 ``sk_std_to_shuffled``) and take torch tensors; ``paged_decode_attention``
 chains the three attention calls the way a serving step does.  Around them:
 ``sk_rope_and_cache`` (rotary positions with the KV write),
+``sk_rope_axes_and_cache`` (the same with several axes),
 ``paged_prefill_attention`` (attention of a chunk of new tokens over the
-pages), ``sk_accum_attn_weights`` (the attention weight each cached key
+pages), ``paged_window_attention`` (attention with a sliding window and
+sinks, steps and chunks), ``sk_accum_attn_weights`` (the attention weight each cached key
 receives) and ``evict_rows`` (a cache cut down to its heaviest and latest
 rows).  If ``libsk.so`` has not been built, every call raises: there is no
 fallback.
@@ -32,6 +34,8 @@ __all__ = [
     "SK_DEV_BAD_SEQ", "SK_DEV_TIMEOUT", "sk_rope_frequencies", "sk_rope_and_cache", "sk_evict_capacity",
     "sk_evict_select", "sk_evict_move", "evict_rows", "sk_prefill_workspace_bytes",
     "sk_paged_prefill_attn", "paged_prefill_attention", "sk_accum_attn_weights", "sk_accum_workspace_bytes",
+    "sk_window_workspace_bytes", "sk_paged_window_attn", "paged_window_attention", "sk_rope_axes",
+    "sk_rope_axes_and_cache",
 ]
 
 SK_OK = 0
@@ -102,6 +106,16 @@ def lib():
         L.sk_paged_prefill_attn.restype = i32
         L.sk_paged_prefill_attn.argtypes = [P, P, i32, f32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32,
                                             f32, i32, i32, P, i64, P, P, P]
+        L.sk_window_workspace_bytes.restype = i64
+        L.sk_window_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.sk_paged_window_attn.restype = i32
+        L.sk_paged_window_attn.argtypes = [P, P, i32, f32, f32, P, i32, i32, i32, P, P, i32, i32, i32, i32, i32, i32,
+                                           f32, i32, i32, i32, P, i64, P, P, P]
+        L.sk_rope_axes.restype = i32
+        L.sk_rope_axes.argtypes = [i32, i32, ctypes.POINTER(i32), i32, ctypes.POINTER(ctypes.c_uint8)]
+        L.sk_rope_axes_and_cache.restype = i32
+        L.sk_rope_axes_and_cache.argtypes = [P, P, P, i64, i64, i64, P, i64, i32, P, P, i32, i32, f32, P, i32, i32, i32,
+                                             i32, P, P, i32, f32, f32, i32, i32, P, P, P]
         L.sk_accum_workspace_bytes.restype = i64
         L.sk_accum_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
         L.sk_accum_attn_weights.restype = i32
@@ -464,6 +478,17 @@ def sk_rope_and_cache(q, key, value, positions, freqs, slot_mapping, kv_pages, q
     stored token: the state that eviction works on."""
     import torch
     dev = q.get_device()
+    head, tail = _rope_args(q, key, value, freqs, slot_mapping, kv_pages, q_out, interleaved, attn_factor, k_scale,
+                            v_scale, acc_pages, pos_pages, dev)
+    return _launch(dev, stream, "sk_rope_and_cache", lib().sk_rope_and_cache, *head,
+                   _fits(positions, torch.int64, (q.shape[0],), "positions", dev),
+                   _fits(freqs, torch.float64, freqs.shape, "freqs", dev), *tail)
+
+
+def _rope_args(q, key, value, freqs, slot_mapping, kv_pages, q_out, interleaved, attn_factor, k_scale, v_scale,
+               acc_pages, pos_pages, dev):
+    """The checked arguments of a rotary write, those before the positions and those after the frequencies."""
+    import torch
     (pq, qs), (pk, ks), (pv, vs) = _heads_view(q, "q", dev), _heads_view(key, "key", dev), _heads_view(value, "value", dev)
     nt, hq, d = q.shape
     hkv = key.shape[1]
@@ -474,13 +499,49 @@ def sk_rope_and_cache(q, key, value, positions, freqs, slot_mapping, kv_pages, q
         raise ValueError("kv_pages must be [num_blocks, num_kv_heads, page, 2 * head_dim]")
     acc = None if acc_pages is None else _fits(acc_pages, torch.float32, (nb, hkv, page), "acc_pages", dev)
     pos = None if pos_pages is None else _fits(pos_pages, torch.int32, (nb, hkv, page), "pos_pages", dev)
-    rot2 = freqs.numel()
-    return _launch(dev, stream, "sk_rope_and_cache", lib().sk_rope_and_cache, pq, pk, pv, qs, ks, vs,
-                   _fits(positions, torch.int64, (nt,), "positions", dev),
-                   _fits(freqs, torch.float64, (rot2,), "freqs", dev), 2 * rot2, 1 if interleaved else 0, attn_factor,
-                   _fits(slot_mapping, torch.int64, (nt,), "slot_mapping", dev), nt, hq, hkv, d,
-                   _fits(q_out, torch.bfloat16, (nt, hq, d), "q_out", dev), pp, dt, k_scale, v_scale, nb, page, acc,
-                   pos)
+    if freqs.dim() != 1:
+        _need(freqs, torch.float64, "freqs", 1)
+    return ((pq, pk, pv, qs, ks, vs),
+            (2 * freqs.numel(), 1 if interleaved else 0, attn_factor,
+             _fits(slot_mapping, torch.int64, (nt,), "slot_mapping", dev), nt, hq, hkv, d,
+             _fits(q_out, torch.bfloat16, (nt, hq, d), "q_out", dev), pp, dt, k_scale, v_scale, nb, page, acc, pos))
+
+
+def sk_rope_axes(rot_dim: int, sections, *, cycled: bool = False, device=None):
+    """The axis that turns each pair of a rotary embedding with several axes (uint8 [rot_dim / 2] on ``device``):
+    ``sections`` pairs for each axis, one axis's after the other's, or ``cycled``: the axes in turn while they have pairs
+    left, what is left at the end for the first."""
+    import torch
+    sec = (ctypes.c_int * max(1, len(sections)))(*[int(n) for n in sections])
+    out = (ctypes.c_uint8 * max(1, int(rot_dim) // 2))()
+    _check(lib().sk_rope_axes(int(rot_dim), len(sections), sec, 1 if cycled else 0, out), "sk_rope_axes")
+    return torch.tensor(list(out), dtype=torch.uint8, device=device)
+
+
+def sk_rope_axes_and_cache(q, key, value, positions, freqs, axes, slot_mapping, kv_pages, q_out, *,
+                           interleaved: bool = False, attn_factor: float = 1.0, k_scale: float = 1.0,
+                           v_scale: float = 1.0, acc_pages=None, pos_pages=None, stream=None) -> int:
+    """sk_rope_and_cache with several axes (time, height and width of image and video patches): pair i of token t turns
+    by ``positions[axes[i], t] * freqs[i]``.  ``positions``: int64 [num_axes, num_tokens], its rows contiguous (a view
+    of a wider buffer will do); ``axes``: uint8 [rot_dim / 2] (sk_rope_axes).  ``pos_pages`` receives the position on
+    axis 0.  The other arguments as there."""
+    import torch
+    dev = q.get_device()
+    head, tail = _rope_args(q, key, value, freqs, slot_mapping, kv_pages, q_out, interleaved, attn_factor, k_scale,
+                            v_scale, acc_pages, pos_pages, dev)
+    nt = q.shape[0]
+    if positions.dtype is not torch.int64 or positions.dim() != 2 or positions.shape[1] != nt:
+        raise ValueError(f"positions must be int64 [num_axes, {nt}], is {positions.dtype} {tuple(positions.shape)}")
+    num_axes = positions.shape[0]
+    stride, step = positions.stride()
+    if step != 1 and nt > 1:
+        raise ValueError(f"positions must have contiguous rows, has strides {positions.stride()}")
+    if positions.get_device() != dev:
+        raise ValueError(f"positions must be a CUDA tensor on the device of the other arguments, is on {positions.device}")
+    return _launch(dev, stream, "sk_rope_axes_and_cache", lib().sk_rope_axes_and_cache, *head, positions.data_ptr(),
+                   max(stride, nt) if num_axes == 1 else stride, num_axes,
+                   _fits(freqs, torch.float64, freqs.shape, "freqs", dev),
+                   _fits(axes, torch.uint8, freqs.shape, "axes", dev), *tail)
 
 
 def _batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q):
@@ -594,6 +655,58 @@ def paged_prefill_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *,
     sk_paged_prefill_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, max_q_len=max_q_len,
                           sm_scale=sm_scale, max_seq_len=max_seq_len, k_scale=k_scale, v_scale=v_scale, causal=causal,
                           workspace=workspace, stream=stream)
+    return out, lse
+
+
+def sk_window_workspace_bytes(num_tokens: int, num_q_heads: int, num_kv_heads: int, max_q_len: int,
+                              kv_dtype: int) -> int:
+    """Bytes of device workspace that sk_paged_window_attn needs on the current device (computed by the library)."""
+    return _check(lib().sk_window_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype),
+                  "sk_window_workspace_bytes")
+
+
+def sk_paged_window_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse=None, *, window: int,
+                         sinks: int = 0, max_q_len: int, sm_scale: float, max_seq_len: Optional[int] = None,
+                         k_scale: float = 1.0, v_scale: float = 1.0, workspace=None, stream=None) -> int:
+    """Attention of new tokens over the last ``window`` rows of the paged cache (a token's own among them) and its first
+    ``sinks`` ones, into ``out`` (bf16 [num_tokens, num_q_heads, 128]) and ``lse`` (fp32 [num_tokens, num_q_heads], or
+    None); for decode and verify steps as for chunks.  Block table entries of pages that no token of the call sees are
+    not looked at.  ``max_seq_len`` and ``workspace`` as for sk_paged_prefill_attn."""
+    import torch
+    dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,
+                                                                               cu_seqlens_q)
+    po = _fits(out, torch.bfloat16, (nt, hq, d), "out", dev)
+    pl = None if lse is None else _fits(lse, torch.float32, (nt, hq), "lse", dev)
+    buf, need = None, 0
+    if dev >= 0:
+        if torch.cuda.current_device() == dev:
+            need = sk_window_workspace_bytes(nt, hq, hkv, max_q_len, dt)
+        else:
+            with torch.cuda.device(dev):
+                need = sk_window_workspace_bytes(nt, hq, hkv, max_q_len, dt)
+        if need:
+            buf = _buffer(workspace if workspace is not None else {}, "window", need, q.device, stream)
+    return _launch(dev, stream, "sk_paged_window_attn", lib().sk_paged_window_attn, pq, pp, dt, k_scale, v_scale, pb,
+                   stride, nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, window, sinks,
+                   stride * page if max_seq_len is None else max_seq_len, buf, need, po, pl)
+
+
+def paged_window_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *, window: int, sinks: int = 0,
+                           max_q_len: int, sm_scale: float, max_seq_len: Optional[int] = None, k_scale: float = 1.0,
+                           v_scale: float = 1.0, workspace=None, out=None, lse=None, stream=None):
+    """One call of attention with a sliding window and sinks (decode and verify steps, prompts, chunks of prompts);
+    arguments as sk_paged_window_attn.  Returns (out bf16 [NT, H_q, 128], lse fp32 [NT, H_q])."""
+    import torch
+    nt, hq, d = q.shape
+    if out is None or lse is None:
+        with _owned_by(stream, q.device):
+            if out is None:
+                out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=q.device)
+            if lse is None:
+                lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
+    sk_paged_window_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, window=window, sinks=sinks,
+                         max_q_len=max_q_len, sm_scale=sm_scale, max_seq_len=max_seq_len, k_scale=k_scale,
+                         v_scale=v_scale, workspace=workspace, stream=stream)
     return out, lse
 
 

@@ -533,43 +533,44 @@ int sk_rope_frequencies(int rot_dim, double base, int scaling, double factor, do
     return SK_OK;
 }
 
-int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t q_stride, int64_t key_stride,
-                      int64_t value_stride, const int64_t *positions, const double *freqs, int rot_dim,
-                      int interleaved, float attn_factor, const int64_t *slot_mapping, int num_tokens,
-                      int num_q_heads, int num_kv_heads, int head_dim, void *q_out, void *kv_pages, int kv_dtype,
-                      float k_scale, float v_scale, int num_blocks, int page_size, float *acc_pages,
-                      int32_t *pos_pages, void *stream)
+// Both rotary writes: `axes` NULL for the one with a single axis.
+static int rope_call(const char *name, const void *q, const void *key, const void *value, int64_t q_stride,
+                     int64_t key_stride, int64_t value_stride, const int64_t *positions, int64_t pos_stride,
+                     int num_axes, const uint8_t *axes, const double *freqs, int rot_dim, int interleaved,
+                     float attn_factor, const int64_t *slot_mapping, int num_tokens, int num_q_heads, int num_kv_heads,
+                     int head_dim, void *q_out, void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                     int num_blocks, int page_size, float *acc_pages, int32_t *pos_pages, void *stream)
 {
     if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1)
-        return fail(SK_ERR_INVALID, "sk_rope_and_cache: num_tokens=%d num_q_heads=%d num_kv_heads=%d num_blocks=%d",
+        return fail(SK_ERR_INVALID, "%s: num_tokens=%d num_q_heads=%d num_kv_heads=%d num_blocks=%d", name,
                     num_tokens, num_q_heads, num_kv_heads, num_blocks);
     if (num_q_heads > (1 << 20) || num_kv_heads > (1 << 20))
-        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: %d query heads, %d kv heads", num_q_heads, num_kv_heads);
+        return fail(SK_ERR_UNSUPPORTED, "%s: %d query heads, %d kv heads", name, num_q_heads, num_kv_heads);
     if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
-        return fail(SK_ERR_INVALID, "sk_rope_and_cache: kv_dtype=%d", kv_dtype);
+        return fail(SK_ERR_INVALID, "%s: kv_dtype=%d", name, kv_dtype);
     if (head_dim != kHeadDim)
-        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: head_dim=%d (only 128)", head_dim);
+        return fail(SK_ERR_UNSUPPORTED, "%s: head_dim=%d (only 128)", name, head_dim);
     if (page_size != kPage)
-        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: page_size=%d (only 16)", page_size);
+        return fail(SK_ERR_UNSUPPORTED, "%s: page_size=%d (only 16)", name, page_size);
     if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0)
-        return fail(SK_ERR_UNSUPPORTED, "sk_rope_and_cache: rot_dim=%d (multiples of 16 up to 128)", rot_dim);
+        return fail(SK_ERR_UNSUPPORTED, "%s: rot_dim=%d (multiples of 16 up to 128)", name, rot_dim);
     if (!(attn_factor > 0.f && attn_factor < INFINITY))
-        return fail(SK_ERR_INVALID, "sk_rope_and_cache: attn_factor must be positive and finite");
+        return fail(SK_ERR_INVALID, "%s: attn_factor must be positive and finite", name);
     if (kv_dtype == SK_KV_FP8_E4M3 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY))
-        return fail(SK_ERR_INVALID, "sk_rope_and_cache: scales must be positive and finite");
+        return fail(SK_ERR_INVALID, "%s: scales must be positive and finite", name);
     if (num_tokens == 0)
         return SK_OK;
     if (q == nullptr || key == nullptr || value == nullptr || positions == nullptr || freqs == nullptr ||
         slot_mapping == nullptr || q_out == nullptr || kv_pages == nullptr)
-        return fail(SK_ERR_INVALID, "sk_rope_and_cache: null pointer argument");
+        return fail(SK_ERR_INVALID, "%s: null pointer argument", name);
     if (q_stride < (int64_t)num_q_heads * kHeadDim || key_stride < (int64_t)num_kv_heads * kHeadDim ||
         value_stride < (int64_t)num_kv_heads * kHeadDim || ((q_stride | key_stride | value_stride) & 7))
         return fail(SK_ERR_INVALID,
-                    "sk_rope_and_cache: token strides %lld, %lld, %lld must cover the heads and be multiples of 8",
+                    "%s: token strides %lld, %lld, %lld must cover the heads and be multiples of 8", name,
                     (long long)q_stride, (long long)key_stride, (long long)value_stride);
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value) |
          reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(kv_pages)) & 15)
-        return fail(SK_ERR_INVALID, "sk_rope_and_cache: q, key, value, q_out and kv_pages must be 16-byte aligned");
+        return fail(SK_ERR_INVALID, "%s: q, key, value, q_out and kv_pages must be 16-byte aligned", name);
     int *status = nullptr;
     int sms = 0;
     int rc = status_ptr(&status);
@@ -581,11 +582,79 @@ int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t
                                       static_cast<const uint16_t *>(value), q_stride, key_stride, value_stride,
                                       positions, freqs, slot_mapping, num_tokens, num_q_heads, num_kv_heads, rot_dim,
                                       interleaved ? 1 : 0, attn_factor, static_cast<uint16_t *>(q_out), kv_pages,
-                                      kv_dtype, k_scale, v_scale, num_blocks, acc_pages, pos_pages, status, sms,
-                                      static_cast<cudaStream_t>(stream));
+                                      kv_dtype, k_scale, v_scale, num_blocks, acc_pages, pos_pages, axes,
+                                      pos_stride, num_axes, status, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "rope kernel launch");
     return SK_OK;
+}
+
+int sk_rope_and_cache(const void *q, const void *key, const void *value, int64_t q_stride, int64_t key_stride,
+                      int64_t value_stride, const int64_t *positions, const double *freqs, int rot_dim,
+                      int interleaved, float attn_factor, const int64_t *slot_mapping, int num_tokens,
+                      int num_q_heads, int num_kv_heads, int head_dim, void *q_out, void *kv_pages, int kv_dtype,
+                      float k_scale, float v_scale, int num_blocks, int page_size, float *acc_pages,
+                      int32_t *pos_pages, void *stream)
+{
+    return rope_call("sk_rope_and_cache", q, key, value, q_stride, key_stride, value_stride, positions, 0, 1, nullptr,
+                     freqs, rot_dim, interleaved, attn_factor, slot_mapping, num_tokens, num_q_heads, num_kv_heads,
+                     head_dim, q_out, kv_pages, kv_dtype, k_scale, v_scale, num_blocks, page_size, acc_pages,
+                     pos_pages, stream);
+}
+
+int sk_rope_axes(int rot_dim, int num_axes, const int *sections, int cycled, uint8_t *axes)
+{
+    if (rot_dim < 2 || (rot_dim & 1) || num_axes < 1 || num_axes > SK_MAX_AXES || sections == nullptr || axes == nullptr)
+        return fail(SK_ERR_INVALID, "sk_rope_axes: rot_dim=%d num_axes=%d (1 to %d) sections=%p axes=%p", rot_dim,
+                    num_axes, SK_MAX_AXES, (const void *)sections, (void *)axes);
+    const int half = rot_dim / 2;
+    long long total = 0;
+    for (int a = 0; a < num_axes; ++a) {
+        if (sections[a] < 0)
+            return fail(SK_ERR_INVALID, "sk_rope_axes: section %d has %d pairs", a, sections[a]);
+        total += sections[a];
+    }
+    if (total != half)
+        return fail(SK_ERR_INVALID, "sk_rope_axes: the sections hold %lld pairs, rot_dim=%d has %d", total, rot_dim, half);
+    if (!cycled) {
+        for (int a = 0, i = 0; a < num_axes; ++a)
+            for (int n = 0; n < sections[a]; ++n)
+                axes[i++] = (uint8_t)a;
+        return SK_OK;
+    }
+    // pair i belongs to axis i mod num_axes while that axis has pairs left, and to the first axis after that
+    int count[SK_MAX_AXES] = {};
+    for (int i = 0; i < half; ++i) {
+        const int a = i % num_axes;
+        axes[i] = (uint8_t)(i / num_axes < sections[a] ? a : 0);
+        ++count[axes[i]];
+    }
+    for (int a = 0; a < num_axes; ++a)
+        if (count[a] != sections[a])
+            return fail(SK_ERR_INVALID, "sk_rope_axes: %d pairs cannot go round %d axes with %d for axis %d (the first "
+                        "axis takes what is left, so it has at least as many as the others)", half, num_axes,
+                        sections[a], a);
+    return SK_OK;
+}
+
+int sk_rope_axes_and_cache(const void *q, const void *key, const void *value, int64_t q_stride, int64_t key_stride,
+                           int64_t value_stride, const int64_t *positions, int64_t positions_stride, int num_axes,
+                           const double *freqs, const uint8_t *axes, int rot_dim, int interleaved, float attn_factor,
+                           const int64_t *slot_mapping, int num_tokens, int num_q_heads, int num_kv_heads,
+                           int head_dim, void *q_out, void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                           int num_blocks, int page_size, float *acc_pages, int32_t *pos_pages, void *stream)
+{
+    if (num_axes < 1 || num_axes > SK_MAX_AXES)
+        return fail(SK_ERR_INVALID, "sk_rope_axes_and_cache: num_axes=%d (1 to %d)", num_axes, SK_MAX_AXES);
+    if (positions_stride < num_tokens && num_axes > 1)
+        return fail(SK_ERR_INVALID, "sk_rope_axes_and_cache: positions_stride=%lld below num_tokens=%d",
+                    (long long)positions_stride, num_tokens);
+    if (axes == nullptr)
+        return fail(SK_ERR_INVALID, "sk_rope_axes_and_cache: null pointer argument");
+    return rope_call("sk_rope_axes_and_cache", q, key, value, q_stride, key_stride, value_stride, positions,
+                     positions_stride, num_axes, axes, freqs, rot_dim, interleaved, attn_factor, slot_mapping,
+                     num_tokens, num_q_heads, num_kv_heads, head_dim, q_out, kv_pages, kv_dtype, k_scale, v_scale,
+                     num_blocks, page_size, acc_pages, pos_pages, stream);
 }
 
 int sk_evict_capacity(int budget, int max_seq_len)
@@ -682,45 +751,47 @@ int64_t sk_prefill_workspace_bytes(int num_tokens, int num_q_heads, int kv_dtype
     return rc != SK_OK ? rc : prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
 }
 
-int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
-                          const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
-                          const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
-                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int max_seq_len,
-                          void *workspace, int64_t workspace_bytes, void *out, float *lse, void *stream)
+// Attention of new tokens over the pages: the whole cache (window 0), or the last `window` rows and the first `sinks`.
+static int chunk_call(const char *name, const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                      const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                      int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int window,
+                      int sinks, int max_seq_len, void *workspace, int64_t workspace_bytes, void *out, float *lse,
+                      void *stream)
 {
     if (kv_pages == nullptr || block_table == nullptr || seq_lens == nullptr || cu_seqlens_q == nullptr ||
         (num_tokens != 0 && (q == nullptr || out == nullptr)))       // arrays of no tokens may have no address
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: null pointer argument");
+        return fail(SK_ERR_INVALID, "%s: null pointer argument", name);
     if (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: kv_dtype=%d", kv_dtype);
+        return fail(SK_ERR_INVALID, "%s: kv_dtype=%d", name, kv_dtype);
     if (head_dim != kHeadDim)
-        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: head_dim=%d (only 128)", head_dim);
+        return fail(SK_ERR_UNSUPPORTED, "%s: head_dim=%d (only 128)", name, head_dim);
     if (page_size != kPage)
-        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: page_size=%d (only 16)", page_size);
+        return fail(SK_ERR_UNSUPPORTED, "%s: page_size=%d (only 16)", name, page_size);
     if (bs < 1 || bs > 32767)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: bs=%d outside [1, 32767]", bs);
+        return fail(SK_ERR_INVALID, "%s: bs=%d outside [1, 32767]", name, bs);
     if (num_tokens < 0 || max_q_len < 0 || (num_tokens > 0 && max_q_len < 1) || block_table_stride < 1 ||
         num_blocks < 1)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: num_tokens=%d max_q_len=%d stride=%d num_blocks=%d",
+        return fail(SK_ERR_INVALID, "%s: num_tokens=%d max_q_len=%d stride=%d num_blocks=%d", name,
                     num_tokens, max_q_len, block_table_stride, num_blocks);
     if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: %d query heads, %d kv heads", num_q_heads, num_kv_heads);
+        return fail(SK_ERR_INVALID, "%s: %d query heads, %d kv heads", name, num_q_heads, num_kv_heads);
     if (max_seq_len < 0)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: max_seq_len=%d", max_seq_len);
+        return fail(SK_ERR_INVALID, "%s: max_seq_len=%d", name, max_seq_len);
     if (!(sm_scale > 0.f && sm_scale < INFINITY) ||
         (kv_dtype == SK_KV_FP8_E4M3 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY)))
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: scales must be positive and finite");
+        return fail(SK_ERR_INVALID, "%s: scales must be positive and finite", name);
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(kv_pages) | reinterpret_cast<uintptr_t>(out) |
          reinterpret_cast<uintptr_t>(workspace)) & 15)
-        return fail(SK_ERR_INVALID, "sk_paged_prefill_attn: q, kv_pages, out and workspace must be 16-byte aligned");
+        return fail(SK_ERR_INVALID, "%s: q, kv_pages, out and workspace must be 16-byte aligned", name);
     const int G = num_q_heads / num_kv_heads;
     if ((long long)num_q_heads * max_q_len > 0x3FFFFFFFLL || (long long)num_q_heads * num_tokens > 0x7FFFFFFFLL ||
         (long long)num_blocks * num_kv_heads * 2 > 0x7FFFFFFFLL)
-        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: %d blocks of %d heads or %d query tokens of %d heads "
-                    "exceed the kernel's limits (2^30)", num_blocks, num_kv_heads, max_q_len, num_q_heads);
+        return fail(SK_ERR_UNSUPPORTED, "%s: %d blocks of %d heads or %d query tokens of %d heads "
+                    "exceed the kernel's limits (2^30)", name, num_blocks, num_kv_heads, max_q_len, num_q_heads);
     if (block_table_stride > kMaxStride || (long long)bs * num_kv_heads > kMaxPairs)
-        return fail(SK_ERR_UNSUPPORTED, "sk_paged_prefill_attn: %d blocks a sequence (at most 2^26), %d sequences of %d "
-                    "heads (2^24)", block_table_stride, bs, num_kv_heads);
+        return fail(SK_ERR_UNSUPPORTED, "%s: %d blocks a sequence (at most 2^26), %d sequences of %d "
+                    "heads (2^24)", name, block_table_stride, bs, num_kv_heads);
     if (num_tokens == 0)
         return SK_OK;
     int *status = nullptr;
@@ -732,7 +803,7 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
         return rc;
     const int64_t need = prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
     if (workspace == nullptr || workspace_bytes < need)
-        return fail(SK_ERR_CAPACITY, "sk_paged_prefill_attn: workspace of %lld bytes, %lld needed",
+        return fail(SK_ERR_CAPACITY, "%s: workspace of %lld bytes, %lld needed", name,
                     (long long)workspace_bytes, (long long)need);
     PrefillParams p{};
     p.q = static_cast<const uint16_t *>(q);
@@ -752,6 +823,9 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
     p.H_kv = num_kv_heads;
     p.G = G;
     p.causal = causal ? 1 : 0;
+    constexpr int kAll = kMaxStride * kPage;         // rows of a sequence at most
+    p.window = window < kAll ? window : kAll;
+    p.sinks = sinks < kAll ? sinks : kAll;
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
     p.score_scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
     p.v_scale = fp8 ? v_scale : 1.f;
@@ -760,6 +834,41 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
     if (e != cudaSuccess)
         return cuda_fail(e, "chunk attention kernel launch");
     return SK_OK;
+}
+
+int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                          const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                          const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                          int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int causal, int max_seq_len,
+                          void *workspace, int64_t workspace_bytes, void *out, float *lse, void *stream)
+{
+    return chunk_call("sk_paged_prefill_attn", q, kv_pages, kv_dtype, k_scale, v_scale, block_table,
+                      block_table_stride, num_blocks, page_size, seq_lens, cu_seqlens_q, bs, num_tokens, max_q_len,
+                      num_q_heads, num_kv_heads, head_dim, sm_scale, causal, 0, 0, max_seq_len, workspace,
+                      workspace_bytes, out, lse, stream);
+}
+
+int64_t sk_window_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int max_q_len, int kv_dtype)
+{
+    if (num_tokens < 0 || max_q_len < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 ||
+        (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3))
+        return fail(SK_ERR_INVALID, "sk_window_workspace_bytes: num_tokens=%d num_q_heads=%d num_kv_heads=%d max_q_len=%d "
+                    "kv_dtype=%d", num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype);
+    return sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype);
+}
+
+int sk_paged_window_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,
+                         const int32_t *block_table, int block_table_stride, int num_blocks, int page_size,
+                         const int32_t *seq_lens, const int32_t *cu_seqlens_q, int bs, int num_tokens, int max_q_len,
+                         int num_q_heads, int num_kv_heads, int head_dim, float sm_scale, int window, int sinks,
+                         int max_seq_len, void *workspace, int64_t workspace_bytes, void *out, float *lse, void *stream)
+{
+    if (window < 1 || sinks < 0)
+        return fail(SK_ERR_INVALID, "sk_paged_window_attn: window=%d (at least 1), sinks=%d (at least 0)", window, sinks);
+    return chunk_call("sk_paged_window_attn", q, kv_pages, kv_dtype, k_scale, v_scale, block_table,
+                      block_table_stride, num_blocks, page_size, seq_lens, cu_seqlens_q, bs, num_tokens, max_q_len,
+                      num_q_heads, num_kv_heads, head_dim, sm_scale, 1, window, sinks, max_seq_len, workspace,
+                      workspace_bytes, out, lse, stream);
 }
 
 int64_t sk_accum_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int max_q_len, int kv_dtype)

@@ -11,7 +11,7 @@ struct PrefillPiece {
     int s, h, unit, L, q_len, tok0;
     int t, a, b;
     int nA, nB;                  // tiles of [a, b) that row tiles A and B need
-    int pad;
+    int gap;                     // window: pages between the sinks and the window, which no tile holds
 };
 
 // Attention of a chunk of new tokens, resolved on the host.
@@ -31,6 +31,8 @@ struct PrefillParams {
     int gb, tpb, nsub;           // heads and tokens of a row tile, row tiles per token (set by the launcher)
     int deal;                    // whole units are dealt to the CTAs first (set by the launcher)
     int causal;
+    int window, sinks;           // window > 0: a token sees its last `window` rows and the first `sinks` ones (causal)
+    int sink_pages;              // (set by the launcher)
     float score_scale_log2;      // sm_scale * k_scale * log2(e)
     float v_scale;
     long long wait_limit;
@@ -72,8 +74,8 @@ cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16
                               long long k_stride, long long v_stride, const int64_t *pos, const double *freqs,
                               const int64_t *slots, int num_tokens, int hq, int hkv, int rot, int interleaved,
                               float factor, uint16_t *q_out, void *pages, int kv_dtype, float k_scale, float v_scale,
-                              long long num_blocks, float *acc, int32_t *pos_pages, int *status, int num_sms,
-                              cudaStream_t stream);
+                              long long num_blocks, float *acc, int32_t *pos_pages, const uint8_t *axes,
+                              long long pos_stride, int num_axes, int *status, int num_sms, cudaStream_t stream);
 cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int32_t *block_table, int bt_stride,
                                 int num_blocks, const int32_t *seq_lens, const int32_t *next_pos, int bs, int hkv,
                                 int budget, int recent, int max_len, int cap, int32_t *src, int32_t *dst,
