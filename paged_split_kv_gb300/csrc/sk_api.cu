@@ -801,36 +801,49 @@ static int chunk_call(const char *name, const void *q, const void *kv_pages, int
         rc = sm_count(&sms);
     if (rc != SK_OK)
         return rc;
-    const int64_t need = prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
+    const bool step = window > 0 && window_step_takes((long long)G * max_q_len);
+    const int64_t need = step ? window_step_workspace_bytes(G * max_q_len, sms)
+                              : prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
     if (workspace == nullptr || workspace_bytes < need)
         return fail(SK_ERR_CAPACITY, "%s: workspace of %lld bytes, %lld needed", name,
                     (long long)workspace_bytes, (long long)need);
-    PrefillParams p{};
-    p.q = static_cast<const uint16_t *>(q);
-    p.kv = kv_pages;
-    p.block_table = block_table;
-    p.seq_lens = seq_lens;
-    p.cu_q = cu_seqlens_q;
-    p.out = static_cast<uint16_t *>(out);
-    p.lse = lse;
-    p.status = status;
-    p.num_blocks = num_blocks;
-    p.bt_stride = block_table_stride;
-    p.bs = bs;
-    p.num_tokens = num_tokens;
-    p.max_q_len = max_q_len;
-    p.H_q = num_q_heads;
-    p.H_kv = num_kv_heads;
-    p.G = G;
-    p.causal = causal ? 1 : 0;
-    constexpr int kAll = kMaxStride * kPage;         // rows of a sequence at most
-    p.window = window < kAll ? window : kAll;
-    p.sinks = sinks < kAll ? sinks : kAll;
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
-    p.score_scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
-    p.v_scale = fp8 ? v_scale : 1.f;
-    p.wait_limit = wait_limit();
-    cudaError_t e = launch_prefill(p, kv_dtype, max_seq_len, workspace, sms, static_cast<cudaStream_t>(stream));
+    constexpr int kAll = kMaxStride * kPage;         // rows of a sequence at most
+    auto fill = [&](auto &p) {
+        p.q = static_cast<const uint16_t *>(q);
+        p.kv = kv_pages;
+        p.block_table = block_table;
+        p.seq_lens = seq_lens;
+        p.cu_q = cu_seqlens_q;
+        p.out = static_cast<uint16_t *>(out);
+        p.lse = lse;
+        p.status = status;
+        p.num_blocks = num_blocks;
+        p.bt_stride = block_table_stride;
+        p.bs = bs;
+        p.num_tokens = num_tokens;
+        p.max_q_len = max_q_len;
+        p.H_q = num_q_heads;
+        p.H_kv = num_kv_heads;
+        p.G = G;
+        p.window = window < kAll ? window : kAll;
+        p.sinks = sinks < kAll ? sinks : kAll;
+        p.score_scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
+        p.v_scale = fp8 ? v_scale : 1.f;
+        p.wait_limit = wait_limit();
+    };
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (step) {
+        WindowParams p{};
+        fill(p);
+        e = launch_window_step(p, kv_dtype, max_seq_len, workspace, sms, st);
+    } else {
+        PrefillParams p{};
+        fill(p);
+        p.causal = causal ? 1 : 0;
+        e = launch_prefill(p, kv_dtype, max_seq_len, workspace, sms, st);
+    }
     if (e != cudaSuccess)
         return cuda_fail(e, "chunk attention kernel launch");
     return SK_OK;
@@ -854,7 +867,12 @@ int64_t sk_window_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_he
         (kv_dtype != SK_KV_BF16 && kv_dtype != SK_KV_FP8_E4M3))
         return fail(SK_ERR_INVALID, "sk_window_workspace_bytes: num_tokens=%d num_q_heads=%d num_kv_heads=%d max_q_len=%d "
                     "kv_dtype=%d", num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype);
-    return sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype);
+    const long long rows = (long long)max_q_len * (num_q_heads / num_kv_heads);
+    if (!window_step_takes(rows))
+        return sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype);
+    int sms = 0;
+    const int rc = sm_count(&sms);
+    return rc != SK_OK ? rc : window_step_workspace_bytes((int)rows, sms);
 }
 
 int sk_paged_window_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,

@@ -41,6 +41,38 @@ long long prefill_workspace_bytes(int num_tokens, int H_q, int kv_dtype, int num
 cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,
                            cudaStream_t stream);
 
+// Windowed attention of a step: a piece of a (sequence, KV head), key tiles [a, b) of its t.
+struct WindowPiece {
+    int s, h, L, q_len, tok0;
+    int t, a, b;
+    int gap;                     // pages between the sinks and the window
+    int pad[3];
+};
+
+// Windowed attention of a step (up to 64 rows a sequence and KV head), resolved on the host.
+struct WindowParams {
+    const uint16_t *q;           // bf16 bits [NT, H_q, D]
+    const void *kv;              // pages
+    const int32_t *block_table, *seq_lens, *cu_q;
+    uint16_t *out;               // bf16 bits [NT, H_q, D]
+    float *lse;                  // [NT, H_q] or NULL
+    float *part_o, *part_m, *part_l;   // partial states of the pieces (set by the launcher) ...
+    WindowPiece *shared;         // ... and what they are pieces of, two per run
+    int *status;
+    int64_t num_blocks;
+    int bt_stride, bs, num_tokens, max_q_len;
+    int H_q, H_kv, G;
+    int window, sinks;
+    int rows, sink_pages;        // rows of a partial state (set by the launcher)
+    float score_scale_log2;      // sm_scale * k_scale * log2(e)
+    float v_scale;
+    long long wait_limit;
+};
+bool window_step_takes(long long rows);
+long long window_step_workspace_bytes(int rows, int num_sms);
+cudaError_t launch_window_step(const WindowParams &p, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,
+                               cudaStream_t stream);
+
 // A run's part of a unit that others share: the keys from tile a on of a sequence and head, and whether it has the unit's
 // last rows.
 struct AccumPiece {
