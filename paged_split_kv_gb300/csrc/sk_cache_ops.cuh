@@ -64,6 +64,8 @@ struct WindowParams {
     int H_q, H_kv, G;
     int window, sinks;
     int rows, sink_pages;        // rows of a partial state (set by the launcher)
+    int inv_G;                   // 2^16 / G, rounded up (set by the launcher)
+    int small;                   // the runs are found by a warp (set by the launcher)
     float score_scale_log2;      // sm_scale * k_scale * log2(e)
     float v_scale;
     long long wait_limit;

@@ -14,21 +14,22 @@
 //     S^T[128 keys x R] = K Q^T,   O^T[128 dimensions x R] += V^T P^T
 //
 // Roles (384 threads; 512 for e4m3 pages):
-//   warp 0      copies: one TMA copy per page (8 KB, e4m3 4 KB) into 128-byte-swizzled atoms that are the operands K and V^T
+//   warp 0      walks the run, publishes its pieces to the others and copies their pages: one TMA copy per page (8 KB, e4m3
+//               4 KB) into 128-byte-swizzled atoms that are the operands K and V^T
 //   warp 1      issues QK (and allocates TMEM), warp 2 PV
-//   warp 3      walks the run, publishes its pieces to the others and writes their Q (e4m3: as two terms, see below)
+//   warp 3      bf16: copies Q
 //   warps 4-7, 8-11  softmax of the even and of the odd key tiles, each group with its own O, reference and sums: a group
 //               has the time of two tiles for one, and the groups meet only at a unit's end, where their states are joined.
 //               A thread is a key (its TMEM lane).  A row's reference is its largest score of the group's first tile;
 //               it moves only when a later score beats it by far, on which the group's threads vote once per tile.
 //               P^T goes over the tile's own K, which QK no longer needs.
-//   warps 12-15 (e4m3)  V's codes to f16 (exactly): PV runs on f16 with P as f16
-// e4m3 pages: QK runs on the codes, with Q as two e4m3 terms and a power-of-two scale per row, side by side as 2 R columns
-// of one product; the softmax adds the two.
+//   warps 12-15 (e4m3)  Q as two e4m3 terms, and V's codes to f16 (exactly): PV runs on f16 with P as f16
+// e4m3 pages: QK runs on the codes, with Q as two e4m3 terms and a power-of-two scale per row, two products into one S.
 //
 // Every wait is bounded; on expiry SK_DEV_TIMEOUT is set and every role gives up, after its copies and products in flight.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -46,18 +47,15 @@ constexpr int kKeys = 128;                           // keys of a tile (MMA M)
 constexpr int kPagesPerTile = kKeys / kPage;
 constexpr long long kDrainLimit = 4000000000LL;      // cycles (~2 s): waits for work already issued
 constexpr int kMaxSmem = 232448;
-constexpr int kRing = 4;                             // pieces published ahead
+constexpr int kRing = 8;                             // pieces published ahead
 constexpr int kUnitFixed = 1;                        // cost of starting and finishing a unit, in key tiles
-// What a row without a reference subtracts from its scores: negated here, so that any score exceeds the threshold.
-constexpr float kNoRef = 0x1p100f;
-
 template <int RP, bool FP8>
 struct WCfg {
     static_assert(RP == 16 || RP == 32 || RP == 64, "rows: 16, 32 or 64");
     static constexpr int kThreads = FP8 ? 512 : 384;
     // registers per thread after the reallocation; no more in all than at launch (4 x 128, or 3 x 168)
     static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-    static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoftmax = FP8 ? 200 : 216, kRegsConvert = 48;
+    static constexpr int kRegsIssue = FP8 ? 56 : 72, kRegsSoftmax = FP8 ? 200 : 216, kRegsConvert = 56;
     static_assert(kRegsIssue + 2 * kRegsSoftmax + (FP8 ? kRegsConvert : 0) <= kThreads / 128 * kRegsLaunch, "registers");
     static constexpr int kGroupBytes = FP8 ? 2048 : 4096;          // 8 tokens as copied: 128-byte chunks of K, then of V
     static constexpr int kPageBytes = 2 * kGroupBytes;
@@ -72,9 +70,8 @@ struct WCfg {
     static constexpr int kOffMisc = kOffQ + 2 * kQBytes;
     static constexpr int kSmemBytes = kOffMisc + kMisc;
     // TMEM columns: S buffers (even and odd tiles in turn), then O of the even and of the odd tiles
-    static constexpr int kSCols = FP8 ? 2 * RP : RP;
-    static constexpr int kSBufs = FP8 && RP == 64 ? 2 : 4;
-    static constexpr int kColO = kSBufs * kSCols;
+    static constexpr int kSBufs = 4;
+    static constexpr int kColO = kSBufs * RP;
     static constexpr int kTmemNeed = kColO + 2 * RP;
     static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
     static_assert(kTmemNeed <= 512, "TMEM columns");
@@ -102,12 +99,12 @@ struct WCfg {
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kFound = (kAbort + 4 + 7) / 8 * 8;        // where the run starts
     static constexpr int kPieces = (kFound + 16 + 15) / 16 * 16;   // WindowPiece[kRing]
-    static constexpr int kRef = kPieces + 48 * kRing;              // float[2][RP] reference of a group's rows (log2), or -inf
-    static constexpr int kNeg = kRef + 8 * RP;                     // float[2][RP] minus that, or kNoRef
-    static constexpr int kAlpha = kNeg + 8 * RP;                   // float[2][RP]; float2[2][RP / 2] at a unit's end
+    static constexpr int kNeg = kPieces + 48 * kRing;              // float[2][RP] minus the reference of a group's rows (log2)
+    static constexpr int kDelta = kNeg + 8 * RP;                   // float[2][RP] what it changes by
+    static constexpr int kAlpha = kDelta + 8 * RP;                 // float[2][RP] 2^delta; float2[2][RP / 2] at a unit's end
     static constexpr int kScale = kAlpha + 8 * RP;                 // float[2][RP] e4m3: score scale of a Q buffer's rows
     static_assert(kScale + (FP8 ? 8 * RP : 0) <= kMisc, "misc area");
-    static constexpr int kReaders = FP8 ? 15 : 11;                 // warps that read the pieces
+    static constexpr int kReaders = FP8 ? 14 : 11;                 // warps that read the pieces
     static_assert(kStages >= 3 && kSmemBytes <= kMaxSmem && kOffQ % 1024 == 0, "shared memory");
 };
 
@@ -158,6 +155,108 @@ __device__ __forceinline__ void reduce_step(float *v, int lane)
     }
 }
 
+// Half a warp's row of Q (8 bf16 elements a lane) as two e4m3 terms of q * 2^e = hi + lo, the row's largest |q| * 2^e in
+// [128, 256); returns e.  A bf16 element of at least 2^-9 of the largest is hi + lo exactly.
+__device__ __forceinline__ int split_q_half_row(uint4 raw, uint2 &hi, uint2 &lo)
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float q[8], amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        q[2 * k] = __uint_as_float(w[k] << 16);
+        q[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        amax = fmax3(amax, fabsf(q[2 * k]), fabsf(q[2 * k + 1]));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+    // amax in [2^(ex - 127), 2^(ex - 126)); none for a row of zeros, and for infinities, which saturate
+    const int ex = __float_as_int(amax) >> 23;
+    const int e = amax == 0.f || ex == 255 ? 0 : max(-100, min(100, 134 - ex));
+    const float by = __int_as_float((127 + e) << 23);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float x0 = q[2 * k] * by, x1 = q[2 * k + 1] * by;
+        uint16_t hc, lc;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hc) : "f"(x1), "f"(x0));
+        float h0, h1;
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(h0), "=f"(h1)
+            : "r"(f16x2_of_e4m3(hc)));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lc) : "f"(x1 - h1), "f"(x0 - h0));
+        h[k] = hc;
+        l[k] = lc;
+    }
+    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+    return e;
+}
+
+// min(a / b, most) for a >= 0 and 0 < b < 2^24 (a division of 64 bits takes a thousand cycles).
+__device__ __forceinline__ int quotient(long long a, int b, int most)
+{
+    if (a >= (long long)b * most)
+        return most;
+    int x = (int)__fdividef((float)a, (float)b);     // within 2^-22 of the quotient, which is below 2^24
+    while ((long long)x * b > a)
+        --x;
+    while ((long long)(x + 1) * b <= a)
+        ++x;
+    return x;
+}
+
+// Row r of a unit among the rows of q: the token's, times H_q, and the head.
+__device__ __forceinline__ long long unit_row(const WindowParams &p, const Piece &pc, int r)
+{
+    const int j = r * p.inv_G >> 16;                 // r / G
+    return (long long)(pc.tok0 + j) * p.H_q + pc.h * p.G + (r - j * p.G);
+}
+
+// The run of CTA `index` of `count` for a batch of at most 32 * kSmall sequences and a cost below 2^31; called by a warp.
+constexpr int kSmall = 4;
+
+__device__ __forceinline__ Run small_run(const WindowParams &p, int index, int count)
+{
+    const int lane = threadIdx.x & 31;
+    auto cost = [&](int s0) {                        // of sequence s0 + lane
+        const Seq q = sequence(p, min(s0 + lane, p.bs - 1));
+        return s0 + lane < p.bs && q.q_len > 0 ? p.H_kv * (q.t + kUnitFixed) : 0;
+    };
+    int mine = cost(0), total = __reduce_add_sync(kFull, mine);
+#pragma unroll 1
+    for (int s0 = 32; s0 < p.bs; s0 += 32)
+        total += __reduce_add_sync(kFull, cost(s0));
+    Run r;
+    const int each = (total + count - 1) / count;
+    r.lo = min((long long)total, (long long)each * index);
+    r.hi = min((long long)total, (long long)each * (index + 1));
+    r.before = 0;
+    r.s = p.bs;
+    if (r.lo >= r.hi)
+        return r;
+    int before = 0, s0 = 0;
+#pragma unroll 1
+    while (true) {                                   // the sequence that lo lies in
+        const int here = __reduce_add_sync(kFull, mine);
+        if (r.lo < before + here)
+            break;
+        before += here;
+        s0 += 32;
+        mine = cost(s0);
+    }
+    int incl = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, incl, o);
+        incl += lane >= o ? x : 0;
+    }
+    const int src = __ffs(__ballot_sync(kFull, r.lo < before + incl)) - 1;
+    r.s = s0 + src;
+    r.before = before + __shfl_sync(kFull, incl - mine, src);
+    return r;
+}
+
 template <int RP, bool FP8>
 __global__ void __launch_bounds__(WCfg<RP, FP8>::kThreads, 1)
 window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParams p)
@@ -183,7 +282,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             mbar_init(bar(C::kBarSFree, i), 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(C::kBarQ, i), 1);
+            mbar_init(bar(C::kBarQ, i), FP8 ? 4 : 1);
             mbar_init(bar(C::kBarQFree, i), 1 + 8);
             mbar_init(bar(C::kBarV, i), 4);
             mbar_init(bar(C::kBarVFree, i), 1);
@@ -205,8 +304,10 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
     wait_prior_grid();
     if (blockIdx.x == 0 && threadIdx.x == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_q + p.bs) != p.num_tokens))
         atomicOr(p.status, SK_DEV_BAD_SEQ);
-    // found in the stages' memory, before the first copy
-    Run run = find_run<C::kThreads>(p.bs, blockIdx.x, gridDim.x, 0, 0, reinterpret_cast<long long *>(smem),
+    // A large batch's runs are found by the whole CTA, in the stages' memory, before the first copy; else warp 0 finds its own.
+    Run run{0, 0, 0, p.bs};
+    if (!p.small)
+        run = find_run<C::kThreads>(p.bs, blockIdx.x, gridDim.x, 0, 0, reinterpret_cast<long long *>(smem),
                                     reinterpret_cast<long long *>(misc + C::kFound), [&](int s) {
                                         const Seq q = sequence(p, s);
                                         return q.q_len > 0 ? (long long)p.H_kv * (q.t + kUnitFixed) : 0LL;
@@ -216,11 +317,9 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc + C::kTmemSlot);
-    if ((sbase & 1023u) != 0) {
-        if (threadIdx.x == 0)
-            atomicOr(p.status, SK_DEV_INTERNAL);
-        run.s = p.bs;                                // nothing is done
-    }
+    const bool aligned = (sbase & 1023u) == 0;
+    if (!aligned && threadIdx.x == 0)
+        atomicOr(p.status, SK_DEV_INTERNAL);
     auto wait = [&](uint32_t b, uint32_t parity) {
         return __all_sync(kFull, wait_bar(b, parity, abort_flag, p.wait_limit)) != 0;
     };
@@ -249,75 +348,38 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
     if (warp < 4) {
         reg_dec<C::kRegsIssue>();
         if (warp == 0) {
-            // ============================================================ pages
+            // ============================================================ the pieces and their pages
             if (lane == 0)
                 prefetch_tensormap(&kv_map);
-            int u = 0;                               // tiles so far
-            while (ok && next_piece(pc, ok)) {
-                const int page_end = (pc.L + kPage - 1) / kPage;
-                const int32_t *bt = p.block_table + (long long)pc.s * p.bt_stride;
-                auto page_at = [&](int t) {
-                    const int pg = t * kPagesPerTile + lane;
-                    return pg >= p.sink_pages ? pg + pc.gap : pg;
-                };
-                auto block_at = [&](int t) {
-                    const int pg = page_at(t);
-                    return lane < kPagesPerTile && t < pc.b && pg < page_end ? __ldg(bt + pg) : -1;
-                };
-                int blk = block_at(pc.a), blk1 = block_at(pc.a + 1);
-                for (int t = pc.a; t < pc.b; ++t, ++u) {
-                    const int blk2 = block_at(t + 2);
-                    const int i = u % C::kStages;
-                    if (u >= C::kStages)
-                        ok = wait(bar(C::kBarEmpty, i), (u / C::kStages - 1) & 1);
-                    if (!ok)
-                        break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(bar(C::kBarFull, i), C::kStageBytes);
-                    __syncwarp();
-                    if (lane < kPagesPerTile) {
-                        int grp = -2;                // whole box out of bounds: zero fill
-                        if (page_at(t) < page_end) {
-                            if (blk >= 0 && blk < p.num_blocks)
-                                grp = (blk * p.H_kv + pc.h) * 2;
-                            else
-                                atomicOr(p.status, SK_DEV_BAD_BLOCK);
-                        }
-                        tma_load_4d(sbase + i * C::kStageBytes + lane * C::kPageBytes, &kv_map, 0, 0, 0, grp,
-                                    bar(C::kBarFull, i));
-                    }
-                    blk = blk1;
-                    blk1 = blk2;
-                }
-            }
-            if (!ok)
-                give_up();
-            // every copy issued lands before the CTA exits
-            for (int t = u > C::kStages ? u - C::kStages : 0; t < u; ++t)
-                wait_bar(bar(C::kBarFull, t % C::kStages), (t / C::kStages) & 1, nullptr, kDrainLimit);
-        } else if (warp == 3) {
-            // ============================================================ the pieces, and their Q
+            if (p.small)
+                run = small_run(p, blockIdx.x, gridDim.x);
+            if (!aligned)
+                run.s = p.bs;                            // nothing is done
             Piece *shared = p.shared + 2 * blockIdx.x;   // this run's pieces of units that others have a part of
             if (lane < 2)
                 shared[lane].s = -1;
             __syncwarp();
-            int s = run.s, h = -1, copied = 0;
+            Seq q;
+            int s = run.s, h = -1, count = 0;
             long long off = run.before;                  // where sequence s starts
-            bool more = true;
-            for (int k = 0; more; ++k) {
-                more = false;
+            // The next piece, published; its s is -1 at the run's end (and after a wait that gave up).
+            auto next = [&]() {
+                bool more = false;
                 while (s < p.bs && off < run.hi) {
-                    const Seq q = sequence(p, s);
-                    const long long unit = q.t + kUnitFixed;
-                    if (h < 0)
-                        h = run.lo > off ? (int)min((run.lo - off) / unit, (long long)p.H_kv) : 0;
+                    if (h < 0) {
+                        q = sequence(p, s);
+                        h = 0;
+                        if (q.q_len > 0 && run.lo > off)     // the head that the run starts in
+                            h = quotient(run.lo - off, q.t + kUnitFixed, p.H_kv);
+                    }
+                    const int unit = q.t + kUnitFixed;
                     if (q.q_len == 0 || h >= p.H_kv) {
-                        off += q.q_len > 0 ? unit * p.H_kv : 0;
+                        off += q.q_len > 0 ? (long long)unit * p.H_kv : 0;
                         ++s;
                         h = -1;
                         continue;
                     }
-                    const long long start = off + h * unit;
+                    const long long start = off + (long long)h * unit;
                     if (start >= run.hi)
                         break;
                     // tile i stands at start + kUnitFixed + i
@@ -338,18 +400,85 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 }
                 if (!more)
                     pc.s = -1;
-                if (k >= kRing)
-                    ok = wait(bar(C::kBarPieceFree, k % kRing), (k / kRing - 1) & 1);
-                if (!ok)
-                    break;
+                const int i = count % kRing;
+                if (count >= kRing)
+                    ok = wait(bar(C::kBarPieceFree, i), (count / kRing - 1) & 1);
+                if (!ok) {
+                    pc.s = -1;
+                    return;
+                }
+                ++count;
                 if (lane == 0) {
-                    ring[k % kRing] = pc;
+                    ring[i] = pc;
                     if (more && pc.b - pc.a < pc.t)
                         shared[pc.a > 0 ? 0 : 1] = pc;
-                    mbar_arrive(bar(C::kBarPiece, k % kRing));
+                    mbar_arrive(bar(C::kBarPiece, i));
                 }
                 __syncwarp();
-                if (!more || pc.a == pc.b)
+            };
+            // Block ids of four tiles of a piece, from tile t on, one page a lane.  (A tile's eight at a time, two tiles ahead,
+            // each copy waited a thousand cycles for the register moves of the ids read last.)
+            auto page_of = [&](const Piece &x, int v) { return v >= p.sink_pages ? v + x.gap : v; };
+            auto blocks_at = [&](const Piece &x, int t) {
+                const int v = t * kPagesPerTile + lane, pg = page_of(x, v);
+                return v < x.b * kPagesPerTile && pg * kPage < x.L
+                           ? __ldg(p.block_table + (long long)x.s * p.bt_stride + pg) : -1;
+            };
+            next();
+            int u = 0;                                   // tiles so far
+            int blocks = pc.s >= 0 ? blocks_at(pc, pc.a) : -1;
+            while (ok && pc.s >= 0) {
+                // the piece after this one is found, and its first blocks are read, once the first copies are out
+                const Piece now = pc;
+                const int turn = min(now.b, now.a + C::kStages);
+                int after = -1, more = blocks_at(now, now.a + 4);
+                for (int t = now.a; t <= now.b; ++t) {
+                    if (t == turn) {
+                        next();
+                        if (pc.s >= 0)
+                            after = blocks_at(pc, pc.a);
+                    }
+                    if (t == now.b)
+                        break;
+                    const int k = (t - now.a) & 3;
+                    if (k == 0 && t > now.a) {
+                        blocks = more;
+                        more = blocks_at(now, t + 4);
+                    }
+                    const int blk = __shfl_sync(kFull, blocks, k * kPagesPerTile + (lane & (kPagesPerTile - 1)));
+                    const int i = u % C::kStages;
+                    if (u >= C::kStages && ok)
+                        ok = wait(bar(C::kBarEmpty, i), (u / C::kStages - 1) & 1);
+                    if (!ok)
+                        break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar(C::kBarFull, i), C::kStageBytes);
+                    __syncwarp();
+                    if (lane < kPagesPerTile) {
+                        int grp = -2;                    // whole box out of bounds: zero fill
+                        if (page_of(now, t * kPagesPerTile + lane) * kPage < now.L) {
+                            if (blk >= 0 && blk < p.num_blocks)
+                                grp = (blk * p.H_kv + now.h) * 2;
+                            else
+                                atomicOr(p.status, SK_DEV_BAD_BLOCK);
+                        }
+                        tma_load_4d(sbase + i * C::kStageBytes + lane * C::kPageBytes, &kv_map, 0, 0, 0, grp,
+                                    bar(C::kBarFull, i));
+                    }
+                    ++u;
+                }
+                blocks = after;
+            }
+            if (!ok)
+                give_up();
+            // every copy issued lands before the CTA exits
+            for (int t = u > C::kStages ? u - C::kStages : 0; t < u; ++t)
+                wait_bar(bar(C::kBarFull, t % C::kStages), (t / C::kStages) & 1, nullptr, kDrainLimit);
+        } else if (warp == 3) {
+            // ============================================================ bf16: Q, K-major with the 128-byte swizzle
+            int copied = 0;
+            while (!FP8 && ok && next_piece(pc, ok)) {
+                if (pc.a == pc.b)
                     continue;
                 const int buf = copied & 1;
                 if (copied >= 2)
@@ -357,53 +486,18 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 if (!ok)
                     break;
                 ++copied;
-                const int R = p.G * pc.q_len;
-                uint8_t *qs = smem + C::kOffQ + buf * C::kQBytes;
-                auto row_of = [&](int r) {               // row r of the unit
-                    const int j = r / p.G;
-                    return p.q + ((long long)(pc.tok0 + j) * p.H_q + pc.h * p.G + (r - j * p.G)) * kHeadDim;
-                };
-                if constexpr (!FP8) {
-                    // two rows a load, 16 bytes a lane, K-major with the 128-byte swizzle; zeros past the rows
-#pragma unroll 1
-                    for (int r0 = 0; r0 < RP; r0 += 16) {
-                        uint4 x[8];
-#pragma unroll
-                        for (int k2 = 0; k2 < 8; ++k2) {
-                            const int r = r0 + 2 * k2 + (lane >> 4);
-                            x[k2] = r < R ? __ldg(reinterpret_cast<const uint4 *>(row_of(r)) + (lane & 15))
-                                          : make_uint4(0u, 0u, 0u, 0u);
-                        }
-#pragma unroll
-                        for (int k2 = 0; k2 < 8; ++k2) {
-                            const int r = r0 + 2 * k2 + (lane >> 4), unit = lane & 15;
-                            *reinterpret_cast<uint4 *>(qs + (unit >> 3) * (RP * 128) + r * 128 +
-                                                       (((unit & 7) ^ (r & 7)) << 4)) = x[k2];
-                        }
-                    }
-                } else {
-                    float *scale = reinterpret_cast<float *>(misc + C::kScale) + buf * RP;
-#pragma unroll 1
-                    for (int r0 = 0; r0 < RP; r0 += 8) {
-                        uint2 x[8];
-#pragma unroll
-                        for (int k2 = 0; k2 < 8; ++k2)
-                            x[k2] = r0 + k2 < R ? __ldg(reinterpret_cast<const uint2 *>(row_of(r0 + k2)) + lane)
-                                                : make_uint2(0u, 0u);
-#pragma unroll
-                        for (int k2 = 0; k2 < 8; ++k2) {
-                            const int r = r0 + k2;
-                            uint32_t hi, lo;
-                            int e;
-                            split_q_row(x[k2], hi, lo, e);
-                            const uint32_t at = r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2));
-                            *reinterpret_cast<uint32_t *>(qs + at) = hi;
-                            *reinterpret_cast<uint32_t *>(qs + RP * 128 + at) = lo;
-                            if (lane == 0)
-                                scale[r] = p.score_scale_log2 * ldexpf(1.f, -e);
-                        }
-                    }
+                const int R = p.G * pc.q_len, unit = lane & 15;
+#pragma unroll 4
+                for (int r = lane >> 4; r < RP; r += 2) {      // two rows at a time, 16 bytes a lane; zeros past the rows
+                    const uint32_t dst = sbase + C::kOffQ + buf * C::kQBytes + (unit >> 3) * (RP * 128) + r * 128 +
+                                         (((unit & 7) ^ (r & 7)) << 4);
+                    const int rr = min(r, R - 1);
+                    const uint16_t *src = p.q + unit_row(p, pc, rr) * kHeadDim + unit * 8;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                                 "r"(r < R ? 16 : 0)
+                                 : "memory");
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -413,7 +507,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 give_up();
         } else if (warp == 1) {
             // ============================================================ S^T = K Q^T
-            constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(kKeys, C::kSCols, 0, 0) : idesc_bf16_f32(kKeys, RP, 0, 0);
+            constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(kKeys, RP, 0, 0) : idesc_bf16_f32(kKeys, RP, 0, 0);
             const uint64_t d_k = smem_desc_sw128(sbase, 16, C::kGroupBytes);
             const uint64_t d_q = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
             int u = 0, pieces = 0;
@@ -432,10 +526,11 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t sd = tmem + b * C::kSCols;
+                    const uint32_t sd = tmem + b * RP;
                     const uint64_t k0 = d_k + (uint64_t)(st * C::kStageBytes >> 4);
                     if constexpr (FP8) {
                         mma4_f8_ss<2, 2>(sd, k0, q0, idesc, 0);
+                        mma4_f8_ss<2, 2>(sd, k0, q0 + (RP * 128 >> 4), idesc, 1);
                     } else {
                         mma4_f16_ss<2, 2>(sd, k0, q0, idesc, 0);
                         mma4_f16_ss<2, 2>(sd, k0 + (1024 >> 4), q0 + (RP * 128 >> 4), idesc, 1);
@@ -501,8 +596,8 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
         const uint32_t lane_off = (uint32_t)(tw * 32) << 16;
         const uint32_t group_bar = 1 + g, both_bar = 3;
         constexpr int kLd = RP >= 32 ? 32 : RP;                    // TMEM columns per load
-        float *ref = reinterpret_cast<float *>(misc + C::kRef) + g * RP;
         float *neg = reinterpret_cast<float *>(misc + C::kNeg) + g * RP;
+        float *delta = reinterpret_cast<float *>(misc + C::kDelta) + g * RP;
         float *alpha = reinterpret_cast<float *>(misc + C::kAlpha) + g * RP;
         int u = 0, pieces = 0;
         bool failed = false;
@@ -527,6 +622,9 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
 #pragma unroll
             for (int r = 0; r < RP; ++r)
                 lsum[r] = 0.f;
+            bool open = true;                                      // some row has no reference yet
+            if (FP8 && n > 0 && !wait(bar(C::kBarQ, pieces & 1), (pieces >> 1) & 1))     // (the rows' scales)
+                failed = true;
             for (int j = (u ^ g) & 1; j < n; j += 2) {
                 const int v = u + j;                               // this tile's number
                 const int b = v % C::kSBufs, st = v % C::kStages;
@@ -538,35 +636,21 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 jmax = max(0, min(jmax, pc.q_len));
                 const int rmin = jmin * p.G, rmax = jmax * p.G;
                 float x[RP];
-                ok = wait(bar(C::kBarS, b), (v / C::kSBufs) & 1);
-                // scores of this key, -inf where a row does not see it (padding rows are 0)
-                auto load = [&]() {
+                ok = !failed && wait(bar(C::kBarS, b), (v / C::kSBufs) & 1);
+                // x = the key's scores (log2 units) less the rows' references; -inf where a row does not see it (padding rows
+                // are 0).  A row without a reference has 0 for one.
+                bool move = open;
+                if (ok) {
                     tc_fence_after();
-                    const uint32_t col = tmem + b * C::kSCols + lane_off;
 #pragma unroll
                     for (int c = 0; c < RP; c += kLd)
-                        tmem_ld32<kLd>(col + c, x + c);
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int c = 0; c < RP; c += kLd) {
-                            float y[kLd];
-                            tmem_ld32<kLd>(col + RP + c, y);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int r = 0; r < kLd; ++r)
-                                x[c + r] += y[r];
-                        }
-                    } else {
-                        tmem_wait_ld();
-                    }
+                        tmem_ld32<kLd>(tmem + b * RP + c + lane_off, x + c);
+                    tmem_wait_ld();
                     if (rmin > 0 || rmax < R) {
 #pragma unroll
                         for (int r = 0; r < RP; ++r)
                             x[r] = r >= rmin && r < rmax ? x[r] : -CUDART_INF_F;
                     }
-                };
-                // x * scale + neg, and the largest of them
-                auto shift = [&]() {
                     float top = -CUDART_INF_F;
 #pragma unroll
                     for (int r = 0; r < RP; r += 4) {
@@ -574,7 +658,9 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                                                 p.score_scale_log2);
                         if constexpr (FP8)
                             c4 = *reinterpret_cast<const float4 *>(scale + r);
-                        const float4 n4 = *reinterpret_cast<const float4 *>(neg + r);
+                        float4 n4 = *reinterpret_cast<const float4 *>(neg + r);
+                        if (j < 2)
+                            n4 = make_float4(0.f, 0.f, 0.f, 0.f);
                         const float2 a = ffma2(make_float2(x[r], x[r + 1]), make_float2(c4.x, c4.y), make_float2(n4.x, n4.y));
                         const float2 c = ffma2(make_float2(x[r + 2], x[r + 3]), make_float2(c4.z, c4.w),
                                                make_float2(n4.z, n4.w));
@@ -584,14 +670,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                         x[r + 3] = c.y;
                         top = fmaxf(fmax3(top, a.x, a.y), fmaxf(c.x, c.y));
                     }
-                    return top;
-                };
-                const bool first = j < 2;                          // the group's first tile of the piece
-                bool move = first;
-                if (ok) {
-                    load();
-                    if (!first)
-                        move = shift() > C::kMost;
+                    move = open || top > C::kMost;
                 }
                 // one vote per tile: does a reference move, or has a wait failed?  Only then a second one tells which.
                 if (named_bar_or(group_bar, 128, move || !ok)) {
@@ -599,49 +678,56 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                         failed = true;
                         break;
                     }
-                    if (!first)
-                        load();
                     // the tile's largest score of each row, by way of the tile's dead K
                     float *red = reinterpret_cast<float *>(smem + st * C::kStageBytes);
 #pragma unroll
-                    for (int c0 = 0; c0 < RP; c0 += kLd) {
-                        float y[kLd];
+                    for (int c0 = 0; c0 < RP; c0 += 32) {
+                        float mine = 0.f;
 #pragma unroll
-                        for (int r = 0; r < kLd; ++r)
-                            y[r] = x[c0 + r] * (FP8 ? scale[c0 + r] : p.score_scale_log2);
-                        reduce_step<kLd, 16, true>(y, lane);
-                        red[tw * RP + c0 + lane / (32 / kLd)] = y[0];
+                        for (int r = 0; r < (RP < 32 ? RP : 32); ++r) {
+                            float most;
+                            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(most) : "f"(x[c0 + r]));
+                            mine = lane == r ? most : mine;
+                        }
+                        if (RP >= 32 || lane < RP)
+                            red[tw * RP + c0 + lane] = mine;
                     }
                     named_bar_sync(group_bar, 128);
+                    bool none = false;
                     if (tau < RP) {
                         const float top = fmaxf(fmaxf(red[tau], red[RP + tau]), fmaxf(red[2 * RP + tau], red[3 * RP + tau]));
-                        const float old = first ? -CUDART_INF_F : ref[tau];
-                        const float now = fmaxf(old, top - C::kAbove);
-                        alpha[tau] = old == -CUDART_INF_F ? 0.f : exp2f(old - now);
-                        ref[tau] = now;
-                        neg[tau] = now == -CUDART_INF_F ? kNoRef : -now;
+                        const float old = j < 2 ? 0.f : neg[tau];
+                        const bool had = j >= 2 && alpha[tau] >= 0.f;      // a row's alpha is -1 until it has a reference
+                        // x is relative to the old reference: the new one stands kAbove below top, but no lower than the old
+                        float by = top - C::kAbove;
+                        by = had ? fmaxf(by, 0.f) : by;
+                        none = by == -CUDART_INF_F && tau < R;
+                        by = by == -CUDART_INF_F ? 0.f : by;
+                        delta[tau] = -by;
+                        neg[tau] = old - by;
+                        alpha[tau] = none || (!had && top == -CUDART_INF_F) ? -1.f : had ? ex2_ftz(-by) : 0.f;
                     }
-                    named_bar_sync(group_bar, 128);
-                    if (!first) {
+                    open = named_bar_or(group_bar, 128, none);
+                    if (j >= 2) {
 #pragma unroll
                         for (int r = 0; r < RP; ++r)
-                            lsum[r] *= alpha[r];
+                            lsum[r] *= fmaxf(alpha[r], 0.f);
                         // O holds the group's tiles before this one: its last product is complete once that tile's stage
                         // is free.  (The stage's next tile is past this one, so its phase cannot be over.)
                         const int prev = v - 2;
                         const bool done = wait(bar(C::kBarEmpty, prev % C::kStages), (prev / C::kStages) & 1);
                         if (done) {
                             tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < RP; c += kLd) {
-                                float o[kLd];
+#pragma unroll 1
+                            for (int c = 0; c < RP; c += 16) {
+                                float o[16];
                                 const uint32_t col = tmem + C::kColO + g * RP + c + lane_off;
-                                tmem_ld32<kLd>(col, o);
+                                tmem_ld32<16>(col, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int r = 0; r < kLd; ++r)
-                                    o[r] *= alpha[c + r];
-                                tmem_st32<kLd>(col, o);
+                                for (int r = 0; r < 16; ++r)
+                                    o[r] *= fmaxf(alpha[c + r], 0.f);
+                                tmem_st32<16>(col, o);
                             }
                             tmem_wait_st();
                         } else {
@@ -649,7 +735,14 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                             *abort_flag = 1;
                         }
                     }
-                    shift();
+#pragma unroll
+                    for (int r = 0; r < RP; r += 4) {
+                        const float4 d4 = *reinterpret_cast<const float4 *>(delta + r);
+                        x[r] += d4.x;
+                        x[r + 1] += d4.y;
+                        x[r + 2] += d4.z;
+                        x[r + 3] += d4.w;
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -694,10 +787,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             const int r0 = g * kHalf;
             float2 *weight = reinterpret_cast<float2 *>(misc + C::kAlpha) + r0;
             const int part = (2 * blockIdx.x + (pc.a > 0 ? 0 : 1)) * RP;
-            auto out_row = [&](int r) {
-                const int jr = r / p.G;
-                return (long long)(pc.tok0 + jr) * p.H_q + pc.h * p.G + (r - jr * p.G);
-            };
+            auto out_row = [&](int r) { return unit_row(p, pc, r); };
             if (n > 0) {
                 float *red = reinterpret_cast<float *>(smem + C::kOffQ + (pieces & 1) * C::kQBytes);     // [2][4][RP]
 #pragma unroll
@@ -712,13 +802,13 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 named_bar_sync(both_bar, 256);
                 if (tau < kHalf) {
                     const int r = r0 + tau;
-                    const float *other = reinterpret_cast<const float *>(misc + C::kRef);
+                    const float *negs = reinterpret_cast<const float *>(misc + C::kNeg);
                     float l[2], m[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float *x = red + k * 4 * RP + r;
                         l[k] = (x[0] + x[RP]) + (x[2 * RP] + x[3 * RP]);
-                        m[k] = l[k] == 0.f ? -CUDART_INF_F : other[k * RP + r];
+                        m[k] = l[k] == 0.f ? -CUDART_INF_F : -negs[k * RP + r];
                     }
                     const float M = fmaxf(m[0], m[1]);
                     const float w0 = l[0] == 0.f ? 0.f : exp2f(m[0] - M), w1 = l[1] == 0.f ? 0.f : exp2f(m[1] - M);
@@ -809,8 +899,46 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
         // dimensions become units 2 unit and 2 unit + 1 of f16, the upper half of the lanes storing the odd one first, so
         // that a store's lanes meet no bank twice
         const int unit = lane & 7, sub = lane >> 3;
-        int u = 0;
+        int u = 0, copied = 0;
         while (ok && next_piece(pc, ok)) {
+            if (pc.a == pc.b)
+                continue;
+            const int buf = copied & 1;
+            if (copied >= 2)
+                ok = wait(bar(C::kBarQFree, buf), ((copied >> 1) - 1) & 1);
+            if (!ok)
+                break;
+            ++copied;
+            // a quarter of the rows each, two at a time, 8 elements a lane; zeros past the rows
+            const int R = p.G * pc.q_len;
+            uint8_t *qs = smem + C::kOffQ + buf * C::kQBytes;
+            float *scale = reinterpret_cast<float *>(misc + C::kScale) + buf * RP;
+            constexpr int kLoads = RP >= 32 ? 4 : RP / 8;              // in flight
+#pragma unroll 1
+            for (int r0 = w * (RP / 4); r0 < (w + 1) * (RP / 4); r0 += 2 * kLoads) {
+                uint4 x[kLoads];
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    const int r = r0 + 2 * k + (lane >> 4);
+                    x[k] = r < R ? __ldg(reinterpret_cast<const uint4 *>(p.q + unit_row(p, pc, r) * kHeadDim) + (lane & 15))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    const int r = r0 + 2 * k + (lane >> 4);
+                    uint2 hi, lo;
+                    const int e = split_q_half_row(x[k], hi, lo);
+                    const uint32_t at = r * 128 + (((((lane & 15) >> 1) ^ (r & 7)) << 4) | ((lane & 1) << 3));
+                    *reinterpret_cast<uint2 *>(qs + at) = hi;
+                    *reinterpret_cast<uint2 *>(qs + RP * 128 + at) = lo;
+                    if ((lane & 15) == 0)
+                        scale[r] = p.score_scale_log2 * __int_as_float((127 - e) << 23);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(C::kBarQ, buf));
             const int lo = max(0, pc.L - pc.q_len + 1 - p.window);
             for (int t = pc.a; t < pc.b; ++t, ++u) {
                 const int st = u % C::kStages, vb = u & 1;
@@ -857,62 +985,62 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
 }
 
 // Joins the pieces of the units that several runs share: block `index` those of the unit whose last piece is that run's
-// first; a warp takes a row at a time.  In key order, whatever the timing: with M = max m_i over the pieces with l_i > 0,
+// first, four rows of them, one a warp.  In key order, whatever the timing: with M = max m_i over the pieces with l_i > 0,
 //     out = sum o_i 2^(m_i - M) / sum l_i 2^(m_i - M)
-constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 4;                         // rows (warps) of a block
 constexpr int kMaxRuns = 1024;                       // runs (SMs) at most
 
-__global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const WindowParams p)
+__global__ void __launch_bounds__(32 * kJoinRows) window_join_kernel(const WindowParams p)
 {
     __shared__ int slots[kMaxRuns], count;
     wait_prior_grid();
     const int index = blockIdx.x;
     const Piece pc = p.shared[2 * index];
-    if (pc.s < 0 || pc.b != pc.t)
-        return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * kJoinRows + warp, R = p.G * pc.q_len;
+    if (pc.s < 0 || pc.b != pc.t || (int)blockIdx.y * kJoinRows >= R)
+        return;
     if (warp == 0) {
         const int n = shared_slots(index, [&](int slot) { return p.shared[slot].s >= 0; }, slots);
         if (lane == 0)
             count = n;
     }
     __syncthreads();
-    const int pieces = count, R = p.G * pc.q_len;
-    for (int r = warp; r < R; r += kJoinThreads / 32) {
-        float M = -CUDART_INF_F, lam = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kAtOnce = 8;
-        for (int g0 = 0; g0 < pieces; g0 += kAtOnce) {
-            float m[kAtOnce], l[kAtOnce];
-            float4 o[kAtOnce];
+    if (r >= R)
+        return;
+    const int pieces = count;
+    float M = -CUDART_INF_F, lam = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAtOnce = 8;
+    for (int g0 = 0; g0 < pieces; g0 += kAtOnce) {
+        float m[kAtOnce], l[kAtOnce];
+        float4 o[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                const long long slot = (long long)slots[max(pieces - 1 - g0 - i, 0)] * p.rows + r;
-                m[i] = __ldg(p.part_m + slot);
-                l[i] = g0 + i < pieces ? __ldg(p.part_l + slot) : 0.f;
-                o[i] = __ldg(reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim) + lane);
-            }
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                if (l[i] == 0.f)
-                    continue;
-                const float mn = fmaxf(M, m[i]), wa = M == -CUDART_INF_F ? 0.f : exp2f(M - mn), wb = exp2f(m[i] - mn);
-                M = mn;
-                lam = lam * wa + l[i] * wb;
-                acc.x = acc.x * wa + o[i].x * wb;
-                acc.y = acc.y * wa + o[i].y * wb;
-                acc.z = acc.z * wa + o[i].z * wb;
-                acc.w = acc.w * wa + o[i].w * wb;
-            }
+        for (int i = 0; i < kAtOnce; ++i) {
+            const long long slot = (long long)slots[max(pieces - 1 - g0 - i, 0)] * p.rows + r;
+            m[i] = __ldg(p.part_m + slot);
+            l[i] = g0 + i < pieces ? __ldg(p.part_l + slot) : 0.f;
+            o[i] = __ldg(reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim) + lane);
         }
-        const float inv = lam == 0.f ? 0.f : 1.f / lam;
-        const int j = r / p.G;
-        const long long row = (long long)(pc.tok0 + j) * p.H_q + pc.h * p.G + (r - j * p.G);
-        *reinterpret_cast<uint2 *>(p.out + row * kHeadDim + lane * 4) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (lane == 0 && p.lse != nullptr)
-            p.lse[row] = lam == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(lam);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (l[i] == 0.f)
+                continue;
+            const float mn = fmaxf(M, m[i]), wa = M == -CUDART_INF_F ? 0.f : exp2f(M - mn), wb = exp2f(m[i] - mn);
+            M = mn;
+            lam = lam * wa + l[i] * wb;
+            acc.x = acc.x * wa + o[i].x * wb;
+            acc.y = acc.y * wa + o[i].y * wb;
+            acc.z = acc.z * wa + o[i].z * wb;
+            acc.w = acc.w * wa + o[i].w * wb;
+        }
     }
+    const float inv = lam == 0.f ? 0.f : 1.f / lam;
+    const long long row = unit_row(p, pc, r);
+    *reinterpret_cast<uint2 *>(p.out + row * kHeadDim + lane * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[row] = lam == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(lam);
 }
 
 template <int RP, bool FP8>
@@ -966,6 +1094,8 @@ cudaError_t launch_window_step(const WindowParams &params, int kv_dtype, long lo
     const long long keys = max_seq_len < most ? max_seq_len : most;
     const long long tiles = (keys + kKeys - 1) / kKeys;
     const long long units = (long long)(p.bs < p.num_tokens ? p.bs : p.num_tokens) * p.H_kv;
+    p.inv_G = (65536 + p.G - 1) / p.G;               // r / G = r * inv_G >> 16 for the rows r < 64
+    p.small = p.bs <= 32 * kSmall && (long long)p.bs * p.H_kv * (most / kKeys + 1 + kUnitFixed) + num_sms < INT_MAX;
     long long runs = units * (tiles < 1 ? 1 : tiles);
     runs = runs < 1 ? 1 : (runs < num_sms ? runs : num_sms);
     runs = runs < kMaxRuns ? runs : kMaxRuns;
@@ -975,7 +1105,8 @@ cudaError_t launch_window_step(const WindowParams &params, int kv_dtype, long lo
     e = launch(kv_map, p, (int)runs, stream);
     if (e != cudaSuccess || runs == 1)
         return e;
-    return launch_pdl(window_join_kernel, dim3((unsigned)runs), dim3(kJoinThreads), 0, stream, p);
+    return launch_pdl(window_join_kernel, dim3((unsigned)runs, (unsigned)((p.G * p.max_q_len + kJoinRows - 1) / kJoinRows)),
+                      dim3(32 * kJoinRows), 0, stream, p);
 }
 
 }  // namespace sk
