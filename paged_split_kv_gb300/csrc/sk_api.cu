@@ -802,8 +802,9 @@ static int chunk_call(const char *name, const void *q, const void *kv_pages, int
     if (rc != SK_OK)
         return rc;
     const bool step = window > 0 && window_step_takes((long long)G * max_q_len);
-    const int64_t need = step ? window_step_workspace_bytes(G * max_q_len, sms)
-                              : prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
+    const int64_t need = step         ? window_step_workspace_bytes(G * max_q_len, sms)
+                         : window > 0 ? window_chunk_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms)
+                                      : prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
     if (workspace == nullptr || workspace_bytes < need)
         return fail(SK_ERR_CAPACITY, "%s: workspace of %lld bytes, %lld needed", name,
                     (long long)workspace_bytes, (long long)need);
@@ -826,18 +827,19 @@ static int chunk_call(const char *name, const void *q, const void *kv_pages, int
         p.H_q = num_q_heads;
         p.H_kv = num_kv_heads;
         p.G = G;
-        p.window = window < kAll ? window : kAll;
-        p.sinks = sinks < kAll ? sinks : kAll;
         p.score_scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
         p.v_scale = fp8 ? v_scale : 1.f;
         p.wait_limit = wait_limit();
     };
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (step) {
+    if (window > 0) {
         WindowParams p{};
         fill(p);
-        e = launch_window_step(p, kv_dtype, max_seq_len, workspace, sms, st);
+        p.window = window < kAll ? window : kAll;
+        p.sinks = sinks < kAll ? sinks : kAll;
+        e = step ? launch_window_step(p, kv_dtype, max_seq_len, workspace, sms, st)
+                 : launch_window_chunk(p, kv_dtype, max_seq_len, workspace, sms, st);
     } else {
         PrefillParams p{};
         fill(p);
@@ -868,11 +870,12 @@ int64_t sk_window_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_he
         return fail(SK_ERR_INVALID, "sk_window_workspace_bytes: num_tokens=%d num_q_heads=%d num_kv_heads=%d max_q_len=%d "
                     "kv_dtype=%d", num_tokens, num_q_heads, num_kv_heads, max_q_len, kv_dtype);
     const long long rows = (long long)max_q_len * (num_q_heads / num_kv_heads);
-    if (!window_step_takes(rows))
-        return sk_prefill_workspace_bytes(num_tokens, num_q_heads, kv_dtype);
     int sms = 0;
     const int rc = sm_count(&sms);
-    return rc != SK_OK ? rc : window_step_workspace_bytes((int)rows, sms);
+    if (rc != SK_OK)
+        return rc;
+    return window_step_takes(rows) ? window_step_workspace_bytes((int)rows, sms)
+                                   : window_chunk_workspace_bytes(num_tokens, num_q_heads, kv_dtype, sms);
 }
 
 int sk_paged_window_attn(const void *q, const void *kv_pages, int kv_dtype, float k_scale, float v_scale,

@@ -11,7 +11,7 @@ struct PrefillPiece {
     int s, h, unit, L, q_len, tok0;
     int t, a, b;
     int nA, nB;                  // tiles of [a, b) that row tiles A and B need
-    int gap;                     // window: pages between the sinks and the window, which no tile holds
+    int pad;
 };
 
 // Attention of a chunk of new tokens, resolved on the host.
@@ -31,8 +31,6 @@ struct PrefillParams {
     int gb, tpb, nsub;           // heads and tokens of a row tile, row tiles per token (set by the launcher)
     int deal;                    // whole units are dealt to the CTAs first (set by the launcher)
     int causal;
-    int window, sinks;           // window > 0: a token sees its last `window` rows and the first `sinks` ones (causal)
-    int sink_pages;              // (set by the launcher)
     float score_scale_log2;      // sm_scale * k_scale * log2(e)
     float v_scale;
     long long wait_limit;
@@ -40,6 +38,17 @@ struct PrefillParams {
 long long prefill_workspace_bytes(int num_tokens, int H_q, int kv_dtype, int num_sms);
 cudaError_t launch_prefill(const PrefillParams &p, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,
                            cudaStream_t stream);
+
+// Windowed attention of a chunk: a piece of a unit of work (two row tiles of one sequence and KV head), key tiles [a, b) of
+// its t.
+struct ChunkPiece {
+    int s, h, unit, L, q_len, tok0;
+    int t, a, b;
+    int nA, nB;                  // tiles of [a, b) that row tiles A and B need
+    int gap;                     // pages between the sinks and the window, which no tile holds
+    int lo, hi;                  // the unit's rows see rows below the sinks, and [lo, hi)
+    int pad[2];
+};
 
 // Windowed attention of a step: a piece of a (sequence, KV head), key tiles [a, b) of its t.
 struct WindowPiece {
@@ -49,27 +58,35 @@ struct WindowPiece {
     int pad[3];
 };
 
-// Windowed attention of a step (up to 64 rows a sequence and KV head), resolved on the host.
+// Windowed attention, resolved on the host.
 struct WindowParams {
     const uint16_t *q;           // bf16 bits [NT, H_q, D]
     const void *kv;              // pages
     const int32_t *block_table, *seq_lens, *cu_q;
     uint16_t *out;               // bf16 bits [NT, H_q, D]
     float *lse;                  // [NT, H_q] or NULL
-    float *part_o, *part_m, *part_l;   // partial states of the pieces (set by the launcher) ...
-    WindowPiece *shared;         // ... and what they are pieces of, two per run
     int *status;
     int64_t num_blocks;
     int bt_stride, bs, num_tokens, max_q_len;
     int H_q, H_kv, G;
     int window, sinks;
-    int rows, sink_pages;        // rows of a partial state (set by the launcher)
-    int inv_G;                   // 2^16 / G, rounded up (set by the launcher)
-    int small;                   // the runs are found by a warp (set by the launcher)
     float score_scale_log2;      // sm_scale * k_scale * log2(e)
     float v_scale;
     long long wait_limit;
+    // set by the launchers: partial states of the pieces that runs share ...
+    float *part_o, *part_m, *part_l;
+    WindowPiece *shared;         // ... and what they are pieces of, two per run, of a step ...
+    ChunkPiece *units;           // ... or of a chunk
+    int sink_pages;
+    int rows, inv_G, small;      // step: rows of a partial state; 2^16 / G, rounded up; the runs are found by a warp
+    const float *q_scale;        // chunk, e4m3 pages: 2^-e of each row of the split Q
+    int gb, tpb, nsub;           // chunk: heads and tokens of a row tile, row tiles per token
+    int deal, shift;             // chunk: whole units are dealt first; costs are in 2^shift keys
+    int wide, out_heads;         // chunk: out takes 32-byte stores; a softmax warp's rows are this many heads of tokens, or 0
 };
+long long window_chunk_workspace_bytes(int num_tokens, int H_q, int kv_dtype, int num_sms);
+cudaError_t launch_window_chunk(const WindowParams &p, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,
+                                cudaStream_t stream);
 bool window_step_takes(long long rows);
 long long window_step_workspace_bytes(int rows, int num_sms);
 cudaError_t launch_window_step(const WindowParams &p, int kv_dtype, long long max_seq_len, void *workspace, int num_sms,

@@ -126,40 +126,19 @@ constexpr int kColS = 0, kColO = 256;                // S_A, S_B, then O_A, O_B,
 // 32k keys, 8 KV heads, 151 MB: 1433 us with 0.2 GB read from HBM, against 1543 us and 3.6 GB).  Dealing takes no account of
 // what units cost, so it is done only where the largest costs at most 1.4 times the mean (no CTA then gets more
 // than that times its share) or an eighth of a CTA's share.
-//
-// With a window (WIN) a unit's keys are the sinks' pages and the pages from the first row that its first token's window
-// holds: they are numbered without the pages between (`gap` of them), so that a tile is eight pages that some row needs,
-// the sinks share theirs with the window's first pages, and a unit of 2 * tpb tokens costs about sinks + window + 2 * tpb
-// keys wherever it lies.  A unit of the first tokens sees fewer: the cost rises until the window is full.
-template <bool WIN>
 struct Seq {
     int L, q_len, tok0, units;                       // units of one head
-    long long base, step;                            // unit i costs base + step * (i + 1) ...
-    long long top;                                   // ... but no more than this (WIN)
-    int rising;                                      // units below that
-    __device__ __forceinline__ long long before(int i) const
-    {
-        if constexpr (WIN) {
-            const long long n = min(i, rising);
-            return n * base + step * n * (n + 1) / 2 + (i - n) * top;
-        }
-        return i * base + step * i * (i + 1) / 2;
-    }
-    __device__ __forceinline__ long long cost(int i) const
-    {
-        if constexpr (WIN)
-            return i < rising ? base + step * (i + 1) : top;
-        return base + step * (i + 1);
-    }
+    long long base, step;                            // unit i costs base + step * (i + 1)
+    __device__ __forceinline__ long long before(int i) const { return i * base + step * i * (i + 1) / 2; }
+    __device__ __forceinline__ long long cost(int i) const { return base + step * (i + 1); }
 };
 
 constexpr double kL2Share = 60e6;                    // bytes of K and V that stay in the L2 (126 MB in two halves)
 constexpr int kUnitFixed = 384;                      // cost of starting and finishing a unit, in keys
 
-template <bool WIN>
-__device__ __forceinline__ Seq<WIN> sequence(const PrefillParams &p, int s)
+__device__ __forceinline__ Seq sequence(const PrefillParams &p, int s)
 {
-    Seq<WIN> q;
+    Seq q;
     q.L = __ldg(p.seq_lens + s);
     q.tok0 = __ldg(p.cu_q + s);
     const int end = __ldg(p.cu_q + s + 1);
@@ -172,12 +151,6 @@ __device__ __forceinline__ Seq<WIN> sequence(const PrefillParams &p, int s)
     const bool rising = p.causal && p.nsub == 1;     // later units see more keys
     q.base = kUnitFixed + (rising ? max(0, q.L - q.q_len) : q.L);
     q.step = rising ? 2 * p.tpb : 0;
-    if constexpr (WIN) {
-        q.top = kUnitFixed + (long long)p.sink_pages * kPage + p.window + 2 * p.tpb;
-        q.rising = q.top <= q.base ? 0 : INT_MAX;
-        if (q.rising > 0 && q.step > 0)
-            q.rising = (int)min((q.top - q.base) / (long long)q.step, (long long)INT_MAX);
-    }
     return q;
 }
 
@@ -195,33 +168,14 @@ __device__ __forceinline__ void tile_origin(const PrefillParams &p, int T, int &
     }
 }
 
-// What a unit's rows see (WIN): rows below the sinks, and from lo on those below hi (lo <= hi).
-struct Range {
-    int lo, hi, gap;                                 // gap: pages between the sinks' and the one that holds row lo
-};
-
-__device__ __forceinline__ Range unit_range(const PrefillParams &p, int L, int q_len, int unit)
-{
-    int j0, i0, j1, i1;
-    tile_origin(p, 2 * unit, j0, i0);
-    tile_origin(p, 2 * unit + 1, j1, i1);
-    Range r;
-    r.hi = visible_keys(L, q_len, min(q_len, j1 + p.tpb) - 1, 1);
-    r.lo = max(0, visible_keys(L, q_len, j0, 1) - p.window);
-    r.gap = max(0, r.lo / kPage - p.sink_pages);
-    return r;
-}
-
-// Key tiles that row tile T of a sequence needs (0 when it has no tokens).  `gap`: see Range.
-template <bool WIN>
-__device__ __forceinline__ int tiles_of(const PrefillParams &p, int L, int q_len, int T, int gap)
+// Key tiles that row tile T of a sequence needs (0 when it has no tokens).
+__device__ __forceinline__ int tiles_of(const PrefillParams &p, int L, int q_len, int T)
 {
     int j0, i0;
     tile_origin(p, T, j0, i0);
     if (j0 >= q_len)
         return 0;
-    const int seen = visible_keys(L, q_len, min(q_len, j0 + p.tpb) - 1, p.causal);
-    return (seen - (WIN ? gap * kPage : 0) + kKeys - 1) / kKeys;
+    return (visible_keys(L, q_len, min(q_len, j0 + p.tpb) - 1, p.causal) + kKeys - 1) / kKeys;
 }
 
 // What a CTA has to do: whole units first, first + stride, ... below `dealt` (in the order of sequence, head, unit), then the
@@ -232,20 +186,19 @@ struct Share {
 };
 
 // Walks a share's pieces; called by a converged warp.
-template <bool WIN>
 struct Walk {
     const PrefillParams &p;
     long long lo, hi, off;                           // the run, and where the current sequence starts
     int s, h, unit;
     int deal, stride, dealt, seek, passed;           // next unit dealt; the sequence that the search is at, units before it
     bool loaded;
-    Seq<WIN> q;
+    Seq q;
     __device__ Walk(const PrefillParams &pp, const Share &sh)
         : p(pp), lo(sh.lo), hi(sh.hi), off(sh.before), s(sh.s), h(0), unit(-1), deal(sh.first), stride(sh.stride),
           dealt(sh.dealt), seek(0), passed(0), loaded(false)
     {
     }
-    __device__ __forceinline__ void fill(Piece &pc, int s_, int h_, int unit_, const Seq<WIN> &sq, int &tA, int &tB) const
+    __device__ __forceinline__ void fill(Piece &pc, int s_, int h_, int unit_, const Seq &sq, int &tA, int &tB) const
     {
         pc.s = s_;
         pc.h = h_;
@@ -253,21 +206,18 @@ struct Walk {
         pc.L = sq.L;
         pc.q_len = sq.q_len;
         pc.tok0 = sq.tok0;
-        pc.gap = 0;
-        if constexpr (WIN)
-            pc.gap = unit_range(p, sq.L, sq.q_len, unit_).gap;
-        tA = tiles_of<WIN>(p, sq.L, sq.q_len, 2 * unit_, pc.gap);
-        tB = tiles_of<WIN>(p, sq.L, sq.q_len, 2 * unit_ + 1, pc.gap);
+        tA = tiles_of(p, sq.L, sq.q_len, 2 * unit_);
+        tB = tiles_of(p, sq.L, sq.q_len, 2 * unit_ + 1);
         pc.t = max(tA, tB);
     }
     // Unit number `deal`: 32 sequences at a time until the one that has it.
     __device__ __forceinline__ void dealt_unit(Piece &pc)
     {
         const int lane = threadIdx.x & 31;
-        Seq<WIN> sq;
+        Seq sq;
         int own, incl;
         while (true) {
-            sq = sequence<WIN>(p, min(seek + lane, p.bs - 1));
+            sq = sequence(p, min(seek + lane, p.bs - 1));
             own = seek + lane < p.bs ? sq.units * p.H_kv : 0;
             incl = own;
             for (int o = 1; o < 32; o <<= 1) {
@@ -283,7 +233,7 @@ struct Walk {
         const int src = __ffs(__ballot_sync(kFull, deal < passed + incl)) - 1;
         const int index = deal - passed - __shfl_sync(kFull, incl - own, src);
         const int at = seek + src;
-        Seq<WIN> found = sequence<WIN>(p, at);
+        Seq found = sequence(p, at);
         int tA, tB;
         fill(pc, at, index / found.units, index % found.units, found, tA, tB);
         pc.a = 0;
@@ -313,7 +263,7 @@ struct Walk {
         }
         while (s < p.bs && off < hi) {
             if (!loaded) {
-                q = sequence<WIN>(p, s);
+                q = sequence(p, s);
                 loaded = true;
             }
             const long long head = q.before(q.units);
@@ -366,7 +316,7 @@ struct Walk {
 
 // The share of CTA `index` of `count`; every thread of the block calls it.  `part` (2 words of 64 bits per warp) and
 // `found` (3) are shared memory; the share is there for all threads on return.
-template <int kThreads, bool WIN>
+template <int kThreads>
 __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, int count, long long *part, long long *found)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -377,7 +327,7 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
     uint32_t largest = 0;                            // one unit's cost (its keys and the fixed part: below 2^32)
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-        const Seq<WIN> q = sequence<WIN>(p, s);
+        const Seq q = sequence(p, s);
         cost += q.before(q.units) * p.H_kv;
         units += q.units * p.H_kv;
         if (q.units > 0)
@@ -425,7 +375,7 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
         int left = sh.dealt - (int)units_before;
 #pragma unroll 1
         for (int s = s0; s < s1; ++s) {
-            const Seq<WIN> q = sequence<WIN>(p, s);
+            const Seq q = sequence(p, s);
             const int here = q.units * p.H_kv;
             if (left < here) {
                 found[2] = before + (long long)(left / q.units) * q.before(q.units) + q.before(left % q.units);
@@ -446,7 +396,7 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
         int s = s0;
 #pragma unroll 1
         for (; s < s1 - 1; ++s) {
-            const Seq<WIN> q = sequence<WIN>(p, s);
+            const Seq q = sequence(p, s);
             const long long here = q.before(q.units) * p.H_kv;
             if (sh.lo < before + here)
                 break;
@@ -461,7 +411,7 @@ __device__ __forceinline__ Share find_share(const PrefillParams &p, int index, i
     return sh;
 }
 
-template <bool FP8, bool WIN>
+template <bool FP8>
 __global__ void __launch_bounds__(PCfg<FP8>::kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                const PrefillParams p)
@@ -519,7 +469,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
     if (blockIdx.x == 0 && threadIdx.x == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_q + p.bs) != p.num_tokens))
         atomicOr(p.status, SK_DEV_BAD_SEQ);
     // found in the K and V slots' memory, before the first copy
-    Share share = find_share<C::kThreads, WIN>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(smem),
+    Share share = find_share<C::kThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(smem),
                                           reinterpret_cast<long long *>(misc + C::kStart));
     fence_proxy_async_smem();
     tc_fence_before();
@@ -555,16 +505,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
             int u = 0;
             bool ok = true;
             while (ok && next_piece(pc, ok)) {
-                // (with a window no page past the unit's last row: the next may be another's)
-                const int page_end =
-                    ((WIN ? unit_range(p, pc.L, pc.q_len, pc.unit).hi : pc.L) + kPage - 1) / kPage;
+                const int page_end = (pc.L + kPage - 1) / kPage;
                 const int32_t *bt = p.block_table + (long long)pc.s * p.bt_stride;
-                auto page_at = [&](int t) {
-                    const int pg = t * C::kPagesPerTile + lane;
-                    return WIN && pg >= p.sink_pages ? pg + pc.gap : pg;
-                };
                 auto block_at = [&](int t) {
-                    const int pg = page_at(t);
+                    const int pg = t * C::kPagesPerTile + lane;
                     return (lane < C::kPagesPerTile && t < pc.b && pg < page_end) ? __ldg(bt + pg) : -1;
                 };
                 int blk = block_at(pc.a), blk1 = block_at(pc.a + 1);
@@ -583,7 +527,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                         __syncwarp();
                         if (lane < C::kPagesPerTile) {
                             int grp = -2;            // whole box out of bounds: zero fill
-                            if (page_at(t) < page_end) {
+                            if (t * C::kPagesPerTile + lane < page_end) {
                                 if (blk >= 0 && blk < p.num_blocks)
                                     grp = (blk * p.H_kv + pc.h) * 2;
                                 else
@@ -611,7 +555,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                 share.s = p.bs;
                 share.dealt = 0;
             }
-            Walk<WIN> walk(p, share);
+            Walk walk(p, share);
             Piece *shared = p.shared + 2 * blockIdx.x;   // this run's pieces of units that others have a part of
             if (lane < 2)
                 shared[lane].s = -1;
@@ -800,25 +744,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
         const int nx = x ? pc->nB : pc->nA;
         const int first_key = pc->a * kKeys, L = pc->L;
         int limit, least;                                          // keys that the row sees; that all of the warp's see
-        // WIN, keys numbered without the gap: the row's window starts at low (0 where it reaches the sinks), and at `high`
-        // or below in all of the warp's rows; V's rows [dead_lo, dead_hi) and from the end on are no row's of the unit
-        int low = 0, high = 0, dead_lo = 0, dead_hi = 0, end = L;
         float c = p.score_scale_log2;
         {
             int j, i;
             const bool live = row_at(j, i);
             limit = live ? visible_keys(L, pc->q_len, j, p.causal) : 0;
-            if constexpr (WIN) {
-                const Range r = unit_range(p, L, pc->q_len, pc->unit);
-                const int gap = r.gap * kPage;
-                low = limit - p.window;
-                low = low > p.sinks ? low - gap : 0;
-                limit = max(0, limit - gap);
-                high = __reduce_max_sync(kFull, low);
-                end = r.hi - gap;
-                dead_lo = p.sinks;
-                dead_hi = r.lo > p.sinks ? r.lo - gap : 0;
-            }
             least = __reduce_min_sync(kFull, live ? limit : INT_MAX);        // what padding rows hold is never used
             if (FP8 && live)
                 c *= __ldg(p.q_scale + (long long)(pc->tok0 + j) * p.H_q + pc->h * p.G + i);
@@ -841,20 +771,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                 tmem_ld32<32>(ts + cc, v + cc);
             tmem_wait_ld();
             const int lim = limit - key0;                          // columns [0, lim) are visible
-            bool sees = lim > 0;
-            bool cut_low = false;                                  // some column below a row's window
-            if constexpr (WIN) {
-                cut_low = key0 < high;                             // uniform in the warp
-                if (cut_low) {
-                    // columns below the sinks or in the row's window
-                    const int from = low - key0, sk = min(p.sinks, limit) - key0;
-                    sees = sk > 0 || (lim > 0 && from < kKeys);
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        v[i] = (i >= from && i < lim) || i < sk ? v[i] : -CUDART_INF_F;
-                }
-            }
-            if (!cut_low && key0 + kKeys > least) {                // uniform in the warp
+            if (key0 + kKeys > least) {                            // uniform in the warp
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     v[i] = i < lim ? v[i] : -CUDART_INF_F;
@@ -896,28 +813,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
             };
             // A row's first scores give it a reference: the largest of the first 16 will do (see below).
             if (!anchored) {
-                if (__any_sync(kFull, m_ref == -CUDART_INF_F && sees)) {
+                if (__any_sync(kFull, m_ref == -CUDART_INF_F && lim > 0)) {
                     float top = v[0];
 #pragma unroll
                     for (int i = 1; i < 15; i += 2)
                         top = fmax3(top, v[i], v[i + 1]);
-                    top = fmaxf(top, v[15]) * c;
-                    if (WIN && cut_low)                            // the first 16 are often below the window
-                        top = tile_top();
-                    raise(top, j > 0);
+                    raise(fmaxf(top, v[15]) * c, j > 0);
                 }
                 anchored = !__any_sync(kFull, m_ref == -CUDART_INF_F && limit > 0);
             }
             // rows past the sequence's end in its last page hold anything, and 0 * NaN would reach O: their V
             // becomes zeros, before either row tile multiplies it
-            const bool dead_start = WIN && key0 < dead_hi && key0 + kKeys > dead_lo;
-            if (!FP8 && (dead_start || (end < key0 + kKeys && (end & (kPage - 1)) != 0))) {
+            if (!FP8 && L < key0 + kKeys && (L & (kPage - 1)) != 0) {
                 const int i = u + 2 * j + 1;
                 ok = wait_bar(bar_full(i % C::kSlots), (i / C::kSlots) & 1, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 const int tok = key0 + tau;
-                if (ok && ((tok >= end && tok < (end + kPage - 1) / kPage * kPage) ||
-                           (WIN && tok >= dead_lo && tok < dead_hi))) {
+                if (ok && tok >= L && tok < (L + kPage - 1) / kPage * kPage) {
                     uint8_t *row = smem + i % C::kSlots * C::kSlotBytes + (tau >> 3) * C::kGroupBytes +
                                    (tau & 7) * 128;
 #pragma unroll
@@ -960,7 +872,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                 }
                 h2 = fadd2(h2, g2);
                 const bool redo = limit > 0 && !(h2.x + h2.y <= C::kSumMost);
-                if (again || !__any_sync(kFull, redo || (sees && m_ref == -CUDART_INF_F)))
+                if (again || !__any_sync(kFull, redo || (lim > 0 && m_ref == -CUDART_INF_F)))
                     break;
                 tmem_wait_st();
                 raise(tile_top(), j > 0);
@@ -1060,14 +972,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
         const int u = lane & 7, sub = lane >> 3;
         int v = 0;                                                 // key tiles so far
         bool ok = true;
-        while (ok && next_piece(pc, ok)) {
-        int end = pc.L, dead_lo = 0, dead_hi = 0;                   // rows that no row of the unit sees, as above
-        if constexpr (WIN) {
-            const Range r = unit_range(p, pc.L, pc.q_len, pc.unit);
-            end = r.hi - r.gap * kPage;
-            dead_lo = p.sinks;
-            dead_hi = r.lo > p.sinks ? r.lo - r.gap * kPage : 0;
-        }
+        while (ok && next_piece(pc, ok))
         for (int tile = pc.a; tile < pc.b; ++tile, ++v) {
             const int slot = (2 * v + 1) % C::kSlots, vb = v & 1;
             ok = wait_bar(bar_full(slot), ((2 * v + 1) / C::kSlots) & 1, abort_flag, p.wait_limit);
@@ -1083,8 +988,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
             for (int k = 0; k < 8; ++k) {
                 const int t = w * 32 + k * 4 + sub, x8 = t & 7;
                 uint4 a = *reinterpret_cast<const uint4 *>(src + (t >> 3) * 1024 + x8 * 128 + ((u ^ x8) << 4));
-                if (key0 + t >= end || (WIN && key0 + t >= dead_lo && key0 + t < dead_hi))
-                    a = make_uint4(0u, 0u, 0u, 0u);                 // such rows may hold anything
+                if (key0 + t >= pc.L)                               // past the end the page holds anything
+                    a = make_uint4(0u, 0u, 0u, 0u);
                 const uint4 lo = make_uint4(f16x2_of_e4m3(a.x), f16x2_of_e4m3(a.x >> 16), f16x2_of_e4m3(a.y),
                                             f16x2_of_e4m3(a.y >> 16));
                 const uint4 hi = make_uint4(f16x2_of_e4m3(a.z), f16x2_of_e4m3(a.z >> 16), f16x2_of_e4m3(a.w),
@@ -1100,7 +1005,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant
                 mbar_arrive(bar_vfull(vb));
                 mbar_arrive(bar_empty(slot));
             }
-        }
         }
         if (!ok) {
             *abort_flag = 1;
@@ -1185,22 +1089,22 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
     }
 }
 
-template <bool FP8, bool WIN>
+template <bool FP8>
 cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const PrefillParams &p, int runs,
                      cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<FP8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                PCfg<FP8>::kSmemBytes);
     if (e != cudaSuccess)
         return e;
     // the warpgroups' shares after the reallocation may not exceed what the CTA was launched with
     static const int regs = [] {
         cudaFuncAttributes a{};
-        return cudaFuncGetAttributes(&a, prefill_kernel<FP8, WIN>) == cudaSuccess ? a.numRegs : 0;
+        return cudaFuncGetAttributes(&a, prefill_kernel<FP8>) == cudaSuccess ? a.numRegs : 0;
     }();
     if (regs < PCfg<FP8>::kRegsLaunch)
         return cudaErrorInvalidConfiguration;
-    return launch_pdl(prefill_kernel<FP8, WIN>, dim3((unsigned)runs), dim3(PCfg<FP8>::kThreads), PCfg<FP8>::kSmemBytes,
+    return launch_pdl(prefill_kernel<FP8>, dim3((unsigned)runs), dim3(PCfg<FP8>::kThreads), PCfg<FP8>::kSmemBytes,
                       stream, kv_map, q_map, p);
 }
 
@@ -1301,20 +1205,12 @@ cudaError_t launch_prefill(const PrefillParams &params, int kv_dtype, long long 
     const long long per_seq = ((long long)(p.max_q_len + p.tpb - 1) / p.tpb * p.nsub + 1) / 2 * p.bs;
     const long long by_tokens = ((long long)(p.num_tokens + p.tpb - 1) / p.tpb * p.nsub + 1) / 2 + p.bs;
     const long long units = (per_seq < by_tokens ? per_seq : by_tokens) * p.H_kv;
-    if (p.window > 0) {
-        // what a unit sees at most
-        p.sink_pages = (p.sinks + kPage - 1) / kPage;
-        const long long most = (long long)p.sink_pages * kPage + p.window + 2 * p.tpb;
-        max_seq_len = max_seq_len < most ? max_seq_len : most;
-    }
     const long long tiles = (max_seq_len + kKeys - 1) / kKeys;
     long long runs = units * (tiles < 2 ? 1 : tiles / 2);
     runs = runs < 1 ? 1 : (runs < num_sms ? runs : num_sms);
     runs = runs < kMaxRuns ? runs : kMaxRuns;
     p.deal = (double)p.bs * max_seq_len * p.H_kv * (fp8 ? 256 : 512) > kL2Share ? 1 : 0;
-    auto launch = p.window > 0 ? (fp8 ? launch_t<true, true> : launch_t<false, true>)
-                               : (fp8 ? launch_t<true, false> : launch_t<false, false>);
-    e = launch(kv_map, q_map, p, (int)runs, stream);
+    e = fp8 ? launch_t<true>(kv_map, q_map, p, (int)runs, stream) : launch_t<false>(kv_map, q_map, p, (int)runs, stream);
     if (e != cudaSuccess || runs == 1)
         return e;
     return launch_pdl(prefill_join_kernel, dim3((unsigned)runs * kJoinParts), dim3(kJoinThreads), 0, stream, p);
