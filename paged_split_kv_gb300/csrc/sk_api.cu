@@ -829,7 +829,6 @@ static int chunk_call(const char *name, const void *q, const void *kv_pages, int
         p.G = G;
         p.score_scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
         p.v_scale = fp8 ? v_scale : 1.f;
-        p.wait_limit = wait_limit();
     };
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -838,12 +837,14 @@ static int chunk_call(const char *name, const void *q, const void *kv_pages, int
         fill(p);
         p.window = window < kAll ? window : kAll;
         p.sinks = sinks < kAll ? sinks : kAll;
+        p.wait_limit = (uint32_t)(wait_limit() < kDefaultWaitLimit ? wait_limit() : kDefaultWaitLimit);
         e = step ? launch_window_step(p, kv_dtype, max_seq_len, workspace, sms, st)
                  : launch_window_chunk(p, kv_dtype, max_seq_len, workspace, sms, st);
     } else {
         PrefillParams p{};
         fill(p);
         p.causal = causal ? 1 : 0;
+        p.wait_limit = wait_limit();
         e = launch_prefill(p, kv_dtype, max_seq_len, workspace, sms, st);
     }
     if (e != cudaSuccess)

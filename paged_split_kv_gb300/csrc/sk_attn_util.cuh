@@ -139,6 +139,26 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const vo
     return ok && !late;
 }
 
+// The same in fewer instructions, for kernels whose code fills the instruction cache: the clock in 32 bits, so limits up to
+// the default of 4e9 cycles; no test before the first wait.
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, const volatile int *abort, uint32_t limit)
+{
+    const uint32_t t0 = (uint32_t)clock();
+    uint32_t ok;
+    bool late;
+    do {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        late = (uint32_t)clock() - t0 > limit;
+    } while (!ok && !late && !(abort != nullptr && *abort));
+    return ok && !late;
+}
+
 // Transposes a 4 x 4 matrix of 16-byte units held by a quad of lanes: lane b ends with unit b of every lane.
 __device__ __forceinline__ void quad_transpose(uint4 (&w)[4], int lane)
 {

@@ -72,7 +72,7 @@ struct WindowParams {
     int window, sinks;
     float score_scale_log2;      // sm_scale * k_scale * log2(e)
     float v_scale;
-    long long wait_limit;
+    uint32_t wait_limit;
     // set by the launchers: partial states of the pieces that runs share ...
     float *part_o, *part_m, *part_l;
     WindowPiece *shared;         // ... and what they are pieces of, two per run, of a step ...

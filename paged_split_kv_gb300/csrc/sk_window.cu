@@ -45,7 +45,7 @@ using namespace sm100;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kKeys = 128;                           // keys of a tile (MMA M)
 constexpr int kPagesPerTile = kKeys / kPage;
-constexpr long long kDrainLimit = 4000000000LL;      // cycles (~2 s): waits for work already issued
+constexpr uint32_t kDrainLimit = 4000000000u;        // cycles (~2 s): waits for work already issued
 constexpr int kMaxSmem = 232448;
 constexpr int kRing = 8;                             // pieces published ahead
 constexpr int kUnitFixed = 1;                        // cost of starting and finishing a unit, in key tiles
@@ -321,7 +321,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
     if (!aligned && threadIdx.x == 0)
         atomicOr(p.status, SK_DEV_INTERNAL);
     auto wait = [&](uint32_t b, uint32_t parity) {
-        return __all_sync(kFull, wait_bar(b, parity, abort_flag, p.wait_limit)) != 0;
+        return __all_sync(kFull, wait_short(b, parity, abort_flag, p.wait_limit)) != 0;
     };
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -473,7 +473,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 give_up();
             // every copy issued lands before the CTA exits
             for (int t = u > C::kStages ? u - C::kStages : 0; t < u; ++t)
-                wait_bar(bar(C::kBarFull, t % C::kStages), (t / C::kStages) & 1, nullptr, kDrainLimit);
+                wait_short(bar(C::kBarFull, t % C::kStages), (t / C::kStages) & 1, nullptr, kDrainLimit);
         } else if (warp == 3) {
             // ============================================================ bf16: Q, K-major with the 128-byte swizzle
             int copied = 0;
@@ -545,7 +545,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 give_up();
             // every product completes before TMEM is freed and shared memory is left
             mma_commit_warp(bar(C::kBarDrain, 0));
-            wait_bar(bar(C::kBarDrain, 0), 0, nullptr, kDrainLimit);
+            wait_short(bar(C::kBarDrain, 0), 0, nullptr, kDrainLimit);
         } else {
             // ============================================================ O^T += V^T P^T
             constexpr uint32_t idesc = FP8 ? idesc_f16_f32(kHeadDim, RP, 1, 1) : idesc_bf16_f32(kHeadDim, RP, 1, 1);
@@ -584,7 +584,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             if (!ok)
                 give_up();
             mma_commit_warp(bar(C::kBarDrain, 1));
-            wait_bar(bar(C::kBarDrain, 1), 0, nullptr, kDrainLimit);
+            wait_short(bar(C::kBarDrain, 1), 0, nullptr, kDrainLimit);
         }
         __syncwarp();
     } else if (!FP8 || warp < 12) {

@@ -43,7 +43,7 @@ using namespace sm100;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRows = 128;                           // rows of one tile (MMA M)
 constexpr int kKeys = 128;                           // keys of one tile (MMA N)
-constexpr long long kDrainLimit = 4000000000LL;      // cycles (~2 s): waits for work already issued
+constexpr uint32_t kDrainLimit = 4000000000u;        // cycles (~2 s): waits for work already issued
 constexpr int kMaxSmem = 232448;
 constexpr int kRing = 4;                             // pieces published ahead
 
@@ -126,22 +126,6 @@ __device__ __forceinline__ void tile_origin(const WindowParams &p, int T, int &j
         j0 = T / p.nsub;                             // then a row tile is part of one token
         i0 = (T - j0 * p.nsub) * p.gb;
     }
-}
-
-struct Range {
-    int lo, hi, gap;                                 // a unit's rows see rows below the sinks, and from lo on those below hi
-};
-
-__device__ __forceinline__ Range unit_range(const WindowParams &p, int L, int q_len, int unit)
-{
-    int j0, i0, j1, i1;
-    tile_origin(p, 2 * unit, j0, i0);
-    tile_origin(p, 2 * unit + 1, j1, i1);
-    Range r;
-    r.hi = visible_keys(L, q_len, min(q_len, j1 + p.tpb) - 1, 1);
-    r.lo = max(0, visible_keys(L, q_len, j0, 1) - p.window);
-    r.gap = max(0, r.lo / kPage - p.sink_pages);
-    return r;
 }
 
 struct WindowWalk {
@@ -245,24 +229,21 @@ struct WindowWalk {
             const bool whole = deal < dealt;
             if (!whole && lo >= hi)
                 return false;
-            int src, start = 0, cost = count;            // the unit's place in the run's cost
-            if (whole || left_over) {
-                const int x = whole ? deal : unit;
-                if (whole)
-                    deal += count;
-                src = seek(x, false);
-                const int n = of(units, src);
-                const int i = x - units_before - of(units_to - units * p.H_kv, src);
+            const bool by_unit = whole || left_over;     // else the unit that lo lies in
+            const int x = whole ? deal : by_unit ? unit : lo;
+            const int src = seek(x, !by_unit);
+            int start, cost = count;                     // the unit's place in the run's cost
+            if (by_unit) {
+                deal += whole ? count : 0;
+                const int n = of(units, src), i = x - units_before - of(units_to - units * p.H_kv, src);
                 pc.h = i / n;
                 pc.unit = i - pc.h * n;
                 start = (x - dealt) * count;
             } else {
-                // the unit that lo lies in
-                src = seek(lo, true);
                 const int head = of(before(units), src);
-                const int from = cost_before + of(cost_to - before(units) * p.H_kv, src);
-                pc.h = (lo - from) / head;
-                const int in_head = lo - from - pc.h * head;
+                const int in = x - cost_before - of(cost_to - before(units) * p.H_kv, src);
+                pc.h = in / head;
+                const int in_head = in - pc.h * head;
                 const int b = of(base, src), st = of(step, src), tp = of(top, src), ri = of(rising, src);
                 auto upto = [&](int i) {
                     const int n = min(i, ri);
@@ -285,18 +266,16 @@ struct WindowWalk {
             pc.L = of(L, src);
             pc.q_len = of(q_len, src);
             pc.tok0 = of(tok0, src);
-            const Range r = unit_range(p, pc.L, pc.q_len, pc.unit);
-            pc.gap = r.gap;
-            pc.lo = r.lo;
-            pc.hi = r.hi;
-            // key tiles of the two row tiles
-            auto tiles = [&](int T) {
-                int j0, i0;
-                tile_origin(p, T, j0, i0);
-                const int seen = visible_keys(pc.L, pc.q_len, min(pc.q_len, j0 + p.tpb) - 1, 1);
-                return j0 >= pc.q_len ? 0 : (seen - r.gap * kPage + kKeys - 1) / kKeys;
-            };
-            const int tA = tiles(2 * pc.unit), tB = tiles(2 * pc.unit + 1);
+            // its two row tiles: their first tokens (the second's heads may be of the next token), what their rows see
+            int j0, i0;
+            tile_origin(p, 2 * pc.unit, j0, i0);
+            const int j1 = p.nsub == 1 ? j0 + p.tpb : i0 + p.gb < p.nsub * p.gb ? j0 : j0 + 1;
+            auto end = [&](int j) { return visible_keys(pc.L, pc.q_len, min(pc.q_len, j + p.tpb) - 1, 1); };
+            pc.lo = max(0, visible_keys(pc.L, pc.q_len, j0, 1) - p.window);
+            pc.hi = end(j1);
+            pc.gap = max(0, pc.lo / kPage - p.sink_pages);
+            auto tiles = [&](int j) { return j >= pc.q_len ? 0 : (end(j) - pc.gap * kPage + kKeys - 1) / kKeys; };
+            const int tA = tiles(j0), tB = tiles(j1);
             pc.t = max(tA, tB);
             pc.a = 0;
             pc.b = pc.t;
@@ -418,7 +397,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
     int read = 0;
     auto next_piece = [&](Piece &pc, bool &ok) {
         const int i = read % kRing;
-        ok = __all_sync(kFull, wait_bar(bar_piece(i), (read / kRing) & 1, abort_flag, p.wait_limit));
+        ok = __all_sync(kFull, wait_short(bar_piece(i), (read / kRing) & 1, abort_flag, p.wait_limit));
         if (!ok)
             return false;
         pc = ring[i];
@@ -453,11 +432,11 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
                 int blk = block_at(pc.a), blk1 = block_at(pc.a + 1);
                 for (int t = pc.a; t < pc.b && ok; ++t) {
                     const int blk2 = block_at(t + 2);
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part, ++u) {
                         const int i = u % C::kSlots;
                         if (u >= C::kSlots)
-                            ok = wait_bar(bar_empty(i), (u / C::kSlots - 1) & 1, abort_flag, p.wait_limit);
+                            ok = wait_short(bar_empty(i), (u / C::kSlots - 1) & 1, abort_flag, p.wait_limit);
                         ok = __all_sync(kFull, ok);
                         if (!ok)
                             break;
@@ -487,7 +466,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             }
             // every copy issued lands before the CTA exits
             for (int t = u > C::kSlots ? u - C::kSlots : 0; t < u; ++t)
-                wait_bar(bar_full(t % C::kSlots), (t / C::kSlots) & 1, nullptr, kDrainLimit);
+                wait_short(bar_full(t % C::kSlots), (t / C::kSlots) & 1, nullptr, kDrainLimit);
         } else if (warp == 3) {
             // ============================================================ the pieces, and their Q tiles
             WindowWalk walk(p, blockIdx.x, gridDim.x, !aligned);
@@ -502,7 +481,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
                 if (!more)
                     pc.s = -1;
                 if (k >= kRing)
-                    ok = wait_bar(bar_piece_free(k % kRing), (k / kRing - 1) & 1, abort_flag, p.wait_limit);
+                    ok = wait_short(bar_piece_free(k % kRing), (k / kRing - 1) & 1, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 if (!ok)
                     break;
@@ -520,7 +499,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
                     if (!ok || (x ? pc.nB : pc.nA) == 0)
                         continue;
                     if (used[x] > 0)
-                        ok = wait_bar(bar_qfree(x), (used[x] - 1) & 1, abort_flag, p.wait_limit);
+                        ok = wait_short(bar_qfree(x), (used[x] - 1) & 1, abort_flag, p.wait_limit);
                     ok = __all_sync(kFull, ok);
                     if (ok && lane == 0) {
                         int j0, i0;
@@ -541,7 +520,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             }
             for (int x = 0; x < 2; ++x)
                 if (used[x] > 0)
-                    wait_bar(bar_q(x), (used[x] - 1) & 1, nullptr, kDrainLimit);
+                    wait_short(bar_q(x), (used[x] - 1) & 1, nullptr, kDrainLimit);
         } else if (warp <= 2) {
             // ============================================================ products of row tile x
             constexpr uint32_t idesc_qk = FP8 ? idesc_e4m3_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
@@ -558,7 +537,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             int mine = 0, pieces = 0;                // this row tile's key tiles and pieces so far
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 if (ok)
-                    ok = wait_bar(bar, parity, abort_flag, p.wait_limit);
+                    ok = wait_short(bar, parity, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 return ok;
             };
@@ -643,7 +622,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             }
             // every product completes before TMEM is freed and shared memory is left
             mma_commit_warp(bar_drain(x));
-            wait_bar(bar_drain(x), 0, nullptr, kDrainLimit);
+            wait_short(bar_drain(x), 0, nullptr, kDrainLimit);
         }
         __syncwarp();
     } else if (!FP8 || warp < 12) {
@@ -662,7 +641,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
         // spill the scores.
         const int place = read % kRing;
         volatile Piece *pc = ring + place;
-        if (!__all_sync(kFull, wait_bar(bar_piece(place), (read / kRing) & 1, abort_flag, p.wait_limit))) {
+        if (!__all_sync(kFull, wait_short(bar_piece(place), (read / kRing) & 1, abort_flag, p.wait_limit))) {
             failed = true;
             break;
         }
@@ -703,7 +682,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
         float2 l2 = make_float2(0.f, 0.f);
         for (int j = 0; j < nx; ++j) {
             const int key0 = first_key + j * kKeys;
-            bool ok = wait_bar(bar_s(x), (mine + j) & 1, abort_flag, p.wait_limit);
+            bool ok = wait_short(bar_s(x), (mine + j) & 1, abort_flag, p.wait_limit);
             ok = __all_sync(kFull, ok);
             if (!ok) {
                 failed = true;
@@ -714,7 +693,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             // before either row tile multiplies it
             if (!FP8 && ((key0 < dead_hi && key0 + kKeys > dead_lo) || (end < key0 + kKeys && (end & (kPage - 1)) != 0))) {
                 const int i = u + 2 * j + 1;
-                ok = wait_bar(bar_full(i % C::kSlots), (i / C::kSlots) & 1, abort_flag, p.wait_limit);
+                ok = wait_short(bar_full(i % C::kSlots), (i / C::kSlots) & 1, abort_flag, p.wait_limit);
                 ok = __all_sync(kFull, ok);
                 const int tok = key0 + tau;
                 if (ok && ((tok >= end && tok < (end + kPage - 1) / kPage * kPage) || (tok >= dead_lo && tok < dead_hi))) {
@@ -803,6 +782,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
                     l2.x *= alpha;
                     l2.y *= alpha;
                     tmem_wait_st();
+#pragma unroll 1
                     for (int cc = 0; half > 0 && cc < 32; cc += 16) {      // the tile's probabilities so far
                         float w[16];
                         tmem_ld32<16>(ts + cc, w);
@@ -815,6 +795,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
                         }
                         tmem_st32<16>(ts + cc, w);
                     }
+#pragma unroll 1
                     for (int cc = 0; j > 0 && cc < 128; cc += 32) {        // O holds something
                         float o[32];
                         tmem_ld32<32>(to + cc, o);
@@ -852,7 +833,7 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
         const float l = l2.x + l2.y;
         const float mul = !whole ? p.v_scale : (l == 0.f ? 0.f : p.v_scale / l);
         if (nx > 0) {
-            const bool ok = wait_bar(bar_o(x), pieces & 1, abort_flag, p.wait_limit);
+            const bool ok = wait_short(bar_o(x), pieces & 1, abort_flag, p.wait_limit);
             if (!__all_sync(kFull, ok)) {
                 failed = true;
                 break;
@@ -976,9 +957,9 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
         const int end = pc.hi - pc.gap * kPage, dead_lo = p.sinks, dead_hi = pc.lo > p.sinks ? pc.lo - pc.gap * kPage : 0;
         for (int tile = pc.a; tile < pc.b; ++tile, ++v) {
             const int slot = (2 * v + 1) % C::kSlots, vb = v & 1;
-            ok = wait_bar(bar_full(slot), ((2 * v + 1) / C::kSlots) & 1, abort_flag, p.wait_limit);
+            ok = wait_short(bar_full(slot), ((2 * v + 1) / C::kSlots) & 1, abort_flag, p.wait_limit);
             if (ok && v >= 2)
-                ok = wait_bar(bar_vempty(vb), ((v >> 1) - 1) & 1, abort_flag, p.wait_limit);
+                ok = wait_short(bar_vempty(vb), ((v >> 1) - 1) & 1, abort_flag, p.wait_limit);
             ok = __all_sync(kFull, ok);
             if (!ok)
                 break;
