@@ -690,25 +690,28 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             }
             tc_fence_after();
             // page rows that no row of the unit sees may hold anything, and 0 * NaN would reach O: their V becomes zeros,
-            // before either row tile multiplies it
-            if (!FP8 && ((key0 < dead_hi && key0 + kKeys > dead_lo) || (end < key0 + kKeys && (end & (kPage - 1)) != 0))) {
-                const int i = u + 2 * j + 1;
-                ok = wait_short(bar_full(i % C::kSlots), (i / C::kSlots) & 1, abort_flag, p.wait_limit);
-                ok = __all_sync(kFull, ok);
+            // before either row tile multiplies it (the fence is below, when the stores are long done)
+            bool zeroed = false;
+            if constexpr (!FP8) {
                 const int tok = key0 + tau;
-                if (ok && ((tok >= end && tok < (end + kPage - 1) / kPage * kPage) || (tok >= dead_lo && tok < dead_hi))) {
-                    uint8_t *row = smem + i % C::kSlots * C::kSlotBytes + (tau >> 3) * C::kGroupBytes +
-                                   (tau & 7) * 128;
-#pragma unroll 1
-                    for (int cc = 0; cc < C::kGroupBytes / 128; ++cc)
-                        *reinterpret_cast<uint4 *>(row + (cc >> 3) * 1024 + (cc & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                const bool dead = (tok >= end && tok < (end + kPage - 1) / kPage * kPage) || (tok >= dead_lo && tok < dead_hi);
+                zeroed = __any_sync(kFull, dead);
+                if (zeroed) {
+                    const int i = u + 2 * j + 1;
+                    ok = __all_sync(kFull, wait_short(bar_full(i % C::kSlots), (i / C::kSlots) & 1, abort_flag,
+                                                      p.wait_limit));
+                    if (!ok) {
+                        failed = true;
+                        break;
+                    }
+                    uint8_t *row = smem + i % C::kSlots * C::kSlotBytes + (tau >> 3) * C::kGroupBytes + (tau & 7) * 128;
+                    if (dead) {
+#pragma unroll 4
+                        for (int cc = 0; cc < 16; ++cc)
+                            *reinterpret_cast<uint4 *>(row + (cc >> 3) * 1024 + (cc & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
                 }
-                fence_proxy_async_smem();
-                if (!ok) {
-                    *abort_flag = 1;                               // the other roles' waits end with it
-                    atomicOr(p.status, SK_DEV_TIMEOUT);
-                }
-                __syncwarp();
             }
             // Half of the columns after the other: scores, probabilities, their sum.  P goes over the first columns of its
             // half of S.  A row's reference need not follow its maximum while the probabilities stay well inside their
@@ -814,6 +817,8 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             if (!anchored)
                 anchored = !__any_sync(kFull, m_ref == -CUDART_INF_F && limit > 0);
             tmem_wait_st();
+            if (zeroed)
+                fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
