@@ -40,6 +40,7 @@ __all__ = [
 
 SK_OK = 0
 SK_CACHED = 1
+SK_ERR_CAPACITY = -2
 SK_ERR_TIMEOUT = -5
 SK_KV_BF16 = 0
 SK_KV_FP8_E4M3 = 1
@@ -526,9 +527,36 @@ def sk_rope_axes_and_cache(q, key, value, positions, freqs, axes, slot_mapping, 
     of a wider buffer will do); ``axes``: uint8 [rot_dim / 2] (sk_rope_axes).  ``pos_pages`` receives the position on
     axis 0.  The other arguments as there."""
     import torch
+    bf, f64 = torch.bfloat16, torch.float64
     dev = q.get_device()
-    head, tail = _rope_args(q, key, value, freqs, slot_mapping, kv_pages, q_out, interleaved, attn_factor, k_scale,
-                            v_scale, acc_pages, pos_pages, dev)
+    # in one expression where all is well (a decode step's call is short); else _rope_args finds what is wrong
+    if (q.dtype is bf and q.dim() == 3 and key.dtype is bf and key.dim() == 3 and value.dtype is bf
+            and value.shape == key.shape and key.get_device() == dev and value.get_device() == dev
+            and kv_pages.dim() == 4 and kv_pages.is_contiguous() and kv_pages.get_device() == dev
+            and q_out.dtype is bf and q_out.is_contiguous() and q_out.get_device() == dev and q_out.shape == q.shape
+            and slot_mapping.dtype is torch.int64 and slot_mapping.dim() == 1 and slot_mapping.is_contiguous()
+            and slot_mapping.get_device() == dev and freqs.dtype is f64 and freqs.dim() == 1 and acc_pages is None
+            and pos_pages is None):
+        nt, hq, d = q.shape
+        hkv = key.shape[1]
+        nb, hkv2, page, d2 = kv_pages.shape
+        qs, qh, qd = q.stride()
+        ks, kh, kd = key.stride()
+        vs, vh, vd = value.stride()
+        plain = (qd == 1 and kd == 1 and vd == 1 and qh == d and kh == d and vh == d and nt > 0 and d2 == 2 * d
+                 and hkv2 == hkv and key.shape[0] == nt and key.shape[2] == d and slot_mapping.shape[0] == nt)
+    else:
+        plain = False
+    if plain:
+        dt = SK_KV_BF16 if kv_pages.dtype is bf else _kv_dtype(kv_pages)
+        if nt == 1:                                  # a stride that nothing steps over may be anything
+            qs, ks, vs = max(qs, hq * d), max(ks, hkv * d), max(vs, hkv * d)
+        head = (q.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs)
+        tail = (2 * freqs.shape[0], 1 if interleaved else 0, attn_factor, slot_mapping.data_ptr(), nt, hq, hkv, d,
+                q_out.data_ptr(), kv_pages.data_ptr(), dt, k_scale, v_scale, nb, page, None, None)
+    else:
+        head, tail = _rope_args(q, key, value, freqs, slot_mapping, kv_pages, q_out, interleaved, attn_factor, k_scale,
+                                v_scale, acc_pages, pos_pages, dev)
     nt = q.shape[0]
     if positions.dtype is not torch.int64 or positions.dim() != 2 or positions.shape[1] != nt:
         raise ValueError(f"positions must be int64 [num_axes, {nt}], is {positions.dtype} {tuple(positions.shape)}")
@@ -538,10 +566,9 @@ def sk_rope_axes_and_cache(q, key, value, positions, freqs, axes, slot_mapping, 
         raise ValueError(f"positions must have contiguous rows, has strides {positions.stride()}")
     if positions.get_device() != dev:
         raise ValueError(f"positions must be a CUDA tensor on the device of the other arguments, is on {positions.device}")
-    return _launch(dev, stream, "sk_rope_axes_and_cache", lib().sk_rope_axes_and_cache, *head, positions.data_ptr(),
-                   max(stride, nt) if num_axes == 1 else stride, num_axes,
-                   _fits(freqs, torch.float64, freqs.shape, "freqs", dev),
-                   _fits(axes, torch.uint8, freqs.shape, "axes", dev), *tail)
+    return _launch(dev, stream, "sk_rope_axes_and_cache", (_lib or lib()).sk_rope_axes_and_cache, *head,
+                   positions.data_ptr(), max(stride, nt) if num_axes == 1 else stride, num_axes,
+                   _fits(freqs, f64, freqs.shape, "freqs", dev), _fits(axes, torch.uint8, freqs.shape, "axes", dev), *tail)
 
 
 def _batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q):
@@ -665,6 +692,79 @@ def sk_window_workspace_bytes(num_tokens: int, num_q_heads: int, num_kv_heads: i
                   "sk_window_workspace_bytes")
 
 
+def _window(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, fresh, window, sinks, max_q_len, sm_scale,
+            max_seq_len, k_scale, v_scale, workspace, stream):
+    """The call behind sk_paged_window_attn; with ``fresh``, outputs that are None are made.  A decode step's call is as short as
+    its kernels, so the arguments are checked in one expression (_batch finds what is wrong with them), and the library is
+    asked for the size of the workspace only where there is none or it has turned out too small."""
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = q.get_device()
+    if not (q.dtype is bf and q.dim() == 3 and q.is_contiguous() and kv_pages.dim() == 4 and kv_pages.is_contiguous()
+            and kv_pages.get_device() == dev and block_table.dim() == 2 and block_table.dtype is i32
+            and block_table.is_contiguous() and block_table.get_device() == dev and seq_lens.dim() == 1
+            and seq_lens.dtype is i32 and seq_lens.is_contiguous() and seq_lens.get_device() == dev
+            and cu_seqlens_q.dim() == 1 and cu_seqlens_q.dtype is i32 and cu_seqlens_q.is_contiguous()
+            and cu_seqlens_q.get_device() == dev):
+        _batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
+    nt, hq, d = q.shape
+    nb, hkv, page, d2 = kv_pages.shape
+    rows, stride = block_table.shape
+    bs = seq_lens.shape[0]
+    if d2 != 2 * d or hkv < 1 or hq % hkv or rows < bs or cu_seqlens_q.shape[0] != bs + 1:
+        _check_batch(q, kv_pages, block_table, seq_lens, cu_seqlens_q)
+    dt = SK_KV_BF16 if kv_pages.dtype is bf else _kv_dtype(kv_pages)
+    if out is not None:
+        po = _fits(out, bf, (nt, hq, d), "out", dev)
+    if lse is not None:
+        pl = _fits(lse, torch.float32, (nt, hq), "lse", dev)
+    if dev < 0:
+        raise ValueError("sk_paged_window_attn: the arguments must be CUDA tensors")
+    if torch._C._cuda_getDevice() != dev:            # streams and the status word are per device
+        with torch.cuda.device(dev):
+            return _window(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, fresh, window, sinks, max_q_len,
+                           sm_scale, max_seq_len, k_scale, v_scale, workspace, stream)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not fresh:
+        if lse is None:
+            pl = None
+    elif stream is None:
+        if out is None:
+            out = torch.empty_like(q)
+            po = out.data_ptr()
+        if lse is None:
+            lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
+            pl = lse.data_ptr()
+    elif out is None or lse is None:
+        with _owned_by(stream, q.device):
+            out = torch.empty_like(q) if out is None else out
+            lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device) if lse is None else lse
+        po, pl = out.data_ptr(), lse.data_ptr()
+    ws = workspace if workspace is not None else {}
+    buf = ws.get("window")
+    if buf is None or buf.get_device() != dev or raw not in ws["window_streams"]:
+        _buffer(ws, "window", sk_window_workspace_bytes(nt, hq, hkv, max_q_len, dt), q.device, stream)
+        buf = ws["window"]
+    f = (_lib or lib()).sk_paged_window_attn
+    while True:
+        rc = f(q.data_ptr(), kv_pages.data_ptr(), dt, k_scale, v_scale, block_table.data_ptr(), stride, nb, page,
+               seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), bs, nt, max_q_len, hq, hkv, d, sm_scale, window, sinks,
+               stride * page if max_seq_len is None else max_seq_len, buf.data_ptr(), buf.numel(), po, pl, raw)
+        if rc != SK_ERR_CAPACITY:
+            break
+        need = sk_window_workspace_bytes(nt, hq, hkv, max_q_len, dt)
+        if buf.numel() >= need:
+            break
+        _buffer(ws, "window", need, q.device, stream)
+        buf = ws["window"]
+    if rc < 0:
+        _check(rc, "sk_paged_window_attn")
+    return out, lse
+
+
 def sk_paged_window_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse=None, *, window: int,
                          sinks: int = 0, max_q_len: int, sm_scale: float, max_seq_len: Optional[int] = None,
                          k_scale: float = 1.0, v_scale: float = 1.0, workspace=None, stream=None) -> int:
@@ -672,23 +772,11 @@ def sk_paged_window_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, 
     ``sinks`` ones, into ``out`` (bf16 [num_tokens, num_q_heads, 128]) and ``lse`` (fp32 [num_tokens, num_q_heads], or
     None); for decode and verify steps as for chunks.  Block table entries of pages that no token of the call sees are
     not looked at.  ``max_seq_len`` and ``workspace`` as for sk_paged_prefill_attn."""
-    import torch
-    dev, pq, pp, dt, pb, ps, pc, nt, hq, d, nb, hkv, page, bs, stride = _batch(q, kv_pages, block_table, seq_lens,
-                                                                               cu_seqlens_q)
-    po = _fits(out, torch.bfloat16, (nt, hq, d), "out", dev)
-    pl = None if lse is None else _fits(lse, torch.float32, (nt, hq), "lse", dev)
-    buf, need = None, 0
-    if dev >= 0:
-        if torch.cuda.current_device() == dev:
-            need = sk_window_workspace_bytes(nt, hq, hkv, max_q_len, dt)
-        else:
-            with torch.cuda.device(dev):
-                need = sk_window_workspace_bytes(nt, hq, hkv, max_q_len, dt)
-        if need:
-            buf = _buffer(workspace if workspace is not None else {}, "window", need, q.device, stream)
-    return _launch(dev, stream, "sk_paged_window_attn", lib().sk_paged_window_attn, pq, pp, dt, k_scale, v_scale, pb,
-                   stride, nb, page, ps, pc, bs, nt, max_q_len, hq, hkv, d, sm_scale, window, sinks,
-                   stride * page if max_seq_len is None else max_seq_len, buf, need, po, pl)
+    if out is None:
+        raise ValueError("out is required")
+    _window(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, False, window, sinks, max_q_len, sm_scale,
+            max_seq_len, k_scale, v_scale, workspace, stream)
+    return SK_OK
 
 
 def paged_window_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *, window: int, sinks: int = 0,
@@ -696,18 +784,8 @@ def paged_window_attention(q, kv_pages, block_table, seq_lens, cu_seqlens_q, *, 
                            v_scale: float = 1.0, workspace=None, out=None, lse=None, stream=None):
     """One call of attention with a sliding window and sinks (decode and verify steps, prompts, chunks of prompts);
     arguments as sk_paged_window_attn.  Returns (out bf16 [NT, H_q, 128], lse fp32 [NT, H_q])."""
-    import torch
-    nt, hq, d = q.shape
-    if out is None or lse is None:
-        with _owned_by(stream, q.device):
-            if out is None:
-                out = torch.empty((nt, hq, d), dtype=torch.bfloat16, device=q.device)
-            if lse is None:
-                lse = torch.empty((nt, hq), dtype=torch.float32, device=q.device)
-    sk_paged_window_attn(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, window=window, sinks=sinks,
-                         max_q_len=max_q_len, sm_scale=sm_scale, max_seq_len=max_seq_len, k_scale=k_scale,
-                         v_scale=v_scale, workspace=workspace, stream=stream)
-    return out, lse
+    return _window(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, True, window, sinks, max_q_len, sm_scale,
+                   max_seq_len, k_scale, v_scale, workspace, stream)
 
 
 def sk_accum_workspace_bytes(num_tokens: int, num_q_heads: int, num_kv_heads: int, max_q_len: int, kv_dtype: int) -> int:

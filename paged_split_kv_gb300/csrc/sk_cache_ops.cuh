@@ -79,6 +79,7 @@ struct WindowParams {
     ChunkPiece *units;           // ... or of a chunk
     int sink_pages;
     int rows, inv_G, small;      // step: rows of a partial state; 2^16 / G, rounded up; the runs are found by a warp
+    int split;                   // step: CTAs that share a unit, as a cluster; 0: runs of the batch
     const float *q_scale;        // chunk, e4m3 pages: 2^-e of each row of the split Q
     int gb, tpb, nsub;           // chunk: heads and tokens of a row tile, row tiles per token
     int deal, shift;             // chunk: whole units are dealt first; costs are in 2^shift keys

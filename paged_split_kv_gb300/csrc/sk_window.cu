@@ -5,10 +5,11 @@
 //     S = scale Q K^T over the keys p <= P with p < sinks or p > P - window,   O = softmax(S) V,   lse = log sum exp S
 //
 // Bound by HBM: 512 bytes of K and V (256 for e4m3 pages) per key, once.  A window bounds what a unit, one (sequence, KV
-// head), can cost, so that no plan of segments is needed: the batch's key tiles (128 keys: eight pages, the sinks' first,
-// then those from the page with the first row that the window of the first token holds) stand in one line, unit after
-// unit, and each CTA, one per SM, takes an equal run of it.  Inside its run a CTA goes from unit to unit without a pause;
-// what several runs have of a unit is joined by a second kernel.
+// head), can cost, so that no plan of segments is needed.  The batch's key tiles (128 keys: eight pages, the sinks' first,
+// then those from the page with the first row that the window of the first token holds) stand in one line, unit after unit,
+// and each CTA, one per SM, takes an equal run of it.  Inside its run a CTA goes from unit to unit without a pause; what
+// several runs have of a unit is joined by a second kernel.  A batch of few units is divided otherwise: a unit has a
+// cluster of CTAs, as many as fit, which share its key tiles and join their states through shared memory.
 //
 // The products take the keys as M, so that nothing but the padding of the rows to 16, 32 or 64 is wasted:
 //     S^T[128 keys x R] = K Q^T,   O^T[128 dimensions x R] += V^T P^T
@@ -32,6 +33,8 @@
 #include <limits.h>
 #include <math_constants.h>
 #include <stdint.h>
+
+#include <array>
 
 #include "sk_attn_util.cuh"
 #include "sk_cache_ops.cuh"
@@ -67,6 +70,7 @@ struct WCfg {
     static constexpr int kStages = (kMaxSmem - 2 * kQBytes - 2 * kV16Bytes - kMisc) / kStageBytes;
     static constexpr int kOffV16 = kStages * kStageBytes;
     static constexpr int kOffQ = kOffV16 + 2 * kV16Bytes;
+    static constexpr int kOffSums = kOffQ + 64 * RP;               // a cluster's part: float[2][RP], past the unit's-end scratch
     static constexpr int kOffMisc = kOffQ + 2 * kQBytes;
     static constexpr int kSmemBytes = kOffMisc + kMisc;
     // TMEM columns: S buffers (even and odd tiles in turn), then O of the even and of the odd tiles
@@ -99,7 +103,8 @@ struct WCfg {
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kFound = (kAbort + 4 + 7) / 8 * 8;        // where the run starts
     static constexpr int kPieces = (kFound + 16 + 15) / 16 * 16;   // WindowPiece[kRing]
-    static constexpr int kNeg = kPieces + 48 * kRing;              // float[2][RP] minus the reference of a group's rows (log2)
+    static constexpr int kUnit = kPieces + 48 * kRing;             // WindowPiece: the cluster's unit
+    static constexpr int kNeg = kUnit + 48;                  // float[2][RP] minus the reference of a group's rows (log2)
     static constexpr int kDelta = kNeg + 8 * RP;                   // float[2][RP] what it changes by
     static constexpr int kAlpha = kDelta + 8 * RP;                 // float[2][RP] 2^delta; float2[2][RP / 2] at a unit's end
     static constexpr int kScale = kAlpha + 8 * RP;                 // float[2][RP] e4m3: score scale of a Q buffer's rows
@@ -257,6 +262,19 @@ __device__ __forceinline__ Run small_run(const WindowParams &p, int index, int c
     return r;
 }
 
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Shared memory of CTA `rank` of the cluster at the address that `local` has in this one.
+__device__ __forceinline__ uint32_t of_rank(uint32_t local, int rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+    return a;
+}
+
 template <int RP, bool FP8>
 __global__ void __launch_bounds__(WCfg<RP, FP8>::kThreads, 1)
 window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParams p)
@@ -306,7 +324,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
         atomicOr(p.status, SK_DEV_BAD_SEQ);
     // A large batch's runs are found by the whole CTA, in the stages' memory, before the first copy; else warp 0 finds its own.
     Run run{0, 0, 0, p.bs};
-    if (!p.small)
+    if (!p.small && p.split == 0)
         run = find_run<C::kThreads>(p.bs, blockIdx.x, gridDim.x, 0, 0, reinterpret_cast<long long *>(smem),
                                     reinterpret_cast<long long *>(misc + C::kFound), [&](int s) {
                                         const Seq q = sequence(p, s);
@@ -351,12 +369,12 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             // ============================================================ the pieces and their pages
             if (lane == 0)
                 prefetch_tensormap(&kv_map);
-            if (p.small)
+            if (p.small && p.split == 0)
                 run = small_run(p, blockIdx.x, gridDim.x);
             if (!aligned)
                 run.s = p.bs;                            // nothing is done
             Piece *shared = p.shared + 2 * blockIdx.x;   // this run's pieces of units that others have a part of
-            if (lane < 2)
+            if (lane < 2 && p.split == 0)
                 shared[lane].s = -1;
             __syncwarp();
             Seq q;
@@ -365,7 +383,27 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             // The next piece, published; its s is -1 at the run's end (and after a wait that gave up).
             auto next = [&]() {
                 bool more = false;
-                while (s < p.bs && off < run.hi) {
+                if (p.split > 0 && h < 0) {              // this CTA's part of its cluster's unit, once
+                    const uint32_t unit = blockIdx.x / (uint32_t)p.split, rank = blockIdx.x - unit * p.split;
+                    s = unit / (uint32_t)p.H_kv;
+                    h = unit - s * p.H_kv;
+                    q = sequence(p, s);
+                    pc.s = s;
+                    pc.h = h;
+                    pc.L = q.L;
+                    pc.q_len = q.q_len;
+                    pc.tok0 = q.tok0;
+                    pc.gap = q.gap;
+                    pc.t = q.q_len > 0 ? q.t : 0;
+                    // the first ranks have one tile more where they do not come out even
+                    const int each = (uint32_t)pc.t / (uint32_t)p.split, rest = pc.t - each * p.split;
+                    pc.a = rank * each + min((int)rank, rest);
+                    pc.b = pc.a + each + ((int)rank < rest ? 1 : 0);
+                    if (lane == 0)
+                        *reinterpret_cast<Piece *>(misc + C::kUnit) = pc;
+                    more = aligned && (pc.a < pc.b || (pc.t == 0 && rank == 0 && q.q_len > 0));
+                }
+                while (p.split == 0 && s < p.bs && off < run.hi) {
                     if (h < 0) {
                         q = sequence(p, s);
                         h = 0;
@@ -410,7 +448,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 ++count;
                 if (lane == 0) {
                     ring[i] = pc;
-                    if (more && pc.b - pc.a < pc.t)
+                    if (more && pc.b - pc.a < pc.t && p.split == 0)
                         shared[pc.a > 0 ? 0 : 1] = pc;
                     mbar_arrive(bar(C::kBarPiece, i));
                 }
@@ -424,9 +462,9 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                 return v < x.b * kPagesPerTile && pg * kPage < x.L
                            ? __ldg(p.block_table + (long long)x.s * p.bt_stride + pg) : -1;
             };
-            next();
             int u = 0;                                   // tiles so far
-            int blocks = pc.s >= 0 ? blocks_at(pc, pc.a) : -1;
+            int blocks = -1;
+            pc = Piece{};                                // begins with a piece of no tiles
             while (ok && pc.s >= 0) {
                 // the piece after this one is found, and its first blocks are read, once the first copies are out
                 const Piece now = pc;
@@ -786,7 +824,12 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             constexpr int kHalf = RP / 2;
             const int r0 = g * kHalf;
             float2 *weight = reinterpret_cast<float2 *>(misc + C::kAlpha) + r0;
+            // where a part of a unit goes: a cluster's to the stages' memory once the last product is complete, its sums to
+            // that of its Q
             const int part = (2 * blockIdx.x + (pc.a > 0 ? 0 : 1)) * RP;
+            float *part_o = p.split > 0 ? reinterpret_cast<float *>(smem) : p.part_o + (long long)part * kHeadDim;
+            float *part_m = p.split > 0 ? reinterpret_cast<float *>(smem + C::kOffSums) : p.part_m + part;
+            float *part_l = p.split > 0 ? part_m + RP : p.part_l + part;
             auto out_row = [&](int r) { return unit_row(p, pc, r); };
             if (n > 0) {
                 float *red = reinterpret_cast<float *>(smem + C::kOffQ + (pieces & 1) * C::kQBytes);     // [2][4][RP]
@@ -817,8 +860,8 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                     weight[tau] = make_float2(w0 * mul, w1 * mul);
                     if (r < R) {
                         if (!whole) {
-                            p.part_m[part + r] = M;
-                            p.part_l[part + r] = sum;
+                            part_m[r] = M;
+                            part_l[r] = sum;
                         } else if (p.lse != nullptr) {
                             p.lse[out_row(r)] = sum == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(sum);
                         }
@@ -864,7 +907,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                                     *reinterpret_cast<uint2 *>(p.out + out_row(r) * kHeadDim + dim) =
                                         make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
                                 else
-                                    *reinterpret_cast<float4 *>(p.part_o + (long long)(part + r) * kHeadDim + dim) = y;
+                                    *reinterpret_cast<float4 *>(part_o + r * kHeadDim + dim) = y;
                             }
                         }
                     }
@@ -891,6 +934,53 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
         }
         if (failed)
             give_up();
+        if (p.split > 1) {
+            // the cluster's parts of its unit, in key order: this CTA joins the rows of its rank, a warp a row
+            __syncwarp();
+            cluster_sync();
+            const Piece unit = *reinterpret_cast<const Piece *>(misc + C::kUnit);
+            const int R = p.G * unit.q_len, rank = blockIdx.x % (uint32_t)p.split, parts = min(p.split, unit.t);
+            for (int r = rank + p.split * (warp - 4); unit.t > 1 && r < R; r += p.split * 8) {
+                float M = -CUDART_INF_F, lam = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int k0 = 0; k0 < parts; k0 += 4) {
+                    float m[4], l[4];
+                    float4 o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t base = of_rank(sbase, min(k0 + k, parts - 1));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m[k]) : "r"(base + C::kOffSums + r * 4));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l[k]) : "r"(base + C::kOffSums + RP * 4 + r * 4));
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(o[k].x), "=f"(o[k].y), "=f"(o[k].z), "=f"(o[k].w)
+                                     : "r"(base + r * 512 + lane * 16));
+                        l[k] = k0 + k < parts ? l[k] : 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (l[k] == 0.f)
+                            continue;
+                        const float mn = fmaxf(M, m[k]), wa = M == -CUDART_INF_F ? 0.f : exp2f(M - mn),
+                                    wb = exp2f(m[k] - mn);
+                        M = mn;
+                        lam = lam * wa + l[k] * wb;
+                        acc.x = acc.x * wa + o[k].x * wb;
+                        acc.y = acc.y * wa + o[k].y * wb;
+                        acc.z = acc.z * wa + o[k].z * wb;
+                        acc.w = acc.w * wa + o[k].w * wb;
+                    }
+                }
+                const float inv = lam == 0.f ? 0.f : 1.f / lam;
+                const long long row = unit_row(p, unit, r);
+                *reinterpret_cast<uint2 *>(p.out + row * kHeadDim + lane * 4) =
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                if (lane == 0 && p.lse != nullptr)
+                    p.lse[row] = lam == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(lam);
+            }
+            __syncwarp();
+            cluster_sync();                                        // the others have read this CTA's memory
+        }
     } else {
         // ================================================================ e4m3: V codes to f16 (exact)
         reg_dec<C::kRegsConvert>();
@@ -976,6 +1066,11 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             give_up();
     }
 
+    if (p.split > 1 && (warp < 4 || warp >= 12)) {                 // (the softmax warps' two are above)
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -1043,11 +1138,15 @@ __global__ void __launch_bounds__(32 * kJoinRows) window_join_kernel(const Windo
         p.lse[row] = lam == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(lam);
 }
 
+constexpr int kMaxSplit = 8;                         // CTAs of a cluster
+constexpr int kJoinTiles = 5;                        // what the join kernel costs, in key tiles of a CTA
+
 template <int RP, bool FP8>
-cudaError_t launch_t(const CUtensorMap &kv_map, const WindowParams &p, int runs, cudaStream_t stream)
+cudaError_t launch_t(const CUtensorMap &kv_map, WindowParams p, long long tiles, int num_sms, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(window_step_kernel<RP, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               WCfg<RP, FP8>::kSmemBytes);
+    using C = WCfg<RP, FP8>;
+    const auto kernel = window_step_kernel<RP, FP8>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess)
         return e;
     // the warpgroups' shares after the reallocation may not exceed what the CTA was launched with
@@ -1055,10 +1154,52 @@ cudaError_t launch_t(const CUtensorMap &kv_map, const WindowParams &p, int runs,
         cudaFuncAttributes a{};
         return cudaFuncGetAttributes(&a, window_step_kernel<RP, FP8>) == cudaSuccess ? a.numRegs : 0;
     }();
-    if (regs < WCfg<RP, FP8>::kRegsLaunch)
+    if (regs < C::kRegsLaunch)
         return cudaErrorInvalidConfiguration;
-    return launch_pdl(window_step_kernel<RP, FP8>, dim3((unsigned)runs), dim3(WCfg<RP, FP8>::kThreads),
-                      WCfg<RP, FP8>::kSmemBytes, stream, kv_map, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    // clusters of each size that run at the same time (looked up once)
+    static const auto fit = [&] {
+        std::array<int, kMaxSplit + 1> n{};
+        cfg.numAttrs = 2;
+        for (int c = 2; c <= kMaxSplit; ++c) {
+            cfg.gridDim = dim3((unsigned)c);
+            attr[1].val.clusterDim.x = (unsigned)c;
+            if (cudaOccupancyMaxActiveClusters(&n[c], kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n[c] = 0;
+            }
+        }
+        return n;
+    }();
+    // Units that fit at once have a cluster each, as large as fits and as they have tiles, where that takes no longer than
+    // equal runs and their join.
+    const long long units = (long long)p.bs * p.H_kv;
+    long long runs = units * (tiles < 1 ? 1 : tiles);
+    runs = runs < num_sms ? runs : num_sms;
+    p.split = units <= runs ? 1 : 0;
+    for (int c = 2; p.split > 0 && c <= kMaxSplit && c <= tiles; ++c)
+        if (fit[c] >= units)
+            p.split = c;
+    if (p.split > 0 && (tiles + p.split - 1) / p.split > units * tiles / runs + kJoinTiles)
+        p.split = 0;
+    const unsigned grid = (unsigned)(p.split > 0 ? units * p.split : runs);
+    cfg.gridDim = dim3(grid);
+    attr[1].val.clusterDim.x = (unsigned)(p.split > 1 ? p.split : 1);
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    const cudaError_t rc = cudaLaunchKernelEx(&cfg, kernel, kv_map, p);
+    if (rc != cudaSuccess || p.split > 0)
+        return rc;
+    return launch_pdl(window_join_kernel, dim3(grid, (unsigned)((p.G * p.max_q_len + kJoinRows - 1) / kJoinRows)),
+                      dim3(32 * kJoinRows), 0, stream, p);
 }
 
 int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -1089,24 +1230,15 @@ cudaError_t launch_window_step(const WindowParams &params, int kv_dtype, long lo
     cudaError_t e = encode_page_map(&kv_map, p.kv, p.num_blocks, p.H_kv, fp8, fp8 ? 2 : 4);
     if (e != cudaSuccess)
         return e;
-    // a run per SM, but none without a key tile on average
     const long long most = (long long)p.sink_pages * kPage + p.window + p.max_q_len + kPage;
     const long long keys = max_seq_len < most ? max_seq_len : most;
     const long long tiles = (keys + kKeys - 1) / kKeys;
-    const long long units = (long long)(p.bs < p.num_tokens ? p.bs : p.num_tokens) * p.H_kv;
     p.inv_G = (65536 + p.G - 1) / p.G;               // r / G = r * inv_G >> 16 for the rows r < 64
     p.small = p.bs <= 32 * kSmall && (long long)p.bs * p.H_kv * (most / kKeys + 1 + kUnitFixed) + num_sms < INT_MAX;
-    long long runs = units * (tiles < 1 ? 1 : tiles);
-    runs = runs < 1 ? 1 : (runs < num_sms ? runs : num_sms);
-    runs = runs < kMaxRuns ? runs : kMaxRuns;
     auto launch = p.rows == 16 ? (fp8 ? launch_t<16, true> : launch_t<16, false>)
                   : p.rows == 32 ? (fp8 ? launch_t<32, true> : launch_t<32, false>)
                                  : (fp8 ? launch_t<64, true> : launch_t<64, false>);
-    e = launch(kv_map, p, (int)runs, stream);
-    if (e != cudaSuccess || runs == 1)
-        return e;
-    return launch_pdl(window_join_kernel, dim3((unsigned)runs, (unsigned)((p.G * p.max_q_len + kJoinRows - 1) / kJoinRows)),
-                      dim3(32 * kJoinRows), 0, stream, p);
+    return launch(kv_map, p, tiles, num_sms < kMaxRuns ? num_sms : kMaxRuns, stream);
 }
 
 }  // namespace sk
