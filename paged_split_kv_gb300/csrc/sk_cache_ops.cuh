@@ -55,7 +55,8 @@ struct WindowPiece {
     int s, h, L, q_len, tok0;
     int t, a, b;
     int gap;                     // pages between the sinks and the window
-    int pad[3];
+    int first;                   // of a unit that starts in another run: that run
+    int pad[2];
 };
 
 // Windowed attention, resolved on the host.

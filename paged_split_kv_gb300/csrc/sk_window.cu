@@ -198,15 +198,15 @@ __device__ __forceinline__ int split_q_half_row(uint4 raw, uint2 &hi, uint2 &lo)
     return e;
 }
 
-// min(a / b, most) for a >= 0 and 0 < b < 2^24 (a division of 64 bits takes a thousand cycles).
-__device__ __forceinline__ int quotient(long long a, int b, int most)
+// min(a / b, most) for a >= 0, b > 0 and most < 2^24 (a division of 64 bits takes a thousand cycles).
+__device__ __forceinline__ int quotient(long long a, long long b, int most)
 {
-    if (a >= (long long)b * most)
+    if (a >= b * most)
         return most;
     int x = (int)__fdividef((float)a, (float)b);     // within 2^-22 of the quotient, which is below 2^24
-    while ((long long)x * b > a)
+    while (x * b > a)
         --x;
-    while ((long long)(x + 1) * b <= a)
+    while ((x + 1) * b <= a)
         ++x;
     return x;
 }
@@ -377,6 +377,8 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             if (lane < 2 && p.split == 0)
                 shared[lane].s = -1;
             __syncwarp();
+            // equal shares: all runs are as long as the ones before this, or as this
+            const long long share = blockIdx.x > 0 ? run.lo / blockIdx.x : run.hi;
             Seq q;
             int s = run.s, h = -1, count = 0;
             long long off = run.before;                  // where sequence s starts
@@ -433,6 +435,7 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                     pc.b = (int)max(0LL, min((long long)q.t, run.hi - first));
                     // a unit without keys belongs to the run that it starts in
                     more = pc.a < pc.b || (q.t == 0 && start >= run.lo);
+                    pc.first = more && pc.a > 0 ? quotient(first, share, blockIdx.x) : blockIdx.x;
                     if (more)
                         break;
                 }
@@ -1080,30 +1083,22 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
 }
 
 // Joins the pieces of the units that several runs share: block `index` those of the unit whose last piece is that run's
-// first, four rows of them, one a warp.  In key order, whatever the timing: with M = max m_i over the pieces with l_i > 0,
+// first, four rows of them, one a warp.  The unit's other pieces are the first ones of the runs before, and the last one of the
+// run that it starts in.  In key order, whatever the timing: with M = max m_i over the pieces with l_i > 0,
 //     out = sum o_i 2^(m_i - M) / sum l_i 2^(m_i - M)
 constexpr int kJoinRows = 4;                         // rows (warps) of a block
 constexpr int kMaxRuns = 1024;                       // runs (SMs) at most
 
 __global__ void __launch_bounds__(32 * kJoinRows) window_join_kernel(const WindowParams p)
 {
-    __shared__ int slots[kMaxRuns], count;
     wait_prior_grid();
     const int index = blockIdx.x;
     const Piece pc = p.shared[2 * index];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * kJoinRows + warp, R = p.G * pc.q_len;
-    if (pc.s < 0 || pc.b != pc.t || (int)blockIdx.y * kJoinRows >= R)
+    const int r = blockIdx.y * kJoinRows + warp;
+    if (pc.s < 0 || pc.b != pc.t || r >= p.G * pc.q_len)
         return;
-    if (warp == 0) {
-        const int n = shared_slots(index, [&](int slot) { return p.shared[slot].s >= 0; }, slots);
-        if (lane == 0)
-            count = n;
-    }
-    __syncthreads();
-    if (r >= R)
-        return;
-    const int pieces = count;
+    const int pieces = index - pc.first + 1;
     float M = -CUDART_INF_F, lam = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kAtOnce = 8;
@@ -1112,7 +1107,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) window_join_kernel(const Windo
         float4 o[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const long long slot = (long long)slots[max(pieces - 1 - g0 - i, 0)] * p.rows + r;
+            const int run = pc.first + min(g0 + i, pieces - 1);
+            const long long slot = (2LL * run + (run == pc.first ? 1 : 0)) * p.rows + r;
             m[i] = __ldg(p.part_m + slot);
             l[i] = g0 + i < pieces ? __ldg(p.part_l + slot) : 0.f;
             o[i] = __ldg(reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim) + lane);
