@@ -58,7 +58,8 @@ struct WCfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
     // registers per thread after the reallocation; no more in all than at launch (4 x 128, or 3 x 168)
     static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-    static constexpr int kRegsIssue = FP8 ? 56 : 72, kRegsSoftmax = FP8 ? 200 : 216, kRegsConvert = 56;
+    static constexpr int kRegsIssue = FP8 ? 56 : 72, kRegsSoftmax = !FP8 ? 216 : RP == 64 ? 192 : 176,
+                         kRegsConvert = RP == 64 ? 72 : 104;
     static_assert(kRegsIssue + 2 * kRegsSoftmax + (FP8 ? kRegsConvert : 0) <= kThreads / 128 * kRegsLaunch, "registers");
     static constexpr int kGroupBytes = FP8 ? 2048 : 4096;          // 8 tokens as copied: 128-byte chunks of K, then of V
     static constexpr int kPageBytes = 2 * kGroupBytes;
@@ -988,10 +989,19 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
         // ================================================================ e4m3: V codes to f16 (exact)
         reg_dec<C::kRegsConvert>();
         const int w = warp - 12;
-        // a warp's load is four keys' 128 codes, 16 a lane; key t's unit lies at unit ^ (t % 8) in its row.  The 16
-        // dimensions become units 2 unit and 2 unit + 1 of f16, the upper half of the lanes storing the odd one first, so
-        // that a store's lanes meet no bank twice
-        const int unit = lane & 7, sub = lane >> 3;
+        // A warp has 32 keys of a tile, in eight loads of four keys' 128 codes, 16 a lane; all are under way before the first
+        // is converted (one at a time, a tile took 2000 cycles and was what the kernel waited for).  Key t's unit lies at
+        // unit ^ (t % 8) in its row.  The 16 dimensions become units 2 unit and 2 unit + 1 of f16, the upper half of the lanes
+        // storing the odd one first, so that a store's lanes meet no bank twice.
+        const int unit = lane & 7, sub = lane >> 3, one = (2 * unit & 7) + (unit >> 2);
+        int from[2], to[2][2];                                     // of the keys with t % 8 = sub and 4 + sub
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int x8 = 4 * e + sub;
+            from[e] = C::kOffV + w * 4 * C::kGroupBytes + x8 * 128 + ((unit ^ x8) << 4);
+            to[e][0] = C::kOffV16 + w * 4 * 2048 + (unit >> 2) * 1024 + x8 * 128 + ((one ^ x8) << 4);
+            to[e][1] = C::kOffV16 + w * 4 * 2048 + (unit >> 2) * 1024 + x8 * 128 + ((one ^ 1 ^ x8) << 4);
+        }
         int u = 0, copied = 0;
         while (ok && next_piece(pc, ok)) {
             if (pc.a == pc.b)
@@ -1032,7 +1042,9 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar(C::kBarQ, buf));
-            const int lo = max(0, pc.L - pc.q_len + 1 - p.window);
+            // keys as numbered without the gap: those from the sinks to dead_hi and from end on are no token's
+            const int lo = max(0, pc.L - pc.q_len + 1 - p.window), end = pc.L - pc.gap * kPage;
+            const int dead_hi = lo > p.sinks ? lo - pc.gap * kPage : 0;
             for (int t = pc.a; t < pc.b; ++t, ++u) {
                 const int st = u % C::kStages, vb = u & 1;
                 ok = wait(bar(C::kBarFull, st), (u / C::kStages) & 1);
@@ -1040,24 +1052,29 @@ window_step_kernel(const __grid_constant__ CUtensorMap kv_map, const WindowParam
                     ok = wait(bar(C::kBarVFree, vb), ((u >> 1) - 1) & 1);
                 if (!ok)
                     break;
-                const uint8_t *src = smem + st * C::kStageBytes + C::kOffV;
-                uint8_t *dst = smem + C::kOffV16 + vb * C::kV16Bytes;
+                const uint8_t *src = smem + st * C::kStageBytes;
+                uint8_t *dst = smem + vb * C::kV16Bytes;
+                uint4 a[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    a[k] = *reinterpret_cast<const uint4 *>(src + from[k & 1] + (k >> 1) * C::kGroupBytes);
+                // rows that no token sees may hold anything
+                if ((t + 1) * kKeys > end || (t * kKeys < dead_hi && (t + 1) * kKeys > p.sinks)) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int vk = t * kKeys + w * 32 + k * 4 + sub;
+                        if (vk >= end || (vk >= p.sinks && vk < dead_hi))
+                            a[k] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int i = w * 32 + k * 4 + sub, x8 = i & 7;
-                    uint4 a = *reinterpret_cast<const uint4 *>(src + (i >> 3) * C::kGroupBytes + x8 * 128 +
-                                                               ((unit ^ x8) << 4));
-                    const int vk = t * kKeys + i, key = vk >= p.sink_pages * kPage ? vk + pc.gap * kPage : vk;
-                    if (key >= pc.L || (key >= p.sinks && key < lo))        // such rows may hold anything
-                        a = make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 lo16 = make_uint4(f16x2_of_e4m3(a.x), f16x2_of_e4m3(a.x >> 16), f16x2_of_e4m3(a.y),
-                                                  f16x2_of_e4m3(a.y >> 16));
-                    const uint4 hi16 = make_uint4(f16x2_of_e4m3(a.z), f16x2_of_e4m3(a.z >> 16), f16x2_of_e4m3(a.w),
-                                                  f16x2_of_e4m3(a.w >> 16));
-                    uint8_t *row = dst + (i >> 3) * 2048 + (unit >> 2) * 1024 + x8 * 128;
-                    const int one = (2 * unit & 7) + (unit >> 2), two = one ^ 1;
-                    *reinterpret_cast<uint4 *>(row + ((one ^ x8) << 4)) = unit >> 2 ? hi16 : lo16;
-                    *reinterpret_cast<uint4 *>(row + ((two ^ x8) << 4)) = unit >> 2 ? lo16 : hi16;
+                    const uint4 lo16 = make_uint4(f16x2_of_e4m3(a[k].x), f16x2_of_e4m3(a[k].x >> 16),
+                                                  f16x2_of_e4m3(a[k].y), f16x2_of_e4m3(a[k].y >> 16));
+                    const uint4 hi16 = make_uint4(f16x2_of_e4m3(a[k].z), f16x2_of_e4m3(a[k].z >> 16),
+                                                  f16x2_of_e4m3(a[k].w), f16x2_of_e4m3(a[k].w >> 16));
+                    *reinterpret_cast<uint4 *>(dst + to[k & 1][0] + (k >> 1) * 2048) = unit >> 2 ? hi16 : lo16;
+                    *reinterpret_cast<uint4 *>(dst + to[k & 1][1] + (k >> 1) * 2048) = unit >> 2 ? lo16 : hi16;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
