@@ -578,12 +578,19 @@ static int rope_call(const char *name, const void *q, const void *key, const voi
         rc = sm_count(&sms);
     if (rc != SK_OK)
         return rc;
-    cudaError_t e = launch_rope_cache(static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(key),
-                                      static_cast<const uint16_t *>(value), q_stride, key_stride, value_stride,
-                                      positions, freqs, slot_mapping, num_tokens, num_q_heads, num_kv_heads, rot_dim,
-                                      interleaved ? 1 : 0, attn_factor, static_cast<uint16_t *>(q_out), kv_pages,
-                                      kv_dtype, k_scale, v_scale, num_blocks, acc_pages, pos_pages, axes,
-                                      pos_stride, num_axes, status, sms, static_cast<cudaStream_t>(stream));
+    const auto *qp = static_cast<const uint16_t *>(q), *kp = static_cast<const uint16_t *>(key),
+               *vp = static_cast<const uint16_t *>(value);
+    auto *qo = static_cast<uint16_t *>(q_out);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int inter = interleaved ? 1 : 0;
+    const cudaError_t e =
+        axes == nullptr
+            ? launch_rope_cache(qp, kp, vp, q_stride, key_stride, value_stride, positions, freqs, slot_mapping, num_tokens,
+                                num_q_heads, num_kv_heads, rot_dim, inter, attn_factor, qo, kv_pages, kv_dtype, k_scale,
+                                v_scale, num_blocks, acc_pages, pos_pages, status, sms, st)
+            : launch_rope_axes(qp, kp, vp, q_stride, key_stride, value_stride, positions, pos_stride, num_axes, freqs,
+                               axes, slot_mapping, num_tokens, num_q_heads, num_kv_heads, rot_dim, inter, attn_factor, qo,
+                               kv_pages, kv_dtype, k_scale, v_scale, num_blocks, acc_pages, pos_pages, status, sms, st);
     if (e != cudaSuccess)
         return cuda_fail(e, "rope kernel launch");
     return SK_OK;

@@ -127,8 +127,14 @@ cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16
                               long long k_stride, long long v_stride, const int64_t *pos, const double *freqs,
                               const int64_t *slots, int num_tokens, int hq, int hkv, int rot, int interleaved,
                               float factor, uint16_t *q_out, void *pages, int kv_dtype, float k_scale, float v_scale,
-                              long long num_blocks, float *acc, int32_t *pos_pages, const uint8_t *axes,
-                              long long pos_stride, int num_axes, int *status, int num_sms, cudaStream_t stream);
+                              long long num_blocks, float *acc, int32_t *pos_pages, int *status, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_rope_axes(const uint16_t *q, const uint16_t *k, const uint16_t *v, long long q_stride,
+                             long long k_stride, long long v_stride, const int64_t *pos, long long pos_stride, int num_axes,
+                             const double *freqs, const uint8_t *axes, const int64_t *slots, int num_tokens, int hq,
+                             int hkv, int rot, int interleaved, float factor, uint16_t *q_out, void *pages, int kv_dtype,
+                             float k_scale, float v_scale, long long num_blocks, float *acc, int32_t *pos_pages,
+                             int *status, int num_sms, cudaStream_t stream);
 cudaError_t launch_evict_select(const float *acc, const int32_t *pos, const int32_t *block_table, int bt_stride,
                                 int num_blocks, const int32_t *seq_lens, const int32_t *next_pos, int bs, int hkv,
                                 int budget, int recent, int max_len, int cap, int32_t *src, int32_t *dst,

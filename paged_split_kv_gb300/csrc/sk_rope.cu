@@ -3,8 +3,7 @@
 // A pair (a, b) of a head's first rot_dim elements -- (2i, 2i + 1) interleaved, (i, i + rot_dim / 2)
 // in halves -- turns by pos * freqs[i]:
 //     a' = f (a cos - b sin),  b' = f (b cos + a sin)
-// with f the attention factor of a long-context scaling.  With several axes (time, height, width of image and video
-// patches) pos is the token's position on the pair's axis.  Elements past rot_dim pass through.  q goes to
+// with f the attention factor of a long-context scaling.  Elements past rot_dim pass through.  q goes to
 // q_out; k, turned, and v go to the page row of the token's slot (the row layout and the e4m3 rounding of
 // sk_reshape_and_cache, except that k is rounded once, from its turned fp32 value).
 //
@@ -21,8 +20,6 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "sk_cache_ops.cuh"
 #include "sk_quant.cuh"
 
@@ -38,9 +35,6 @@ struct RopeArgs {
     long long q_stride, k_stride, v_stride;      // elements between tokens
     const int64_t *pos, *slots;
     const double *freqs;
-    const uint8_t *axes;                         // AXES: pair i turns by the position at pos + axes[i] * pos_stride
-    long long pos_stride;
-    int num_axes;
     uint16_t *q_out;
     void *pages;
     float *acc;
@@ -51,7 +45,7 @@ struct RopeArgs {
     float factor, k_scale, v_scale;
 };
 
-template <bool FP8, bool RECIP, bool INTER, bool AXES>
+template <bool FP8, bool RECIP, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a)
 {
     __shared__ float2 turn[2][kHeadDim / 2];     // (cos, sin) of the token's angles, two tokens deep
@@ -69,23 +63,9 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a)
         rev -= floor(rev);
         step = (uint64_t)(rev * 18446744073709551616.0);
     }
-    const int64_t *own_pos = a.pos;              // the positions that turn pair `tid`
-    if constexpr (AXES) {
-        if (tid < half) {
-            const int axis = __ldg(a.axes + tid);
-            if (axis < a.num_axes) {
-                own_pos += axis * a.pos_stride;
-            } else {                             // no such axis: the pair stays as it is
-                step = 0;
-                if (blockIdx.x == 0)
-                    atomicOr(a.status, SK_DEV_BAD_SEQ);
-            }
-        }
-    }
     int buf = 0;
     for (int t = blockIdx.x; t < a.num_tokens; t += gridDim.x, buf ^= 1) {
         const long long pos = __ldg(a.pos + t);
-        const long long turn_pos = AXES && tid < half ? __ldg(own_pos + t) : pos;
         const long long slot = __ldg(a.slots + t);
         const bool bad = slot >= a.num_slots;
         const bool stored = slot >= 0 && !bad;
@@ -108,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const RopeArgs a)
             }
             if (r0 == 0) {
                 if (tid < half) {
-                    const uint64_t phase = (uint64_t)turn_pos * step;
+                    const uint64_t phase = (uint64_t)pos * step;
                     float s, c;
                     sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
                     turn[buf][tid] = make_float2(c * a.factor, s * a.factor);
@@ -199,24 +179,19 @@ cudaError_t launch_rope_cache(const uint16_t *q, const uint16_t *k, const uint16
                               long long k_stride, long long v_stride, const int64_t *pos, const double *freqs,
                               const int64_t *slots, int num_tokens, int hq, int hkv, int rot, int interleaved,
                               float factor, uint16_t *q_out, void *pages, int kv_dtype, float k_scale, float v_scale,
-                              long long num_blocks, float *acc, int32_t *pos_pages, const uint8_t *axes,
-                              long long pos_stride, int num_axes, int *status, int num_sms, cudaStream_t stream)
+                              long long num_blocks, float *acc, int32_t *pos_pages, int *status, int num_sms,
+                              cudaStream_t stream)
 {
-    RopeArgs a{q, k, v, q_stride, k_stride, v_stride, pos, slots, freqs, axes, pos_stride, num_axes, q_out, pages, acc,
-               pos_pages, status, num_blocks * kPage, num_tokens, hq, hkv, rot, factor, k_scale, v_scale};
+    RopeArgs a{q, k, v, q_stride, k_stride, v_stride, pos, slots, freqs, q_out, pages, acc, pos_pages, status,
+               num_blocks * kPage, num_tokens, hq, hkv, rot, factor, k_scale, v_scale};
     const int cap = num_sms * 8;                 // 8 CTAs of 256 threads per SM
     const dim3 grid((unsigned)(num_tokens < cap ? num_tokens : cap));
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
     const bool recip = fp8 && exact_reciprocal(k_scale) && exact_reciprocal(v_scale);
-    auto pick = [&](auto inter, auto by_axes) {
-        constexpr bool I = decltype(inter)::value, A = decltype(by_axes)::value;
-        return !fp8 ? rope_cache_kernel<false, false, I, A>
-                    : recip ? rope_cache_kernel<true, true, I, A> : rope_cache_kernel<true, false, I, A>;
-    };
-    using T = std::true_type;
-    using F = std::false_type;
-    auto kernel = axes != nullptr ? (interleaved ? pick(T{}, T{}) : pick(F{}, T{}))
-                                  : (interleaved ? pick(T{}, F{}) : pick(F{}, F{}));
+    auto kernel = interleaved ? (!fp8 ? rope_cache_kernel<false, false, true>
+                                 : recip ? rope_cache_kernel<true, true, true> : rope_cache_kernel<true, false, true>)
+                              : (!fp8 ? rope_cache_kernel<false, false, false>
+                                 : recip ? rope_cache_kernel<true, true, false> : rope_cache_kernel<true, false, false>);
     return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a);
 }
 
