@@ -53,7 +53,7 @@ struct CCfg {
     // registers per thread after the reallocation: copies and products, softmax, e4m3's conversion of V; no more in all
     // than at launch (4 x 128, or 3 x 168)
     static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-    static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoftmax = FP8 ? 208 : 216, kRegsConvert = 32;
+    static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoftmax = FP8 ? 184 : 216, kRegsConvert = 80;
     static_assert(kRegsIssue + 2 * kRegsSoftmax + (FP8 ? kRegsConvert : 0) <= kThreads / 128 * kRegsLaunch, "registers");
     static constexpr int kQTile = kRows * 256;                     // bf16: two 64-dimension chunks; e4m3: hi and lo
     static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K (or V) of 8 tokens, as copied
@@ -951,15 +951,23 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
         // ================================================================ e4m3: V codes to f16 (exact)
         reg_dec<C::kRegsConvert>();
         const int w = warp - 12;
-        // a warp's load is four tokens' 128 codes, 16 a lane; token t's unit u lies at u ^ (t % 8) in its row.  The 16
-        // dimensions become units 2 u and 2 u + 1 of f16, the upper half of the lanes storing the odd one first, so
-        // that a store's lanes meet no bank twice
-        const int u = lane & 7, sub = lane >> 3;
+        // A warp has 32 tokens of a tile, in eight loads of four tokens' 128 codes, 16 a lane; all are under way before the
+        // first is converted.  Token t's unit u lies at u ^ (t % 8) in its row.  The 16 dimensions become units 2 u and 2 u + 1
+        // of f16, the upper half of the lanes storing the odd one first, so that a store's lanes meet no bank twice.
+        const int u = lane & 7, sub = lane >> 3, first = (2 * u & 7) + (u >> 2);
+        int from[2], to[2][2];                                     // of the tokens with t % 8 = sub and 4 + sub
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int x8 = 4 * e + sub;
+            from[e] = w * 4 * 1024 + x8 * 128 + ((u ^ x8) << 4);
+            to[e][0] = C::kOffV + w * 4 * 2048 + (u >> 2) * 1024 + x8 * 128 + ((first ^ x8) << 4);
+            to[e][1] = C::kOffV + w * 4 * 2048 + (u >> 2) * 1024 + x8 * 128 + ((first ^ 1 ^ x8) << 4);
+        }
         int v = 0;                                                 // key tiles so far
         bool ok = true;
         while (ok && next_piece(pc, ok)) {
         // rows that no row of the unit sees, as above
-        const int end = pc.hi - pc.gap * kPage, dead_lo = p.sinks, dead_hi = pc.lo > p.sinks ? pc.lo - pc.gap * kPage : 0;
+        const int end = pc.hi - pc.gap * kPage, dead_hi = pc.lo > p.sinks ? pc.lo - pc.gap * kPage : 0;
         for (int tile = pc.a; tile < pc.b; ++tile, ++v) {
             const int slot = (2 * v + 1) % C::kSlots, vb = v & 1;
             ok = wait_short(bar_full(slot), ((2 * v + 1) / C::kSlots) & 1, abort_flag, p.wait_limit);
@@ -969,22 +977,28 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             if (!ok)
                 break;
             const uint8_t *src = smem + slot * C::kSlotBytes;
-            uint8_t *dst = smem + C::kOffV + vb * C::kVBytes;
-            const int key0 = tile * kKeys;
+            uint8_t *dst = smem + vb * C::kVBytes;
+            uint4 a[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                a[k] = *reinterpret_cast<const uint4 *>(src + from[k & 1] + (k >> 1) * 1024);
+            // rows that no token sees may hold anything
+            if ((tile + 1) * kKeys > end || (tile * kKeys < dead_hi && (tile + 1) * kKeys > p.sinks)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int vk = tile * kKeys + w * 32 + k * 4 + sub;
+                    if (vk >= end || (vk >= p.sinks && vk < dead_hi))
+                        a[k] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const int t = w * 32 + k * 4 + sub, x8 = t & 7;
-                uint4 a = *reinterpret_cast<const uint4 *>(src + (t >> 3) * 1024 + x8 * 128 + ((u ^ x8) << 4));
-                if (key0 + t >= end || (key0 + t >= dead_lo && key0 + t < dead_hi))
-                    a = make_uint4(0u, 0u, 0u, 0u);                 // such rows may hold anything
-                const uint4 lo = make_uint4(f16x2_of_e4m3(a.x), f16x2_of_e4m3(a.x >> 16), f16x2_of_e4m3(a.y),
-                                            f16x2_of_e4m3(a.y >> 16));
-                const uint4 hi = make_uint4(f16x2_of_e4m3(a.z), f16x2_of_e4m3(a.z >> 16), f16x2_of_e4m3(a.w),
-                                            f16x2_of_e4m3(a.w >> 16));
-                uint8_t *row = dst + (t >> 3) * 2048 + (u >> 2) * 1024 + x8 * 128;
-                const int first = (2 * u & 7) + (u >> 2), second = first ^ 1;
-                *reinterpret_cast<uint4 *>(row + ((first ^ x8) << 4)) = u >> 2 ? hi : lo;
-                *reinterpret_cast<uint4 *>(row + ((second ^ x8) << 4)) = u >> 2 ? lo : hi;
+                const uint4 lo = make_uint4(f16x2_of_e4m3(a[k].x), f16x2_of_e4m3(a[k].x >> 16), f16x2_of_e4m3(a[k].y),
+                                            f16x2_of_e4m3(a[k].y >> 16));
+                const uint4 hi = make_uint4(f16x2_of_e4m3(a[k].z), f16x2_of_e4m3(a[k].z >> 16), f16x2_of_e4m3(a[k].w),
+                                            f16x2_of_e4m3(a[k].w >> 16));
+                *reinterpret_cast<uint4 *>(dst + to[k & 1][0] + (k >> 1) * 2048) = u >> 2 ? hi : lo;
+                *reinterpret_cast<uint4 *>(dst + to[k & 1][1] + (k >> 1) * 2048) = u >> 2 ? lo : hi;
             }
             fence_proxy_async_smem();
             __syncwarp();
