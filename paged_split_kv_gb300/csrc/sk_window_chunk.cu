@@ -139,7 +139,7 @@ struct WindowWalk {
     int lo, hi;                                      // this CTA's run of the cost; of the units left over, a unit costs `count`
     int deal, dealt;                                 // next unit dealt, and how many units are dealt in all
     int s, h, unit;                                  // cursor of the run
-    bool left_over;
+    bool left_over, falls;                           // `falls`: some offset of the queries is below the one before
 
     __device__ __forceinline__ int before(int i) const
     {
@@ -158,6 +158,7 @@ struct WindowWalk {
                          (long long)L > (long long)p.bt_stride * kPage;
         if (bad)
             atomicOr(p.status, SK_DEV_BAD_SEQ);
+        falls |= end < tok0;
         q_len = bad ? 0 : end - tok0;
         units = at < p.bs ? ((q_len + p.tpb - 1) / p.tpb * p.nsub + 1) / 2 : 0;
         // later units see more keys, unless a token has several row tiles
@@ -190,7 +191,7 @@ struct WindowWalk {
     }
     __device__ WindowWalk(const WindowParams &pp, int index, int runs, bool none)
         : p(pp), lane(threadIdx.x & 31), count(runs), units_before(0), cost_before(0), lo(0), hi(0), deal(index), dealt(0),
-          s(0), h(0), unit(0), left_over(false)
+          s(0), h(0), unit(0), left_over(false), falls(false)
     {
         int total = 0, all = 0, largest = 0;
 #pragma unroll 1
@@ -200,7 +201,8 @@ struct WindowWalk {
             all += of(units_to, 31);
             largest = max(largest, __reduce_max_sync(kFull, units > 0 ? (units <= rising ? base + step * units : top) : 0));
         }
-        if (none)
+        // offsets that fall may give the same tokens to many sequences: more cost than the tokens come to
+        if (none || (!p.bounded && __any_sync(kFull, falls)))
             return;
         if (p.deal && ((float)largest * (float)all <= 1.4f * (float)total ||
                        (float)largest * (float)count * 8.f <= (float)total)) {
@@ -1180,6 +1182,7 @@ cudaError_t launch_window_chunk(const WindowParams &params, int kv_dtype, long l
     runs = runs < kMaxRuns ? runs : kMaxRuns;
     for (p.shift = 4; (units * (kUnitFixed + most) >> p.shift) >> 30; )      // costs below 2^30 in all
         ++p.shift;
+    p.bounded = (double)per_seq * p.H_kv * (kUnitFixed + (double)most) < (double)(1 << 30);
     p.deal = (double)p.bs * keys * p.H_kv * (fp8 ? 256 : 512) > kL2Share ? 1 : 0;
     e = fp8 ? launch_t<true>(kv_map, q_map, out_map, p, (int)runs, stream)
             : launch_t<false>(kv_map, q_map, out_map, p, (int)runs, stream);
