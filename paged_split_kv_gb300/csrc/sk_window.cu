@@ -219,47 +219,28 @@ __device__ __forceinline__ long long unit_row(const WindowParams &p, const Piece
     return (long long)(pc.tok0 + j) * p.H_q + pc.h * p.G + (r - j * p.G);
 }
 
-// The run of CTA `index` of `count` for a batch of at most 32 * kSmall sequences and a cost below 2^31; called by a warp.
-constexpr int kSmall = 4;
-
+// The run of CTA `index` of `count` for a batch of at most 32 sequences and a cost below 2^31; called by a warp.  (The whole
+// CTA's search, with its barriers before the first copy, takes 0.4 us longer for 40 sequences, and 0.6 less for 100 than a
+// warp's, 32 at a time.)
 __device__ __forceinline__ Run small_run(const WindowParams &p, int index, int count)
 {
     const int lane = threadIdx.x & 31;
-    auto cost = [&](int s0) {                        // of sequence s0 + lane
-        const Seq q = sequence(p, min(s0 + lane, p.bs - 1));
-        return s0 + lane < p.bs && q.q_len > 0 ? p.H_kv * (q.t + kUnitFixed) : 0;
-    };
-    int mine = cost(0), total = __reduce_add_sync(kFull, mine);
-#pragma unroll 1
-    for (int s0 = 32; s0 < p.bs; s0 += 32)
-        total += __reduce_add_sync(kFull, cost(s0));
-    Run r;
-    const int each = (total + count - 1) / count;
-    r.lo = min((long long)total, (long long)each * index);
-    r.hi = min((long long)total, (long long)each * (index + 1));
-    r.before = 0;
-    r.s = p.bs;
-    if (r.lo >= r.hi)
-        return r;
-    int before = 0, s0 = 0;
-#pragma unroll 1
-    while (true) {                                   // the sequence that lo lies in
-        const int here = __reduce_add_sync(kFull, mine);
-        if (r.lo < before + here)
-            break;
-        before += here;
-        s0 += 32;
-        mine = cost(s0);
-    }
-    int incl = mine;
+    const Seq q = sequence(p, min(lane, p.bs - 1));
+    const int mine = lane < p.bs && q.q_len > 0 ? p.H_kv * (q.t + kUnitFixed) : 0;
+    int upto = mine;                                 // of the sequences up to this lane's
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kFull, incl, o);
-        incl += lane >= o ? x : 0;
+        const int x = __shfl_up_sync(kFull, upto, o);
+        upto += lane >= o ? x : 0;
     }
-    const int src = __ffs(__ballot_sync(kFull, r.lo < before + incl)) - 1;
-    r.s = s0 + src;
-    r.before = before + __shfl_sync(kFull, incl - mine, src);
+    const int total = __shfl_sync(kFull, upto, 31), each = (total + count - 1) / count;
+    Run r;
+    r.lo = min((long long)total, (long long)each * index);
+    r.hi = min((long long)total, (long long)each * (index + 1));
+    const uint32_t past = __ballot_sync(kFull, r.lo < upto);
+    const int src = past ? __ffs(past) - 1 : 0;      // the sequence that lo lies in
+    r.s = past ? src : p.bs;
+    r.before = __shfl_sync(kFull, upto - mine, src);
     return r;
 }
 
@@ -1152,7 +1133,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) window_join_kernel(const Windo
 }
 
 constexpr int kMaxSplit = 8;                         // CTAs of a cluster
-constexpr int kJoinTiles = 5;                        // what the join kernel costs, in key tiles of a CTA
+constexpr int kJoinTiles = 7;                        // what the join kernel costs, in key tiles of a CTA: 96 units of 9 tiles take
+                                                     // 11.9 us as clusters (of one) and 15.2 as runs, of 17 tiles 20.1 and 21.2
 
 template <int RP, bool FP8>
 cudaError_t launch_t(const CUtensorMap &kv_map, WindowParams p, long long tiles, int num_sms, cudaStream_t stream)
@@ -1219,6 +1201,9 @@ int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 }  // namespace
 
+// Rows of a (sequence, KV head) up to which this kernel is the faster one: for 64 rows it takes 17.0 us where the chunk kernel
+// takes 27.4 (64 units of each of two heads over a window of 1024), 99.7 against 111.9 over 8192, on e4m3 pages 76.6 against
+// 106.5; it has no room for more.
 bool window_step_takes(long long rows) { return rows <= 64; }
 
 // Two pieces of the padded rows (o, m, l) per run, with what they are pieces of.
@@ -1247,7 +1232,7 @@ cudaError_t launch_window_step(const WindowParams &params, int kv_dtype, long lo
     const long long keys = max_seq_len < most ? max_seq_len : most;
     const long long tiles = (keys + kKeys - 1) / kKeys;
     p.inv_G = (65536 + p.G - 1) / p.G;               // r / G = r * inv_G >> 16 for the rows r < 64
-    p.small = p.bs <= 32 * kSmall && (long long)p.bs * p.H_kv * (most / kKeys + 1 + kUnitFixed) + num_sms < INT_MAX;
+    p.small = p.bs <= 32 && (long long)p.bs * p.H_kv * (most / kKeys + 1 + kUnitFixed) + num_sms < INT_MAX;
     auto launch = p.rows == 16 ? (fp8 ? launch_t<16, true> : launch_t<16, false>)
                   : p.rows == 32 ? (fp8 ? launch_t<32, true> : launch_t<32, false>)
                                  : (fp8 ? launch_t<64, true> : launch_t<64, false>);
