@@ -301,7 +301,11 @@ int sk_paged_prefill_attn(const void *q, const void *kv_pages, int kv_dtype, flo
  * server may hand them back and leave anything there.  They are the whole pages between row sinks and row
  * seq_lens[s] - q_s + 1 - window.  Rows in pages that are read, but that no token of the call sees, may hold anything as
  * well.  The rule on a NaN or an infinity in V that sk_paged_prefill_attn gives holds for rows that only some
- * tokens of the call see.
+ * tokens of the call see.  Where cu_seqlens_q falls somewhere, which sets SK_DEV_BAD_SEQ, the sequences whose offsets are in
+ * order are worked on all the same, or, in a large batch, none is.
+ *
+ * Up to 64 query rows of a (sequence, KV head), max_q_len * num_q_heads / num_kv_heads, are a step's: its cost is divided by
+ * key tiles over the SMs, or, for few sequences, each (sequence, KV head) has a cluster of CTAs.  More are a chunk's.
  *
  * workspace (device, 16-byte aligned): sk_window_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, max_q_len,
  * kv_dtype) bytes.  max_seq_len as for sk_paged_prefill_attn.  Asynchronous on `stream`, no allocation, capture safe.
@@ -518,7 +522,8 @@ int sk_get_device_status(void *stream, int clear);
 int sk_last_device_status(void);
 
 /* Limit, in SM clock cycles, of each wait of the attention kernels (decode and
- * verify, chunk attention, attention weights) that can give up (for a copy to
+ * verify, chunk attention, windowed attention, whose limit is at most the
+ * default, attention weights) that can give up (for a copy to
  * land, a product to complete, another role to finish its part of a tile).
  * It applies to the launches made after the call;
  * cycles < 0 restores the default of 4e9 (about two seconds).  Returns the
