@@ -14,11 +14,10 @@
 // lane takes two of the token's 64 angles, exchanged there too.  Warps stay for several pieces, so that the frequencies,
 // whose fractions take FP64, are converted once.
 //
-// Measured, 8191 tokens of 32 query and 8 KV heads: 33.8 us to bf16 pages (201 MB, 6.0 TB/s), 34.1 us to e4m3 pages
-// (185 MB, 5.4 TB/s); the rows of a token shared out among a CTA, with barriers and lanes that exchange partners, took 44.5
-// and 38.3.  Pieces of 8, 16 and 24 rows: 37.6 / 41.7, 33.7 / 34.4, 34.8 / 38.3 us; three stages instead of two 35.0 / 36.1;
-// three CTAs of an SM (80 registers) instead of two 37.2 / 47.2.  64 tokens: 3.1 us, of which an empty launch is about 2; with
-// CTAs of eight warps there too, on fewer SMs, 3.6.
+// Measured, 8191 tokens of 32 query and 8 KV heads: 33.3 us to bf16 pages (201 MB, 6.0 TB/s), 32.2 us to e4m3 pages
+// (185 MB, 5.7 TB/s); the rows of a token shared out among a CTA, with barriers and lanes that exchange partners, took 44.5
+// and 38.3.  Pieces of 24 rows 33.6 and 36.3, of 32 35.4 and 54.3, of 12 with three CTAs of an SM 34.3 and 40.9, of 8 32.6
+// and 44.4.  64 tokens: 2.8 us, of which an empty launch is about 2; with CTAs of eight warps there too, on fewer SMs, 3.6.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -34,7 +33,7 @@ namespace {
 constexpr int kThreads = 256;                    // at most; a warp where there is less than one for each SM
 constexpr int kPasses = 4;                       // a pass is four rows of a warp
 constexpr int kPieceRows = 4 * kPasses;          // rows of a token that a warp takes at once
-constexpr int kStages = 2;                       // pieces of a warp in shared memory
+constexpr int kStages = 2;                       // pieces of a warp in shared memory: this one and the next
 constexpr int kPieceBytes = kPieceRows * kHeadDim * 2;
 constexpr int kWarpBytes = kStages * kPieceBytes + kHeadDim / 2 * 8;     // and (cos, sin) of its token's angles
 constexpr int kCtas = 2;                         // CTAs of an SM
@@ -77,12 +76,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_axes_kernel(const AxesAr
     const bool low = part < half / 8;
     const int d0 = 8 * (low ? part : a.rot / 8 + 2 * (part - half / 8)), d1 = low ? d0 + half : d0 + 8;
     const bool turned = low;                     // of both units
-    const long long items = (long long)a.num_tokens * a.pieces, stride = (long long)gridDim.x * (blockDim.x >> 5);
-    const long long first = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
+    // The warp's pieces, every `stride`-th, by token and piece of it (with divisions of 64 bits e4m3 pages took 34.1 us).
+    const int stride = gridDim.x * (blockDim.x >> 5), first = blockIdx.x * (blockDim.x >> 5) + warp;
+    const int step_t = stride / a.pieces, step_piece = stride - step_t * a.pieces;
+    struct Item {
+        int t, piece;
+    };
+    auto after = [&](Item i) {
+        i.t += step_t;
+        i.piece += step_piece;
+        if (i.piece >= a.pieces) {
+            i.piece -= a.pieces;
+            ++i.t;
+        }
+        return i;
+    };
     // Copies of a piece's rows into stage `st`; always a group, of nothing past the end.
-    auto fetch = [&](long long item, int st) {
-        if (item < items) {
-            const int t = (int)(item / a.pieces), r0 = (int)(item - (long long)t * a.pieces) * kPieceRows + sub;
+    auto fetch = [&](Item at, int st) {
+        if (at.t < a.num_tokens) {
+            const int t = at.t, r0 = at.piece * kPieceRows + sub;
             const uint32_t dst = (uint32_t)__cvta_generic_to_shared(ring + st * kPieceBytes + sub * 256);
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
@@ -100,11 +112,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_axes_kernel(const AxesAr
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if (first >= items)
+    Item item{first / a.pieces, first % a.pieces};
+    if (item.t >= a.num_tokens)
         return;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i)
-        fetch(first + i * stride, i);
+    fetch(item, 0);
     // Pairs `lane` and `32 + lane`: revolutions per position, times 2^64, and the positions that they go by.
     uint64_t step[2] = {0, 0};
     const int64_t *own_pos[2] = {a.pos, a.pos};
@@ -127,18 +138,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_axes_kernel(const AxesAr
     struct Place {
         long long pos, slot, turn[2];
     };
-    auto place = [&](long long item) {
-        const int t = (int)((item < items ? item : items - 1) / a.pieces);
+    auto place = [&](Item at) {
+        const int t = min(at.t, a.num_tokens - 1);
         return Place{__ldg(a.pos + t), __ldg(a.slots + t), {__ldg(own_pos[0] + t), __ldg(own_pos[1] + t)}};
     };
-    Place next = place(first);
-    int st = 0;
-    for (long long item = first; item < items; item += stride, st = st + 1 == kStages ? 0 : st + 1) {
-        const int t = (int)(item / a.pieces), r0 = (int)(item - (long long)t * a.pieces) * kPieceRows + sub;
+    Place next = place(item);
+    for (int st = 0; item.t < a.num_tokens; st ^= 1) {
+        const int t = item.t, r0 = item.piece * kPieceRows + sub;
         const long long pos = next.pos, slot = next.slot, turn_pos0 = next.turn[0], turn_pos1 = next.turn[1];
         __syncwarp();                            // every lane is done with the stage that is filled now
-        fetch(item + (kStages - 1) * stride, st == 0 ? kStages - 1 : st - 1);
-        next = place(item + stride);
+        item = after(item);
+        fetch(item, st ^ 1);
+        next = place(item);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (32 * i + lane < half) {
@@ -148,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_axes_kernel(const AxesAr
                 turn[32 * i + lane] = make_float2(c * a.factor, s * a.factor);
             }
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         // of this lane's pairs: eight in halves, four of each unit interleaved
         float2 cs[8];
