@@ -748,6 +748,8 @@ def _window(q, kv_pages, block_table, seq_lens, cu_seqlens_q, out, lse, fresh, w
     if buf is None or buf.get_device() != dev or raw not in ws["window_streams"]:
         _buffer(ws, "window", sk_window_workspace_bytes(nt, hq, hkv, max_q_len, dt), q.device, stream)
         buf = ws["window"]
+    # more is all of a sequence as well; ctypes would take them modulo 2^32
+    window, sinks = max(-1, min(window, 0x7FFFFFFF)), max(-1, min(sinks, 0x7FFFFFFF))
     f = (_lib or lib()).sk_paged_window_attn
     while True:
         rc = f(q.data_ptr(), kv_pages.data_ptr(), dt, k_scale, v_scale, block_table.data_ptr(), stride, nb, page,

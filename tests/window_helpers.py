@@ -4,6 +4,9 @@ Bounds.  Scores accumulate 128 products in fp32: at most 130 * 2^-24 * scale * s
 row, plus 2^-20 for the exponential and the sums).  Each probability rounds by at most 2^-8 (bf16; f16 for e4m3 pages)
 and the output by another 2^-8:
     |out - ref| <= 2^-8 |ref| + (2^-8 + 2 e) sum p |v|.  lse is off by e.
+On e4m3 pages q is two e4m3 terms of q 2^e, its row's largest element there in [128, 256): hi has 4 bits of an element's 8, lo the
+others exactly unless their last is below 2^-9, the type's least, so for elements of 2^-9 of the largest or less lo is off
+by up to 2^-10, which is 2^-17 of the largest.  That adds scale * 2^-17 max |q| sum |k| over those elements to e.
 f16 has a fixed half step of 2^-25 below 2^-14, and the row's largest probability is held as 2^8 or more: each probability
 of e4m3 pages may also be off by 2^-25 / 2^8 = 2^-33 of the row's sum, which adds 2^-33 sum |v| over the rows seen."""
 import math
@@ -55,8 +58,8 @@ def rows_of(b, s, h, rows, part):
     return x.double()
 
 
-def reference(b):
-    """out, lse in 64 bits and the bounds of both."""
+def reference(b, gone=()):
+    """out, lse in 64 bits and the bounds of both; keys `gone` of every sequence have the weight 0."""
     w = b["w"]
     g = w.group
     out = torch.zeros(w.num_tokens, w.num_q_heads, D, dtype=torch.float64, device=DEV)
@@ -68,12 +71,18 @@ def reference(b):
         rows = see.any(0).nonzero()[:, 0].to(DEV)
         if q == 0 or rows.numel() == 0:
             continue
-        hide = ~see.to(DEV)[:, rows]
+        drop = torch.isin(rows, torch.tensor(list(gone), dtype=torch.int64, device=DEV))
+        hide = ~see.to(DEV)[:, rows] | drop[None]
         for h in range(w.num_kv_heads):
             k, v = rows_of(b, s, h, rows, 0), rows_of(b, s, h, rows, 1)
+            k = torch.where(drop[:, None], 0.0, k)
             x = b["q"][a:a + q, h * g:(h + 1) * g].double()
             sc = torch.einsum("tgd,nd->tgn", x, k) * w.sm_scale
             e = 130 * 2.0 ** -24 * w.sm_scale * torch.einsum("tgd,nd->tgn", x.abs(), k.abs()).amax(2) + 2.0 ** -20
+            if w.kv_dtype == si.KV_FP8:
+                top = x.abs().amax(2, keepdim=True)
+                small = (x.abs() < 2.0 ** -8 * top).double()
+                e = e + w.sm_scale * 2.0 ** -17 * top[..., 0] * torch.einsum("tgd,nd->tgn", small, k.abs()).amax(2)
             sc.masked_fill_(hide[:, None, :], -math.inf)
             p = torch.nan_to_num(torch.softmax(sc, 2))
             ref, l = torch.einsum("tgn,nd->tgd", p, v), torch.logsumexp(sc, 2)
