@@ -734,30 +734,30 @@ __global__ void __launch_bounds__(kGroup * kKeys) accum_join_kernel(const AccumP
     atomicAdd(p.acc + ((long long)blk * p.H_kv + pc.h) * kPage + key % kPage, sum);
 }
 
+constexpr int kSplitPairs = 4;                       // pairs of rows of a warp, in flight together
+
 __global__ void __launch_bounds__(256) split_q_kernel(const uint16_t *__restrict__ q, long long rows,
                                                       uint8_t *__restrict__ codes, float *__restrict__ scale)
 {
     wait_prior_grid();
-    const int lane = threadIdx.x & 31;
-    constexpr int kAtOnce = 4;
-    const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kAtOnce;
-    uint2 raw[kAtOnce];
+    const int lane = threadIdx.x & 31, part = lane & 15;         // half a warp a row
+    const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (2 * kSplitPairs) + (lane >> 4);
+    uint4 raw[kSplitPairs];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-        raw[i] = r0 + i < rows ? __ldg(reinterpret_cast<const uint2 *>(q + (r0 + i) * kHeadDim) + lane)
-                               : make_uint2(0u, 0u);
+    for (int i = 0; i < kSplitPairs; ++i)
+        raw[i] = r0 + 2 * i < rows ? __ldg(reinterpret_cast<const uint4 *>(q + (r0 + 2 * i) * kHeadDim) + part)
+                                   : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-        if (r0 + i >= rows)
-            break;
-        uint32_t hi, lo;
-        int e;
-        split_q_row(raw[i], hi, lo, e);
-        uint32_t *dst = reinterpret_cast<uint32_t *>(codes + (r0 + i) * 256);
-        dst[lane] = hi;
-        dst[32 + lane] = lo;
-        if (lane == 0)
-            scale[r0 + i] = ldexpf(1.f, -e);
+    for (int i = 0; i < kSplitPairs; ++i) {
+        uint2 hi, lo;
+        const int e = split_q_half_row(raw[i], hi, lo);
+        if (r0 + 2 * i < rows) {
+            uint2 *dst = reinterpret_cast<uint2 *>(codes + (r0 + 2 * i) * 256);
+            dst[part] = hi;
+            dst[16 + part] = lo;
+            if (part == 0)
+                scale[r0 + 2 * i] = __int_as_float((127 - e) << 23);
+        }
     }
 }
 
@@ -781,7 +781,8 @@ cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const 
 cudaError_t launch_split_q(const uint16_t *q, long long rows, void *codes, cudaStream_t stream)
 {
     uint8_t *c = static_cast<uint8_t *>(codes);
-    return launch_pdl(split_q_kernel, dim3((unsigned)((rows + 31) / 32)), dim3(256), 0, stream, q, rows, c,
+    const long long block = 8 * 2 * kSplitPairs;     // rows
+    return launch_pdl(split_q_kernel, dim3((unsigned)((rows + block - 1) / block)), dim3(256), 0, stream, q, rows, c,
                       reinterpret_cast<float *>(c + rows * 256));
 }
 

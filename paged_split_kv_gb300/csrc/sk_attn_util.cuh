@@ -82,37 +82,42 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t v)
     return r;
 }
 
-// One row of Q spread over a warp (lane l: elements 4 l .. 4 l + 3, bf16) as two e4m3 terms of q * 2^e = hi + lo,
-// with the row's largest |q| * 2^e in [128, 256).  A bf16 element of at least 2^-9 of that is hi + lo exactly.
-__device__ __forceinline__ void split_q_row(uint2 raw, uint32_t &hi, uint32_t &lo, int &e)
+// Half a warp's row of Q (8 bf16 elements a lane) as two e4m3 terms of q * 2^e = hi + lo, the row's largest |q| * 2^e in
+// [128, 256); returns e.  A bf16 element of at least 2^-9 of the largest is hi + lo exactly.
+__device__ __forceinline__ int split_q_half_row(uint4 raw, uint2 &hi, uint2 &lo)
 {
-    float q[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u), __uint_as_float(raw.y << 16),
-                  __uint_as_float(raw.y & 0xFFFF0000u)};
-    float amax = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
-    for (int o = 16; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    e = 0;
-    if (amax > 0.f && amax < CUDART_INF_F) {
-        int ex;
-        frexpf(amax, &ex);                       // amax in [2^(ex-1), 2^ex)
-        e = 8 - ex;
-        e = e > 100 ? 100 : (e < -100 ? -100 : e);
-    }
-    hi = lo = 0;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float q[8], amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-        const float x0 = ldexpf(q[k], e), x1 = ldexpf(q[k + 1], e);
+    for (int k = 0; k < 4; ++k) {
+        q[2 * k] = __uint_as_float(w[k] << 16);
+        q[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        amax = fmax3(amax, fabsf(q[2 * k]), fabsf(q[2 * k + 1]));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // amax in [2^(ex - 127), 2^(ex - 126)); none for a row of zeros, and for infinities, which saturate
+    const int ex = __float_as_int(amax) >> 23;
+    const int e = amax == 0.f || ex == 255 ? 0 : max(-100, min(100, 134 - ex));
+    const float by = __int_as_float((127 + e) << 23);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float x0 = q[2 * k] * by, x1 = q[2 * k + 1] * by;
         uint16_t hc, lc;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hc) : "f"(x1), "f"(x0));
-        const uint32_t hf = f16x2_of_e4m3(hc);
         float h0, h1;
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
             : "=f"(h0), "=f"(h1)
-            : "r"(hf));
+            : "r"(f16x2_of_e4m3(hc)));
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lc) : "f"(x1 - h1), "f"(x0 - h0));
-        hi |= (uint32_t)hc << (8 * k);
-        lo |= (uint32_t)lc << (8 * k);
+        h[k] = hc;
+        l[k] = lc;
     }
+    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+    return e;
 }
 
 // Waits for the phase with the given parity like mbar_wait_bounded, in few instructions (every role waits in many places,

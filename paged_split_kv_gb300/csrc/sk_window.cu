@@ -167,44 +167,6 @@ __device__ __forceinline__ void reduce_step(float *v, int lane)
     }
 }
 
-// Half a warp's row of Q (8 bf16 elements a lane) as two e4m3 terms of q * 2^e = hi + lo, the row's largest |q| * 2^e in
-// [128, 256); returns e.  A bf16 element of at least 2^-9 of the largest is hi + lo exactly.
-__device__ __forceinline__ int split_q_half_row(uint4 raw, uint2 &hi, uint2 &lo)
-{
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float q[8], amax = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        q[2 * k] = __uint_as_float(w[k] << 16);
-        q[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        amax = fmax3(amax, fabsf(q[2 * k]), fabsf(q[2 * k + 1]));
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    // amax in [2^(ex - 127), 2^(ex - 126)); none for a row of zeros, and for infinities, which saturate
-    const int ex = __float_as_int(amax) >> 23;
-    const int e = amax == 0.f || ex == 255 ? 0 : max(-100, min(100, 134 - ex));
-    const float by = __int_as_float((127 + e) << 23);
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float x0 = q[2 * k] * by, x1 = q[2 * k + 1] * by;
-        uint16_t hc, lc;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hc) : "f"(x1), "f"(x0));
-        float h0, h1;
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-            : "=f"(h0), "=f"(h1)
-            : "r"(f16x2_of_e4m3(hc)));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lc) : "f"(x1 - h1), "f"(x0 - h0));
-        h[k] = hc;
-        l[k] = lc;
-    }
-    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
-    return e;
-}
-
 // min(a / b, most) for a >= 0, b > 0 and most < 2^24 (a division of 64 bits takes a thousand cycles).
 __device__ __forceinline__ int quotient(long long a, long long b, int most)
 {
