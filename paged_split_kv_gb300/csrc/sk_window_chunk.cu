@@ -28,7 +28,7 @@
 //
 // Measured: 4096 tokens over a window of 4096, 32/8 heads: 210 us, 1.31 PFLOP/s of the pairs that are seen.  24 prompts of up to
 // 2000 tokens over 512, 16/2 heads: 111 us; 16001 tokens over 128: 51 us; 1919 tokens of four prompts over 2048 on e4m3 pages:
-// 42 us.  A key tile takes 3050 cycles: the softmax of a row tile (1600) and its products (1024 for both of its own), one after
+// 40 us.  A key tile takes 3050 cycles: the softmax of a row tile (1600) and its products (1024 for both of its own), one after
 // the other, beside those of the other row tile; the tensor pipe is busy 57 % of the first call, 41 % of the second.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -124,7 +124,7 @@ constexpr int kUnitFixed = 128;
 // than this (4096 tokens over a window of 4096: 212 us with 768, 210 with 512; the 24 prompts 111 with 384, 110 with 640).
 constexpr int kCutFixed = 512;
 // Where units cost alike, none is cut if the longest run is then longer by this or less than if they were: 1919 tokens of e4m3
-// pages over a window of 2048, 122 units, take 42.0 us, and 46.8 cut; 168 units on the 152 SMs take 37.3 cut, and 42.8 whole.
+// pages over a window of 2048, 122 units, took 42.0 us, and 46.8 cut; 168 units on the 152 SMs take 37.3 cut, and 42.8 whole.
 constexpr int kJoinCost = 800;
 
 using Piece = ChunkPiece;
