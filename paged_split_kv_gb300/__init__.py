@@ -535,8 +535,7 @@ def sk_rope_axes_and_cache(q, key, value, positions, freqs, axes, slot_mapping, 
             and kv_pages.dim() == 4 and kv_pages.is_contiguous() and kv_pages.get_device() == dev
             and q_out.dtype is bf and q_out.is_contiguous() and q_out.get_device() == dev and q_out.shape == q.shape
             and slot_mapping.dtype is torch.int64 and slot_mapping.dim() == 1 and slot_mapping.is_contiguous()
-            and slot_mapping.get_device() == dev and freqs.dtype is f64 and freqs.dim() == 1 and acc_pages is None
-            and pos_pages is None):
+            and slot_mapping.get_device() == dev and freqs.dtype is f64 and freqs.dim() == 1):
         nt, hq, d = q.shape
         hkv = key.shape[1]
         nb, hkv2, page, d2 = kv_pages.shape
@@ -553,7 +552,9 @@ def sk_rope_axes_and_cache(q, key, value, positions, freqs, axes, slot_mapping, 
             qs, ks, vs = max(qs, hq * d), max(ks, hkv * d), max(vs, hkv * d)
         head = (q.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs)
         tail = (2 * freqs.shape[0], 1 if interleaved else 0, attn_factor, slot_mapping.data_ptr(), nt, hq, hkv, d,
-                q_out.data_ptr(), kv_pages.data_ptr(), dt, k_scale, v_scale, nb, page, None, None)
+                q_out.data_ptr(), kv_pages.data_ptr(), dt, k_scale, v_scale, nb, page,
+                None if acc_pages is None else _fits(acc_pages, torch.float32, (nb, hkv, page), "acc_pages", dev),
+                None if pos_pages is None else _fits(pos_pages, torch.int32, (nb, hkv, page), "pos_pages", dev))
     else:
         head, tail = _rope_args(q, key, value, freqs, slot_mapping, kv_pages, q_out, interleaved, attn_factor, k_scale,
                                 v_scale, acc_pages, pos_pages, dev)

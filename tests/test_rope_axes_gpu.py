@@ -176,3 +176,21 @@ def test_another_stream_and_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     check(q, k, v, slots, pages0, pages, pos, axes, freqs, q_out, False, 1.0, False, 1.0, 1.0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_slots_past_4_gb_and_2_to_the_31_elements(fp8):
+    """The same rows at the near and the far end of a cache."""
+    q, k, v, slots, pages0, pages, _, freqs = setup(70, 8, 2, 128, fp8, 1000, 11)
+    pos = positions(3, 70, 1000, 11)
+    axes = sk.sk_rope_axes(128, [16, 24, 24], device=DEV)
+    far = torch.empty((1200000 if fp8 else 600000, *pages.shape[1:]), dtype=pages.dtype, device=DEV)
+    shift = far.shape[0] - pages.shape[0]
+    far[shift:].copy_(pages)
+    out = [torch.empty((70, 8, D), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    sk.sk_rope_axes_and_cache(q, k, v, pos, freqs, axes, slots, pages, out[0], k_scale=0.5, v_scale=0.5)
+    sk.sk_rope_axes_and_cache(q, k, v, pos, freqs, axes, torch.where(slots >= 0, slots + shift * PAGE, slots), far, out[1],
+                              k_scale=0.5, v_scale=0.5)
+    assert sk.sk_get_device_status() == 0
+    assert torch.equal(out[0], out[1])
+    assert torch.equal(far[shift:].view(torch.uint8), pages.view(torch.uint8))
