@@ -12,8 +12,8 @@
 // five key tiles for a window of 512.  Its bound is the tensor cores' 4 * 128 flops per (row, key); what costs beside them is
 // a unit's start, its end, its masked tiles, and the code that these take: roles that together run through more of it than
 // the instruction cache holds stall on it (with the softmax unrolled over 128 columns and a walk with sums of 64 bits, 107 KB,
-// 2.3 warps waited for instructions for each that issued).  So the softmax takes half of a tile at a time, and the
-// shares are found and walked by one warp in 32 bits.
+// 2.3 warps waited for instructions for each that issued).  So the softmax takes half of a tile at a time, but
+// for long units, and the shares are found and walked by one warp in 32 bits.
 //
 // Roles (384 threads; 512 for e4m3 pages):
 //   warp 0      copies: K and V of a key tile apart, 32 KB (16 KB e4m3) slots, one TMA copy per page and part
@@ -26,10 +26,10 @@
 //
 // Every wait is bounded: on expiry SK_DEV_TIMEOUT is set and every role gives up, after its copies and products in flight.
 //
-// Measured: 4096 tokens over a window of 4096, 32/8 heads: 210 us, 1.31 PFLOP/s of the pairs that are seen.  24 prompts of up to
+// Measured: 4096 tokens over a window of 4096, 32/8 heads: 196 us, 1.40 PFLOP/s of the pairs that are seen.  24 prompts of up to
 // 2000 tokens over 512, 16/2 heads: 111 us; 16001 tokens over 128: 51 us; 1919 tokens of four prompts over 2048 on e4m3 pages:
 // 40 us.  A key tile takes 3050 cycles: the softmax of a row tile (1600) and its products (1024 for both of its own), one after
-// the other, beside those of the other row tile; the tensor pipe is busy 57 % of the first call, 41 % of the second.
+// the other, beside those of the other row tile; the tensor pipe is busy 61 % of the first call, 40 % of the second.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -52,13 +52,16 @@ constexpr uint32_t kDrainLimit = 4000000000u;        // cycles (~2 s): waits for
 constexpr int kMaxSmem = 232448;
 constexpr int kRing = 4;                             // pieces published ahead
 
-template <bool FP8>
+// WIDE: a tile that a warp's rows all see is taken in one go, for units of many key tiles (kWideTiles)
+template <bool FP8, bool WIDE>
 struct CCfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
     // registers per thread after the reallocation: copies and products, softmax, e4m3's conversion of V; no more in all
     // than at launch (4 x 128, or 3 x 168)
     static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-    static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoftmax = FP8 ? 184 : 216, kRegsConvert = 80;
+    static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoftmax = !FP8 ? 216 : WIDE ? 208 : 184,
+                         kRegsConvert = WIDE ? 32 : 80;
+    static constexpr int kLoads = WIDE ? 2 : 8;                    // of a tile's V, under way before the first is converted
     static_assert(kRegsIssue + 2 * kRegsSoftmax + (FP8 ? kRegsConvert : 0) <= kThreads / 128 * kRegsLaunch, "registers");
     static constexpr int kQTile = kRows * 256;                     // bf16: two 64-dimension chunks; e4m3: hi and lo
     static constexpr int kGroupBytes = FP8 ? 1024 : 2048;          // K (or V) of 8 tokens, as copied
@@ -121,11 +124,18 @@ constexpr double kL2Share = 60e6;                    // bytes of K and V that st
 // over a window of 512 took 119.4 us with 384, 117.2 with 160, 111.2 with 128, 123.5 with 32.
 constexpr int kUnitFixed = 128;
 // A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
-// than this (4096 tokens over a window of 4096: 212 us with 768, 210 with 512; the 24 prompts 111 with 384, 110 with 640).
+// than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384, 110 with 640).
 constexpr int kCutFixed = 512;
 // Where units cost alike, none is cut if the longest run is then longer by this or less than if they were: 1919 tokens of e4m3
 // pages over a window of 2048, 122 units, took 42.0 us, and 46.8 cut; 168 units on the 152 SMs take 37.3 cut, and 42.8 whole.
 constexpr int kJoinCost = 800;
+
+// Key tiles of a unit, on average, from which on a tile that a warp's rows all see is taken in one go instead of by halves.  That
+// waits for the tensor memory and votes once, but its code beside that of the masked tiles costs units that change between
+// them often.  Measured, in one go and by halves: 4096 tokens over a window of 4096 198 and 210 us (e4m3 pages 227 and 235),
+// 2048 over 8192 184 and 200 (198 and 215), two prompts of 8000 over 4096 486 and 501 (553 and 576); eight prompts of up to
+// 4000 over 4096, 16 tiles on average, 196 and 188 (238 and 230), 24 of up to 2000 over 512 121 and 111.
+constexpr int kWideTiles = 23;
 
 using Piece = ChunkPiece;
 static_assert(sizeof(Piece) == 64, "the ring holds pieces of four 16-byte words");
@@ -347,12 +357,12 @@ __device__ __forceinline__ void unpack16x2(uint32_t v, float &lo, float &hi)
     }
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(CCfg<FP8>::kThreads, 1)
+template <bool FP8, bool WIDE>
+__global__ void __launch_bounds__(CCfg<FP8, WIDE>::kThreads, 1)
 window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                     const __grid_constant__ CUtensorMap out_map, const WindowParams p)
 {
-    using C = CCfg<FP8>;
+    using C = CCfg<FP8, WIDE>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -731,106 +741,158 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
                         __syncwarp();
                     }
                 }
-                // Half of the columns after the other: scores, probabilities, their sum.  P goes over the first columns of its
-                // half of S.  A row's reference need not follow its maximum while the probabilities stay well inside their
-                // type's range, and their sum shows whether some did not: then the reference moves by whole powers of two, so that
-                // what the row has summed and stored is rescaled exactly.
+                // Scores, probabilities, their sum; P goes over the first columns of each half of S.  A row's reference need not
+                // follow its maximum while the probabilities stay well inside their type's range, and their sum shows whether some
+                // did not: then the reference moves by whole powers of two, so that what the row has summed and stored is rescaled
+                // exactly.
+                auto scale_o = [&](float alpha) {
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const int k0 = key0 + 64 * half;
-                    const uint32_t tp = ts + half * 64;
-                    float v[64];
-                    tmem_ld32<32>(tp, v);
-                    tmem_ld32<32>(tp + 32, v + 32);
-                    bool sees = true;
-                    // uniform: some row does not see all of them
-                    const bool masked = k0 + 64 > least || (k0 < high && k0 + 64 > p.sinks);
+                    for (int cc = 0; j > 0 && cc < 128; cc += 32) {        // O holds something
+                        float o[32];
+                        tmem_ld32<32>(to + cc, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] *= alpha;
+                        tmem_st32<32>(to + cc, o);
+                    }
+                };
+                if (WIDE && anchored && key0 + kKeys <= least && !(key0 < high && key0 + kKeys > p.sinks)) {
+                    float v[128];
+#pragma unroll
+                    for (int cc = 0; cc < 128; cc += 32)
+                        tmem_ld32<32>(ts + cc, v + cc);
                     tmem_wait_ld();
-                    if (masked) {
-                        const int from = low - k0, to_ = limit - k0, sk = min(p.sinks, limit) - k0;
-                        const uint32_t m0 = columns(from, to_) | columns(0, sk),
-                                       m1 = columns(from - 32, to_ - 32) | columns(0, sk - 32);
-                        sees = (m0 | m1) != 0;
-                        if (!__any_sync(kFull, sees)) {
-                            const uint32_t none[16] = {};
-                            tmem_st32_u<16>(tp, none);
-                            tmem_st32_u<16>(tp + 16, none);
-                            continue;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            v[i] = m0 & (1u << i) ? v[i] : -CUDART_INF_F;
-                            v[32 + i] = m1 & (1u << i) ? v[32 + i] : -CUDART_INF_F;
-                        }
-                    }
-                    auto largest = [&]() {
-                        float mx = fmax3(v[0], v[1], v[2]), my = v[3];
-#pragma unroll
-                        for (int i = 4; i < 64; i += 4) {
-                            mx = fmax3(mx, v[i], v[i + 1]);
-                            my = fmax3(my, v[i + 2], v[i + 3]);
-                        }
-                        return fmaxf(mx, my) * c;
-                    };
-                    // a row's first scores give it a reference
-                    if (!anchored && __any_sync(kFull, sees && m_ref == -CUDART_INF_F)) {
-                        const float top = largest() - C::kAbove;
-                        m_ref = m_ref == -CUDART_INF_F ? top : m_ref;
-                    }
                     float2 h2;
-                    uint32_t pk[32];
 #pragma unroll 1
                     for (int again = 0; again < 2; ++again) {
-                        const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-                        const float2 s2 = make_float2(-msub, -msub);
+                        const float2 s2 = make_float2(-m_ref, -m_ref);
                         float2 g2 = make_float2(0.f, 0.f);
                         h2 = g2;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float2 d = ffma2(make_float2(v[2 * i], v[2 * i + 1]), c2, s2);
-                            const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
-                            (i & 1 ? g2 : h2) = fadd2(i & 1 ? g2 : h2, e);
-                            pk[i] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int k = q * 32 + 2 * i;
+                                const float2 d = ffma2(make_float2(v[k], v[k + 1]), c2, s2);
+                                const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
+                                (i & 1 ? g2 : h2) = fadd2(i & 1 ? g2 : h2, e);
+                                pk[i] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                            }
+                            tmem_st32_u<16>(ts + (q >> 1) * 64 + (q & 1) * 16, pk);
                         }
                         h2 = fadd2(h2, g2);
                         const bool over = limit > 0 && !(h2.x + h2.y <= C::kSumMost);
                         if (again || !__any_sync(kFull, over))
                             break;
-                        // up by `by`, to kAbove below the largest score or just above it
-                        const float by = over ? fmaxf(0.f, ceilf(largest() - C::kAbove - m_ref)) : 0.f;
+                        float mx = fmax3(v[0], v[1], v[2]), my = v[3];
+#pragma unroll
+                        for (int i = 4; i < 128; i += 4) {
+                            mx = fmax3(mx, v[i], v[i + 1]);
+                            my = fmax3(my, v[i + 2], v[i + 3]);
+                        }
+                        const float by = over ? fmaxf(0.f, ceilf(fmaxf(mx, my) * c - C::kAbove - m_ref)) : 0.f;
                         const float alpha = by < 126.f ? __int_as_float((127 - (int)by) << 23) : 0.f;
                         m_ref += by;
                         l2.x *= alpha;
                         l2.y *= alpha;
                         tmem_wait_st();
-#pragma unroll 1
-                        for (int cc = 0; half > 0 && cc < 32; cc += 16) {      // the tile's probabilities so far
-                            float w[16];
-                            tmem_ld32<16>(ts + cc, w);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float a, b;
-                                unpack16x2<FP8>(__float_as_uint(w[i]), a, b);
-                                w[i] = __uint_as_float(FP8 ? pack_f16x2(a * alpha, b * alpha) : pack_bf16x2(a * alpha, b * alpha));
-                            }
-                            tmem_st32<16>(ts + cc, w);
-                        }
-#pragma unroll 1
-                        for (int cc = 0; j > 0 && cc < 128; cc += 32) {        // O holds something
-                            float o[32];
-                            tmem_ld32<32>(to + cc, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[i] *= alpha;
-                            tmem_st32<32>(to + cc, o);
-                        }
+                        scale_o(alpha);
                         tmem_wait_st();
                     }
-                    tmem_st32_u<16>(tp, pk);
-                    tmem_st32_u<16>(tp + 16, pk + 16);
                     l2 = fadd2(l2, h2);
+                } else {
+                    // half of the columns after the other
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        const int k0 = key0 + 64 * half;
+                        const uint32_t tp = ts + half * 64;
+                        float v[64];
+                        tmem_ld32<32>(tp, v);
+                        tmem_ld32<32>(tp + 32, v + 32);
+                        bool sees = true;
+                        // uniform: some row does not see all of them
+                        const bool masked = k0 + 64 > least || (k0 < high && k0 + 64 > p.sinks);
+                        tmem_wait_ld();
+                        if (masked) {
+                            const int from = low - k0, to_ = limit - k0, sk = min(p.sinks, limit) - k0;
+                            const uint32_t m0 = columns(from, to_) | columns(0, sk),
+                                           m1 = columns(from - 32, to_ - 32) | columns(0, sk - 32);
+                            sees = (m0 | m1) != 0;
+                            if (!__any_sync(kFull, sees)) {
+                                const uint32_t none[16] = {};
+                                tmem_st32_u<16>(tp, none);
+                                tmem_st32_u<16>(tp + 16, none);
+                                continue;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                v[i] = m0 & (1u << i) ? v[i] : -CUDART_INF_F;
+                                v[32 + i] = m1 & (1u << i) ? v[32 + i] : -CUDART_INF_F;
+                            }
+                        }
+                        auto largest = [&]() {
+                            float mx = fmax3(v[0], v[1], v[2]), my = v[3];
+#pragma unroll
+                            for (int i = 4; i < 64; i += 4) {
+                                mx = fmax3(mx, v[i], v[i + 1]);
+                                my = fmax3(my, v[i + 2], v[i + 3]);
+                            }
+                            return fmaxf(mx, my) * c;
+                        };
+                        // a row's first scores give it a reference
+                        if (!anchored && __any_sync(kFull, sees && m_ref == -CUDART_INF_F)) {
+                            const float top = largest() - C::kAbove;
+                            m_ref = m_ref == -CUDART_INF_F ? top : m_ref;
+                        }
+                        float2 h2;
+                        uint32_t pk[32];
+#pragma unroll 1
+                        for (int again = 0; again < 2; ++again) {
+                            const float msub = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+                            const float2 s2 = make_float2(-msub, -msub);
+                            float2 g2 = make_float2(0.f, 0.f);
+                            h2 = g2;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float2 d = ffma2(make_float2(v[2 * i], v[2 * i + 1]), c2, s2);
+                                const float2 e = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
+                                (i & 1 ? g2 : h2) = fadd2(i & 1 ? g2 : h2, e);
+                                pk[i] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                            }
+                            h2 = fadd2(h2, g2);
+                            const bool over = limit > 0 && !(h2.x + h2.y <= C::kSumMost);
+                            if (again || !__any_sync(kFull, over))
+                                break;
+                            // up by `by`, to kAbove below the largest score or just above it
+                            const float by = over ? fmaxf(0.f, ceilf(largest() - C::kAbove - m_ref)) : 0.f;
+                            const float alpha = by < 126.f ? __int_as_float((127 - (int)by) << 23) : 0.f;
+                            m_ref += by;
+                            l2.x *= alpha;
+                            l2.y *= alpha;
+                            tmem_wait_st();
+#pragma unroll 1
+                            for (int cc = 0; half > 0 && cc < 32; cc += 16) {      // the tile's probabilities so far
+                                float w[16];
+                                tmem_ld32<16>(ts + cc, w);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float a, b;
+                                    unpack16x2<FP8>(__float_as_uint(w[i]), a, b);
+                                    w[i] = __uint_as_float(FP8 ? pack_f16x2(a * alpha, b * alpha)
+                                                               : pack_bf16x2(a * alpha, b * alpha));
+                                }
+                                tmem_st32<16>(ts + cc, w);
+                            }
+                            scale_o(alpha);
+                            tmem_wait_st();
+                        }
+                        tmem_st32_u<16>(tp, pk);
+                        tmem_st32_u<16>(tp + 16, pk + 16);
+                        l2 = fadd2(l2, h2);
+                    }
                 }
                 if (!anchored)
                     anchored = !__any_sync(kFull, m_ref == -CUDART_INF_F && limit > 0);
@@ -996,27 +1058,31 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
                     break;
                 const uint8_t *src = smem + slot * C::kSlotBytes;
                 uint8_t *dst = smem + vb * C::kVBytes;
-                uint4 a[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    a[k] = *reinterpret_cast<const uint4 *>(src + from[k & 1] + (k >> 1) * 1024);
                 // rows that no token sees may hold anything
-                if ((tile + 1) * kKeys > end || (tile * kKeys < dead_hi && (tile + 1) * kKeys > p.sinks)) {
+                const bool dead = (tile + 1) * kKeys > end || (tile * kKeys < dead_hi && (tile + 1) * kKeys > p.sinks);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int vk = tile * kKeys + w * 32 + k * 4 + sub;
-                        if (vk >= end || (vk >= p.sinks && vk < dead_hi))
-                            a[k] = make_uint4(0u, 0u, 0u, 0u);
+                for (int k0 = 0; k0 < 8; k0 += C::kLoads) {
+                    uint4 a[C::kLoads];
+#pragma unroll
+                    for (int k = 0; k < C::kLoads; ++k)
+                        a[k] = *reinterpret_cast<const uint4 *>(src + from[k & 1] + (k0 + k >> 1) * 1024);
+                    if (dead) {
+#pragma unroll
+                        for (int k = 0; k < C::kLoads; ++k) {
+                            const int vk = tile * kKeys + w * 32 + (k0 + k) * 4 + sub;
+                            if (vk >= end || (vk >= p.sinks && vk < dead_hi))
+                                a[k] = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
-                }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 lo = make_uint4(f16x2_of_e4m3(a[k].x), f16x2_of_e4m3(a[k].x >> 16), f16x2_of_e4m3(a[k].y),
-                                                f16x2_of_e4m3(a[k].y >> 16));
-                    const uint4 hi = make_uint4(f16x2_of_e4m3(a[k].z), f16x2_of_e4m3(a[k].z >> 16), f16x2_of_e4m3(a[k].w),
-                                                f16x2_of_e4m3(a[k].w >> 16));
-                    *reinterpret_cast<uint4 *>(dst + to[k & 1][0] + (k >> 1) * 2048) = u >> 2 ? hi : lo;
-                    *reinterpret_cast<uint4 *>(dst + to[k & 1][1] + (k >> 1) * 2048) = u >> 2 ? lo : hi;
+                    for (int k = 0; k < C::kLoads; ++k) {
+                        const uint4 lo = make_uint4(f16x2_of_e4m3(a[k].x), f16x2_of_e4m3(a[k].x >> 16),
+                                                    f16x2_of_e4m3(a[k].y), f16x2_of_e4m3(a[k].y >> 16));
+                        const uint4 hi = make_uint4(f16x2_of_e4m3(a[k].z), f16x2_of_e4m3(a[k].z >> 16),
+                                                    f16x2_of_e4m3(a[k].w), f16x2_of_e4m3(a[k].w >> 16));
+                        *reinterpret_cast<uint4 *>(dst + to[k & 1][0] + (k0 + k >> 1) * 2048) = u >> 2 ? hi : lo;
+                        *reinterpret_cast<uint4 *>(dst + to[k & 1][1] + (k0 + k >> 1) * 2048) = u >> 2 ? lo : hi;
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1119,23 +1185,24 @@ __global__ void __launch_bounds__(kJoinThreads) window_chunk_join_kernel(const W
         p.lse[qrow] = lam == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(lam);
 }
 
-template <bool FP8>
+template <bool FP8, bool WIDE>
 cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const CUtensorMap &out_map, const WindowParams &p,
                      int runs, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(window_chunk_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               CCfg<FP8>::kSmemBytes);
+    using C = CCfg<FP8, WIDE>;
+    const cudaError_t e = cudaFuncSetAttribute(window_chunk_kernel<FP8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               C::kSmemBytes);
     if (e != cudaSuccess)
         return e;
     // the warpgroups' shares after the reallocation may not exceed what the CTA was launched with
     static const int regs = [] {
         cudaFuncAttributes a{};
-        return cudaFuncGetAttributes(&a, window_chunk_kernel<FP8>) == cudaSuccess ? a.numRegs : 0;
+        return cudaFuncGetAttributes(&a, window_chunk_kernel<FP8, WIDE>) == cudaSuccess ? a.numRegs : 0;
     }();
-    if (regs < CCfg<FP8>::kRegsLaunch)
+    if (regs < C::kRegsLaunch)
         return cudaErrorInvalidConfiguration;
-    return launch_pdl(window_chunk_kernel<FP8>, dim3((unsigned)runs), dim3(CCfg<FP8>::kThreads), CCfg<FP8>::kSmemBytes,
-                      stream, kv_map, q_map, out_map, p);
+    return launch_pdl(window_chunk_kernel<FP8, WIDE>, dim3((unsigned)runs), dim3(C::kThreads), C::kSmemBytes, stream,
+                      kv_map, q_map, out_map, p);
 }
 
 }  // namespace
@@ -1200,8 +1267,11 @@ cudaError_t launch_window_chunk(const WindowParams &params, int kv_dtype, long l
         ++p.shift;
     p.bounded = (double)per_seq * p.H_kv * (kUnitFixed + (double)most) < (double)(1 << 30);
     p.deal = (double)p.bs * keys * p.H_kv * (fp8 ? 256 : 512) > kL2Share ? 1 : 0;
-    e = fp8 ? launch_t<true>(kv_map, q_map, out_map, p, (int)runs, stream)
-            : launch_t<false>(kv_map, q_map, out_map, p, (int)runs, stream);
+    // (a prompt's first units see less: on average keys / 2 less over its first `keys` tokens)
+    const bool wide = keys > 0 && keys * (1. - 0.5 * keys / max_seq_len) >= kWideTiles * (double)kKeys;
+    auto launch = fp8 ? (wide ? launch_t<true, true> : launch_t<true, false>)
+                      : (wide ? launch_t<false, true> : launch_t<false, false>);
+    e = launch(kv_map, q_map, out_map, p, (int)runs, stream);
     if (e != cudaSuccess || runs == 1)
         return e;
     return launch_pdl(window_chunk_join_kernel, dim3((unsigned)runs, 2 * kRows / 32), dim3(kJoinThreads), 0, stream, p);

@@ -87,3 +87,23 @@ def test_windows_and_sinks_of_any_whole_number(qs):
         with pytest.raises((sk.SkError, ValueError)):
             run(b, **kw)
     assert sk.sk_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,qs,hq,hkv,window,sinks", [
+    ([9000], [300], 8, 2, 5000, 4), ([7000, 9001, 6500], [33, 260, 1], 16, 2, 4000, 70), ([12000], [130], 5, 1, 9000, 0),
+    ([6200], [6200], 4, 1, 5000, 17), ([20001, 300], [70, 300], 12, 4, 6000, 4)])
+@pytest.mark.parametrize("rising", [False, True])
+def test_long_units(lens, qs, hq, hkv, window, sinks, rising, fp8):
+    """Units of many key tiles, which take a tile in one go where all rows see it; scores that grow by far along the keys move
+    the references again and again."""
+    b = batch(lens, qs, hq, hkv, fp8, 95, window, sinks, gain=6.0 if rising else 1.0, forget=not rising)
+    if rising:
+        for s, n in enumerate(lens):
+            for i in range(0, (n + PAGE - 1) // PAGE):
+                blk = int(b["table"][s, i])
+                k = b["kv"].view(torch.float8_e4m3fn)[blk, :, :, :D] if fp8 else b["kv"][blk, :, :, :D]
+                k.copy_((k.float() * (0.05 + 2.0 * i * PAGE / n)).to(k.dtype))
+    out, lse = run(b)
+    assert sk.sk_get_device_status() == 0
+    check(b, out, lse)
