@@ -664,50 +664,177 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
         int mine = 0, pieces = 0, u = 0;                           // this row tile's key tiles and pieces, slots so far
         bool failed = false;
         const int own_j = tau / p.gb;
-        while (!failed) {
-            // The piece stays in the ring, to be read again for the output, until that is written: in registers it would
-            // spill the scores.
+        // The piece at work: its key tiles (and this row tile's), and where its row's output goes: token (-1: there is none), head,
+        // whether the piece is the whole unit, and whether it starts it.
+        int n = 0, nx = 0, tok = -1, head = 0, first_key = 0;
+        bool whole = false, starts = false;
+        // Keys are numbered without the gap: the row sees those below the sinks and those from low (0 where its window reaches the
+        // sinks) on below limit; all of the warp's rows those from high on below least.  V's rows [dead_lo, dead_hi) and from
+        // end on are no row's of the unit.
+        int limit = 0, low = 0, least = 0, high = 0, end = 0, dead_hi = 0;
+        const int dead_lo = p.sinks;
+        float c = 0.f;
+        // Takes the next piece; false at the run's end, and (failed becomes true) when the wait gave up.
+        auto take = [&]() {
             const int place = read % kRing;
-            volatile Piece *pc = ring + place;
-            if (!__all_sync(kFull, wait_short(bar_piece(place), (read / kRing) & 1, abort_flag, p.wait_limit))) {
-                failed = true;
-                break;
-            }
-            if (pc->s < 0)
-                break;
+            failed = !__all_sync(kFull, wait_short(bar_piece(place), (read / kRing) & 1, abort_flag, p.wait_limit));
+            const volatile Piece *pc = ring + place;
+            if (failed || pc->s < 0)
+                return false;
             ++read;
-            // this row: its token, and its head in the group
-            auto row_at = [&](int &j, int &i) {
-                tile_origin(p, 2 * pc->unit + x, j, i);
-                j += own_j;
-                i += tau - own_j * p.gb;
-                return own_j < p.tpb && j < pc->q_len && i < p.G;
-            };
-            const int nx = x ? pc->nB : pc->nA;
-            const int first_key = pc->a * kKeys;
-            // Keys are numbered without the gap: the row sees those below the sinks and those from low (0 where its window
-            // reaches the sinks) on below limit; all of the warp's rows those from high on below least.  V's rows [dead_lo,
-            // dead_hi) and from end on are no row's of the unit.
-            int limit, low, least, high;
-            float c = p.score_scale_log2;
-            const int gap = pc->gap * kPage, end = pc->hi - gap;
-            const int dead_lo = p.sinks, dead_hi = pc->lo > p.sinks ? pc->lo - gap : 0;
-            {
-                int j, i;
-                const bool live = row_at(j, i);
-                const int seen = live ? visible_keys(pc->L, pc->q_len, j, 1) : 0;
-                low = seen - p.window;
-                low = low > p.sinks ? low - gap : 0;
-                limit = max(0, seen - gap);
-                least = __reduce_min_sync(kFull, live ? limit : INT_MAX);        // what padding rows hold is never used
-                high = __reduce_max_sync(kFull, low);
-                if (FP8 && live)
-                    c *= __ldg(p.q_scale + (long long)(pc->tok0 + j) * p.H_q + pc->h * p.G + i);
+            n = pc->b - pc->a;
+            nx = x ? pc->nB : pc->nA;
+            first_key = pc->a * kKeys;
+            starts = pc->a == 0;
+            whole = starts && pc->b == pc->t;
+            const int gap = pc->gap * kPage, q_len = pc->q_len;
+            end = pc->hi - gap;
+            dead_hi = pc->lo > p.sinks ? pc->lo - gap : 0;
+            int j, i;
+            tile_origin(p, 2 * pc->unit + x, j, i);
+            j += own_j;
+            i += tau - own_j * p.gb;
+            const bool live = own_j < p.tpb && j < q_len && i < p.G;
+            const int seen = live ? visible_keys(pc->L, q_len, j, 1) : 0;
+            low = seen - p.window;
+            low = low > p.sinks ? low - gap : 0;
+            limit = max(0, seen - gap);
+            tok = live ? pc->tok0 + j : -1;
+            head = pc->h * p.G + i;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_piece_free(place));
+            least = __reduce_min_sync(kFull, live ? limit : INT_MAX);            // what padding rows hold is never used
+            high = __reduce_max_sync(kFull, low);
+            c = p.score_scale_log2;
+            if (FP8 && live)
+                c *= __ldg(p.q_scale + (long long)tok * p.H_q + head);
+            return true;
+        };
+        float m_ref = -CUDART_INF_F;
+        float2 l2 = make_float2(0.f, 0.f);
+        for (bool worked = false;; worked = true) {
+            // The next piece is taken before the output of the one that was worked on, while its last products run (with that
+            // after the output 24 prompts over a window of 512 took 111 us, 107 so).
+            const int out_n = n, out_nx = nx, out_tok = tok, out_head = head;
+            const bool out_whole = whole, out_starts = starts;
+            const bool more = take();
+            if (failed)
+                break;
+            if (worked) {
+                // ---- the row's output, or its partial state
+                const bool live = out_tok >= 0;
+                const int qrow = out_tok * p.H_q + out_head;
+                // a run has at most one piece that does not start its unit, and one more that does not end it
+                const int part = (2 * blockIdx.x + (out_starts ? 1 : 0)) * (2 * kRows) + x * kRows + tau;
+                const float l = l2.x + l2.y;
+                const float mul = !out_whole ? p.v_scale : (l == 0.f ? 0.f : p.v_scale / l);
+                if (out_nx > 0) {
+                    const bool ok = wait_short(bar_o(x), pieces & 1, abort_flag, p.wait_limit);
+                    if (!__all_sync(kFull, ok)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                // A warp whose rows all exist and see something stages 64 dimensions of them at a time, swizzled, for a copy that
+                // runs beside the next unit, and loads 32 dimensions while it rounds the 32 before.  (A lane's own row, 32 bytes a
+                // store, took 4400 cycles a unit and row tile, the exchange between lanes below 5200, of 25000 that a unit of
+                // five key tiles took.)
+                const bool blind = out_nx == 0 || l == 0.f;
+                if (out_whole && p.out_heads > 0 && !__any_sync(kFull, !live || blind)) {
+                    uint8_t *stage = smem + C::kOffOut + (warp - 4) * C::kOutWarp;
+                    const float2 mul2 = make_float2(mul, mul);
+                    float o[2][32];
+                    tmem_ld32<32>(to, o[0]);
+                    if (lane == 0)                                     // the copy before has read the stage
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        tmem_wait_ld();
+                        if (k < 3)
+                            tmem_ld32<32>(to + 32 * k + 32, o[(k + 1) & 1]);
+                        const float *y = o[k & 1];
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 z = fmul2(make_float2(y[2 * i], y[2 * i + 1]), mul2);
+                            w[i] = pack_bf16x2(z.x, z.y);
+                        }
+                        if (k == 2) {
+                            if (lane == 0)
+                                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((((k & 1) * 4 + i) ^ (lane & 7)) << 4)) =
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                        if (k & 1) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                asm volatile(
+                                    "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                                        reinterpret_cast<uint64_t>(&out_map)),
+                                    "r"(32 * k - 32), "r"(out_head), "r"(out_tok), "r"(smem_u32(stage))
+                                    : "memory");
+                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int cc = 0; cc < 128; cc += 32) {
+                        float o[32];
+                        if (out_nx > 0) {
+                            tmem_ld32<32>(to + cc, o);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = blind ? 0.f : o[i] * mul;
+                        if (!out_whole) {
+                            // four dimensions of 32 rows are 512 bytes: part_o is [slot][dimension / 4][row][4]
+                            float4 *dst = reinterpret_cast<float4 *>(p.part_o) +
+                                          (long long)(part / (2 * kRows)) * (32 * 2 * kRows) + (cc / 4) * (2 * kRows) +
+                                          (x * kRows + tau);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[i * (2 * kRows)] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        } else if (live) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+                            uint16_t *dst = p.out + (long long)qrow * kHeadDim + cc;
+                            store32(dst, w, p.wide);
+                            store32(dst + 16, w + 8, p.wide);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (live) {
+                    if (!out_whole) {
+                        p.part_m[part] = m_ref;
+                        p.part_l[part] = l;
+                    } else if (p.lse != nullptr) {
+                        p.lse[qrow] = l == 0.f ? -CUDART_INF_F : m_ref * 0.69314718055994531f + logf(l);
+                    }
+                }
+                // the next piece's first product into O waits for its P, which this thread writes after these reads
+                tc_fence_before();
+                mine += out_nx;
+                pieces += out_nx > 0 ? 1 : 0;
+                u += 2 * out_n;
             }
+            if (!more)
+                break;
             const float2 c2 = make_float2(c, c);
-            float m_ref = -CUDART_INF_F;
+            m_ref = -CUDART_INF_F;
             bool anchored = false;                                     // every row that sees a key has a reference
-            float2 l2 = make_float2(0.f, 0.f);
+            l2 = make_float2(0.f, 0.f);
             for (int j = 0; j < nx; ++j) {
                 const int key0 = first_key + j * kKeys;
                 bool ok = wait_short(bar_s(x), (mine + j) & 1, abort_flag, p.wait_limit);
@@ -906,119 +1033,6 @@ window_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_con
             }
             if (failed)
                 break;
-            // ---- the row's output, or its partial state (its place is found while the last products run).  A lane's row is
-            // transposed within quads of lanes, so that a warp's store writes 64 contiguous bytes of eight rows (with 16 bytes
-            // of 32 rows it took 5000 cycles)
-            int jr, ir;
-            const bool live = row_at(jr, ir);
-            const bool whole = pc->a == 0 && pc->b == pc->t;
-            const int qrow = live ? (pc->tok0 + jr) * p.H_q + pc->h * p.G + ir : -1;
-            // a run has at most one piece that does not start its unit, and one more that does not end it
-            const int part = (2 * blockIdx.x + (pc->a > 0 ? 0 : 1)) * (2 * kRows) + x * kRows + tau;
-            const float l = l2.x + l2.y;
-            const float mul = !whole ? p.v_scale : (l == 0.f ? 0.f : p.v_scale / l);
-            if (nx > 0) {
-                const bool ok = wait_short(bar_o(x), pieces & 1, abort_flag, p.wait_limit);
-                if (!__all_sync(kFull, ok)) {
-                    failed = true;
-                    break;
-                }
-                tc_fence_after();
-            }
-            // A warp whose rows all exist and see something stages 64 dimensions of them at a time, swizzled, for a copy that
-            // runs beside the next unit, and loads 32 dimensions while it rounds the 32 before.  (A lane's own row, 32 bytes a
-            // store, took 4400 cycles a unit and row tile, the exchange between lanes below 5200, of 25000 that a unit of
-            // five key tiles took.)
-            const bool blind = nx == 0 || l == 0.f;
-            if (whole && p.out_heads > 0 && !__any_sync(kFull, !live || blind)) {
-                uint8_t *stage = smem + C::kOffOut + (warp - 4) * C::kOutWarp;
-                const float2 mul2 = make_float2(mul, mul);
-                float o[2][32];
-                tmem_ld32<32>(to, o[0]);
-                if (lane == 0)                                     // the copy before has read the stage
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    tmem_wait_ld();
-                    if (k < 3)
-                        tmem_ld32<32>(to + 32 * k + 32, o[(k + 1) & 1]);
-                    const float *y = o[k & 1];
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 z = fmul2(make_float2(y[2 * i], y[2 * i + 1]), mul2);
-                        w[i] = pack_bf16x2(z.x, z.y);
-                    }
-                    if (k == 2) {
-                        if (lane == 0)
-                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        __syncwarp();
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((((k & 1) * 4 + i) ^ (lane & 7)) << 4)) =
-                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                    if (k & 1) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            asm volatile(
-                                "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                                    reinterpret_cast<uint64_t>(&out_map)),
-                                "r"(32 * k - 32), "r"(pc->h * p.G + ir), "r"(pc->tok0 + jr), "r"(smem_u32(stage))
-                                : "memory");
-                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                        }
-                    }
-                }
-            } else {
-#pragma unroll 1
-                for (int cc = 0; cc < 128; cc += 32) {
-                    float o[32];
-                    if (nx > 0) {
-                        tmem_ld32<32>(to + cc, o);
-                        tmem_wait_ld();
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = blind ? 0.f : o[i] * mul;
-                    if (!whole) {
-                        // four dimensions of 32 rows are 512 bytes: part_o is [slot][dimension / 4][row][4]
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o) +
-                                      (long long)(part / (2 * kRows)) * (32 * 2 * kRows) + (cc / 4) * (2 * kRows) +
-                                      (x * kRows + tau);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i * (2 * kRows)] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    } else if (live) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
-                        uint16_t *dst = p.out + (long long)qrow * kHeadDim + cc;
-                        store32(dst, w, p.wide);
-                        store32(dst + 16, w + 8, p.wide);
-                    }
-                    __syncwarp();
-                }
-            }
-            if (live) {
-                if (!whole) {
-                    p.part_m[part] = m_ref;
-                    p.part_l[part] = l;
-                } else if (p.lse != nullptr) {
-                    p.lse[qrow] = l == 0.f ? -CUDART_INF_F : m_ref * 0.69314718055994531f + logf(l);
-                }
-            }
-            // the next piece's first product into O waits for its P, which this thread writes after these reads
-            tc_fence_before();
-            mine += nx;
-            pieces += nx > 0 ? 1 : 0;
-            u += 2 * (pc->b - pc->a);
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_piece_free(place));
         }
         if (lane == 0)                                             // (its own copies: nothing is left in flight)
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
