@@ -27,9 +27,10 @@
 // Every wait is bounded: on expiry SK_DEV_TIMEOUT is set and every role gives up, after its copies and products in flight.
 //
 // Measured: 4096 tokens over a window of 4096, 32/8 heads: 196 us, 1.40 PFLOP/s of the pairs that are seen.  24 prompts of up to
-// 2000 tokens over 512, 16/2 heads: 111 us; 16001 tokens over 128: 51 us; 1919 tokens of four prompts over 2048 on e4m3 pages:
+// 2000 tokens over 512, 16/2 heads: 107 us; 16001 tokens over 128: 51 us; 1919 tokens of four prompts over 2048 on e4m3 pages:
 // 40 us.  A key tile takes 3050 cycles: the softmax of a row tile (1600) and its products (1024 for both of its own), one after
-// the other, beside those of the other row tile; the tensor pipe is busy 61 % of the first call, 40 % of the second.
+// the other, beside those of the other row tile; a unit's start and end take 5000 more, a call's first S 12000, on code that runs once
+// in a while; the tensor pipe is busy 61 % of the first call, 40 % of the second.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -124,7 +125,8 @@ constexpr double kL2Share = 60e6;                    // bytes of K and V that st
 // over a window of 512 took 119.4 us with 384, 117.2 with 160, 111.2 with 128, 123.5 with 32.
 constexpr int kUnitFixed = 128;
 // A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
-// than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384, 110 with 640).
+// than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384,
+// 110 with 640).
 constexpr int kCutFixed = 512;
 // Where units cost alike, none is cut if the longest run is then longer by this or less than if they were: 1919 tokens of e4m3
 // pages over a window of 2048, 122 units, took 42.0 us, and 46.8 cut; 168 units on the 152 SMs take 37.3 cut, and 42.8 whole.
