@@ -84,6 +84,7 @@ struct WindowParams {
     const float *q_scale;        // chunk, e4m3 pages: 2^-e of each row of the split Q
     int gb, tpb, nsub;           // chunk: heads and tokens of a row tile, row tiles per token
     int deal, shift;             // chunk: whole units are dealt first; costs are in 2^shift keys
+    uint32_t slope;              // chunk: what a unit sees more than the one before
     int bounded;                 // chunk: the batch's cost fits 32 bits whatever the query offsets are
     int wide, out_heads;         // chunk: out takes 32-byte stores; a softmax warp's rows are this many heads of tokens, or 0
 };

@@ -40,6 +40,7 @@
 #include "sk_attn_util.cuh"
 #include "sk_cache_ops.cuh"
 #include "sk_sm100.cuh"
+#include "sk_window_cost.cuh"
 
 namespace sk {
 namespace {
@@ -47,8 +48,8 @@ namespace {
 using namespace sm100;
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kRows = 128;                           // rows of one tile (MMA M)
-constexpr int kKeys = 128;                           // keys of one tile (MMA N)
+constexpr int kRows = kChunkRows;                    // rows of one tile (MMA M)
+constexpr int kKeys = kChunkKeys;                    // keys of one tile (MMA N)
 constexpr uint32_t kDrainLimit = 4000000000u;        // cycles (~2 s): waits for work already issued
 constexpr int kMaxSmem = 232448;
 constexpr int kRing = 4;                             // pieces published ahead
@@ -121,17 +122,6 @@ constexpr int kColS = 0, kColO = 256;                // S_A, S_B, then O_A, O_B,
 // stay in the L2 begins with whole units, dealt to the CTAs in turn, so that neighbours read the same window at the same
 // time; what is left over is shared out.  Costs are counted in 2^shift keys, so that a batch's fits 32 bits.
 constexpr double kL2Share = 60e6;                    // bytes of K and V that stay in the L2 (126 MB in two halves)
-// Cost of starting and finishing a unit, in keys, next to other units, which hide most of it: 24 prompts of up to 2000 tokens
-// over a window of 512 took 119.4 us with 384, 117.2 with 160, 111.2 with 128, 123.5 with 32.
-constexpr int kUnitFixed = 128;
-// A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
-// than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384,
-// 110 with 640).
-constexpr int kCutFixed = 512;
-// Where units cost alike, none is cut if the longest run is then longer by this or less than if they were: 1919 tokens of e4m3
-// pages over a window of 2048, 122 units, took 42.0 us, and 46.8 cut; 168 units on the 152 SMs take 37.3 cut, and 42.8 whole.
-constexpr int kJoinCost = 800;
-
 // Key tiles of a unit, on average, from which on a tile that a warp's rows all see is taken in one go instead of by halves.  That
 // waits for the tensor memory and votes once, but its code beside that of the masked tiles costs units that change between
 // them often.  Measured, in one go and by halves: 4096 tokens over a window of 4096 198 and 210 us (e4m3 pages 227 and 235),
@@ -158,19 +148,15 @@ struct WindowWalk {
     const int lane, count;
     int s0;                                          // the 32 sequences that the lanes hold: what follows is lane's
     int L, q_len, tok0, units;                       // units of one head
-    int base, step, top, rising;                     // unit i costs base + step * (i + 1) below `rising`, then top
+    UnitCosts costs;                                 // of its units
+    int head_cost;                                   // of one head's
     int units_to, cost_to;                           // of the lanes' sequences, all heads, up to this one's end
-    int units_before, cost_before;                   // (uniform) of the sequences before s0
+    int units_before, cost_done;                     // (uniform) of the sequences before s0
     int lo, hi;                                      // this CTA's run of the cost; of the units left over, a unit costs `count`
     int deal, dealt;                                 // next unit dealt, and how many units are dealt in all
     int s, h, unit;                                  // cursor of the run
-    bool left_over, uncut, falls;                           // `falls`: some offset of the queries is below the one before
+    bool left_over, uncut, falls;                    // `falls`: some offset of the queries is below the one before
 
-    __device__ __forceinline__ int before(int i) const
-    {
-        const int n = min(i, rising);
-        return n * base + step * (int)((uint32_t)n * (n + 1) / 2) + (i - n) * top;
-    }
     __device__ __forceinline__ void load(int first)
     {
         s0 = first;
@@ -186,13 +172,10 @@ struct WindowWalk {
         falls |= end < tok0;
         q_len = bad ? 0 : end - tok0;
         units = at < p.bs ? ((q_len + p.tpb - 1) / p.tpb * p.nsub + 1) / 2 : 0;
-        // later units see more keys, unless a token has several row tiles
-        base = ((kUnitFixed + (p.nsub == 1 ? max(0, L - q_len) : L)) >> p.shift) + 1;
-        step = p.nsub == 1 ? 2 * p.tpb >> p.shift : 0;
-        top = (int)((kUnitFixed + (long long)p.sink_pages * kPage + p.window + 2 * p.tpb) >> p.shift) + 1;
-        rising = base >= top ? 0 : step > 0 ? (top - base) / step : INT_MAX;
+        costs = unit_costs(max(0, L - q_len), p.sink_pages, kPage, p.window, p.tpb, p.slope, p.shift);
+        head_cost = cost_before(units, costs, p.slope, p.shift);
         units_to = units * p.H_kv;
-        cost_to = before(units) * p.H_kv;
+        cost_to = head_cost * p.H_kv;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(kFull, units_to, o), y = __shfl_up_sync(kFull, cost_to, o);
@@ -205,17 +188,17 @@ struct WindowWalk {
     __device__ __forceinline__ int seek(int x, bool by_cost)
     {
         while (true) {
-            const int to = by_cost ? cost_before + cost_to : units_before + units_to;
+            const int to = by_cost ? cost_done + cost_to : units_before + units_to;
             const uint32_t past = __ballot_sync(kFull, x < to);
             if (past != 0)
                 return __ffs(past) - 1;
             units_before += of(units_to, 31);
-            cost_before += of(cost_to, 31);
+            cost_done += of(cost_to, 31);
             load(s0 + 32);
         }
     }
     __device__ WindowWalk(const WindowParams &pp, int index, int runs, bool none)
-        : p(pp), lane(threadIdx.x & 31), count(runs), units_before(0), cost_before(0), lo(0), hi(0), deal(index), dealt(0),
+        : p(pp), lane(threadIdx.x & 31), count(runs), units_before(0), cost_done(0), lo(0), hi(0), deal(index), dealt(0),
           s(0), h(0), unit(0), left_over(false), uncut(false), falls(false)
     {
         int total = 0, all = 0, largest = 0;
@@ -224,13 +207,14 @@ struct WindowWalk {
             load(first);
             total += of(cost_to, 31);
             all += of(units_to, 31);
-            largest = max(largest, __reduce_max_sync(kFull, units > 0 ? (units <= rising ? base + step * units : top) : 0));
+            largest = max(largest, __reduce_max_sync(kFull, units > 0 ? cost_of(units - 1, costs, p.slope, p.shift) : 0));
         }
         // offsets that fall may give the same tokens to many sequences: more cost than the tokens come to
         if (none || (!p.bounded && __any_sync(kFull, falls)))
             return;
-        if (p.deal && ((float)largest * (float)all <= 1.4f * (float)total ||
-                       (float)largest * (float)count * 8.f <= (float)total)) {
+        const Division d = divide(total, all, largest, count, p.deal != 0, p.shift);
+        uncut = d.uncut;
+        if (d.deal) {
             // whole units in turn; each unit that is left over is shared by neighbours, as one of `count` parts
             dealt = all / count * count;
             left_over = true;
@@ -238,20 +222,9 @@ struct WindowWalk {
             hi = lo + (all - dealt);
             unit = dealt + lo / count;
         } else {
-            const int each = total / count + 1;
-            lo = min((long long)total, (long long)each * index);
-            hi = min((long long)total, (long long)each * (index + 1));
-            const int most = (all + count - 1) / count;      // units of a run, if none is cut
-            uncut = (float)largest * (float)all <= 1.1f * (float)total &&
-                    (float)largest * (float)(most * count - all) <= (float)(kJoinCost >> p.shift) * (float)count;
+            lo = min((long long)total, (long long)d.each * index);
+            hi = min((long long)total, (long long)d.each * (index + 1));
         }
-    }
-    // Key tile at which a run's bound cuts a unit of t tiles, `at` of `cost` in.
-    __device__ __forceinline__ int cut(int at, int cost, int t) const
-    {
-        const float f = __fdividef((float)at, (float)cost);
-        const float g = uncut ? 0.5f : __fdividef((float)kCutFixed, (float)(kCutFixed + t * kKeys));
-        return at >= cost ? t : f <= g ? 0 : f >= 1.f - g ? t : min(t, (int)((float)t * f));
     }
     __device__ __forceinline__ bool next(Piece &pc)
     {
@@ -270,27 +243,26 @@ struct WindowWalk {
                 pc.unit = i - pc.h * n;
                 start = (x - dealt) * count;
             } else {
-                const int head = of(before(units), src);
-                const int in = x - cost_before - of(cost_to - before(units) * p.H_kv, src);
+                const int head = of(head_cost, src);
+                const int in = x - cost_done - of(cost_to - head_cost * p.H_kv, src);
                 pc.h = in / head;
                 const int in_head = in - pc.h * head;
-                const int b = of(base, src), st = of(step, src), tp = of(top, src), ri = of(rising, src);
-                auto upto = [&](int i) {
-                    const int n = min(i, ri);
-                    return n * b + st * (int)((uint32_t)n * (n + 1) / 2) + (i - n) * tp;
-                };
-                int left = 0, right = of(units, src) - 1;
+                const UnitCosts c{of(costs.base, src), of(costs.top, src), of(costs.rising, src)};
+                auto upto = [&](int i) { return cost_before(i, c, p.slope, p.shift); };
+                int left = 0, right = of(units, src) - 1, from = 0;      // `from`: upto(left)
 #pragma unroll 1
                 while (left < right) {
-                    const int mid = (left + right + 1) >> 1;
-                    if (upto(mid) <= in_head)
+                    const int mid = (left + right + 1) >> 1, at = upto(mid);
+                    if (at <= in_head) {
                         left = mid;
-                    else
+                        from = at;
+                    } else {
                         right = mid - 1;
+                    }
                 }
                 pc.unit = left;
-                start = lo - in_head + upto(left);
-                cost = left < ri ? b + st * (left + 1) : tp;
+                start = lo - in_head + from;
+                cost = upto(left + 1) - from;
             }
             pc.s = s0 + src;
             pc.L = of(L, src);
@@ -311,8 +283,8 @@ struct WindowWalk {
             pc.b = pc.t;
             bool mine = true;
             if (!whole) {
-                pc.a = cut(lo - start, cost, pc.t);
-                pc.b = cut(hi - start, cost, pc.t);
+                pc.a = cut_tile(lo - start, cost, pc.t, uncut);
+                pc.b = cut_tile(hi - start, cost, pc.t, uncut);
                 mine = pc.a < pc.b || (pc.t == 0 && lo == start);      // one without keys belongs to the run that starts it
                 ++unit;
                 lo = start + cost;                       // the next unit
@@ -1236,9 +1208,11 @@ cudaError_t launch_window_chunk(const WindowParams &params, int kv_dtype, long l
 {
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
     WindowParams p = params;
-    p.gb = p.G < kRows ? p.G : kRows;
-    p.nsub = (p.G + p.gb - 1) / p.gb;
-    p.tpb = kRows / p.gb;
+    const ChunkShape shape = chunk_shape(p.G);
+    p.gb = shape.gb;
+    p.nsub = shape.nsub;
+    p.tpb = shape.tpb;
+    p.slope = shape.slope;
     const long long slots = 2LL * num_sms * 2 * kRows;
     p.part_o = static_cast<float *>(workspace);
     p.part_m = p.part_o + slots * kHeadDim;
@@ -1279,8 +1253,7 @@ cudaError_t launch_window_chunk(const WindowParams &params, int kv_dtype, long l
     long long runs = units * (tiles < 2 ? 1 : tiles / 2);
     runs = runs < 1 ? 1 : (runs < num_sms ? runs : num_sms);
     runs = runs < kMaxRuns ? runs : kMaxRuns;
-    for (p.shift = 4; (units * (kUnitFixed + most) >> p.shift) >> 30; )      // costs below 2^30 in all
-        ++p.shift;
+    p.shift = cost_shift(units, most);
     p.bounded = (double)per_seq * p.H_kv * (kUnitFixed + (double)most) < (double)(1 << 30);
     p.deal = (double)p.bs * keys * p.H_kv * (fp8 ? 256 : 512) > kL2Share ? 1 : 0;
     // (a prompt's first units see less: on average keys / 2 less over its first `keys` tokens)

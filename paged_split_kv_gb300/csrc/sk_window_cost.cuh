@@ -1,0 +1,113 @@
+// Windowed chunks: what a unit of work costs, and where the batch's cost is cut into the CTAs' runs.  Plain arithmetic, for
+// the host as well.
+#pragma once
+#include <limits.h>
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define SK_COST_FN __device__ __forceinline__
+#define SK_COST_DIV(a, b) __fdividef(a, b)
+#else
+#define SK_COST_FN inline
+#define SK_COST_DIV(a, b) ((a) / (b))
+#endif
+
+namespace sk {
+
+constexpr int kChunkKeys = 128;                      // keys of a tile
+constexpr int kChunkRows = 128;                      // rows of a row tile
+// Cost of starting and finishing a unit, in keys, next to other units, which hide most of it: 24 prompts of up to 2000 tokens
+// over a window of 512 took 119.4 us with 384, 117.2 with 160, 111.2 with 128, 123.5 with 32.
+constexpr int kUnitFixed = 128;
+// A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
+// than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384,
+// 110 with 640).
+constexpr int kCutFixed = 512;
+// Where units cost alike, none is cut if the longest run is then longer by this or less than if they were: 1919 tokens of e4m3
+// pages over a window of 2048, 122 units, took 42.0 us, and 46.8 cut; 168 units on the 152 SMs take 37.3 cut, and 42.8 whole.
+constexpr int kJoinCost = 800;
+
+// A row tile is `tpb` query tokens times `gb` heads of the group, or one of the `nsub` tiles of a token whose group has more
+// than 128 heads; a unit is two row tiles.  `slope`: what a unit sees more than the one before, in 2^-kSlopeBits keys (a
+// unit of 2 tpb tokens, or of 2 / nsub of one).
+constexpr int kSlopeBits = 8;
+struct ChunkShape {
+    int gb, nsub, tpb;
+    uint32_t slope;
+};
+inline ChunkShape chunk_shape(int G)
+{
+    ChunkShape c;
+    c.gb = G < kChunkRows ? G : kChunkRows;
+    c.nsub = (G + c.gb - 1) / c.gb;
+    c.tpb = kChunkRows / c.gb;
+    c.slope = (uint32_t)((2 * c.tpb << kSlopeBits) / c.nsub);
+    return c;
+}
+
+// Costs are counted in 2^shift keys, so that those of `units` units of `most` keys or less come to less than 2^30.
+inline int cost_shift(long long units, long long most)
+{
+    int shift = 4;
+    while ((units * (kUnitFixed + most) >> shift) >> 30)
+        ++shift;
+    return shift;
+}
+
+// The units of one (sequence, KV head): unit i costs what its last tokens see, base + slope (i + 1), below `rising`, then
+// `top`, a full window.  Sums keep the slope's fraction of 2^shift keys: with a slope of whole steps, 8 tokens a unit and
+// shift 4, all units cost alike, the longest run of 4000 tokens of 32/1 heads over a window of 4096 had 125 key tiles where
+// the average is 53, and the call took 214 us; it takes 116 so (48/2 heads: 319 and 202; 5000 tokens of 24/2 heads: 145 and 146).
+struct UnitCosts {
+    int base, top, rising;
+};
+SK_COST_FN UnitCosts unit_costs(int cached, int sink_pages, int page, int window, int tpb, uint32_t slope, int shift)
+{
+    UnitCosts c;
+    c.base = ((kUnitFixed + cached) >> shift) + 1;
+    c.top = (int)((kUnitFixed + (long long)sink_pages * page + window + 2 * tpb) >> shift) + 1;
+    const float rise = (float)(c.top - c.base) * (float)(1 << kSlopeBits) * (float)(1 << shift);
+    const float steps = slope == 0 ? 2e9f : SK_COST_DIV(rise, (float)slope);
+    c.rising = c.base >= c.top ? 0 : (int)(steps < 2e9f ? steps : 2e9f);
+    return c;
+}
+// Cost of the units before unit i.  (slope n / 2^kSlopeBits is below 2^32 for n up to `rising`, and n below 2^24.)
+SK_COST_FN int cost_before(int i, UnitCosts c, uint32_t slope, int shift)
+{
+    const int n = i < c.rising ? i : c.rising;
+    const uint64_t rise = (uint64_t)(uint32_t)n * (uint32_t)(n + 1) * slope >> (kSlopeBits + 1 + shift);
+    return n * c.base + (int)rise + (i - n) * c.top;
+}
+// Cost of unit i.
+SK_COST_FN int cost_of(int i, UnitCosts c, uint32_t slope, int shift)
+{
+    return cost_before(i + 1, c, slope, shift) - cost_before(i, c, slope, shift);
+}
+
+// How `count` runs share `all` units that cost `total`, the dearest of them `largest`: with `may_deal`, whole units in turn
+// where they cost alike or little beside a share; else equal shares of the cost, cut within units or, `uncut`, between them.
+struct Division {
+    bool deal, uncut;
+    int each;
+};
+SK_COST_FN Division divide(int total, int all, int largest, int count, bool may_deal, int shift)
+{
+    Division d;
+    d.deal = may_deal && ((float)largest * (float)all <= 1.4f * (float)total ||
+                          (float)largest * (float)count * 8.f <= (float)total);
+    d.each = total / count + 1;
+    const int most = (all + count - 1) / count;      // units of a run, if none is cut
+    d.uncut = !d.deal && (float)largest * (float)all <= 1.1f * (float)total &&
+              (float)largest * (float)(most * count - all) <= (float)(kJoinCost >> shift) * (float)count;
+    return d;
+}
+// Key tile at which a run's bound cuts a unit of t tiles, `at` of `cost` in.
+SK_COST_FN int cut_tile(int at, int cost, int t, bool uncut)
+{
+    const float f = SK_COST_DIV((float)at, (float)cost);
+    const float g = uncut ? 0.5f : SK_COST_DIV((float)kCutFixed, (float)(kCutFixed + t * kChunkKeys));
+    const int tile = (int)((float)t * f);
+    return at >= cost ? t : f <= g ? 0 : f >= 1.f - g ? t : tile < t ? tile : t;
+}
+
+}  // namespace sk
