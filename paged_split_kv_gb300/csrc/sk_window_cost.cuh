@@ -16,9 +16,13 @@ namespace sk {
 
 constexpr int kChunkKeys = 128;                      // keys of a tile
 constexpr int kChunkRows = 128;                      // rows of a row tile
-// Cost of starting and finishing a unit, in keys, next to other units, which hide most of it: 24 prompts of up to 2000 tokens
-// over a window of 512 took 119.4 us with 384, 117.2 with 160, 111.2 with 128, 123.5 with 32.
-constexpr int kUnitFixed = 128;
+// Cost of starting and finishing a unit, in keys, next to other units, which hide part of it, and of its last key tile, which
+// is filled in part.  The geometric mean over 52 calls (26 shapes: one to 24 prompts and chunks, groups of 8 to 160 heads,
+// windows of 128, 512, 4096 and of all; bf16 and e4m3 pages) is 131.4 us with 128, 126.7 with 160, 124.1 with 192, 123.0 with
+// 224, 123.4 with 256, 124.0 with 320; on another machine 129.8 with 128, 125.6 with 384, 128.7 with 640.  Single shapes, with
+// 128 and 224: 24 prompts of up to 2000 tokens over 512, 16/2 heads, 109 and 108, with 32/1 heads 194 and 198; eight of up to
+// 4000 over 4096 174 and 175; 8000 tokens of 16/2 heads 157 and 151; 4000 of 48/2 heads 201 and 173.
+constexpr int kUnitFixed = 224;
 // A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
 // than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384,
 // 110 with 640).
@@ -57,7 +61,8 @@ inline int cost_shift(long long units, long long most)
 // The units of one (sequence, KV head): unit i costs what its last tokens see, base + slope (i + 1), below `rising`, then
 // `top`, a full window.  Sums keep the slope's fraction of 2^shift keys: with a slope of whole steps, 8 tokens a unit and
 // shift 4, all units cost alike, the longest run of 4000 tokens of 32/1 heads over a window of 4096 had 125 key tiles where
-// the average is 53, and the call took 214 us; it takes 116 so (48/2 heads: 319 and 202; 5000 tokens of 24/2 heads: 145 and 146).
+// the average is 53, and the call took 214 us; it takes 114 so (48/2 heads: 319 and 174; 5000 tokens of 24/2 heads: 145 and
+// 136).
 struct UnitCosts {
     int base, top, rising;
 };
