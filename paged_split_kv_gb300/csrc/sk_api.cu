@@ -13,6 +13,7 @@
 #include "sk.h"
 #include "sk_cache_ops.cuh"
 #include "sk_internal.cuh"
+#include "sk_window_cost.cuh"
 
 namespace sk {
 
@@ -816,7 +817,6 @@ static int chunk_call(const char *name, const void *q, const void *kv_pages, int
         return fail(SK_ERR_CAPACITY, "%s: workspace of %lld bytes, %lld needed", name,
                     (long long)workspace_bytes, (long long)need);
     const bool fp8 = kv_dtype == SK_KV_FP8_E4M3;
-    constexpr int kAll = kMaxStride * kPage;         // rows of a sequence at most
     auto fill = [&](auto &p) {
         p.q = static_cast<const uint16_t *>(q);
         p.kv = kv_pages;
@@ -842,8 +842,8 @@ static int chunk_call(const char *name, const void *q, const void *kv_pages, int
     if (window > 0) {
         WindowParams p{};
         fill(p);
-        p.window = window < kAll ? window : kAll;
-        p.sinks = sinks < kAll ? sinks : kAll;
+        p.window = rows_in_table(window, block_table_stride, kPage);
+        p.sinks = rows_in_table(sinks, block_table_stride, kPage);
         p.wait_limit = (uint32_t)(wait_limit() < kDefaultWaitLimit ? wait_limit() : kDefaultWaitLimit);
         e = step ? launch_window_step(p, kv_dtype, max_seq_len, workspace, sms, st)
                  : launch_window_chunk(p, kv_dtype, max_seq_len, workspace, sms, st);

@@ -26,8 +26,8 @@ def longest_run(tmp_path_factory):
         """Key tiles of the longest run, and the most that it may have."""
         n, units = len(lens), ctypes.c_int()
         tiles = (ctypes.c_int * count)()
-        total = f(n, (ctypes.c_int * n)(*lens), (ctypes.c_int * n)(*qs), hq, hkv, window, 4, count, int(deal), tiles,
-                   ctypes.byref(units))
+        total = f(n, (ctypes.c_int * n)(*lens), (ctypes.c_int * n)(*qs), hq, hkv, window, 4, (max(lens) + 15) // 16, count,
+                  int(deal), tiles, ctypes.byref(units))
         assert total >= 0 and sum(tiles) == total              # every unit is covered, in order
         return max(tiles), (1.4 if deal else 1.1) * (total + 2 * units.value) / count + 8
 
@@ -50,6 +50,13 @@ def test_many_sequences(longest_run, group, count):
     lens = [q + 57 * (i % 5) for i, q in enumerate(qs)]
     longest, most = longest_run(lens, qs, group, 1, 512, count=count)
     assert longest <= most
+
+
+@pytest.mark.parametrize("group", [1, 8, 32, 48, 71, 128, 160, 300])
+def test_a_window_of_more_rows_than_the_table_has(longest_run, group):
+    for hkv, tokens, cached in ((1, 2000, 0), (2, 4000, 0), (2, 2000, 100), (1, 3000, 2500), (4, 777, 0), (1, 120000, 0)):
+        longest, most = longest_run([cached + tokens], [tokens], group * hkv, hkv, 2 ** 31 - 1)
+        assert longest <= most, (hkv, tokens, cached)
 
 
 @pytest.mark.parametrize("group", [8, 32, 128])

@@ -19,10 +19,13 @@ int tiles_of(int L, int q, int last, int first, int window, int sink_pages)
 }
 }  // namespace
 
-// Key tiles of each of `count` runs; returns the batch's, or -1 where the runs do not cover each unit in order.
-extern "C" int window_division(int bs, const int *lens, const int *qs, int hq, int hkv, int window, int sinks, int count,
-                               int may_deal, int *tiles, int *num_units)
+// Key tiles of each of `count` runs, for a block table of `stride` pages a sequence; returns the batch's, or -1 where the runs
+// do not cover each unit in order.
+extern "C" int window_division(int bs, const int *lens, const int *qs, int hq, int hkv, int window, int sinks, int stride,
+                               int count, int may_deal, int *tiles, int *num_units)
 {
+    window = rows_in_table(window, stride, 16);
+    sinks = rows_in_table(sinks, stride, 16);
     const ChunkShape c = chunk_shape(hq / hkv);
     const int sink_pages = (sinks + 15) / 16;
     long long all = 0;
@@ -37,7 +40,8 @@ extern "C" int window_division(int bs, const int *lens, const int *qs, int hq, i
         for (int h = 0; h < hkv; ++h)
             for (int i = 0; i < n; ++i) {
                 const int first = 2 * i / c.nsub * c.tpb, last = (2 * i + 1) / c.nsub * c.tpb + c.tpb - 1;
-                units.push_back({tiles_of(lens[s], qs[s], last, first, window, sink_pages), total, cost_of(i, uc, c.slope, shift)});
+                units.push_back({tiles_of(lens[s], qs[s], last, first, window, sink_pages), total,
+                                 cost_of(i, uc, c.slope, shift)});
                 if (units.back().cost < 1)
                     return -1;
                 total += units.back().cost;
