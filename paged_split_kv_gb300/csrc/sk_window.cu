@@ -45,6 +45,7 @@
 #include "sk_attn_util.cuh"
 #include "sk_cache_ops.cuh"
 #include "sk_sm100.cuh"
+#include "sk_window_cost.cuh"
 
 namespace sk {
 namespace {
@@ -1100,10 +1101,6 @@ __global__ void __launch_bounds__(32 * kJoinRows) window_join_kernel(const Windo
         p.lse[row] = lam == 0.f ? -CUDART_INF_F : M * 0.69314718055994531f + logf(lam);
 }
 
-constexpr int kMaxSplit = 8;                         // CTAs of a cluster
-constexpr int kJoinTiles = 7;                        // what the join kernel costs, in key tiles of a CTA: 96 units of 9 tiles take
-                                                     // 11.9 us as clusters (of one) and 15.2 as runs, of 17 tiles 20.1 and 21.2
-
 template <int RP, bool FP8>
 cudaError_t launch_t(const CUtensorMap &kv_map, WindowParams p, long long tiles, int num_sms, cudaStream_t stream)
 {
@@ -1143,17 +1140,8 @@ cudaError_t launch_t(const CUtensorMap &kv_map, WindowParams p, long long tiles,
         }
         return n;
     }();
-    // Units that fit at once have a cluster each, as large as fits and as they have tiles, where that takes no longer than
-    // equal runs and their join.
-    const long long units = (long long)p.bs * p.H_kv;
-    long long runs = units * (tiles < 1 ? 1 : tiles);
-    runs = runs < num_sms ? runs : num_sms;
-    p.split = units <= runs ? 1 : 0;
-    for (int c = 2; p.split > 0 && c <= kMaxSplit && c <= tiles; ++c)
-        if (fit[c] >= units)
-            p.split = c;
-    if (p.split > 0 && (tiles + p.split - 1) / p.split > units * tiles / runs + kJoinTiles)
-        p.split = 0;
+    const long long units = (long long)p.bs * p.H_kv, runs = step_runs(units, tiles, num_sms);
+    p.split = step_cluster(units, tiles, num_sms, fit.data());
     const unsigned grid = (unsigned)(p.split > 0 ? units * p.split : runs);
     cfg.gridDim = dim3(grid);
     attr[1].val.clusterDim.x = (unsigned)(p.split > 1 ? p.split : 1);

@@ -1,5 +1,5 @@
-// Windowed chunks: what a unit of work costs, and where the batch's cost is cut into the CTAs' runs.  Plain arithmetic, for
-// the host as well.
+// Windowed attention: how a call's work is shared among the CTAs.  Chunks: what a unit of work costs, and where the batch's
+// cost is cut into the CTAs' runs; steps: clusters or runs.  Plain arithmetic, for the host as well.
 #pragma once
 #include <limits.h>
 #include <stdint.h>
@@ -22,7 +22,7 @@ constexpr int kChunkRows = 128;                      // rows of a row tile
 // 224, 123.4 with 256, 124.0 with 320; on another machine 129.8 with 128, 125.6 with 384, 128.7 with 640.  Single shapes, with
 // 128 and 224: 24 prompts of up to 2000 tokens over 512, 16/2 heads, 109 and 108, with 32/1 heads 194 and 198; eight of up to
 // 4000 over 4096 174 and 175; 8000 tokens of 16/2 heads 157 and 151; 4000 of 48/2 heads 201 and 173.
-constexpr int kUnitFixed = 224;
+constexpr int kChunkFixed = 224;
 // A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
 // than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384,
 // 110 with 640).
@@ -61,7 +61,7 @@ inline int rows_in_table(int rows, int stride, int page)
 inline int cost_shift(long long units, long long most)
 {
     int shift = 4;
-    while ((units * (kUnitFixed + most) >> shift) >> 30)
+    while ((units * (kChunkFixed + most) >> shift) >> 30)
         ++shift;
     return shift;
 }
@@ -77,8 +77,8 @@ struct UnitCosts {
 SK_COST_FN UnitCosts unit_costs(int cached, int sink_pages, int page, int window, int tpb, uint32_t slope, int shift)
 {
     UnitCosts c;
-    c.base = ((kUnitFixed + cached) >> shift) + 1;
-    c.top = (int)((kUnitFixed + (long long)sink_pages * page + window + 2 * tpb) >> shift) + 1;
+    c.base = ((kChunkFixed + cached) >> shift) + 1;
+    c.top = (int)((kChunkFixed + (long long)sink_pages * page + window + 2 * tpb) >> shift) + 1;
     const float rise = (float)(c.top - c.base) * (float)(1 << kSlopeBits) * (float)(1 << shift);
     const float steps = slope == 0 ? 2e9f : SK_COST_DIV(rise, (float)slope);
     c.rising = c.base >= c.top ? 0 : (int)(steps < 2e9f ? steps : 2e9f);
@@ -121,6 +121,43 @@ SK_COST_FN int cut_tile(int at, int cost, int t, bool uncut)
     const float g = uncut ? 0.5f : SK_COST_DIV((float)kCutFixed, (float)(kCutFixed + t * kChunkKeys));
     const int tile = (int)((float)t * f);
     return at >= cost ? t : f <= g ? 0 : f >= 1.f - g ? t : tile < t ? tile : t;
+}
+
+// ------------------------------------------------------------------ steps
+constexpr int kMaxSplit = 8;                         // CTAs of a cluster
+// What the join kernel costs, in key tiles of a CTA: 96 units of 9 tiles take 11.9 us as clusters (of one) and 15.2 as runs, of
+// 17 tiles 20.1 and 21.2.
+constexpr int kJoinTiles = 7;
+// Key tiles of a cluster's CTA up to which clusters are taken.  `tiles` is a bound on the units: where sequences are shorter,
+// runs share what there is, while a cluster still walks its own unit, so that what clusters can lose grows with their tiles,
+// and what they gain, the join and the cuts, does not.  Clusters and runs of 19 sequences of 32/8 heads (clusters of one), us:
+//   window (tiles)    all full       0.1 to 1 of it    one full, 18 of 300
+//   4096 (33)         50.9, 53.4     37.1, 36.8        31.7, 16.8     (e4m3 pages 34.3, 36.8;  34.1, 29.3;  33.7, 17.8)
+//   6144 (49)         72.8, 75.0     52.2, 49.1        43.2, 18.3     (47.6, 50.0;  47.3, 37.3;  47.0, 20.9)
+//   16384 (129)       180, 182       127, 109          99.9, 25.6     (114, 116;  113, 73.7;  114, 27.9)
+// and of 9 sequences (clusters of two) over 12288: 70.2, 75.1; 51.5, 46.4; 43.3, 20.3 (48.9, 50.9; 48.4, 34.5; 48.1, 22.2).
+constexpr int kClusterTiles = 40;
+
+// Runs of a step's call: one per SM, and no more than there are key tiles.
+inline long long step_runs(long long units, long long tiles, int num_sms)
+{
+    const long long most = units * (tiles < 1 ? 1 : tiles);
+    return most < num_sms ? most : num_sms;
+}
+// CTAs of each unit's cluster; 0: the batch is divided into equal runs.  Units that fit at once have a cluster each, as large as
+// fits (fit[c] clusters of c CTAs run at the same time) and as they have tiles, where units of `tiles` key tiles take no
+// longer than equal runs and their join, and shorter ones not much longer.
+inline int step_cluster(long long units, long long tiles, int num_sms, const int *fit)
+{
+    const long long runs = step_runs(units, tiles, num_sms);
+    if (units > runs)
+        return 0;
+    int split = 1;
+    for (int c = 2; c <= kMaxSplit && c <= tiles; ++c)
+        if (fit[c] >= units)
+            split = c;
+    const long long own = (tiles + split - 1) / split;
+    return own > units * tiles / runs + kJoinTiles || own > kClusterTiles ? 0 : split;
 }
 
 }  // namespace sk

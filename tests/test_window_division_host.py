@@ -15,12 +15,17 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
-def longest_run(tmp_path_factory):
+def library(tmp_path_factory):
     so = str(tmp_path_factory.mktemp("division") / "division.so")
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "paged_split_kv_gb300", "csrc"), "-o", so,
                     os.path.join(ROOT, "tests", "window_division.cpp")], check=True)
-    f = ctypes.CDLL(so).window_division
+    return ctypes.CDLL(so)
+
+
+@pytest.fixture(scope="module")
+def longest_run(library):
+    f = library.window_division
 
     def call(lens, qs, hq, hkv, window, count=152, deal=False):
         """Key tiles of the longest run, and the most that it may have."""
@@ -63,3 +68,19 @@ def test_a_window_of_more_rows_than_the_table_has(longest_run, group):
 def test_costs_past_32_bits_are_counted_in_coarser_steps(longest_run, group):
     longest, most = longest_run([120000], [120000], group, 1, 120000)
     assert longest <= most
+
+
+@pytest.mark.parametrize("hkv", [1, 2, 8])
+def test_a_step_whose_units_may_be_short_is_not_left_to_long_clusters(library, hkv):
+    """One sequence of a full window among short ones: its units' CTAs walk at most 40 key tiles each, whatever the window, or
+    the batch is divided into runs."""
+    fit = (ctypes.c_int * 9)(0, 0, 76, 50, 36, 28, 24, 20, 16)
+    f = library.window_step_cluster
+    f.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
+    for bs in range(1, 153):
+        for tiles in (0, 1, 2, 5, 9, 17, 33, 40, 41, 49, 65, 129, 400, 10 ** 6):
+            split = f(bs * hkv, tiles, 152, fit)
+            assert 0 <= split <= 8 and (split < 2 or fit[split] >= bs * hkv) and split <= max(1, tiles)
+            assert split == 0 or (tiles + split - 1) // split <= 40
+            # (no more CTAs than SMs, each with a place in the workspace)
+            assert bs * hkv * split <= 152

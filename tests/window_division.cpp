@@ -78,3 +78,8 @@ extern "C" int window_division(int bs, const int *lens, const int *qs, int hq, i
     *num_units = (int)all;
     return sum;
 }
+
+extern "C" int window_step_cluster(long long units, long long tiles, int num_sms, const int *fit)
+{
+    return step_cluster(units, tiles, num_sms, fit);
+}
