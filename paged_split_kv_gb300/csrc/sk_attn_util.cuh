@@ -360,6 +360,17 @@ __device__ __forceinline__ int shared_slots(int index, Used used, int *slots)
     return n;
 }
 
+// Registers per thread that a kernel is launched with; -1 where the query fails.
+template <typename Kernel>
+int kernel_registers(Kernel kernel)
+{
+    cudaFuncAttributes a{};
+    if (cudaFuncGetAttributes(&a, kernel) == cudaSuccess)
+        return a.numRegs;
+    cudaGetLastError();
+    return -1;
+}
+
 // Q as two e4m3 terms for e4m3 pages: row (t, hq) becomes 128 hi codes, then 128 lo codes at codes + 256 * row, and
 // 2^-e in the float array behind them.
 cudaError_t launch_split_q(const uint16_t *q, long long rows, void *codes, cudaStream_t stream);

@@ -40,8 +40,6 @@
 #include <math_constants.h>
 #include <stdint.h>
 
-#include <array>
-
 #include "sk_attn_util.cuh"
 #include "sk_cache_ops.cuh"
 #include "sk_sm100.cuh"
@@ -1106,16 +1104,17 @@ cudaError_t launch_t(const CUtensorMap &kv_map, WindowParams p, long long tiles,
 {
     using C = WCfg<RP, FP8>;
     const auto kernel = window_step_kernel<RP, FP8>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess)
         return e;
     // the warpgroups' shares after the reallocation may not exceed what the CTA was launched with
-    static const int regs = [] {
-        cudaFuncAttributes a{};
-        return cudaFuncGetAttributes(&a, window_step_kernel<RP, FP8>) == cudaSuccess ? a.numRegs : 0;
-    }();
-    if (regs < C::kRegsLaunch)
+    static PerDevice registers;
+    if (registers.get(device, [&] { return kernel_registers(kernel); }) < C::kRegsLaunch)
         return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
@@ -1126,22 +1125,23 @@ cudaError_t launch_t(const CUtensorMap &kv_map, WindowParams p, long long tiles,
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    // clusters of each size that run at the same time (looked up once)
-    static const auto fit = [&] {
-        std::array<int, kMaxSplit + 1> n{};
-        cfg.numAttrs = 2;
-        for (int c = 2; c <= kMaxSplit; ++c) {
-            cfg.gridDim = dim3((unsigned)c);
-            attr[1].val.clusterDim.x = (unsigned)c;
-            if (cudaOccupancyMaxActiveClusters(&n[c], kernel, &cfg) != cudaSuccess) {
-                cudaGetLastError();
-                n[c] = 0;
-            }
-        }
-        return n;
-    }();
+    // clusters of each size that run at the same time; none where the query fails
+    static PerDevice most_clusters[kMaxSplit + 1];
+    int fit[kMaxSplit + 1] = {};
+    cfg.numAttrs = 2;
+    for (int c = 2; c <= kMaxSplit; ++c) {
+        cfg.gridDim = dim3((unsigned)c);
+        attr[1].val.clusterDim.x = (unsigned)c;
+        fit[c] = most_clusters[c].get(device, [&] {
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess)
+                return n;
+            cudaGetLastError();
+            return -1;
+        });
+    }
     const long long units = (long long)p.bs * p.H_kv, runs = step_runs(units, tiles, num_sms);
-    p.split = step_cluster(units, tiles, num_sms, fit.data());
+    p.split = step_cluster(units, tiles, num_sms, fit);
     const unsigned grid = (unsigned)(p.split > 0 ? units * p.split : runs);
     cfg.gridDim = dim3(grid);
     attr[1].val.clusterDim.x = (unsigned)(p.split > 1 ? p.split : 1);

@@ -1178,18 +1178,19 @@ cudaError_t launch_t(const CUtensorMap &kv_map, const CUtensorMap &q_map, const 
                      int runs, cudaStream_t stream)
 {
     using C = CCfg<FP8, WIDE>;
-    const cudaError_t e = cudaFuncSetAttribute(window_chunk_kernel<FP8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               C::kSmemBytes);
+    const auto kernel = window_chunk_kernel<FP8, WIDE>;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess)
         return e;
     // the warpgroups' shares after the reallocation may not exceed what the CTA was launched with
-    static const int regs = [] {
-        cudaFuncAttributes a{};
-        return cudaFuncGetAttributes(&a, window_chunk_kernel<FP8, WIDE>) == cudaSuccess ? a.numRegs : 0;
-    }();
-    if (regs < C::kRegsLaunch)
+    static PerDevice registers;
+    if (registers.get(device, [&] { return kernel_registers(kernel); }) < C::kRegsLaunch)
         return cudaErrorInvalidConfiguration;
-    return launch_pdl(window_chunk_kernel<FP8, WIDE>, dim3((unsigned)runs), dim3(C::kThreads), C::kSmemBytes, stream,
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(kernel, dim3((unsigned)runs), dim3(C::kThreads), C::kSmemBytes, stream,
                       kv_map, q_map, out_map, p);
 }
 

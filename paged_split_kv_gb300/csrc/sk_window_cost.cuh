@@ -4,6 +4,8 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #ifdef __CUDACC__
 #define SK_COST_FN __device__ __forceinline__
 #define SK_COST_DIV(a, b) __fdividef(a, b)
@@ -159,5 +161,25 @@ inline int step_cluster(long long units, long long tiles, int num_sms, const int
     const long long own = (tiles + split - 1) / split;
     return own > units * tiles / runs + kJoinTiles || own > kClusterTiles ? 0 : split;
 }
+
+// Answers of a query about a device, asked once for each: ask() gives one of at least 0, or a negative value where it fails.
+// A failure is not kept: the next call asks again.
+struct PerDevice {
+    static constexpr int kDevices = 64;
+    std::atomic<int> kept[kDevices] = {};            // the answer and 1
+    template <typename Ask>
+    int get(int device, Ask ask)
+    {
+        if (device < 0 || device >= kDevices)
+            return ask();
+        int x = kept[device].load() - 1;
+        if (x < 0) {
+            x = ask();
+            if (x >= 0)
+                kept[device].store(x + 1);
+        }
+        return x;
+    }
+};
 
 }  // namespace sk

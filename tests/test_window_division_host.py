@@ -84,3 +84,11 @@ def test_a_step_whose_units_may_be_short_is_not_left_to_long_clusters(library, h
             assert split == 0 or (tiles + split - 1) // split <= 40
             # (no more CTAs than SMs, each with a place in the workspace)
             assert bs * hkv * split <= 152
+
+
+def test_answers_are_kept_per_device_and_failures_are_not(library):
+    calls = [(0, -1), (0, 7), (0, 9), (1, 3), (0, 1), (63, 0), (63, 5), (64, 2), (64, 4), (1, -1)]
+    n = len(calls)
+    got = (ctypes.c_int * n)()
+    asked = library.per_device(n, (ctypes.c_int * n)(*[d for d, _ in calls]), (ctypes.c_int * n)(*[a for _, a in calls]), got)
+    assert list(got) == [-1, 7, 7, 3, 7, 0, 0, 2, 4, 3] and asked == 6

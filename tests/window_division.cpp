@@ -79,6 +79,16 @@ extern "C" int window_division(int bs, const int *lens, const int *qs, int hq, i
     return sum;
 }
 
+// What PerDevice answers to calls on devices[i] where the query gives answers[i]; returns how often it asked.
+extern "C" int per_device(int n, const int *devices, const int *answers, int *got)
+{
+    PerDevice kept;
+    int asked = 0;
+    for (int i = 0; i < n; ++i)
+        got[i] = kept.get(devices[i], [&] { return ++asked, answers[i]; });
+    return asked;
+}
+
 extern "C" int window_step_cluster(long long units, long long tiles, int num_sms, const int *fit)
 {
     return step_cluster(units, tiles, num_sms, fit);
