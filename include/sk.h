@@ -413,7 +413,8 @@ int sk_rope_axes(int rot_dim, int num_axes, const int *sections, int cycled, uin
  * p w_i with p = positions[axes[i]][t], its position on the pair's axis.  Text tokens have the same position on
  * every axis; an image or video patch has its place in the grid.
  *
- * positions int64 [num_axes][num_tokens] with positions_stride elements between axes (a view of a wider buffer will do);
+ * positions int64 [num_axes][num_tokens] with positions_stride elements between axes (a view of a wider buffer will do;
+ * 0 where all axes share one row of positions, as text does);
  * axes uint8 [rot_dim / 2] (device), from sk_rope_axes or the caller's own; 1 <= num_axes <= SK_MAX_AXES.  pos_pages, where
  * given, receives the position on axis 0.  An axis of num_axes or more sets SK_DEV_BAD_SEQ, and its pair does not
  * turn (it is multiplied by attn_factor).  Everything else as for sk_rope_and_cache. */

@@ -524,8 +524,8 @@ def sk_rope_axes_and_cache(q, key, value, positions, freqs, axes, slot_mapping, 
                            v_scale: float = 1.0, acc_pages=None, pos_pages=None, stream=None) -> int:
     """sk_rope_and_cache with several axes (time, height and width of image and video patches): pair i of token t turns
     by ``positions[axes[i], t] * freqs[i]``.  ``positions``: int64 [num_axes, num_tokens], its rows contiguous (a view
-    of a wider buffer will do); ``axes``: uint8 [rot_dim / 2] (sk_rope_axes).  ``pos_pages`` receives the position on
-    axis 0.  The other arguments as there."""
+    of a wider buffer will do, or for text one row for all axes, ``pos.expand(num_axes, -1)``); ``axes``: uint8
+    [rot_dim / 2] (sk_rope_axes).  ``pos_pages`` receives the position on axis 0.  The other arguments as there."""
     import torch
     bf, f64 = torch.bfloat16, torch.float64
     dev = q.get_device()

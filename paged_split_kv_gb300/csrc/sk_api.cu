@@ -654,8 +654,8 @@ int sk_rope_axes_and_cache(const void *q, const void *key, const void *value, in
 {
     if (num_axes < 1 || num_axes > SK_MAX_AXES)
         return fail(SK_ERR_INVALID, "sk_rope_axes_and_cache: num_axes=%d (1 to %d)", num_axes, SK_MAX_AXES);
-    if (positions_stride < num_tokens && num_axes > 1)
-        return fail(SK_ERR_INVALID, "sk_rope_axes_and_cache: positions_stride=%lld below num_tokens=%d",
+    if (positions_stride < num_tokens && positions_stride != 0 && num_axes > 1)
+        return fail(SK_ERR_INVALID, "sk_rope_axes_and_cache: positions_stride=%lld is neither 0 nor num_tokens=%d or more",
                     (long long)positions_stride, num_tokens);
     if (axes == nullptr)
         return fail(SK_ERR_INVALID, "sk_rope_axes_and_cache: null pointer argument");

@@ -97,6 +97,19 @@ def test_equal_positions_are_the_single_axis_write(fp8):
     assert sk.sk_get_device_status() == 0
 
 
+@pytest.mark.parametrize("nt", [1, 70])
+def test_one_row_of_positions_for_all_axes(nt):
+    q, k, v, slots, pages0, pages, pos, freqs = setup(nt, 16, 2, 128, False, 50000, 4)
+    axes = sk.sk_rope_axes(128, [16, 24, 24], device=DEV)
+    other = pages.clone()
+    a, b = torch.empty_like(q.contiguous()), torch.empty_like(q.contiguous())
+    sk.sk_rope_axes_and_cache(q, k, v, pos.expand(3, nt).contiguous(), freqs, axes, slots, pages, a)
+    sk.sk_rope_axes_and_cache(q, k, v, pos.expand(3, nt), freqs, axes, slots, other, b)
+    assert torch.equal(a, b) and torch.equal(pages.view(torch.int16), other.view(torch.int16))
+    check(q, k, v, slots, pages0, pages, pos.expand(3, nt), axes, freqs, a, False, 1.0, False, 1.0, 1.0)
+    assert sk.sk_get_device_status() == 0
+
+
 def test_more_tokens_than_ctas_and_the_state_of_eviction():
     q, k, v, slots, pages0, pages, _, freqs = setup(2500, 8, 2, 64, False, 1000, 5, fused=False)
     pos = positions(3, 2500, 40000, 5)

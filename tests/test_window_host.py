@@ -71,6 +71,18 @@ def test_axes_write_refusals(sk):
     assert call(nt=0, q=None, k=None, v=None, pos=None, sl=None, qo=None, pg=None) == 0
 
 
+def test_axes_may_share_their_positions(sk):
+    """A stride of 0 between the axes: one row of positions for all of them, as text has.  (The write refuses the heads
+    after it has taken the positions' stride.)"""
+    call = caller(sk.lib().sk_rope_axes_and_cache, dict(
+        q=FAKE, k=FAKE, v=FAKE, qs=1024, ks=256, vs=256, pos=FAKE, ps=0, na=3, fr=FAKE, ax=FAKE, rot=64, inter=0, f=1.0,
+        sl=FAKE, nt=4, hq=8, hkv=2, d=64, qo=FAKE, pg=FAKE, dt=0, ksc=1.0, vsc=1.0, nb=8, page=16, acc=None, pp=None,
+        st=None))
+    assert call() == -3
+    for ps in (-1, 1, 2, 3):
+        assert call(ps=ps) == -1, ps
+
+
 def test_binding_checks_shapes_before_raw_pointers(sk):
     bf, i32, i64 = torch.bfloat16, torch.int32, torch.int64
 
