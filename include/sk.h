@@ -416,7 +416,15 @@ int sk_rope_axes(int rot_dim, int num_axes, const int *sections, int cycled, uin
  * positions int64 [num_axes][num_tokens] with positions_stride elements between axes (a view of a wider buffer will do;
  * 0 where all axes share one row of positions, as text does);
  * axes uint8 [rot_dim / 2] (device), from sk_rope_axes or the caller's own; 1 <= num_axes <= SK_MAX_AXES.  pos_pages, where
- * given, receives the position on axis 0.  An axis of num_axes or more sets SK_DEV_BAD_SEQ, and its pair does not
+ * given, receives the position on axis 0.
+ *
+ * A cache that is evicted from needs the token's place in its sequence there: sk_evict_select takes the rows at or past
+ * next_pos - recent for the latest, and of more of them than fit keeps the lower.  On a time axis all patches of an image
+ * have one position, so that an image within `recent` can push out the text behind it.  So give the places an axis of
+ * their own, the first, that turns no pair: positions [place, time, height, width] with sections {0, ...}, or with the
+ * axes of sk_rope_axes plus 1, and next_pos in places.
+ *
+ * An axis of num_axes or more sets SK_DEV_BAD_SEQ, and its pair does not
  * turn (it is multiplied by attn_factor).  Everything else as for sk_rope_and_cache. */
 int sk_rope_axes_and_cache(const void *q, const void *key, const void *value, int64_t q_stride, int64_t key_stride,
                            int64_t value_stride, const int64_t *positions, int64_t positions_stride, int num_axes,
@@ -431,7 +439,9 @@ int sk_rope_axes_and_cache(const void *q, const void *key, const void *value, in
  * weight acc_pages and the position pos_pages at its place in the pages.  Rows with a position of at least
  * next_pos[s] - recent rank first (next_pos: the position that the sequence's next token will have), then
  * rows rank by weight, larger first; equal ranks go to the lower row; NaN ranks like -inf.  The first
- * `budget` rows stay.
+ * `budget` rows stay.  (Positions that rise along a sequence have at most `recent` such rows.  Where they repeat, as on
+ * the time axis of an image, there can be more than fit, and the lower rows stay, not the latest: see
+ * sk_rope_axes_and_cache.)
  *   counts[s][h]                n = how many rows at or past `budget` stay
  *   src_rows[s][h][m], m < n    the m-th of them, ascending
  *   dst_rows[s][h][m], m < n    the m-th row below `budget` that does not stay, ascending

@@ -525,7 +525,10 @@ def sk_rope_axes_and_cache(q, key, value, positions, freqs, axes, slot_mapping, 
     """sk_rope_and_cache with several axes (time, height and width of image and video patches): pair i of token t turns
     by ``positions[axes[i], t] * freqs[i]``.  ``positions``: int64 [num_axes, num_tokens], its rows contiguous (a view
     of a wider buffer will do, or for text one row for all axes, ``pos.expand(num_axes, -1)``); ``axes``: uint8
-    [rot_dim / 2] (sk_rope_axes).  ``pos_pages`` receives the position on axis 0.  The other arguments as there."""
+    [rot_dim / 2] (sk_rope_axes).  ``pos_pages`` receives the position on axis 0: for a cache that is evicted from, make that
+    the token's place in its sequence, an axis of its own that turns no pair (``positions`` [place, time, height, width],
+    ``axes`` = sk_rope_axes(...) + 1, and ``next_pos`` in places), since all patches of an image have the same time.
+    The other arguments as there."""
     import torch
     bf, f64 = torch.bfloat16, torch.float64
     dev = q.get_device()
@@ -902,7 +905,8 @@ def evict_rows(kv_pages, acc_pages, pos_pages, block_table, seq_lens, next_pos, 
                max_seq_len: Optional[int] = None, workspace=None, stream=None):
     """One eviction: sk_evict_select and sk_evict_move.  Every sequence longer than ``budget`` is cut down to
     ``budget`` rows per KV head, in place; such a sequence must not share blocks with others (a common prefix: copy
-    those blocks first).  ``workspace`` is an optional dict that keeps the lists
+    those blocks first).  ``recent`` counts positions: they must rise along a sequence
+    (see sk_rope_axes_and_cache for images).  ``workspace`` is an optional dict that keeps the lists
     (src_rows, dst_rows, counts, of this call's shapes; ones put there beforehand are used where they fit); calls
     that may overlap need one each.  Returns the new lengths (int32 [bs], a new tensor); the pages past them can be
     handed out again."""

@@ -129,6 +129,48 @@ def test_more_tokens_than_ctas_and_the_state_of_eviction():
     assert torch.equal(acc, acc0) and torch.equal(pp, pp0)
 
 
+def image_between_texts(words, side, more):
+    """Positions [time, height, width] of text, a still image of side x side patches and text behind it."""
+    text = lambda at, n: (at + torch.arange(n)).expand(3, n)
+    cells = torch.stack([torch.zeros(side, side), *torch.meshgrid(torch.arange(side), torch.arange(side), indexing="ij")])
+    return torch.cat([text(0, words), words + cells.reshape(3, -1).long(), text(words + side, more)], 1).to(DEV)
+
+
+@pytest.mark.parametrize("cycled", [False, True])
+def test_the_latest_rows_of_an_image_and_text_stay(cycled):
+    """The token's place as an axis without pairs: the rotation is that of the other axes, and eviction keeps the last
+    `recent` tokens, although an image of more patches than the budget has the same time throughout."""
+    words, side, more, budget, recent, hkv = 100, 40, 200, 512, 256, 2
+    grid = image_between_texts(words, side, more)
+    n = grid.shape[1]
+    q, k, v, slots, pages0, pages, _, freqs = setup(n, 4, hkv, 128, False, 10, 12, holes=False)
+    place = torch.arange(n, device=DEV)
+    axes = sk.sk_rope_axes(128, [24, 20, 20], cycled=cycled, device=DEV)
+    blocks = torch.arange(-(-n // PAGE), device=DEV, dtype=torch.int32).flip(0)[None]
+    at = blocks[0].long()[place // PAGE] * PAGE + place % PAGE
+    state = [torch.zeros(pages.shape[:3], device=DEV), torch.full(pages.shape[:3], -7, dtype=torch.int32, device=DEV)]
+    a, b = torch.empty((n, 4, D), dtype=torch.bfloat16, device=DEV), torch.empty((n, 4, D), dtype=torch.bfloat16, device=DEV)
+    other = pages.clone()
+    sk.sk_rope_axes_and_cache(q, k, v, grid, freqs, axes, at, other, a)
+    sk.sk_rope_axes_and_cache(q, k, v, torch.cat([place[None], grid]), freqs, axes + 1, at, pages, b, acc_pages=state[0],
+                              pos_pages=state[1])
+    assert torch.equal(a, b) and torch.equal(pages.view(torch.int16), other.view(torch.int16))
+    # the image weighs the most, the last text the least
+    state[0].view(-1, PAGE)[:] = 1.0
+    state[0][at[words:words + side * side] // PAGE, :, at[words:words + side * side] % PAGE] = 5.0
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    new = sk.evict_rows(pages, *state, blocks, lens, lens, budget=budget, recent=recent)
+    assert new.tolist() == [budget] and sk.sk_get_device_status() == 0
+    rows = torch.arange(budget, device=DEV)
+    for h in range(hkv):
+        kept = state[1][blocks[0].long()[rows // PAGE], h, rows % PAGE].sort().values
+        # the last `recent`; of the others the heaviest, ties to the lower rows: the image's first patches
+        assert torch.equal(kept, torch.cat([words + torch.arange(budget - recent), n - recent + torch.arange(recent)]).to(kept))
+        keys = pages[blocks[0].long()[rows // PAGE], h, rows % PAGE]
+        order = state[1][blocks[0].long()[rows // PAGE], h, rows % PAGE].long()
+        assert torch.equal(keys, other[at[order] // PAGE, h, at[order] % PAGE])
+
+
 def test_in_place_negative_and_far_positions():
     q, k, v, slots, pages0, pages, _, freqs = setup(40, 4, 2, 128, False, 10, 6, fused=False)
     pos = torch.as_tensor(np.random.default_rng(3).integers(-2 ** 31, 2 ** 31, size=(3, 40)), device=DEV)
