@@ -1255,7 +1255,7 @@ cudaError_t launch_window_chunk(const WindowParams &params, int kv_dtype, long l
     runs = runs < 1 ? 1 : (runs < num_sms ? runs : num_sms);
     runs = runs < kMaxRuns ? runs : kMaxRuns;
     p.shift = cost_shift(units, most);
-    p.bounded = (double)per_seq * p.H_kv * (kChunkFixed + (double)most) < (double)(1 << 30);
+    p.bounded = (double)per_seq * p.H_kv * (kChunkFixed + kChunkEdge + (double)most) < (double)(1 << 30);
     p.deal = (double)p.bs * keys * p.H_kv * (fp8 ? 256 : 512) > kL2Share ? 1 : 0;
     // (a prompt's first units see less: on average keys / 2 less over its first `keys` tokens)
     const bool wide = keys > 0 && keys * (1. - 0.5 * keys / max_seq_len) >= kWideTiles * (double)kKeys;

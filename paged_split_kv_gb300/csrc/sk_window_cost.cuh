@@ -1,7 +1,6 @@
 // Windowed attention: how a call's work is shared among the CTAs.  Chunks: what a unit of work costs, and where the batch's
 // cost is cut into the CTAs' runs; steps: clusters or runs.  Plain arithmetic, for the host as well.
 #pragma once
-#include <limits.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -19,12 +18,16 @@ namespace sk {
 constexpr int kChunkKeys = 128;                      // keys of a tile
 constexpr int kChunkRows = 128;                      // rows of a row tile
 // Cost of starting and finishing a unit, in keys, next to other units, which hide part of it, and of its last key tile, which
-// is filled in part.  The geometric mean over 52 calls (26 shapes: one to 24 prompts and chunks, groups of 8 to 160 heads,
-// windows of 128, 512, 4096 and of all; bf16 and e4m3 pages) is 131.4 us with 128, 126.7 with 160, 124.1 with 192, 123.0 with
-// 224, 123.4 with 256, 124.0 with 320; on another machine 129.8 with 128, 125.6 with 384, 128.7 with 640.  Single shapes, with
-// 128 and 224: 24 prompts of up to 2000 tokens over 512, 16/2 heads, 109 and 108, with 32/1 heads 194 and 198; eight of up to
-// 4000 over 4096 174 and 175; 8000 tokens of 16/2 heads 157 and 151; 4000 of 48/2 heads 201 and 173.
+// is filled in part; and what a unit of a full window costs more, whose first tile is masked too.  Geometric means over 94
+// calls (one to 24 prompts and chunks, groups of 4 to 160 heads, windows of 128 to 4096 and of all; bf16 and e4m3 pages), us:
+//   128 and 0    112.3      160 and 32   110.2      192 and 64   108.9      224 and 0    108.6      224 and 64   108.4
+//   256 and 64   108.4      224 and 128  108.9      224 and 192  109.8      224 and 320  112.5      160 and 96   111.1
+// Single long prompts gain, whose first CTAs have nothing but small units: with 128 and 0, and with 224 and 64, 8000 tokens
+// of 16/2 heads over 4096 take 158 and 151, 4000 of 48/2 heads 203 and 174.  Batches differ by where their cuts fall: eight
+// prompts of up to 4000 over 4096 177 and 176, six of 24 prompts over 512 98 to 120, and 100 to 120, ten of up to 3000 over
+// 1024 167 to 217, and 165 to 216.
 constexpr int kChunkFixed = 224;
+constexpr int kChunkEdge = 64;
 // A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
 // than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384,
 // 110 with 640).
@@ -63,16 +66,16 @@ inline int rows_in_table(int rows, int stride, int page)
 inline int cost_shift(long long units, long long most)
 {
     int shift = 4;
-    while ((units * (kChunkFixed + most) >> shift) >> 30)
+    while ((units * (kChunkFixed + kChunkEdge + most) >> shift) >> 30)
         ++shift;
     return shift;
 }
 
 // The units of one (sequence, KV head): unit i costs what its last tokens see, base + slope (i + 1), below `rising`, then
-// `top`, a full window.  Sums keep the slope's fraction of 2^shift keys: with a slope of whole steps, 8 tokens a unit and
-// shift 4, all units cost alike, the longest run of 4000 tokens of 32/1 heads over a window of 4096 had 125 key tiles where
-// the average is 53, and the call took 214 us; it takes 114 so (48/2 heads: 319 and 174; 5000 tokens of 24/2 heads: 145 and
-// 136).
+// `top`, a full window and its edge.  Sums keep the slope's fraction of 2^shift keys: with a slope of whole steps, 8 tokens a
+// unit and shift 4, all units cost alike, the longest run of 4000 tokens of 32/1 heads over a window of 4096 had 125 key tiles
+// where the average is 53, and the call took 214 us; it takes 114 so (48/2 heads: 319 and 174; 5000 tokens of 24/2 heads: 145
+// and 136).
 struct UnitCosts {
     int base, top, rising;
 };
@@ -84,6 +87,7 @@ SK_COST_FN UnitCosts unit_costs(int cached, int sink_pages, int page, int window
     const float rise = (float)(c.top - c.base) * (float)(1 << kSlopeBits) * (float)(1 << shift);
     const float steps = slope == 0 ? 2e9f : SK_COST_DIV(rise, (float)slope);
     c.rising = c.base >= c.top ? 0 : (int)(steps < 2e9f ? steps : 2e9f);
+    c.top += kChunkEdge >> shift;
     return c;
 }
 // Cost of the units before unit i.  (slope n / 2^kSlopeBits is below 2^32 for n up to `rising`, and n below 2^24.)
@@ -146,8 +150,8 @@ inline long long step_runs(long long units, long long tiles, int num_sms)
     const long long most = units * (tiles < 1 ? 1 : tiles);
     return most < num_sms ? most : num_sms;
 }
-// CTAs of each unit's cluster; 0: the batch is divided into equal runs.  Units that fit at once have a cluster each, as large as
-// fits (fit[c] clusters of c CTAs run at the same time) and as they have tiles, where units of `tiles` key tiles take no
+// CTAs of each unit's cluster; 0: the batch is divided into equal runs.  Units that fit at once have a cluster each, as large
+// as fits (fit[c] clusters of c CTAs run at the same time) and as they have tiles, where units of `tiles` key tiles take no
 // longer than equal runs and their join, and shorter ones not much longer.
 inline int step_cluster(long long units, long long tiles, int num_sms, const int *fit)
 {

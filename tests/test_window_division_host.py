@@ -1,10 +1,11 @@
 """The division of a windowed chunk call among its CTAs, on the CPU: the kernel's own arithmetic, compiled for the host.
 
-Bound.  A run has an equal share of the batch's price.  A unit's price is its keys and 224, rounded up by 32 at most (two steps
-of 16); its tiles are its keys rounded up by less than 128.  So a share is at most the average of key tiles and two for each
-unit of a run on average, and a cut moves by less than 4 tiles (512 keys) at either end.  Runs of whole units are taken where
-the longest is then at most 1.1 times as long as the share and 6.25 tiles (800 keys) more.  Units are dealt in turn where the
-dearest costs at most 1.4 times the average, and those left over are shared with 4 tiles more at either end."""
+Bound.  A run has an equal share of the batch's price.  A unit's price is its keys and 224, with a full window 288, rounded up
+by 32 at most (two steps of 16); its tiles are its keys rounded up by less than 128.  So a share is at most the average of
+key tiles and 2.5 for each unit of a run on average, and a cut moves by less than 4 tiles (512 keys) at either end.  Runs of
+whole units are taken where the longest is then at most 1.1 times as long as the share and 6.25 tiles (800 keys) more.  Units
+are dealt in turn where the dearest costs at most 1.4 times the average, and those left over are shared with 4 tiles more at
+either end."""
 import ctypes
 import os
 import subprocess
@@ -34,7 +35,7 @@ def longest_run(library):
         total = f(n, (ctypes.c_int * n)(*lens), (ctypes.c_int * n)(*qs), hq, hkv, window, 4, (max(lens) + 15) // 16, count,
                   int(deal), tiles, ctypes.byref(units))
         assert total >= 0 and sum(tiles) == total              # every unit is covered, in order
-        return max(tiles), (1.4 if deal else 1.1) * (total + 2 * units.value) / count + 8
+        return max(tiles), (1.4 if deal else 1.1) * (total + 2.5 * units.value) / count + 8
 
     return call
 
