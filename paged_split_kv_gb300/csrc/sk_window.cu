@@ -23,7 +23,9 @@
 //               has the time of two tiles for one, and the groups meet only at a unit's end, where their states are joined.
 //               A thread is a key (its TMEM lane).  A row's reference is its largest score of the group's first tile;
 //               it moves only when a later score beats it by far, on which the group's threads vote once per tile.
-//               P^T goes over the tile's own K, which QK no longer needs.
+//               P^T goes over the tile's own K, which QK no longer needs.  It is rounded to V's type, bf16, as the product
+//               takes both of one (f16 on e4m3 pages); its sum is not.  The output is then off from 64 bits by 0.0023 of its
+//               size, where rounding the output alone is 0.0016 (f16: 0.0017).
 //   warps 12-15 (e4m3)  Q as two e4m3 terms, and V's codes to f16 (exactly): PV runs on f16 with P as f16
 // e4m3 pages: QK runs on the codes, with Q as two e4m3 terms and a power-of-two scale per row, two products into one S.
 //
@@ -32,7 +34,7 @@
 // Measured (calls replayed from a graph): 128 tokens over a window of 4096, 32/8 heads, 2150 MB: 312 us, 6.9 TB/s (e4m3 pages
 // 209 us, 5.1: a copy of a page costs the SM's copy unit 130 cycles and 3.3 for each 128 bytes, whatever else it does).  64 ragged
 // ones over 1024, 269 MB: 53 us, of which the join is 4 and the pages stream at 6.8 TB/s.  One token over 4096, 17 MB: 10.5 us;
-// 16 times 4 tokens over 8192 on e4m3 pages with 2 KV heads, 35 MB: 20.4 us.  These two are a chain: launch, block ids, pages,
+// 16 times 4 tokens over 4096 on e4m3 pages with 2 KV heads, 35 MB: 20.4 us.  These two are a chain: launch, block ids, pages,
 // products and softmax of few tiles, end, join, on code that is fetched as it is first run.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -1157,9 +1159,9 @@ int padded_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 }  // namespace
 
-// Rows of a (sequence, KV head) up to which this kernel is the faster one: for 64 rows it takes 17.0 us where the chunk kernel
-// takes 27.4 (64 units of each of two heads over a window of 1024), 99.7 against 111.9 over 8192, on e4m3 pages 76.6 against
-// 106.5; it has no room for more.
+// Rows of a (sequence, KV head) up to which this kernel is the faster one: for 64 rows it takes 22 us where the chunk kernel
+// takes 29 (64 sequences of two KV heads over a window of 1024), 99 against 111 over 8192, on e4m3 pages 77 against 103; it
+// has no room for more.
 bool window_step_takes(long long rows) { return rows <= 64; }
 
 // Two pieces of the padded rows (o, m, l) per run, with what they are pieces of.

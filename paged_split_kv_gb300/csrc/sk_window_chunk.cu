@@ -24,13 +24,16 @@
 // S(j) complete implies PV(j - 1) complete (products of one issuer complete in issue order), so the softmax may rescale O
 // at once; it does so only when scores beat the reference by far.
 //
+// P is rounded to V's type, bf16, as the product takes both of one (f16 on e4m3 pages); its sum is not: the output is off from
+// 64 bits by 0.0023 of its size, where rounding the output alone is 0.0016 (f16: 0.0017).
+//
 // Every wait is bounded: on expiry SK_DEV_TIMEOUT is set and every role gives up, after its copies and products in flight.
 //
 // Measured: 4096 tokens over a window of 4096, 32/8 heads: 196 us, 1.40 PFLOP/s of the pairs that are seen.  24 prompts of up to
-// 2000 tokens over 512, 16/2 heads: 107 us; 16001 tokens over 128: 51 us; 1919 tokens of four prompts over 2048 on e4m3 pages:
+// 2000 tokens over 512, 16/2 heads: 112 us; 16001 tokens over 128: 53 us; 1919 tokens of four prompts over 2048 on e4m3 pages:
 // 40 us.  A key tile takes 3050 cycles: the softmax of a row tile (1600) and its products (1024 for both of its own), one after
-// the other, beside those of the other row tile; a unit's start and end take 5000 more, a call's first S 12000, on code that runs once
-// in a while; the tensor pipe is busy 61 % of the first call, 40 % of the second.
+// the other, beside those of the other row tile; a unit's start and end take 5000 more, a call's first S 12000, on code that runs
+// once in a while; the tensor pipe is busy 61 % of the first call, 41 % of the second.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -124,9 +127,9 @@ constexpr int kColS = 0, kColO = 256;                // S_A, S_B, then O_A, O_B,
 constexpr double kL2Share = 60e6;                    // bytes of K and V that stay in the L2 (126 MB in two halves)
 // Key tiles of a unit, on average, from which on a tile that a warp's rows all see is taken in one go instead of by halves.  That
 // waits for the tensor memory and votes once, but its code beside that of the masked tiles costs units that change between
-// them often.  Measured, in one go and by halves: 4096 tokens over a window of 4096 198 and 210 us (e4m3 pages 227 and 235),
-// 2048 over 8192 184 and 200 (198 and 215), two prompts of 8000 over 4096 486 and 501 (553 and 576); eight prompts of up to
-// 4000 over 4096, 16 tiles on average, 196 and 188 (238 and 230), 24 of up to 2000 over 512 121 and 111.
+// them often.  Measured, in one go and by halves: 4096 tokens over a window of 4096 197 and 210 us (e4m3 pages 226 and 234),
+// 2048 over 8192 190 and 204 (208 and 220), two prompts of 8000 over 4096, 16/2 heads, 287 and 300 (314 and 330); eight prompts
+// of up to 4000 over 4096, 16 tiles on average, 147 and 147 (173 and 168), 24 of up to 2000 over 512 123 and 113 (172 and 152).
 constexpr int kWideTiles = 23;
 
 using Piece = ChunkPiece;

@@ -29,11 +29,11 @@ constexpr int kChunkRows = 128;                      // rows of a row tile
 constexpr int kChunkFixed = 224;
 constexpr int kChunkEdge = 64;
 // A cut costs a piece's start and end, and the join of the unit: it moves to the unit's start or end where that is no further
-// than this (4096 tokens over a window of 4096, tiles by halves: 212 us with 768, 210 with 512; the 24 prompts 111 with 384,
-// 110 with 640).
+// than this (106 calls, the geometric mean: 98.7 us with 256, 98.6 with 384, 98.6 with 512, 99.2 with 640, 99.9 with 768).
 constexpr int kCutFixed = 512;
-// Where units cost alike, none is cut if the longest run is then longer by this or less than if they were: 1919 tokens of e4m3
-// pages over a window of 2048, 122 units, took 42.0 us, and 46.8 cut; 168 units on the 152 SMs take 37.3 cut, and 42.8 whole.
+// Where units cost alike, none is cut if the longest run is then longer by this or less than if they were: 122 units over a
+// window of 2048 take 39.4 us, and 44.4 cut (e4m3 pages 41.3 and 46.2), 100 over 1024 26.5 and 29.6; 168 over 1024 on the 152
+// SMs take 38.4 cut, and 42.6 whole.  The mean of the 106 calls: 99.4 us with 0, 99.3 with 400, 98.6 with 800, 99.1 with 1600.
 constexpr int kJoinCost = 800;
 
 // A row tile is `tpb` query tokens times `gb` heads of the group, or one of the `nsub` tiles of a token whose group has more
