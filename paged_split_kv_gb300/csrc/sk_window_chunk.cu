@@ -32,8 +32,8 @@
 // Measured: 4096 tokens over a window of 4096, 32/8 heads: 196 us, 1.40 PFLOP/s of the pairs that are seen.  24 prompts of up to
 // 2000 tokens over 512, 16/2 heads: 112 us; 16001 tokens over 128: 53 us; 1919 tokens of four prompts over 2048 on e4m3 pages:
 // 40 us.  A key tile takes 3050 cycles: the softmax of a row tile (1600) and its products (1024 for both of its own), one after
-// the other, beside those of the other row tile; a unit's start and end take 5000 more, a call's first S 12000, on code that runs
-// once in a while; the tensor pipe is busy 61 % of the first call, 41 % of the second.
+// the other, beside those of the other row tile; a unit's start and end take 5000 more, a call's first S 12000, on code that
+// runs once in a while; the tensor pipe is busy 61 % of the first call, 41 % of the second.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
